@@ -1,0 +1,478 @@
+// The paged key-value cache: who holds which page, and the rows that move.
+//
+// A page is free when its reference count is 0, so the counts are the whole
+// state of the pool: no free list has to be kept consistent, every change is
+// an integer add (whose order does not matter), and pages are given lowest id
+// first, so a sequence of calls always gives the same table.
+//
+// Bookkeeping kernels are latency-bound (a few dependent loads of a few
+// words); the data movers are bound by HBM: each row is read and written once
+// with 16-byte accesses, several per lane in flight.
+#include "ns_internal.cuh"
+#include "ns_ops.cuh"
+
+namespace ns {
+namespace {
+
+constexpr int kSeqThreads = 128;      // truncate, fork: one CTA per sequence
+constexpr int kExtendThreads = 1024;  // extend: one CTA
+constexpr int kMoveThreads = 256;
+constexpr int kMoveWarps = kMoveThreads / kWarp;
+constexpr int kUnroll = 8;  // 16-byte loads a lane keeps in flight in the movers
+
+__host__ __device__ inline int pages_for(long long len, int page) { return (int)((len + page - 1) / page); }
+
+// Whether entry i of ids also stands before i (the later one is skipped).
+// Called by a whole CTA; the answer is the same in every thread.
+__device__ __forceinline__ bool repeated(const int32_t *ids, int i) {
+  const int32_t mine = ids[i];
+  int hit = 0;
+  for (int j = threadIdx.x; j < i; j += blockDim.x) hit |= ids[j] == mine;
+  return __syncthreads_or(hit) != 0;
+}
+
+__device__ __forceinline__ bool seq_ok(const ns_kv_pages &c, int s) { return s >= 0 && s < c.max_seqs; }
+__device__ __forceinline__ bool len_ok(const ns_kv_pages &c, int len) {
+  return len >= 0 && (long long)len <= (long long)c.table_ld * c.page_size;
+}
+
+// Drops this holder from the pages of table row `row` in slots [from, to).
+__device__ __forceinline__ void drop_pages(const ns_kv_pages &c, int32_t *row, int from, int to, uint32_t *err) {
+  for (int q = from + (int)threadIdx.x; q < to; q += blockDim.x) {
+    const int p = row[q];
+    row[q] = -1;
+    if (p < 0 || p >= c.pages) {
+      set_flag(err, NS_FLAG_BAD_ID);
+      continue;
+    }
+    if (atomicSub(c.refs + p, 1) <= 0) {  // a count that was free already: undo
+      atomicAdd(c.refs + p, 1);
+      set_flag(err, NS_FLAG_BAD_ID);
+    }
+  }
+}
+
+// Truncation, and the second half of compaction (base given: to base +
+// new_len, where new_len is at most `most`, the rows that could be kept).
+__global__ void __launch_bounds__(kSeqThreads) truncate_kernel(ns_kv_pages c, const int32_t *seqs,
+                                                               const int32_t *new_len, const int32_t *base,
+                                                               int most, uint32_t *err) {
+  const int i = blockIdx.x;
+  const int s = seqs[i];
+  const bool again = repeated(seqs, i);
+  if (again || !seq_ok(c, s)) {
+    if (threadIdx.x == 0) set_flag(err, NS_FLAG_BAD_SEQ);
+    return;
+  }
+  const int len = c.lengths[s];
+  const long long want = (long long)(new_len ? new_len[i] : 0) + (base ? base[i] : 0);
+  if (!len_ok(c, len) || want < 0 || (new_len && (new_len[i] < 0 || new_len[i] > most)) || (base && base[i] < 0)) {
+    if (threadIdx.x == 0) set_flag(err, NS_FLAG_BAD_SEQ);
+    return;
+  }
+  if (want >= len) return;
+  drop_pages(c, c.table + (size_t)s * c.table_ld, pages_for(want, c.page_size), pages_for(len, c.page_size), err);
+  __syncthreads();  // every thread has read the old length
+  if (threadIdx.x == 0) c.lengths[s] = (int)want;
+}
+
+__global__ void __launch_bounds__(kSeqThreads) fork_kernel(ns_kv_pages c, const int32_t *src, const int32_t *dst,
+                                                           int n, uint32_t *err) {
+  const int i = blockIdx.x;
+  const int a = src[i], b = dst[i];
+  int clash = 0;  // the destination is another entry's destination (the first wins) or any entry's source
+  for (int j = threadIdx.x; j < n; j += blockDim.x) clash |= (j < i && dst[j] == b) || src[j] == b;
+  clash = __syncthreads_or(clash);
+  if (clash || !seq_ok(c, a) || !seq_ok(c, b)) {
+    if (threadIdx.x == 0) set_flag(err, NS_FLAG_BAD_SEQ);
+    return;
+  }
+  const int len = c.lengths[a];
+  if (!len_ok(c, len) || c.lengths[b] != 0) {
+    if (threadIdx.x == 0) set_flag(err, NS_FLAG_BAD_SEQ);
+    return;
+  }
+  const int held = pages_for(len, c.page_size);
+  const int32_t *from = c.table + (size_t)a * c.table_ld;
+  int32_t *to = c.table + (size_t)b * c.table_ld;
+  for (int q = threadIdx.x; q < held; q += blockDim.x) {
+    const int p = from[q];
+    to[q] = p;
+    if (p >= 0 && p < c.pages)
+      atomicAdd(c.refs + p, 1);
+    else
+      set_flag(err, NS_FLAG_BAD_ID);
+  }
+  __syncthreads();  // every thread has seen the destination empty
+  if (threadIdx.x == 0) c.lengths[b] = len;
+}
+
+// Workspace of an extension, int32 words: [0] copies, [1] unused, then per
+// sequence its first new slot (-1: skipped), its rank among the given pages,
+// their number, and the page to copy (-1: none); the copies' sources and
+// destinations; the free pages found.
+struct ExtendWs {
+  int32_t *n_copies, *first, *start, *count, *shared, *src, *dst, *list;
+  __host__ __device__ ExtendWs(void *p, int n) {
+    int32_t *w = static_cast<int32_t *>(p);
+    n_copies = w;
+    first = w + 4;
+    start = first + n;
+    count = start + n;
+    shared = count + n;
+    src = shared + n;
+    dst = src + n;
+    list = dst + n;
+  }
+};
+
+// One CTA: what each sequence needs (a scan over the call's order), then the
+// lowest free pages (a scan over the counts, which ends once there are
+// enough), then the table rows, one warp per sequence.
+__global__ void __launch_bounds__(kExtendThreads) extend_kernel(ns_kv_pages c, const int32_t *seqs,
+                                                                const int32_t *n_new, int n, void *ws,
+                                                                uint32_t *err) {
+  __shared__ int sh[kExtendThreads / kWarp];
+  __shared__ int s_ids[NS_MAX_PAGE_SEQS];
+  const ExtendWs w(ws, n);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  for (int i = tid; i < n; i += kExtendThreads) s_ids[i] = seqs[i];
+  __syncthreads();
+
+  long long total = 0;  // pages wanted; may pass 32 bits only where it is refused below
+  int copies = 0;
+  for (int i0 = 0; i0 < n; i0 += kExtendThreads) {
+    const int i = i0 + tid;
+    int count = 0, first = -1, shared = -1;
+    if (i < n) {
+      const int s = s_ids[i], add = n_new[i];
+      bool ok = seq_ok(c, s) && add >= 0;
+      for (int j = 0; j < i && ok; ++j) ok = s_ids[j] != s;
+      const int len = ok ? c.lengths[s] : 0;
+      ok = ok && len_ok(c, len) && (long long)len + add <= (long long)c.table_ld * c.page_size;
+      if (ok) {
+        first = pages_for(len, c.page_size);
+        const int want = pages_for((long long)len + add, c.page_size);
+        if (add > 0 && len % c.page_size != 0) {  // the next position is in a page that is held already
+          const int p = c.table[(size_t)s * c.table_ld + first - 1];
+          if (p < 0 || p >= c.pages) {
+            ok = false;
+            first = -1;
+            set_flag(err, NS_FLAG_BAD_ID);
+          } else if (c.refs[p] > 1) {
+            shared = p;
+            --first;
+          }
+        }
+        if (ok) count = want - first;
+      } else {
+        set_flag(err, NS_FLAG_BAD_SEQ);
+      }
+    }
+    int sum, csum;
+    const int off = block_exclusive_scan(count, sh, &sum);
+    const int coff = block_exclusive_scan(shared >= 0 ? 1 : 0, sh, &csum);
+    if (i < n) {
+      // start saturates: a call that wants more pages than exist is refused
+      w.start[i] = total + off > 0x3fffffffLL ? 0x3fffffff : (int)(total + off);
+      w.first[i] = first;
+      w.count[i] = count;
+      w.shared[i] = shared;
+      if (shared >= 0) w.src[copies + coff] = shared;
+    }
+    total += sum;
+    copies += csum;
+  }
+
+  // the `total` lowest free pages, in order
+  bool enough = total <= c.pages;
+  int found = 0;
+  if (enough && total > 0) {
+    constexpr int kPer = 8;
+    for (int p0 = 0; p0 < c.pages && found < total; p0 += kExtendThreads * kPer) {
+      const int p = p0 + tid * kPer;
+      uint32_t free_bits = 0;
+      int r[kPer];
+#pragma unroll
+      for (int q = 0; q < kPer; ++q) r[q] = p + q < c.pages ? c.refs[p + q] : 1;
+#pragma unroll
+      for (int q = 0; q < kPer; ++q) free_bits |= (r[q] == 0 ? 1u : 0u) << q;
+      int sum;
+      int at = found + block_exclusive_scan(__popc(free_bits), sh, &sum);
+      for (; free_bits && at < total; free_bits &= free_bits - 1, ++at) w.list[at] = p + __ffs(free_bits) - 1;
+      found += sum;
+    }
+    enough = found >= total;
+  }
+  if (!enough) {
+    if (tid == 0) {
+      set_flag(err, NS_FLAG_NO_PAGES);
+      *w.n_copies = 0;
+    }
+    return;
+  }
+  if (tid == 0) *w.n_copies = copies;
+  __syncthreads();  // the list, and every sequence's entry
+
+  int done = 0;  // copies of the chunks before
+  for (int i0 = 0; i0 < n; i0 += kExtendThreads) {
+    const int i = i0 + tid;
+    int csum;
+    const int coff = block_exclusive_scan(i < n && w.shared[i] >= 0 ? 1 : 0, sh, &csum);
+    if (i < n && w.first[i] >= 0) {
+      const int s = s_ids[i];
+      c.lengths[s] += n_new[i];
+      if (w.shared[i] >= 0) {
+        w.dst[done + coff] = w.list[w.start[i]];
+        atomicSub(c.refs + w.shared[i], 1);
+      }
+    }
+    done += csum;
+  }
+  for (int i = warp; i < n; i += kExtendThreads / kWarp) {
+    if (w.first[i] < 0) continue;
+    int32_t *row = c.table + (size_t)s_ids[i] * c.table_ld + w.first[i];
+    for (int q = lane; q < w.count[i]; q += kWarp) {
+      const int p = w.list[w.start[i] + q];
+      row[q] = p;
+      atomicAdd(c.refs + p, 1);  // 0 -> 1
+    }
+  }
+}
+
+// Copies whole pages.  A warp takes one (page pair, layer, head) of k or v:
+// page_size rows of row_bytes, 16 bytes a lane.  The pairs' number is on the
+// device when n_ptr is given (at most n).
+__global__ void __launch_bounds__(kMoveThreads) copy_pages_kernel(ns_kv_pages c, const int32_t *src,
+                                                                  const int32_t *dst, const int32_t *n_ptr, int n,
+                                                                  uint32_t *err) {
+  const int lane = threadIdx.x & 31;
+  const int pairs = n_ptr ? min(*n_ptr, n) : n;
+  const long long items = (long long)pairs * c.layers * c.heads * 2;
+  const int cols = c.row_bytes / 16, units = c.page_size * cols;
+  for (long long it = (long long)blockIdx.x * kMoveWarps + (threadIdx.x >> 5); it < items;
+       it += (long long)gridDim.x * kMoveWarps) {
+    const int kv = (int)(it & 1);
+    const long long u = it >> 1;
+    const int head = (int)(u % c.heads), layer = (int)(u / c.heads % c.layers), i = (int)(u / c.heads / c.layers);
+    const int a = src[i], b = dst[i];
+    if (a < 0 || a >= c.pages || b < 0 || b >= c.pages) {
+      if (lane == 0) set_flag(err, NS_FLAG_BAD_ID);
+      continue;
+    }
+    const int64_t sp = kv ? c.v_page : c.k_page, st = kv ? c.v_token : c.k_token;
+    char *base = static_cast<char *>(kv ? c.v : c.k) + layer * (kv ? c.v_layer : c.k_layer) +
+                 head * (kv ? c.v_head : c.k_head);
+    const char *from = base + a * sp;
+    char *to = base + b * sp;
+    for (int x0 = lane; x0 < units; x0 += kWarp * kUnroll) {
+      uint4 val[kUnroll];
+#pragma unroll
+      for (int q = 0; q < kUnroll; ++q) {
+        const int x = x0 + q * kWarp;
+        if (x < units) val[q] = __ldcs(reinterpret_cast<const uint4 *>(from + x / cols * st + x % cols * 16));
+      }
+#pragma unroll
+      for (int q = 0; q < kUnroll; ++q) {
+        const int x = x0 + q * kWarp;
+        if (x < units) *reinterpret_cast<uint4 *>(to + x / cols * st + x % cols * 16) = val[q];
+      }
+    }
+  }
+}
+
+// New rows of one layer: a warp per token, its 16-byte pieces of every head
+// of k and v over the lanes.
+__global__ void __launch_bounds__(kMoveThreads) write_kernel(ns_kv_pages c, int layer, const int32_t *seqs,
+                                                             const int32_t *cu, int n, const char *k_new,
+                                                             const char *v_new, int64_t k_token, int64_t k_head,
+                                                             int64_t v_token, int64_t v_head, int tokens,
+                                                             uint32_t *err) {
+  const int lane = threadIdx.x & 31;
+  const int t = blockIdx.x * kMoveWarps + (threadIdx.x >> 5);
+  if (t >= tokens) return;
+  int lo = 0, hi = n;  // the last i with cu[i] <= t
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (cu[mid] <= t)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  const int t0 = cu[lo], t1 = cu[lo + 1];
+  if (t < t0 || t >= t1) return;  // a token of no sequence
+  const int s = seqs[lo];
+  if (!seq_ok(c, s)) {
+    if (lane == 0) set_flag(err, NS_FLAG_BAD_SEQ);
+    return;
+  }
+  const int len = c.lengths[s];
+  const long long pos = (long long)len - (t1 - t);
+  if (!len_ok(c, len) || pos < 0) {
+    if (lane == 0) set_flag(err, NS_FLAG_BAD_SEQ);
+    return;
+  }
+  const int page = c.table[(size_t)s * c.table_ld + (int)(pos / c.page_size)], r = (int)(pos % c.page_size);
+  if (page < 0 || page >= c.pages) {
+    if (lane == 0) set_flag(err, NS_FLAG_BAD_ID);
+    return;
+  }
+  if (c.refs[page] > 1) {
+    if (lane == 0) set_flag(err, NS_FLAG_SHARED_PAGE);
+    return;
+  }
+  const int cols = c.row_bytes / 16, units = c.heads * cols;
+  char *kd = static_cast<char *>(c.k) + layer * c.k_layer + page * c.k_page + r * c.k_token;
+  char *vd = static_cast<char *>(c.v) + layer * c.v_layer + page * c.v_page + r * c.v_token;
+  const char *ks = k_new + t * k_token, *vs = v_new + t * v_token;
+  for (int x0 = lane; x0 < units; x0 += kWarp * 4) {
+    uint4 a[4], b[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int x = x0 + q * kWarp;
+      if (x < units) {
+        a[q] = __ldcs(reinterpret_cast<const uint4 *>(ks + x / cols * k_head + x % cols * 16));
+        b[q] = __ldcs(reinterpret_cast<const uint4 *>(vs + x / cols * v_head + x % cols * 16));
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int x = x0 + q * kWarp;
+      if (x < units) {
+        *reinterpret_cast<uint4 *>(kd + x / cols * c.k_head + x % cols * 16) = a[q];
+        *reinterpret_cast<uint4 *>(vd + x / cols * c.v_head + x % cols * 16) = b[q];
+      }
+    }
+  }
+}
+
+// Kept rows move down.  A warp takes one (sequence, layer, head, up to 512
+// bytes of the row) of k or v and walks its rows in order, a batch of rows at
+// a time: all of a batch's loads, then its stores.  Row t comes from keep[t]
+// >= t, so a batch's destinations lie before every later batch's sources,
+// and within a batch the loads come first: the move is in place.
+__global__ void __launch_bounds__(kMoveThreads) compact_kernel(ns_kv_pages c, const int32_t *seqs,
+                                                               const int32_t *base, const int32_t *keep, int keep_ld,
+                                                               const int32_t *n_keep, int n, int segs,
+                                                               uint32_t *err) {
+  const int lane = threadIdx.x & 31;
+  const long long it = (long long)blockIdx.x * kMoveWarps + (threadIdx.x >> 5);
+  const long long items = (long long)n * c.layers * c.heads * 2 * segs;
+  if (it >= items) return;
+  const int kv = (int)(it & 1);
+  long long u = it >> 1;
+  const int seg = (int)(u % segs);
+  u /= segs;
+  const int head = (int)(u % c.heads), layer = (int)(u / c.heads % c.layers), i = (int)(u / c.heads / c.layers);
+  const int s = seqs[i], m = n_keep[i], b0 = base[i];
+  bool ok = seq_ok(c, s) && m >= 0 && m <= keep_ld && b0 >= 0;
+  if (ok) {  // the first of a repeated sequence only
+    int hit = 0;
+    for (int j = lane; j < i; j += kWarp) hit |= seqs[j] == s;
+    ok = !__any_sync(0xffffffffu, hit);
+  }
+  const int len = ok ? c.lengths[s] : 0;
+  if (!ok || !len_ok(c, len)) {
+    if (lane == 0) set_flag(err, NS_FLAG_BAD_SEQ);
+    return;
+  }
+  const int32_t *row = c.table + (size_t)s * c.table_ld;
+  const int32_t *kp = keep + (size_t)i * keep_ld;
+  const int64_t sp = kv ? c.v_page : c.k_page, st = kv ? c.v_token : c.k_token;
+  char *data = static_cast<char *>(kv ? c.v : c.k) + layer * (kv ? c.v_layer : c.k_layer) +
+               head * (kv ? c.v_head : c.k_head) + seg * 512;
+  const int cols = min(c.row_bytes - seg * 512, 512) / 16;  // lanes a row takes
+  const int per = kWarp / cols;                             // rows a warp moves at once
+  const int sub = lane / cols, col = lane % cols;
+  for (int t0 = 0; t0 < m; t0 += per * kUnroll) {
+    uint4 val[kUnroll];
+    char *to[kUnroll];
+#pragma unroll
+    for (int q = 0; q < kUnroll; ++q) {
+      const int t = t0 + q * per + sub;
+      to[q] = nullptr;
+      if (sub < per && t < m) {
+        const int from = kp[t];
+        if (from < t || (t > 0 && from <= kp[t - 1]) || (long long)b0 + from >= len) {
+          set_flag(err, NS_FLAG_BAD_SEQ);
+        } else if (from != t) {
+          const int p = b0 + from, d = b0 + t;
+          const int pa = row[p / c.page_size], pb = row[d / c.page_size];
+          if (pa < 0 || pa >= c.pages || pb < 0 || pb >= c.pages) {
+            set_flag(err, NS_FLAG_BAD_ID);
+          } else if (c.refs[pb] > 1) {
+            set_flag(err, NS_FLAG_SHARED_PAGE);
+          } else {
+            val[q] = *reinterpret_cast<const uint4 *>(data + pa * sp + p % c.page_size * st + col * 16);
+            to[q] = data + pb * sp + d % c.page_size * st + col * 16;
+          }
+        }
+      }
+    }
+    __syncwarp();  // every load of the batch before its stores
+#pragma unroll
+    for (int q = 0; q < kUnroll; ++q)
+      if (to[q]) *reinterpret_cast<uint4 *>(to[q]) = val[q];
+    __syncwarp();
+  }
+}
+
+unsigned grid_for(long long items, long long most) {
+  const long long g = (items + kMoveWarps - 1) / kMoveWarps;
+  return (unsigned)(g < 1 ? 1 : g > most ? most : g);
+}
+
+}  // namespace
+
+cudaError_t launch_pages_truncate(const ns_kv_pages &c, const int32_t *seqs, const int32_t *new_len, int n,
+                                  uint32_t *err, cudaStream_t st) {
+  truncate_kernel<<<n, kSeqThreads, 0, st>>>(c, seqs, new_len, nullptr, 0x7fffffff, err);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_pages_fork(const ns_kv_pages &c, const int32_t *src, const int32_t *dst, int n, uint32_t *err,
+                              cudaStream_t st) {
+  fork_kernel<<<n, kSeqThreads, 0, st>>>(c, src, dst, n, err);
+  return cudaGetLastError();
+}
+
+int64_t pages_extend_ws(const ns_kv_pages &c, int n) { return 4 * (4 + 6 * (int64_t)n + c.pages); }
+
+cudaError_t launch_pages_extend(const ns_kv_pages &c, const int32_t *seqs, const int32_t *n_new, int n, void *ws,
+                                uint32_t *err, cudaStream_t st) {
+  extend_kernel<<<1, kExtendThreads, 0, st>>>(c, seqs, n_new, n, ws, err);
+  const ExtendWs w(ws, n);
+  const unsigned grid = grid_for((long long)n * c.layers * c.heads * 2, 2432);
+  copy_pages_kernel<<<grid, kMoveThreads, 0, st>>>(c, w.src, w.dst, w.n_copies, n, err);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_pages_write(const ns_kv_pages &c, int layer, const int32_t *seqs, const int32_t *cu, int n,
+                               const void *k_new, const void *v_new, int64_t k_token, int64_t k_head,
+                               int64_t v_token, int64_t v_head, int tokens, uint32_t *err, cudaStream_t st) {
+  write_kernel<<<(tokens + kMoveWarps - 1) / kMoveWarps, kMoveThreads, 0, st>>>(
+      c, layer, seqs, cu, n, static_cast<const char *>(k_new), static_cast<const char *>(v_new), k_token, k_head,
+      v_token, v_head, tokens, err);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_pages_compact(const ns_kv_pages &c, const int32_t *seqs, const int32_t *base, const int32_t *keep,
+                                 int keep_ld, const int32_t *n_keep, int n, uint32_t *err, cudaStream_t st) {
+  const int segs = (c.row_bytes + 511) / 512;
+  const long long items = (long long)n * c.layers * c.heads * 2 * segs;
+  if ((items + kMoveWarps - 1) / kMoveWarps > 0x7fffffffLL) return cudaErrorInvalidValue;
+  if (keep_ld > 0)
+    compact_kernel<<<(unsigned)((items + kMoveWarps - 1) / kMoveWarps), kMoveThreads, 0, st>>>(
+        c, seqs, base, keep, keep_ld, n_keep, n, segs, err);
+  truncate_kernel<<<n, kSeqThreads, 0, st>>>(c, seqs, n_keep, base, keep_ld, err);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_pages_copy(const ns_kv_pages &c, const int32_t *src, const int32_t *dst, int n, uint32_t *err,
+                              cudaStream_t st) {
+  copy_pages_kernel<<<grid_for((long long)n * c.layers * c.heads * 2, 2432), kMoveThreads, 0, st>>>(c, src, dst,
+                                                                                                   nullptr, n, err);
+  return cudaGetLastError();
+}
+
+}  // namespace ns

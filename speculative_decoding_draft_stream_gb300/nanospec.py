@@ -28,7 +28,7 @@ MAX_SELECT_K = 16
 MAX_TOPK = 32
 MAX_ROWS = 64
 
-# Every entry point declared in include/nanospec.h.
+# Every entry point declared in include/.
 EXPORTED = (
     "ns_status_string", "ns_create", "ns_destroy", "ns_device_bytes", "ns_stream_init", "ns_stream_append",
     "ns_build_active_vocab", "ns_gather_head_rows", "ns_sub_lm_head_logits_topk", "ns_step",
@@ -37,6 +37,10 @@ EXPORTED = (
     "ns_slot_lm_head_logits_topk", "ns_step_slots", "ns_get_slots", "ns_step_batch", "ns_sub_lm_head_indexed_topk",
     "ns_step_launches", "ns_step_batch_union", "ns_get_union", "ns_set_copy_ctas", "ns_step_host",
     "ns_step_slots_fused", "ns_state_export_bytes", "ns_state_export", "ns_state_import",
+    # include/nanospec_ops.h (bound in serving.py)
+    "ns_ops_get_error", "ns_attend_prompt", "ns_attend_paged_workspace", "ns_attend_paged", "ns_pages_truncate",
+    "ns_pages_fork", "ns_pages_workspace", "ns_pages_extend", "ns_pages_write", "ns_pages_compact", "ns_pages_copy",
+    "ns_token_logprobs",
 )
 NOALLOC_MAX_LOGITS = 1 << 20
 
@@ -101,6 +105,19 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "ns_step_batch_union": (I32, [P, I32, P, I32, P, I32, ctypes.POINTER(I32), U16P, U16P, I32, I32, P, I32, P,
                                       P, P]),
         "ns_get_union": (I32, [P] + [ctypes.POINTER(P)] * 4 + [ctypes.POINTER(I64)]),
+        "ns_ops_get_error": (I32, [ctypes.POINTER(ctypes.c_uint32), I32]),
+        "ns_attend_prompt": (I32, [P] * 3 + [I32] * 5 + [I64] * 6 + [P, I32, I32, ctypes.c_float, P, P, P]),
+        "ns_attend_paged_workspace": (I64, [I32] * 5),
+        "ns_attend_paged": (I32, [P] + [I32] * 6 + [I64] * 3 + [P, P, I32, I32] + [I64] * 6 +
+                            [P, I32, I32, P, P, P, ctypes.c_float, I32, P, P, P, I64, P]),
+        "ns_pages_truncate": (I32, [P, P, P, I32, P]),
+        "ns_pages_fork": (I32, [P, P, P, I32, P]),
+        "ns_pages_workspace": (I64, [P, I32]),
+        "ns_pages_extend": (I32, [P, P, P, I32, P, I64, P]),
+        "ns_pages_write": (I32, [P, I32, P, P, I32, P, P] + [I64] * 4 + [I32, P]),
+        "ns_pages_compact": (I32, [P, P, P, P, I32, P, I32, P]),
+        "ns_pages_copy": (I32, [P, P, P, I32, P]),
+        "ns_token_logprobs": (I32, [P, I32, I32, I32, I64, ctypes.c_float, P, I32, I32] + [P] * 6),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)

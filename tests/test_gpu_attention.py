@@ -1,0 +1,520 @@
+"""attend_prompt and attend_paged against softmax attention in 64 bits."""
+
+import random
+
+import pytest
+import torch
+
+from serving_ref import attend_rows, check
+
+pytestmark = pytest.mark.gpu
+
+BF16, F16 = torch.bfloat16, torch.float16
+
+
+@pytest.fixture(scope="module")
+def ns():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA GPU")
+    import speculative_decoding_draft_stream_gb300 as p
+    from speculative_decoding_draft_stream_gb300 import build
+
+    build.build()
+    p.ops_error(clear=True)
+    return p
+
+
+def gen(seed):
+    g = torch.Generator()
+    g.manual_seed(seed)
+    return g
+
+
+def normal(g, shape, dtype, std=1.0):
+    return (torch.randn(shape, generator=g) * std).to(dtype)
+
+
+# ---------------------------------------------------------------------------
+# Whole prompts
+# ---------------------------------------------------------------------------
+def run_prompt(ns, lens, hq, hkv, d, dtype, seed, layout="packed", std=1.0, poison=None, scale=None, max_len=None):
+    g = gen(seed)
+    T = sum(lens)
+    cu = [0]
+    for n in lens:
+        cu.append(cu[-1] + n)
+    q, k, v = normal(g, (T, hq, d), dtype, std), normal(g, (T, hkv, d), dtype, std), normal(g, (T, hkv, d), dtype)
+    if poison is not None:
+        poison(q, k, v, cu)
+    if layout == "packed":
+        dq, dk, dv = q.cuda(), k.cuda(), v.cuda()
+    elif layout == "fused":  # slices of one projection's rows
+        row = torch.cat([q, k, v], 1).cuda()
+        dq, dk, dv = row[:, :hq], row[:, hq:hq + hkv], row[:, hq + hkv:]
+    else:  # heads outermost
+        dq, dk, dv = (t.transpose(0, 1).contiguous().cuda().transpose(0, 1) for t in (q, k, v))
+    scale = d ** -0.5 if scale is None else scale
+    out, lse = ns.attend_prompt(dq, dk, dv, torch.tensor(cu, dtype=torch.int32).cuda(),
+                                max(lens) if max_len is None else max_len, scale=scale)
+    out, lse = out.cpu(), lse.cpu()
+    for a, b in zip(cu[:-1], cu[1:]):
+        sees = torch.ones(b - a, b - a, dtype=torch.bool).tril()
+        for h in range(hq):
+            kh = h // (hq // hkv)
+            o, z, to, tz = attend_rows(q[a:b, h], k[a:b, kh], v[a:b, kh], sees, scale)
+            check(out[a:b, h], o, to, f"out of {a}:{b} head {h}")
+            check(lse[a:b, h], z, tz, f"lse of {a}:{b} head {h}")
+    assert ns.ops_error() == 0
+
+
+EDGES = [0, 1, 2, 0, 15, 16, 17, 63, 64, 65, 127, 128, 129, 200, 255, 256, 257, 0]
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("d", [64, 128])
+def test_prompt_lengths(ns, dtype, d):
+    run_prompt(ns, EDGES, 4, 2, d, dtype, 1)
+
+
+@pytest.mark.parametrize("hq,hkv", [(1, 1), (7, 1), (14, 2), (8, 8), (16, 1), (12, 4)])
+def test_prompt_heads(ns, hq, hkv):
+    run_prompt(ns, [70, 1, 130], hq, hkv, 128, BF16, 2)
+    run_prompt(ns, [70, 1, 130], hq, hkv, 64, F16, 3)
+
+
+@pytest.mark.parametrize("layout", ["fused", "heads"])
+def test_prompt_strides(ns, layout):
+    run_prompt(ns, [33, 129, 300], 6, 2, 128, BF16, 4, layout)
+    run_prompt(ns, [33, 129, 300], 6, 2, 64, F16, 5, layout)
+
+
+@pytest.mark.parametrize("n", [511, 513, 1000, 1537])
+def test_prompt_longer(ns, n):
+    run_prompt(ns, [n, 3], 3, 1, 128, BF16, n)
+    run_prompt(ns, [n, 3], 2, 1, 64, F16, n)
+
+
+def test_prompt_peaked_scores(ns):
+    """Scores of a few hundred: one key has nearly all the probability."""
+    run_prompt(ns, [300, 90], 2, 1, 128, BF16, 6, std=6.0)
+    run_prompt(ns, [300, 90], 2, 1, 128, F16, 7, std=6.0)
+
+
+def test_prompt_rising_and_falling_scores(ns):
+    """The running maximum grows with every key, or was largest at the first."""
+    def ramp(sign):
+        def f(q, k, v, cu):
+            for a, b in zip(cu[:-1], cu[1:]):
+                q[a:b] = 1.0
+                k[a:b] = (sign * torch.arange(b - a) / 16.0)[:, None, None].to(k.dtype)
+        return f
+    run_prompt(ns, [700], 2, 1, 128, BF16, 8, poison=ramp(1.0))
+    run_prompt(ns, [700], 2, 1, 128, BF16, 9, poison=ramp(-1.0))
+
+
+def test_prompt_lowest_values(ns):
+    """Scores near the type's lowest value for some keys (a mask by addition ends there)."""
+    def low(q, k, v, cu):
+        q[:, :, 1:] = 0
+        q[:, :, 0] = 1.0
+        k[:, :, 0] = torch.where(torch.arange(k.shape[0])[:, None] % 3 == 1, torch.finfo(k.dtype).min, 0.5).to(k.dtype)
+    run_prompt(ns, [200, 70], 2, 1, 64, BF16, 10, poison=low)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("what", [float("nan"), float("inf"), float("-inf")])
+def test_prompt_wild_values_reach_only_rows_that_see_them(ns, d, what):
+    """Values that are not finite: rows before them, and other sequences, do not see them."""
+    def wild(q, k, v, cu):
+        v[cu[1] + 70, 0, 5] = what
+        v[cu[2] - 1, 0, d - 1] = what
+        v[cu[3], 0, 0] = what
+    # the reference says NaN for every row that sees one; an infinity alone gives infinities there
+    g = gen(11)
+    lens, hq = [40, 150, 64, 200], 2
+    cu = [0, 40, 190, 254, 454]
+    q, k, v = normal(g, (454, hq, d), BF16), normal(g, (454, 1, d), BF16), normal(g, (454, 1, d), BF16)
+    wild(q, k, v, cu)
+    out, lse = ns.attend_prompt(q.cuda(), k.cuda(), v.cuda(), torch.tensor(cu, dtype=torch.int32).cuda(), max(lens))
+    out = out.cpu()
+    for a, b in zip(cu[:-1], cu[1:]):
+        sees = torch.ones(b - a, b - a, dtype=torch.bool).tril()
+        for h in range(hq):
+            o, z, to, tz = attend_rows(q[a:b, h], k[a:b, 0], v[a:b, 0], sees, d ** -0.5)
+            bad = torch.isnan(o)
+            assert not torch.isfinite(out[a:b, h][bad]).any()
+            check(out[a:b, h].double().masked_fill(bad, 0), o.masked_fill(bad, 0), to, "rows that see none")
+
+
+def test_prompt_wild_keys_of_other_rows(ns):
+    """Keys that are not finite: rows before them, and other sequences, are as without them."""
+    g = gen(12)
+    cu = [0, 100, 230]
+    q, k, v = normal(g, (230, 2, 128), BF16), normal(g, (230, 1, 128), BF16), normal(g, (230, 1, 128), BF16)
+    bounds = torch.tensor(cu, dtype=torch.int32).cuda()
+    clean, _ = ns.attend_prompt(q.cuda(), k.cuda(), v.cuda(), bounds, 130)
+    k[90:100], k[200:230] = float("nan"), float("inf")
+    out, _ = ns.attend_prompt(q.cuda(), k.cuda(), v.cuda(), bounds, 130)
+    assert torch.equal(out[:90], clean[:90]) and torch.equal(out[100:200], clean[100:200])
+    assert torch.isnan(out[95]).all()
+
+
+def test_prompt_bound_on_lengths(ns):
+    """max_len only bounds: a larger one changes nothing; tokens past a smaller one are left and flagged."""
+    g = gen(13)
+    q, k, v = normal(g, (300, 2, 64), BF16).cuda(), normal(g, (300, 2, 64), BF16).cuda(), normal(g, (300, 2, 64), BF16).cuda()
+    cu = torch.tensor([0, 100, 300], dtype=torch.int32).cuda()
+    a, la = ns.attend_prompt(q, k, v, cu, 200)
+    b, lb = ns.attend_prompt(q, k, v, cu, 5000)
+    assert torch.equal(a, b) and torch.equal(la, lb) and ns.ops_error() == 0
+    ns.attend_prompt(q, k, v, cu, 150)
+    assert ns.ops_error(clear=True) == ns.FLAG_BAD_SEQ
+
+
+def test_prompt_offsets_past_32_bits(ns):
+    """Token strides that put the last rows past 2^32 elements."""
+    T, step = 520, 1 << 23
+    g = gen(14)
+    vals = [normal(g, (T, 1, 64), BF16) for _ in range(3)]
+    buf = torch.empty(T * step, dtype=BF16, device="cuda")
+    views = []
+    for i, t in enumerate(vals):
+        w = buf.as_strided((T, 1, 64), (step, 64, 1), i * 64)
+        w.copy_(t)
+        views.append(w)
+    cu = torch.tensor([0, T], dtype=torch.int32).cuda()
+    out, lse = ns.attend_prompt(*views, cu, T)
+    want, wl = ns.attend_prompt(*(t.cuda() for t in vals), cu, T)
+    assert torch.equal(out, want) and torch.equal(lse, wl)
+
+
+def test_prompt_other_stream_and_outputs(ns):
+    g = gen(15)
+    q, k, v = (normal(g, (100, 2, 128), F16).cuda() for _ in range(3))
+    cu = torch.tensor([0, 60, 100], dtype=torch.int32).cuda()
+    want, wl = ns.attend_prompt(q, k, v, cu, 60)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    out, lse = torch.empty_like(want), torch.empty_like(wl)
+    r = ns.attend_prompt(q, k, v, cu, 60, out=out, lse=lse, stream=s)
+    s.synchronize()
+    assert r[0] is out and torch.equal(out, want) and torch.equal(lse, wl)
+
+
+def test_prompt_repeats_bit_for_bit(ns):
+    g = gen(16)
+    q, k, v = normal(g, (900, 8, 128), BF16).cuda(), normal(g, (900, 2, 128), BF16).cuda(), normal(g, (900, 2, 128), BF16).cuda()
+    cu = torch.tensor([0, 650, 900], dtype=torch.int32).cuda()
+    a, la = ns.attend_prompt(q, k, v, cu, 650)
+    for _ in range(5):
+        b, lb = ns.attend_prompt(q, k, v, cu, 650)
+        assert torch.equal(a, b) and torch.equal(la, lb)
+
+
+def test_prompt_refusals(ns):
+    q = torch.zeros(10, 4, 64, dtype=BF16, device="cuda")
+    k = torch.zeros(10, 2, 64, dtype=BF16, device="cuda")
+    cu = torch.tensor([0, 10], dtype=torch.int32, device="cuda")
+    bad = [
+        lambda: ns.attend_prompt(q.float(), k.float(), k.float(), cu, 10),
+        lambda: ns.attend_prompt(q, k.half(), k, cu, 10),
+        lambda: ns.attend_prompt(q, k[:, :, :32], k[:, :, :32], cu, 10),
+        lambda: ns.attend_prompt(q[:, :3], k, k, cu, 10),
+        lambda: ns.attend_prompt(q, k, k, cu.long(), 10),
+        lambda: ns.attend_prompt(q, k, k, cu.cpu(), 10),
+        lambda: ns.attend_prompt(q.cpu(), k, k, cu, 10),
+        lambda: ns.attend_prompt(q, k, k, cu, 10, out=torch.empty(10, 4, 64, device="cuda")),
+        lambda: ns.attend_prompt(q.transpose(1, 2), k, k, cu, 10),
+    ]
+    for f in bad:
+        with pytest.raises(ValueError):
+            f()
+    worse = [
+        lambda: ns.attend_prompt(q, k, k, cu, -1),
+        lambda: ns.attend_prompt(q, k, k, cu, 10, scale=0.0),
+        lambda: ns.attend_prompt(q, k, k, cu, 10, scale=float("nan")),
+        lambda: ns.attend_prompt(torch.zeros(10, 4, 32, dtype=BF16, device="cuda"),
+                                 *[torch.zeros(10, 2, 32, dtype=BF16, device="cuda")] * 2, cu, 10),
+        # rows that begin off a 16-byte boundary
+        lambda: ns.attend_prompt(torch.zeros(10, 4, 65, dtype=BF16, device="cuda")[:, :, 1:], k, k, cu, 10),
+        lambda: ns.attend_prompt(q, torch.zeros(10, 2, 68, dtype=BF16, device="cuda")[:, :, :64], k, cu, 10),
+    ]
+    for f in worse:
+        with pytest.raises(ns.NanoSpecError):
+            f()
+    assert ns.attend_prompt(q[:0], k[:0], k[:0], cu[:1], 0)[0].shape == (0, 4, 64)
+    # bounds that leave the tokens are skipped and flagged
+    ns.attend_prompt(q, k, k, torch.tensor([0, 11], dtype=torch.int32, device="cuda"), 10)
+    assert ns.ops_error(clear=True) == ns.FLAG_BAD_SEQ
+
+
+# ---------------------------------------------------------------------------
+# New tokens over a paged cache
+# ---------------------------------------------------------------------------
+def make_cache(g, rng, lens, hkv, P, d, dtype, layout="heads", spare=3):
+    """A pool whose unused rows hold NaN, the sequences' keys and values, and their table."""
+    held = [-(-n // P) for n in lens]
+    pages = sum(held) + spare
+    order = list(range(pages))
+    rng.shuffle(order)
+    table = torch.full((len(lens), max(held + [1]) + 2), -1, dtype=torch.int32)
+    kp = torch.full((pages, hkv, P, d), float("nan"), dtype=dtype)
+    vp = torch.full((pages, hkv, P, d), float("nan"), dtype=dtype)
+    keys, vals, at = [], [], 0
+    for b, n in enumerate(lens):
+        k, v = normal(g, (n, hkv, d), dtype), normal(g, (n, hkv, d), dtype)
+        keys.append(k)
+        vals.append(v)
+        for slot in range(held[b]):
+            page = order[at]
+            at += 1
+            table[b, slot] = page
+            m = min(P, n - slot * P)
+            kp[page, :, :m] = k[slot * P:slot * P + m].transpose(0, 1)
+            vp[page, :, :m] = v[slot * P:slot * P + m].transpose(0, 1)
+    if layout == "tokens":  # [pages, page, heads, dim] in memory
+        dk, dv = (t.transpose(1, 2).contiguous().cuda().transpose(1, 2) for t in (kp, vp))
+    elif layout == "joint":  # keys and values of a page next to each other
+        both = torch.stack([kp, vp], 1).cuda()
+        dk, dv = both[:, 0], both[:, 1]
+    else:
+        dk, dv = kp.cuda(), vp.cuda()
+    return dk, dv, table, keys, vals
+
+
+def tree_masks(rng, B, n):
+    rows = []
+    for _ in range(B):
+        bits = []
+        for i in range(n):
+            parent = rng.randrange(-1, i) if i else -1
+            bits.append((1 << i) | (bits[parent] if parent >= 0 else 0))
+        rows.append(bits)
+    return rows
+
+
+def signed(rows):
+    return torch.tensor([[b - (1 << 64) if b >> 63 else b for b in r] for r in rows], dtype=torch.int64)
+
+
+def run_paged(ns, lens, n, hq, hkv, d, P, dtype, seed, layout="heads", masks=None, max_len=0, order=None):
+    g, rng = gen(seed), random.Random(seed)
+    dk, dv, table, keys, vals = make_cache(g, rng, lens, hkv, P, d, dtype, layout)
+    order = list(range(len(lens))) if order is None else order
+    B = len(order)
+    q = normal(g, (B, n, hq, d), dtype)
+    if masks == "tree":
+        masks = tree_masks(rng, B, n)
+    out, lse = ns.attend_paged(q.cuda(), dk, dv, table.cuda(), torch.tensor(lens, dtype=torch.int32).cuda(),
+                               torch.tensor(order, dtype=torch.int32).cuda(),
+                               mask=None if masks is None else signed(masks).cuda(), max_len=max_len)
+    out, lse = out.cpu(), lse.cpu()
+    grp = hq // hkv
+    for b, s in enumerate(order):
+        N = lens[s]
+        sees = torch.zeros(n, N, dtype=torch.bool)
+        for i in range(n):
+            word = (1 << (i + 1)) - 1 if masks is None else masks[b][i]
+            for p in range(N):
+                j = p - (N - n)
+                sees[i, p] = j < 0 or bool(word >> j & 1)
+        for h in range(hq):
+            o, z, to, tz = attend_rows(q[b, :, h], keys[s][:, h // grp], vals[s][:, h // grp], sees, d ** -0.5)
+            check(out[b, :, h], o, to, f"out of sequence {s} head {h}")
+            check(lse[b, :, h], z, tz, f"lse of sequence {s} head {h}")
+    assert ns.ops_error() == 0
+
+
+RAGGED = [1, 2, 7, 8, 9, 15, 16, 17, 31, 63, 64, 65, 127, 128, 129, 300]
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("P", [8, 16, 64, 256])
+def test_paged_one_token(ns, dtype, d, P):
+    run_paged(ns, RAGGED, 1, 8, 2, d, P, dtype, P + d)
+
+
+@pytest.mark.parametrize("hq,hkv", [(1, 1), (7, 1), (28, 4), (8, 8), (16, 1), (17, 1), (32, 1), (64, 1)])
+def test_paged_heads(ns, hq, hkv):
+    run_paged(ns, [5, 200, 1], 1, hq, hkv, 128, 16, BF16, hq)
+    run_paged(ns, [5, 200, 1], 1, hq, hkv, 64, 32, F16, hq)
+
+
+@pytest.mark.parametrize("n", [2, 3, 5, 16, 17, 33, 63, 64])
+def test_paged_chain_of_new_tokens(ns, n):
+    run_paged(ns, [n, n + 1, n + 63, n + 64, 200 + n], n, 4, 1, 128, 16, BF16, n)
+    run_paged(ns, [n, n + 130], n, 2, 2, 64, 8, F16, n)
+
+
+@pytest.mark.parametrize("n", [1, 4, 10, 60, 64])
+def test_paged_draft_tree(ns, n):
+    run_paged(ns, [n, n + 1, n + 100, n + 517], n, 8, 2, 128, 16, BF16, n, masks="tree")
+    run_paged(ns, [n, n + 77], n, 7, 1, 64, 64, F16, n, masks="tree")
+
+
+@pytest.mark.parametrize("layout", ["tokens", "joint"])
+def test_paged_cache_layouts(ns, layout):
+    run_paged(ns, [100, 1, 333], 1, 8, 2, 128, 16, BF16, 21, layout)
+    run_paged(ns, [100, 33, 333], 20, 8, 2, 64, 32, F16, 22, layout, masks="tree")
+
+
+def test_paged_empty_sequences_and_rows(ns):
+    """Lengths of zero, fewer positions than new tokens, and masks that leave nothing."""
+    run_paged(ns, [0, 40, 0, 1], 1, 8, 2, 128, 16, BF16, 23)
+    run_paged(ns, [0, 2, 5, 80], 5, 8, 2, 128, 16, BF16, 24)
+    nothing = [[0, 1, 0, 7, 0]] * 3
+    run_paged(ns, [5, 4, 90], 5, 4, 1, 64, 8, F16, 25, masks=nothing)
+    run_paged(ns, [1, 30], 1, 4, 1, 64, 8, F16, 26, masks=[[0], [0]])
+
+
+def test_paged_sequences_in_any_order(ns):
+    run_paged(ns, [30, 500, 7, 64, 129], 1, 8, 2, 128, 16, BF16, 27, order=[3, 0, 4])
+
+
+@pytest.mark.parametrize("max_len", [1, 100, 1 << 20])
+def test_paged_bound_only_sizes_the_launch(ns, max_len):
+    run_paged(ns, [700, 3, 64], 1, 8, 2, 128, 16, BF16, 28, max_len=max_len)
+    run_paged(ns, [700, 30, 64], 9, 8, 2, 128, 16, BF16, 29, max_len=max_len, masks="tree")
+
+
+@pytest.mark.parametrize("lens", [[5000], [9001, 1], [3333, 2, 4000, 64]])
+def test_paged_split_and_joined(ns, lens):
+    """Few rows and long caches: every item is shared by many CTAs."""
+    run_paged(ns, lens, 1, 4, 1, 128, 16, BF16, 30)
+    run_paged(ns, [x + 20 for x in lens], 20, 4, 1, 64, 64, F16, 31, masks="tree")
+
+
+def test_paged_many_short_sequences(ns):
+    rng = random.Random(32)
+    run_paged(ns, [rng.randrange(0, 40) for _ in range(700)], 1, 2, 1, 64, 8, BF16, 32)
+
+
+def test_paged_wild_values_of_hidden_nodes(ns):
+    """A tree node whose values are not finite reaches only the nodes that see it."""
+    for n, lens in ((10, [10, 150]), (40, [41, 200])):
+        g, rng = gen(33), random.Random(33)
+        dk, dv, table, keys, vals = make_cache(g, rng, lens, 1, 16, 128, BF16)
+        masks = tree_masks(rng, 2, n)
+        q = normal(g, (2, n, 4, 128), BF16)
+        for b, N in enumerate(lens):
+            pos = N - n + n // 2
+            vals[b][pos, 0, 3] = float("nan")
+            vals[b][N - 1, 0, 64] = float("inf")
+            dv[table[b, pos // 16], 0, pos % 16, 3] = float("nan")
+            dv[table[b, (N - 1) // 16], 0, (N - 1) % 16, 64] = float("inf")
+        out, _ = ns.attend_paged(q.cuda(), dk, dv, table.cuda(), torch.tensor(lens, dtype=torch.int32).cuda(),
+                                 torch.tensor([0, 1], dtype=torch.int32).cuda(), mask=signed(masks).cuda())
+        out = out.cpu()
+        for b, N in enumerate(lens):
+            sees = torch.tensor([[p < N - n or bool(masks[b][i] >> (p - N + n) & 1) for p in range(N)] for i in range(n)])
+            for h in range(4):
+                o, _, to, _ = attend_rows(q[b, :, h], keys[b][:, 0], vals[b][:, 0], sees, 128 ** -0.5)
+                bad = torch.isnan(o)
+                assert bad.any() and not bad.all()
+                assert not torch.isfinite(out[b, :, h][bad]).any()
+                check(out[b, :, h].double().masked_fill(bad, 0), o.masked_fill(bad, 0), to, "nodes that see none")
+
+
+def test_paged_offsets_past_32_bits(ns):
+    """Pages whose elements lie past 2^32."""
+    hkv, P, d = 8, 64, 128
+    pages = (1 << 32) // (hkv * P * d) + 9
+    pool = torch.empty((pages, hkv, P, d), dtype=BF16, device="cuda")
+    g = gen(34)
+    lens = [200, 130]
+    small = normal(g, (8, hkv, P, d), BF16).cuda()
+    pool[pages - 8:] = small
+    table = torch.tensor([[0, 3, 5, 1], [7, 2, 6, -1]], dtype=torch.int32)
+    q = normal(g, (2, 1, 32, d), BF16).cuda()
+    le, se = torch.tensor(lens, dtype=torch.int32).cuda(), torch.tensor([0, 1], dtype=torch.int32).cuda()
+    want, wl = ns.attend_paged(q, small, small, table.cuda(), le, se)
+    far = torch.where(table >= 0, table + (pages - 8), table).cuda()
+    out, lse = ns.attend_paged(q, pool, pool, far, le, se)
+    assert torch.equal(out, want) and torch.equal(lse, wl) and ns.ops_error() == 0
+
+
+def test_paged_bad_ids_are_skipped_and_flagged(ns):
+    g, rng = gen(35), random.Random(35)
+    dk, dv, table, keys, vals = make_cache(g, rng, [100, 60], 2, 16, 64, BF16)
+    dk.nan_to_num_(), dv.nan_to_num_()
+    q = normal(g, (2, 1, 4, 64), BF16).cuda()
+    le, se = torch.tensor([100, 60], dtype=torch.int32).cuda(), torch.tensor([0, 1], dtype=torch.int32).cuda()
+    want, _ = ns.attend_paged(q, dk, dv, table.cuda(), le, se)
+    t = table.clone()
+    t[0, 2] = 1 << 20
+    out, _ = ns.attend_paged(q, dk, dv, t.cuda(), le, se)
+    assert ns.ops_error(clear=True) == 0x1 and torch.equal(out[1], want[1])
+    out, lse = ns.attend_paged(q, dk, dv, table.cuda(), le, torch.tensor([7, 1], dtype=torch.int32).cuda())
+    assert ns.ops_error(clear=True) == ns.FLAG_BAD_SEQ and torch.equal(out[1], want[1])
+    assert (out[0] == 0).all() and torch.isinf(lse[0]).all()
+    out, _ = ns.attend_paged(q, dk, dv, table.cuda(), torch.tensor([-5, 60], dtype=torch.int32).cuda(), se)
+    assert ns.ops_error(clear=True) == ns.FLAG_BAD_SEQ and torch.equal(out[1], want[1]) and (out[0] == 0).all()
+
+
+def test_paged_workspace_stream_and_repeats(ns):
+    g, rng = gen(36), random.Random(36)
+    lens = [3000, 40]
+    dk, dv, table, _, _ = make_cache(g, rng, lens, 2, 16, 128, BF16)
+    q = normal(g, (2, 1, 8, 128), BF16).cuda()
+    args = (q, dk, dv, table.cuda(), torch.tensor(lens, dtype=torch.int32).cuda(),
+            torch.tensor([0, 1], dtype=torch.int32).cuda())
+    want, wl = ns.attend_paged(*args)
+    need = ns.load_library().ns_attend_paged_workspace(2, 1, 8, 2, 128)
+    ws = torch.full((need,), 255, dtype=torch.uint8, device="cuda")
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    for _ in range(5):
+        out, lse = ns.attend_paged(*args, workspace=ws, stream=s)
+    s.synchronize()
+    assert torch.equal(out, want) and torch.equal(lse, wl)
+    with pytest.raises(ns.NanoSpecError):
+        ns.attend_paged(*args, workspace=ws[:need - 1])
+
+
+def test_paged_in_a_graph(ns):
+    """Captured once, replayed with other lengths."""
+    g, rng = gen(37), random.Random(37)
+    lens = [900, 300]
+    dk, dv, table, keys, vals = make_cache(g, rng, lens, 2, 16, 128, BF16)
+    q = normal(g, (2, 1, 8, 128), BF16).cuda()
+    table, le = table.cuda(), torch.tensor(lens, dtype=torch.int32).cuda()
+    se = torch.tensor([0, 1], dtype=torch.int32).cuda()
+    ns.attend_paged(q, dk, dv, table, le, se)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out, lse = ns.attend_paged(q, dk, dv, table, le, se)
+    for new in ([900, 300], [17, 1], [640, 299]):
+        le.copy_(torch.tensor(new, dtype=torch.int32))
+        graph.replay()
+        want, wl = ns.attend_paged(q, dk, dv, table, le, se)
+        assert torch.equal(out, want) and torch.equal(lse, wl)
+
+
+def test_paged_refusals(ns):
+    q = torch.zeros(2, 1, 4, 64, dtype=BF16, device="cuda")
+    k = torch.zeros(6, 2, 16, 64, dtype=BF16, device="cuda")
+    i32 = {"dtype": torch.int32, "device": "cuda"}
+    t, le, se = torch.zeros(3, 2, **i32), torch.zeros(3, **i32), torch.zeros(2, **i32)
+    bad = [
+        lambda: ns.attend_paged(q.float(), k, k, t, le, se),
+        lambda: ns.attend_paged(q, k.half(), k.half(), t, le, se),
+        lambda: ns.attend_paged(q, k, k[:, :1], t, le, se),
+        lambda: ns.attend_paged(q[:, :, :3], k, k, t, le, se),
+        lambda: ns.attend_paged(q, k, k, t, le[:2], se),
+        lambda: ns.attend_paged(q, k, k, t, le, se[:1]),
+        lambda: ns.attend_paged(q, k, k, t.long(), le, se),
+        lambda: ns.attend_paged(q, k, k, t, le, se, mask=torch.zeros(2, 2, dtype=torch.int64, device="cuda")),
+        lambda: ns.attend_paged(q.expand(2, 65, 4, 64), k, k, t, le, se),
+        lambda: ns.attend_paged(q.cpu(), k, k, t, le, se),
+    ]
+    for f in bad:
+        with pytest.raises(ValueError):
+            f()
+    for f in (lambda: ns.attend_paged(q, k[:, :, :12], k[:, :, :12], t, le, se),
+              lambda: ns.attend_paged(q, k, k, t, le, se, scale=-1.0),
+              lambda: ns.attend_paged(q, k, k, t, le, se, max_len=-1),
+              lambda: ns.attend_paged(q[..., :32], k[..., :32], k[..., :32], t, le, se)):
+        with pytest.raises(ns.NanoSpecError):
+            f()
+    assert ns.ops_error() == 0
