@@ -1,108 +1,537 @@
-// Causal attention over whole packed prompts.
+// Causal attention over whole packed prompts, on the 5th-generation tensor
+// cores.
 //
-// A CTA has 64 consecutive tokens of one sequence and one query head; its
-// four warps have 16 rows each and walk the keys up to their own diagonal in
-// tiles of 64, two ahead in flight (cp.async).  The longest blocks come first.
+// Mathematics: for each query row, over its keys in tiles of 128,
+//   x_j = scale log2(e) q . k_j,  m = running bound of max x,
+//   l = sum 2^(x_j - m),  o = sum 2^(x_j - m) v_j;   out = o / l.
+// m is raised (and l and o multiplied by 2^(old - new)) only when a tile's
+// maximum passes it by more than 2^8: any m near the maximum gives the same
+// quotient, and the accumulator in tensor memory is then hardly ever
+// rewritten.  Scores, sums and o are fp32; a probability is rounded once, to
+// the values' type, as an operand of the second product (l sums it
+// unrounded).  fp16 probabilities are kept 2^6 times larger, so that with the
+// 2^8 above they stay within fp16's range, and 2^-30 of the largest is not lost.
+//
+// Rows: the query heads that share a key-value head are packed with their
+// tokens into tiles of 128 rows (128 / group tokens each), so a tile of keys
+// is fetched once for all of them; a work item is two such row tiles.
+//
+// A CTA (one per SM, it keeps taking items, longest first) has five roles:
+//   warp 0     TMA loads: the item's queries, then key and value tiles into a
+//              ring of five;
+//   warp 1     tcgen05.mma: S_i = Q_i K^T into tensor memory, O_i += P_i V
+//              with P_i read from tensor memory, for the row tiles i = 0, 1 in
+//              turn: while one tile's softmax runs, the other's products do;
+//   warp 2     looks through the value tiles that are hidden from some rows
+//              (see below);
+//   warp 3     deals the items;
+//   warps 4-7 and 8-11  softmax of row tile 0 and 1: a thread has a row, reads
+//              its 128 scores, writes its probabilities over them (16 bits
+//              each), and at the item's end scales O and stores it.
+// Tensor memory: S_0, S_1, O_0, O_1, 128 fp32 columns each: all of it.
+//
+// Hidden values: a probability of 0 times a value that is infinite or NaN
+// would be NaN, and the last tiles of an item hold values that some rows may
+// not see: later tokens, and tokens of the next sequence.  Warp 2 looks for
+// such values there; where it finds one it puts 0 in its place and notes, per
+// column, the first position of each kind, from which the rows that do see it
+// set their result.
+//
+// Every wait is bounded (NS_FLAG_TIMEOUT).
+#include "ns_attn_tile.cuh"
 #include "ns_internal.cuh"
 #include "ns_ops.cuh"
-#include "ns_attn_tile.cuh"
+#include "ns_umma_ptx.cuh"
 
 namespace ns {
 namespace {
 
-using namespace attn;
+using attn::Type;
+using attn::ex2;
+using attn::kNegInf;
 
-constexpr int kPrThreads = 128;
-constexpr int kPrRows = 64, kPrKeys = 64, kPrStages = 3;
+constexpr int kFaThreads = 384;
+constexpr int kFaRing = 5;       // key or value tiles in flight
+constexpr int kFaKeys = 128;     // keys of a tile
+constexpr int kFaHalf = 128 * 128;  // bytes of 128 rows of 64 elements
+constexpr float kFaSlack = 8.f;  // log2 of how far scores may pass m before it is raised
+constexpr int kFaChecks = 4;     // value tiles looked through ahead of the product
+
+template <typename T>
+constexpr float kFaOffset = 0.f;
+template <>
+constexpr float kFaOffset<__half> = 6.f;
+
+struct Work {
+  int seq0, len;     // the sequence's first token and its length
+  int tok0;          // first token of row tile 0
+  int unit;          // query heads unit * pack .. + pack - 1
+  int n0, n1;        // key tiles of the row tiles (0: no such row tile); n0 = 0: no more work
+};
+struct Wild {  // first positions of values that are not finite, from the first looked-through tile on
+  uint16_t nan[128], pos[128], neg[128];
+};
+constexpr uint16_t kNever = 0xffff;
 
 template <int D>
-__host__ __device__ constexpr int pr_stage() {
-  return 2 * kPrKeys * D * 2;
+struct FaSmem {
+  static constexpr int kTile = D / 64 * kFaHalf;  // a row tile of queries, or a key or value tile
+  static constexpr int kQ = 0, kKV = 2 * kTile, kMisc = kKV + kFaRing * kTile;
+  // barriers, 8 bytes each
+  static constexpr int kKvFull = kMisc, kKvEmpty = kKvFull + 8 * kFaRing, kQFull = kKvEmpty + 8 * kFaRing,
+                       kQEmpty = kQFull + 8, kSFull = kQEmpty + 8, kPFull = kSFull + 16, kOFull = kPFull + 16,
+                       kOEmpty = kOFull + 16, kCheck = kOEmpty + 16, kWFull = kCheck + 8 * kFaChecks,
+                       kWEmpty = kWFull + 16, kSlot = kWEmpty + 16, kWork = kSlot + 16, kWildAny = kWork + 2 * 32,
+                       kWild = kWildAny + 16, kEnd = kWild + 2 * (int)sizeof(Wild);
+  static constexpr int kBytes = kEnd + 1024;  // the base is rounded up to 1024 bytes
+};
+static_assert(FaSmem<128>::kBytes <= 232448, "shared memory of a CTA");
+constexpr int kWorkReaders = 11;  // producer, MMA, checker, and the eight softmax warps
+
+struct FaArgs {
+  const int32_t *cu;
+  int32_t tokens, n_seqs, max_len, q_heads, group, pack, per_tile, units;
+  float c;  // scale * log2(e)
+  void *out;
+  float *lse;
+  uint32_t *err;
+};
+
+// The position of an item's first value tile that is hidden from some rows.
+__device__ __forceinline__ int first_hidden_tile(const Work &w) { return (w.tok0 + 1) / kFaKeys; }
+
+__device__ __forceinline__ bool get_work(uint32_t base, int full, const uint8_t *g, int work_off, int i, Work &w,
+                                         uint32_t *err) {
+  if (!mbar_wait(base + full + 8 * (i & 1), (i >> 1) & 1, err)) return false;
+  w = *reinterpret_cast<const Work *>(g + work_off + 32 * (i & 1));
+  return w.n0 > 0;
 }
 
-template <typename T, int D>
-__global__ void __launch_bounds__(kPrThreads) prompt_attn_kernel(const PromptAttnArgs a) {
-  constexpr int kLanesRow = D / 8, kPass = kPrThreads / kLanesRow;
-  extern __shared__ __align__(128) uint8_t smem[];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int seq = blockIdx.z, head = blockIdx.y, kvh = head / a.group;
-  const int t0 = a.cu[seq], t1 = a.cu[seq + 1];
-  if (t0 < 0 || t1 < t0 || t1 > a.tokens) {
-    if (tid == 0) set_flag(a.err, NS_FLAG_BAD_SEQ);
-    return;
-  }
-  if (t1 - t0 > a.max_len && blockIdx.x == 0 && tid == 0) set_flag(a.err, NS_FLAG_BAD_SEQ);
-  const int len = min(t1 - t0, a.max_len);
-  const int r0 = ((int)gridDim.x - 1 - (int)blockIdx.x) * kPrRows;
-  if (r0 >= len) return;
-  const uint32_t s0 = (uint32_t)__cvta_generic_to_shared(smem);
-  const T *kb = static_cast<const T *>(a.k) + (int64_t)t0 * a.k_token + (int64_t)kvh * a.k_head;
-  const T *vb = static_cast<const T *>(a.v) + (int64_t)t0 * a.v_token + (int64_t)kvh * a.v_head;
-  const T *qb = static_cast<const T *>(a.q) + (int64_t)t0 * a.q_token + (int64_t)head * a.q_head;
-  const int last = min(len, r0 + kPrRows);  // keys this block sees
-  const int tiles = (last + kPrKeys - 1) / kPrKeys;
-  const int fr = tid / kLanesRow, fc = tid % kLanesRow;
-  auto issue = [&](int t) {
-    if (t < tiles) {
-      const uint32_t sk = s0 + (t % kPrStages) * pr_stage<D>(), sv = sk + kPrKeys * D * 2;
-#pragma unroll
-      for (int pass = 0; pass < kPrKeys / kPass; ++pass) {
-        const int r = pass * kPass + fr, p = t * kPrKeys + r;
-        const bool ok = p < last;
-        const int64_t row = ok ? p : 0;
-        cp16(sk + piece<D>(r, fc), kb + row * a.k_token + fc * 8, ok);
-        cp16(sv + piece<D>(r, fc), vb + row * a.v_token + fc * 8, ok);
+// Warp 3: the items of CTA `cta` in order.  All items, longest first, are in
+// one line: block x of tokens (from the last), sequence, unit; the CTAs take
+// turns forth and back, so each gets a like share of every length.
+template <typename Put>
+__device__ __forceinline__ void deal(const FaArgs &a, int cta, int ctas, const Put &put) {
+  const int lane = threadIdx.x & 31, block = 2 * a.per_tile;
+  const int X = (a.max_len + block - 1) / block;
+  const long long pairs = (long long)X * a.n_seqs;
+  long long before = 0, turn = 0, mine = cta;
+  for (long long p0 = 0; p0 < pairs; p0 += 32) {
+    const long long p = p0 + lane;
+    int x = 0, t0 = 0, len = 0;
+    bool ok = false;
+    if (p < pairs) {
+      const int s = (int)(p % a.n_seqs);
+      x = X - 1 - (int)(p / a.n_seqs);
+      t0 = a.cu[s];
+      const int t1 = a.cu[s + 1];
+      if (t0 < 0 || t1 < t0 || t1 > a.tokens) {
+        if (cta == 0) set_flag(a.err, NS_FLAG_BAD_SEQ);
+      } else {
+        if (t1 - t0 > a.max_len && cta == 0) set_flag(a.err, NS_FLAG_BAD_SEQ);
+        len = min(t1 - t0, a.max_len);
+        ok = (long long)x * block < len;
       }
     }
-    cp_commit();
-  };
-  issue(0);
-  issue(1);
-  uint32_t q[D / 16][4];
-  const int row[2] = {r0 + warp * 16 + (lane >> 2), r0 + warp * 16 + (lane >> 2) + 8};
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const bool ok = row[h] < len;
-    const T *src = qb + (int64_t)(ok ? row[h] : 0) * a.q_token + (lane & 3) * 2;
-#pragma unroll
-    for (int kk = 0; kk < D / 16; ++kk) {
-      q[kk][h] = ok ? *reinterpret_cast<const uint32_t *>(src + kk * 16) : 0u;
-      q[kk][2 + h] = ok ? *reinterpret_cast<const uint32_t *>(src + kk * 16 + 8) : 0u;
+    const uint32_t live = __ballot_sync(0xffffffffu, ok);
+    const long long here = (long long)__popc(live) * a.units;
+    while (mine < before + here) {
+      const int nth = (int)((mine - before) / a.units);
+      const int from = __fns(live, 0, nth + 1);
+      Work w;
+      w.seq0 = __shfl_sync(0xffffffffu, t0, from);
+      w.len = __shfl_sync(0xffffffffu, len, from);
+      w.tok0 = __shfl_sync(0xffffffffu, x, from) * block;
+      w.unit = (int)((mine - before) % a.units);
+      w.n0 = (min(w.len, w.tok0 + a.per_tile) + kFaKeys - 1) / kFaKeys;
+      w.n1 = w.tok0 + a.per_tile < w.len ? (min(w.len, w.tok0 + block) + kFaKeys - 1) / kFaKeys : 0;
+      if (!put(w)) return;
+      ++turn;
+      mine = turn * ctas + ((turn & 1) ? ctas - 1 - cta : cta);
     }
+    before += here;
   }
-  Rows<T, D> rows;
-  rows.clear();
-  const float c = a.scale * kLog2e;
-  for (int t = 0; t < tiles; ++t) {
-    cp_wait<kPrStages - 2>();
-    __syncthreads();
-    issue(t + kPrStages - 1);
-    const uint32_t sk = s0 + (t % kPrStages) * pr_stage<D>(), sv = sk + kPrKeys * D * 2;
-    const int p0 = t * kPrKeys;
-    if (p0 + kPrKeys - 1 <= r0 + warp * 16) {
-      rows.template tile<kPrKeys, false>(q, sk, sv, 0, c, [](int, int) { return false; }, false);
-    } else {
-      const bool wild = __any_sync(0xffffffffu, wild_pieces<T>(sv, kPrKeys * D / 8, lane, kWarp));
-      rows.template tile<kPrKeys, true>(q, sk, sv, 0, c, [&](int h, int key) { return p0 + key > row[h]; }, wild);
-    }
-  }
-  rows.sum_l();
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    if (row[h] >= len) continue;
-    const int64_t at = (int64_t)(t0 + row[h]) * a.q_heads + head;
-    const float inv = rows.l[h] == 0.f ? 0.f : 1.f / rows.l[h];
-    uint32_t *dst = reinterpret_cast<uint32_t *>(static_cast<T *>(a.out) + at * D) + (lane & 3);
-#pragma unroll
-    for (int i = 0; i < D / 8; ++i) dst[i * 4] = Type<T>::pack(rows.o[i][2 * h] * inv, rows.o[i][2 * h + 1] * inv);
-    if (a.lse && (lane & 3) == 0) a.lse[at] = row_lse<T>(rows.m[h], rows.l[h]);
-  }
+  Work end{};
+  put(end);
 }
 
 template <typename T, int D>
-cudaError_t launch(const PromptAttnArgs &a, cudaStream_t st) {
-  const dim3 grid((unsigned)((a.max_len + kPrRows - 1) / kPrRows), (unsigned)a.q_heads, (unsigned)a.n_seqs);
-  prompt_attn_kernel<T, D><<<grid, kPrThreads, kPrStages * pr_stage<D>(), st>>>(a);
+__global__ void __launch_bounds__(kFaThreads, 1)
+    prompt_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                       const __grid_constant__ CUtensorMap tmV, const __grid_constant__ FaArgs a) {
+  using L = FaSmem<D>;
+  constexpr bool kBf16 = sizeof(T) == 2 && kFaOffset<T> == 0.f;
+  constexpr uint32_t kIdS = umma::idesc(kBf16, kFaKeys, false), kIdO = umma::idesc(kBf16, D, true);
+  extern __shared__ uint8_t smem_raw[];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
+  uint8_t *g = smem_raw + (base - raw);
+  uint32_t *err = a.err;
+
+  if (tid == 0) {
+    for (int s = 0; s < kFaRing; ++s) {
+      mbar_init(base + L::kKvFull + 8 * s, 1);
+      mbar_init(base + L::kKvEmpty + 8 * s, 1);
+    }
+    mbar_init(base + L::kQFull, 1);
+    mbar_init(base + L::kQEmpty, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(base + L::kSFull + 8 * i, 1);
+      mbar_init(base + L::kPFull + 8 * i, 128);
+      mbar_init(base + L::kOFull + 8 * i, 1);
+      mbar_init(base + L::kOEmpty + 8 * i, 128);
+      mbar_init(base + L::kWFull + 8 * i, 1);
+      mbar_init(base + L::kWEmpty + 8 * i, kWorkReaders);
+    }
+    for (int i = 0; i < kFaChecks; ++i) mbar_init(base + L::kCheck + 8 * i, 1);
+    mbar_fence_init();
+    umma::prefetch_map(&tmQ);
+    umma::prefetch_map(&tmK);
+    umma::prefetch_map(&tmV);
+  }
+  if (warp == 1) umma::alloc(base + L::kSlot, 512);
+  umma::fence_before();
+  __syncthreads();
+  umma::fence_after();
+  const uint32_t tmem = *reinterpret_cast<uint32_t *>(g + L::kSlot);
+
+  if (warp == 0) {
+    if (lane == 0) {  // loads
+      Work w;
+      int it = 0;  // ring position: K0 V0 K1 V1 ... over all items
+      bool ok = true;
+      int i = 0;
+      for (; ok && get_work(base, L::kWFull, g, L::kWork, i, w, err); ++i) {
+        mbar_arrive(base + L::kWEmpty + 8 * (i & 1));
+        if (i > 0 && !(ok = mbar_wait(base + L::kQEmpty, (i - 1) & 1, err))) break;
+        const int tiles = w.n1 > 0 ? 2 : 1, n = max(w.n0, w.n1);
+        const int rows = a.pack * a.per_tile;
+        mbar_expect_tx(base + L::kQFull, tiles * rows * D * 2);
+        for (int t = 0; t < tiles; ++t)
+          for (int h = 0; h < D / 64; ++h)
+            umma::tma3(base + L::kQ + t * L::kTile + h * kFaHalf, &tmQ, h * 64, w.unit * a.pack,
+                       w.seq0 + w.tok0 + t * a.per_tile, base + L::kQFull);
+        const int kvh = w.unit * a.pack / a.group;
+        for (int j = 0; j < n && ok; ++j) {
+          for (int kv = 0; kv < 2; ++kv, ++it) {
+            const int s = it % kFaRing;
+            if (it >= kFaRing && !(ok = mbar_wait(base + L::kKvEmpty + 8 * s, (it / kFaRing - 1) & 1, err))) break;
+            mbar_expect_tx(base + L::kKvFull + 8 * s, L::kTile);
+            for (int h = 0; h < D / 64; ++h)
+              umma::tma3(base + L::kKV + s * L::kTile + h * kFaHalf, kv ? &tmV : &tmK, h * 64, kvh,
+                         w.seq0 + j * kFaKeys, base + L::kKvFull + 8 * s);
+          }
+        }
+      }
+      // nothing may still be landing in shared memory when the CTA leaves
+      if (i > 0) mbar_wait(base + L::kQFull, (i - 1) & 1, err);
+      for (int q = it > kFaRing ? it - kFaRing : 0; q < it; ++q)
+        mbar_wait(base + L::kKvFull + 8 * (q % kFaRing), (q / kFaRing) & 1, err);
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {  // products
+      Work w;
+      int it = 0, checked = 0;
+      int np[2] = {0, 0}, no[2] = {0, 0};  // probabilities awaited, items begun, of each row tile
+      bool ok = true;
+      auto scores = [&](int t, int stage) {
+        const uint32_t A = base + L::kQ + t * L::kTile, B = base + L::kKV + stage * L::kTile;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off = (kk >> 2) * kFaHalf + (kk & 3) * 32;
+          umma::mma_ss(tmem + t * 128, umma::desc_k(A + off), umma::desc_k(B + off), kIdS, kk != 0);
+        }
+        umma::commit(base + L::kSFull + 8 * t);
+      };
+      for (int i = 0; ok && get_work(base, L::kWFull, g, L::kWork, i, w, err); ++i) {
+        mbar_arrive(base + L::kWEmpty + 8 * (i & 1));
+        const int nt[2] = {w.n0, w.n1}, n = max(w.n0, w.n1), hidden = first_hidden_tile(w);
+        if (!(ok = mbar_wait(base + L::kQFull, i & 1, err))) break;
+        if (!(ok = mbar_wait(base + L::kKvFull + 8 * (it % kFaRing), (it / kFaRing) & 1, err))) break;
+        umma::fence_after();
+        for (int t = 0; t < 2; ++t)
+          if (nt[t] > 0) scores(t, it % kFaRing);
+        umma::commit(base + L::kKvEmpty + 8 * (it % kFaRing));
+        if (n == 1) umma::commit(base + L::kQEmpty);
+        ++it;
+        for (int j = 0; j < n && ok; ++j) {
+          const int sv = it % kFaRing, sk = (it + 1) % kFaRing;
+          if (!(ok = mbar_wait(base + L::kKvFull + 8 * sv, (it / kFaRing) & 1, err))) break;
+          if (j >= hidden) {
+            if (!(ok = mbar_wait(base + L::kCheck + 8 * (checked % kFaChecks), (checked / kFaChecks) & 1, err))) break;
+            ++checked;
+          }
+          bool have_k = false;
+          for (int t = 0; t < 2 && ok; ++t) {
+            if (j < nt[t]) {
+              if (j == 0 && no[t] > 0 && !(ok = mbar_wait(base + L::kOEmpty + 8 * t, (no[t] - 1) & 1, err))) break;
+              if (!(ok = mbar_wait(base + L::kPFull + 8 * t, np[t] & 1, err))) break;
+              ++np[t];
+              umma::fence_after();
+              const uint32_t V = base + L::kKV + sv * L::kTile;
+#pragma unroll
+              for (int kk = 0; kk < kFaKeys / 16; ++kk)
+                umma::mma_ts(tmem + 256 + t * 128, tmem + t * 128 + kk * 8, umma::desc_mn(V + kk * 2048, kFaHalf),
+                             kIdO, j > 0 || kk > 0);
+              if (j + 1 == nt[t]) {
+                umma::commit(base + L::kOFull + 8 * t);
+                ++no[t];
+              }
+            }
+            if (j + 1 < nt[t]) {
+              if (!have_k && !(ok = mbar_wait(base + L::kKvFull + 8 * sk, ((it + 1) / kFaRing) & 1, err))) break;
+              have_k = true;
+              umma::fence_after();
+              scores(t, sk);
+            }
+          }
+          if (!ok) break;
+          umma::commit(base + L::kKvEmpty + 8 * sv);
+          ++it;
+          if (j + 1 < n) {
+            umma::commit(base + L::kKvEmpty + 8 * sk);
+            if (j + 2 == n) umma::commit(base + L::kQEmpty);
+            ++it;
+          }
+        }
+      }
+      // the last commit has arrived before the CTA leaves
+      if (ok && it > 0) mbar_wait(base + L::kKvEmpty + 8 * ((it - 1) % kFaRing), ((it - 1) / kFaRing) & 1, err);
+    }
+  } else if (warp == 2) {  // hidden values
+    Work w;
+    int it = 0, checked = 0;
+    bool ok = true;
+    for (int i = 0; ok; ++i) {
+      const bool more = get_work(base, L::kWFull, g, L::kWork, i, w, err);
+      if (!__all_sync(0xffffffffu, more)) break;
+      Wild *wild = reinterpret_cast<Wild *>(g + L::kWild) + (i & 1);
+      volatile int *any = reinterpret_cast<volatile int *>(g + L::kWildAny) + (i & 1);
+      const int n = max(w.n0, w.n1), hidden = first_hidden_tile(w);
+      bool reset = false;
+      for (int j = hidden; j < n && ok; ++j) {
+        const int pos = it + 2 * j + 1, s = pos % kFaRing;
+        ok = __all_sync(0xffffffffu, mbar_wait(base + L::kKvFull + 8 * s, (pos / kFaRing) & 1, err));
+        if (!ok) break;
+        const uint32_t V = base + L::kKV + s * L::kTile;
+        if (__any_sync(0xffffffffu, attn::wild_pieces<T>(V, L::kTile / 16, lane, kWarp))) {
+          if (!reset) {
+            for (int d = lane; d < D; d += kWarp) wild->nan[d] = wild->pos[d] = wild->neg[d] = kNever;
+            reset = true;
+          }
+          for (int d = lane; d < D; d += kWarp) {
+            for (int r = 0; r < kFaKeys; ++r) {
+              T *v = reinterpret_cast<T *>(g + L::kKV + s * L::kTile + (d >> 6) * kFaHalf + r * 128 +
+                                           ((((d & 63) >> 3) ^ (r & 7)) << 4) + (d & 7) * 2);
+              const float x = static_cast<float>(*v);
+              if (!(fabsf(x) < __int_as_float(0x7f800000))) {
+                const uint16_t at = (uint16_t)((j - hidden) * kFaKeys + r);
+                if (x != x)
+                  wild->nan[d] = min(wild->nan[d], at);
+                else if (x > 0.f)
+                  wild->pos[d] = min(wild->pos[d], at);
+                else
+                  wild->neg[d] = min(wild->neg[d], at);
+                *v = static_cast<T>(0.f);
+              }
+            }
+          }
+          if (lane == 0) *any = 1;
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the zeros, for the tensor core
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(base + L::kCheck + 8 * (checked % kFaChecks));
+        ++checked;
+      }
+      it += 2 * n;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(base + L::kWEmpty + 8 * (i & 1));
+    }
+  } else if (warp == 3) {  // the items
+    int i = 0;
+    deal(a, blockIdx.x, gridDim.x, [&](const Work &w) {
+      bool ok = true;
+      if (i >= 2) ok = __all_sync(0xffffffffu, mbar_wait(base + L::kWEmpty + 8 * (i & 1), ((i >> 1) - 1) & 1, err));
+      if (ok && lane == 0) {
+        *reinterpret_cast<Work *>(g + L::kWork + 32 * (i & 1)) = w;
+        *(reinterpret_cast<volatile int *>(g + L::kWildAny) + (i & 1)) = 0;
+        mbar_arrive(base + L::kWFull + 8 * (i & 1));
+      }
+      __syncwarp();
+      ++i;
+      return ok;
+    });
+  } else {  // softmax of row tile t
+    const int t = (warp - 4) >> 2, wq = warp & 3;
+    const int r = wq * 32 + lane;
+    const int tok_r = r / a.pack, head_r = r % a.pack;  // the row's token in the tile and head in the unit
+    const bool row_used = tok_r < a.per_tile;
+    const uint32_t lanes = (uint32_t)(wq * 32) << 16;
+    const uint32_t tS = tmem + t * 128 + lanes, tO = tmem + 256 + t * 128 + lanes;
+    const uint64_t c2 = umma::pack2(a.c, a.c);
+    Work w;
+    int ns = 0, items = 0;  // scores awaited, items of this row tile begun
+    bool ok = true;
+    for (int i = 0; ok; ++i) {
+      const bool more = get_work(base, L::kWFull, g, L::kWork, i, w, err);
+      if (!__all_sync(0xffffffffu, more)) break;
+      const int nt = t ? w.n1 : w.n0;
+      const int tok = w.tok0 + t * a.per_tile + tok_r;  // position in the sequence
+      const bool live = row_used && tok < w.len;
+      float m = kNegInf, l = 0.f;
+      const int clear = (w.tok0 + t * a.per_tile + 1) / kFaKeys;  // tiles that every row sees whole
+      for (int j = 0; j < nt; ++j, ++ns) {
+        ok = __all_sync(0xffffffffu, mbar_wait(base + L::kSFull + 8 * t, ns & 1, err));
+        if (!ok) break;
+        umma::fence_after();
+        const int see = j >= clear ? tok + 1 - j * kFaKeys : kFaKeys;  // keys of the tile that the row sees
+        // registers hold the first 64 scores; the others are read for the maximum, and again for the exponentials
+        uint32_t s[64];
+        float mx[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
+        auto load = [&](int col) {
+          umma::ld32(tS + col, s);
+          umma::ld32(tS + col + 32, s + 32);
+          umma::wait_ld();
+          if (j >= clear) {
+#pragma unroll
+            for (int e = 0; e < 64; ++e)
+              if (col + e >= see) s[e] = 0xff800000u;
+          }
+        };
+        auto most = [&]() {
+#pragma unroll
+          for (int e = 0; e < 64; e += 4)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) mx[q] = fmaxf(mx[q], __uint_as_float(s[e + q]));
+        };
+        load(64);
+        most();
+        load(0);
+        most();
+        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.c;
+        const bool raise = live && (top > m + kFaSlack || m == kNegInf);
+        const float was = m;
+        if (raise) m = fmaxf(m, top);
+        const float safe = m == kNegInf ? 0.f : m;
+        if (__any_sync(0xffffffffu, raise) && j > 0) {
+          // the accumulator is still: S of this tile came after the last product into it
+          const float f = raise ? ex2(was - safe) : 1.f;
+          l *= f;
+          const uint64_t f2 = umma::pack2(f, f);
+#pragma unroll
+          for (int q = 0; q < D / 32; ++q) {
+            uint32_t o[32];
+            umma::ld32(tO + q * 32, o);
+            umma::wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) {
+              float x, y;
+              umma::unpack2(umma::mul2(umma::pack2(__uint_as_float(o[e]), __uint_as_float(o[e + 1])), f2), x, y);
+              o[e] = __float_as_uint(x), o[e + 1] = __float_as_uint(y);
+            }
+            umma::st32(tO + q * 32, o);
+          }
+        }
+        const float shift = kFaOffset<T> - safe;
+        const uint64_t shift2 = umma::pack2(shift, shift);
+        uint64_t sum2[2] = {0, 0};
+        auto probabilities = [&](int col) {  // of the 64 scores held, to 32 columns
+          uint32_t p[32];
+#pragma unroll
+          for (int e = 0; e < 64; e += 2) {
+            float x, y;
+            umma::unpack2(umma::fma2(umma::pack2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), c2, shift2), x, y);
+            x = ex2(x), y = ex2(y);
+            p[e / 2] = Type<T>::pack(x, y);
+            sum2[(e >> 1) & 1] = umma::add2(sum2[(e >> 1) & 1], umma::pack2(x, y));
+          }
+          umma::st32(tS + col, p);
+        };
+        probabilities(0);
+        load(64);
+        probabilities(32);
+        float x, y;
+        umma::unpack2(umma::add2(sum2[0], sum2[1]), x, y);
+        l += x + y;
+        umma::wait_st();
+        umma::fence_before();
+        mbar_arrive(base + L::kPFull + 8 * t);
+      }
+      if (!ok) break;
+      if (nt > 0) {
+        ok = __all_sync(0xffffffffu, mbar_wait(base + L::kOFull + 8 * t, items & 1, err));
+        if (!ok) break;
+        ++items;
+        umma::fence_after();
+        const int64_t at = (int64_t)(w.seq0 + tok) * a.q_heads + w.unit * a.pack + head_r;
+        const float inv = 1.f / l;
+        const bool wild = *(reinterpret_cast<volatile int *>(g + L::kWildAny) + (i & 1)) != 0;
+        const Wild *wd = reinterpret_cast<const Wild *>(g + L::kWild) + (i & 1);
+        const int upto = tok - first_hidden_tile(w) * kFaKeys;  // last position the row sees
+        uint4 *dst = reinterpret_cast<uint4 *>(static_cast<T *>(a.out) + at * D);
+#pragma unroll
+        for (int q = 0; q < D / 32; ++q) {
+          uint32_t o[32];
+          umma::ld32(tO + q * 32, o);
+          umma::wait_ld();
+          if (wild) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              const int d = q * 32 + e;
+              const bool n = (int)wd->nan[d] <= upto, p = (int)wd->pos[d] <= upto, b = (int)wd->neg[d] <= upto;
+              if (n || (p && b))
+                o[e] = 0x7fffffffu;
+              else if (p || b)
+                o[e] = __float_as_uint(__uint_as_float(o[e]) + (p ? -kNegInf : kNegInf));
+            }
+          }
+          if (live) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 8)
+              dst[q * 4 + e / 8] =
+                  make_uint4(Type<T>::pack(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv),
+                             Type<T>::pack(__uint_as_float(o[e + 2]) * inv, __uint_as_float(o[e + 3]) * inv),
+                             Type<T>::pack(__uint_as_float(o[e + 4]) * inv, __uint_as_float(o[e + 5]) * inv),
+                             Type<T>::pack(__uint_as_float(o[e + 6]) * inv, __uint_as_float(o[e + 7]) * inv));
+          }
+        }
+        umma::fence_before();
+        mbar_arrive(base + L::kOEmpty + 8 * t);
+        if (live && a.lse) a.lse[at] = (m - kFaOffset<T> + log2f(l)) * attn::kLn2;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(base + L::kWEmpty + 8 * (i & 1));
+    }
+  }
+  umma::fence_before();
+  __syncthreads();
+  umma::fence_after();
+  if (warp == 1) umma::dealloc(tmem, 512);
+}
+
+template <typename T, int D>
+cudaError_t launch(const PromptAttnArgs &p, int sms, cudaStream_t st) {
+  FaArgs a{};
+  a.cu = p.cu, a.tokens = p.tokens, a.n_seqs = p.n_seqs, a.max_len = p.max_len;
+  a.q_heads = p.q_heads, a.group = p.group;
+  // heads packed into a row tile: all of a group's, up to 32 (then at most a fifth of the rows is left over)
+  a.pack = p.group <= 32 ? p.group : 1;
+  a.per_tile = 128 / a.pack, a.units = p.q_heads / a.pack;
+  a.c = p.scale * attn::kLog2e;
+  a.out = p.out, a.lse = p.lse, a.err = p.err;
+  CUtensorMap tmQ, tmK, tmV;
+  const uint64_t dq[3] = {D, (uint64_t)p.q_heads, (uint64_t)p.tokens}, dk[3] = {D, (uint64_t)p.kv_heads, (uint64_t)p.tokens};
+  const uint64_t sq[2] = {(uint64_t)p.q_head * 2, (uint64_t)p.q_token * 2};
+  const uint64_t sk[2] = {(uint64_t)p.k_head * 2, (uint64_t)p.k_token * 2};
+  const uint64_t sv[2] = {(uint64_t)p.v_head * 2, (uint64_t)p.v_token * 2};
+  const uint32_t bq[3] = {64, (uint32_t)a.pack, (uint32_t)a.per_tile}, bk[3] = {64, 1, kFaKeys};
+  if (!encode_16bit(&tmQ, p.q, 3, dq, sq, bq) || !encode_16bit(&tmK, p.k, 3, dk, sk, bk) ||
+      !encode_16bit(&tmV, p.v, 3, dk, sv, bk))
+    return cudaErrorInvalidValue;
+  const long long items =
+      (long long)((p.max_len + 2 * a.per_tile - 1) / (2 * a.per_tile)) * p.n_seqs * a.units;
+  prompt_attn_kernel<T, D><<<(unsigned)(items < sms ? items : sms), kFaThreads, FaSmem<D>::kBytes, st>>>(tmQ, tmK, tmV,
+                                                                                                        a);
   return cudaGetLastError();
 }
 
@@ -113,17 +542,17 @@ cudaError_t prepare_prompt_attn() {
   auto set = [&](const void *f, int bytes) {
     if (e == cudaSuccess) e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   };
-  set((const void *)prompt_attn_kernel<__nv_bfloat16, 128>, kPrStages * pr_stage<128>());
-  set((const void *)prompt_attn_kernel<__nv_bfloat16, 64>, kPrStages * pr_stage<64>());
-  set((const void *)prompt_attn_kernel<__half, 128>, kPrStages * pr_stage<128>());
-  set((const void *)prompt_attn_kernel<__half, 64>, kPrStages * pr_stage<64>());
+  set((const void *)prompt_attn_kernel<__nv_bfloat16, 128>, FaSmem<128>::kBytes);
+  set((const void *)prompt_attn_kernel<__nv_bfloat16, 64>, FaSmem<64>::kBytes);
+  set((const void *)prompt_attn_kernel<__half, 128>, FaSmem<128>::kBytes);
+  set((const void *)prompt_attn_kernel<__half, 64>, FaSmem<64>::kBytes);
   return e;
 }
 
 cudaError_t launch_prompt_attn(const PromptAttnArgs &a, int dtype, int dim, int sms, cudaStream_t st) {
-  (void)sms;
-  if (dtype == NS_DTYPE_BF16) return dim == 128 ? launch<__nv_bfloat16, 128>(a, st) : launch<__nv_bfloat16, 64>(a, st);
-  return dim == 128 ? launch<__half, 128>(a, st) : launch<__half, 64>(a, st);
+  if (dtype == NS_DTYPE_BF16)
+    return dim == 128 ? launch<__nv_bfloat16, 128>(a, sms, st) : launch<__nv_bfloat16, 64>(a, sms, st);
+  return dim == 128 ? launch<__half, 128>(a, sms, st) : launch<__half, 64>(a, sms, st);
 }
 
 }  // namespace ns

@@ -76,7 +76,7 @@ def test_prompt_lengths(ns, dtype, d):
     run_prompt(ns, EDGES, 4, 2, d, dtype, 1)
 
 
-@pytest.mark.parametrize("hq,hkv", [(1, 1), (7, 1), (14, 2), (8, 8), (16, 1), (12, 4)])
+@pytest.mark.parametrize("hq,hkv", [(1, 1), (7, 1), (14, 2), (8, 8), (16, 1), (12, 4), (32, 1), (33, 1), (20, 1)])
 def test_prompt_heads(ns, hq, hkv):
     run_prompt(ns, [70, 1, 130], hq, hkv, 128, BF16, 2)
     run_prompt(ns, [70, 1, 130], hq, hkv, 64, F16, 3)
