@@ -79,7 +79,7 @@ struct FaSmem {
   static constexpr int kQ = 0, kKV = 2 * kTile, kMisc = kKV + kFaRing * kTile;
   // barriers, 8 bytes each
   static constexpr int kKvFull = kMisc, kKvEmpty = kKvFull + 8 * kFaRing, kQFull = kKvEmpty + 8 * kFaRing,
-                       kQEmpty = kQFull + 8, kSFull = kQEmpty + 8, kPFull = kSFull + 16, kOFull = kPFull + 16,
+                       kQEmpty = kQFull + 8, kSFull = kQEmpty + 8, kPFull = kSFull + 16, kOFull = kPFull + 32,
                        kOEmpty = kOFull + 16, kCheck = kOEmpty + 16, kWFull = kCheck + 8 * kFaChecks,
                        kWEmpty = kWFull + 16, kSlot = kWEmpty + 16, kWork = kSlot + 16, kWildAny = kWork + 2 * 32,
                        kWild = kWildAny + 16, kEnd = kWild + 2 * (int)sizeof(Wild);
@@ -102,7 +102,7 @@ __device__ __forceinline__ int first_hidden_tile(const Work &w) { return (w.tok0
 
 __device__ __forceinline__ bool get_work(uint32_t base, int full, const uint8_t *g, int work_off, int i, Work &w,
                                          uint32_t *err) {
-  if (!mbar_wait(base + full + 8 * (i & 1), (i >> 1) & 1, err)) return false;
+  if (!umma::inline_wait(base + full + 8 * (i & 1), (i >> 1) & 1, err)) return false;
   w = *reinterpret_cast<const Work *>(g + work_off + 32 * (i & 1));
   return w.n0 > 0;
 }
@@ -177,7 +177,8 @@ __global__ void __launch_bounds__(kFaThreads, 1)
     mbar_init(base + L::kQEmpty, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(base + L::kSFull + 8 * i, 1);
-      mbar_init(base + L::kPFull + 8 * i, 128);
+      mbar_init(base + L::kPFull + 16 * i, 128);      // the probabilities of the first 64 keys
+      mbar_init(base + L::kPFull + 16 * i + 8, 128);  // and of the others
       mbar_init(base + L::kOFull + 8 * i, 1);
       mbar_init(base + L::kOEmpty + 8 * i, 128);
       mbar_init(base + L::kWFull + 8 * i, 1);
@@ -195,6 +196,9 @@ __global__ void __launch_bounds__(kFaThreads, 1)
   umma::fence_after();
   const uint32_t tmem = *reinterpret_cast<uint32_t *>(g + L::kSlot);
 
+  // registers: 128 threads x 88 + 256 x 208 = 384 x 168, the launch's own
+  if (warp < 4)
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
   if (warp == 0) {
     if (lane == 0) {  // loads
       Work w;
@@ -203,7 +207,7 @@ __global__ void __launch_bounds__(kFaThreads, 1)
       int i = 0;
       for (; ok && get_work(base, L::kWFull, g, L::kWork, i, w, err); ++i) {
         mbar_arrive(base + L::kWEmpty + 8 * (i & 1));
-        if (i > 0 && !(ok = mbar_wait(base + L::kQEmpty, (i - 1) & 1, err))) break;
+        if (i > 0 && !(ok = umma::inline_wait(base + L::kQEmpty, (i - 1) & 1, err))) break;
         const int tiles = w.n1 > 0 ? 2 : 1, n = max(w.n0, w.n1);
         const int rows = a.pack * a.per_tile;
         mbar_expect_tx(base + L::kQFull, tiles * rows * D * 2);
@@ -215,7 +219,7 @@ __global__ void __launch_bounds__(kFaThreads, 1)
         for (int j = 0; j < n && ok; ++j) {
           for (int kv = 0; kv < 2; ++kv, ++it) {
             const int s = it % kFaRing;
-            if (it >= kFaRing && !(ok = mbar_wait(base + L::kKvEmpty + 8 * s, (it / kFaRing - 1) & 1, err))) break;
+            if (it >= kFaRing && !(ok = umma::inline_wait(base + L::kKvEmpty + 8 * s, (it / kFaRing - 1) & 1, err))) break;
             mbar_expect_tx(base + L::kKvFull + 8 * s, L::kTile);
             for (int h = 0; h < D / 64; ++h)
               umma::tma3(base + L::kKV + s * L::kTile + h * kFaHalf, kv ? &tmV : &tmK, h * 64, kvh,
@@ -224,80 +228,101 @@ __global__ void __launch_bounds__(kFaThreads, 1)
         }
       }
       // nothing may still be landing in shared memory when the CTA leaves
-      if (i > 0) mbar_wait(base + L::kQFull, (i - 1) & 1, err);
+      if (i > 0) umma::inline_wait(base + L::kQFull, (i - 1) & 1, err);
       for (int q = it > kFaRing ? it - kFaRing : 0; q < it; ++q)
-        mbar_wait(base + L::kKvFull + 8 * (q % kFaRing), (q / kFaRing) & 1, err);
+        umma::inline_wait(base + L::kKvFull + 8 * (q % kFaRing), (q / kFaRing) & 1, err);
     }
   } else if (warp == 1) {
-    if (lane == 0) {  // products
-      Work w;
-      int it = 0, checked = 0;
-      int np[2] = {0, 0}, no[2] = {0, 0};  // probabilities awaited, items begun, of each row tile
-      bool ok = true;
-      auto scores = [&](int t, int stage) {
-        const uint32_t A = base + L::kQ + t * L::kTile, B = base + L::kKV + stage * L::kTile;
+    // products: the whole warp waits and counts, one lane issues
+    Work w;
+    int it = 0, checked = 0;
+    int np[2] = {0, 0}, no[2] = {0, 0};  // probabilities awaited, items begun, of each row tile
+    bool ok = true;
+    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0), kv0 = __shfl_sync(0xffffffffu, base, 0) + L::kKV;
+    auto wait = [&](uint32_t bar, int phase) {
+      return __all_sync(0xffffffffu, umma::inline_wait(base + bar, phase & 1, err));
+    };
+    auto scores = [&](int t, int stage) {
+      const uint64_t A = umma::desc_k(kv0 - L::kKV + L::kQ + t * L::kTile), B = umma::desc_k(kv0 + stage * L::kTile);
+      if (umma::elect()) {
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t off = (kk >> 2) * kFaHalf + (kk & 3) * 32;
-          umma::mma_ss(tmem + t * 128, umma::desc_k(A + off), umma::desc_k(B + off), kIdS, kk != 0);
+          const uint32_t off = ((kk >> 2) * kFaHalf + (kk & 3) * 32) >> 4;  // in the descriptors' 16-byte units
+          umma::mma_ss(tm + t * 128, A + off, B + off, kIdS, kk != 0);
         }
         umma::commit(base + L::kSFull + 8 * t);
-      };
-      for (int i = 0; ok && get_work(base, L::kWFull, g, L::kWork, i, w, err); ++i) {
-        mbar_arrive(base + L::kWEmpty + 8 * (i & 1));
-        const int nt[2] = {w.n0, w.n1}, n = max(w.n0, w.n1), hidden = first_hidden_tile(w);
-        if (!(ok = mbar_wait(base + L::kQFull, i & 1, err))) break;
-        if (!(ok = mbar_wait(base + L::kKvFull + 8 * (it % kFaRing), (it / kFaRing) & 1, err))) break;
-        umma::fence_after();
-        for (int t = 0; t < 2; ++t)
-          if (nt[t] > 0) scores(t, it % kFaRing);
-        umma::commit(base + L::kKvEmpty + 8 * (it % kFaRing));
-        if (n == 1) umma::commit(base + L::kQEmpty);
-        ++it;
-        for (int j = 0; j < n && ok; ++j) {
-          const int sv = it % kFaRing, sk = (it + 1) % kFaRing;
-          if (!(ok = mbar_wait(base + L::kKvFull + 8 * sv, (it / kFaRing) & 1, err))) break;
-          if (j >= hidden) {
-            if (!(ok = mbar_wait(base + L::kCheck + 8 * (checked % kFaChecks), (checked / kFaChecks) & 1, err))) break;
-            ++checked;
-          }
-          bool have_k = false;
-          for (int t = 0; t < 2 && ok; ++t) {
-            if (j < nt[t]) {
-              if (j == 0 && no[t] > 0 && !(ok = mbar_wait(base + L::kOEmpty + 8 * t, (no[t] - 1) & 1, err))) break;
-              if (!(ok = mbar_wait(base + L::kPFull + 8 * t, np[t] & 1, err))) break;
-              ++np[t];
-              umma::fence_after();
-              const uint32_t V = base + L::kKV + sv * L::kTile;
+      }
+      __syncwarp();
+    };
+    auto commit = [&](uint32_t bar) {
+      if (umma::elect()) umma::commit(base + bar);
+      __syncwarp();
+    };
+    for (int i = 0; ok; ++i) {
+      const bool more = get_work(base, L::kWFull, g, L::kWork, i, w, err);
+      if (!__all_sync(0xffffffffu, more)) break;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(base + L::kWEmpty + 8 * (i & 1));
+      const int n0 = __shfl_sync(0xffffffffu, w.n0, 0), n1 = __shfl_sync(0xffffffffu, w.n1, 0), n = max(n0, n1);
+      const int hidden = __shfl_sync(0xffffffffu, first_hidden_tile(w), 0);
+      if (!(ok = wait(L::kQFull, i))) break;
+      if (!(ok = wait(L::kKvFull + 8 * (it % kFaRing), it / kFaRing))) break;
+      umma::fence_after();
+      scores(0, it % kFaRing);
+      if (n1 > 0) scores(1, it % kFaRing);
+      commit(L::kKvEmpty + 8 * (it % kFaRing));
+      if (n == 1) commit(L::kQEmpty);
+      ++it;
+      for (int j = 0; j < n && ok; ++j) {
+        const int sv = it % kFaRing, sk = (it + 1) % kFaRing;
+        if (!(ok = wait(L::kKvFull + 8 * sv, it / kFaRing))) break;
+        if (j >= hidden) {
+          if (!(ok = wait(L::kCheck + 8 * (checked % kFaChecks), checked / kFaChecks))) break;
+          ++checked;
+        }
+        bool have_k = false;
 #pragma unroll
-              for (int kk = 0; kk < kFaKeys / 16; ++kk)
-                umma::mma_ts(tmem + 256 + t * 128, tmem + t * 128 + kk * 8, umma::desc_mn(V + kk * 2048, kFaHalf),
-                             kIdO, j > 0 || kk > 0);
-              if (j + 1 == nt[t]) {
-                umma::commit(base + L::kOFull + 8 * t);
-                ++no[t];
-              }
-            }
-            if (j + 1 < nt[t]) {
-              if (!have_k && !(ok = mbar_wait(base + L::kKvFull + 8 * sk, ((it + 1) / kFaRing) & 1, err))) break;
-              have_k = true;
+        for (int t = 0; t < 2; ++t) {
+          const int nt = t ? n1 : n0;
+          if (ok && j < nt) {
+            if (j == 0 && no[t] > 0) ok = wait(L::kOEmpty + 8 * t, no[t] - 1);
+            const uint64_t V = umma::desc_mn(kv0 + sv * L::kTile, kFaHalf);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              if (ok) ok = wait(L::kPFull + 16 * t + 8 * h, np[t]);
               umma::fence_after();
-              scores(t, sk);
+              if (ok && umma::elect()) {
+#pragma unroll
+                for (int kk = 4 * h; kk < 4 * h + 4; ++kk)
+                  umma::mma_ts(tm + 256 + t * 128, tm + t * 128 + kk * 8, V + kk * (2048 >> 4), kIdO, j > 0 || kk > 0);
+              }
+              __syncwarp();
+            }
+            ++np[t];
+            if (ok && j + 1 == nt) {
+              commit(L::kOFull + 8 * t);
+              ++no[t];
             }
           }
-          if (!ok) break;
-          umma::commit(base + L::kKvEmpty + 8 * sv);
-          ++it;
-          if (j + 1 < n) {
-            umma::commit(base + L::kKvEmpty + 8 * sk);
-            if (j + 2 == n) umma::commit(base + L::kQEmpty);
-            ++it;
+          if (ok && j + 1 < nt) {
+            if (!have_k) ok = wait(L::kKvFull + 8 * sk, (it + 1) / kFaRing);
+            have_k = true;
+            umma::fence_after();
+            if (ok) scores(t, sk);
           }
         }
+        if (!ok) break;
+        commit(L::kKvEmpty + 8 * sv);
+        ++it;
+        if (j + 1 < n) {
+          commit(L::kKvEmpty + 8 * sk);
+          if (j + 2 == n) commit(L::kQEmpty);
+          ++it;
+        }
       }
-      // the last commit has arrived before the CTA leaves
-      if (ok && it > 0) mbar_wait(base + L::kKvEmpty + 8 * ((it - 1) % kFaRing), ((it - 1) / kFaRing) & 1, err);
     }
+    // the last commit has arrived before the CTA leaves
+    if (ok && it > 0) wait(L::kKvEmpty + 8 * ((it - 1) % kFaRing), (it - 1) / kFaRing);
   } else if (warp == 2) {  // hidden values
     Work w;
     int it = 0, checked = 0;
@@ -311,7 +336,7 @@ __global__ void __launch_bounds__(kFaThreads, 1)
       bool reset = false;
       for (int j = hidden; j < n && ok; ++j) {
         const int pos = it + 2 * j + 1, s = pos % kFaRing;
-        ok = __all_sync(0xffffffffu, mbar_wait(base + L::kKvFull + 8 * s, (pos / kFaRing) & 1, err));
+        ok = __all_sync(0xffffffffu, umma::inline_wait(base + L::kKvFull + 8 * s, (pos / kFaRing) & 1, err));
         if (!ok) break;
         const uint32_t V = base + L::kKV + s * L::kTile;
         if (__any_sync(0xffffffffu, attn::wild_pieces<T>(V, L::kTile / 16, lane, kWarp))) {
@@ -351,7 +376,7 @@ __global__ void __launch_bounds__(kFaThreads, 1)
     int i = 0;
     deal(a, blockIdx.x, gridDim.x, [&](const Work &w) {
       bool ok = true;
-      if (i >= 2) ok = __all_sync(0xffffffffu, mbar_wait(base + L::kWEmpty + 8 * (i & 1), ((i >> 1) - 1) & 1, err));
+      if (i >= 2) ok = __all_sync(0xffffffffu, umma::inline_wait(base + L::kWEmpty + 8 * (i & 1), ((i >> 1) - 1) & 1, err));
       if (ok && lane == 0) {
         *reinterpret_cast<Work *>(g + L::kWork + 32 * (i & 1)) = w;
         *(reinterpret_cast<volatile int *>(g + L::kWildAny) + (i & 1)) = 0;
@@ -362,6 +387,7 @@ __global__ void __launch_bounds__(kFaThreads, 1)
       return ok;
     });
   } else {  // softmax of row tile t
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     const int t = (warp - 4) >> 2, wq = warp & 3;
     const int r = wq * 32 + lane;
     const int tok_r = r / a.pack, head_r = r % a.pack;  // the row's token in the tile and head in the unit
@@ -381,85 +407,93 @@ __global__ void __launch_bounds__(kFaThreads, 1)
       float m = kNegInf, l = 0.f;
       const int clear = (w.tok0 + t * a.per_tile + 1) / kFaKeys;  // tiles that every row sees whole
       for (int j = 0; j < nt; ++j, ++ns) {
-        ok = __all_sync(0xffffffffu, mbar_wait(base + L::kSFull + 8 * t, ns & 1, err));
+        ok = __all_sync(0xffffffffu, umma::inline_wait(base + L::kSFull + 8 * t, ns & 1, err));
         if (!ok) break;
         umma::fence_after();
-        const int see = j >= clear ? tok + 1 - j * kFaKeys : kFaKeys;  // keys of the tile that the row sees
-        // registers hold the first 64 scores; the others are read for the maximum, and again for the exponentials
-        uint32_t s[64];
+        uint32_t s[128];
         float mx[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
-        auto load = [&](int col) {
-          umma::ld32(tS + col, s);
-          umma::ld32(tS + col + 32, s + 32);
-          umma::wait_ld();
-          if (j >= clear) {
+        auto mask = [&](int from) {  // keys after the row's token, among 64
+          const int see = tok + 1 - j * kFaKeys;
 #pragma unroll
-            for (int e = 0; e < 64; ++e)
-              if (col + e >= see) s[e] = 0xff800000u;
-          }
+          for (int e = from; e < from + 64; ++e)
+            if (e >= see) s[e] = 0xff800000u;
         };
-        auto most = [&]() {
+        auto most = [&](int from) {
 #pragma unroll
-          for (int e = 0; e < 64; e += 4)
+          for (int e = from; e < from + 64; e += 8)
 #pragma unroll
-            for (int q = 0; q < 4; ++q) mx[q] = fmaxf(mx[q], __uint_as_float(s[e + q]));
+            for (int q = 0; q < 4; ++q)
+              mx[q] = fmaxf(fmaxf(mx[q], __uint_as_float(s[e + 2 * q])), __uint_as_float(s[e + 2 * q + 1]));
         };
-        load(64);
-        most();
-        load(0);
-        most();
-        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.c;
-        const bool raise = live && (top > m + kFaSlack || m == kNegInf);
-        const float was = m;
-        if (raise) m = fmaxf(m, top);
-        const float safe = m == kNegInf ? 0.f : m;
-        if (__any_sync(0xffffffffu, raise) && j > 0) {
-          // the accumulator is still: S of this tile came after the last product into it
-          const float f = raise ? ex2(was - safe) : 1.f;
-          l *= f;
-          const uint64_t f2 = umma::pack2(f, f);
-#pragma unroll
-          for (int q = 0; q < D / 32; ++q) {
-            uint32_t o[32];
-            umma::ld32(tO + q * 32, o);
-            umma::wait_ld();
-#pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-              float x, y;
-              umma::unpack2(umma::mul2(umma::pack2(__uint_as_float(o[e]), __uint_as_float(o[e + 1])), f2), x, y);
-              o[e] = __float_as_uint(x), o[e + 1] = __float_as_uint(y);
-            }
-            umma::st32(tO + q * 32, o);
-          }
-        }
-        const float shift = kFaOffset<T> - safe;
-        const uint64_t shift2 = umma::pack2(shift, shift);
-        uint64_t sum2[2] = {0, 0};
-        auto probabilities = [&](int col) {  // of the 64 scores held, to 32 columns
-          uint32_t p[32];
+        umma::ld32(tS, s);
+        umma::ld32(tS + 32, s + 32);
+        umma::wait_ld();
+        umma::ld32(tS + 64, s + 64);
+        umma::ld32(tS + 96, s + 96);
+        if (j >= clear) mask(0);
+        most(0);
+        // the probabilities of 64 keys with the m that there is; sum2 gets their sum
+        uint32_t p[32];
+        uint64_t sum2[2];
+        auto probabilities = [&](int from) {
+          const float shift = kFaOffset<T> - (m == kNegInf ? 0.f : m);
+          const uint64_t shift2 = umma::pack2(shift, shift);
 #pragma unroll
           for (int e = 0; e < 64; e += 2) {
             float x, y;
-            umma::unpack2(umma::fma2(umma::pack2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), c2, shift2), x, y);
+            umma::unpack2(umma::fma2(umma::pack2(__uint_as_float(s[from + e]), __uint_as_float(s[from + e + 1])), c2,
+                                     shift2),
+                          x, y);
             x = ex2(x), y = ex2(y);
             p[e / 2] = Type<T>::pack(x, y);
             sum2[(e >> 1) & 1] = umma::add2(sum2[(e >> 1) & 1], umma::pack2(x, y));
           }
-          umma::st32(tS + col, p);
         };
-        probabilities(0);
-        load(64);
-        probabilities(32);
+        // m hardly ever changes after the first tile, so the first half is taken with the old one while the
+        // maximum is found, and again where that was wrong
+        sum2[0] = sum2[1] = 0;
+        if (j > 0) probabilities(0);
+        umma::wait_ld();
+        if (j >= clear) mask(64);
+        most(64);
+        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.c;
+        const bool raise = live && (top > m + kFaSlack || m == kNegInf);
+        if (j == 0 || __any_sync(0xffffffffu, raise)) {
+          const float was = m;
+          if (raise) m = fmaxf(m, top);
+          if (j > 0) {
+            // the accumulator is still: S of this tile came after the last product into it
+            const float f = raise ? ex2(was - (m == kNegInf ? 0.f : m)) : 1.f;
+            l *= f;
+#pragma unroll 1
+            for (int q = 0; q < D / 16; ++q) {
+              uint32_t o[16];
+              umma::ld16(tO + q * 16, o);
+              umma::wait_ld();
+#pragma unroll
+              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+              umma::st16(tO + q * 16, o);
+            }
+          }
+          sum2[0] = sum2[1] = 0;
+          probabilities(0);
+        }
+        umma::st32(tS, p);
+        umma::wait_st();
+        umma::fence_before();
+        mbar_arrive(base + L::kPFull + 16 * t);
+        probabilities(64);
+        umma::st32(tS + 32, p);
         float x, y;
         umma::unpack2(umma::add2(sum2[0], sum2[1]), x, y);
         l += x + y;
         umma::wait_st();
         umma::fence_before();
-        mbar_arrive(base + L::kPFull + 8 * t);
+        mbar_arrive(base + L::kPFull + 16 * t + 8);
       }
       if (!ok) break;
       if (nt > 0) {
-        ok = __all_sync(0xffffffffu, mbar_wait(base + L::kOFull + 8 * t, items & 1, err));
+        ok = __all_sync(0xffffffffu, umma::inline_wait(base + L::kOFull + 8 * t, items & 1, err));
         if (!ok) break;
         ++items;
         umma::fence_after();

@@ -24,6 +24,18 @@ __device__ __forceinline__ void commit(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
 
+// One lane of a converged warp (the same one each time).  Code that issues
+// tcgen05.mma runs in the whole warp, with only the instruction itself under
+// this: its operands then stay in uniform registers.  Under `if (lane == 0)`
+// mixed products issue at 101 clocks each, so at 68 (M = N = 128, K = 16).
+__device__ __forceinline__ bool elect() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred P;\n\telect.sync _|P, 0xffffffff;\n\tselp.u32 %0, 1, 0, P;\n\t}\n"
+      : "=r"(p));
+  return p != 0;
+}
+
 // Shared-memory operand descriptors, 128-byte swizzle (descriptor version 1).
 // K-major (rows of 64 16-bit elements along K, 8-row groups 1024 bytes apart):
 __device__ __forceinline__ uint64_t desc_k(uint32_t saddr) {
@@ -81,6 +93,24 @@ __device__ __forceinline__ void st32(uint32_t t, const uint32_t *r) {
       : "memory");
 }
 
+__device__ __forceinline__ void ld16(uint32_t t, uint32_t *r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+      "[%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(t)
+      : "memory");
+}
+__device__ __forceinline__ void st16(uint32_t t, const uint32_t *r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
+      "%14, %15};" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(t)
+      : "memory");
+}
+
 __device__ __forceinline__ void prefetch_map(const CUtensorMap *m) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
 }
@@ -97,6 +127,20 @@ __device__ __forceinline__ void tma4(uint32_t dst, const CUtensorMap *m, int x, 
       "[%6];" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
       : "memory");
+}
+
+// mbar_wait without a call: a kernel that shifts registers between its warps
+// (setmaxnreg) cannot make one.
+__device__ __forceinline__ bool inline_wait(uint32_t bar, uint32_t parity, uint32_t *err) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const long long t0 = clock64();
+  while (!mbar_try_wait(bar, parity)) {
+    if (clock64() - t0 > kWaitCycles) {
+      atomicOr(err, NS_FLAG_TIMEOUT);
+      return false;
+    }
+  }
+  return true;
 }
 
 // two fp32 operations in one instruction
