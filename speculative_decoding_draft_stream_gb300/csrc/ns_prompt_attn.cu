@@ -4,13 +4,15 @@
 // Mathematics: for each query row, over its keys in tiles of 128,
 //   x_j = scale log2(e) q . k_j,  m = running bound of max x,
 //   l = sum 2^(x_j - m),  o = sum 2^(x_j - m) v_j;   out = o / l.
-// m is raised (and l and o multiplied by 2^(old - new)) only when a tile's
-// maximum passes it by more than 2^8: any m near the maximum gives the same
-// quotient, and the accumulator in tensor memory is then hardly ever
-// rewritten.  Scores, sums and o are fp32; a probability is rounded once, to
-// the values' type, as an operand of the second product (l sums it
-// unrounded).  fp16 probabilities are kept 2^6 times larger, so that with the
-// 2^8 above they stay within fp16's range, and 2^-30 of the largest is not lost.
+// m is the first tile's maximum, and is raised (l and o multiplied by
+// 2^(old - new)) only when the sum of 64 probabilities passes 2^15: any m
+// that is not far below the maximum gives the same quotient, so after the
+// first tile no maximum is taken (the sum is needed anyway) and the
+// accumulator in tensor memory is hardly ever rewritten.  Scores, sums and o
+// are fp32; a probability is rounded once, to the values' type, as an operand
+// of the second product (l sums it unrounded).  fp16 probabilities are kept
+// 2^6 times larger: within fp16's range under the bound on the sum, and 2^-30
+// of the largest is not lost.
 //
 // Rows: the query heads that share a key-value head are packed with their
 // tokens into tiles of 128 rows (128 / group tokens each), so a tile of keys
@@ -54,7 +56,7 @@ constexpr int kFaThreads = 384;
 constexpr int kFaRing = 5;       // key or value tiles in flight
 constexpr int kFaKeys = 128;     // keys of a tile
 constexpr int kFaHalf = 128 * 128;  // bytes of 128 rows of 64 elements
-constexpr float kFaSlack = 8.f;  // log2 of how far scores may pass m before it is raised
+constexpr float kFaLimit = 32768.f;  // a sum of 64 probabilities above this says that m is too low
 constexpr int kFaChecks = 4;     // value tiles looked through ahead of the product
 
 template <typename T>
@@ -79,7 +81,7 @@ struct FaSmem {
   static constexpr int kQ = 0, kKV = 2 * kTile, kMisc = kKV + kFaRing * kTile;
   // barriers, 8 bytes each
   static constexpr int kKvFull = kMisc, kKvEmpty = kKvFull + 8 * kFaRing, kQFull = kKvEmpty + 8 * kFaRing,
-                       kQEmpty = kQFull + 8, kSFull = kQEmpty + 8, kPFull = kSFull + 16, kOFull = kPFull + 32,
+                       kQEmpty = kQFull + 8, kSFull = kQEmpty + 8, kPFull = kSFull + 16, kPvHalf = kPFull + 32, kOFull = kPvHalf + 16,
                        kOEmpty = kOFull + 16, kCheck = kOEmpty + 16, kWFull = kCheck + 8 * kFaChecks,
                        kWEmpty = kWFull + 16, kSlot = kWEmpty + 16, kWork = kSlot + 16, kWildAny = kWork + 2 * 32,
                        kWild = kWildAny + 16, kEnd = kWild + 2 * (int)sizeof(Wild);
@@ -179,6 +181,7 @@ __global__ void __launch_bounds__(kFaThreads, 1)
       mbar_init(base + L::kSFull + 8 * i, 1);
       mbar_init(base + L::kPFull + 16 * i, 128);      // the probabilities of the first 64 keys
       mbar_init(base + L::kPFull + 16 * i + 8, 128);  // and of the others
+      mbar_init(base + L::kPvHalf + 8 * i, 1);        // the product with the first 64 keys is over
       mbar_init(base + L::kOFull + 8 * i, 1);
       mbar_init(base + L::kOEmpty + 8 * i, 128);
       mbar_init(base + L::kWFull + 8 * i, 1);
@@ -233,96 +236,115 @@ __global__ void __launch_bounds__(kFaThreads, 1)
         umma::inline_wait(base + L::kKvFull + 8 * (q % kFaRing), (q / kFaRing) & 1, err);
     }
   } else if (warp == 1) {
-    // products: the whole warp waits and counts, one lane issues
-    Work w;
-    int it = 0, checked = 0;
-    int np[2] = {0, 0}, no[2] = {0, 0};  // probabilities awaited, items begun, of each row tile
-    bool ok = true;
-    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0), kv0 = __shfl_sync(0xffffffffu, base, 0) + L::kKV;
-    auto wait = [&](uint32_t bar, int phase) {
-      return __all_sync(0xffffffffu, umma::inline_wait(base + bar, phase & 1, err));
-    };
-    auto scores = [&](int t, int stage) {
-      const uint64_t A = umma::desc_k(kv0 - L::kKV + L::kQ + t * L::kTile), B = umma::desc_k(kv0 + stage * L::kTile);
-      if (umma::elect()) {
+    if (umma::elect()) {  // products
+      // A product that waits for its operands leaves the tensor cores idle: only one or two are queued behind
+      // the running one.  So each group looks whether the next one's barrier is over before its own last products.
+      Work w;
+      int sl = 0, ph = 0, checked = 0;  // ring slot and phase of the next tile
+      int np[2] = {0, 0}, no[2] = {0, 0};  // probabilities awaited, items begun, of each row tile
+      bool ok = true, begun = false;
+      auto next = [&]() {
+        if (++sl == kFaRing) sl = 0, ph ^= 1;
+      };
+      auto peek = [&](uint32_t bar, int phase) { return umma::test_wait(base + bar, phase & 1); };
+      auto wait = [&](uint32_t bar, int phase, bool seen = false) {
+        if (!seen && ok) ok = umma::inline_wait(base + bar, phase & 1, err);
+        umma::fence_after();
+      };
+      // S_t = Q_t K^T; the look at the next barrier comes before the last two products
+      auto scores = [&](int t, int slot, uint32_t bar, int phase) {
+        const uint64_t A = umma::desc_k(base + L::kQ + t * L::kTile), B = umma::desc_k(base + L::kKV + slot * L::kTile);
+        bool seen = false;
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
+          if (kk == D / 16 - 2) seen = peek(bar, phase);
           const uint32_t off = ((kk >> 2) * kFaHalf + (kk & 3) * 32) >> 4;  // in the descriptors' 16-byte units
-          umma::mma_ss(tm + t * 128, A + off, B + off, kIdS, kk != 0);
+          umma::mma_ss(tmem + t * 128, A + off, B + off, kIdS, kk != 0);
         }
         umma::commit(base + L::kSFull + 8 * t);
-      }
-      __syncwarp();
-    };
-    auto commit = [&](uint32_t bar) {
-      if (umma::elect()) umma::commit(base + bar);
-      __syncwarp();
-    };
-    for (int i = 0; ok; ++i) {
-      const bool more = get_work(base, L::kWFull, g, L::kWork, i, w, err);
-      if (!__all_sync(0xffffffffu, more)) break;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(base + L::kWEmpty + 8 * (i & 1));
-      const int n0 = __shfl_sync(0xffffffffu, w.n0, 0), n1 = __shfl_sync(0xffffffffu, w.n1, 0), n = max(n0, n1);
-      const int hidden = __shfl_sync(0xffffffffu, first_hidden_tile(w), 0);
-      if (!(ok = wait(L::kQFull, i))) break;
-      if (!(ok = wait(L::kKvFull + 8 * (it % kFaRing), it / kFaRing))) break;
-      umma::fence_after();
-      scores(0, it % kFaRing);
-      if (n1 > 0) scores(1, it % kFaRing);
-      commit(L::kKvEmpty + 8 * (it % kFaRing));
-      if (n == 1) commit(L::kQEmpty);
-      ++it;
-      for (int j = 0; j < n && ok; ++j) {
-        const int sv = it % kFaRing, sk = (it + 1) % kFaRing;
-        if (!(ok = wait(L::kKvFull + 8 * sv, it / kFaRing))) break;
-        if (j >= hidden) {
-          if (!(ok = wait(L::kCheck + 8 * (checked % kFaChecks), checked / kFaChecks))) break;
-          ++checked;
+        return seen;
+      };
+      // O_t += P_t V, 64 keys
+      auto values = [&](int t, int slot, int h, bool more, uint32_t bar, int phase) {
+        const uint64_t V = umma::desc_mn(base + L::kKV + slot * L::kTile, kFaHalf);
+        bool seen = false;
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) {
+          if (kk == 2) seen = peek(bar, phase);
+          umma::mma_ts(tmem + 256 + t * 128, tmem + t * 128 + (h * 4 + kk) * 8, V + (h * 4 + kk) * (2048 >> 4), kIdO,
+                       more || h > 0 || kk > 0);
         }
-        bool have_k = false;
+        return seen;
+      };
+      for (int i = 0; get_work(base, L::kWFull, g, L::kWork, i, w, err); ++i) {
+        mbar_arrive(base + L::kWEmpty + 8 * (i & 1));
+        const int n0 = w.n0, n1 = w.n1, n = max(n0, n1), hidden = first_hidden_tile(w);
+        wait(L::kQFull, i);
+        wait(L::kKvFull + 8 * sl, ph);
+        if (!ok) break;
+        scores(0, sl, L::kQFull, 0);
+        if (n1 > 0) scores(1, sl, L::kQFull, 0);
+        umma::commit(base + L::kKvEmpty + 8 * sl);
+        if (n == 1) umma::commit(base + L::kQEmpty);
+        next();
+        begun = true;
+        bool seen_p = false;  // the first half of row tile 0's probabilities
+        for (int j = 0; j < n && ok; ++j) {
+          const int sv = sl, pv = ph;
+          next();
+          const int sk = sl, pk = ph;
+          const bool more = j + 1 < n;
+          if (more) next();
+          wait(L::kKvFull + 8 * sv, pv);
+          if (j >= hidden) {
+            wait(L::kCheck + 8 * (checked % kFaChecks), checked / kFaChecks);
+            ++checked;
+          }
+          bool seen_k = false, seen = seen_p, have_k = false;
+          seen_p = false;
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          const int nt = t ? n1 : n0;
-          if (ok && j < nt) {
-            if (j == 0 && no[t] > 0) ok = wait(L::kOEmpty + 8 * t, no[t] - 1);
-            const uint64_t V = umma::desc_mn(kv0 + sv * L::kTile, kFaHalf);
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              if (ok) ok = wait(L::kPFull + 16 * t + 8 * h, np[t]);
-              umma::fence_after();
-              if (ok && umma::elect()) {
-#pragma unroll
-                for (int kk = 4 * h; kk < 4 * h + 4; ++kk)
-                  umma::mma_ts(tm + 256 + t * 128, tm + t * 128 + kk * 8, V + kk * (2048 >> 4), kIdO, j > 0 || kk > 0);
+          for (int t = 0; t < 2; ++t) {
+            const int nt = t ? n1 : n0;
+            if (ok && j < nt) {
+              if (j == 0 && no[t] > 0) wait(L::kOEmpty + 8 * t, no[t] - 1);
+              wait(L::kPFull + 16 * t, np[t], seen);
+              if (!ok) break;
+              seen = values(t, sv, 0, j > 0, L::kPFull + 16 * t + 8, np[t]);
+              umma::commit(base + L::kPvHalf + 8 * t);
+              wait(L::kPFull + 16 * t + 8, np[t], seen);
+              if (!ok) break;
+              seen = values(t, sv, 1, j > 0, L::kKvFull + 8 * sk, pk);
+              if (!have_k) seen_k = seen;
+              seen = false;
+              ++np[t];
+              if (j + 1 == nt) {
+                umma::commit(base + L::kOFull + 8 * t);
+                ++no[t];
               }
-              __syncwarp();
             }
-            ++np[t];
-            if (ok && j + 1 == nt) {
-              commit(L::kOFull + 8 * t);
-              ++no[t];
+            if (ok && j + 1 < nt) {
+              if (!have_k) wait(L::kKvFull + 8 * sk, pk, seen_k);
+              have_k = true;
+              if (!ok) break;
+              seen = scores(t, sk, L::kPFull + 16 * (1 - t), np[1 - t]);
+              if (t == 1) seen_p = seen && j + 1 < n0;
             }
           }
-          if (ok && j + 1 < nt) {
-            if (!have_k) ok = wait(L::kKvFull + 8 * sk, (it + 1) / kFaRing);
-            have_k = true;
-            umma::fence_after();
-            if (ok) scores(t, sk);
+          if (!ok) break;
+          umma::commit(base + L::kKvEmpty + 8 * sv);
+          if (more) {
+            umma::commit(base + L::kKvEmpty + 8 * sk);
+            if (j + 2 == n) umma::commit(base + L::kQEmpty);
           }
         }
         if (!ok) break;
-        commit(L::kKvEmpty + 8 * sv);
-        ++it;
-        if (j + 1 < n) {
-          commit(L::kKvEmpty + 8 * sk);
-          if (j + 2 == n) commit(L::kQEmpty);
-          ++it;
-        }
+      }
+      // the last commit has arrived before the CTA leaves
+      if (ok && begun) {
+        const int last = sl ? sl - 1 : kFaRing - 1;
+        wait(L::kKvEmpty + 8 * last, sl ? ph : ph ^ 1);
       }
     }
-    // the last commit has arrived before the CTA leaves
-    if (ok && it > 0) wait(L::kKvEmpty + 8 * ((it - 1) % kFaRing), (it - 1) / kFaRing);
   } else if (warp == 2) {  // hidden values
     Work w;
     int it = 0, checked = 0;
@@ -410,8 +432,8 @@ __global__ void __launch_bounds__(kFaThreads, 1)
         ok = __all_sync(0xffffffffu, umma::inline_wait(base + L::kSFull + 8 * t, ns & 1, err));
         if (!ok) break;
         umma::fence_after();
-        uint32_t s[128];
-        float mx[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
+        uint32_t s[128], p[32];
+        float sum;
         auto mask = [&](int from) {  // keys after the row's token, among 64
           const int see = tok + 1 - j * kFaKeys;
 #pragma unroll
@@ -419,25 +441,19 @@ __global__ void __launch_bounds__(kFaThreads, 1)
             if (e >= see) s[e] = 0xff800000u;
         };
         auto most = [&](int from) {
+          float mx[2] = {kNegInf, kNegInf};
 #pragma unroll
-          for (int e = from; e < from + 64; e += 8)
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-              mx[q] = fmaxf(fmaxf(mx[q], __uint_as_float(s[e + 2 * q])), __uint_as_float(s[e + 2 * q + 1]));
+          for (int e = from; e < from + 64; e += 4) {
+            mx[0] = fmaxf(fmaxf(mx[0], __uint_as_float(s[e])), __uint_as_float(s[e + 1]));
+            mx[1] = fmaxf(fmaxf(mx[1], __uint_as_float(s[e + 2])), __uint_as_float(s[e + 3]));
+          }
+          return fmaxf(mx[0], mx[1]) * a.c;
         };
-        umma::ld32(tS, s);
-        umma::ld32(tS + 32, s + 32);
-        umma::wait_ld();
-        umma::ld32(tS + 64, s + 64);
-        umma::ld32(tS + 96, s + 96);
-        if (j >= clear) mask(0);
-        most(0);
-        // the probabilities of 64 keys with the m that there is; sum2 gets their sum
-        uint32_t p[32];
-        uint64_t sum2[2];
+        // the probabilities of 64 keys with the m that there is, and their sum
         auto probabilities = [&](int from) {
           const float shift = kFaOffset<T> - (m == kNegInf ? 0.f : m);
           const uint64_t shift2 = umma::pack2(shift, shift);
+          uint64_t sum2[2] = {0, 0};
 #pragma unroll
           for (int e = 0; e < 64; e += 2) {
             float x, y;
@@ -448,48 +464,77 @@ __global__ void __launch_bounds__(kFaThreads, 1)
             p[e / 2] = Type<T>::pack(x, y);
             sum2[(e >> 1) & 1] = umma::add2(sum2[(e >> 1) & 1], umma::pack2(x, y));
           }
+          float x, y;
+          umma::unpack2(umma::add2(sum2[0], sum2[1]), x, y);
+          sum = x + y;
         };
-        // m hardly ever changes after the first tile, so the first half is taken with the old one while the
-        // maximum is found, and again where that was wrong
-        sum2[0] = sum2[1] = 0;
-        if (j > 0) probabilities(0);
-        umma::wait_ld();
-        if (j >= clear) mask(64);
-        most(64);
-        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.c;
-        const bool raise = live && (top > m + kFaSlack || m == kNegInf);
-        if (j == 0 || __any_sync(0xffffffffu, raise)) {
+        // where the sum says that m is too low for some row: its new m, and everything before in terms of it
+        auto raise = [&](bool row, float top) {
           const float was = m;
-          if (raise) m = fmaxf(m, top);
-          if (j > 0) {
-            // the accumulator is still: S of this tile came after the last product into it
-            const float f = raise ? ex2(was - (m == kNegInf ? 0.f : m)) : 1.f;
-            l *= f;
+          if (row) m = fmaxf(m, top);
+          const float f = row ? ex2(was - (m == kNegInf ? 0.f : m)) : 1.f;
+          l *= f;
 #pragma unroll 1
-            for (int q = 0; q < D / 16; ++q) {
-              uint32_t o[16];
-              umma::ld16(tO + q * 16, o);
-              umma::wait_ld();
+          for (int q = 0; q < D / 16; ++q) {
+            uint32_t o[16];
+            umma::ld16(tO + q * 16, o);
+            umma::wait_ld();
 #pragma unroll
-              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-              umma::st16(tO + q * 16, o);
-            }
+            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+            umma::st16(tO + q * 16, o);
           }
-          sum2[0] = sum2[1] = 0;
-          probabilities(0);
+        };
+        umma::ld32(tS, s);
+        umma::ld32(tS + 32, s + 32);
+        umma::wait_ld();
+        umma::ld32(tS + 64, s + 64);
+        umma::ld32(tS + 96, s + 96);
+        if (j >= clear) mask(0);
+        bool whole = false;  // the second half has come
+        if (j == 0) {
+          umma::wait_ld();
+          if (j >= clear) mask(64);
+          whole = true;
+          m = fmaxf(most(0), most(64));
+        }
+        probabilities(0);
+        if (j > 0) {
+          const bool low = live && (sum > kFaLimit || m == kNegInf);
+          if (__any_sync(0xffffffffu, low)) {
+            umma::wait_ld();
+            if (j >= clear) mask(64);
+            whole = true;
+            // the accumulator is still: S of this tile came after the last product into it
+            raise(low, fmaxf(most(0), most(64)));
+            probabilities(0);
+          }
         }
         umma::st32(tS, p);
         umma::wait_st();
         umma::fence_before();
         mbar_arrive(base + L::kPFull + 16 * t);
+        l += sum;
+        if (!whole) {
+          umma::wait_ld();
+          if (j >= clear) mask(64);
+        }
         probabilities(64);
+        if (j > 0) {
+          const bool low = live && sum > kFaLimit;
+          if (__any_sync(0xffffffffu, low)) {
+            // the product with the first half must be over before the accumulator is touched
+            ok = __all_sync(0xffffffffu, umma::inline_wait(base + L::kPvHalf + 8 * t, ns & 1, err));
+            umma::fence_after();
+            raise(low, most(64));
+            probabilities(64);
+          }
+        }
         umma::st32(tS + 32, p);
-        float x, y;
-        umma::unpack2(umma::add2(sum2[0], sum2[1]), x, y);
-        l += x + y;
+        l += sum;
         umma::wait_st();
         umma::fence_before();
         mbar_arrive(base + L::kPFull + 16 * t + 8);
+        if (!ok) break;
       }
       if (!ok) break;
       if (nt > 0) {

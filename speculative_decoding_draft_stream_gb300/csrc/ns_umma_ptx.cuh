@@ -24,10 +24,9 @@ __device__ __forceinline__ void commit(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
 
-// One lane of a converged warp (the same one each time).  Code that issues
-// tcgen05.mma runs in the whole warp, with only the instruction itself under
-// this: its operands then stay in uniform registers.  Under `if (lane == 0)`
-// mixed products issue at 101 clocks each, so at 68 (M = N = 128, K = 16).
+// One lane of a converged warp (the same one each time), as the compiler
+// knows.  Mixed products (M = N = 128, K = 16) issue every 68 clocks under
+// this and every 101 under `if (lane == 0)`.
 __device__ __forceinline__ bool elect() {
   uint32_t p;
   asm volatile(
@@ -127,6 +126,17 @@ __device__ __forceinline__ void tma4(uint32_t dst, const CUtensorMap *m, int x, 
       "[%6];" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
       : "memory");
+}
+
+// Whether a phase is over; never waits.
+__device__ __forceinline__ bool test_wait(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
 }
 
 // mbar_wait without a call: a kernel that shifts registers between its warps
