@@ -20,7 +20,7 @@
 //
 // A CTA (one per SM, it keeps taking items, longest first) has five roles:
 //   warp 0     TMA loads: the item's queries, then key and value tiles into a
-//              ring of five;
+//              ring of four;
 //   warp 1     tcgen05.mma: S_i = Q_i K^T into tensor memory, O_i += P_i V
 //              with P_i read from tensor memory, for the row tiles i = 0, 1 in
 //              turn: while one tile's softmax runs, the other's products do;
@@ -53,7 +53,7 @@ using attn::ex2;
 using attn::kNegInf;
 
 constexpr int kFaThreads = 384;
-constexpr int kFaRing = 5;       // key or value tiles in flight
+constexpr int kFaRing = 4;       // key or value tiles in flight
 constexpr int kFaKeys = 128;     // keys of a tile
 constexpr int kFaHalf = 128 * 128;  // bytes of 128 rows of 64 elements
 constexpr float kFaLimit = 32768.f;  // a sum of 64 probabilities above this says that m is too low
@@ -78,7 +78,7 @@ constexpr uint16_t kNever = 0xffff;
 template <int D>
 struct FaSmem {
   static constexpr int kTile = D / 64 * kFaHalf;  // a row tile of queries, or a key or value tile
-  static constexpr int kQ = 0, kKV = 2 * kTile, kMisc = kKV + kFaRing * kTile;
+  static constexpr int kQ = 0, kKV = 2 * kTile, kOut = kKV + kFaRing * kTile, kMisc = kOut + 8 * 4096;
   // barriers, 8 bytes each
   static constexpr int kKvFull = kMisc, kKvEmpty = kKvFull + 8 * kFaRing, kQFull = kKvEmpty + 8 * kFaRing,
                        kQEmpty = kQFull + 8, kSFull = kQEmpty + 8, kPFull = kSFull + 16, kPvHalf = kPFull + 32, kOFull = kPvHalf + 16,
@@ -547,16 +547,23 @@ __global__ void __launch_bounds__(kFaThreads, 1)
         const bool wild = *(reinterpret_cast<volatile int *>(g + L::kWildAny) + (i & 1)) != 0;
         const Wild *wd = reinterpret_cast<const Wild *>(g + L::kWild) + (i & 1);
         const int upto = tok - first_hidden_tile(w) * kFaKeys;  // last position the row sees
-        uint4 *dst = reinterpret_cast<uint4 *>(static_cast<T *>(a.out) + at * D);
-#pragma unroll
-        for (int q = 0; q < D / 32; ++q) {
-          uint32_t o[32];
-          umma::ld32(tO + q * 32, o);
+        // 64 columns at a time through shared memory, so that a store covers whole lines of a few rows
+        uint8_t *stage = g + L::kOut + (warp - 4) * 4096;
+        const long long row_at = live ? at : -1;
+#pragma unroll 1
+        for (int q = 0; q < D / 64; ++q) {
+          uint32_t o[64];
+          umma::ld32(tO + q * 64, o);
+          umma::ld32(tO + q * 64 + 32, o + 32);
           umma::wait_ld();
+          if (q == D / 64 - 1) {
+            umma::fence_before();
+            mbar_arrive(base + L::kOEmpty + 8 * t);
+          }
           if (wild) {
 #pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              const int d = q * 32 + e;
+            for (int e = 0; e < 64; ++e) {
+              const int d = q * 64 + e;
               const bool n = (int)wd->nan[d] <= upto, p = (int)wd->pos[d] <= upto, b = (int)wd->neg[d] <= upto;
               if (n || (p && b))
                 o[e] = 0x7fffffffu;
@@ -564,18 +571,23 @@ __global__ void __launch_bounds__(kFaThreads, 1)
                 o[e] = __float_as_uint(__uint_as_float(o[e]) + (p ? -kNegInf : kNegInf));
             }
           }
-          if (live) {
 #pragma unroll
-            for (int e = 0; e < 32; e += 8)
-              dst[q * 4 + e / 8] =
-                  make_uint4(Type<T>::pack(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv),
-                             Type<T>::pack(__uint_as_float(o[e + 2]) * inv, __uint_as_float(o[e + 3]) * inv),
-                             Type<T>::pack(__uint_as_float(o[e + 4]) * inv, __uint_as_float(o[e + 5]) * inv),
-                             Type<T>::pack(__uint_as_float(o[e + 6]) * inv, __uint_as_float(o[e + 7]) * inv));
+          for (int e = 0; e < 64; e += 8)
+            *reinterpret_cast<uint4 *>(stage + lane * 128 + (((e >> 3) ^ (lane & 7)) << 4)) =
+                make_uint4(Type<T>::pack(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv),
+                           Type<T>::pack(__uint_as_float(o[e + 2]) * inv, __uint_as_float(o[e + 3]) * inv),
+                           Type<T>::pack(__uint_as_float(o[e + 4]) * inv, __uint_as_float(o[e + 5]) * inv),
+                           Type<T>::pack(__uint_as_float(o[e + 6]) * inv, __uint_as_float(o[e + 7]) * inv));
+          __syncwarp();
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const int row = e * 4 + (lane >> 3);
+            const long long to = __shfl_sync(0xffffffffu, row_at, row);
+            const uint4 x = *reinterpret_cast<const uint4 *>(stage + row * 128 + (((lane & 7) ^ (row & 7)) << 4));
+            if (to >= 0) *reinterpret_cast<uint4 *>(static_cast<T *>(a.out) + to * D + q * 64 + (lane & 7) * 8) = x;
           }
+          __syncwarp();
         }
-        umma::fence_before();
-        mbar_arrive(base + L::kOEmpty + 8 * t);
         if (live && a.lse) a.lse[at] = (m - kFaOffset<T> + log2f(l)) * attn::kLn2;
       }
       __syncwarp();
