@@ -109,53 +109,76 @@ __device__ __forceinline__ bool get_work(uint32_t base, int full, const uint8_t 
   return w.n0 > 0;
 }
 
-// Warp 3: the items of CTA `cta` in order.  All items, longest first, are in
-// one line: block x of tokens (from the last), sequence, unit; the CTAs take
-// turns forth and back, so each gets a like share of every length.
-template <typename Put>
-__device__ __forceinline__ void deal(const FaArgs &a, int cta, int ctas, const Put &put) {
-  const int lane = threadIdx.x & 31, block = 2 * a.per_tile;
-  const int X = (a.max_len + block - 1) / block;
-  const long long pairs = (long long)X * a.n_seqs;
-  long long before = 0, turn = 0, mine = cta;
-  for (long long p0 = 0; p0 < pairs; p0 += 32) {
-    const long long p = p0 + lane;
-    int x = 0, t0 = 0, len = 0;
-    bool ok = false;
-    if (p < pairs) {
-      const int s = (int)(p % a.n_seqs);
-      x = X - 1 - (int)(p / a.n_seqs);
-      t0 = a.cu[s];
-      const int t1 = a.cu[s + 1];
-      if (t0 < 0 || t1 < t0 || t1 > a.tokens) {
-        if (cta == 0) set_flag(a.err, NS_FLAG_BAD_SEQ);
-      } else {
-        if (t1 - t0 > a.max_len && cta == 0) set_flag(a.err, NS_FLAG_BAD_SEQ);
-        len = min(t1 - t0, a.max_len);
-        ok = (long long)x * block < len;
-      }
-    }
-    const uint32_t live = __ballot_sync(0xffffffffu, ok);
-    const long long here = (long long)__popc(live) * a.units;
-    while (mine < before + here) {
-      const int nth = (int)((mine - before) / a.units);
-      const int from = __fns(live, 0, nth + 1);
-      Work w;
-      w.seq0 = __shfl_sync(0xffffffffu, t0, from);
-      w.len = __shfl_sync(0xffffffffu, len, from);
-      w.tok0 = __shfl_sync(0xffffffffu, x, from) * block;
-      w.unit = (int)((mine - before) % a.units);
-      w.n0 = (min(w.len, w.tok0 + a.per_tile) + kFaKeys - 1) / kFaKeys;
-      w.n1 = w.tok0 + a.per_tile < w.len ? (min(w.len, w.tok0 + block) + kFaKeys - 1) / kFaKeys : 0;
-      if (!put(w)) return;
-      ++turn;
-      mine = turn * ctas + ((turn & 1) ? ctas - 1 - cta : cta);
-    }
-    before += here;
-  }
-  Work end{};
-  put(end);
+// A sequence's first token and its length (0 where its bounds are invalid).
+__device__ __forceinline__ int sequence(const FaArgs &a, int s, int &len) {
+  const int t0 = a.cu[s], t1 = a.cu[s + 1];
+  len = t0 < 0 || t1 < t0 || t1 > a.tokens ? 0 : min(t1 - t0, a.max_len);
+  return t0;
 }
+
+// The items of CTA `cta` in order (a whole warp).  All items, longest first,
+// are in one line: block x of tokens (from the last), sequence, unit; the CTAs
+// take turns forth and back, so each gets a like share of every length.  A
+// lane keeps the longest of its 32nd of the sequences, so at each x only
+// groups that reach it are looked at.
+struct Dealer {
+  int cta, ctas, lane, block, size;
+  int most;                // blocks of the lane's group's longest sequence
+  int x, s;                // where the line is: block, and the lane's sequence
+  uint32_t groups, live;   // groups left at x; sequences of the 32 at s that reach x
+  int t0, len;             // of the lane's sequence
+  int before, here;        // items before these 32 sequences, and of them
+  int turn, mine;          // the CTA's next item
+
+  __device__ __forceinline__ void begin(const FaArgs &a, int cta_, int ctas_) {
+    cta = cta_, ctas = ctas_, lane = threadIdx.x & 31, block = 2 * a.per_tile;
+    size = (a.n_seqs + 1023) / 1024 * 32;
+    most = 0;
+    for (int q = lane * size; q < min(a.n_seqs, (lane + 1) * size); ++q) {
+      int n;
+      sequence(a, q, n);
+      if (cta == 0 && a.cu[q + 1] - a.cu[q] != n) set_flag(a.err, NS_FLAG_BAD_SEQ);
+      most = max(most, (n + block - 1) / block);
+    }
+    x = __reduce_max_sync(0xffffffffu, most);
+    groups = 0, s = 0, before = 0, here = 0, turn = 0, mine = cta;
+  }
+  // the next 32 sequences that reach x, or some of the next lower x; false at the end
+  __device__ __forceinline__ bool advance(const FaArgs &a) {
+    before += here;
+    const int g0 = groups ? (__ffs(groups) - 1) * size : 0;
+    if (groups && s - lane + 32 < g0 + size) {
+      s += 32;
+    } else {
+      groups &= groups - 1;
+      while (groups == 0) {
+        if (--x < 0) return false;
+        groups = __ballot_sync(0xffffffffu, most > x);
+      }
+      s = (__ffs(groups) - 1) * size + lane;
+    }
+    t0 = len = 0;
+    if (s < a.n_seqs) t0 = sequence(a, s, len);
+    live = __ballot_sync(0xffffffffu, len > x * block);
+    here = __popc(live) * a.units;
+    return true;
+  }
+  __device__ __forceinline__ Work next(const FaArgs &a) {
+    Work w{};
+    while (mine >= before + here)
+      if (!advance(a)) return w;
+    const int from = __fns(live, 0, (mine - before) / a.units + 1);
+    w.seq0 = __shfl_sync(0xffffffffu, t0, from);
+    w.len = __shfl_sync(0xffffffffu, len, from);
+    w.tok0 = x * block;
+    w.unit = (mine - before) % a.units;
+    w.n0 = (min(w.len, w.tok0 + a.per_tile) + kFaKeys - 1) / kFaKeys;
+    w.n1 = w.tok0 + a.per_tile < w.len ? (min(w.len, w.tok0 + block) + kFaKeys - 1) / kFaKeys : 0;
+    ++turn;
+    mine = turn * ctas + ((turn & 1) ? ctas - 1 - cta : cta);
+    return w;
+  }
+};
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kFaThreads, 1)
@@ -395,19 +418,21 @@ __global__ void __launch_bounds__(kFaThreads, 1)
       if (lane == 0) mbar_arrive(base + L::kWEmpty + 8 * (i & 1));
     }
   } else if (warp == 3) {  // the items
-    int i = 0;
-    deal(a, blockIdx.x, gridDim.x, [&](const Work &w) {
-      bool ok = true;
-      if (i >= 2) ok = __all_sync(0xffffffffu, umma::inline_wait(base + L::kWEmpty + 8 * (i & 1), ((i >> 1) - 1) & 1, err));
-      if (ok && lane == 0) {
+    Dealer dealer;
+    dealer.begin(a, blockIdx.x, gridDim.x);
+    for (int i = 0;; ++i) {
+      const Work w = dealer.next(a);
+      if (i >= 2 &&
+          !__all_sync(0xffffffffu, umma::inline_wait(base + L::kWEmpty + 8 * (i & 1), ((i >> 1) - 1) & 1, err)))
+        break;
+      if (lane == 0) {
         *reinterpret_cast<Work *>(g + L::kWork + 32 * (i & 1)) = w;
         *(reinterpret_cast<volatile int *>(g + L::kWildAny) + (i & 1)) = 0;
         mbar_arrive(base + L::kWFull + 8 * (i & 1));
       }
       __syncwarp();
-      ++i;
-      return ok;
-    });
+      if (w.n0 == 0) break;
+    }
   } else {  // softmax of row tile t
     asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     const int t = (warp - 4) >> 2, wq = warp & 3;
