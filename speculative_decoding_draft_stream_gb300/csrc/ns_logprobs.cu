@@ -25,6 +25,7 @@
 
 #include "ns_internal.cuh"
 #include "ns_ops.cuh"
+#include "ns_umma_ptx.cuh"
 
 namespace ns {
 namespace {
@@ -114,16 +115,29 @@ struct Part {
 #pragma unroll
     for (int i = 1; i < N; ++i) top = fmaxf(top, x[i]);
     if (top > m) raise(top, c);
-    const float at = m == kNegInf ? 0.f : m;  // nothing but -inf so far: exponents of -inf, not NaN
-    float s1 = 0.f, u1 = 0.f;
+    const float at = m == kNegInf ? 0.f : -m;  // nothing but -inf so far: exponents of -inf, not NaN
+    if (N == 1) {
+      const float d = floor_nan((x[0] + at) * c, kFloorD), e = ex2(d);
+      s += e;
+      u = fmaf(e, d, u);
+    } else {  // two at a time
+      const uint64_t at2 = umma::pack2(at, at), c2 = umma::pack2(c, c);
+      uint64_t s2 = 0, u2 = 0;
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const float d = floor_nan((x[i] - at) * c, kFloorD), e = ex2(d);
-      s1 += e;
-      u1 = fmaf(e, d, u1);
+      for (int i = 0; i + 1 < N; i += 2) {
+        float a, b;
+        umma::unpack2(umma::mul2(umma::add2(umma::pack2(x[i], x[i + 1]), at2), c2), a, b);
+        a = floor_nan(a, kFloorD), b = floor_nan(b, kFloorD);
+        const uint64_t e2 = umma::pack2(ex2(a), ex2(b));
+        s2 = umma::add2(s2, e2);
+        u2 = umma::fma2(e2, umma::pack2(a, b), u2);
+      }
+      float a, b;
+      umma::unpack2(s2, a, b);
+      s += a + b;
+      umma::unpack2(u2, a, b);
+      u += a + b;
     }
-    s += s1;
-    u += u1;
   }
 };
 

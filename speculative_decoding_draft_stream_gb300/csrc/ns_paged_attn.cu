@@ -323,43 +323,73 @@ __global__ void __launch_bounds__(kPaThreads) paged_attn_kernel(const PagedAttnA
   }
 }
 
-// Joins the parts of an item that several CTAs had: a warp per row.
+// Joins the parts of an item that several CTAs had.  A CTA has some rows of an
+// item; kGroups warps have a row's parts in turns and join in group order.
+constexpr int kJoinWarps = 8;
+template <int WM>
+struct Join {
+  static constexpr int kGroups = WM == 1 ? 4 : 1;  // few rows may have hundreds of parts, many rows have two or three
+  static constexpr int kRows = kJoinWarps / kGroups;
+};
 template <typename T, int D, int WM>
-__global__ void __launch_bounds__(kPaThreads) paged_join_kernel(const PagedAttnArgs a, int blocks, int ctas) {
-  constexpr int kRows = 16 * WM, N = D / 32;
-  const int lane = threadIdx.x & 31, rl = blockIdx.y * (kPaThreads / kWarp) + (threadIdx.x >> 5);
+__global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const PagedAttnArgs a, int blocks, int ctas) {
+  constexpr int kRows = 16 * WM, N = D / 32, G = Join<WM>::kGroups;
+  extern __shared__ int s_part[];  // [ctas] rows before each part
+  __shared__ float s_o[G][Join<WM>::kRows][D];
+  __shared__ float s_l[G][Join<WM>::kRows];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, grp = warp % G, rw = warp / G;
   const int items = a.kv_heads * blocks, b = blockIdx.x / items, item = blockIdx.x % items;
-  const int head = item / blocks, r = item % blocks * kRows + rl;
+  const int head = item / blocks, rl = blockIdx.y * Join<WM>::kRows + rw, r = item % blocks * kRows + rl;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (r >= a.n * a.group) return;
   const PaWs ws = pa_ws(a.ws, a.n_seqs, ctas, kRows);
-  const long long total = ws.cum[a.n_seqs];
-  const long long nt = (ws.cum[b + 1] - ws.cum[b]) / items;
-  const long long from = ws.cum[b] + item * nt, to = from + nt;  // the item's tiles
+  const long long total = ws.cum[a.n_seqs], cb = ws.cum[b];
+  const long long nt = (ws.cum[b + 1] - cb) / items;
+  const long long from = cb + item * nt, to = from + nt;  // the item's tiles
   const int c0 = (int)(((from + 1) * ctas - 1) / total), c1 = (int)((to * ctas - 1) / total);
   if (c0 == c1) return;  // one CTA had it all
-  // a part is its CTA's first unless the CTA began before the item
-  auto part = [&](int c) { return ((size_t)c * 2 + (total * c / ctas >= from ? 0 : 1)) * kRows + rl; };
-  float m = kNegInf;
-  for (int c = c0 + lane; c <= c1; c += kWarp)
-    if (total * c / ctas < total * (c + 1) / ctas) m = fmaxf(m, ws.ml[part(c)].x);
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-  const float safe = m == kNegInf ? 0.f : m;
-  float l = 0.f, o[N];
+  for (int c = c0 + tid; c <= c1; c += kJoinWarps * 32) {
+    const long long first = total * c / ctas;
+    // a part is its CTA's first unless the CTA began before the item; a CTA may have no tiles at all
+    s_part[c - c0] = first == total * (c + 1) / ctas ? -1 : (c * 2 + (first >= from ? 0 : 1)) * kRows;
+  }
+  __syncthreads();
+  const bool live = r < a.n * a.group && rl < kRows;
+  const int parts = c1 - c0 + 1;
+  float m = kNegInf, l = 0.f, o[N];
 #pragma unroll
   for (int i = 0; i < N; ++i) o[i] = 0.f;
-#pragma unroll 4
-  for (int c = c0; c <= c1; ++c) {
-    if (total * c / ctas >= total * (c + 1) / ctas) continue;  // a CTA without tiles
-    const size_t at = part(c);
-    const float2 ml = ws.ml[at];
-    const float f = ex2(ml.x - safe);
-    l += ml.y * f;
-    const float *src = ws.o + at * D + lane * N;
+  if (live) {
+    for (int q = lane; q < parts; q += kWarp)
+      if (s_part[q] >= 0) m = fmaxf(m, ws.ml[s_part[q] + rl].x);
 #pragma unroll
-    for (int i = 0; i < N; ++i) o[i] = fmaf(src[i], f, o[i]);
+    for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+    const float safe = m == kNegInf ? 0.f : m;
+#pragma unroll 8
+    for (int q = grp; q < parts; q += G) {
+      if (s_part[q] < 0) continue;
+      const size_t at = (size_t)s_part[q] + rl;
+      const float2 ml = ws.ml[at];
+      const float f = ex2(ml.x - safe);
+      l += ml.y * f;
+      const float *src = ws.o + at * D + lane * N;
+#pragma unroll
+      for (int i = 0; i < N; ++i) o[i] = fmaf(src[i], f, o[i]);
+    }
   }
+  if (G > 1) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) s_o[grp][rw][lane * N + i] = o[i];
+    if (lane == 0) s_l[grp][rw] = l;
+    __syncthreads();
+    if (grp != 0) return;
+#pragma unroll
+    for (int g = 1; g < G; ++g) {
+      l += s_l[g][rw];
+#pragma unroll
+      for (int i = 0; i < N; ++i) o[i] += s_o[g][rw][lane * N + i];
+    }
+  }
+  if (!live) return;
   const int64_t at = ((int64_t)b * a.n + r / a.group) * a.q_heads + head * a.group + r % a.group;
   const float inv = l == 0.f ? 0.f : 1.f / l;
   uint32_t *dst = reinterpret_cast<uint32_t *>(static_cast<T *>(a.out) + at * D + lane * N);
@@ -381,8 +411,10 @@ cudaError_t launch(const PagedAttnArgs &a, int sms, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   const int rows = a.n * a.group < kRows ? a.n * a.group : kRows;
-  cfg.gridDim = dim3((unsigned)((long long)a.n_seqs * a.kv_heads * blocks), (unsigned)((rows + 3) / 4));
-  cfg.blockDim = dim3(kPaThreads);
+  cfg.gridDim = dim3((unsigned)((long long)a.n_seqs * a.kv_heads * blocks),
+                     (unsigned)((rows + Join<WM>::kRows - 1) / Join<WM>::kRows));
+  cfg.blockDim = dim3(kJoinWarps * 32);
+  cfg.dynamicSmemBytes = ctas * 4;
   cfg.stream = st;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -346,74 +346,89 @@ __global__ void __launch_bounds__(kMoveThreads) write_kernel(ns_kv_pages c, int 
   }
 }
 
-// Kept rows move down.  A warp takes one (sequence, layer, head, up to 512
-// bytes of the row) of k or v and walks its rows in order, a batch of rows at
-// a time: all of a batch's loads, then its stores.  Row t comes from keep[t]
-// >= t, so a batch's destinations lie before every later batch's sources,
-// and within a batch the loads come first: the move is in place.
-__global__ void __launch_bounds__(kMoveThreads) compact_kernel(ns_kv_pages c, const int32_t *seqs,
-                                                               const int32_t *base, const int32_t *keep, int keep_ld,
-                                                               const int32_t *n_keep, int n, int segs,
-                                                               uint32_t *err) {
-  const int lane = threadIdx.x & 31;
-  const long long it = (long long)blockIdx.x * kMoveWarps + (threadIdx.x >> 5);
-  const long long items = (long long)n * c.layers * c.heads * 2 * segs;
-  if (it >= items) return;
-  const int kv = (int)(it & 1);
-  long long u = it >> 1;
-  const int seg = (int)(u % segs);
-  u /= segs;
-  const int head = (int)(u % c.heads), layer = (int)(u / c.heads % c.layers), i = (int)(u / c.heads / c.layers);
+// Kept rows move down.  A CTA takes one sequence, k or v, and kMoverWarps of
+// its (layer, head, up to 512 bytes of the row), a warp each.  It walks the
+// kept rows in order, kMoveRows at a time: the threads find each row's two
+// places, for the next rows while these move, and every warp moves its part
+// of them, kMoveBatch 16-byte pieces a lane: all loads of a batch, then its
+// stores.  Row t comes from keep[t] >= t, so a batch's destinations lie before
+// every later batch's sources, and within a batch the loads come first: the
+// move is in place.
+//
+// Bound by HBM when there are many rows; the batch is what keeps enough bytes
+// in flight when there are few (layer, head) parts.
+constexpr int kMoverWarps = 4;
+constexpr int kMoveRows = 128;
+constexpr int kMoveBatch = 16;
+__global__ void __launch_bounds__(kMoverWarps * 32, 4)
+    compact_kernel(ns_kv_pages c, const int32_t *seqs, const int32_t *base, const int32_t *keep, int keep_ld,
+                   const int32_t *n_keep, int segs, uint32_t *err) {
+  __shared__ long long s_from[2][kMoveRows], s_to[2][kMoveRows];  // -1: stays
+  const int tid = threadIdx.x, lane = tid & 31, i = blockIdx.z, kv = blockIdx.y;
   const int s = seqs[i], m = n_keep[i], b0 = base[i];
-  bool ok = seq_ok(c, s) && m >= 0 && m <= keep_ld && b0 >= 0;
-  if (ok) {  // the first of a repeated sequence only
-    int hit = 0;
-    for (int j = lane; j < i; j += kWarp) hit |= seqs[j] == s;
-    ok = !__any_sync(0xffffffffu, hit);
-  }
-  const int len = ok ? c.lengths[s] : 0;
-  if (!ok || !len_ok(c, len)) {
-    if (lane == 0) set_flag(err, NS_FLAG_BAD_SEQ);
+  const bool again = repeated(seqs, i);  // only the first of a repeated sequence
+  const int len = seq_ok(c, s) ? c.lengths[s] : -1;
+  if (again || !seq_ok(c, s) || m < 0 || m > keep_ld || b0 < 0 || !len_ok(c, len)) {
+    if (tid == 0) set_flag(err, NS_FLAG_BAD_SEQ);
     return;
   }
   const int32_t *row = c.table + (size_t)s * c.table_ld;
   const int32_t *kp = keep + (size_t)i * keep_ld;
   const int64_t sp = kv ? c.v_page : c.k_page, st = kv ? c.v_token : c.k_token;
-  char *data = static_cast<char *>(kv ? c.v : c.k) + layer * (kv ? c.v_layer : c.k_layer) +
-               head * (kv ? c.v_head : c.k_head) + seg * 512;
-  const int cols = min(c.row_bytes - seg * 512, 512) / 16;  // lanes a row takes
-  const int per = kWarp / cols;                             // rows a warp moves at once
-  const int sub = lane / cols, col = lane % cols;
-  for (int t0 = 0; t0 < m; t0 += per * kUnroll) {
-    uint4 val[kUnroll];
-    char *to[kUnroll];
-#pragma unroll
-    for (int q = 0; q < kUnroll; ++q) {
-      const int t = t0 + q * per + sub;
-      to[q] = nullptr;
-      if (sub < per && t < m) {
-        const int from = kp[t];
-        if (from < t || (t > 0 && from <= kp[t - 1]) || (long long)b0 + from >= len) {
-          set_flag(err, NS_FLAG_BAD_SEQ);
-        } else if (from != t) {
-          const int p = b0 + from, d = b0 + t;
-          const int pa = row[p / c.page_size], pb = row[d / c.page_size];
-          if (pa < 0 || pa >= c.pages || pb < 0 || pb >= c.pages) {
-            set_flag(err, NS_FLAG_BAD_ID);
-          } else if (c.refs[pb] > 1) {
-            set_flag(err, NS_FLAG_SHARED_PAGE);
-          } else {
-            val[q] = *reinterpret_cast<const uint4 *>(data + pa * sp + p % c.page_size * st + col * 16);
-            to[q] = data + pb * sp + d % c.page_size * st + col * 16;
-          }
+  auto find = [&](int t0) {  // the places of rows t0 .. t0 + kMoveRows - 1
+    const int t = t0 + tid, slot = (t0 / kMoveRows) & 1;
+    long long src = -1, dst = -1;
+    if (t < m) {
+      const int from = kp[t];
+      if (from < t || (t > 0 && from <= kp[t - 1]) || (long long)b0 + from >= len) {
+        set_flag(err, NS_FLAG_BAD_SEQ);
+      } else if (from != t) {
+        const int p = b0 + from, d = b0 + t;
+        const int pa = row[p / c.page_size], pb = row[d / c.page_size];
+        if (pa < 0 || pa >= c.pages || pb < 0 || pb >= c.pages) {
+          set_flag(err, NS_FLAG_BAD_ID);
+        } else if (c.refs[pb] > 1) {
+          set_flag(err, NS_FLAG_SHARED_PAGE);
+        } else {
+          src = pa * sp + p % c.page_size * st;
+          dst = pb * sp + d % c.page_size * st;
         }
       }
     }
-    __syncwarp();  // every load of the batch before its stores
+    s_from[slot][tid] = src;
+    s_to[slot][tid] = dst;
+  };
+  static_assert(kMoveRows == kMoverWarps * 32, "a thread finds one row's places");
+  const int u = blockIdx.x * kMoverWarps + (tid >> 5);
+  const bool mine = u < c.layers * c.heads * segs;
+  const int seg = u % segs, head = u / segs % c.heads, layer = u / segs / c.heads;
+  char *data = static_cast<char *>(kv ? c.v : c.k) + (mine ? layer : 0) * (kv ? c.v_layer : c.k_layer) +
+               head * (kv ? c.v_head : c.k_head) + seg * 512;
+  const int cols = min(c.row_bytes - seg * 512, 512) / 16;  // lanes a row takes
+  const int per = kWarp / cols, sub = lane / cols;          // rows a warp moves at once
+  data += lane % cols * 16;
+  if (m > 0) find(0);
+  for (int t0 = 0; t0 < m; t0 += kMoveRows) {
+    __syncthreads();  // the places are there, and nobody reads the other ones any more
+    if (t0 + kMoveRows < m) find(t0 + kMoveRows);
+    if (!mine) continue;
+    const int slot = (t0 / kMoveRows) & 1, rows = min(kMoveRows, m - t0);
+    for (int q0 = 0; q0 < rows; q0 += per * kMoveBatch) {
+      uint4 val[kMoveBatch];
 #pragma unroll
-    for (int q = 0; q < kUnroll; ++q)
-      if (to[q]) *reinterpret_cast<uint4 *>(to[q]) = val[q];
-    __syncwarp();
+      for (int q = 0; q < kMoveBatch; ++q) {
+        const int t = q0 + q * per + sub;
+        if (sub < per && t < rows && s_from[slot][t] >= 0)
+          val[q] = __ldcs(reinterpret_cast<const uint4 *>(data + s_from[slot][t]));
+      }
+      __syncwarp();  // every load of the batch before its stores
+#pragma unroll
+      for (int q = 0; q < kMoveBatch; ++q) {
+        const int t = q0 + q * per + sub;
+        if (sub < per && t < rows && s_to[slot][t] >= 0) *reinterpret_cast<uint4 *>(data + s_to[slot][t]) = val[q];
+      }
+      __syncwarp();
+    }
   }
 }
 
@@ -459,11 +474,11 @@ cudaError_t launch_pages_write(const ns_kv_pages &c, int layer, const int32_t *s
 cudaError_t launch_pages_compact(const ns_kv_pages &c, const int32_t *seqs, const int32_t *base, const int32_t *keep,
                                  int keep_ld, const int32_t *n_keep, int n, uint32_t *err, cudaStream_t st) {
   const int segs = (c.row_bytes + 511) / 512;
-  const long long items = (long long)n * c.layers * c.heads * 2 * segs;
-  if ((items + kMoveWarps - 1) / kMoveWarps > 0x7fffffffLL) return cudaErrorInvalidValue;
+  const long long units = (long long)c.layers * c.heads * segs;
+  if (units > 0x7fffffffLL - kMoverWarps) return cudaErrorInvalidValue;
   if (keep_ld > 0)
-    compact_kernel<<<(unsigned)((items + kMoveWarps - 1) / kMoveWarps), kMoveThreads, 0, st>>>(
-        c, seqs, base, keep, keep_ld, n_keep, n, segs, err);
+    compact_kernel<<<dim3((unsigned)((units + kMoverWarps - 1) / kMoverWarps), 2, (unsigned)n), kMoverWarps * 32, 0,
+                     st>>>(c, seqs, base, keep, keep_ld, n_keep, segs, err);
   truncate_kernel<<<n, kSeqThreads, 0, st>>>(c, seqs, n_keep, base, keep_ld, err);
   return cudaGetLastError();
 }

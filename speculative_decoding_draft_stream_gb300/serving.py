@@ -42,14 +42,16 @@ class ns_kv_pages(ctypes.Structure):
                 [(n, ctypes.c_void_p) for n in ("table", "lengths", "refs")])
 
 
-def _need(cond: bool, what: str) -> None:
-    if not cond:
-        raise ValueError(what)
+# Every call's host time is part of its latency (a kernel here may take less
+# than its launch), so the checks below are plain comparisons on the path that
+# passes, and messages are only made when one fails.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+if _raw_stream is None:
+    def _raw_stream(index: int) -> int:
+        return torch.cuda.current_stream(index).cuda_stream
 
-
-def _on_device(what: str, t: torch.Tensor, device: torch.device) -> None:
-    if t.device != device:
-        raise ValueError(f"{what} must be on {device}, not {t.device}")
+_I32, _F32, _U8 = torch.int32, torch.float32, torch.uint8
+_empty = torch.empty
 
 
 def _device(t: torch.Tensor, what: str) -> torch.device:
@@ -59,40 +61,56 @@ def _device(t: torch.Tensor, what: str) -> torch.device:
     return d
 
 
-def _i32(what: str, t: torch.Tensor, device: torch.device, *shape) -> int:
-    if t.dtype != torch.int32 or t.device != device or not t.is_contiguous():
+def _i32(what: str, t: torch.Tensor, device: torch.device, shape) -> int:
+    if t.dtype is not _I32 or t.device != device or not t.is_contiguous():
         raise ValueError(f"{what} must be a contiguous int32 tensor on {device}")
-    if t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape)):
-        raise ValueError(f"{what} has shape {tuple(t.shape)}, expected {shape}")
+    if t.shape != shape:
+        raise ValueError(f"{what} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     return t.data_ptr()
 
 
-def _rows(what: str, t: torch.Tensor, device: torch.device, dtype: torch.dtype) -> None:
-    if t.dtype != dtype or t.device != device:
+def _i32_2d(what: str, t: torch.Tensor, device: torch.device) -> int:
+    if t.dim() != 2:
+        raise ValueError(f"{what} must have two dimensions")
+    return _i32(what, t, device, t.shape)
+
+
+def _rows(what: str, t: torch.Tensor, device: torch.device, dtype: torch.dtype):
+    """The strides of a tensor whose last dimension has consecutive elements."""
+    if t.dtype is not dtype or t.device != device:
         raise ValueError(f"{what} must be {dtype} on {device}, not {t.dtype} on {t.device}")
-    if t.stride(-1) != 1 and t.shape[-1] > 1:
+    st = t.stride()
+    if st[-1] != 1 and t.shape[-1] > 1:
         raise ValueError(f"{what} must have consecutive elements in its last dimension")
+    return st
 
 
 def _stream(stream, device, *made) -> int:
     """The stream's handle; tensors made here and used on another stream are recorded there."""
+    now = _raw_stream(device.index)
     if stream is None:
-        return torch.cuda.current_stream(device).cuda_stream
+        return now
     if not hasattr(stream, "cuda_stream"):
         stream = torch.cuda.ExternalStream(int(stream), device=device)
-    if stream.cuda_stream != torch.cuda.current_stream(device).cuda_stream:
+    if stream.cuda_stream != now:
         for t in made:
             t.record_stream(stream)
     return stream.cuda_stream
 
 
-def _output(what: str, t: Optional[torch.Tensor], shape, dtype, device, made: list) -> torch.Tensor:
-    if t is None:
-        t = torch.empty(shape, dtype=dtype, device=device)
-        made.append(t)
-    elif t.dtype != dtype or tuple(t.shape) != tuple(shape) or t.device != device or not t.is_contiguous():
+def _given(what: str, t: torch.Tensor, shape, dtype, device) -> None:
+    if t.dtype is not dtype or t.shape != shape or t.device != device or not t.is_contiguous():
         raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
-    return t
+
+
+def _workspace(workspace: Optional[torch.Tensor], need: int, device, made: list):
+    """The workspace (made here when it is None), its address and size."""
+    if workspace is None:
+        workspace = _empty(need if need > 16 else 16, dtype=_U8, device=device)
+        made.append(workspace)
+    elif workspace.device != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {device}")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 def attend_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu: torch.Tensor, max_len: int, *,
@@ -103,23 +121,38 @@ def attend_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu: torch.T
     longest.  Returns (out [T, Hq, D], lse fp32 [T, Hq]).  scale: 1 / sqrt(D) by default."""
     lib = load_library()
     dev = _device(q, "q")
-    _need(q.dtype in (torch.bfloat16, torch.float16), "q must be bf16 or fp16")
-    _need(q.dim() == 3 and k.dim() == 3 and v.dim() == 3, "q, k and v must be [tokens, heads, dim]")
+    dtype = q.dtype
+    if dtype is not torch.bfloat16 and dtype is not torch.float16:
+        raise ValueError("q must be bf16 or fp16")
+    if q.dim() != 3 or k.dim() != 3 or v.dim() != 3:
+        raise ValueError("q, k and v must be [tokens, heads, dim]")
     T, hq, d = q.shape
-    hkv = k.shape[1]
-    _need(tuple(k.shape) == (T, hkv, d) and k.shape == v.shape, "k and v must be [tokens, kv_heads, dim]")
-    _need(hkv > 0 and hq % hkv == 0, "q_heads must be a multiple of kv_heads")
-    for what, t in (("q", q), ("k", k), ("v", v)):
-        _rows(what, t, dev, q.dtype)
-    cu_ptr = _i32("cu", cu, dev, None)
-    _need(cu.shape[0] >= 1, "cu must have one more entry than there are sequences")
+    ks = k.shape
+    hkv = ks[1]
+    if ks[0] != T or ks[2] != d or v.shape != ks:
+        raise ValueError("k and v must be [tokens, kv_heads, dim]")
+    if hkv == 0 or hq % hkv:
+        raise ValueError("q_heads must be a multiple of kv_heads")
+    qst, kst, vst = _rows("q", q, dev, dtype), _rows("k", k, dev, dtype), _rows("v", v, dev, dtype)
+    n = cu.shape[0] if cu.dim() == 1 else 0
+    cu_ptr = _i32("cu", cu, dev, (n,))
+    if n < 1:
+        raise ValueError("cu must have one more entry than there are sequences")
     made = []
-    out = _output("out", out, (T, hq, d), q.dtype, dev, made)
-    lse = _output("lse", lse, (T, hq), torch.float32, dev, made)
-    _check(lib.ns_attend_prompt(q.data_ptr(), k.data_ptr(), v.data_ptr(), _DTYPES[q.dtype], T, hq, hkv, d,
-                                q.stride(0), q.stride(1), k.stride(0), k.stride(1), v.stride(0), v.stride(1), cu_ptr,
-                                cu.shape[0] - 1, max_len, d ** -0.5 if scale is None else scale, out.data_ptr(),
-                                lse.data_ptr(), _stream(stream, dev, *made)), "ns_attend_prompt")
+    if out is None:
+        out = _empty((T, hq, d), dtype=dtype, device=dev)
+        made.append(out)
+    else:
+        _given("out", out, (T, hq, d), dtype, dev)
+    if lse is None:
+        lse = _empty((T, hq), dtype=_F32, device=dev)
+        made.append(lse)
+    else:
+        _given("lse", lse, (T, hq), _F32, dev)
+    _check(lib.ns_attend_prompt(q.data_ptr(), k.data_ptr(), v.data_ptr(), _DTYPES[dtype], T, hq, hkv, d, qst[0],
+                                qst[1], kst[0], kst[1], vst[0], vst[1], cu_ptr, n - 1, max_len,
+                                d ** -0.5 if scale is None else scale, out.data_ptr(), lse.data_ptr(),
+                                _stream(stream, dev, *made)), "ns_attend_prompt")
     return out, lse
 
 
@@ -135,37 +168,44 @@ def attend_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, 
     launch.  Returns (out [B, n, Hq, D], lse fp32 [B, n, Hq])."""
     lib = load_library()
     dev = _device(q, "q")
-    _need(q.dtype in (torch.bfloat16, torch.float16), "q must be bf16 or fp16")
-    _need(q.dim() == 4 and k_pages.dim() == 4, "q must be [B, n, heads, dim], the cache [pages, heads, page_size, dim]")
-    B, n, hq, d = q.shape
-    pages, hkv, page, _ = k_pages.shape
-    _need(k_pages.shape[3] == d and k_pages.shape == v_pages.shape, "k_pages and v_pages must have q's dim")
-    _need(hkv > 0 and hq % hkv == 0, "q_heads must be a multiple of kv_heads")
-    _need(1 <= n <= MAX_NEW and B <= MAX_ATTEND_SEQS, f"at most {MAX_NEW} new tokens and {MAX_ATTEND_SEQS} sequences")
-    for what, t in (("q", q), ("k_pages", k_pages), ("v_pages", v_pages)):
-        _rows(what, t, dev, q.dtype)
-    t_ptr, l_ptr = _i32("table", table, dev, None, None), _i32("lengths", lengths, dev, table.shape[0])
-    s_ptr = _i32("seqs", seqs, dev, B)
+    dtype = q.dtype
+    if dtype is not torch.bfloat16 and dtype is not torch.float16:
+        raise ValueError("q must be bf16 or fp16")
+    if q.dim() != 4 or k_pages.dim() != 4:
+        raise ValueError("q must be [B, n, heads, dim], the cache [pages, heads, page_size, dim]")
+    B, n, hq, d = shape = q.shape
+    ks = k_pages.shape
+    pages, hkv, page, kd = ks
+    if kd != d or v_pages.shape != ks:
+        raise ValueError("k_pages and v_pages must have q's dim")
+    if hkv == 0 or hq % hkv:
+        raise ValueError("q_heads must be a multiple of kv_heads")
+    if not (1 <= n <= MAX_NEW and B <= MAX_ATTEND_SEQS):
+        raise ValueError(f"at most {MAX_NEW} new tokens and {MAX_ATTEND_SEQS} sequences")
+    qst = _rows("q", q, dev, dtype)
+    kst, vst = _rows("k_pages", k_pages, dev, dtype), _rows("v_pages", v_pages, dev, dtype)
+    t_ptr = _i32_2d("table", table, dev)
+    rows, ld = table.shape
+    l_ptr, s_ptr = _i32("lengths", lengths, dev, (rows,)), _i32("seqs", seqs, dev, (B,))
     if mask is not None:
-        _need(mask.dtype == torch.int64 and mask.is_contiguous() and tuple(mask.shape) == (B, n) and
-              mask.device == dev, f"mask must be a contiguous int64 tensor of shape {(B, n)} on {dev}")
+        _given("mask", mask, (B, n), torch.int64, dev)
     made = []
-    out = _output("out", out, (B, n, hq, d), q.dtype, dev, made)
-    lse = _output("lse", lse, (B, n, hq), torch.float32, dev, made)
-    need = lib.ns_attend_paged_workspace(B, n, hq, hkv, d)
-    if workspace is None:
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
-        made.append(workspace)
+    if out is None:
+        out = _empty(shape, dtype=dtype, device=dev)
+        made.append(out)
     else:
-        _on_device("workspace", workspace, dev)
-        _need(workspace.is_contiguous(), "workspace must be contiguous")
-    _check(lib.ns_attend_paged(q.data_ptr(), _DTYPES[q.dtype], B, n, hq, hkv, d, q.stride(0), q.stride(1),
-                               q.stride(2), k_pages.data_ptr(), v_pages.data_ptr(), pages, page, k_pages.stride(0),
-                               k_pages.stride(1), k_pages.stride(2), v_pages.stride(0), v_pages.stride(1),
-                               v_pages.stride(2), t_ptr, table.shape[1], table.shape[0], l_ptr, s_ptr,
+        _given("out", out, shape, dtype, dev)
+    if lse is None:
+        lse = _empty((B, n, hq), dtype=_F32, device=dev)
+        made.append(lse)
+    else:
+        _given("lse", lse, (B, n, hq), _F32, dev)
+    ws, ws_bytes = _workspace(workspace, lib.ns_attend_paged_workspace(B, n, hq, hkv, d), dev, made)
+    _check(lib.ns_attend_paged(q.data_ptr(), _DTYPES[dtype], B, n, hq, hkv, d, qst[0], qst[1], qst[2],
+                               k_pages.data_ptr(), v_pages.data_ptr(), pages, page, kst[0], kst[1], kst[2], vst[0],
+                               vst[1], vst[2], t_ptr, ld, rows, l_ptr, s_ptr,
                                None if mask is None else mask.data_ptr(), d ** -0.5 if scale is None else scale,
-                               max_len, out.data_ptr(), lse.data_ptr(), workspace.data_ptr(),
-                               workspace.numel() * workspace.element_size(), _stream(stream, dev, *made)),
+                               max_len, out.data_ptr(), lse.data_ptr(), ws, ws_bytes, _stream(stream, dev, *made)),
            "ns_attend_paged")
     return out, lse
 
@@ -180,25 +220,19 @@ class KvPages:
                  refs: torch.Tensor):
         self._lib = load_library()
         self.device = dev = _device(k, "k")
-        _need(k.dim() == 5 and k.shape == v.shape, "k and v must be [layers, pages, heads, page_size, dim]")
-        _need(k.dtype == v.dtype, "k and v must have one type")
-        _rows("k", k, dev, k.dtype)
-        _rows("v", v, dev, v.dtype)
+        shape, dtype = k.shape, k.dtype
+        if len(shape) != 5 or v.shape != shape:
+            raise ValueError("k and v must be [layers, pages, heads, page_size, dim]")
+        s, t = _rows("k", k, dev, dtype), _rows("v", v, dev, dtype)
         self.k, self.v, self.table, self.lengths, self.refs = k, v, table, lengths, refs
         e = k.element_size()
-        L, pages, heads, page, d = k.shape
-        s, t = k.stride(), v.stride()
-        c = ns_kv_pages()
-        c.k, c.v = k.data_ptr(), v.data_ptr()
-        c.k_layer, c.k_page, c.k_head, c.k_token = s[0] * e, s[1] * e, s[2] * e, s[3] * e
-        c.v_layer, c.v_page, c.v_head, c.v_token = t[0] * e, t[1] * e, t[2] * e, t[3] * e
-        c.layers, c.pages, c.heads, c.page_size, c.row_bytes = L, pages, heads, page, d * e
-        c.table = _i32("table", table, dev, None, None)
-        c.max_seqs, c.table_ld = table.shape
-        c.lengths = _i32("lengths", lengths, dev, c.max_seqs)
-        c.refs = _i32("refs", refs, dev, pages)
-        self._c = c
-        self._p = ctypes.byref(c)
+        L, pages, heads, page, d = shape
+        t_ptr = _i32_2d("table", table, dev)
+        rows, ld = table.shape
+        self._c = ns_kv_pages(k.data_ptr(), v.data_ptr(), s[0] * e, s[1] * e, s[2] * e, s[3] * e, t[0] * e, t[1] * e,
+                              t[2] * e, t[3] * e, L, pages, heads, page, d * e, rows, ld, t_ptr,
+                              _i32("lengths", lengths, dev, (rows,)), _i32("refs", refs, dev, (pages,)))
+        self._p = ctypes.byref(self._c)
 
     @classmethod
     def new(cls, layers: int, pages: int, kv_heads: int, page_size: int, dim: int, max_seqs: int, max_pages: int,
@@ -212,65 +246,58 @@ class KvPages:
 
     def truncate(self, seqs: torch.Tensor, new_len: Optional[torch.Tensor] = None, stream=None) -> None:
         """Shortens sequences to new_len [n] positions (None: frees them)."""
-        n = seqs.shape[0]
-        _check(self._lib.ns_pages_truncate(self._p, _i32("seqs", seqs, self.device, n),
-                                           None if new_len is None else _i32("new_len", new_len, self.device, n), n,
-                                           _stream(stream, self.device)), "ns_pages_truncate")
+        dev, n = self.device, (len(seqs),)
+        _check(self._lib.ns_pages_truncate(self._p, _i32("seqs", seqs, dev, n),
+                                           None if new_len is None else _i32("new_len", new_len, dev, n), n[0],
+                                           _stream(stream, dev)), "ns_pages_truncate")
 
     def fork(self, src: torch.Tensor, dst: torch.Tensor, stream=None) -> None:
         """The empty sequences dst [n] come to hold the pages of src [n]."""
-        n = src.shape[0]
-        _check(self._lib.ns_pages_fork(self._p, _i32("src", src, self.device, n), _i32("dst", dst, self.device, n), n,
-                                       _stream(stream, self.device)), "ns_pages_fork")
+        dev, n = self.device, (len(src),)
+        _check(self._lib.ns_pages_fork(self._p, _i32("src", src, dev, n), _i32("dst", dst, dev, n), n[0],
+                                       _stream(stream, dev)), "ns_pages_fork")
 
     def extend(self, seqs: torch.Tensor, n_new: torch.Tensor, workspace: Optional[torch.Tensor] = None,
                stream=None) -> None:
         """Lengthens sequences by n_new [n] positions; a partly filled last page that others hold too is copied."""
-        n = seqs.shape[0]
-        ps, pn = _i32("seqs", seqs, self.device, n), _i32("n_new", n_new, self.device, n)
+        dev, n = self.device, (len(seqs),)
+        ps, pn = _i32("seqs", seqs, dev, n), _i32("n_new", n_new, dev, n)
         made = []
-        if workspace is None:
-            need = self._lib.ns_pages_workspace(self._p, n)
-            workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=self.device)
-            made.append(workspace)
-        else:
-            _on_device("workspace", workspace, self.device)
-            _need(workspace.is_contiguous(), "workspace must be contiguous")
-        _check(self._lib.ns_pages_extend(self._p, ps, pn, n, workspace.data_ptr(),
-                                         workspace.numel() * workspace.element_size(),
-                                         _stream(stream, self.device, *made)), "ns_pages_extend")
+        ws, ws_bytes = _workspace(workspace, self._lib.ns_pages_workspace(self._p, n[0]), dev, made)
+        _check(self._lib.ns_pages_extend(self._p, ps, pn, n[0], ws, ws_bytes, _stream(stream, dev, *made)),
+               "ns_pages_extend")
 
     def write(self, layer: int, seqs: torch.Tensor, cu: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor,
               stream=None) -> None:
         """Writes k_new and v_new [tokens, heads, dim] as the last positions of the sequences in one layer; tokens
         cu[i] .. cu[i + 1] - 1 are sequence seqs[i]'s (cu int32 [n + 1])."""
-        n = seqs.shape[0]
-        T = k_new.shape[0]
-        want = (T, self.k.shape[2], self.k.shape[4])
-        for what, t in (("k_new", k_new), ("v_new", v_new)):
-            _rows(what, t, self.device, self.k.dtype)
-            _need(tuple(t.shape) == want, f"{what} must be [tokens, heads, dim] = {want}")
+        dev, n, c = self.device, len(seqs), self._c
+        kst, vst = _rows("k_new", k_new, dev, self.k.dtype), _rows("v_new", v_new, dev, self.k.dtype)
         e = k_new.element_size()
-        _check(self._lib.ns_pages_write(self._p, layer, _i32("seqs", seqs, self.device, n),
-                                        _i32("cu", cu, self.device, n + 1), n, k_new.data_ptr(), v_new.data_ptr(),
-                                        k_new.stride(0) * e, k_new.stride(1) * e, v_new.stride(0) * e,
-                                        v_new.stride(1) * e, T, _stream(stream, self.device)), "ns_pages_write")
+        T, heads, dim = k_new.shape if k_new.dim() == 3 else (0, 0, 0)
+        if heads != c.heads or dim * e != c.row_bytes or v_new.shape != k_new.shape:
+            raise ValueError(f"k_new and v_new must be [tokens, {c.heads}, {c.row_bytes // e}]")
+        _check(self._lib.ns_pages_write(self._p, layer, _i32("seqs", seqs, dev, (n,)), _i32("cu", cu, dev, (n + 1,)), n,
+                                        k_new.data_ptr(), v_new.data_ptr(), kst[0] * e, kst[1] * e, vst[0] * e,
+                                        vst[1] * e, T, _stream(stream, dev)), "ns_pages_write")
 
     def compact(self, seqs: torch.Tensor, base: torch.Tensor, keep: torch.Tensor, n_keep: torch.Tensor,
                 stream=None) -> None:
         """From position base [n] on, keeps the positions base + keep [n, m] (the first n_keep [n] of each row,
         strictly increasing) in every layer, and drops the rest."""
-        n = seqs.shape[0]
-        _check(self._lib.ns_pages_compact(self._p, _i32("seqs", seqs, self.device, n),
-                                          _i32("base", base, self.device, n), _i32("keep", keep, self.device, n, None),
-                                          keep.shape[1], _i32("n_keep", n_keep, self.device, n), n,
-                                          _stream(stream, self.device)), "ns_pages_compact")
+        dev, n = self.device, (len(seqs),)
+        k_ptr = _i32_2d("keep", keep, dev)
+        if keep.shape[0] != n[0]:
+            raise ValueError(f"keep has shape {tuple(keep.shape)}, expected ({n[0]}, any)")
+        _check(self._lib.ns_pages_compact(self._p, _i32("seqs", seqs, dev, n), _i32("base", base, dev, n), k_ptr,
+                                          keep.shape[1], _i32("n_keep", n_keep, dev, n), n[0], _stream(stream, dev)),
+               "ns_pages_compact")
 
     def copy(self, src: torch.Tensor, dst: torch.Tensor, stream=None) -> None:
         """Copies pages src [n] onto pages dst [n] in every layer."""
-        n = src.shape[0]
-        _check(self._lib.ns_pages_copy(self._p, _i32("src", src, self.device, n), _i32("dst", dst, self.device, n), n,
-                                       _stream(stream, self.device)), "ns_pages_copy")
+        dev, n = self.device, (len(src),)
+        _check(self._lib.ns_pages_copy(self._p, _i32("src", src, dev, n), _i32("dst", dst, dev, n), n[0],
+                                       _stream(stream, dev)), "ns_pages_copy")
 
     def attend(self, layer: int, q: torch.Tensor, seqs: torch.Tensor, **kw) -> Tuple[torch.Tensor, torch.Tensor]:
         """attend_paged over one layer of this cache."""
@@ -292,20 +319,26 @@ def token_logprobs(logits: torch.Tensor, ids: Optional[torch.Tensor] = None, k: 
     the k most probable tokens (ties to the smaller id)."""
     lib = load_library()
     dev = _device(logits, "logits")
-    _need(logits.dtype in _DTYPES and logits.dim() == 2, "logits must be [rows, V] of fp32, bf16 or fp16")
-    _rows("logits", logits, dev, logits.dtype)
-    _need(0 <= k <= MAX_ALTERNATIVES, f"k must be from 0 to {MAX_ALTERNATIVES}")
+    code = _DTYPES.get(logits.dtype)
+    if code is None or logits.dim() != 2:
+        raise ValueError("logits must be [rows, V] of fp32, bf16 or fp16")
+    st = _rows("logits", logits, dev, logits.dtype)
+    if not 0 <= k <= MAX_ALTERNATIVES:
+        raise ValueError(f"k must be from 0 to {MAX_ALTERNATIVES}")
     rows, V = logits.shape
-    m = 0 if ids is None else ids.shape[-1]
-    ids_ptr = None if ids is None else _i32("ids", ids, dev, rows, None)
-    ld = logits.stride(0) if rows > 1 else max(logits.stride(0), V)
-    f32 = {"dtype": torch.float32, "device": dev}
-    r = TokenLogprobs(torch.empty((rows, m), **f32), torch.empty(rows, **f32), torch.empty(rows, **f32),
-                      torch.empty((rows, k), dtype=torch.int32, device=dev), torch.empty((rows, k), **f32))
-    _check(lib.ns_token_logprobs(logits.data_ptr(), _DTYPES[logits.dtype], rows, V, ld, temperature, ids_ptr, m, k,
-                                 r.logprobs.data_ptr(), r.entropy.data_ptr(), r.lse.data_ptr(), r.top_ids.data_ptr(),
-                                 r.top_logprobs.data_ptr(), _stream(stream, dev, *r)), "ns_token_logprobs")
-    return r
+    m, ids_ptr = 0, None
+    if ids is not None:
+        ids_ptr = _i32_2d("ids", ids, dev)
+        if ids.shape[0] != rows:
+            raise ValueError(f"ids has shape {tuple(ids.shape)}, expected ({rows}, any)")
+        m = ids.shape[1]
+    lp, ent = _empty((rows, m), dtype=_F32, device=dev), _empty(rows, dtype=_F32, device=dev)
+    lse, tid = _empty(rows, dtype=_F32, device=dev), _empty((rows, k), dtype=_I32, device=dev)
+    tlp = _empty((rows, k), dtype=_F32, device=dev)
+    _check(lib.ns_token_logprobs(logits.data_ptr(), code, rows, V, st[0] if rows > 1 else max(st[0], V), temperature,
+                                 ids_ptr, m, k, lp.data_ptr(), ent.data_ptr(), lse.data_ptr(), tid.data_ptr(),
+                                 tlp.data_ptr(), _stream(stream, dev, lp, ent, lse, tid, tlp)), "ns_token_logprobs")
+    return TokenLogprobs(lp, ent, lse, tid, tlp)
 
 
 def ops_error(clear: bool = False) -> int:
