@@ -28,6 +28,7 @@ template <typename T>
 struct Type;
 template <>
 struct Type<__nv_bfloat16> {
+  static constexpr bool kBf16 = true;
   static constexpr float kOffset = 0.f;
   static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
     uint32_t r;
@@ -51,6 +52,7 @@ struct Type<__nv_bfloat16> {
 };
 template <>
 struct Type<__half> {
+  static constexpr bool kBf16 = false;
   static constexpr float kOffset = 8.f;
   static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
     uint32_t r;

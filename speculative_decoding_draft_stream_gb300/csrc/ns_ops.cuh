@@ -60,6 +60,11 @@ int64_t paged_attn_ws(int n_seqs, int n, int q_heads, int kv_heads, int dim, int
 cudaError_t prepare_paged_attn();
 cudaError_t launch_paged_attn(const PagedAttnArgs &a, int dtype, int dim, int sms, cudaStream_t st);
 
+// The same for more than 16 rows, on tcgen05 (ns_paged_umma.cu).
+bool paged_umma_ok(const PagedAttnArgs &a);
+cudaError_t prepare_paged_umma();
+cudaError_t launch_paged_umma(const PagedAttnArgs &a, int dtype, int dim, int sms, cudaStream_t st);
+
 // Attention over whole prompts (ns_prompt_attn.cu).
 struct PromptAttnArgs {
   const void *q, *k, *v;

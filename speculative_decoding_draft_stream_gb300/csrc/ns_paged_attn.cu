@@ -21,14 +21,12 @@
 //
 // What bounds it: HBM for one-token steps (each key is used by `group` rows,
 // a few flops a byte); the mma.sync rate for 64-row blocks.
-#include "ns_internal.cuh"
-#include "ns_ops.cuh"
-#include "ns_attn_tile.cuh"
+#include "ns_paged_attn.cuh"
 
 namespace ns {
 namespace {
 
-using namespace attn;
+using namespace paged;
 
 constexpr int kPaThreads = 128;
 constexpr int kPaKeys = 64;   // keys of a tile
@@ -46,42 +44,13 @@ __host__ __device__ constexpr int pa_smem() {
 
 __host__ __device__ inline long long pa_tiles(int len) { return len > 0 ? (len + kPaKeys - 1) / kPaKeys : 1; }
 
-// Workspace: cum int64 [n_seqs + 1], then (m, l) and o of two parts per CTA.
-struct PaWs {
-  long long *cum;
-  float2 *ml;  // [ctas x 2 x rows]
-  float *o;    // [ctas x 2 x rows x D]
-};
-__host__ __device__ inline PaWs pa_ws(void *p, int n_seqs, int ctas, int rows) {
-  PaWs w;
-  w.cum = static_cast<long long *>(p);
-  const size_t c = ((size_t)(n_seqs + 1) * 8 + 255) & ~(size_t)255;
-  w.ml = reinterpret_cast<float2 *>(static_cast<char *>(p) + c);
-  w.o = reinterpret_cast<float *>(w.ml + (size_t)ctas * 2 * rows);
-  return w;
-}
-
-__device__ __forceinline__ int pa_length(const PagedAttnArgs &a, int b, uint32_t *err) {
-  const int s = a.seqs[b];
-  if (s < 0 || s >= a.max_seqs) {
-    if (err) set_flag(err, NS_FLAG_BAD_SEQ);
-    return 0;
-  }
-  const int len = a.lengths[s];
-  if (len < 0 || (long long)len > ((long long)a.table_ld << a.page_shift)) {
-    if (err) set_flag(err, NS_FLAG_BAD_SEQ);
-    return 0;
-  }
-  return len;
-}
-
 // Where a CTA is in the line of tiles: item (sequence b, `item` = head *
 // blocks + block of rows) and its tile.
 struct Cursor {
   int b, item, tile, nt, len;
   const int32_t *table;
   __device__ __forceinline__ void enter(const PagedAttnArgs &a) {
-    len = pa_length(a, b, nullptr);
+    len = length(a, b, nullptr);
     nt = (int)pa_tiles(len);
     const int s = a.seqs[b];
     table = a.table + (size_t)(s >= 0 && s < a.max_seqs ? s : 0) * a.table_ld;
@@ -113,7 +82,7 @@ __global__ void __launch_bounds__(kPaThreads) paged_attn_kernel(const PagedAttnA
   long long total = 0;
   for (int b0 = 0; b0 < a.n_seqs; b0 += kPaThreads) {
     const int b = b0 + tid;
-    const long long mine = b < a.n_seqs ? pa_tiles(pa_length(a, b, blockIdx.x == 0 ? a.err : nullptr)) * items : 0;
+    const long long mine = b < a.n_seqs ? pa_tiles(length(a, b, blockIdx.x == 0 ? a.err : nullptr)) * items : 0;
     long long sum = mine;
 #pragma unroll
     for (int off = 1; off < kWarp; off <<= 1) {
@@ -130,7 +99,7 @@ __global__ void __launch_bounds__(kPaThreads) paged_attn_kernel(const PagedAttnA
     if (b < a.n_seqs) s_cum[b] = before + sum - mine;
     __syncthreads();
   }
-  const PaWs ws = pa_ws(a.ws, a.n_seqs, gridDim.x, kRows);
+  const Ws ws = workspace(a.ws, a.n_seqs, gridDim.x, kRows);
   if (blockIdx.x == 0) {
     for (int b = tid; b < a.n_seqs; b += kPaThreads) ws.cum[b] = s_cum[b];
     if (tid == 0) ws.cum[a.n_seqs] = total;
@@ -323,80 +292,23 @@ __global__ void __launch_bounds__(kPaThreads) paged_attn_kernel(const PagedAttnA
   }
 }
 
-// Joins the parts of an item that several CTAs had.  A CTA has some rows of an
-// item; kGroups warps have a row's parts in turns and join in group order.
-constexpr int kJoinWarps = 8;
+// The rows of an item for the join: row r of head h and block rb is new token
+// (16 WM rb + r) / group.
 template <int WM>
-struct Join {
+struct Rows16 {
+  int blocks;
+  static constexpr int kRows = 16 * WM;
   static constexpr int kGroups = WM == 1 ? 4 : 1;  // few rows may have hundreds of parts, many rows have two or three
-  static constexpr int kRows = kJoinWarps / kGroups;
+  template <typename T>
+  __device__ __forceinline__ float offset() const {
+    return Type<T>::kOffset;
+  }
+  __device__ __forceinline__ bool place(const PagedAttnArgs &a, int item, int rl, int &node, int &qh) const {
+    const int r = item % blocks * kRows + rl;
+    node = r / a.group, qh = item / blocks * a.group + r % a.group;
+    return r < a.n * a.group;
+  }
 };
-template <typename T, int D, int WM>
-__global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const PagedAttnArgs a, int blocks, int ctas) {
-  constexpr int kRows = 16 * WM, N = D / 32, G = Join<WM>::kGroups;
-  extern __shared__ int s_part[];  // [ctas] rows before each part
-  __shared__ float s_o[G][Join<WM>::kRows][D];
-  __shared__ float s_l[G][Join<WM>::kRows];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, grp = warp % G, rw = warp / G;
-  const int items = a.kv_heads * blocks, b = blockIdx.x / items, item = blockIdx.x % items;
-  const int head = item / blocks, rl = blockIdx.y * Join<WM>::kRows + rw, r = item % blocks * kRows + rl;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const PaWs ws = pa_ws(a.ws, a.n_seqs, ctas, kRows);
-  const long long total = ws.cum[a.n_seqs], cb = ws.cum[b];
-  const long long nt = (ws.cum[b + 1] - cb) / items;
-  const long long from = cb + item * nt, to = from + nt;  // the item's tiles
-  const int c0 = (int)(((from + 1) * ctas - 1) / total), c1 = (int)((to * ctas - 1) / total);
-  if (c0 == c1) return;  // one CTA had it all
-  for (int c = c0 + tid; c <= c1; c += kJoinWarps * 32) {
-    const long long first = total * c / ctas;
-    // a part is its CTA's first unless the CTA began before the item; a CTA may have no tiles at all
-    s_part[c - c0] = first == total * (c + 1) / ctas ? -1 : (c * 2 + (first >= from ? 0 : 1)) * kRows;
-  }
-  __syncthreads();
-  const bool live = r < a.n * a.group && rl < kRows;
-  const int parts = c1 - c0 + 1;
-  float m = kNegInf, l = 0.f, o[N];
-#pragma unroll
-  for (int i = 0; i < N; ++i) o[i] = 0.f;
-  if (live) {
-    for (int q = lane; q < parts; q += kWarp)
-      if (s_part[q] >= 0) m = fmaxf(m, ws.ml[s_part[q] + rl].x);
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-    const float safe = m == kNegInf ? 0.f : m;
-#pragma unroll 8
-    for (int q = grp; q < parts; q += G) {
-      if (s_part[q] < 0) continue;
-      const size_t at = (size_t)s_part[q] + rl;
-      const float2 ml = ws.ml[at];
-      const float f = ex2(ml.x - safe);
-      l += ml.y * f;
-      const float *src = ws.o + at * D + lane * N;
-#pragma unroll
-      for (int i = 0; i < N; ++i) o[i] = fmaf(src[i], f, o[i]);
-    }
-  }
-  if (G > 1) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) s_o[grp][rw][lane * N + i] = o[i];
-    if (lane == 0) s_l[grp][rw] = l;
-    __syncthreads();
-    if (grp != 0) return;
-#pragma unroll
-    for (int g = 1; g < G; ++g) {
-      l += s_l[g][rw];
-#pragma unroll
-      for (int i = 0; i < N; ++i) o[i] += s_o[g][rw][lane * N + i];
-    }
-  }
-  if (!live) return;
-  const int64_t at = ((int64_t)b * a.n + r / a.group) * a.q_heads + head * a.group + r % a.group;
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  uint32_t *dst = reinterpret_cast<uint32_t *>(static_cast<T *>(a.out) + at * D + lane * N);
-#pragma unroll
-  for (int i = 0; i < N / 2; ++i) dst[i] = Type<T>::pack(o[2 * i] * inv, o[2 * i + 1] * inv);
-  if (a.lse && lane == 0) a.lse[at] = row_lse<T>(m, l);
-}
 
 template <typename T, int D, int WM>
 cudaError_t launch(const PagedAttnArgs &a, int sms, cudaStream_t st) {
@@ -409,19 +321,8 @@ cudaError_t launch(const PagedAttnArgs &a, int sms, cudaStream_t st) {
   paged_attn_kernel<T, D, WM><<<ctas, kPaThreads, smem, st>>>(a, blocks);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg{};
   const int rows = a.n * a.group < kRows ? a.n * a.group : kRows;
-  cfg.gridDim = dim3((unsigned)((long long)a.n_seqs * a.kv_heads * blocks),
-                     (unsigned)((rows + Join<WM>::kRows - 1) / Join<WM>::kRows));
-  cfg.blockDim = dim3(kJoinWarps * 32);
-  cfg.dynamicSmemBytes = ctas * 4;
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, paged_join_kernel<T, D, WM>, a, blocks, ctas);
+  return launch_join<T, D>(a, Rows16<WM>{blocks}, rows, a.kv_heads * blocks, ctas, st);
 }
 
 template <typename T, int D, int WM>
@@ -430,18 +331,23 @@ cudaError_t prepare() {
                               pa_smem<D, WM>() + NS_MAX_ATTEND_SEQS * 8);
 }
 
+// Up to 16 rows the keys are what costs: each is fetched once and the warps
+// split them.  Above, the products are: they belong on the tensor cores of
+// ns_paged_umma.cu, which want queries that TMA can fetch (16-byte aligned,
+// strides multiples of 8); other queries take 64 rows a CTA here.
 template <typename T>
 cudaError_t by_rows(const PagedAttnArgs &a, int dim, int sms, cudaStream_t st) {
-  const bool few = a.n * a.group <= 16;
-  if (dim == 128) return few ? launch<T, 128, 1>(a, sms, st) : launch<T, 128, 4>(a, sms, st);
-  return few ? launch<T, 64, 1>(a, sms, st) : launch<T, 64, 4>(a, sms, st);
+  if (a.n * a.group <= 16) return dim == 128 ? launch<T, 128, 1>(a, sms, st) : launch<T, 64, 1>(a, sms, st);
+  if (paged_umma_ok(a)) return launch_paged_umma(a, Type<T>::kBf16 ? NS_DTYPE_BF16 : NS_DTYPE_F16, dim, sms, st);
+  return dim == 128 ? launch<T, 128, 4>(a, sms, st) : launch<T, 64, 4>(a, sms, st);
 }
 
 }  // namespace
 
 int64_t paged_attn_ws(int n_seqs, int n, int q_heads, int kv_heads, int dim, int sms) {
-  const int rows = n * (q_heads / kv_heads) <= 16 ? 16 : 64;
-  return (((int64_t)(n_seqs + 1) * 8 + 255) & ~(int64_t)255) + (int64_t)2 * sms * 2 * rows * (dim + 2) * 4;
+  // two parts for each CTA: 2 sms CTAs of 16 rows, or sms CTAs of 256 (2 sms of 64 are fewer)
+  const int64_t rows = n * (q_heads / kv_heads) <= 16 ? (int64_t)2 * sms * 2 * 16 : (int64_t)sms * 2 * 256;
+  return (((int64_t)(n_seqs + 1) * 8 + 255) & ~(int64_t)255) + rows * (dim + 2) * 4;
 }
 
 cudaError_t prepare_paged_attn() {
@@ -451,6 +357,7 @@ cudaError_t prepare_paged_attn() {
   also(prepare<__nv_bfloat16, 64, 1>()), also(prepare<__nv_bfloat16, 64, 4>());
   also(prepare<__half, 128, 1>()), also(prepare<__half, 128, 4>());
   also(prepare<__half, 64, 1>()), also(prepare<__half, 64, 4>());
+  also(prepare_paged_umma());
   return e;
 }
 

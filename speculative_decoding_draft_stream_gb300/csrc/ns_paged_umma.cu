@@ -1,0 +1,297 @@
+// Attention of many rows (a draft tree's nodes, or a long chain of new tokens)
+// over a paged cache, on the 5th-generation tensor cores (ns_umma_attn.cuh has
+// the kernel).
+//
+// An item is 2 * (128 / group) new tokens of one sequence, all query heads of
+// one key-value head, and the sequence's keys; the CTAs have equal shares of
+// all items' tiles (ns_paged_attn.cuh).  Keys and values come page by page:
+// each page's part of a tile is one TMA box for each 64 columns, its id
+// fetched a tile ahead.  A page id out of range is a box outside the tensor,
+// which reads as zeros.  Every row sees the context whole; in the tiles from
+// there on a row sees the new tokens of its mask, and what lies behind the
+// sequence's end is put to zero before it is used.
+#include "ns_paged_attn.cuh"
+#include "ns_umma_attn.cuh"
+
+namespace ns {
+namespace {
+
+using fa::kKeys;
+
+struct TreeArgs {
+  const int32_t *table, *lengths, *seqs;
+  const int64_t *mask;
+  int32_t n_seqs, n, q_heads, group, pack, per_tile, units, blocks;
+  int32_t page_shift, table_ld, max_seqs, n_pages;
+  float c;  // scale * log2(e)
+  void *out;
+  float *lse;
+  float2 *part_ml;
+  float *part_o;
+  long long *cum;  // [n_seqs + 1] tiles before each sequence, for the join
+  uint32_t *err;
+};
+
+struct Work {
+  int n0, n1, hidden;
+  int b, seq, len;   // the call's sequence, the cache's, its length
+  int unit, node0;   // query heads unit * pack .., first new token of row tile 0
+  int j0, slot;      // first key tile; the part's place (-1: the item is whole)
+  int ctx;           // positions that every row sees: len - n
+};
+
+// A sequence's tiles (one, all masked, when it is empty) and length.
+__device__ __forceinline__ int tiles(const TreeArgs &a, int b, int &len, uint32_t *err) {
+  const int s = a.seqs[b];
+  len = s >= 0 && s < a.max_seqs ? a.lengths[s] : -1;
+  if (len < 0 || (long long)len > ((long long)a.table_ld << a.page_shift)) {
+    if (err) set_flag(err, NS_FLAG_BAD_SEQ);
+    len = 0;
+  }
+  return len > 0 ? (len - 1) / kKeys + 1 : 1;
+}
+
+// A CTA's share of the line of tiles, item by item (a whole warp).
+struct Dealer {
+  long long at, first, end, before;  // next tile, the share's bounds, tiles before sequence b
+  int items, cta, b, nt, len;
+
+  __device__ __forceinline__ void begin(const TreeArgs &a, int cta_, int ctas) {
+    const int lane = threadIdx.x & 31;
+    cta = cta_, items = a.units * a.blocks;
+    long long total = 0;
+    for (int b0 = 0; b0 < a.n_seqs; b0 += 32) {
+      long long mine = b0 + lane < a.n_seqs ? (long long)tiles(a, b0 + lane, len, cta == 0 ? a.err : nullptr) * items : 0;
+      long long sum = mine;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const long long o = __shfl_up_sync(0xffffffffu, sum, off);
+        if (lane >= off) sum += o;
+      }
+      if (cta == 0 && b0 + lane < a.n_seqs) a.cum[b0 + lane] = total + sum - mine;
+      total += __shfl_sync(0xffffffffu, sum, 31);
+    }
+    if (cta == 0 && lane == 0) a.cum[a.n_seqs] = total;
+    first = at = total * cta / ctas, end = total * (cta + 1) / ctas;
+    b = 0, before = 0, nt = 0, len = 0;
+    long long passed = 0;  // the sequence with the share's first tile
+    for (int b0 = 0; b0 < a.n_seqs && at < end; b0 += 32) {
+      int n;
+      const int t = b0 + lane < a.n_seqs ? tiles(a, b0 + lane, n, nullptr) : 0;
+      long long sum = (long long)t * items;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const long long o = __shfl_up_sync(0xffffffffu, sum, off);
+        if (lane >= off) sum += o;
+      }
+      const uint32_t past = __ballot_sync(0xffffffffu, passed + sum > at);
+      if (past) {
+        const int l = __ffs(past) - 1;
+        b = b0 + l;
+        nt = __shfl_sync(0xffffffffu, t, l);
+        before = passed + __shfl_sync(0xffffffffu, sum, l) - (long long)nt * items;
+        break;
+      }
+      passed += __shfl_sync(0xffffffffu, sum, 31);
+    }
+    if (at < end) tiles(a, b, len, nullptr);
+  }
+  __device__ __forceinline__ Work next(const TreeArgs &a) {
+    Work w{};
+    if (at >= end) return w;
+    while (at >= before + (long long)nt * items) {
+      before += (long long)nt * items;
+      nt = tiles(a, ++b, len, nullptr);
+    }
+    const int item = (int)((at - before) / nt), tile = (int)((at - before) % nt);
+    const int count = (int)min((long long)(nt - tile), end - at);
+    const int ctx = len - a.n;
+    w.b = b, w.seq = a.seqs[b], w.len = len;
+    w.unit = item / a.blocks, w.node0 = item % a.blocks * 2 * a.per_tile;
+    w.j0 = tile, w.ctx = ctx;
+    w.n0 = count, w.n1 = w.node0 + a.per_tile < a.n ? count : 0;
+    w.hidden = max(0, (ctx > 0 ? ctx / kKeys : 0) - tile);
+    w.slot = tile == 0 && count == nt ? -1 : cta * 2 + (at == first ? 0 : 1);
+    at += count;
+    return w;
+  }
+};
+
+using TreeWork = Work;
+using TreeDealer = Dealer;
+
+struct Mode {
+  using Args = TreeArgs;
+  using Work = TreeWork;
+  using Dealer = TreeDealer;
+  static constexpr bool kParts = true;
+  static constexpr int kStageRow = 64;
+
+  struct Loader {
+    int ids, next;  // lane l: the id of the l-th page of this tile, and of the next
+    // pages of tile j that hold keys of the sequence
+    __device__ __forceinline__ int pages(const TreeArgs &a, const Work &w, int j) const {
+      const int rows = min(kKeys, w.len - (w.j0 + j) * kKeys), page = 1 << a.page_shift;
+      return rows <= 0 ? 0 : page >= kKeys ? 1 : (rows + page - 1) >> a.page_shift;
+    }
+    __device__ __forceinline__ int fetch(const TreeArgs &a, const Work &w, int j, int lane) const {
+      if (j >= w.n0 || lane >= pages(a, w, j)) return 0;
+      const int p = ((w.j0 + j) * kKeys >> a.page_shift) + lane;
+      const int id = a.table[(size_t)w.seq * a.table_ld + p];
+      if (id >= 0 && id < a.n_pages) return id;
+      set_flag(a.err, NS_FLAG_BAD_ID);
+      return a.n_pages;  // outside the tensor: zeros
+    }
+    __device__ __forceinline__ void begin(const TreeArgs &a, const Work &w, int lane) { next = fetch(a, w, 0, lane); }
+    __device__ __forceinline__ void queries(const TreeArgs &a, const Work &w, int t, int h, uint32_t dst,
+                                            const CUtensorMap *m, uint32_t bar) {
+      umma::tma4(dst, m, h * 64, w.unit * a.pack, w.node0 + t * a.per_tile, w.b, bar);
+    }
+    template <int D>
+    __device__ __forceinline__ void keys(const TreeArgs &a, const Work &w, int j, int kv, uint32_t dst,
+                                         const CUtensorMap *m, uint32_t bar, int lane) {
+      if (kv == 0) {
+        ids = next;
+        next = fetch(a, w, j + 1, lane);
+      }
+      const int n = pages(a, w, j), page = 1 << a.page_shift, rows = min(page, kKeys);
+      if (lane == 0) mbar_expect_tx(bar, n * rows * D * 2);
+      __syncwarp();
+      if (lane < n) {
+        const int row = page > kKeys ? (w.j0 + j) * kKeys & (page - 1) : 0;
+        for (int h = 0; h < D / 64; ++h)
+          umma::tma4(dst + h * fa::kHalf + lane * rows * 128, m, h * 64, row, w.unit * a.pack / a.group, ids, bar);
+      }
+      __syncwarp();
+    }
+  };
+
+  struct Row {
+    bool live, part;
+    int64_t at;     // its place in the output, or among the parts
+    int ctx;        // positions that every row sees
+    uint64_t word;  // new tokens that it sees
+    __device__ __forceinline__ void begin(const TreeArgs &a, const Work &w, int t, int r) {
+      const int in_tile = r / a.pack, node = w.node0 + t * a.per_tile + in_tile;
+      live = in_tile < a.per_tile && node < a.n;
+      part = w.slot >= 0;
+      at = part ? (int64_t)w.slot * 256 + t * 128 + r
+                : ((int64_t)w.b * a.n + node) * a.q_heads + w.unit * a.pack + r % a.pack;
+      ctx = w.len - a.n;
+      word = !live ? 0ull : (a.mask ? (uint64_t)a.mask[(int64_t)w.b * a.n + node] : ~0ull >> (63 - node)) &
+                                ~0ull >> (64 - a.n);
+    }
+    __device__ __forceinline__ uint64_t sees(const Work &w, int j, int from) const {
+      const int d = ctx - (w.j0 + j) * kKeys - from;  // keys of the 64 in the context
+      if (d >= 64) return ~0ull;
+      if (d > 0) return word << d | ((1ull << d) - 1);
+      return d > -64 ? word >> -d : 0ull;
+    }
+  };
+
+  struct Wild {  // new tokens whose value is not finite, per column
+    unsigned long long nan[128], pos[128], neg[128];
+    __device__ __forceinline__ void none(int d) { nan[d] = pos[d] = neg[d] = 0; }
+    // (a value of the context stays: every row sees it)
+    __device__ __forceinline__ bool note(const Work &w, int j, int r, int d, float x) {
+      const int node = (w.j0 + j) * kKeys + r - w.ctx;
+      if (node < 0) return false;
+      (x != x ? nan[d] : x > 0.f ? pos[d] : neg[d]) |= 1ull << node;
+      return true;
+    }
+    __device__ __forceinline__ int seen(const Row &row, int d) const {
+      const bool n = nan[d] & row.word, p = pos[d] & row.word, b = neg[d] & row.word;
+      return n || (p && b) ? 1 : p ? 2 : b ? 3 : 0;
+    }
+  };
+
+  // Rows of a value tile behind the sequence's end: what the ring held before, or what their page holds.
+  template <typename T, int D>
+  static __device__ __forceinline__ bool clear(const TreeArgs &, const Work &w, int j, uint8_t *tile, int lane) {
+    const int r0 = max(0, w.len - (w.j0 + j) * kKeys);
+    for (int h = 0; h < D / 64; ++h)
+      for (int x = r0 * 8 + lane; x < kKeys * 8; x += kWarp)
+        reinterpret_cast<uint4 *>(tile + h * fa::kHalf)[x] = make_uint4(0, 0, 0, 0);
+    __syncwarp();
+    return r0 < kKeys;
+  }
+};
+
+// The rows of an item for the join.
+struct Rows256 {
+  int blocks, pack, per_tile;
+  static constexpr int kRows = 256, kGroups = 1;
+  template <typename T>
+  __device__ __forceinline__ float offset() const {
+    return fa::kOffset<T>;
+  }
+  __device__ __forceinline__ bool place(const PagedAttnArgs &a, int item, int rl, int &node, int &qh) const {
+    const int in_tile = (rl & 127) / pack;
+    node = (item % blocks * 2 + (rl >> 7)) * per_tile + in_tile;
+    qh = item / blocks * pack + (rl & 127) % pack;
+    return in_tile < per_tile && node < a.n;
+  }
+};
+
+template <typename T, int D>
+cudaError_t launch(const PagedAttnArgs &p, int sms, cudaStream_t st) {
+  TreeArgs a{};
+  a.table = p.table, a.lengths = p.lengths, a.seqs = p.seqs, a.mask = p.mask;
+  a.n_seqs = p.n_seqs, a.n = p.n, a.q_heads = p.q_heads, a.group = p.group;
+  a.pack = p.group <= 32 ? p.group : 1;
+  a.per_tile = 128 / a.pack, a.units = p.q_heads / a.pack;
+  a.blocks = (p.n + 2 * a.per_tile - 1) / (2 * a.per_tile);
+  a.page_shift = p.page_shift, a.table_ld = p.table_ld, a.max_seqs = p.max_seqs, a.n_pages = p.n_pages;
+  a.c = p.scale * attn::kLog2e;
+  a.out = p.out, a.lse = p.lse, a.err = p.err;
+  const int items = a.units * a.blocks;
+  const long long most = (long long)(p.max_len > 0 ? (p.max_len - 1) / kKeys + 1 : 1) * p.n_seqs * items;
+  const int ctas = (int)(most < sms ? most : sms);
+  const paged::Ws ws = paged::workspace(p.ws, p.n_seqs, ctas, Rows256::kRows);
+  a.cum = ws.cum, a.part_ml = ws.ml, a.part_o = ws.o;
+  CUtensorMap tmQ, tmK, tmV;
+  const uint32_t page = 1u << p.page_shift;
+  const uint64_t dq[4] = {D, (uint64_t)p.q_heads, (uint64_t)p.n, (uint64_t)p.n_seqs};
+  const uint64_t dk[4] = {D, page, (uint64_t)p.kv_heads, (uint64_t)p.n_pages};
+  const uint64_t sq[3] = {(uint64_t)p.q_head * 2, (uint64_t)p.q_token * 2, (uint64_t)p.q_seq * 2};
+  const uint64_t sk[3] = {(uint64_t)p.k_token * 2, (uint64_t)p.k_head * 2, (uint64_t)p.k_page * 2};
+  const uint64_t sv[3] = {(uint64_t)p.v_token * 2, (uint64_t)p.v_head * 2, (uint64_t)p.v_page * 2};
+  const uint32_t bq[4] = {64, (uint32_t)a.pack, (uint32_t)a.per_tile, 1};
+  const uint32_t bk[4] = {64, page < kKeys ? page : kKeys, 1, 1};
+  if (!encode_16bit(&tmQ, p.q, 4, dq, sq, bq) || !encode_16bit(&tmK, p.k, 4, dk, sk, bk) ||
+      !encode_16bit(&tmV, p.v, 4, dk, sv, bk))
+    return cudaErrorInvalidValue;
+  fa::attn_kernel<T, D, Mode><<<ctas, fa::kThreads, fa::Smem<D, Mode>::kBytes, st>>>(tmQ, tmK, tmV, a);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  return paged::launch_join<T, D>(p, Rows256{a.blocks, a.pack, a.per_tile}, Rows256::kRows, items, ctas, st);
+}
+
+}  // namespace
+
+bool paged_umma_ok(const PagedAttnArgs &a) {
+  const int64_t s[9] = {a.q_seq, a.q_token, a.q_head, a.k_page, a.k_head, a.k_token, a.v_page, a.v_head, a.v_token};
+  for (int64_t x : s)
+    if (x <= 0 || x % 8 || x >= (int64_t)1 << 39) return false;
+  return reinterpret_cast<uintptr_t>(a.q) % 16 == 0;
+}
+
+cudaError_t prepare_paged_umma() {
+  cudaError_t e = cudaSuccess;
+  auto set = [&](const void *f, int bytes) {
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  };
+  set((const void *)fa::attn_kernel<__nv_bfloat16, 128, Mode>, fa::Smem<128, Mode>::kBytes);
+  set((const void *)fa::attn_kernel<__nv_bfloat16, 64, Mode>, fa::Smem<64, Mode>::kBytes);
+  set((const void *)fa::attn_kernel<__half, 128, Mode>, fa::Smem<128, Mode>::kBytes);
+  set((const void *)fa::attn_kernel<__half, 64, Mode>, fa::Smem<64, Mode>::kBytes);
+  return e;
+}
+
+cudaError_t launch_paged_umma(const PagedAttnArgs &a, int dtype, int dim, int sms, cudaStream_t st) {
+  if (dtype == NS_DTYPE_BF16)
+    return dim == 128 ? launch<__nv_bfloat16, 128>(a, sms, st) : launch<__nv_bfloat16, 64>(a, sms, st);
+  return dim == 128 ? launch<__half, 128>(a, sms, st) : launch<__half, 64>(a, sms, st);
+}
+
+}  // namespace ns

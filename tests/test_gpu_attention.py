@@ -359,6 +359,36 @@ def test_paged_cache_layouts(ns, layout):
     run_paged(ns, [100, 33, 333], 20, 8, 2, 64, 32, F16, 22, layout, masks="tree")
 
 
+@pytest.mark.parametrize("hq,hkv", [(3, 1), (7, 1), (20, 1), (33, 1), (64, 2), (4, 4)])
+@pytest.mark.parametrize("n", [6, 37, 64])
+def test_paged_many_rows(ns, hq, hkv, n):
+    """Heads that fill their row tiles unevenly, and pages of every kind of size against a tile."""
+    run_paged(ns, [n, n + 128, n + 300], n, hq, hkv, 64, 256, BF16, n + hq, masks="tree")
+    run_paged(ns, [n + 127, n + 1], n, hq, hkv, 128, 128, F16, n + hq)
+    run_paged(ns, [n + 255, 0, n - 1], n, hq, hkv, 128, 8, BF16, n + hq)
+
+
+def test_paged_queries_off_16_byte_boundaries(ns):
+    """Queries that begin off a 16-byte boundary, and with odd strides of pairs, give what aligned ones give."""
+    g, rng = gen(40), random.Random(40)
+    lens, n = [300, 64, 41], 40
+    dk, dv, table, _, _ = make_cache(g, rng, lens, 2, 16, 64, BF16)
+    q = normal(g, (3, n, 8, 64), BF16).cuda()
+    masks = signed(tree_masks(rng, 3, n)).cuda()
+    rest = (dk, dv, table.cuda(), torch.tensor(lens, dtype=torch.int32).cuda(),
+            torch.tensor([0, 1, 2], dtype=torch.int32).cuda())
+    want, wl = ns.attend_paged(q, *rest, mask=masks)
+    wide = torch.zeros((3, n, 8, 70), dtype=BF16, device="cuda")[..., 2:66]
+    wide.copy_(q)
+    out, lse = ns.attend_paged(wide, *rest, mask=masks)
+    # both are within their bounds of the exact result: twice the roundings of p and o apart at most
+    assert (out.float() - want.float()).abs().max() <= 4 * 2.0 ** -8 * want.float().abs().max()
+    assert (lse - wl).abs().max() < 1e-3
+    few, fl = ns.attend_paged(wide[:, :2], *rest)
+    want, wl = ns.attend_paged(q[:, :2], *rest)
+    assert torch.equal(few, want) and torch.equal(fl, wl) and ns.ops_error() == 0
+
+
 def test_paged_empty_sequences_and_rows(ns):
     """Lengths of zero, fewer positions than new tokens, and masks that leave nothing."""
     run_paged(ns, [0, 40, 0, 1], 1, 8, 2, 128, 16, BF16, 23)
