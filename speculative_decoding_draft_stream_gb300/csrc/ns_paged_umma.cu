@@ -16,6 +16,7 @@
 namespace ns {
 namespace {
 
+using attn::kNegInf;
 using fa::kKeys;
 
 struct TreeArgs {
@@ -85,7 +86,7 @@ struct Dealer {
         if (lane >= off) sum += o;
       }
       const uint32_t past = __ballot_sync(0xffffffffu, passed + sum > at);
-      if (past) {
+      if (past) {  // (the join finds a tile's CTA from the same bounds)
         const int l = __ffs(past) - 1;
         b = b0 + l;
         nt = __shfl_sync(0xffffffffu, t, l);
@@ -167,16 +168,14 @@ struct Mode {
   };
 
   struct Row {
-    bool live, part;
-    int64_t at;     // its place in the output, or among the parts
+    bool live;
+    int64_t at;     // its place in the output
     int ctx;        // positions that every row sees
     uint64_t word;  // new tokens that it sees
     __device__ __forceinline__ void begin(const TreeArgs &a, const Work &w, int t, int r) {
       const int in_tile = r / a.pack, node = w.node0 + t * a.per_tile + in_tile;
       live = in_tile < a.per_tile && node < a.n;
-      part = w.slot >= 0;
-      at = part ? (int64_t)w.slot * 256 + t * 128 + r
-                : ((int64_t)w.b * a.n + node) * a.q_heads + w.unit * a.pack + r % a.pack;
+      at = ((int64_t)w.b * a.n + node) * a.q_heads + w.unit * a.pack + r % a.pack;
       ctx = w.len - a.n;
       word = !live ? 0ull : (a.mask ? (uint64_t)a.mask[(int64_t)w.b * a.n + node] : ~0ull >> (63 - node)) &
                                 ~0ull >> (64 - a.n);
@@ -217,21 +216,69 @@ struct Mode {
   }
 };
 
-// The rows of an item for the join.
-struct Rows256 {
-  int blocks, pack, per_tile;
-  static constexpr int kRows = 256, kGroups = 1;
-  template <typename T>
-  __device__ __forceinline__ float offset() const {
-    return fa::kOffset<T>;
+// Joins the parts of an item that several CTAs had: a CTA has 32 of its rows,
+// a lane one of them, a warp a quarter of the columns.
+constexpr int kJoinThreads = 128;
+template <typename T, int D>
+__global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const TreeArgs a, int ctas) {
+  constexpr int N = D / 4, kPitch = D / 2 + 4;  // words of a row: its 16-byte pieces fall into different banks
+  extern __shared__ int s_part[];               // [ctas] places of the parts
+  __shared__ __align__(16) uint32_t s_out[32 * kPitch];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int items = a.units * a.blocks, b = blockIdx.x / items, item = blockIdx.x % items;
+  const int rl = blockIdx.y * 32 + lane, in_tile = (rl & 127) / a.pack;
+  const int node = (item % a.blocks * 2 + (rl >> 7)) * a.per_tile + in_tile;
+  const bool live = in_tile < a.per_tile && node < a.n;
+  const int64_t at = ((int64_t)b * a.n + node) * a.q_heads + item / a.blocks * a.pack + (rl & 127) % a.pack;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (!__any_sync(0xffffffffu, live)) return;  // (every warp has the same rows)
+  const long long total = a.cum[a.n_seqs], cb = a.cum[b];
+  const long long nt = (a.cum[b + 1] - cb) / items;
+  const long long from = cb + item * nt, to = from + nt;  // the item's tiles
+  const int c0 = (int)(((from + 1) * ctas - 1) / total), c1 = (int)((to * ctas - 1) / total);
+  if (c0 == c1) return;  // one CTA had it all
+  for (int c = c0 + tid; c <= c1; c += kJoinThreads) {
+    const long long first = total * c / ctas;
+    // a part is its CTA's first unless the CTA began before the item; a CTA may have no tiles at all
+    s_part[c - c0] = first == total * (c + 1) / ctas ? -1 : c * 2 + (first >= from ? 0 : 1);
   }
-  __device__ __forceinline__ bool place(const PagedAttnArgs &a, int item, int rl, int &node, int &qh) const {
-    const int in_tile = (rl & 127) / pack;
-    node = (item % blocks * 2 + (rl >> 7)) * per_tile + in_tile;
-    qh = item / blocks * pack + (rl & 127) % pack;
-    return in_tile < per_tile && node < a.n;
+  __syncthreads();
+  const int parts = c1 - c0 + 1;
+  float m = kNegInf, l = 0.f, o[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) o[i] = 0.f;
+#pragma unroll 4
+  for (int q = 0; q < parts; ++q)
+    if (s_part[q] >= 0) m = fmaxf(m, a.part_ml[s_part[q] * 256 + rl].x);
+  const float safe = m == kNegInf ? 0.f : m;
+  for (int q = 0; q < parts; ++q) {
+    if (s_part[q] < 0) continue;
+    const float2 ml = a.part_ml[s_part[q] * 256 + rl];
+    const float f = attn::ex2(ml.x - safe);
+    l += ml.y * f;
+    const float *src = a.part_o + ((int64_t)s_part[q] * D + warp * N) * 256 + rl;
+#pragma unroll
+    for (int i = 0; i < N; ++i) o[i] = fmaf(src[i * 256], f, o[i]);
   }
-};
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+  for (int i = 0; i < N; i += 8)
+    *reinterpret_cast<uint4 *>(s_out + lane * kPitch + (warp * N + i) / 2) =
+        make_uint4(attn::Type<T>::pack(o[i] * inv, o[i + 1] * inv), attn::Type<T>::pack(o[i + 2] * inv, o[i + 3] * inv),
+                   attn::Type<T>::pack(o[i + 4] * inv, o[i + 5] * inv),
+                   attn::Type<T>::pack(o[i + 6] * inv, o[i + 7] * inv));
+  if (live && warp == 0 && a.lse) a.lse[at] = l == 0.f ? kNegInf : (m - fa::kOffset<T> + log2f(l)) * attn::kLn2;
+  __syncthreads();
+  const long long mine = live ? at : -1;
+#pragma unroll
+  for (int e = 0; e < 32 * D / 8 / kJoinThreads; ++e) {
+    const int x = e * kJoinThreads + tid, r = x / (D / 8), c = x % (D / 8);
+    const long long row = __shfl_sync(0xffffffffu, mine, r);
+    if (row >= 0)
+      *reinterpret_cast<uint4 *>(static_cast<T *>(a.out) + row * D + c * 8) =
+          *reinterpret_cast<const uint4 *>(s_out + r * kPitch + c * 4);
+  }
+}
 
 template <typename T, int D>
 cudaError_t launch(const PagedAttnArgs &p, int sms, cudaStream_t st) {
@@ -247,7 +294,7 @@ cudaError_t launch(const PagedAttnArgs &p, int sms, cudaStream_t st) {
   const int items = a.units * a.blocks;
   const long long most = (long long)(p.max_len > 0 ? (p.max_len - 1) / kKeys + 1 : 1) * p.n_seqs * items;
   const int ctas = (int)(most < sms ? most : sms);
-  const paged::Ws ws = paged::workspace(p.ws, p.n_seqs, ctas, Rows256::kRows);
+  const paged::Ws ws = paged::workspace(p.ws, p.n_seqs, ctas, 256);
   a.cum = ws.cum, a.part_ml = ws.ml, a.part_o = ws.o;
   CUtensorMap tmQ, tmK, tmV;
   const uint32_t page = 1u << p.page_shift;
@@ -264,7 +311,17 @@ cudaError_t launch(const PagedAttnArgs &p, int sms, cudaStream_t st) {
   fa::attn_kernel<T, D, Mode><<<ctas, fa::kThreads, fa::Smem<D, Mode>::kBytes, st>>>(tmQ, tmK, tmV, a);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  return paged::launch_join<T, D>(p, Rows256{a.blocks, a.pack, a.per_tile}, Rows256::kRows, items, ctas, st);
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)((long long)p.n_seqs * items), 8);
+  cfg.blockDim = dim3(kJoinThreads);
+  cfg.dynamicSmemBytes = ctas * 4;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, tree_join_kernel<T, D>, a, ctas);
 }
 
 }  // namespace

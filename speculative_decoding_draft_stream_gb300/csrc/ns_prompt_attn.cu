@@ -29,6 +29,7 @@ struct Work {
   int seq0, len;     // the sequence's first token and its length
   int tok0;          // first token of row tile 0
   int unit;          // query heads unit * pack .. + pack - 1
+  int slot;          // unused: items are whole
 };
 
 // A sequence's first token and its length (0 where its bounds are invalid).
@@ -131,14 +132,12 @@ struct Mode {
   struct Row {
     int tok;       // position in the sequence
     bool live;
-    bool part;
     int64_t at;    // its place in the output
     int first;     // position of the first looked-through tile
     __device__ __forceinline__ void begin(const FaArgs &a, const Work &w, int t, int r) {
       const int in_tile = r / a.pack;
       tok = w.tok0 + t * a.per_tile + in_tile;
       live = in_tile < a.per_tile && tok < w.len;
-      part = false;
       at = (int64_t)(w.seq0 + tok) * a.q_heads + w.unit * a.pack + r % a.pack;
       first = w.hidden * kKeys;
     }

@@ -152,6 +152,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   umma::fence_after();
   const uint32_t tmem = *reinterpret_cast<uint32_t *>(g + L::kSlot);
+  if (M::kParts) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join waits for this grid
 
   // registers: 128 threads x 88 + 256 x 208 = 384 x 168, the launch's own
   if (warp < 4)
@@ -514,8 +515,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           umma::fence_before();
           mbar_arrive(base + L::kOEmpty + 8 * t);
         };
-        const bool part = M::kParts && row.part;
-        if (!part) {
+        if (!M::kParts || w.slot < 0) {
           const float inv = l == 0.f ? 0.f : 1.f / l;
           const long long to = live ? reinterpret_cast<long long>(static_cast<T *>(a.out) + row.at * D) : 0;
 #pragma unroll 1
@@ -539,25 +539,22 @@ __global__ void __launch_bounds__(kThreads, 1)
             flush(to, q * kRow);
           }
           if (live && a.lse) a.lse[row.at] = l == 0.f ? kNegInf : (m - kOffset<T> + log2f(l)) * attn::kLn2;
-        } else {  // a part: fp32 sums for the join
-          const long long to = live ? reinterpret_cast<long long>(a.part_o + row.at * D) : 0;
+        } else {  // a part: fp32 sums for the join, column by column (32 rows of a column are one line)
+          float *to = a.part_o + (int64_t)w.slot * D * 256 + t * 128 + r;
 #pragma unroll 1
-          for (int q = 0; q < D / 16; ++q) {
-            static_assert(!M::kParts || kWords == 16, "parts go 16 columns at a time");
-            uint32_t o[16];
-            umma::ld16(tO + q * 16, o);
+          for (int q = 0; q < D / 32; ++q) {
+            uint32_t o[32];
+            umma::ld32(tO + q * 32, o);
             umma::wait_ld();
-            if (q + 1 == D / 16) drained();
+            if (q + 1 == D / 32) drained();
             if (wild) {
 #pragma unroll
-              for (int e = 0; e < 16; ++e) o[e] = fixed(o[e], q * 16 + e);
+              for (int e = 0; e < 32; ++e) o[e] = fixed(o[e], q * 32 + e);
             }
 #pragma unroll
-            for (int e = 0; e < 16; e += 4)
-              *reinterpret_cast<uint4 *>(place(lane, e >> 2)) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
-            flush(to, q * 64);
+            for (int e = 0; e < 32; ++e) to[(q * 32 + e) * 256] = __uint_as_float(o[e]);
           }
-          if (live) a.part_ml[row.at] = make_float2(m, l);
+          a.part_ml[w.slot * 256 + t * 128 + r] = make_float2(m, l);
         }
       }
       __syncwarp();
