@@ -9,10 +9,13 @@
 // maximum grows by delta, S and U move with it: S' = S 2^-delta,
 // U' = 2^-delta (U - delta S).  Two such triples join the same way.
 //
-// The top k need no second read of the row.  A thread's maximum is m, so the
-// k-th largest of the CTA's thread maxima bounds the k-th largest value from
-// below, and only the k or so threads whose maximum reaches it can hold one
-// of the top k: their few values alone are read again (from L2) and ranked.
+// The top k need no second read of the row.  A thread's maximum is m; the k-th
+// largest of the maxima of 32 groups of threads bounds the k-th largest value
+// from below, and only threads whose maximum reaches it can hold one of the
+// top k: their few values alone are read again (from L2).  Those that reach
+// the bound go to a buffer in any order, and each one's place is the number
+// of better ones.  Where they do not fit (rows of many equal values), every
+// warp keeps a sorted list of its best instead, and the lists are merged.
 //
 // A row is one CTA, or a cluster of up to eight that split it and join their
 // triples and lists through distributed shared memory: one launch, no
@@ -30,11 +33,10 @@
 namespace ns {
 namespace {
 
-constexpr int kLpThreads = 256;
-constexpr int kLpWarps = kLpThreads / kWarp;
 constexpr int kLpVecs = 4;        // 16-byte loads a thread keeps in flight
 constexpr int kLpMaxCluster = 8;  // portable cluster size
 constexpr int kLpMinSlice = 4096; // least logits of a CTA of a split row
+constexpr int kLpBuffer = kLpMaxCluster * NS_MAX_ALTERNATIVES;  // candidates of a CTA, or the lists of a cluster
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kNegInf = -__builtin_huge_valf();
@@ -102,18 +104,20 @@ struct Part {
     s *= f;
     m = to;
   }
-  __device__ __forceinline__ void join(Part o, float c) {
-    const float to = fmaxf(m, o.m);
-    raise(to, c);
-    o.raise(to, c);
-    s += o.s;
-    u += o.u;
-  }
   template <int N>
   __device__ __forceinline__ void add(const float *x, float c) {
     float top = x[0];
+    if (N >= 8) {
+      float t[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-    for (int i = 1; i < N; ++i) top = fmaxf(top, x[i]);
+      for (int i = 4; i + 3 < N; i += 4)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) t[q] = fmaxf(t[q], x[i + q]);
+      top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
+    } else {
+#pragma unroll
+      for (int i = 1; i < N; ++i) top = fmaxf(top, x[i]);
+    }
     if (top > m) raise(top, c);
     const float at = m == kNegInf ? 0.f : -m;  // nothing but -inf so far: exponents of -inf, not NaN
     if (N == 1) {
@@ -148,13 +152,13 @@ __device__ __forceinline__ uint32_t peer_addr(const void *p, uint32_t rank) {
                : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(rank));
   return r;
 }
-__device__ __forceinline__ uint32_t ld_peer(uint32_t a) {
-  uint32_t v;
-  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
-  return v;
+__device__ __forceinline__ void st_peer(uint32_t a, unsigned long long v) {
+  asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(a), "l"(v) : "memory");
 }
-__device__ __forceinline__ void sync_cluster() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+__device__ __forceinline__ void st_peer(uint32_t a, const Part &p) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(a), "f"(p.m) : "memory");
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(a + 4), "f"(p.s) : "memory");
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(a + 8), "f"(p.u) : "memory");
 }
 
 // A warp's sorted list of its k best (key, id): lane r holds the r-th.
@@ -171,24 +175,65 @@ struct WarpList {
   }
 };
 
+// A candidate as one number: the larger is the better (key, then lower id);
+// 0 is none.
+__device__ __forceinline__ unsigned long long candidate(uint32_t key, uint32_t id) {
+  return (unsigned long long)key << 32 | (0xffffffffu - id);
+}
+
+// The k best of n <= kLpBuffer candidates, best first, each at the place that
+// the number of better ones says (a CTA; s has room for n + 1; places left
+// over get 0).
+template <int kLpThreads>
+__device__ __forceinline__ void place_best(const unsigned long long *s, int n, int k, unsigned long long *out) {
+  static_assert(kLpThreads >= kLpBuffer, "a thread places one candidate");
+  const int tid = threadIdx.x;
+  if (tid < n || tid < k) {
+    const unsigned long long mine = tid < n ? s[tid] : 0;
+    int better = 0, filled = 0;
+    const ulonglong2 *s2 = reinterpret_cast<const ulonglong2 *>(s);
+#pragma unroll 4
+    for (int q = 0; q < (n + 1) / 2; ++q) {
+      const ulonglong2 o = s2[q];
+      better += o.x > mine;
+      filled += o.x != 0;
+      if (2 * q + 1 < n) {
+        better += o.y > mine;
+        filled += o.y != 0;
+      }
+    }
+    if (mine && better < k) out[better] = mine;
+    if (tid < k && tid >= filled) out[tid] = 0;
+  }
+}
+
 // One row by the `split` CTAs of a cluster (split = 1: no cluster).  The
 // row's 16-byte pieces are counted from the aligned address at or before its
 // first logit; the pieces at its ends may be partly outside and are read
 // value by value.
-template <typename T, bool kSplit>
-__global__ void __launch_bounds__(kLpThreads) logprob_kernel(const LogprobArgs a, int split) {
+template <typename T, bool kSplit, int kLpThreads>
+__global__ void __launch_bounds__(kLpThreads, 1024 / kLpThreads + 1024 / kLpThreads / 4)
+    logprob_kernel(const LogprobArgs a, int split) {
+  constexpr int kLpWarps = kLpThreads / kWarp;
   using V = Vec<T>;
   constexpr int N = V::N;
-  __shared__ Part s_part[kLpWarps];
-  __shared__ Part s_all;
-  __shared__ __align__(16) uint32_t s_keys[kLpThreads];
-  __shared__ uint32_t s_mask[kLpWarps], s_min[kLpWarps];
+  constexpr int kGroups = 32, kGroup = kLpThreads / kGroups;  // threads of a group
+  __shared__ uint32_t s_group[kGroups];
+  __shared__ float s_top[kLpWarps];
+  __shared__ float2 s_sums[kLpWarps];
+  __shared__ uint32_t s_mask[kLpWarps];
+  __shared__ int s_count;
+  __shared__ __align__(16) unsigned long long s_cand[kLpBuffer + 2], s_best[NS_MAX_ALTERNATIVES];
   __shared__ uint32_t s_lk[kLpWarps * NS_MAX_ALTERNATIVES], s_li[kLpWarps * NS_MAX_ALTERNATIVES];
-  __shared__ uint32_t s_rk[NS_MAX_ALTERNATIVES], s_ri[NS_MAX_ALTERNATIVES];
+  __shared__ uint32_t s_ok[NS_MAX_ALTERNATIVES], s_oi[NS_MAX_ALTERNATIVES];
+  // rank 0's: every CTA's triple and list
+  __shared__ Part s_peer[kLpMaxCluster];
+  __shared__ __align__(16) unsigned long long s_lists[kSplit ? kLpBuffer + 2 : 1];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rank = kSplit ? (int)(blockIdx.x % split) : 0;
   const int r = kSplit ? (int)(blockIdx.x / split) : (int)blockIdx.x;
   const float c = kLog2e * a.inv_temperature;
+  if (kSplit) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");  // this CTA has begun
   const T *row = static_cast<const T *>(a.logits) + (int64_t)r * a.ld;
   const int mis = (int)((reinterpret_cast<uintptr_t>(row) & 15u) / sizeof(T));
   const uint4 *vec = reinterpret_cast<const uint4 *>(row - mis);
@@ -197,6 +242,14 @@ __global__ void __launch_bounds__(kLpThreads) logprob_kernel(const LogprobArgs a
   const int v0 = rank * per, v1 = min(pieces, v0 + per);
   const int first_whole = mis ? 1 : 0, last_whole = (a.V + mis) / N;
   const int w0 = max(v0, first_whole), w1 = min(v1, last_whole);  // whole pieces of this CTA
+
+  // the given tokens' logits, on their way while the row is read
+  int my_id = -1;
+  float my_x = 0.f;
+  if (rank == 0 && tid < a.n_ids) {
+    my_id = a.ids[(int64_t)r * a.n_ids + tid];
+    if (my_id >= 0 && my_id < a.V) my_x = V::one(row[my_id]);
+  }
 
   Part p{kNegInf, 0.f, 0.f};
   {
@@ -232,47 +285,84 @@ __global__ void __launch_bounds__(kLpThreads) logprob_kernel(const LogprobArgs a
   }
 
   const uint32_t my_key = order_key(p.m);
-  if (a.k > 0) s_keys[tid] = my_key;
+  {
+    uint32_t most = my_key;
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) {
-    Part o;
-    o.m = __shfl_xor_sync(0xffffffffu, p.m, off);
-    o.s = __shfl_xor_sync(0xffffffffu, p.s, off);
-    o.u = __shfl_xor_sync(0xffffffffu, p.u, off);
-    p.join(o, c);
+    for (int off = kGroup / 2; off > 0; off >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, off));
+    if (a.k > 0 && lane % kGroup == 0) s_group[tid / kGroup] = most;
+    most = __reduce_max_sync(0xffffffffu, most);
+    if (lane == 0) s_top[warp] = most ? key_value(most) : kNegInf;
+    if (tid == 0) s_count = 0;
   }
-  if (lane == 0) s_part[warp] = p;
   __syncthreads();
-  if (warp == 0) {
-    p = s_part[lane % kLpWarps];
+  {  // the CTA's maximum, and every thread's sums in terms of it
+    float top = s_top[0];
 #pragma unroll
-    for (int off = kLpWarps / 2; off > 0; off >>= 1) {
-      Part o;
-      o.m = __shfl_xor_sync(0xffffffffu, p.m, off);
-      o.s = __shfl_xor_sync(0xffffffffu, p.s, off);
-      o.u = __shfl_xor_sync(0xffffffffu, p.u, off);
-      p.join(o, c);
+    for (int q = 1; q < kLpWarps; ++q) top = fmaxf(top, s_top[q]);
+    p.raise(top, c);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) {
+      p.s += __shfl_xor_sync(0xffffffffu, p.s, off);
+      p.u += __shfl_xor_sync(0xffffffffu, p.u, off);
     }
-    if (lane == 0) s_all = p;
+    if (lane == 0) s_sums[warp] = make_float2(p.s, p.u);
   }
-
   if (a.k > 0) {
-    // threads that may hold one of the CTA's k best: fewer than k maxima are larger
+    // threads that may hold one of the CTA's k best: those whose maximum reaches the k-th largest group's
+    const uint32_t mine = s_group[lane];
     int larger = 0;
-    const uint4 *k4 = reinterpret_cast<const uint4 *>(s_keys);
-#pragma unroll 8
-    for (int q = 0; q < kLpThreads / 4; ++q) {
-      const uint4 u = k4[q];
-      larger += (u.x > my_key) + (u.y > my_key) + (u.z > my_key) + (u.w > my_key);
-    }
-    const bool mine = larger < a.k;
-    const uint32_t ball = __ballot_sync(0xffffffffu, mine);
-    const uint32_t low = __reduce_min_sync(0xffffffffu, mine ? my_key : 0xffffffffu);
-    if (lane == 0) s_mask[warp] = ball, s_min[warp] = low;
-    __syncthreads();
-    uint32_t least = s_min[0];
 #pragma unroll
-    for (int q = 1; q < kLpWarps; ++q) least = min(least, s_min[q]);
+    for (int q = 0; q < kGroups; ++q) larger += s_group[q] > mine;
+    const uint32_t least = __reduce_min_sync(0xffffffffu, larger < a.k ? mine : 0xffffffffu);
+    const uint32_t ball = __ballot_sync(0xffffffffu, my_key >= least && my_key != 0u);
+    if (lane == 0) s_mask[warp] = ball;
+    __syncthreads();
+    // every lane's value x of logit i (ok: there is one), for each piece that an owner of the mask has read;
+    // half a warp takes an owner, 16 of its pieces at a time
+    auto rescan = [&](auto offer) {
+      const int half = lane >> 4, hl = lane & 15;
+      int nth = 0;
+      for (int w = 0; w < kLpWarps; ++w) {
+        uint32_t left = s_mask[w];
+        while (left) {
+          // the next two owners' turn is this warp's, or both are passed over
+          const int o0 = __ffs(left) - 1;
+          left &= left - 1;
+          const int o1 = left ? __ffs(left) - 1 : -1;
+          left &= left - 1;
+          if (nth++ % kLpWarps != warp) continue;
+          const int owner = w * kWarp + (half ? o1 : o0);
+          const bool live = !half || o1 >= 0;
+          for (int v = w0 + w * kWarp + o0; v < w1; v += 16 * kLpThreads) {  // (o0 < o1: o0 has at least as many)
+            const int piece = v - (w * kWarp + o0) + owner + hl * kLpThreads;
+            const bool ok = live && piece < w1;
+            float x[N];
+            V::unpack(ok ? __ldg(vec + piece) : make_uint4(0, 0, 0, 0), x);
+#pragma unroll
+            for (int e = 0; e < N; ++e) offer(x[e], piece * N + e - mis, ok);
+          }
+          const bool head = w == 0 && mis && v0 == 0;  // the row's end pieces: threads 0 and 1 of their CTAs
+          const bool tail = w == 0 && v1 == pieces && v0 < pieces && last_whole < pieces && !(mis && pieces == 1);
+          if ((head && o0 == 0) || (tail && (o0 == 1 || o1 == 1))) {
+            const bool mine = live && ((owner == 0 && head) || (owner == 1 && tail));
+            const int i = (owner == 0 ? 0 : pieces - 1) * N + hl - mis;
+            const bool ok = mine && hl < N && i >= 0 && i < a.V;
+            offer(ok ? V::one(row[i]) : 0.f, i, ok);
+          }
+        }
+      }
+    };
+    rescan([&](float x, int i, bool ok) {
+      const uint32_t key = ok ? order_key(x) : 0u;
+      if (key != 0u && key >= least) {
+        const int at = atomicAdd(&s_count, 1);
+        if (at < kLpBuffer) s_cand[at] = candidate(key, (uint32_t)i);
+      }
+    });
+    __syncthreads();
+    if (s_count <= kLpBuffer) {
+      place_best<kLpThreads>(s_cand, s_count, a.k, s_best);
+    } else {
     WarpList L;
     L.clear();
     // inserts every lane's value (x of logit i; ok: there is one) that may be among the k best
@@ -285,67 +375,44 @@ __global__ void __launch_bounds__(kLpThreads) logprob_kernel(const LogprobArgs a
         L.insert(__shfl_sync(0xffffffffu, key, from), (uint32_t)__shfl_sync(0xffffffffu, i, from), lane);
       }
     };
-    int nth = 0;
-    for (int w = 0; w < kLpWarps; ++w) {
-      for (uint32_t left = s_mask[w]; left; left &= left - 1, ++nth) {
-        if (nth % kLpWarps != warp) continue;
-        const int owner = w * kWarp + __ffs(left) - 1;
-        for (int v = w0 + owner; v < w1; v += kWarp * kLpThreads) {  // 32 of the owner's pieces at a time
-          const int piece = v + lane * kLpThreads;
-          const bool ok = piece < w1;
-          float x[N];
-          V::unpack(ok ? __ldg(vec + piece) : make_uint4(0, 0, 0, 0), x);
-#pragma unroll
-          for (int e = 0; e < N; ++e) offer(x[e], piece * N + e - mis, ok);
-        }
-        const int ep = owner == 0 ? 0 : pieces - 1;
-        const bool end = (owner == 0 && mis && v0 == 0) ||
-                         (owner == 1 && v1 == pieces && v0 < pieces && last_whole < pieces && !(mis && pieces == 1));
-        if (end) {
-          const int i = ep * N + lane - mis;
-          const bool ok = lane < N && i >= 0 && i < a.V;
-          offer(ok ? V::one(row[i]) : 0.f, i, ok);
-        }
+    rescan(offer);
+      if (lane < a.k) {
+        s_lk[warp * a.k + lane] = L.key;
+        s_li[warp * a.k + lane] = L.id;
       }
-    }
-    if (lane < a.k) {
-      s_lk[warp * a.k + lane] = L.key;
-      s_li[warp * a.k + lane] = L.id;
-    }
-    __syncthreads();
-    if (warp == 0) {
-      uint32_t lk, li;
-      warp_merge_lists(s_lk, s_li, kLpWarps, a.k, s_rk, s_ri, lk, li);
+      __syncthreads();
+      if (warp == 0) {
+        uint32_t lk, li;
+        warp_merge_lists(s_lk, s_li, kLpWarps, a.k, s_ok, s_oi, lk, li);
+        if (lane < a.k) s_best[lane] = s_ok[lane] ? candidate(s_ok[lane], s_oi[lane]) : 0;
+      }
     }
   }
   __syncthreads();
 
+  p.s = p.u = 0.f;
+#pragma unroll
+  for (int q = 0; q < kLpWarps; ++q) p.s += s_sums[q].x, p.u += s_sums[q].y;
+  const unsigned long long *best = s_best;
   if (kSplit) {
-    sync_cluster();  // every CTA's triple and list are in its shared memory
-    if (rank == 0 && warp == 0) {
-      Part q{kNegInf, 0.f, 0.f};
-      for (int o = 0; o < split; ++o) {  // in rank order
-        const uint32_t at = peer_addr(&s_all, o);
-        q.join(Part{__uint_as_float(ld_peer(at)), __uint_as_float(ld_peer(at + 4)), __uint_as_float(ld_peer(at + 8))},
-               c);
-      }
-      if (a.k > 0) {
-        for (int e = lane; e < split * a.k; e += kWarp) {
-          s_lk[e] = ld_peer(peer_addr(&s_rk[e % a.k], e / a.k));
-          s_li[e] = ld_peer(peer_addr(&s_ri[e % a.k], e / a.k));
-        }
-      }
-      __syncwarp();
-      uint32_t lk = 0u, li = 0u;
-      if (a.k > 0) warp_merge_lists(s_lk, s_li, split, a.k, s_keys, s_keys + NS_MAX_ALTERNATIVES, lk, li);
-      if (lane == 0) s_all = q;  // only rank 0 reads it from here on: q is what each of its lanes holds
-    }
-    sync_cluster();  // no CTA leaves while rank 0 reads it
+    // to rank 0's shared memory, once it has begun; the others leave, and rank 0 goes on when all have arrived
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    if (tid < a.k) st_peer(peer_addr(&s_lists[rank * a.k + tid], 0), s_best[tid]);
+    if (tid == 0) st_peer(peer_addr(&s_peer[rank], 0), p);
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     if (rank != 0) return;
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    float top = s_peer[0].m;
+    for (int o = 1; o < split; ++o) top = fmaxf(top, s_peer[o].m);
+    p = Part{top, 0.f, 0.f};
+    for (int o = 0; o < split; ++o) {  // in rank order
+      Part q = s_peer[o];
+      q.raise(top, c);
+      p.s += q.s, p.u += q.u;
+    }
+    if (a.k > 0) place_best<kLpThreads>(s_lists, split * a.k, a.k, s_best);
     __syncthreads();
   }
-  const uint32_t *rk = kSplit ? s_keys : s_rk, *ri = kSplit ? s_keys + NS_MAX_ALTERNATIVES : s_ri;
-  p = s_all;
   const float log_s = logf(p.s);
   const bool none = p.m == kNegInf && p.s == 0.f;  // nothing but -inf
   auto logprob = [&](float x) { 
@@ -357,25 +424,33 @@ __global__ void __launch_bounds__(kLpThreads) logprob_kernel(const LogprobArgs a
     if (a.entropy) a.entropy[r] = none ? 0.f : log_s - kLn2 * (p.u / p.s);
   }
   if (tid < a.k) {
-    const uint32_t key = rk[tid];
-    a.top_ids[(int64_t)r * a.k + tid] = key ? (int32_t)ri[tid] : -1;
+    const uint32_t key = (uint32_t)(best[tid] >> 32);
+    a.top_ids[(int64_t)r * a.k + tid] = key ? (int32_t)(0xffffffffu - (uint32_t)best[tid]) : -1;
     a.top_logprobs[(int64_t)r * a.k + tid] = key ? logprob(key_value(key)) : kNegInf;
   }
   for (int j = tid; j < a.n_ids; j += kLpThreads) {
-    const int id = a.ids[(int64_t)r * a.n_ids + j];
+    const int id = j == tid ? my_id : a.ids[(int64_t)r * a.n_ids + j];
     float out = __int_as_float(0x7fffffff);
     if (id >= 0 && id < a.V)
-      out = logprob(V::one(row[id]));
+      out = logprob(j == tid ? my_x : V::one(row[id]));
     else if (id != -1)
       set_flag(a.err, NS_FLAG_BAD_ID);
     a.logprobs[(int64_t)r * a.n_ids + j] = out;
   }
 }
 
+// A row is split while the call has fewer than two CTAs for each SM and every
+// CTA keeps kLpMinSlice logits: one row of 128256 fp32 logits takes XX us on 8
+// CTAs, YY on 2; 60 rows of 151936 ZZ us on 4 each, WW on 8.
+constexpr int kLpThreads = 256;
+
 template <typename T>
-cudaError_t launch(const LogprobArgs &a, int split, cudaStream_t st) {
+cudaError_t launch(const LogprobArgs &a, int sms, cudaStream_t st) {
+  int split = 1;
+  while (split < kLpMaxCluster && (long long)a.rows * split * 2 <= 2LL * sms && a.V / (2 * split) >= kLpMinSlice)
+    split *= 2;
   if (split == 1) {
-    logprob_kernel<T, false><<<a.rows, kLpThreads, 0, st>>>(a, 1);
+    logprob_kernel<T, false, kLpThreads><<<a.rows, kLpThreads, 0, st>>>(a, 1);
     return cudaGetLastError();
   }
   cudaLaunchConfig_t cfg{};
@@ -388,18 +463,15 @@ cudaError_t launch(const LogprobArgs &a, int split, cudaStream_t st) {
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, logprob_kernel<T, true>, a, split);
+  return cudaLaunchKernelEx(&cfg, logprob_kernel<T, true, kLpThreads>, a, split);
 }
 
 }  // namespace
 
 cudaError_t launch_logprobs(const LogprobArgs &a, int dtype, int sms, cudaStream_t st) {
-  // a row is split until there are four CTAs for each SM, as long as each CTA keeps kLpMinSlice logits
-  int split = 1;
-  while (split < kLpMaxCluster && (long long)a.rows * split < 4LL * sms && a.V / (2 * split) >= kLpMinSlice) split *= 2;
-  if (dtype == NS_DTYPE_F32) return launch<float>(a, split, st);
-  if (dtype == NS_DTYPE_BF16) return launch<__nv_bfloat16>(a, split, st);
-  return launch<__half>(a, split, st);
+  if (dtype == NS_DTYPE_F32) return launch<float>(a, sms, st);
+  if (dtype == NS_DTYPE_BF16) return launch<__nv_bfloat16>(a, sms, st);
+  return launch<__half>(a, sms, st);
 }
 
 }  // namespace ns
