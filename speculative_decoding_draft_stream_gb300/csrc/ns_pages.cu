@@ -20,6 +20,26 @@ constexpr int kMoveThreads = 256;
 constexpr int kMoveWarps = kMoveThreads / kWarp;
 constexpr int kUnroll = 8;  // 16-byte loads a lane keeps in flight in the movers
 
+// Each kernel may be launched while the one before it ends; it waits for that
+// one's writes before it reads anything, and lets the next one be launched.
+__device__ __forceinline__ void wait_for_previous() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+template <typename... P, typename... A>
+cudaError_t launch(void (*kernel)(P...), dim3 grid, int threads, cudaStream_t st, A... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+}
+
 __host__ __device__ inline int pages_for(long long len, int page) { return (int)((len + page - 1) / page); }
 
 // Whether entry i of ids also stands before i (the later one is skipped).
@@ -57,6 +77,7 @@ __device__ __forceinline__ void drop_pages(const ns_kv_pages &c, int32_t *row, i
 __global__ void __launch_bounds__(kSeqThreads) truncate_kernel(ns_kv_pages c, const int32_t *seqs,
                                                                const int32_t *new_len, const int32_t *base,
                                                                int most, uint32_t *err) {
+  wait_for_previous();
   const int i = blockIdx.x;
   const int s = seqs[i];
   const bool again = repeated(seqs, i);
@@ -78,6 +99,7 @@ __global__ void __launch_bounds__(kSeqThreads) truncate_kernel(ns_kv_pages c, co
 
 __global__ void __launch_bounds__(kSeqThreads) fork_kernel(ns_kv_pages c, const int32_t *src, const int32_t *dst,
                                                            int n, uint32_t *err) {
+  wait_for_previous();
   const int i = blockIdx.x;
   const int a = src[i], b = dst[i];
   int clash = 0;  // the destination is another entry's destination (the first wins) or any entry's source
@@ -136,6 +158,12 @@ __global__ void __launch_bounds__(kExtendThreads) extend_kernel(ns_kv_pages c, c
   __shared__ int s_ids[NS_MAX_PAGE_SEQS];
   const ExtendWs w(ws, n);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  wait_for_previous();
+  // the first pages' counts, on their way while the needs are found
+  constexpr int kPer = 8;
+  int r[kPer];
+#pragma unroll
+  for (int q = 0; q < kPer; ++q) r[q] = tid * kPer + q < c.pages ? c.refs[tid * kPer + q] : 1;
   for (int i = tid; i < n; i += kExtendThreads) s_ids[i] = seqs[i];
   __syncthreads();
 
@@ -188,13 +216,13 @@ __global__ void __launch_bounds__(kExtendThreads) extend_kernel(ns_kv_pages c, c
   bool enough = total <= c.pages;
   int found = 0;
   if (enough && total > 0) {
-    constexpr int kPer = 8;
     for (int p0 = 0; p0 < c.pages && found < total; p0 += kExtendThreads * kPer) {
       const int p = p0 + tid * kPer;
       uint32_t free_bits = 0;
-      int r[kPer];
+      if (p0 > 0) {
 #pragma unroll
-      for (int q = 0; q < kPer; ++q) r[q] = p + q < c.pages ? c.refs[p + q] : 1;
+        for (int q = 0; q < kPer; ++q) r[q] = p + q < c.pages ? c.refs[p + q] : 1;
+      }
 #pragma unroll
       for (int q = 0; q < kPer; ++q) free_bits |= (r[q] == 0 ? 1u : 0u) << q;
       int sum;
@@ -246,6 +274,7 @@ __global__ void __launch_bounds__(kExtendThreads) extend_kernel(ns_kv_pages c, c
 __global__ void __launch_bounds__(kMoveThreads) copy_pages_kernel(ns_kv_pages c, const int32_t *src,
                                                                   const int32_t *dst, const int32_t *n_ptr, int n,
                                                                   uint32_t *err) {
+  wait_for_previous();
   const int lane = threadIdx.x & 31;
   const int pairs = n_ptr ? min(*n_ptr, n) : n;
   const long long items = (long long)pairs * c.layers * c.heads * 2;
@@ -284,20 +313,21 @@ __global__ void __launch_bounds__(kMoveThreads) copy_pages_kernel(ns_kv_pages c,
 // New rows of one layer: a warp per token, its 16-byte pieces of every head
 // of k and v over the lanes.
 __global__ void __launch_bounds__(kMoveThreads) write_kernel(ns_kv_pages c, int layer, const int32_t *seqs,
-                                                             const int32_t *cu, int n, const char *k_new,
-                                                             const char *v_new, int64_t k_token, int64_t k_head,
+                                                             const int32_t *cu, int n, const void *k_rows,
+                                                             const void *v_rows, int64_t k_token, int64_t k_head,
                                                              int64_t v_token, int64_t v_head, int tokens,
                                                              uint32_t *err) {
+  wait_for_previous();
   const int lane = threadIdx.x & 31;
   const int t = blockIdx.x * kMoveWarps + (threadIdx.x >> 5);
   if (t >= tokens) return;
-  int lo = 0, hi = n;  // the last i with cu[i] <= t
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (cu[mid] <= t)
-      lo = mid;
-    else
-      hi = mid;
+  int lo = 0;  // the last i with cu[i] <= t, a 32nd of what is left at a time
+  for (int size = n; size > 1;) {
+    const int step = (size + 31) / 32, at = lo + lane * step;
+    const uint32_t before = __ballot_sync(0xffffffffu, lane * step < size && cu[at] <= t);
+    const int last = before ? 31 - __clz(before) : 0;
+    lo += last * step;
+    size = min(step, size - last * step);
   }
   const int t0 = cu[lo], t1 = cu[lo + 1];
   if (t < t0 || t >= t1) return;  // a token of no sequence
@@ -324,7 +354,8 @@ __global__ void __launch_bounds__(kMoveThreads) write_kernel(ns_kv_pages c, int 
   const int cols = c.row_bytes / 16, units = c.heads * cols;
   char *kd = static_cast<char *>(c.k) + layer * c.k_layer + page * c.k_page + r * c.k_token;
   char *vd = static_cast<char *>(c.v) + layer * c.v_layer + page * c.v_page + r * c.v_token;
-  const char *ks = k_new + t * k_token, *vs = v_new + t * v_token;
+  const char *ks = static_cast<const char *>(k_rows) + t * k_token;
+  const char *vs = static_cast<const char *>(v_rows) + t * v_token;
   for (int x0 = lane; x0 < units; x0 += kWarp * 4) {
     uint4 a[4], b[4];
 #pragma unroll
@@ -364,6 +395,7 @@ __global__ void __launch_bounds__(kMoverWarps * 32, 4)
     compact_kernel(ns_kv_pages c, const int32_t *seqs, const int32_t *base, const int32_t *keep, int keep_ld,
                    const int32_t *n_keep, int segs, uint32_t *err) {
   __shared__ long long s_from[2][kMoveRows], s_to[2][kMoveRows];  // -1: stays
+  wait_for_previous();
   const int tid = threadIdx.x, lane = tid & 31, i = blockIdx.z, kv = blockIdx.y;
   const int s = seqs[i], m = n_keep[i], b0 = base[i];
   const bool again = repeated(seqs, i);  // only the first of a repeated sequence
@@ -441,34 +473,30 @@ unsigned grid_for(long long items, long long most) {
 
 cudaError_t launch_pages_truncate(const ns_kv_pages &c, const int32_t *seqs, const int32_t *new_len, int n,
                                   uint32_t *err, cudaStream_t st) {
-  truncate_kernel<<<n, kSeqThreads, 0, st>>>(c, seqs, new_len, nullptr, 0x7fffffff, err);
-  return cudaGetLastError();
+  return launch(truncate_kernel, dim3(n), kSeqThreads, st, c, seqs, new_len, nullptr, 0x7fffffff, err);
 }
 
 cudaError_t launch_pages_fork(const ns_kv_pages &c, const int32_t *src, const int32_t *dst, int n, uint32_t *err,
                               cudaStream_t st) {
-  fork_kernel<<<n, kSeqThreads, 0, st>>>(c, src, dst, n, err);
-  return cudaGetLastError();
+  return launch(fork_kernel, dim3(n), kSeqThreads, st, c, src, dst, n, err);
 }
 
 int64_t pages_extend_ws(const ns_kv_pages &c, int n) { return 4 * (4 + 6 * (int64_t)n + c.pages); }
 
 cudaError_t launch_pages_extend(const ns_kv_pages &c, const int32_t *seqs, const int32_t *n_new, int n, void *ws,
                                 uint32_t *err, cudaStream_t st) {
-  extend_kernel<<<1, kExtendThreads, 0, st>>>(c, seqs, n_new, n, ws, err);
+  cudaError_t e = launch(extend_kernel, dim3(1), kExtendThreads, st, c, seqs, n_new, n, ws, err);
+  if (e != cudaSuccess) return e;
   const ExtendWs w(ws, n);
   const unsigned grid = grid_for((long long)n * c.layers * c.heads * 2, 2432);
-  copy_pages_kernel<<<grid, kMoveThreads, 0, st>>>(c, w.src, w.dst, w.n_copies, n, err);
-  return cudaGetLastError();
+  return launch(copy_pages_kernel, dim3(grid), kMoveThreads, st, c, w.src, w.dst, w.n_copies, n, err);
 }
 
 cudaError_t launch_pages_write(const ns_kv_pages &c, int layer, const int32_t *seqs, const int32_t *cu, int n,
                                const void *k_new, const void *v_new, int64_t k_token, int64_t k_head,
                                int64_t v_token, int64_t v_head, int tokens, uint32_t *err, cudaStream_t st) {
-  write_kernel<<<(tokens + kMoveWarps - 1) / kMoveWarps, kMoveThreads, 0, st>>>(
-      c, layer, seqs, cu, n, static_cast<const char *>(k_new), static_cast<const char *>(v_new), k_token, k_head,
-      v_token, v_head, tokens, err);
-  return cudaGetLastError();
+  return launch(write_kernel, dim3((tokens + kMoveWarps - 1) / kMoveWarps), kMoveThreads, st, c, layer, seqs, cu, n,
+                k_new, v_new, k_token, k_head, v_token, v_head, tokens, err);
 }
 
 cudaError_t launch_pages_compact(const ns_kv_pages &c, const int32_t *seqs, const int32_t *base, const int32_t *keep,
@@ -476,18 +504,18 @@ cudaError_t launch_pages_compact(const ns_kv_pages &c, const int32_t *seqs, cons
   const int segs = (c.row_bytes + 511) / 512;
   const long long units = (long long)c.layers * c.heads * segs;
   if (units > 0x7fffffffLL - kMoverWarps) return cudaErrorInvalidValue;
-  if (keep_ld > 0)
-    compact_kernel<<<dim3((unsigned)((units + kMoverWarps - 1) / kMoverWarps), 2, (unsigned)n), kMoverWarps * 32, 0,
-                     st>>>(c, seqs, base, keep, keep_ld, n_keep, segs, err);
-  truncate_kernel<<<n, kSeqThreads, 0, st>>>(c, seqs, n_keep, base, keep_ld, err);
-  return cudaGetLastError();
+  if (keep_ld > 0) {
+    const dim3 grid((unsigned)((units + kMoverWarps - 1) / kMoverWarps), 2, (unsigned)n);
+    cudaError_t e = launch(compact_kernel, grid, kMoverWarps * 32, st, c, seqs, base, keep, keep_ld, n_keep, segs, err);
+    if (e != cudaSuccess) return e;
+  }
+  return launch(truncate_kernel, dim3(n), kSeqThreads, st, c, seqs, n_keep, base, keep_ld, err);
 }
 
 cudaError_t launch_pages_copy(const ns_kv_pages &c, const int32_t *src, const int32_t *dst, int n, uint32_t *err,
                               cudaStream_t st) {
-  copy_pages_kernel<<<grid_for((long long)n * c.layers * c.heads * 2, 2432), kMoveThreads, 0, st>>>(c, src, dst,
-                                                                                                   nullptr, n, err);
-  return cudaGetLastError();
+  const dim3 grid(grid_for((long long)n * c.layers * c.heads * 2, 2432));
+  return launch(copy_pages_kernel, grid, kMoveThreads, st, c, src, dst, nullptr, n, err);
 }
 
 }  // namespace ns
