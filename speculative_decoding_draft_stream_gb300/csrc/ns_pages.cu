@@ -378,7 +378,7 @@ __global__ void __launch_bounds__(kMoveThreads) write_kernel(ns_kv_pages c, int 
 }
 
 // Kept rows move down.  A CTA takes one sequence, k or v, and kMoverWarps of
-// its (layer, head, up to 512 bytes of the row), a warp each.  It walks the
+// its (layer, head, part of the row), a warp each.  It walks the
 // kept rows in order, kMoveRows at a time: the threads find each row's two
 // places, for the next rows while these move, and every warp moves its part
 // of them, kMoveBatch 16-byte pieces a lane: all loads of a batch, then its
@@ -393,7 +393,7 @@ constexpr int kMoveRows = 128;
 constexpr int kMoveBatch = 16;
 __global__ void __launch_bounds__(kMoverWarps * 32, 4)
     compact_kernel(ns_kv_pages c, const int32_t *seqs, const int32_t *base, const int32_t *keep, int keep_ld,
-                   const int32_t *n_keep, int segs, uint32_t *err) {
+                   const int32_t *n_keep, int seg_bytes, uint32_t *err) {
   __shared__ long long s_from[2][kMoveRows], s_to[2][kMoveRows];  // -1: stays
   wait_for_previous();
   const int tid = threadIdx.x, lane = tid & 31, i = blockIdx.z, kv = blockIdx.y;
@@ -431,12 +431,13 @@ __global__ void __launch_bounds__(kMoverWarps * 32, 4)
     s_to[slot][tid] = dst;
   };
   static_assert(kMoveRows == kMoverWarps * 32, "a thread finds one row's places");
+  const int segs = (c.row_bytes + seg_bytes - 1) / seg_bytes;
   const int u = blockIdx.x * kMoverWarps + (tid >> 5);
   const bool mine = u < c.layers * c.heads * segs;
   const int seg = u % segs, head = u / segs % c.heads, layer = u / segs / c.heads;
   char *data = static_cast<char *>(kv ? c.v : c.k) + (mine ? layer : 0) * (kv ? c.v_layer : c.k_layer) +
-               head * (kv ? c.v_head : c.k_head) + seg * 512;
-  const int cols = min(c.row_bytes - seg * 512, 512) / 16;  // lanes a row takes
+               head * (kv ? c.v_head : c.k_head) + seg * seg_bytes;
+  const int cols = min(c.row_bytes - seg * seg_bytes, seg_bytes) / 16;  // lanes a row takes
   const int per = kWarp / cols, sub = lane / cols;          // rows a warp moves at once
   data += lane % cols * 16;
   if (m > 0) find(0);
@@ -501,12 +502,20 @@ cudaError_t launch_pages_write(const ns_kv_pages &c, int layer, const int32_t *s
 
 cudaError_t launch_pages_compact(const ns_kv_pages &c, const int32_t *seqs, const int32_t *base, const int32_t *keep,
                                  int keep_ld, const int32_t *n_keep, int n, uint32_t *err, cudaStream_t st) {
-  const int segs = (c.row_bytes + 511) / 512;
-  const long long units = (long long)c.layers * c.heads * segs;
+  // A warp takes up to 512 bytes of a row, less where the CTAs are too few to keep HBM busy: 16001 rows of 12 x 4
+  // x 256 bytes of k and v move in 163 us by whole rows (192 CTAs), in about 118 us by halves.
+  constexpr int kEnough = 304;
+  int seg_bytes = 512;
+  auto ctas = [&](int seg) {
+    return ((long long)c.layers * c.heads * ((c.row_bytes + seg - 1) / seg) + kMoverWarps - 1) / kMoverWarps * 2 * n;
+  };
+  while (seg_bytes > 128 && ctas(seg_bytes) < kEnough) seg_bytes /= 2;
+  const long long units = (long long)c.layers * c.heads * ((c.row_bytes + seg_bytes - 1) / seg_bytes);
   if (units > 0x7fffffffLL - kMoverWarps) return cudaErrorInvalidValue;
   if (keep_ld > 0) {
     const dim3 grid((unsigned)((units + kMoverWarps - 1) / kMoverWarps), 2, (unsigned)n);
-    cudaError_t e = launch(compact_kernel, grid, kMoverWarps * 32, st, c, seqs, base, keep, keep_ld, n_keep, segs, err);
+    cudaError_t e = launch(compact_kernel, grid, kMoverWarps * 32, st, c, seqs, base, keep, keep_ld, n_keep,
+                           seg_bytes, err);
     if (e != cudaSuccess) return e;
   }
   return launch(truncate_kernel, dim3(n), kSeqThreads, st, c, seqs, n_keep, base, keep_ld, err);
