@@ -29,6 +29,7 @@ struct Type;
 template <>
 struct Type<__nv_bfloat16> {
   static constexpr bool kBf16 = true;
+  static constexpr uint32_t kInf = 0x7f80u;  // the pattern of infinity
   static constexpr float kOffset = 0.f;
   static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
     uint32_t r;
@@ -37,10 +38,6 @@ struct Type<__nv_bfloat16> {
   }
   static __device__ __forceinline__ float2 unpack(uint32_t w) {
     return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
-  }
-  // whether either half is infinite or NaN
-  static __device__ __forceinline__ bool wild(uint32_t w) {
-    return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
   }
   static __device__ __forceinline__ void mma(float *d, const uint32_t *a, uint32_t b0, uint32_t b1) {
     asm volatile(
@@ -53,6 +50,7 @@ struct Type<__nv_bfloat16> {
 template <>
 struct Type<__half> {
   static constexpr bool kBf16 = false;
+  static constexpr uint32_t kInf = 0x7c00u;
   static constexpr float kOffset = 8.f;
   static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
     uint32_t r;
@@ -61,9 +59,6 @@ struct Type<__half> {
   }
   static __device__ __forceinline__ float2 unpack(uint32_t w) {
     return __half22float2(*reinterpret_cast<const __half2 *>(&w));
-  }
-  static __device__ __forceinline__ bool wild(uint32_t w) {
-    return (w & 0x7c00u) == 0x7c00u || (w & 0x7c000000u) == 0x7c000000u;
   }
   static __device__ __forceinline__ void mma(float *d, const uint32_t *a, uint32_t b0, uint32_t b1) {
     asm volatile(
@@ -250,20 +245,23 @@ __device__ __forceinline__ float row_lse(float m, float l) {
 }
 
 // Whether any of the n 16-byte pieces at shared address a holds an infinity
-// or NaN (this thread's share of them).
+// or NaN (this thread's share of them): their exponents are all ones, so
+// without the sign no finite value has a larger pattern.
 template <typename T>
 __device__ __forceinline__ bool wild_pieces(uint32_t a, int n, int tid, int threads) {
-  bool w = false;
+  uint32_t most[2] = {0, 0};  // of 16-bit halves
+#pragma unroll 8
   for (int i = tid; i < n; i += threads) {
     uint32_t x[4];
     asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                  : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
                  : "r"(a + 16u * (uint32_t)i)
                  : "memory");
-#pragma unroll
-    for (int q = 0; q < 4; ++q) w = w || Type<T>::wild(x[q]);
+    most[0] = __vimax3_u16x2(most[0], x[0] & 0x7fff7fffu, x[1] & 0x7fff7fffu);
+    most[1] = __vimax3_u16x2(most[1], x[2] & 0x7fff7fffu, x[3] & 0x7fff7fffu);
   }
-  return w;
+  const uint32_t m = __vmaxu2(most[0], most[1]);
+  return (m & 0xffffu) >= Type<T>::kInf || (m >> 16) >= Type<T>::kInf;
 }
 
 }  // namespace attn

@@ -41,73 +41,86 @@ struct Work {
   int ctx;           // positions that every row sees: len - n
 };
 
-// A sequence's tiles (one, all masked, when it is empty) and length.
-__device__ __forceinline__ int tiles(const TreeArgs &a, int b, int &len, uint32_t *err) {
-  const int s = a.seqs[b];
-  len = s >= 0 && s < a.max_seqs ? a.lengths[s] : -1;
-  if (len < 0 || (long long)len > ((long long)a.table_ld << a.page_shift)) {
-    if (err) set_flag(err, NS_FLAG_BAD_SEQ);
-    len = 0;
-  }
-  return len > 0 ? (len - 1) / kKeys + 1 : 1;
+__device__ __forceinline__ long long quotient(long long a, int b) {
+  return a >> 32 ? a / b : (long long)((uint32_t)a / (uint32_t)b);
 }
 
-// A CTA's share of the line of tiles, item by item (a whole warp).
+// A CTA's share of the line of tiles, item by item (a whole warp).  Lane l
+// holds sequence 32 chunk + l of the call, so the line is walked without
+// loads while it stays among 32 sequences.
 struct Dealer {
   long long at, first, end, before;  // next tile, the share's bounds, tiles before sequence b
-  int items, cta, b, nt, len;
+  int items, cta, lane, b, nt;
+  int chunk, c_seq, c_len, c_nt;     // this lane's sequence: the cache's, its length and tiles
 
-  __device__ __forceinline__ void begin(const TreeArgs &a, int cta_, int ctas) {
-    const int lane = threadIdx.x & 31;
-    cta = cta_, items = a.units * a.blocks;
-    long long total = 0;
-    for (int b0 = 0; b0 < a.n_seqs; b0 += 32) {
-      long long mine = b0 + lane < a.n_seqs ? (long long)tiles(a, b0 + lane, len, cta == 0 ? a.err : nullptr) * items : 0;
-      long long sum = mine;
-#pragma unroll
-      for (int off = 1; off < 32; off <<= 1) {
-        const long long o = __shfl_up_sync(0xffffffffu, sum, off);
-        if (lane >= off) sum += o;
+  __device__ __forceinline__ void load(const TreeArgs &a, int k, bool flag) {
+    chunk = k;
+    const int i = k * 32 + lane;
+    c_nt = 0, c_len = 0, c_seq = 0;
+    if (i < a.n_seqs) {
+      c_seq = a.seqs[i];
+      c_len = c_seq >= 0 && c_seq < a.max_seqs ? a.lengths[c_seq] : -1;
+      if (c_len < 0 || (long long)c_len > ((long long)a.table_ld << a.page_shift)) {
+        if (flag) set_flag(a.err, NS_FLAG_BAD_SEQ);
+        c_len = 0;
       }
-      if (cta == 0 && b0 + lane < a.n_seqs) a.cum[b0 + lane] = total + sum - mine;
+      c_nt = c_len > 0 ? (c_len - 1) / kKeys + 1 : 1;  // an empty sequence: one tile, all masked
+    }
+  }
+  // tiles of the chunk's sequences up to and with this lane's
+  __device__ __forceinline__ long long upto() const {
+    long long sum = (long long)c_nt * items;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const long long o = __shfl_up_sync(0xffffffffu, sum, off);
+      if (lane >= off) sum += o;
+    }
+    return sum;
+  }
+  __device__ __forceinline__ void begin(const TreeArgs &a, int cta_, int ctas) {
+    lane = threadIdx.x & 31, cta = cta_, items = a.units * a.blocks;
+    const int chunks = (a.n_seqs + 31) / 32;
+    long long total = 0, sum = 0;
+    for (int k = 0; k < chunks; ++k) {
+      load(a, k, cta == 0);
+      sum = upto();
+      if (cta == 0 && k * 32 + lane < a.n_seqs) a.cum[k * 32 + lane] = total + sum - (long long)c_nt * items;
       total += __shfl_sync(0xffffffffu, sum, 31);
     }
     if (cta == 0 && lane == 0) a.cum[a.n_seqs] = total;
-    first = at = total * cta / ctas, end = total * (cta + 1) / ctas;
-    b = 0, before = 0, nt = 0, len = 0;
+    first = at = quotient(total * cta, ctas), end = quotient(total * (cta + 1), ctas);
+    b = 0, before = 0, nt = 0;
+    if (at >= end) return;
     long long passed = 0;  // the sequence with the share's first tile
-    for (int b0 = 0; b0 < a.n_seqs && at < end; b0 += 32) {
-      int n;
-      const int t = b0 + lane < a.n_seqs ? tiles(a, b0 + lane, n, nullptr) : 0;
-      long long sum = (long long)t * items;
-#pragma unroll
-      for (int off = 1; off < 32; off <<= 1) {
-        const long long o = __shfl_up_sync(0xffffffffu, sum, off);
-        if (lane >= off) sum += o;
+    for (int k = 0; k < chunks; ++k) {
+      if (chunks > 1) {
+        load(a, k, false);
+        sum = upto();
       }
       const uint32_t past = __ballot_sync(0xffffffffu, passed + sum > at);
-      if (past) {  // (the join finds a tile's CTA from the same bounds)
+      if (past) {
         const int l = __ffs(past) - 1;
-        b = b0 + l;
-        nt = __shfl_sync(0xffffffffu, t, l);
+        b = k * 32 + l;
+        nt = __shfl_sync(0xffffffffu, c_nt, l);
         before = passed + __shfl_sync(0xffffffffu, sum, l) - (long long)nt * items;
-        break;
+        return;
       }
       passed += __shfl_sync(0xffffffffu, sum, 31);
     }
-    if (at < end) tiles(a, b, len, nullptr);
   }
   __device__ __forceinline__ Work next(const TreeArgs &a) {
     Work w{};
     if (at >= end) return w;
     while (at >= before + (long long)nt * items) {
       before += (long long)nt * items;
-      nt = tiles(a, ++b, len, nullptr);
+      if (++b / 32 != chunk) load(a, b / 32, false);
+      nt = __shfl_sync(0xffffffffu, c_nt, b % 32);
     }
-    const int item = (int)((at - before) / nt), tile = (int)((at - before) % nt);
+    const int len = __shfl_sync(0xffffffffu, c_len, b % 32);
+    const int item = (int)quotient(at - before, nt), tile = (int)(at - before - (long long)item * nt);
     const int count = (int)min((long long)(nt - tile), end - at);
     const int ctx = len - a.n;
-    w.b = b, w.seq = a.seqs[b], w.len = len;
+    w.b = b, w.seq = __shfl_sync(0xffffffffu, c_seq, b % 32), w.len = len;
     w.unit = item / a.blocks, w.node0 = item % a.blocks * 2 * a.per_tile;
     w.j0 = tile, w.ctx = ctx;
     w.n0 = count, w.n1 = w.node0 + a.per_tile < a.n ? count : 0;
