@@ -104,7 +104,7 @@ __global__ void __launch_bounds__(kPaThreads) paged_attn_kernel(const PagedAttnA
     for (int b = tid; b < a.n_seqs; b += kPaThreads) ws.cum[b] = s_cum[b];
     if (tid == 0) ws.cum[a.n_seqs] = total;
   }
-  const long long t0 = total * blockIdx.x / gridDim.x, t1 = total * (blockIdx.x + 1) / gridDim.x;
+  const long long t0 = quotient(total * blockIdx.x, gridDim.x), t1 = quotient(total * (blockIdx.x + 1), gridDim.x);
   if (t0 >= t1) return;
 
   Cursor ld;
@@ -120,8 +120,8 @@ __global__ void __launch_bounds__(kPaThreads) paged_attn_kernel(const PagedAttnA
     ld.b = lo;
     ld.enter(a);
     const long long local = t0 - s_cum[lo];
-    ld.item = (int)(local / ld.nt);
-    ld.tile = (int)(local % ld.nt);
+    ld.item = (int)quotient(local, ld.nt);
+    ld.tile = (int)(local - (long long)ld.item * ld.nt);
   }
   Cursor cu = ld;
 

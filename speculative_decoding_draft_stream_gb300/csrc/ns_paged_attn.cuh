@@ -33,6 +33,12 @@ __host__ __device__ inline Ws workspace(void *p, int n_seqs, int ctas, int rows)
   return w;
 }
 
+// a / b of nonnegative a: 32 bits where both fit (a division of 64 bits is a
+// hundred instructions, and a chain of them is a good part of a short call).
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+  return (a | b) >> 32 ? a / b : (long long)((uint32_t)a / (uint32_t)b);
+}
+
 __device__ __forceinline__ int length(const PagedAttnArgs &a, int b, uint32_t *err) {
   const int s = a.seqs[b];
   if (s < 0 || s >= a.max_seqs) {
@@ -63,14 +69,14 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const Ws ws = workspace(ws_, a.n_seqs, ctas, kRows);
   const long long total = ws.cum[a.n_seqs], cb = ws.cum[b];
-  const long long nt = (ws.cum[b + 1] - cb) / items;
+  const long long nt = quotient(ws.cum[b + 1] - cb, items);
   const long long from = cb + item * nt, to = from + nt;  // the item's tiles
-  const int c0 = (int)(((from + 1) * ctas - 1) / total), c1 = (int)((to * ctas - 1) / total);
+  const int c0 = (int)quotient((from + 1) * ctas - 1, total), c1 = (int)quotient(to * ctas - 1, total);
   if (c0 == c1) return;  // one CTA had it all
   for (int c = c0 + tid; c <= c1; c += kJoinWarps * 32) {
-    const long long first = total * c / ctas;
+    const long long first = quotient(total * c, ctas);
     // a part is its CTA's first unless the CTA began before the item; a CTA may have no tiles at all
-    s_part[c - c0] = first == total * (c + 1) / ctas ? -1 : (c * 2 + (first >= from ? 0 : 1)) * kRows;
+    s_part[c - c0] = first == quotient(total * (c + 1), ctas) ? -1 : (c * 2 + (first >= from ? 0 : 1)) * kRows;
   }
   __syncthreads();
   int node, qh;

@@ -41,9 +41,7 @@ struct Work {
   int ctx;           // positions that every row sees: len - n
 };
 
-__device__ __forceinline__ long long quotient(long long a, int b) {
-  return a >> 32 ? a / b : (long long)((uint32_t)a / (uint32_t)b);
-}
+using paged::quotient;
 
 // A CTA's share of the line of tiles, item by item (a whole warp).  Lane l
 // holds sequence 32 chunk + l of the call, so the line is walked without
@@ -246,14 +244,14 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const TreeArgs 
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (!__any_sync(0xffffffffu, live)) return;  // (every warp has the same rows)
   const long long total = a.cum[a.n_seqs], cb = a.cum[b];
-  const long long nt = (a.cum[b + 1] - cb) / items;
+  const long long nt = quotient(a.cum[b + 1] - cb, items);
   const long long from = cb + item * nt, to = from + nt;  // the item's tiles
-  const int c0 = (int)(((from + 1) * ctas - 1) / total), c1 = (int)((to * ctas - 1) / total);
+  const int c0 = (int)quotient((from + 1) * ctas - 1, total), c1 = (int)quotient(to * ctas - 1, total);
   if (c0 == c1) return;  // one CTA had it all
   for (int c = c0 + tid; c <= c1; c += kJoinThreads) {
-    const long long first = total * c / ctas;
+    const long long first = quotient(total * c, ctas);
     // a part is its CTA's first unless the CTA began before the item; a CTA may have no tiles at all
-    s_part[c - c0] = first == total * (c + 1) / ctas ? -1 : c * 2 + (first >= from ? 0 : 1);
+    s_part[c - c0] = first == quotient(total * (c + 1), ctas) ? -1 : c * 2 + (first >= from ? 0 : 1);
   }
   __syncthreads();
   const int parts = c1 - c0 + 1;
