@@ -5,22 +5,31 @@
 // each key and value is fetched once for all of them (once for every 64 rows
 // when R is larger; the repeats hit L2).
 //
-// Work: the keys of every (sequence, key-value head, block of rows) are cut
-// into tiles of 64, all tiles of the call are put in one line, and each of
-// the resident CTAs takes an equal, contiguous share of it.  So a batch of
-// very different lengths, or one long sequence, keeps every SM busy to the
-// end, whatever the lengths are (the host does not know them).  A CTA whose
-// share begins or ends inside an item leaves its rows' (m, l, o) in the
-// workspace, at most two of them; the join kernel, whose launch overlaps the
-// end of this one, adds up the parts of such items in CTA order.  No atomics:
-// the same inputs give the same bits.
+// Work, two ways (by_rows has the rule).  The line: the keys of every
+// (sequence, key-value head, block of rows), an item, are cut into tiles of
+// 64, all tiles of the call are put in one line, and each of the resident
+// CTAs takes an equal, contiguous share of it.  So a batch of very different
+// lengths, or one long sequence, keeps every SM busy to the end, whatever the
+// lengths are (the host does not know them).  A CTA whose share begins or
+// ends inside an item leaves its rows' (m, l, o) in the workspace, at most two
+// of them; the join kernel, whose launch overlaps the end of this one, adds
+// up the parts of such items in CTA order.  A cluster: a small call is mostly
+// latency, so each item goes to one cluster, whose CTAs have equal shares of
+// its tiles (of 128 keys) and join through shared memory: one launch, no
+// workspace.  No atomics in either: the same inputs give the same bits.
 //
-// In a CTA: keys and values of three tiles are in flight (cp.async, 16 bytes,
-// page ids fetched a tile ahead).  Up to 16 rows the four warps split a
-// tile's keys and join at the item's end; above, each warp has 16 rows of 64.
+// In a CTA: the next tiles are in flight (cp.async, 16 bytes, page ids
+// fetched a tile ahead).  Up to 16 rows the warps split a tile's keys and
+// join at the item's end; above, each of four warps has 16 rows of 64.
 //
 // What bounds it: HBM for one-token steps (each key is used by `group` rows,
-// a few flops a byte); the mma.sync rate for 64-row blocks.
+// a few flops a byte); the mma.sync rate for 64-row blocks.  Loads and
+// products of one CTA hardly overlap (a warp that issues copies waits for the
+// load unit), so CTAs overlap with each other: three to an SM with two tiles
+// each instead of two with three took 48 sequences of 200 to 40000 tokens (28
+// heads on 4, 128 columns, fp16) from 97.6 to 91.0 us, 5.8 TB/s; with 64
+// columns, four to an SM instead of two, 8 sequences of 16000 (12 heads on 4)
+// from 43.8 to 33.1 us.
 #include "ns_paged_attn.cuh"
 
 namespace ns {
@@ -28,30 +37,43 @@ namespace {
 
 using namespace paged;
 
-constexpr int kPaThreads = 128;
-constexpr int kPaKeys = 64;   // keys of a tile
-constexpr int kPaStages = 3;
-constexpr int kPaMerge = 32 * 4 * 4;  // a lane's m, l (and padding), after its o
-
+// Of CTAs that share the line (C = 0), two to an SM, and of those of a
+// cluster, alone on an SM with twice the warps: threads, keys of a tile.
+template <int C>
+constexpr int kThreads = C == 0 ? 128 : 256;
+template <int C>
+constexpr int kKeys = C == 0 ? 64 : 128;
 template <int D>
+constexpr int kPerSm = D == 128 ? 3 : 4;  // CTAs of the line on an SM
+template <int D, int C>
+constexpr int kStages = D == 128 && C == 0 ? 2 : 3;  // tiles in flight
+constexpr int kMerge = 32 * 4 * 4;    // a lane's m, l (and padding), after its o
+
+template <int D, int C>
 __host__ __device__ constexpr int pa_stage() {
-  return 2 * kPaKeys * D * 2;
+  return 2 * kKeys<C> * D * 2;
 }
-template <int D, int WM>
+// Behind the stages: what a warp hands over to warp 0; in a cluster, (m, l)
+// and o of each of its CTAs for the rows that this CTA joins.
+template <int D, int WM, int C>
 __host__ __device__ constexpr int pa_smem() {
-  return kPaStages * pa_stage<D>() + (WM == 1 ? 32 * D / 2 * 4 + kPaMerge : 0);
+  return kStages<D, C> * pa_stage<D, C>() + (C > 0 ? 16 * (D + 2) * 4 : WM == 1 ? 32 * D / 2 * 4 + kMerge : 0);
 }
 
-__host__ __device__ inline long long pa_tiles(int len) { return len > 0 ? (len + kPaKeys - 1) / kPaKeys : 1; }
+template <int C>
+__host__ __device__ inline long long pa_tiles(int len) {
+  return len > 0 ? (len - 1) / kKeys<C> + 1 : 1;
+}
 
 // Where a CTA is in the line of tiles: item (sequence b, `item` = head *
 // blocks + block of rows) and its tile.
+template <int C>
 struct Cursor {
   int b, item, tile, nt, len;
   const int32_t *table;
-  __device__ __forceinline__ void enter(const PagedAttnArgs &a) {
-    len = length(a, b, nullptr);
-    nt = (int)pa_tiles(len);
+  __device__ __forceinline__ void enter(const PagedAttnArgs &a, uint32_t *err) {
+    len = length(a, b, err);
+    nt = (int)pa_tiles<C>(len);
     const int s = a.seqs[b];
     table = a.table + (size_t)(s >= 0 && s < a.max_seqs ? s : 0) * a.table_ld;
   }
@@ -60,75 +82,101 @@ struct Cursor {
     tile = 0;
     if (++item < items) return;
     item = 0;
-    if (++b < a.n_seqs) enter(a);
+    if (++b < a.n_seqs) enter(a, nullptr);
   }
 };
 
-template <typename T, int D, int WM>
-__global__ void __launch_bounds__(kPaThreads) paged_attn_kernel(const PagedAttnArgs a, int blocks) {
-  constexpr int WK = 4 / WM, NK = kPaKeys / WK, kRows = 16 * WM;
+__device__ __forceinline__ uint32_t shared_at(const void *p) {
+  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+__device__ __forceinline__ uint32_t of_rank(uint32_t a, int rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void push(uint32_t a, float x) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(a), "f"(x) : "memory");
+}
+
+// C = 0: the line of tiles.  C > 0 (at most 16 rows): an item to a cluster of C.
+template <typename T, int D, int WM, int C>
+__global__ void __launch_bounds__(kThreads<C>) paged_attn_kernel(const PagedAttnArgs a, int blocks) {
+  constexpr int kPaThreads = kThreads<C>, kPaKeys = kKeys<C>, kWarps = kPaThreads / kWarp;
+  constexpr int WK = kWarps / WM, NK = kPaKeys / WK, kRows = 16 * WM;
   constexpr int kLanesRow = D / 8;                    // threads that fetch a row
   constexpr int kPass = kPaThreads / kLanesRow;       // rows a pass of the CTA fetches
+  static_assert(C == 0 || WM == 1, "a cluster has 16 rows");
   extern __shared__ __align__(128) uint8_t smem[];
-  long long *s_cum = reinterpret_cast<long long *>(smem + pa_smem<D, WM>());
-  __shared__ long long s_sum[kPaThreads / kWarp];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int wm = WM == 1 ? 0 : warp, wk = WM == 1 ? warp : 0;
   const int items = a.kv_heads * blocks, R = a.n * a.group;
   const uint32_t s0 = (uint32_t)__cvta_generic_to_shared(smem);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-  // tiles of the sequences before each one
-  long long total = 0;
-  for (int b0 = 0; b0 < a.n_seqs; b0 += kPaThreads) {
-    const int b = b0 + tid;
-    const long long mine = b < a.n_seqs ? pa_tiles(length(a, b, blockIdx.x == 0 ? a.err : nullptr)) * items : 0;
-    long long sum = mine;
+  Cursor<C> ld;
+  long long t0, t1;
+  Ws ws{};
+  if constexpr (C > 0) {
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");  // this CTA has begun
+    const int at = blockIdx.x / C, rank = blockIdx.x % C;
+    ld.b = at / items, ld.item = at % items;
+    ld.enter(a, rank == 0 && ld.item == 0 ? a.err : nullptr);
+    t0 = (long long)ld.nt * rank / C, t1 = (long long)ld.nt * (rank + 1) / C;
+    ld.tile = (int)t0;
+  } else {
+    long long *s_cum = reinterpret_cast<long long *>(smem + pa_smem<D, WM, C>());
+    __shared__ long long s_sum[kPaThreads / kWarp];
+    // tiles of the sequences before each one
+    long long total = 0;
+    for (int b0 = 0; b0 < a.n_seqs; b0 += kPaThreads) {
+      const int b = b0 + tid;
+      const long long mine = b < a.n_seqs ? pa_tiles<C>(length(a, b, blockIdx.x == 0 ? a.err : nullptr)) * items : 0;
+      long long sum = mine;
 #pragma unroll
-    for (int off = 1; off < kWarp; off <<= 1) {
-      const long long o = __shfl_up_sync(0xffffffffu, sum, off);
-      if (lane >= off) sum += o;
+      for (int off = 1; off < kWarp; off <<= 1) {
+        const long long o = __shfl_up_sync(0xffffffffu, sum, off);
+        if (lane >= off) sum += o;
+      }
+      if (lane == kWarp - 1) s_sum[warp] = sum;
+      __syncthreads();
+      long long before = total;
+      for (int w = 0; w < kPaThreads / kWarp; ++w) {
+        if (w < warp) before += s_sum[w];
+        total += s_sum[w];
+      }
+      if (b < a.n_seqs) s_cum[b] = before + sum - mine;
+      __syncthreads();
     }
-    if (lane == kWarp - 1) s_sum[warp] = sum;
-    __syncthreads();
-    long long before = total;
-    for (int w = 0; w < kPaThreads / kWarp; ++w) {
-      if (w < warp) before += s_sum[w];
-      total += s_sum[w];
+    ws = workspace(a.ws, a.n_seqs, gridDim.x, kRows);
+    if (blockIdx.x == 0) {
+      for (int b = tid; b < a.n_seqs; b += kPaThreads) ws.cum[b] = s_cum[b];
+      if (tid == 0) ws.cum[a.n_seqs] = total;
     }
-    if (b < a.n_seqs) s_cum[b] = before + sum - mine;
-    __syncthreads();
-  }
-  const Ws ws = workspace(a.ws, a.n_seqs, gridDim.x, kRows);
-  if (blockIdx.x == 0) {
-    for (int b = tid; b < a.n_seqs; b += kPaThreads) ws.cum[b] = s_cum[b];
-    if (tid == 0) ws.cum[a.n_seqs] = total;
-  }
-  const long long t0 = quotient(total * blockIdx.x, gridDim.x), t1 = quotient(total * (blockIdx.x + 1), gridDim.x);
-  if (t0 >= t1) return;
+    t0 = quotient(total * blockIdx.x, gridDim.x), t1 = quotient(total * (blockIdx.x + 1), gridDim.x);
+    if (t0 >= t1) return;
 
-  Cursor ld;
-  {
-    int lo = 0, hi = a.n_seqs;  // the last sequence that begins at or before t0
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (s_cum[mid] <= t0)
-        lo = mid;
-      else
-        hi = mid;
+    {
+      int lo = 0, hi = a.n_seqs;  // the last sequence that begins at or before t0
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (s_cum[mid] <= t0)
+          lo = mid;
+        else
+          hi = mid;
+      }
+      ld.b = lo;
+      ld.enter(a, nullptr);
+      const long long local = t0 - s_cum[lo];
+      ld.item = (int)quotient(local, ld.nt);
+      ld.tile = (int)(local - (long long)ld.item * ld.nt);
     }
-    ld.b = lo;
-    ld.enter(a);
-    const long long local = t0 - s_cum[lo];
-    ld.item = (int)quotient(local, ld.nt);
-    ld.tile = (int)(local - (long long)ld.item * ld.nt);
   }
-  Cursor cu = ld;
+  Cursor<C> cu = ld;
 
-  // page ids of the load cursor's tile, one for each eight rows, in lanes 0 to 7
+  // page ids of the load cursor's tile, one for each eight rows, in as many lanes
   auto fetch_ids = [&]() {
     int id = -1;
-    if (lane < 8) {
+    if (lane < kPaKeys / 8) {
       const int p = ld.tile * kPaKeys + lane * 8;
       if (p < ld.len) {
         id = ld.table[p >> a.page_shift];
@@ -140,20 +188,26 @@ __global__ void __launch_bounds__(kPaThreads) paged_attn_kernel(const PagedAttnA
     }
     return id;
   };
-  const T *kbase = static_cast<const T *>(a.k), *vbase = static_cast<const T *>(a.v);
+  // A lane has the offsets of its eight rows' first; a thread's rows are all the same one of their eight.
   const int fr = tid / kLanesRow, fc = tid % kLanesRow, pmask = (1 << a.page_shift) - 1;
-  auto fetch = [&](int ids, int stage) {
-    const uint32_t sk = s0 + stage * pa_stage<D>(), sv = sk + kPaKeys * D * 2;
-    const int head = ld.item / blocks;
+  static_assert(kPass % 8 == 0, "rows of a thread");
+  const T *kbase = static_cast<const T *>(a.k) + (fr & 7) * a.k_token + fc * 8;
+  const T *vbase = static_cast<const T *>(a.v) + (fr & 7) * a.v_token + fc * 8;
+  const uint32_t to = piece<D>(fr, fc);
+  auto fetch = [&](int id, int stage) {
+    const uint32_t sk = s0 + stage * pa_stage<D, C>() + to, sv = sk + kPaKeys * D * 2;
+    const int left = ld.len - ld.tile * kPaKeys, head = ld.item / blocks;
+    const int64_t page = id >= 0 ? id : 0, row = (ld.tile * kPaKeys + lane * 8) & pmask;
+    const int64_t ko = page * a.k_page + head * a.k_head + row * a.k_token;
+    const int64_t vo = page * a.v_page + head * a.v_head + row * a.v_token;
+    const uint32_t there = __ballot_sync(0xffffffffu, id >= 0);
 #pragma unroll
     for (int pass = 0; pass < kPaKeys / kPass; ++pass) {
       const int r = pass * kPass + fr;
-      const int id = __shfl_sync(0xffffffffu, ids, r >> 3);
-      const int p = ld.tile * kPaKeys + r;
-      const bool ok = id >= 0 && p < ld.len;
-      const int64_t page = ok ? id : 0, row = ok ? p & pmask : 0;
-      cp16(sk + piece<D>(r, fc), kbase + page * a.k_page + head * a.k_head + row * a.k_token + fc * 8, ok);
-      cp16(sv + piece<D>(r, fc), vbase + page * a.v_page + head * a.v_head + row * a.v_token + fc * 8, ok);
+      const bool ok = r < left && (there >> (r >> 3) & 1);
+      const int64_t k = __shfl_sync(0xffffffffu, ko, r >> 3), v = __shfl_sync(0xffffffffu, vo, r >> 3);
+      cp16(sk + pass * kPass * D * 2, kbase + k, ok);
+      cp16(sv + pass * kPass * D * 2, vbase + v, ok);
     }
   };
 
@@ -164,7 +218,7 @@ __global__ void __launch_bounds__(kPaThreads) paged_attn_kernel(const PagedAttnA
   auto issue = [&]() {
     if (left_ld > 0) {
       fetch(ids, st_ld);
-      st_ld = st_ld + 1 == kPaStages ? 0 : st_ld + 1;
+      st_ld = st_ld + 1 == kStages<D, C> ? 0 : st_ld + 1;
       --left_ld;
       if (left_ld > 0) {
         ld.next(a, items);
@@ -174,9 +228,10 @@ __global__ void __launch_bounds__(kPaThreads) paged_attn_kernel(const PagedAttnA
     cp_commit();
   };
 #pragma unroll
-  for (int i = 0; i < kPaStages - 1; ++i) issue();
+  for (int i = 0; i < kStages<D, C> - 1; ++i) issue();
 
   Rows<T, D> rows;
+  if (C > 0) rows.clear();  // (a CTA of a short sequence may have no tile)
   uint32_t q[D / 16][4];
   uint64_t word[2] = {0, 0};
   int st = 0;
@@ -203,11 +258,11 @@ __global__ void __launch_bounds__(kPaThreads) paged_attn_kernel(const PagedAttnA
         }
       }
     }
-    cp_wait<kPaStages - 2>();
+    cp_wait<kStages<D, C> - 2>();
     __syncthreads();  // the tile is there for everyone, and everyone is done with the stage to be filled next
     issue();
-    const uint32_t sk = s0 + st * pa_stage<D>(), sv = sk + kPaKeys * D * 2;
-    st = st + 1 == kPaStages ? 0 : st + 1;
+    const uint32_t sk = s0 + st * pa_stage<D, C>(), sv = sk + kPaKeys * D * 2;
+    st = st + 1 == kStages<D, C> ? 0 : st + 1;
     const int ctx = cu.len - a.n, p0 = cu.tile * kPaKeys, k0 = wk * NK;
     if (p0 + kPaKeys <= ctx) {
       rows.template tile<NK, false>(q, sk, sv, k0, c, [](int, int) { return false; }, false);
@@ -227,8 +282,9 @@ __global__ void __launch_bounds__(kPaThreads) paged_attn_kernel(const PagedAttnA
     const bool ends = cu.tile + 1 == cu.nt;
     if (ends || g + 1 == t1) {
       rows.sum_l();
+      if (C > 0) break;
       if (WM == 1) {  // the warps' keys join, in warp order, in warp 0
-        float4 *bo = reinterpret_cast<float4 *>(smem + kPaStages * pa_stage<D>());
+        float4 *bo = reinterpret_cast<float4 *>(smem + kStages<D, C> * pa_stage<D, C>());
         float4 *bm = bo + (D / 8) * 32;
         for (int w = 1; w < 4; ++w) {
           if (warp == w) {
@@ -290,6 +346,70 @@ __global__ void __launch_bounds__(kPaThreads) paged_attn_kernel(const PagedAttnA
     }
     if (g + 1 < t1) cu.next(a, items);
   }
+  if constexpr (C > 0) {
+    // The warps' parts join here, and the CTAs' in CTA r % C for row r, both in their order.
+    constexpr int kPitch = D + 8;  // of a row of a warp's part: the eight rows of a store in different banks
+    static_assert(kWarps * 16 * (kPitch + 2) * 4 <= kStages<D, C> * pa_stage<D, C>(), "the parts replace the tiles");
+    const int rank = blockIdx.x % C, head = ld.item, b = ld.b;
+    float *w_o = reinterpret_cast<float *>(smem);
+    float2 *w_ml = reinterpret_cast<float2 *>(w_o + kWarps * 16 * kPitch);
+    float *c_o = reinterpret_cast<float *>(smem + kStages<D, C> * pa_stage<D, C>());  // [16 / C][C][D]
+    float2 *c_ml = reinterpret_cast<float2 *>(c_o + 16 * D);
+    __syncthreads();  // (every tile has been waited for and used)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int r = (lane >> 2) + 8 * h;
+      if (r < R) {
+        float2 *dst = reinterpret_cast<float2 *>(w_o + (warp * 16 + r) * kPitch) + (lane & 3);
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) dst[i * 4] = make_float2(rows.o[i][2 * h], rows.o[i][2 * h + 1]);
+        if ((lane & 3) == 0) w_ml[warp * 16 + r] = make_float2(rows.m[h], rows.l[h]);
+      }
+    }
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");  // every CTA of the cluster has begun
+    __syncthreads();
+    const int col = tid % D;
+    for (int r = tid / D; r < R; r += kPaThreads / D) {
+      float2 p[kWarps];
+      float m = kNegInf, l = 0.f, o = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        p[w] = w_ml[w * 16 + r];
+        m = fmaxf(m, p[w].x);
+      }
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float f = ex2(p[w].x - (m == kNegInf ? 0.f : m));
+        l = fmaf(p[w].y, f, l);
+        o = fmaf(w_o[(w * 16 + r) * kPitch + col], f, o);
+      }
+      const int part = r / C * C + rank;
+      push(of_rank(shared_at(c_o + part * D + col), r % C), o);
+      if (col < 2) push(of_rank(shared_at(c_ml + part) + 4 * col, r % C), col ? l : m);
+    }
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    for (int own = tid / D; own < 16 / C; own += kPaThreads / D) {
+      const int r = own * C + rank;
+      if (r >= R) break;
+      float2 p[C];
+      float m = kNegInf, l = 0.f, o = 0.f;
+#pragma unroll
+      for (int i = 0; i < C; ++i) {
+        p[i] = c_ml[own * C + i];
+        m = fmaxf(m, p[i].x);
+      }
+#pragma unroll
+      for (int i = 0; i < C; ++i) {
+        const float f = ex2(p[i].x - (m == kNegInf ? 0.f : m));
+        l = fmaf(p[i].y, f, l);
+        o = fmaf(c_o[(own * C + i) * D + col], f, o);
+      }
+      const int64_t at = ((int64_t)b * a.n + r / a.group) * a.q_heads + head * a.group + r % a.group;
+      static_cast<T *>(a.out)[at * D + col] = static_cast<T>(l == 0.f ? 0.f : o / l);
+      if (a.lse && col == 0) a.lse[at] = row_lse<T>(m, l);
+    }
+  }
 }
 
 // The rows of an item for the join: row r of head h and block rb is new token
@@ -314,55 +434,111 @@ template <typename T, int D, int WM>
 cudaError_t launch(const PagedAttnArgs &a, int sms, cudaStream_t st) {
   constexpr int kRows = 16 * WM;
   const int blocks = (a.n * a.group + kRows - 1) / kRows;
-  const int smem = pa_smem<D, WM>() + a.n_seqs * 8;
-  const long long most = pa_tiles(a.max_len) * a.n_seqs * a.kv_heads * blocks;
-  const int per_sm = smem <= 113 * 1024 ? 2 : 1;
-  const int ctas = (int)(most < (long long)per_sm * sms ? most : per_sm * sms);
-  paged_attn_kernel<T, D, WM><<<ctas, kPaThreads, smem, st>>>(a, blocks);
+  const int smem = pa_smem<D, WM, 0>() + a.n_seqs * 8;
+  const long long most = pa_tiles<0>(a.max_len) * a.n_seqs * a.kv_heads * blocks;
+  const int ctas = (int)(most < (long long)kPerSm<D> * sms ? most : kPerSm<D> * sms);
+  paged_attn_kernel<T, D, WM, 0><<<ctas, kThreads<0>, smem, st>>>(a, blocks);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   const int rows = a.n * a.group < kRows ? a.n * a.group : kRows;
   return launch_join<T, D>(a, Rows16<WM>{blocks}, rows, a.kv_heads * blocks, ctas, st);
 }
 
-template <typename T, int D, int WM>
+struct ClusterLaunch {
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute at[1];
+  ClusterLaunch(int ctas, int c, int smem, cudaStream_t st) {
+    cfg.gridDim = dim3((unsigned)ctas);
+    cfg.blockDim = dim3(kThreads<8>);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = (unsigned)c;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+  }
+};
+template <typename T, int D, int C>
+int resident = 0;  // clusters that the GPU holds at once
+
+// Whether each item can have its own cluster of C, and did (e).
+template <typename T, int D, int C>
+bool launch_clusters(const PagedAttnArgs &a, cudaStream_t st, cudaError_t &e) {
+  constexpr int kTiles = 8;
+  const long long items = (long long)a.n_seqs * a.kv_heads;
+  if (items > resident<T, D, C> || a.max_len > kTiles * C * kKeys<C>) return false;
+  ClusterLaunch l((int)items * C, C, pa_smem<D, 1, C>(), st);
+  e = cudaLaunchKernelEx(&l.cfg, paged_attn_kernel<T, D, 1, C>, a, 1);
+  return true;
+}
+
+template <typename T, int D, int WM, int C>
 cudaError_t prepare() {
-  return cudaFuncSetAttribute(paged_attn_kernel<T, D, WM>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              pa_smem<D, WM>() + NS_MAX_ATTEND_SEQS * 8);
+  cudaError_t e = cudaFuncSetAttribute(paged_attn_kernel<T, D, WM, C>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       pa_smem<D, WM, C>() + (C == 0 ? NS_MAX_ATTEND_SEQS * 8 : 0));
+  if (C > 8 && e == cudaSuccess)
+    e = cudaFuncSetAttribute(paged_attn_kernel<T, D, WM, C>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (C > 0 && e == cudaSuccess) {
+    ClusterLaunch l(C * 64, C, pa_smem<D, 1, C>(), nullptr);
+    e = cudaOccupancyMaxActiveClusters(&resident<T, D, C>, paged_attn_kernel<T, D, WM, C>, &l.cfg);
+  }
+  return e;
 }
 
 // Up to 16 rows the keys are what costs: each is fetched once and the warps
-// split them.  Above, the products are: they belong on the tensor cores of
+// split them.  A call whose items fit on the GPU as clusters of 16, else of 8,
+// all at once, with up to 8 tiles to a CTA, takes clusters.  Measured, line
+// against cluster, one new token, bf16 (us in a graph):
+//   32 heads on 8, 128 columns, 1 sequence:  100 tokens 8.4, 5.6;  4097: 12.9 (two CTAs to an SM), 11.1;
+//     8000: 15.2, 15.2;  16000 (16 tiles): 18.7, 25.4;  2 sequences (a second wave of clusters) 100: 8.6, 9.9
+//   28 on 4, 128 columns, 1 sequence, clusters of 16 (8):  4097: 13.7, 9.0 (11.3);  16000: 17.2, 15.2 (25.8);
+//     32000: 20.7, 25.8 (48.4)
+//   12 on 4, 64 columns, 4 sequences, clusters of 8:  1000: 9.6, 4.9;  8000: 16.0, 13.3;  16000: 20.3, 22.5
+// Above 16 rows the products cost: they belong on the tensor cores of
 // ns_paged_umma.cu, which want queries that TMA can fetch (16-byte aligned,
 // strides multiples of 8); other queries take 64 rows a CTA here.
+template <typename T, int D>
+cudaError_t by_rows(const PagedAttnArgs &a, int sms, cudaStream_t st) {
+  if (a.n * a.group <= 16) {
+    cudaError_t e;
+    if (launch_clusters<T, D, 16>(a, st, e) || launch_clusters<T, D, 8>(a, st, e)) return e;
+    return launch<T, D, 1>(a, sms, st);
+  }
+  if (paged_umma_ok(a)) return launch_paged_umma(a, Type<T>::kBf16 ? NS_DTYPE_BF16 : NS_DTYPE_F16, D, sms, st);
+  return launch<T, D, 4>(a, sms, st);
+}
 template <typename T>
-cudaError_t by_rows(const PagedAttnArgs &a, int dim, int sms, cudaStream_t st) {
-  if (a.n * a.group <= 16) return dim == 128 ? launch<T, 128, 1>(a, sms, st) : launch<T, 64, 1>(a, sms, st);
-  if (paged_umma_ok(a)) return launch_paged_umma(a, Type<T>::kBf16 ? NS_DTYPE_BF16 : NS_DTYPE_F16, dim, sms, st);
-  return dim == 128 ? launch<T, 128, 4>(a, sms, st) : launch<T, 64, 4>(a, sms, st);
+cudaError_t by_dim(const PagedAttnArgs &a, int dim, int sms, cudaStream_t st) {
+  return dim == 128 ? by_rows<T, 128>(a, sms, st) : by_rows<T, 64>(a, sms, st);
+}
+template <typename T, int D>
+cudaError_t prepare_all() {
+  cudaError_t e = prepare<T, D, 1, 0>();
+  if (e == cudaSuccess) e = prepare<T, D, 4, 0>();
+  if (e == cudaSuccess) e = prepare<T, D, 1, 8>();
+  if (e == cudaSuccess) e = prepare<T, D, 1, 16>();
+  return e;
 }
 
 }  // namespace
 
 int64_t paged_attn_ws(int n_seqs, int n, int q_heads, int kv_heads, int dim, int sms) {
-  // two parts for each CTA: 2 sms CTAs of 16 rows, or sms CTAs of 256 (2 sms of 64 are fewer)
-  const int64_t rows = n * (q_heads / kv_heads) <= 16 ? (int64_t)2 * sms * 2 * 16 : (int64_t)sms * 2 * 256;
+  // two parts for each CTA: up to 4 sms CTAs of 16 rows, or sms CTAs of 256 (4 sms of 64 are no more)
+  const int64_t rows = n * (q_heads / kv_heads) <= 16 ? (int64_t)kPerSm<64> * sms * 2 * 16 : (int64_t)sms * 2 * 256;
   return (((int64_t)(n_seqs + 1) * 8 + 255) & ~(int64_t)255) + rows * (dim + 2) * 4;
 }
 
 cudaError_t prepare_paged_attn() {
-  cudaError_t e = cudaSuccess;
-  auto also = [&](cudaError_t x) { e = e == cudaSuccess ? x : e; };
-  also(prepare<__nv_bfloat16, 128, 1>()), also(prepare<__nv_bfloat16, 128, 4>());
-  also(prepare<__nv_bfloat16, 64, 1>()), also(prepare<__nv_bfloat16, 64, 4>());
-  also(prepare<__half, 128, 1>()), also(prepare<__half, 128, 4>());
-  also(prepare<__half, 64, 1>()), also(prepare<__half, 64, 4>());
-  also(prepare_paged_umma());
-  return e;
+  cudaError_t e = prepare_all<__nv_bfloat16, 128>();
+  if (e == cudaSuccess) e = prepare_all<__nv_bfloat16, 64>();
+  if (e == cudaSuccess) e = prepare_all<__half, 128>();
+  if (e == cudaSuccess) e = prepare_all<__half, 64>();
+  return e == cudaSuccess ? prepare_paged_umma() : e;
 }
 
 cudaError_t launch_paged_attn(const PagedAttnArgs &a, int dtype, int dim, int sms, cudaStream_t st) {
-  return dtype == NS_DTYPE_BF16 ? by_rows<__nv_bfloat16>(a, dim, sms, st) : by_rows<__half>(a, dim, sms, st);
+  return dtype == NS_DTYPE_BF16 ? by_dim<__nv_bfloat16>(a, dim, sms, st) : by_dim<__half>(a, dim, sms, st);
 }
 
 }  // namespace ns

@@ -548,3 +548,20 @@ def test_paged_refusals(ns):
         with pytest.raises(ns.NanoSpecError):
             f()
     assert ns.ops_error() == 0
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("d,kinds", [(64, ((2, 1), (4, 2), (16, 2))), (128, ((2, 1), (3, 3), (20, 2)))])
+def test_paged_few_rows_by_number_of_sequences(ns, dtype, d, kinds):
+    """Up to 16 rows: calls of a few items (each split by a cluster, of 16 or of 8) and of many (one line of tiles)."""
+    for seqs, hkv in kinds:
+        lens = [(1, 700, 2049, 64, 0, 129, 3)[(i * 5 + seqs) % 7] + 13 * (i // 7) for i in range(seqs)]
+        run_paged(ns, lens, 1, 4 * hkv, hkv, d, 16, dtype, 40 + seqs)
+        run_paged(ns, [x + 5 for x in lens], 5, 3 * hkv, hkv, d, 64, dtype, 41 + seqs, masks="tree")
+
+
+def test_paged_cluster_repeats_and_lengths_past_its_bound(ns):
+    """A call of one sequence around the longest that its CTAs take as a cluster, with the bound on the lengths low."""
+    for n in (8191, 8192, 8193, 16384, 16385):
+        run_paged(ns, [n], 1, 16, 8, 64, 64, F16, n)
+    run_paged(ns, [20000], 1, 8, 2, 64, 64, F16, 50, max_len=1000)
