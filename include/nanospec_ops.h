@@ -49,7 +49,8 @@ NS_API ns_status ns_ops_get_error(uint32_t *flags, int32_t clear);
  *   lse_i = log sum_j exp(scale * q_i . k_j).
  *   d_q   [tokens x q_heads x dim], d_k, d_v [tokens x kv_heads x dim], of
  *         `dtype` (bf16 or f16), rows of dim consecutive elements, token and
- *         head strides in elements, multiples of 8; 16-byte aligned
+ *         head strides in elements, positive multiples of 8 (any for an axis
+ *         of one); 16-byte aligned
  *   d_cu  int32 [n_seqs + 1]: sequence s holds tokens d_cu[s] .. d_cu[s+1] - 1
  *         (0 first, not decreasing, `tokens` last; empty sequences are fine)
  *   max_len  HOST: no sequence is longer (tokens past it are not computed and

@@ -48,6 +48,12 @@ bool attn_type(int dtype, int dim) {
 }
 bool heads_ok(int q, int kv) { return q >= 1 && kv >= 1 && q <= 65535 && q % kv == 0; }
 bool by8(int64_t s) { return s % 8 == 0; }
+// A stride (elements) that a TMA map takes.  An axis of one place is never
+// stepped along: whatever its stride is, it becomes `row`.
+bool map_stride(int64_t &s, int places, int row) {
+  if (places == 1) s = row;
+  return s > 0 && by8(s) && s < (int64_t)1 << 39;
+}
 
 bool cache_ok(const ns_kv_pages *c) {
   if (!c || !c->k || !c->v || !c->table || !c->lengths || !c->refs) return false;
@@ -88,8 +94,9 @@ ns_status ns_attend_prompt(const void *d_q, const void *d_k, const void *d_v, in
     return NS_ERR_ARG;
   if (tokens == 0 || n_seqs == 0 || max_len == 0) return NS_OK;
   if (!d_q || !d_k || !d_v || !d_cu || !d_out || !aligned(d_q, 16) || !aligned(d_k, 16) || !aligned(d_v, 16) ||
-      !aligned(d_out, 16) || !aligned(d_lse, 4) || !aligned(d_cu, 4) || !by8(q_token) || !by8(q_head) ||
-      !by8(k_token) || !by8(k_head) || !by8(v_token) || !by8(v_head))
+      !aligned(d_out, 16) || !aligned(d_lse, 4) || !aligned(d_cu, 4) || !map_stride(q_token, tokens, dim) ||
+      !map_stride(k_token, tokens, dim) || !map_stride(v_token, tokens, dim) || !map_stride(q_head, q_heads, dim) ||
+      !map_stride(k_head, kv_heads, dim) || !map_stride(v_head, kv_heads, dim))
     return NS_ERR_ARG;
   const Device *d = nullptr;
   if (ns_status s = current(&d)) return s;

@@ -65,7 +65,7 @@ def attend_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu: torch.T
                   scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
                   lse: Optional[torch.Tensor] = None, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
     """Causal attention over packed prompts: q [T, Hq, D], k and v [T, Hkv, D] (bf16 or fp16, D 64 or 128; token
-    and head strides are free multiples of 8 elements), cu int32 [B + 1] the sequences' bounds, max_len the
+    and head strides are free positive multiples of 8 elements), cu int32 [B + 1] the sequences' bounds, max_len the
     longest.  Returns (out [T, Hq, D], lse fp32 [T, Hq]).  scale: 1 / sqrt(D) by default."""
     s = None if stream is None else _other(stream)
     r = _native().attend_prompt(q, k, v, cu, max_len, scale, out, lse, None if s is None else s.cuda_stream)

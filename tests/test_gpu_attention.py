@@ -565,3 +565,17 @@ def test_paged_cluster_repeats_and_lengths_past_its_bound(ns):
     for n in (8191, 8192, 8193, 16384, 16385):
         run_paged(ns, [n], 1, 16, 8, 64, 64, F16, n)
     run_paged(ns, [20000], 1, 8, 2, 64, 64, F16, 50, max_len=1000)
+
+
+def test_prompt_strides_of_single_and_repeated_heads(ns):
+    g = gen(60)
+    q, k, v = normal(g, (70, 4, 64), BF16).cuda(), normal(g, (70, 1, 64), BF16).cuda(), normal(g, (70, 1, 64), BF16).cuda()
+    cu = torch.tensor([0, 70], dtype=torch.int32).cuda()
+    want, wl = ns.attend_prompt(q, k, v, cu, 70)
+    one = [torch.as_strided(t, (70, 1, 64), (64, 0, 1)) for t in (k, v)]  # an axis of one may have any stride
+    got, gl = ns.attend_prompt(q, *one, cu, 70)
+    assert torch.equal(got, want) and torch.equal(gl, wl)
+    with pytest.raises(ns.NanoSpecError):  # two heads that are one in memory
+        ns.attend_prompt(q, k.expand(70, 2, 64), v.expand(70, 2, 64), cu, 70)
+    a, _ = ns.attend_prompt(q[:1], k[:1], v[:1], cu[:1].repeat(2) + torch.tensor([0, 1], device="cuda", dtype=torch.int32), 1)
+    assert torch.equal(a, v[:1].expand(1, 4, 64))
