@@ -61,7 +61,8 @@ using attn::ex2;
 using attn::kNegInf;
 
 constexpr int kThreads = 384;
-constexpr int kRing = 4;             // key or value tiles in flight
+constexpr int kRing = 4;             // key or value tiles in flight: keys in the even places
+static_assert(kRing % 2 == 0, "keys and values take turns");
 constexpr int kKeys = 128;           // keys of a tile
 constexpr int kHalf = 128 * 128;     // bytes of 128 rows of 64 elements
 constexpr float kLimit = 32768.f;    // a sum of 64 probabilities above this says that m is too low
@@ -127,7 +128,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0) {
     for (int s = 0; s < kRing; ++s) {
       mbar_init(base + L::kKvFull + 8 * s, 1);
-      mbar_init(base + L::kKvEmpty + 8 * s, 1);
+      mbar_init(base + L::kKvEmpty + 8 * s, 1 + (s & 1));  // the products; values: and the check
     }
     mbar_init(base + L::kQFull, 1);
     mbar_init(base + L::kQEmpty, 1);
@@ -313,10 +314,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       volatile int *any = reinterpret_cast<volatile int *>(g + L::kWildAny) + (i & 1);
       const int n = max(w.n0, w.n1);
       bool reset = false;
-      for (int j = w.hidden; j < n && ok; ++j) {
+      for (int j = 0; j < n && ok; ++j) {
+        // Every value tile passes here, so that the barrier's phase is this tile's: a slot is not filled again before
+        // it did.
         const int pos = it + 2 * j + 1, s = pos % kRing;
         ok = __all_sync(0xffffffffu, umma::inline_wait(base + L::kKvFull + 8 * s, (pos / kRing) & 1, err));
         if (!ok) break;
+        if (j < w.hidden) {
+          if (lane == 0) mbar_arrive(base + L::kKvEmpty + 8 * s);
+          continue;
+        }
         uint8_t *tile = g + L::kKV + s * L::kTile;
         bool touched = M::template clear<T, D>(a, w, j, tile, lane);
         if (__any_sync(0xffffffffu, attn::wild_pieces<T>(base + L::kKV + s * L::kTile, L::kTile / 16, lane, kWarp))) {
@@ -337,7 +344,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (__any_sync(0xffffffffu, touched))
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the zeros, for the tensor core
         __syncwarp();
-        if (lane == 0) mbar_arrive(base + L::kCheck + 8 * (checked % kChecks));
+        if (lane == 0) {
+          mbar_arrive(base + L::kCheck + 8 * (checked % kChecks));
+          mbar_arrive(base + L::kKvEmpty + 8 * s);
+        }
         ++checked;
       }
       it += 2 * n;

@@ -579,3 +579,57 @@ def test_prompt_strides_of_single_and_repeated_heads(ns):
         ns.attend_prompt(q, k.expand(70, 2, 64), v.expand(70, 2, 64), cu, 70)
     a, _ = ns.attend_prompt(q[:1], k[:1], v[:1], cu[:1].repeat(2) + torch.tensor([0, 1], device="cuda", dtype=torch.int32), 1)
     assert torch.equal(a, v[:1].expand(1, 4, 64))
+
+
+@pytest.mark.parametrize("d,P,dtype", [(128, 16, BF16), (64, 64, F16)])
+def test_paged_several_long_items_to_a_cta(ns, d, P, dtype):
+    """More rows than 16 and far more tiles than SMs: a CTA has whole items and parts of several tiles in a row.
+    (What pages hold behind a sequence's end is NaN.)"""
+    lens = [150 + 47 * i for i in range(20)]
+    run_paged(ns, lens, 24, 16, 16, d, P, dtype, 61, masks="tree")
+    run_paged(ns, lens[::-1], 60, 32, 8, d, P, dtype, 62, masks="tree")
+
+
+def test_paged_wild_values_of_hidden_nodes_of_long_items(ns):
+    """Nodes whose values are not finite, behind contexts of several tiles, several items to a CTA."""
+    n, lens, hkv = 24, [200 + 61 * i for i in range(16)], 16
+    g, rng = gen(63), random.Random(63)
+    dk, dv, table, keys, vals = make_cache(g, rng, lens, hkv, 16, 128, BF16)
+    masks = tree_masks(rng, len(lens), n)
+    q = normal(g, (len(lens), n, hkv, 128), BF16)
+    for b, N in enumerate(lens):
+        for pos, col, what in ((N - n // 2, 3, float("nan")), (N - 1, 64, float("-inf"))):
+            vals[b][pos, :, col] = what
+            dv[table[b, pos // 16], :, pos % 16, col] = what
+    out, _ = ns.attend_paged(q.cuda(), dk, dv, table.cuda(), torch.tensor(lens, dtype=torch.int32).cuda(),
+                             torch.arange(len(lens), dtype=torch.int32).cuda(), mask=signed(masks).cuda())
+    out = out.cpu()
+    for b, N in enumerate(lens):
+        sees = torch.tensor([[p < N - n or bool(masks[b][i] >> (p - N + n) & 1) for p in range(N)] for i in range(n)])
+        for h in range(hkv):
+            o, _, to, _ = attend_rows(q[b, :, h], keys[b][:, h], vals[b][:, h], sees, 128 ** -0.5)
+            bad = torch.isnan(o)
+            assert not torch.isfinite(out[b, :, h][bad]).any()
+            check(out[b, :, h].double().masked_fill(bad, 0), o.masked_fill(bad, 0), to, "nodes that see none")
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_prompt_wild_values_late_in_long_sequences(ns, d):
+    """Values that are not finite many tiles into a sequence: the rows before them do not see them."""
+    g = gen(64)
+    lens, hq, hkv = [900, 1100, 400], 32, 4
+    cu = [0, 900, 2000, 2400]
+    q, k, v = normal(g, (2400, hq, d), BF16), normal(g, (2400, hkv, d), BF16), normal(g, (2400, hkv, d), BF16)
+    for pos, col, what in ((850, 5, float("nan")), (899, 0, float("inf")), (900 + 700, 9, float("-inf")), (900 + 1030, 5, float("nan")),
+                           (2000 + 390, d - 1, float("nan"))):
+        v[pos, :, col] = what
+    out, _ = ns.attend_prompt(q.cuda(), k.cuda(), v.cuda(), torch.tensor(cu, dtype=torch.int32).cuda(), max(lens))
+    out = out.cpu()
+    for a, b in zip(cu[:-1], cu[1:]):
+        sees = torch.ones(b - a, b - a, dtype=torch.bool).tril()
+        for h in range(hq):
+            kh = h // (hq // hkv)
+            o, _, to, _ = attend_rows(q[a:b, h], k[a:b, kh], v[a:b, kh], sees, d ** -0.5)
+            bad = torch.isnan(o)
+            assert not torch.isfinite(out[a:b, h][bad]).any()
+            check(out[a:b, h].double().masked_fill(bad, 0), o.masked_fill(bad, 0), to, "rows that see none")
