@@ -10,8 +10,8 @@
 // U' = 2^-delta (U - delta S).  Two such triples join the same way.
 //
 // The top k need no second read of the row.  A thread's maximum is m; the k-th
-// largest of the maxima of 32 groups of threads bounds the k-th largest value
-// from below, and only threads whose maximum reaches it can hold one of the
+// largest of the maxima of 32 or 64 groups of threads bounds the k-th largest
+// value from below, and only threads whose maximum reaches it can hold one of the
 // top k: their few values alone are read again (from L2).  Those that reach
 // the bound go to a buffer in any order, and each one's place is the number
 // of better ones.  Where they do not fit (rows of many equal values), every
@@ -36,6 +36,10 @@ namespace {
 constexpr int kLpVecs = 4;        // 16-byte loads a thread keeps in flight
 constexpr int kLpMaxCluster = 8;  // portable cluster size
 constexpr int kLpMinSlice = 4096; // least logits of a CTA of a split row
+// Above 16 alternatives, 64 groups instead of 32: 32 groups' least maximum
+// lets a third of the threads through. 126 fp32 rows of 128256, k 32: 76 ->
+// 24 us; 298 bf16 rows, k 31: 41 -> 28; k 17: 27.5 -> 25.0; but k 14: 17.0 -> 17.9.
+constexpr int kFineFrom = 16;
 constexpr int kLpBuffer = kLpMaxCluster * NS_MAX_ALTERNATIVES;  // candidates of a CTA, or the lists of a cluster
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -217,8 +221,8 @@ __global__ void __launch_bounds__(kLpThreads, 1024 / kLpThreads + 1024 / kLpThre
   constexpr int kLpWarps = kLpThreads / kWarp;
   using V = Vec<T>;
   constexpr int N = V::N;
-  constexpr int kGroups = 32, kGroup = kLpThreads / kGroups;  // threads of a group
-  __shared__ uint32_t s_group[kGroups];
+  constexpr int kFine = 64, kCoarse = 32;  // groups of threads
+  __shared__ uint32_t s_group[kFine];
   __shared__ float s_top[kLpWarps];
   __shared__ float2 s_sums[kLpWarps];
   __shared__ uint32_t s_mask[kLpWarps];
@@ -288,8 +292,13 @@ __global__ void __launch_bounds__(kLpThreads, 1024 / kLpThreads + 1024 / kLpThre
   {
     uint32_t most = my_key;
 #pragma unroll
-    for (int off = kGroup / 2; off > 0; off >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, off));
-    if (a.k > 0 && lane % kGroup == 0) s_group[tid / kGroup] = most;
+    for (int off = kLpThreads / kFine / 2; off > 0; off >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, off));
+    if (a.k > kFineFrom) {
+      if (lane % (kLpThreads / kFine) == 0) s_group[tid / (kLpThreads / kFine)] = most;
+    } else if (a.k > 0) {
+      most = max(most, __shfl_xor_sync(0xffffffffu, most, kLpThreads / kFine));
+      if (lane % (kLpThreads / kCoarse) == 0) s_group[tid / (kLpThreads / kCoarse)] = most;
+    }
     most = __reduce_max_sync(0xffffffffu, most);
     if (lane == 0) s_top[warp] = most ? key_value(most) : kNegInf;
     if (tid == 0) s_count = 0;
@@ -309,11 +318,26 @@ __global__ void __launch_bounds__(kLpThreads, 1024 / kLpThreads + 1024 / kLpThre
   }
   if (a.k > 0) {
     // threads that may hold one of the CTA's k best: those whose maximum reaches the k-th largest group's
-    const uint32_t mine = s_group[lane];
-    int larger = 0;
+    const uint32_t ga = s_group[lane];
+    uint32_t least;
+    int la = 0;  // larger groups
 #pragma unroll
-    for (int q = 0; q < kGroups; ++q) larger += s_group[q] > mine;
-    const uint32_t least = __reduce_min_sync(0xffffffffu, larger < a.k ? mine : 0xffffffffu);
+    for (int q = 0; q < kCoarse; ++q) la += s_group[q] > ga;
+    if (a.k > kFineFrom) {
+      const uint32_t gb = s_group[kWarp + lane];
+      int lb = 0;
+#pragma unroll
+      for (int q = 0; q < kCoarse; ++q) lb += s_group[q] > gb;
+#pragma unroll
+      for (int q = kCoarse; q < kFine; ++q) {
+        const uint32_t o = s_group[q];
+        la += o > ga, lb += o > gb;
+      }
+      least = lb < a.k ? gb : 0xffffffffu;
+    } else {
+      least = 0xffffffffu;
+    }
+    least = __reduce_min_sync(0xffffffffu, min(least, la < a.k ? ga : 0xffffffffu));
     const uint32_t ball = __ballot_sync(0xffffffffu, my_key >= least && my_key != 0u);
     if (lane == 0) s_mask[warp] = ball;
     __syncthreads();
