@@ -76,13 +76,14 @@ NS_API ns_status ns_attend_prompt(const void *d_q, const void *d_k, const void *
  * where bit j of d_mask[b * n + i] is set; d_mask NULL means j <= i (a chain).
  * A row that sees nothing (len 0, or an empty mask and no context) gives
  * zeros and an lse of -inf.
- *   d_q    [n_seqs x n x q_heads x dim], strides in elements (multiples of 8)
+ *   d_q    [n_seqs x n x q_heads x dim], strides in elements (even; with positive multiples of 8 and 16-byte
+ *          alignment more than 16 rows, n * q_heads / kv_heads, are faster)
  *   d_k, d_v  [n_pages x kv_heads x page_size x dim] of one layer, strides in
  *          elements (multiples of 8): page, head, token
  *   d_mask int64 [n_seqs x n] or NULL
  *   max_len  HOST: a bound on the lengths, used only to size the launch (0:
  *          table_ld * page_size); results do not depend on it
- *   d_out  [n_seqs x n x q_heads x dim] contiguous, d_lse fp32 [n_seqs x n x q_heads] or NULL
+ *   d_out  [n_seqs x n x q_heads x dim] contiguous, 16-byte aligned, d_lse fp32 [n_seqs x n x q_heads] or NULL
  *   d_ws   device workspace of ns_attend_paged_workspace(...) bytes, 16-byte
  *          aligned, contents immaterial
  * 1 <= n <= NS_MAX_NEW, dim 64 or 128, page_size a power of two from 8 to 1024.

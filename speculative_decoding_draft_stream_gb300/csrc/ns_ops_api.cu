@@ -133,7 +133,7 @@ ns_status ns_attend_paged(const void *d_q, int32_t dtype, int32_t n_seqs, int32_
     return NS_ERR_ARG;
   if (n_seqs == 0) return NS_OK;
   if (!d_q || !d_k || !d_v || !d_table || !d_lengths || !d_seqs || !d_out || !d_ws || !aligned(d_q, 4) ||
-      !aligned(d_k, 16) || !aligned(d_v, 16) || !aligned(d_out, 4) || !aligned(d_lse, 4) || !aligned(d_table, 4) ||
+      !aligned(d_k, 16) || !aligned(d_v, 16) || !aligned(d_out, 16) || !aligned(d_lse, 4) || !aligned(d_table, 4) ||
       !aligned(d_lengths, 4) || !aligned(d_seqs, 4) || !aligned(d_mask, 8) || !aligned(d_ws, 16) || q_seq % 2 ||
       q_token % 2 || q_head % 2 || !by8(k_page) || !by8(k_head) || !by8(k_token) || !by8(v_page) || !by8(v_head) ||
       !by8(v_token))

@@ -59,7 +59,7 @@ def test_prompt_of_nothing_is_done(lib, kw):
     dict(page=4), dict(page=24), dict(page=2048), dict(ld=0), dict(seqs=0), dict(ld=1 << 27), dict(most=-1),
     dict(scale=0.0), dict(scale=float("nan")), dict(q=None), dict(k=None), dict(v=None), dict(table=None),
     dict(lengths=None), dict(ids=None), dict(out=None), dict(ws=None), dict(q=18), dict(k=24), dict(v=24),
-    dict(mask=20), dict(ws=24), dict(lse=18), dict(qs=511), dict(qt=3), dict(qh=1), dict(kp=2049), dict(kh=4),
+    dict(mask=20), dict(ws=24), dict(lse=18), dict(out=18), dict(out=20), dict(out=24), dict(qs=511), dict(qt=3), dict(qh=1), dict(kp=2049), dict(kh=4),
     dict(kt=2), dict(vp=12), dict(vh=12), dict(vt=12),
 ])
 def test_paged_refuses(lib, kw):
