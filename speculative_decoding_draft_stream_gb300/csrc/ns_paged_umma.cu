@@ -228,20 +228,26 @@ struct Mode {
 };
 
 // Joins the parts of an item that several CTAs had: a CTA has 32 of its rows,
-// a lane one of them, a warp an eighth of the columns.  The parts' loads are
-// what it waits for, so two parts are on their way at a time: with one, two
-// or four, a whole call takes 66.0, 49.1, 45.5 us for one sequence of 30000
-// tokens (hundreds of parts), 55.2, 55.7, 59.1 us for 16 of 512 to 4096
-// (two or three parts; fewer of its CTAs fit on an SM).
+// a lane one of them.  What it waits for are the parts' loads.  G = 1: a warp
+// has an eighth of the columns and reads two parts at a time.  G = 8: the
+// warps take the parts of 32 columns in turns and add up in warp order.  By
+// the number of parts (launch has the rule), a whole call took, G = 1 and 8:
+// 16 sequences of 512 to 4096 tokens (two or three parts) 55.7, 69.3 us; 4 of
+// 2300 (five) 24.6, 27.0; 2 of 1754 (nine) 17.2, 16.1; one of 30000 (38)
+// 49.1, 35.6 us.
 constexpr int kJoinThreads = 256;
-template <typename T, int D>
+template <typename T, int D, int G>
 __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const TreeArgs a, int ctas) {
-  constexpr int N = D / 8, kPitch = D / 2 + 4;  // words of a row: its 16-byte pieces fall into different banks
-  extern __shared__ int s_part[];               // [ctas] places of the parts
+  constexpr int N = G == 1 ? D / 8 : 32, kCols = 8 / G * N;  // columns of a warp, of the CTA
+  constexpr int kAhead = G == 1 ? 2 : 1;
+  constexpr int kPitch = kCols / 2 + 4;  // words of a row: its 16-byte pieces fall into different banks
+  extern __shared__ int s_part[];        // [ctas] places of the parts
+  __shared__ float s_sum[G > 1 ? G - 1 : 1][G > 1 ? N + 1 : 1][32];
   __shared__ __align__(16) uint32_t s_out[32 * kPitch];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, grp = warp % G;
   const int items = a.units * a.blocks, b = blockIdx.x / items, item = blockIdx.x % items;
   const int rl = blockIdx.y * 32 + lane, in_tile = (rl & 127) / a.pack;
+  const int c_warp = warp / G * N, col0 = blockIdx.z * kCols;  // the warp's columns in the CTA's, the CTA's in the row
   const int node = (item % a.blocks * 2 + (rl >> 7)) * a.per_tile + in_tile;
   const bool live = in_tile < a.per_tile && node < a.n;
   const int64_t at = ((int64_t)b * a.n + node) * a.q_heads + item / a.blocks * a.pack + (rl & 127) % a.pack;
@@ -266,15 +272,14 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const TreeArgs 
   for (int q = 0; q < parts; ++q)
     if (s_part[q] >= 0) m = fmaxf(m, a.part_ml[s_part[q] * 256 + rl].x);
   const float safe = m == kNegInf ? 0.f : m;
-  constexpr int kAhead = 2;
-  for (int q0 = 0; q0 < parts; q0 += kAhead) {
+  for (int q0 = grp; q0 < parts; q0 += G * kAhead) {
     float x[kAhead][N];
     float2 ml[kAhead];
 #pragma unroll
     for (int e = 0; e < kAhead; ++e) {
-      const int part = q0 + e < parts ? s_part[q0 + e] : -1;
+      const int part = q0 + e * G < parts ? s_part[q0 + e * G] : -1;
       ml[e] = part >= 0 ? a.part_ml[part * 256 + rl] : make_float2(kNegInf, 0.f);
-      const float *src = a.part_o + ((int64_t)part * D + warp * N) * 256 + rl;
+      const float *src = a.part_o + ((int64_t)part * D + col0 + c_warp) * 256 + rl;
 #pragma unroll
       for (int i = 0; i < N; ++i) x[e][i] = part >= 0 ? src[i * 256] : 0.f;
     }
@@ -286,22 +291,41 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const TreeArgs 
       for (int i = 0; i < N; ++i) o[i] = fmaf(x[e][i], f, o[i]);
     }
   }
+  if constexpr (G > 1) {
+    if (grp > 0 && grp < parts) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) s_sum[grp - 1][i][lane] = o[i];
+      s_sum[grp - 1][N][lane] = l;
+    }
+    __syncthreads();
+    if (grp > 0) return;
+    for (int w = 1; w < min(parts, G); ++w) {
+      l += s_sum[w - 1][N][lane];
+#pragma unroll
+      for (int i = 0; i < N; ++i) o[i] += s_sum[w - 1][i][lane];
+    }
+  }
   const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
   for (int i = 0; i < N; i += 8)
-    *reinterpret_cast<uint4 *>(s_out + lane * kPitch + (warp * N + i) / 2) =
+    *reinterpret_cast<uint4 *>(s_out + lane * kPitch + (c_warp + i) / 2) =
         make_uint4(attn::Type<T>::pack(o[i] * inv, o[i + 1] * inv), attn::Type<T>::pack(o[i + 2] * inv, o[i + 3] * inv),
                    attn::Type<T>::pack(o[i + 4] * inv, o[i + 5] * inv),
                    attn::Type<T>::pack(o[i + 6] * inv, o[i + 7] * inv));
-  if (live && warp == 0 && a.lse) a.lse[at] = l == 0.f ? kNegInf : (m - fa::kOffset<T> + log2f(l)) * attn::kLn2;
-  __syncthreads();
+  if (live && col0 + c_warp == 0 && a.lse)
+    a.lse[at] = l == 0.f ? kNegInf : (m - fa::kOffset<T> + log2f(l)) * attn::kLn2;
+  if (G == 1)
+    __syncthreads();
+  else
+    __syncwarp();  // one warp is left
   const long long mine = live ? at : -1;
+  constexpr int kLeft = kJoinThreads / G;
 #pragma unroll
-  for (int e = 0; e < 32 * D / 8 / kJoinThreads; ++e) {
-    const int x = e * kJoinThreads + tid, r = x / (D / 8), c = x % (D / 8);
+  for (int e = 0; e < 32 * kCols / 8 / kLeft; ++e) {
+    const int x = e * kLeft + tid, r = x / (kCols / 8), c = x % (kCols / 8);
     const long long row = __shfl_sync(0xffffffffu, mine, r);
     if (row >= 0)
-      *reinterpret_cast<uint4 *>(static_cast<T *>(a.out) + row * D + c * 8) =
+      *reinterpret_cast<uint4 *>(static_cast<T *>(a.out) + row * D + col0 + c * 8) =
           *reinterpret_cast<const uint4 *>(s_out + r * kPitch + c * 4);
   }
 }
@@ -311,7 +335,9 @@ cudaError_t launch(const PagedAttnArgs &p, int sms, cudaStream_t st) {
   TreeArgs a{};
   a.table = p.table, a.lengths = p.lengths, a.seqs = p.seqs, a.mask = p.mask;
   a.n_seqs = p.n_seqs, a.n = p.n, a.q_heads = p.q_heads, a.group = p.group;
-  a.pack = p.group <= 32 ? p.group : 1;
+  // All heads of a group in one tile, so that its keys are fetched once: 8 sequences of 2300 tokens, 4 new ones, group
+  // 33 (64): 58.7 (104.9) us with a head to a tile, 20.4 (20.6) us so.
+  a.pack = p.group <= 128 ? p.group : 1;
   a.per_tile = 128 / a.pack, a.units = p.q_heads / a.pack;
   a.blocks = (p.n + 2 * a.per_tile - 1) / (2 * a.per_tile);
   a.page_shift = p.page_shift, a.table_ld = p.table_ld, a.max_seqs = p.max_seqs, a.n_pages = p.n_pages;
@@ -338,7 +364,9 @@ cudaError_t launch(const PagedAttnArgs &p, int sms, cudaStream_t st) {
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)((long long)p.n_seqs * items), 8);
+  // an item's parts: some more than its share of the CTAs, if the sequences are of like lengths
+  const bool many = ctas >= 6LL * p.n_seqs * items;
+  cfg.gridDim = dim3((unsigned)((long long)p.n_seqs * items), 8, many ? D / 32 : 1);
   cfg.blockDim = dim3(kJoinThreads);
   cfg.dynamicSmemBytes = ctas * 4;
   cfg.stream = st;
@@ -347,7 +375,8 @@ cudaError_t launch(const PagedAttnArgs &p, int sms, cudaStream_t st) {
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, tree_join_kernel<T, D>, a, ctas);
+  return many ? cudaLaunchKernelEx(&cfg, tree_join_kernel<T, D, 8>, a, ctas)
+              : cudaLaunchKernelEx(&cfg, tree_join_kernel<T, D, 1>, a, ctas);
 }
 
 }  // namespace

@@ -633,3 +633,10 @@ def test_prompt_wild_values_late_in_long_sequences(ns, d):
             bad = torch.isnan(o)
             assert not torch.isfinite(out[a:b, h][bad]).any()
             check(out[a:b, h].double().masked_fill(bad, 0), o.masked_fill(bad, 0), to, "rows that see none")
+
+
+@pytest.mark.parametrize("group", [40, 65, 100, 128, 129])
+def test_paged_large_groups(ns, group):
+    """Query heads that share a key-value head: up to 128 of them are rows of one tile."""
+    run_paged(ns, [30, 400, 0, 129], 1, group, 1, 64, 16, BF16, group)
+    run_paged(ns, [33, 500], 7, 2 * group, 2, 128, 32, F16, group, masks="tree")
