@@ -177,7 +177,12 @@ cudaError_t launch(const PromptAttnArgs &p, int sms, cudaStream_t st) {
   a.cu = p.cu, a.tokens = p.tokens, a.n_seqs = p.n_seqs, a.max_len = p.max_len;
   a.q_heads = p.q_heads, a.group = p.group;
   // heads packed into a row tile: all of a group's, up to 32 (then at most a fifth of the rows is left over)
-  a.pack = p.group <= 32 ? p.group : 1;
+  // The heads of a group in one tile of 128 / group tokens, or a tile of 128 tokens for each head.  The first leaves
+  // fewer of the products behind the diagonal: 16 sequences of 130 to 2047 tokens, 28 heads on 4: 146.5 us, 168.2 with
+  // a head to a tile; 32 on 2 181.8, 213.0.  But its few tokens have many rows of queries, keys of the same tiles for
+  // every CTA, and no more items: one sequence of 2000 tokens with 8 heads on 1 takes 30.1, 29.6 us; 16 on 1 41.6,
+  // 30.7; 32 on 1 77.8, 36.3; 64 on 1 148.5, 64.4.
+  a.pack = p.group <= 8 || (p.group <= 32 && p.n_seqs >= 8) ? p.group : 1;
   a.per_tile = 128 / a.pack, a.units = p.q_heads / a.pack;
   a.c = p.scale * attn::kLog2e;
   a.out = p.out, a.lse = p.lse, a.err = p.err;
