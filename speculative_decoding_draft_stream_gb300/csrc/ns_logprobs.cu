@@ -21,8 +21,10 @@
 // triples and lists through distributed shared memory: one launch, no
 // workspace, and a fixed order of every sum.
 //
-// What bounds it: HBM for many rows (each logit crosses it once); for a few
-// rows, latency (one wave of loads, the joins).
+// What bounds it: HBM for many rows (each logit crosses it once): 2048 rows of
+// 152064 in bf16 take 124 us, 5.0 TB/s; the exponentials and sums that hide
+// behind the loads are the rest.  For a few rows, latency (one wave of loads,
+// the joins): one row of 128256 in fp32 takes 10 us, 60 rows 12.5 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -36,10 +38,10 @@ namespace {
 constexpr int kLpVecs = 4;        // 16-byte loads a thread keeps in flight
 constexpr int kLpMaxCluster = 8;  // portable cluster size
 constexpr int kLpMinSlice = 4096; // least logits of a CTA of a split row
-// Above 16 alternatives, 64 groups instead of 32: 32 groups' least maximum
-// lets a third of the threads through. 126 fp32 rows of 128256, k 32: 76 ->
+// Above 16 alternatives (kMany), 64 groups instead of 32: 32 groups' least
+// maximum lets a third of the threads through. 126 fp32 rows of 128256, k 32: 76 ->
 // 24 us; 298 bf16 rows, k 31: 41 -> 28; k 17: 27.5 -> 25.0; but k 14: 17.0 -> 17.9.
-constexpr int kFineFrom = 16;
+constexpr int kManyFrom = 17;
 constexpr int kLpBuffer = kLpMaxCluster * NS_MAX_ALTERNATIVES;  // candidates of a CTA, or the lists of a cluster
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -215,14 +217,14 @@ __device__ __forceinline__ void place_best(const unsigned long long *s, int n, i
 // row's 16-byte pieces are counted from the aligned address at or before its
 // first logit; the pieces at its ends may be partly outside and are read
 // value by value.
-template <typename T, bool kSplit, int kLpThreads>
+template <typename T, bool kSplit, bool kMany, int kLpThreads>
 __global__ void __launch_bounds__(kLpThreads, 1024 / kLpThreads + 1024 / kLpThreads / 4)
     logprob_kernel(const LogprobArgs a, int split) {
   constexpr int kLpWarps = kLpThreads / kWarp;
   using V = Vec<T>;
   constexpr int N = V::N;
-  constexpr int kFine = 64, kCoarse = 32;  // groups of threads
-  __shared__ uint32_t s_group[kFine];
+  constexpr int kGroups = kMany ? 64 : 32, kGroup = kLpThreads / kGroups;  // groups of threads
+  __shared__ uint32_t s_group[kGroups];
   __shared__ float s_top[kLpWarps];
   __shared__ float2 s_sums[kLpWarps];
   __shared__ uint32_t s_mask[kLpWarps];
@@ -292,13 +294,8 @@ __global__ void __launch_bounds__(kLpThreads, 1024 / kLpThreads + 1024 / kLpThre
   {
     uint32_t most = my_key;
 #pragma unroll
-    for (int off = kLpThreads / kFine / 2; off > 0; off >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, off));
-    if (a.k > kFineFrom) {
-      if (lane % (kLpThreads / kFine) == 0) s_group[tid / (kLpThreads / kFine)] = most;
-    } else if (a.k > 0) {
-      most = max(most, __shfl_xor_sync(0xffffffffu, most, kLpThreads / kFine));
-      if (lane % (kLpThreads / kCoarse) == 0) s_group[tid / (kLpThreads / kCoarse)] = most;
-    }
+    for (int off = kGroup / 2; off > 0; off >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, off));
+    if (a.k > 0 && lane % kGroup == 0) s_group[tid / kGroup] = most;
     most = __reduce_max_sync(0xffffffffu, most);
     if (lane == 0) s_top[warp] = most ? key_value(most) : kNegInf;
     if (tid == 0) s_count = 0;
@@ -318,26 +315,17 @@ __global__ void __launch_bounds__(kLpThreads, 1024 / kLpThreads + 1024 / kLpThre
   }
   if (a.k > 0) {
     // threads that may hold one of the CTA's k best: those whose maximum reaches the k-th largest group's
-    const uint32_t ga = s_group[lane];
-    uint32_t least;
-    int la = 0;  // larger groups
+    const uint32_t ga = s_group[lane], gb = kMany ? s_group[lane + kWarp * kMany] : 0u;
+    int la = 0, lb = 0;  // larger groups than each
 #pragma unroll
-    for (int q = 0; q < kCoarse; ++q) la += s_group[q] > ga;
-    if (a.k > kFineFrom) {
-      const uint32_t gb = s_group[kWarp + lane];
-      int lb = 0;
-#pragma unroll
-      for (int q = 0; q < kCoarse; ++q) lb += s_group[q] > gb;
-#pragma unroll
-      for (int q = kCoarse; q < kFine; ++q) {
-        const uint32_t o = s_group[q];
-        la += o > ga, lb += o > gb;
-      }
-      least = lb < a.k ? gb : 0xffffffffu;
-    } else {
-      least = 0xffffffffu;
+    for (int q = 0; q < kGroups; ++q) {
+      const uint32_t o = s_group[q];
+      la += o > ga;
+      if (kMany) lb += o > gb;
     }
-    least = __reduce_min_sync(0xffffffffu, min(least, la < a.k ? ga : 0xffffffffu));
+    uint32_t least = la < a.k ? ga : 0xffffffffu;
+    if (kMany && lb < a.k) least = min(least, gb);
+    least = __reduce_min_sync(0xffffffffu, least);
     const uint32_t ball = __ballot_sync(0xffffffffu, my_key >= least && my_key != 0u);
     if (lane == 0) s_mask[warp] = ball;
     __syncthreads();
@@ -464,17 +452,19 @@ __global__ void __launch_bounds__(kLpThreads, 1024 / kLpThreads + 1024 / kLpThre
 }
 
 // A row is split while the call has fewer than two CTAs for each SM and every
-// CTA keeps kLpMinSlice logits: one row of 128256 fp32 logits takes XX us on 8
-// CTAs, YY on 2; 60 rows of 151936 ZZ us on 4 each, WW on 8.
+// CTA keeps kLpMinSlice logits: one row of 128256 fp32 logits takes 8.6 us on 8
+// CTAs, 11.9 on 2; 60 rows of 151936 10.5 us on 4 each, 11.7 on 8, 13.1 on 2.
+// Threads of a CTA: 512 or 1024 took 27 to 55 us for those 60 rows with 10
+// alternatives (12.5 with 256): the joins wait for more warps.
 constexpr int kLpThreads = 256;
 
-template <typename T>
+template <typename T, bool kMany>
 cudaError_t launch(const LogprobArgs &a, int sms, cudaStream_t st) {
   int split = 1;
   while (split < kLpMaxCluster && (long long)a.rows * split * 2 <= 2LL * sms && a.V / (2 * split) >= kLpMinSlice)
     split *= 2;
   if (split == 1) {
-    logprob_kernel<T, false, kLpThreads><<<a.rows, kLpThreads, 0, st>>>(a, 1);
+    logprob_kernel<T, false, kMany, kLpThreads><<<a.rows, kLpThreads, 0, st>>>(a, 1);
     return cudaGetLastError();
   }
   cudaLaunchConfig_t cfg{};
@@ -487,15 +477,19 @@ cudaError_t launch(const LogprobArgs &a, int sms, cudaStream_t st) {
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, logprob_kernel<T, true, kLpThreads>, a, split);
+  return cudaLaunchKernelEx(&cfg, logprob_kernel<T, true, kMany, kLpThreads>, a, split);
+}
+template <typename T>
+cudaError_t by_k(const LogprobArgs &a, int sms, cudaStream_t st) {
+  return a.k >= kManyFrom ? launch<T, true>(a, sms, st) : launch<T, false>(a, sms, st);
 }
 
 }  // namespace
 
 cudaError_t launch_logprobs(const LogprobArgs &a, int dtype, int sms, cudaStream_t st) {
-  if (dtype == NS_DTYPE_F32) return launch<float>(a, sms, st);
-  if (dtype == NS_DTYPE_BF16) return launch<__nv_bfloat16>(a, sms, st);
-  return launch<__half>(a, sms, st);
+  if (dtype == NS_DTYPE_F32) return by_k<float>(a, sms, st);
+  if (dtype == NS_DTYPE_BF16) return by_k<__nv_bfloat16>(a, sms, st);
+  return by_k<__half>(a, sms, st);
 }
 
 }  // namespace ns

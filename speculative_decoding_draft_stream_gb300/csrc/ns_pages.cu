@@ -6,8 +6,13 @@
 // first, so a sequence of calls always gives the same table.
 //
 // Bookkeeping kernels are latency-bound (a few dependent loads of a few
-// words); the data movers are bound by HBM: each row is read and written once
-// with 16-byte accesses, several per lane in flight.
+// words): 2.5 to 3.5 us each in a graph, launched into each other's ends.  The
+// data movers are bound by HBM: each row is read and written once with
+// 16-byte accesses, several per lane in flight.  16 sequences that give up
+// their last step, append 60 nodes and keep 5 of them in 16 layers take 21 us
+// for five calls; 64 children with their 64 MB of copied last pages 37 us;
+// 8 sequences of 4001 new rows of which every second stays in 12 layers 168 us
+// (393 MB read and 332 MB written by the compaction: 126 us of it).
 #include "ns_internal.cuh"
 #include "ns_ops.cuh"
 
