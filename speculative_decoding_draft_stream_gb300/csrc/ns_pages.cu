@@ -10,7 +10,7 @@
 // data movers are bound by HBM: each row is read and written once with
 // 16-byte accesses, several per lane in flight.  16 sequences that give up
 // their last step, append 60 nodes and keep 5 of them in 16 layers take 21 us
-// for five calls; 64 children with their 64 MB of copied last pages 37 us;
+// for four calls; 64 children with their 64 MB of copied last pages 37 us;
 // 8 sequences of 4001 new rows of which every second stays in 12 layers 168 us
 // (393 MB read and 332 MB written by the compaction: 126 us of it).
 #include "ns_internal.cuh"
@@ -21,6 +21,7 @@ namespace {
 
 constexpr int kSeqThreads = 128;      // truncate, fork: one CTA per sequence
 constexpr int kExtendThreads = 1024;  // extend: one CTA
+constexpr int kListHere = 2048;        // given pages that extend lists in shared memory
 constexpr int kMoveThreads = 256;
 constexpr int kMoveWarps = kMoveThreads / kWarp;
 constexpr int kUnroll = 8;  // 16-byte loads a lane keeps in flight in the movers
@@ -32,8 +33,9 @@ __device__ __forceinline__ void wait_for_previous() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 template <typename... P, typename... A>
-cudaError_t launch(void (*kernel)(P...), dim3 grid, int threads, cudaStream_t st, A... args) {
+cudaError_t launch(void (*kernel)(P...), dim3 grid, int threads, int smem, cudaStream_t st, A... args) {
   cudaLaunchConfig_t cfg{};
+  cfg.dynamicSmemBytes = smem;
   cfg.gridDim = grid;
   cfg.blockDim = dim3((unsigned)threads);
   cfg.stream = st;
@@ -153,15 +155,23 @@ struct ExtendWs {
   }
 };
 
+constexpr int extend_smem(int n) { return ((n <= kExtendThreads ? 5 * n : n) + kListHere) * 4; }
+static_assert(extend_smem(NS_MAX_PAGE_SEQS) <= 47 * 1024, "shared memory without opting in");
+
 // One CTA: what each sequence needs (a scan over the call's order), then the
 // lowest free pages (a scan over the counts, which ends once there are
-// enough), then the table rows, one warp per sequence.
+// enough), then the table rows, one warp per sequence.  What it takes is its
+// chain of dependent loads (ids, lengths, last pages, their counts), so what
+// the threads tell each other stays in shared memory where it fits (up to
+// kExtendThreads sequences, kListHere pages), and in the workspace otherwise.
 __global__ void __launch_bounds__(kExtendThreads) extend_kernel(ns_kv_pages c, const int32_t *seqs,
                                                                 const int32_t *n_new, int n, void *ws,
                                                                 uint32_t *err) {
   __shared__ int sh[kExtendThreads / kWarp];
-  __shared__ int s_ids[NS_MAX_PAGE_SEQS];
-  const ExtendWs w(ws, n);
+  extern __shared__ int s_ids[];  // [n], then (extend_smem) start, first, count, shared [n] and the list
+  ExtendWs w(ws, n);
+  const bool here = n <= kExtendThreads;
+  if (here) w.start = s_ids + n, w.first = w.start + n, w.count = w.first + n, w.shared = w.count + n;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   wait_for_previous();
   // the first pages' counts, on their way while the needs are found
@@ -173,15 +183,19 @@ __global__ void __launch_bounds__(kExtendThreads) extend_kernel(ns_kv_pages c, c
   __syncthreads();
 
   long long total = 0;  // pages wanted; may pass 32 bits only where it is refused below
-  int copies = 0;
+  int copies = 0, grown = 0, before = 0;  // (the new length, and the copies before this sequence's, when `here`)
   for (int i0 = 0; i0 < n; i0 += kExtendThreads) {
     const int i = i0 + tid;
     int count = 0, first = -1, shared = -1;
     if (i < n) {
       const int s = s_ids[i], add = n_new[i];
-      bool ok = seq_ok(c, s) && add >= 0;
-      for (int j = 0; j < i && ok; ++j) ok = s_ids[j] != s;
+      bool ok = seq_ok(c, s);
       const int len = ok ? c.lengths[s] : 0;
+      int again = 0;  // (while the length is on its way)
+#pragma unroll 8
+      for (int j = 0; j < i; ++j) again |= s_ids[j] == s;
+      ok = ok && add >= 0 && !again;
+      grown = (int)min((long long)len + add, 0x7fffffffLL);
       ok = ok && len_ok(c, len) && (long long)len + add <= (long long)c.table_ld * c.page_size;
       if (ok) {
         first = pages_for(len, c.page_size);
@@ -205,6 +219,7 @@ __global__ void __launch_bounds__(kExtendThreads) extend_kernel(ns_kv_pages c, c
     int sum, csum;
     const int off = block_exclusive_scan(count, sh, &sum);
     const int coff = block_exclusive_scan(shared >= 0 ? 1 : 0, sh, &csum);
+    before = coff;
     if (i < n) {
       // start saturates: a call that wants more pages than exist is refused
       w.start[i] = total + off > 0x3fffffffLL ? 0x3fffffff : (int)(total + off);
@@ -219,6 +234,7 @@ __global__ void __launch_bounds__(kExtendThreads) extend_kernel(ns_kv_pages c, c
 
   // the `total` lowest free pages, in order
   bool enough = total <= c.pages;
+  if (total <= kListHere) w.list = s_ids + (here ? 5 * n : n);
   int found = 0;
   if (enough && total > 0) {
     for (int p0 = 0; p0 < c.pages && found < total; p0 += kExtendThreads * kPer) {
@@ -250,11 +266,11 @@ __global__ void __launch_bounds__(kExtendThreads) extend_kernel(ns_kv_pages c, c
   int done = 0;  // copies of the chunks before
   for (int i0 = 0; i0 < n; i0 += kExtendThreads) {
     const int i = i0 + tid;
-    int csum;
-    const int coff = block_exclusive_scan(i < n && w.shared[i] >= 0 ? 1 : 0, sh, &csum);
+    int csum = 0;
+    const int coff = here ? before : block_exclusive_scan(i < n && w.shared[i] >= 0 ? 1 : 0, sh, &csum);
     if (i < n && w.first[i] >= 0) {
       const int s = s_ids[i];
-      c.lengths[s] += n_new[i];
+      c.lengths[s] = here ? grown : c.lengths[s] + n_new[i];
       if (w.shared[i] >= 0) {
         w.dst[done + coff] = w.list[w.start[i]];
         atomicSub(c.refs + w.shared[i], 1);
@@ -479,29 +495,29 @@ unsigned grid_for(long long items, long long most) {
 
 cudaError_t launch_pages_truncate(const ns_kv_pages &c, const int32_t *seqs, const int32_t *new_len, int n,
                                   uint32_t *err, cudaStream_t st) {
-  return launch(truncate_kernel, dim3(n), kSeqThreads, st, c, seqs, new_len, nullptr, 0x7fffffff, err);
+  return launch(truncate_kernel, dim3(n), kSeqThreads, 0, st, c, seqs, new_len, nullptr, 0x7fffffff, err);
 }
 
 cudaError_t launch_pages_fork(const ns_kv_pages &c, const int32_t *src, const int32_t *dst, int n, uint32_t *err,
                               cudaStream_t st) {
-  return launch(fork_kernel, dim3(n), kSeqThreads, st, c, src, dst, n, err);
+  return launch(fork_kernel, dim3(n), kSeqThreads, 0, st, c, src, dst, n, err);
 }
 
 int64_t pages_extend_ws(const ns_kv_pages &c, int n) { return 4 * (4 + 6 * (int64_t)n + c.pages); }
 
 cudaError_t launch_pages_extend(const ns_kv_pages &c, const int32_t *seqs, const int32_t *n_new, int n, void *ws,
                                 uint32_t *err, cudaStream_t st) {
-  cudaError_t e = launch(extend_kernel, dim3(1), kExtendThreads, st, c, seqs, n_new, n, ws, err);
+  cudaError_t e = launch(extend_kernel, dim3(1), kExtendThreads, extend_smem(n), st, c, seqs, n_new, n, ws, err);
   if (e != cudaSuccess) return e;
   const ExtendWs w(ws, n);
   const unsigned grid = grid_for((long long)n * c.layers * c.heads * 2, 2432);
-  return launch(copy_pages_kernel, dim3(grid), kMoveThreads, st, c, w.src, w.dst, w.n_copies, n, err);
+  return launch(copy_pages_kernel, dim3(grid), kMoveThreads, 0, st, c, w.src, w.dst, w.n_copies, n, err);
 }
 
 cudaError_t launch_pages_write(const ns_kv_pages &c, int layer, const int32_t *seqs, const int32_t *cu, int n,
                                const void *k_new, const void *v_new, int64_t k_token, int64_t k_head,
                                int64_t v_token, int64_t v_head, int tokens, uint32_t *err, cudaStream_t st) {
-  return launch(write_kernel, dim3((tokens + kMoveWarps - 1) / kMoveWarps), kMoveThreads, st, c, layer, seqs, cu, n,
+  return launch(write_kernel, dim3((tokens + kMoveWarps - 1) / kMoveWarps), kMoveThreads, 0, st, c, layer, seqs, cu, n,
                 k_new, v_new, k_token, k_head, v_token, v_head, tokens, err);
 }
 
@@ -519,17 +535,17 @@ cudaError_t launch_pages_compact(const ns_kv_pages &c, const int32_t *seqs, cons
   if (units > 0x7fffffffLL - kMoverWarps) return cudaErrorInvalidValue;
   if (keep_ld > 0) {
     const dim3 grid((unsigned)((units + kMoverWarps - 1) / kMoverWarps), 2, (unsigned)n);
-    cudaError_t e = launch(compact_kernel, grid, kMoverWarps * 32, st, c, seqs, base, keep, keep_ld, n_keep,
+    cudaError_t e = launch(compact_kernel, grid, kMoverWarps * 32, 0, st, c, seqs, base, keep, keep_ld, n_keep,
                            seg_bytes, err);
     if (e != cudaSuccess) return e;
   }
-  return launch(truncate_kernel, dim3(n), kSeqThreads, st, c, seqs, n_keep, base, keep_ld, err);
+  return launch(truncate_kernel, dim3(n), kSeqThreads, 0, st, c, seqs, n_keep, base, keep_ld, err);
 }
 
 cudaError_t launch_pages_copy(const ns_kv_pages &c, const int32_t *src, const int32_t *dst, int n, uint32_t *err,
                               cudaStream_t st) {
   const dim3 grid(grid_for((long long)n * c.layers * c.heads * 2, 2432));
-  return launch(copy_pages_kernel, grid, kMoveThreads, st, c, src, dst, nullptr, n, err);
+  return launch(copy_pages_kernel, grid, kMoveThreads, 0, st, c, src, dst, nullptr, n, err);
 }
 
 }  // namespace ns

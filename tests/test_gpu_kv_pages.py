@@ -302,3 +302,29 @@ def test_refusals(ns):
     c.truncate(i32([]))
     c.extend(i32([]), i32([]))
     assert ns.ops_error() == 0
+
+
+@pytest.mark.parametrize("n", [1023, 1024, 1025, 2100])
+def test_many_sequences_and_pages_in_one_extend(ns, n):
+    """Around the number of sequences, and of given pages, whose bookkeeping one CTA keeps in shared memory."""
+    b = Both(ns, 1, 4 * n + 40, 1, 2, 8, 2 * n, 4)
+    rng = random.Random(n)
+    first = list(range(n))
+    rng.shuffle(first)
+    b.extend(first, [rng.choice([0, 1, 2, 3, 3]) for _ in first])
+    b.same()
+    b.fork(list(range(n)), list(range(n, 2 * n)))
+    some = rng.sample(range(2 * n), n)
+    b.extend(some, [rng.choice([0, 1, 1, 2, 4]) for _ in some])  # copies of shared last pages among them
+    b.same()
+    again = some[: n // 2]
+    b.c.extend(i32(again + again[:3]), i32([1] * (len(again) + 3)))  # the last three are repeated, and skipped
+    b.r.extend(again, [1] * len(again))
+    b.same(ns.FLAG_BAD_SEQ)
+
+
+def test_many_pages_for_one_sequence(ns):
+    for want in (2047, 2048, 2049, 9000):
+        b = Both(ns, 1, 9100, 1, 1, 8, 2, 9050)
+        b.extend([1, 0], [37, want - 37])
+        b.same()
