@@ -142,7 +142,7 @@ struct Mode {
   using Args = TreeArgs;
   using Work = TreeWork;
   using Dealer = TreeDealer;
-  static constexpr bool kParts = true;
+  static constexpr bool kParts = true, kSplit = false;
   static constexpr int kStageRow = 64;
 
   struct Loader {

@@ -1,8 +1,10 @@
 // Causal attention over whole packed prompts, on the 5th-generation tensor
 // cores (ns_umma_attn.cuh has the kernel).
 //
-// An item is 2 * (128 / group) consecutive tokens of one sequence, all query
-// heads of one key-value head, and the keys up to its last token.  Items are
+// An item is two tiles of 128 rows of one sequence and the keys up to its last
+// token: 2 * (128 / group) consecutive tokens of all query heads of one
+// key-value head, or 256 tokens of one head; in calls of few items, one tile
+// of one head with its keys split in two (launch has the rules).  Items are
 // dealt longest first, so that the CTAs end together.  A row sees the keys up
 // to its own token; what lies behind it in the item's last tiles are later
 // tokens and the next sequence's.
@@ -11,7 +13,10 @@
 // on 8, 1.40 ms.  For batches of shorter ones each item's start and end, where
 // only one of softmax and products runs, are a third: 16 sequences of 130 to
 // 2047 tokens, 28 heads on 4, 147 us, 1.02 PFLOP/s.  A few short ones are
-// latency: four of up to 200 tokens, 12 heads on 4 of 64 columns, 9.0 us.
+// latency: four of up to 200 tokens, 12 heads on 4 of 64 columns, 8.0 us; one
+// of 1967 tokens, 8 heads, 21 us (16 key tiles one after the other: 30 us).
+#include <algorithm>
+
 #include "ns_umma_attn.cuh"
 
 namespace ns {
@@ -50,6 +55,7 @@ __device__ __forceinline__ int sequence(const FaArgs &a, int s, int &len) {
 // take turns forth and back, so each gets a like share of every length.  A
 // lane keeps the longest of its 32nd of the sequences, so at each x only
 // groups that reach it are looked at.
+template <bool S>
 struct Dealer {
   int cta, ctas, lane, block, size;
   int most;                // blocks of the lane's group's longest sequence
@@ -60,7 +66,7 @@ struct Dealer {
   int turn, mine;          // the CTA's next item
 
   __device__ __forceinline__ void begin(const FaArgs &a, int cta_, int ctas_) {
-    cta = cta_, ctas = ctas_, lane = threadIdx.x & 31, block = 2 * a.per_tile;
+    cta = cta_, ctas = ctas_, lane = threadIdx.x & 31, block = (S ? 1 : 2) * a.per_tile;
     size = (a.n_seqs + 1023) / 1024 * 32;
     most = 0;
     for (int q = lane * size; q < min(a.n_seqs, (lane + 1) * size); ++q) {
@@ -103,18 +109,22 @@ struct Dealer {
     w.unit = (mine - before) % a.units;
     w.hidden = (w.tok0 + 1) / kKeys;  // tile 0's first token sees the tiles before whole
     w.n0 = (min(w.len, w.tok0 + a.per_tile) + kKeys - 1) / kKeys;
-    w.n1 = w.tok0 + a.per_tile < w.len ? (min(w.len, w.tok0 + block) + kKeys - 1) / kKeys : 0;
+    if (S)
+      w.n1 = w.n0 / 2, w.n0 -= w.n1;
+    else
+      w.n1 = w.tok0 + a.per_tile < w.len ? (min(w.len, w.tok0 + block) + kKeys - 1) / kKeys : 0;
     ++turn;
     mine = turn * ctas + ((turn & 1) ? ctas - 1 - cta : cta);
     return w;
   }
 };
 
+template <bool S>
 struct Mode {
   using Args = FaArgs;
   using Work = ns::Work;
-  using Dealer = ns::Dealer;
-  static constexpr bool kParts = false;
+  using Dealer = ns::Dealer<S>;
+  static constexpr bool kParts = false, kSplit = S;
   static constexpr int kStageRow = 128;
 
   struct Loader {
@@ -182,12 +192,21 @@ cudaError_t launch(const PromptAttnArgs &p, int sms, cudaStream_t st) {
   FaArgs a{};
   a.cu = p.cu, a.tokens = p.tokens, a.n_seqs = p.n_seqs, a.max_len = p.max_len;
   a.q_heads = p.q_heads, a.group = p.group;
-  // The heads of a group in one tile of 128 / group tokens, or a tile of 128 tokens for each head.  The first leaves
-  // fewer of the products behind the diagonal: 16 sequences of 130 to 2047 tokens, 28 heads on 4: 146.5 us, 168.2 with
-  // a head to a tile; 32 on 2 181.8, 213.0.  But its few tokens have many rows of queries, keys of the same tiles for
-  // every CTA, and no more items: one sequence of 2000 tokens with 8 heads on 1 takes 30.1, 29.6 us; 16 on 1 41.6,
+  // Few row tiles (no more than SMs, a head to a tile; 7/4 of them with long keys): an item is one of them, and where
+  // there is more than one key tile its keys are split over both halves of the CTA.  One prompt, us without and with:
+  // 567 tokens, 28 heads on 4 15.2, 12.3; 1967, 8 on 8 30.1, 21.3; 4000, 8 on 8 (1.7 tiles an SM) 52.8, 39.0; 1000, 32
+  // on 8 (1.7) 19.2, 19.9; 1300, 32 on 8 (2.3) 22.5, 27.3; one of 50, 32 on 8 8.6, 7.6 (one key tile); but ten of 1 to
+  // 3, 16 on 1 (1.05) 9.5, 14.0.
+  const long long blocks = (p.max_len + 127) / 128;
+  const long long tiles = std::min((long long)p.tokens / 128 + p.n_seqs, blocks * p.n_seqs) * p.q_heads;
+  const bool few = tiles <= sms || (4 * tiles <= 7LL * sms && p.max_len >= 1024);
+  const bool split = few && p.max_len > kKeys;
+  // Otherwise the heads of a group in one tile of 128 / group tokens, or a tile of 128 tokens for each head.  The first
+  // leaves fewer of the products behind the diagonal: 16 sequences of 130 to 2047 tokens, 28 heads on 4: 146.5 us, 168.2
+  // with a head to a tile; 32 on 2 181.8, 213.0.  But its few tokens have many rows of queries, keys of the same tiles
+  // for every CTA, and no more items: one sequence of 2000 tokens with 8 heads on 1 takes 30.1, 29.6 us; 16 on 1 41.6,
   // 30.7; 32 on 1 77.8, 36.3; 64 on 1 148.5, 64.4.
-  a.pack = p.group <= 8 || (p.group <= 32 && p.n_seqs >= 8) ? p.group : 1;
+  a.pack = !few && (p.group <= 8 || (p.group <= 32 && p.n_seqs >= 8)) ? p.group : 1;
   a.per_tile = 128 / a.pack, a.units = p.q_heads / a.pack;
   a.c = p.scale * attn::kLog2e;
   a.out = p.out, a.lse = p.lse, a.err = p.err;
@@ -200,10 +219,13 @@ cudaError_t launch(const PromptAttnArgs &p, int sms, cudaStream_t st) {
   if (!encode_16bit(&tmQ, p.q, 3, dq, sq, bq) || !encode_16bit(&tmK, p.k, 3, dk, sk, bk) ||
       !encode_16bit(&tmV, p.v, 3, dk, sv, bk))
     return cudaErrorInvalidValue;
-  const long long items =
-      (long long)((p.max_len + 2 * a.per_tile - 1) / (2 * a.per_tile)) * p.n_seqs * a.units;
+  const int block = (split ? 1 : 2) * a.per_tile;
+  const long long items = (long long)((p.max_len + block - 1) / block) * p.n_seqs * a.units;
   const unsigned ctas = (unsigned)(items < sms ? items : sms);
-  fa::attn_kernel<T, D, Mode><<<ctas, fa::kThreads, fa::Smem<D, Mode>::kBytes, st>>>(tmQ, tmK, tmV, a);
+  if (split)
+    fa::attn_kernel<T, D, Mode<true>><<<ctas, fa::kThreads, fa::Smem<D, Mode<true>>::kBytes, st>>>(tmQ, tmK, tmV, a);
+  else
+    fa::attn_kernel<T, D, Mode<false>><<<ctas, fa::kThreads, fa::Smem<D, Mode<false>>::kBytes, st>>>(tmQ, tmK, tmV, a);
   return cudaGetLastError();
 }
 
@@ -214,10 +236,14 @@ cudaError_t prepare_prompt_attn() {
   auto set = [&](const void *f, int bytes) {
     if (e == cudaSuccess) e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   };
-  set((const void *)fa::attn_kernel<__nv_bfloat16, 128, Mode>, fa::Smem<128, Mode>::kBytes);
-  set((const void *)fa::attn_kernel<__nv_bfloat16, 64, Mode>, fa::Smem<64, Mode>::kBytes);
-  set((const void *)fa::attn_kernel<__half, 128, Mode>, fa::Smem<128, Mode>::kBytes);
-  set((const void *)fa::attn_kernel<__half, 64, Mode>, fa::Smem<64, Mode>::kBytes);
+  set((const void *)fa::attn_kernel<__nv_bfloat16, 128, Mode<false>>, fa::Smem<128, Mode<false>>::kBytes);
+  set((const void *)fa::attn_kernel<__nv_bfloat16, 64, Mode<false>>, fa::Smem<64, Mode<false>>::kBytes);
+  set((const void *)fa::attn_kernel<__half, 128, Mode<false>>, fa::Smem<128, Mode<false>>::kBytes);
+  set((const void *)fa::attn_kernel<__half, 64, Mode<false>>, fa::Smem<64, Mode<false>>::kBytes);
+  set((const void *)fa::attn_kernel<__nv_bfloat16, 128, Mode<true>>, fa::Smem<128, Mode<true>>::kBytes);
+  set((const void *)fa::attn_kernel<__nv_bfloat16, 64, Mode<true>>, fa::Smem<64, Mode<true>>::kBytes);
+  set((const void *)fa::attn_kernel<__half, 128, Mode<true>>, fa::Smem<128, Mode<true>>::kBytes);
+  set((const void *)fa::attn_kernel<__half, 64, Mode<true>>, fa::Smem<64, Mode<true>>::kBytes);
   return e;
 }
 

@@ -44,6 +44,8 @@
 //   Args (with pack, per_tile, c, err), Work (with n0, n1: key tiles of the
 //   two row tiles, and hidden: the first that some row does not see whole),
 //   Dealer, Loader, Row, Wild.
+// kSplit: an item is one row tile, and row tile 1 the same rows again with
+// every other tile of keys; row tile 0's threads add the two up.
 //
 // Every wait is bounded (NS_FLAG_TIMEOUT).
 //
@@ -93,12 +95,19 @@ struct Smem {
   static constexpr int kKvFull = kMisc, kKvEmpty = kKvFull + 8 * kRing, kQFull = kKvEmpty + 8 * kRing,
                        kQEmpty = kQFull + 8, kSFull = kQEmpty + 8, kPFull = kSFull + 16, kPvHalf = kPFull + 32,
                        kOFull = kPvHalf + 16, kOEmpty = kOFull + 16, kCheck = kOEmpty + 16,
-                       kWFull = kCheck + 8 * kChecks, kWEmpty = kWFull + 16, kSlot = kWEmpty + 16, kWork = kSlot + 16,
+                       kMerge = kCheck + 8 * kChecks, kWFull = kMerge + 16, kWEmpty = kWFull + 16, kSlot = kWEmpty + 16, kWork = kSlot + 16,
                        kWildAny = kWork + 2 * kWorkBytes, kWild = kWildAny + 16,
                        kEnd = kWild + 2 * (int)sizeof(typename M::Wild);
   static constexpr int kBytes = kEnd + 1024;  // the base is rounded up to 1024 bytes
   static_assert(kBytes <= 232448, "shared memory of a CTA");
 };
+
+// Key tiles of an item: both row tiles see them in turn, or (M::kSplit) they
+// are one row tile twice, with every other key tile each.
+template <typename M>
+__device__ __forceinline__ int key_tiles(const typename M::Work &w) {
+  return M::kSplit ? w.n0 + w.n1 : max(w.n0, w.n1);
+}
 
 template <typename Work>
 __device__ __forceinline__ bool get_work(uint32_t base, int full, const uint8_t *g, int work_off, int i, Work &w,
@@ -152,6 +161,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(base + L::kWFull + 8 * i, 1);
       mbar_init(base + L::kWEmpty + 8 * i, kWorkReaders);
     }
+    mbar_init(base + L::kMerge, 128);
     for (int i = 0; i < kChecks; ++i) mbar_init(base + L::kCheck + 8 * i, 1);
     mbar_fence_init();
     umma::prefetch_map(&tmQ);
@@ -184,12 +194,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(base + L::kWEmpty + 8 * (i & 1));
       if (i > 0 && !(ok = wait(L::kQEmpty, i - 1))) break;
-      const int tiles = w.n1 > 0 ? 2 : 1, n = max(w.n0, w.n1);
+      const int tiles = w.n1 > 0 ? 2 : 1, n = key_tiles<M>(w);
       if (lane == 0) {
         mbar_expect_tx(base + L::kQFull, tiles * a.pack * a.per_tile * D * 2);
         for (int t = 0; t < tiles; ++t)
           for (int h = 0; h < D / 64; ++h)
-            loader.queries(a, w, t, h, base + L::kQ + t * L::kTile + h * kHalf, &tmQ, base + L::kQFull);
+            loader.queries(a, w, M::kSplit ? 0 : t, h, base + L::kQ + t * L::kTile + h * kHalf, &tmQ, base + L::kQFull);
       }
       for (int j = 0; j < n && ok; ++j) {
         for (int kv = 0; kv < 2; ++kv, ++it) {
@@ -209,6 +219,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // the running one.  So each group looks whether the next one's barrier is over before its own last products.
       Work w;
       int sl = 0, ph = 0, checked = 0;  // ring slot and phase of the next tile
+      int pos = 0;                      // ring position (M::kSplit)
       int np[2] = {0, 0}, no[2] = {0, 0};  // probabilities awaited, items begun, of each row tile
       bool ok = true, begun = false;
       auto next = [&]() {
@@ -248,6 +259,53 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive(base + L::kWEmpty + 8 * (i & 1));
         const int n0 = w.n0, n1 = w.n1, n = max(n0, n1), hidden = w.hidden;
         wait(L::kQFull, i);
+        if constexpr (M::kSplit) {
+          // Key tile j goes to the scores and the accumulator of j & 1.
+          const int first = pos, tiles = n0 + n1;
+          auto slot = [&](int x) { return (first + x) % kRing; };
+          auto filled = [&](int x) { wait(L::kKvFull + 8 * slot(x), (first + x) / kRing); };
+          for (int j = 0; j < min(tiles, 2); ++j) {
+            filled(2 * j);
+            if (!ok) break;
+            scores(j, slot(2 * j), L::kQFull, 0);
+            umma::commit(base + L::kKvEmpty + 8 * slot(2 * j));
+            if (j + 1 == tiles || (j == 1 && tiles == 2)) umma::commit(base + L::kQEmpty);
+          }
+          begun = true;
+          for (int j = 0; j < tiles && ok; ++j) {
+            const int t = j & 1;
+            filled(2 * j + 1);
+            if (j >= hidden) {
+              wait(L::kCheck + 8 * (checked % kChecks), checked / kChecks);
+              ++checked;
+            }
+            if (j < 2 && no[t] > 0) wait(L::kOEmpty + 8 * t, no[t] - 1);
+            wait(L::kPFull + 16 * t, np[t]);
+            if (!ok) break;
+            const bool seen = values(t, slot(2 * j + 1), 0, j > 1, L::kPFull + 16 * t + 8, np[t]);
+            umma::commit(base + L::kPvHalf + 8 * t);
+            wait(L::kPFull + 16 * t + 8, np[t], seen);
+            if (!ok) break;
+            values(t, slot(2 * j + 1), 1, j > 1, L::kQFull, 0);
+            ++np[t];
+            if (j + 2 >= tiles) {
+              umma::commit(base + L::kOFull + 8 * t);
+              ++no[t];
+            }
+            umma::commit(base + L::kKvEmpty + 8 * slot(2 * j + 1));
+            if (j + 2 < tiles) {
+              filled(2 * j + 4);
+              if (!ok) break;
+              scores(t, slot(2 * j + 4), L::kQFull, 0);
+              umma::commit(base + L::kKvEmpty + 8 * slot(2 * j + 4));
+              if (j + 3 == tiles) umma::commit(base + L::kQEmpty);
+            }
+          }
+          pos += 2 * tiles;
+          sl = pos % kRing, ph = pos / kRing & 1;
+          if (!ok) break;
+          continue;
+        }
         wait(L::kKvFull + 8 * sl, ph);
         if (!ok) break;
         scores(0, sl, L::kQFull, 0);
@@ -322,7 +380,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!__all_sync(0xffffffffu, more)) break;
       Wild *wild = reinterpret_cast<Wild *>(g + L::kWild) + (i & 1);
       volatile int *any = reinterpret_cast<volatile int *>(g + L::kWildAny) + (i & 1);
-      const int n = max(w.n0, w.n1);
+      const int n = key_tiles<M>(w);
       bool reset = false;
       for (int j = 0; j < n && ok; ++j) {
         // Every value tile passes here, so that the barrier's phase is this tile's: a slot is not filled again before
@@ -389,23 +447,25 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t c2 = umma::pack2(a.c, a.c);
     Work w;
     int ns = 0, items = 0;  // scores awaited, items of this row tile begun
+    int merged = 0;         // items whose two accumulators were added up (M::kSplit)
     bool ok = true;
     for (int i = 0; ok; ++i) {
       const bool more = get_work(base, L::kWFull, g, L::kWork, i, w, err);
       if (!__all_sync(0xffffffffu, more)) break;
       const int nt = t ? w.n1 : w.n0;
       typename M::Row row;
-      row.begin(a, w, t, r);
+      row.begin(a, w, M::kSplit ? 0 : t, r);
       const bool live = row.live;
       float m = kNegInf, l = 0.f;
       for (int j = 0; j < nt; ++j, ++ns) {
         ok = __all_sync(0xffffffffu, umma::inline_wait(base + L::kSFull + 8 * t, ns & 1, err));
         if (!ok) break;
         umma::fence_after();
+        const int key_tile = M::kSplit ? 2 * j + t : j;
         uint32_t s[128], p[32];
         float sum;
         auto mask = [&](int from) {  // keys that the row does not see, among 64
-          const uint64_t sees = row.sees(w, j, from);
+          const uint64_t sees = row.sees(w, key_tile, from);
           NS_FA_MASK(s, from, sees)
         };
         auto most = [&](int from) {
@@ -457,11 +517,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         umma::wait_ld();
         umma::ld32(tS + 64, s + 64);
         umma::ld32(tS + 96, s + 96);
-        if (j >= w.hidden) mask(0);
+        if (key_tile >= w.hidden) mask(0);
         bool whole = false;  // the second half has come
         if (j == 0) {
           umma::wait_ld();
-          if (j >= w.hidden) mask(64);
+          if (key_tile >= w.hidden) mask(64);
           whole = true;
           m = fmaxf(most(0), most(64));
         }
@@ -470,7 +530,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const bool low = live && (sum > kLimit || m == kNegInf);
           if (__any_sync(0xffffffffu, low)) {
             umma::wait_ld();
-            if (j >= w.hidden) mask(64);
+            if (key_tile >= w.hidden) mask(64);
             whole = true;
             // the accumulator is still: S of this tile came after the last product into it
             raise(low, fmaxf(most(0), most(64)));
@@ -484,7 +544,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         l += sum;
         if (!whole) {
           umma::wait_ld();
-          if (j >= w.hidden) mask(64);
+          if (key_tile >= w.hidden) mask(64);
         }
         probabilities(64);
         if (j > 0) {
@@ -510,6 +570,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         ++items;
         umma::fence_after();
+        float f0 = 1.f, f1 = 0.f;
+        if constexpr (M::kSplit) {
+          float2 *hand = reinterpret_cast<float2 *>(g + L::kOut + (4 + wq) * 32 * M::kStageRow) + lane;
+          if (t == 1) {  // row tile 0's thread of the same row has the rest of it
+            *hand = make_float2(m, l);
+            mbar_arrive(base + L::kMerge);
+          } else if (w.n1 > 0) {
+            ok = __all_sync(0xffffffffu, umma::inline_wait(base + L::kMerge, merged & 1, err)) &&
+                 __all_sync(0xffffffffu, umma::inline_wait(base + L::kOFull + 8, merged & 1, err));
+            if (!ok) break;
+            ++merged;
+            umma::fence_after();
+            const float2 o = *hand;
+            const float top = fmaxf(m, o.x), safe = top == kNegInf ? 0.f : top;
+            f0 = ex2(m - safe), f1 = ex2(o.x - safe);
+            l = l * f0 + o.y * f1;
+            m = top;
+          }
+        }
         const bool wild = *(reinterpret_cast<volatile int *>(g + L::kWildAny) + (i & 1)) != 0;
         const Wild *wd = reinterpret_cast<const Wild *>(g + L::kWild) + (i & 1);
         // some columns at a time through shared memory, so that a store covers whole lines of a few rows
@@ -534,8 +613,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto drained = [&]() {  // the accumulator may be written again
           umma::fence_before();
           mbar_arrive(base + L::kOEmpty + 8 * t);
+          if (M::kSplit && w.n1 > 0) mbar_arrive(base + L::kOEmpty + 8);
         };
-        if (!M::kParts || w.slot < 0) {
+        if (M::kSplit && t == 1) {
+        } else if (!M::kParts || w.slot < 0) {
           const float inv = l == 0.f ? 0.f : 1.f / l;
           const long long to = live ? reinterpret_cast<long long>(static_cast<T *>(a.out) + row.at * D) : 0;
 #pragma unroll 1
@@ -543,6 +624,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t o[2 * kWords];
 #pragma unroll
             for (int e = 0; e < 2 * kWords; e += 32) umma::ld32(tO + q * 2 * kWords + e, o + e);
+            if constexpr (M::kSplit) {
+              if (w.n1 > 0) {
+                uint32_t o1[2 * kWords];
+#pragma unroll
+                for (int e = 0; e < 2 * kWords; e += 32) umma::ld32(tO + 128 + q * 2 * kWords + e, o1 + e);
+                umma::wait_ld();
+#pragma unroll
+                for (int e = 0; e < 2 * kWords; ++e)
+                  o[e] = __float_as_uint(__uint_as_float(o[e]) * f0 + __uint_as_float(o1[e]) * f1);
+              }
+            }
             umma::wait_ld();
             if (q + 1 == D / (2 * kWords)) drained();
             if (wild) {

@@ -640,3 +640,33 @@ def test_paged_large_groups(ns, group):
     """Query heads that share a key-value head: up to 128 of them are rows of one tile."""
     run_paged(ns, [30, 400, 0, 129], 1, group, 1, 64, 16, BF16, group)
     run_paged(ns, [33, 500], 7, 2 * group, 2, 128, 32, F16, group, masks="tree")
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("hq,hkv,d", [(48, 8, 64), (36, 4, 128), (40, 40, 64), (64, 2, 128)])
+def test_prompt_many_items(ns, hq, hkv, d, dtype):
+    """Calls whose items are two row tiles each (those of few heads and sequences are one, with its keys split)."""
+    run_prompt(ns, EDGES, hq, hkv, d, dtype, 70)
+
+
+@pytest.mark.parametrize("hq", [2, 64])
+def test_prompt_scores_that_rise_by_key_tile(ns, hq):
+    """Each tile of 128 keys far above or below the one before, whether or not the tiles are split over two halves."""
+    g = gen(71)
+    n, d = 700, 64
+    q, k, v = normal(g, (n, hq, d), BF16), normal(g, (n, 1, d), BF16), normal(g, (n, 1, d), BF16)
+    step = torch.tensor([(0, 60, -40, 80, 10, 90)[i // 128] for i in range(n)], dtype=torch.float32)
+    q[:, :, 0] = 8.0
+    k[:, 0, 0] = step.to(BF16)
+    out, lse = ns.attend_prompt(q.cuda(), k.cuda(), v.cuda(), torch.tensor([0, n], dtype=torch.int32).cuda(), n)
+    sees = torch.ones(n, n, dtype=torch.bool).tril()
+    for h in range(hq):
+        o, z, to, tz = attend_rows(q[:, h], k[:, 0], v[:, 0], sees, d ** -0.5)
+        check(out[:, h], o, to, f"out of head {h}")
+        check(lse[:, h], z, tz, f"lse of head {h}")
+
+
+@pytest.mark.parametrize("lens,hq,hkv,d", [([2900], 4, 4, 128), ([1500, 130, 700], 4, 1, 64), ([129, 128, 127, 1], 8, 4, 64)])
+def test_prompt_few_long_items(ns, lens, hq, hkv, d):
+    """Keys split over the two halves of a CTA: even and odd numbers of tiles, several items to a CTA."""
+    run_prompt(ns, lens, hq, hkv, d, BF16, 72)
