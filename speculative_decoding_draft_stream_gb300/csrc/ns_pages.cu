@@ -9,9 +9,9 @@
 // words): 2.5 to 3.5 us each in a graph, launched into each other's ends.  The
 // data movers are bound by HBM: each row is read and written once with
 // 16-byte accesses, several per lane in flight.  16 sequences that give up
-// their last step, append 60 nodes and keep 5 of them in 16 layers take 21 us
-// for four calls; 64 children with their 64 MB of copied last pages 37 us;
-// 8 sequences of 4001 new rows of which every second stays in 12 layers 168 us
+// their last step, append 60 nodes and keep 5 of them in 16 layers take 20 us
+// for four calls; 64 children with their 64 MB of copied last pages 34 us;
+// 8 sequences of 4001 new rows of which every second stays in 12 layers 166 us
 // (393 MB read and 332 MB written by the compaction: 126 us of it).
 #include "ns_internal.cuh"
 #include "ns_ops.cuh"
@@ -21,7 +21,7 @@ namespace {
 
 constexpr int kSeqThreads = 128;      // truncate, fork: one CTA per sequence
 constexpr int kExtendThreads = 1024;  // extend: one CTA
-constexpr int kListHere = 2048;        // given pages that extend lists in shared memory
+constexpr int kListHere = 2048;       // given pages that extend lists in shared memory
 constexpr int kMoveThreads = 256;
 constexpr int kMoveWarps = kMoveThreads / kWarp;
 constexpr int kUnroll = 8;  // 16-byte loads a lane keeps in flight in the movers
