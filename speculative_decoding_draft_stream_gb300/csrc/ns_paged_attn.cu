@@ -15,7 +15,7 @@
 // of them; the join kernel, whose launch overlaps the end of this one, adds
 // up the parts of such items in CTA order.  A cluster: a small call is mostly
 // latency, so each item goes to one cluster, whose CTAs have equal shares of
-// its tiles (of 128 keys) and join through shared memory: one launch, no
+// its tiles (of 64 or 128 keys) and join through shared memory: one launch, no
 // workspace.  No atomics in either: the same inputs give the same bits.
 //
 // In a CTA: the next tiles are in flight (cp.async, 16 bytes, page ids
@@ -37,43 +37,46 @@ namespace {
 
 using namespace paged;
 
-// Of CTAs that share the line (C = 0), two to an SM, and of those of a
-// cluster, alone on an SM with twice the warps: threads, keys of a tile.
-template <int C>
-constexpr int kThreads = C == 0 ? 128 : 256;
-template <int C>
-constexpr int kKeys = C == 0 ? 64 : 128;
+// How a call is shared out (by_rows has the rule): the line, or a cluster to
+// an item, of CTAs as small as the line's, two or more to an SM, or of large
+// ones, alone on an SM with twice the warps and keys.
+enum Way { kLine, kSmall, kLarge };
+constexpr int kCluster = 16;  // CTAs of an item: one for each row that it may have
+template <int W>
+constexpr int kThreads = W == kLarge ? 256 : 128;
+template <int W>
+constexpr int kKeys = W == kLarge ? 128 : 64;  // of a tile
 template <int D>
 constexpr int kPerSm = D == 128 ? 3 : 4;  // CTAs of the line on an SM
-template <int D, int C>
-constexpr int kStages = D == 128 && C == 0 ? 2 : 3;  // tiles in flight
+template <int D, int W>
+constexpr int kStages = D == 128 && W == kLine ? 2 : 3;  // tiles in flight
 constexpr int kMerge = 32 * 4 * 4;    // a lane's m, l (and padding), after its o
 
-template <int D, int C>
+template <int D, int W>
 __host__ __device__ constexpr int pa_stage() {
-  return 2 * kKeys<C> * D * 2;
+  return 2 * kKeys<W> * D * 2;
 }
 // Behind the stages: what a warp hands over to warp 0; in a cluster, (m, l)
 // and o of each of its CTAs for the rows that this CTA joins.
-template <int D, int WM, int C>
+template <int D, int WM, int W>
 __host__ __device__ constexpr int pa_smem() {
-  return kStages<D, C> * pa_stage<D, C>() + (C > 0 ? 16 * (D + 2) * 4 : WM == 1 ? 32 * D / 2 * 4 + kMerge : 0);
+  return kStages<D, W> * pa_stage<D, W>() + (W != kLine ? 16 * (D + 2) * 4 : WM == 1 ? 32 * D / 2 * 4 + kMerge : 0);
 }
 
-template <int C>
+template <int W>
 __host__ __device__ inline long long pa_tiles(int len) {
-  return len > 0 ? (len - 1) / kKeys<C> + 1 : 1;
+  return len > 0 ? (len - 1) / kKeys<W> + 1 : 1;
 }
 
 // Where a CTA is in the line of tiles: item (sequence b, `item` = head *
 // blocks + block of rows) and its tile.
-template <int C>
+template <int W>
 struct Cursor {
   int b, item, tile, nt, len;
   const int32_t *table;
   __device__ __forceinline__ void enter(const PagedAttnArgs &a, uint32_t *err) {
     len = length(a, b, err);
-    nt = (int)pa_tiles<C>(len);
+    nt = (int)pa_tiles<W>(len);
     const int s = a.seqs[b];
     table = a.table + (size_t)(s >= 0 && s < a.max_seqs ? s : 0) * a.table_ld;
   }
@@ -98,14 +101,15 @@ __device__ __forceinline__ void push(uint32_t a, float x) {
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(a), "f"(x) : "memory");
 }
 
-// C = 0: the line of tiles.  C > 0 (at most 16 rows): an item to a cluster of C.
-template <typename T, int D, int WM, int C>
-__global__ void __launch_bounds__(kThreads<C>) paged_attn_kernel(const PagedAttnArgs a, int blocks) {
-  constexpr int kPaThreads = kThreads<C>, kPaKeys = kKeys<C>, kWarps = kPaThreads / kWarp;
+// (Clusters: at most 16 rows.)
+template <typename T, int D, int WM, int W>
+__global__ void __launch_bounds__(kThreads<W>) paged_attn_kernel(const PagedAttnArgs a, int blocks) {
+  constexpr int kPaThreads = kThreads<W>, kPaKeys = kKeys<W>, kWarps = kPaThreads / kWarp;
   constexpr int WK = kWarps / WM, NK = kPaKeys / WK, kRows = 16 * WM;
   constexpr int kLanesRow = D / 8;                    // threads that fetch a row
   constexpr int kPass = kPaThreads / kLanesRow;       // rows a pass of the CTA fetches
-  static_assert(C == 0 || WM == 1, "a cluster has 16 rows");
+  static_assert(W == kLine || WM == 1, "a cluster has 16 rows");
+  constexpr int C = kCluster;
   extern __shared__ __align__(128) uint8_t smem[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int wm = WM == 1 ? 0 : warp, wk = WM == 1 ? warp : 0;
@@ -113,10 +117,10 @@ __global__ void __launch_bounds__(kThreads<C>) paged_attn_kernel(const PagedAttn
   const uint32_t s0 = (uint32_t)__cvta_generic_to_shared(smem);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-  Cursor<C> ld;
+  Cursor<W> ld;
   long long t0, t1;
   Ws ws{};
-  if constexpr (C > 0) {
+  if constexpr (W != kLine) {
     asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");  // this CTA has begun
     const int at = blockIdx.x / C, rank = blockIdx.x % C;
     ld.b = at / items, ld.item = at % items;
@@ -124,13 +128,13 @@ __global__ void __launch_bounds__(kThreads<C>) paged_attn_kernel(const PagedAttn
     t0 = (long long)ld.nt * rank / C, t1 = (long long)ld.nt * (rank + 1) / C;
     ld.tile = (int)t0;
   } else {
-    long long *s_cum = reinterpret_cast<long long *>(smem + pa_smem<D, WM, C>());
+    long long *s_cum = reinterpret_cast<long long *>(smem + pa_smem<D, WM, W>());
     __shared__ long long s_sum[kPaThreads / kWarp];
     // tiles of the sequences before each one
     long long total = 0;
     for (int b0 = 0; b0 < a.n_seqs; b0 += kPaThreads) {
       const int b = b0 + tid;
-      const long long mine = b < a.n_seqs ? pa_tiles<C>(length(a, b, blockIdx.x == 0 ? a.err : nullptr)) * items : 0;
+      const long long mine = b < a.n_seqs ? pa_tiles<W>(length(a, b, blockIdx.x == 0 ? a.err : nullptr)) * items : 0;
       long long sum = mine;
 #pragma unroll
       for (int off = 1; off < kWarp; off <<= 1) {
@@ -171,7 +175,7 @@ __global__ void __launch_bounds__(kThreads<C>) paged_attn_kernel(const PagedAttn
       ld.tile = (int)(local - (long long)ld.item * ld.nt);
     }
   }
-  Cursor<C> cu = ld;
+  Cursor<W> cu = ld;
 
   // page ids of the load cursor's tile, one for each eight rows, in as many lanes
   auto fetch_ids = [&]() {
@@ -195,7 +199,7 @@ __global__ void __launch_bounds__(kThreads<C>) paged_attn_kernel(const PagedAttn
   const T *vbase = static_cast<const T *>(a.v) + (fr & 7) * a.v_token + fc * 8;
   const uint32_t to = piece<D>(fr, fc);
   auto fetch = [&](int id, int stage) {
-    const uint32_t sk = s0 + stage * pa_stage<D, C>() + to, sv = sk + kPaKeys * D * 2;
+    const uint32_t sk = s0 + stage * pa_stage<D, W>() + to, sv = sk + kPaKeys * D * 2;
     const int left = ld.len - ld.tile * kPaKeys, head = ld.item / blocks;
     const int64_t page = id >= 0 ? id : 0, row = (ld.tile * kPaKeys + lane * 8) & pmask;
     const int64_t ko = page * a.k_page + head * a.k_head + row * a.k_token;
@@ -218,7 +222,7 @@ __global__ void __launch_bounds__(kThreads<C>) paged_attn_kernel(const PagedAttn
   auto issue = [&]() {
     if (left_ld > 0) {
       fetch(ids, st_ld);
-      st_ld = st_ld + 1 == kStages<D, C> ? 0 : st_ld + 1;
+      st_ld = st_ld + 1 == kStages<D, W> ? 0 : st_ld + 1;
       --left_ld;
       if (left_ld > 0) {
         ld.next(a, items);
@@ -228,10 +232,10 @@ __global__ void __launch_bounds__(kThreads<C>) paged_attn_kernel(const PagedAttn
     cp_commit();
   };
 #pragma unroll
-  for (int i = 0; i < kStages<D, C> - 1; ++i) issue();
+  for (int i = 0; i < kStages<D, W> - 1; ++i) issue();
 
   Rows<T, D> rows;
-  if (C > 0) rows.clear();  // (a CTA of a short sequence may have no tile)
+  if (W != kLine) rows.clear();  // (a CTA of a short sequence may have no tile)
   uint32_t q[D / 16][4];
   uint64_t word[2] = {0, 0};
   int st = 0;
@@ -258,11 +262,11 @@ __global__ void __launch_bounds__(kThreads<C>) paged_attn_kernel(const PagedAttn
         }
       }
     }
-    cp_wait<kStages<D, C> - 2>();
+    cp_wait<kStages<D, W> - 2>();
     __syncthreads();  // the tile is there for everyone, and everyone is done with the stage to be filled next
     issue();
-    const uint32_t sk = s0 + st * pa_stage<D, C>(), sv = sk + kPaKeys * D * 2;
-    st = st + 1 == kStages<D, C> ? 0 : st + 1;
+    const uint32_t sk = s0 + st * pa_stage<D, W>(), sv = sk + kPaKeys * D * 2;
+    st = st + 1 == kStages<D, W> ? 0 : st + 1;
     const int ctx = cu.len - a.n, p0 = cu.tile * kPaKeys, k0 = wk * NK;
     if (p0 + kPaKeys <= ctx) {
       rows.template tile<NK, false>(q, sk, sv, k0, c, [](int, int) { return false; }, false);
@@ -282,9 +286,9 @@ __global__ void __launch_bounds__(kThreads<C>) paged_attn_kernel(const PagedAttn
     const bool ends = cu.tile + 1 == cu.nt;
     if (ends || g + 1 == t1) {
       rows.sum_l();
-      if (C > 0) break;
+      if (W != kLine) break;
       if (WM == 1) {  // the warps' keys join, in warp order, in warp 0
-        float4 *bo = reinterpret_cast<float4 *>(smem + kStages<D, C> * pa_stage<D, C>());
+        float4 *bo = reinterpret_cast<float4 *>(smem + kStages<D, W> * pa_stage<D, W>());
         float4 *bm = bo + (D / 8) * 32;
         for (int w = 1; w < 4; ++w) {
           if (warp == w) {
@@ -346,15 +350,15 @@ __global__ void __launch_bounds__(kThreads<C>) paged_attn_kernel(const PagedAttn
     }
     if (g + 1 < t1) cu.next(a, items);
   }
-  if constexpr (C > 0) {
-    // The warps' parts join here, and the CTAs' in CTA r % C for row r, both in their order.
+  if constexpr (W != kLine) {
+    // The warps' parts join here, and the CTAs' in CTA r for row r, both in their order.
     constexpr int kPitch = D + 8;  // of a row of a warp's part: the eight rows of a store in different banks
-    static_assert(kWarps * 16 * (kPitch + 2) * 4 <= kStages<D, C> * pa_stage<D, C>(), "the parts replace the tiles");
+    static_assert(kWarps * 16 * (kPitch + 2) * 4 <= kStages<D, W> * pa_stage<D, W>(), "the parts replace the tiles");
     const int rank = blockIdx.x % C, head = ld.item, b = ld.b;
     float *w_o = reinterpret_cast<float *>(smem);
     float2 *w_ml = reinterpret_cast<float2 *>(w_o + kWarps * 16 * kPitch);
-    float *c_o = reinterpret_cast<float *>(smem + kStages<D, C> * pa_stage<D, C>());  // [16 / C][C][D]
-    float2 *c_ml = reinterpret_cast<float2 *>(c_o + 16 * D);
+    float *c_o = reinterpret_cast<float *>(smem + kStages<D, W> * pa_stage<D, W>());  // [C][D]
+    float2 *c_ml = reinterpret_cast<float2 *>(c_o + C * D);
     __syncthreads();  // (every tile has been waited for and used)
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -383,29 +387,26 @@ __global__ void __launch_bounds__(kThreads<C>) paged_attn_kernel(const PagedAttn
         l = fmaf(p[w].y, f, l);
         o = fmaf(w_o[(w * 16 + r) * kPitch + col], f, o);
       }
-      const int part = r / C * C + rank;
-      push(of_rank(shared_at(c_o + part * D + col), r % C), o);
-      if (col < 2) push(of_rank(shared_at(c_ml + part) + 4 * col, r % C), col ? l : m);
+      push(of_rank(shared_at(c_o + rank * D + col), r), o);
+      if (col < 2) push(of_rank(shared_at(c_ml + rank) + 4 * col, r), col ? l : m);
     }
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-    for (int own = tid / D; own < 16 / C; own += kPaThreads / D) {
-      const int r = own * C + rank;
-      if (r >= R) break;
+    if (rank < R && tid < D) {
       float2 p[C];
       float m = kNegInf, l = 0.f, o = 0.f;
 #pragma unroll
       for (int i = 0; i < C; ++i) {
-        p[i] = c_ml[own * C + i];
+        p[i] = c_ml[i];
         m = fmaxf(m, p[i].x);
       }
 #pragma unroll
       for (int i = 0; i < C; ++i) {
         const float f = ex2(p[i].x - (m == kNegInf ? 0.f : m));
         l = fmaf(p[i].y, f, l);
-        o = fmaf(c_o[(own * C + i) * D + col], f, o);
+        o = fmaf(c_o[i * D + col], f, o);
       }
-      const int64_t at = ((int64_t)b * a.n + r / a.group) * a.q_heads + head * a.group + r % a.group;
+      const int64_t at = ((int64_t)b * a.n + rank / a.group) * a.q_heads + head * a.group + rank % a.group;
       static_cast<T *>(a.out)[at * D + col] = static_cast<T>(l == 0.f ? 0.f : o / l);
       if (a.lse && col == 0) a.lse[at] = row_lse<T>(m, l);
     }
@@ -434,10 +435,10 @@ template <typename T, int D, int WM>
 cudaError_t launch(const PagedAttnArgs &a, int sms, cudaStream_t st) {
   constexpr int kRows = 16 * WM;
   const int blocks = (a.n * a.group + kRows - 1) / kRows;
-  const int smem = pa_smem<D, WM, 0>() + a.n_seqs * 8;
-  const long long most = pa_tiles<0>(a.max_len) * a.n_seqs * a.kv_heads * blocks;
+  const int smem = pa_smem<D, WM, kLine>() + a.n_seqs * 8;
+  const long long most = pa_tiles<kLine>(a.max_len) * a.n_seqs * a.kv_heads * blocks;
   const int ctas = (int)(most < (long long)kPerSm<D> * sms ? most : kPerSm<D> * sms);
-  paged_attn_kernel<T, D, WM, 0><<<ctas, kThreads<0>, smem, st>>>(a, blocks);
+  paged_attn_kernel<T, D, WM, kLine><<<ctas, kThreads<kLine>, smem, st>>>(a, blocks);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   const int rows = a.n * a.group < kRows ? a.n * a.group : kRows;
@@ -447,54 +448,57 @@ cudaError_t launch(const PagedAttnArgs &a, int sms, cudaStream_t st) {
 struct ClusterLaunch {
   cudaLaunchConfig_t cfg{};
   cudaLaunchAttribute at[1];
-  ClusterLaunch(int ctas, int c, int smem, cudaStream_t st) {
-    cfg.gridDim = dim3((unsigned)ctas);
-    cfg.blockDim = dim3(kThreads<8>);
+  ClusterLaunch(int items, int threads, int smem, cudaStream_t st) {
+    cfg.gridDim = dim3((unsigned)items * kCluster);
+    cfg.blockDim = dim3((unsigned)threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = (unsigned)c;
+    at[0].val.clusterDim.x = kCluster;
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
   }
 };
-template <typename T, int D, int C>
+template <typename T, int D, int W>
 int resident = 0;  // clusters that the GPU holds at once
 
-// Whether each item can have its own cluster of C, and did (e).
-template <typename T, int D, int C>
-bool launch_clusters(const PagedAttnArgs &a, cudaStream_t st, cudaError_t &e) {
-  constexpr int kTiles = 8;
-  const long long items = (long long)a.n_seqs * a.kv_heads;
-  if (items > resident<T, D, C> || a.max_len > kTiles * C * kKeys<C>) return false;
-  ClusterLaunch l((int)items * C, C, pa_smem<D, 1, C>(), st);
-  e = cudaLaunchKernelEx(&l.cfg, paged_attn_kernel<T, D, 1, C>, a, 1);
-  return true;
+// Whether each item can have its own cluster with up to 8 tiles to a CTA.
+template <typename T, int D, int W>
+bool clusters_fit(const PagedAttnArgs &a) {
+  return (long long)a.n_seqs * a.kv_heads <= resident<T, D, W> && a.max_len <= 8 * kCluster * kKeys<W>;
+}
+template <typename T, int D, int W>
+cudaError_t launch_clusters(const PagedAttnArgs &a, cudaStream_t st) {
+  ClusterLaunch l(a.n_seqs * a.kv_heads, kThreads<W>, pa_smem<D, 1, W>(), st);
+  return cudaLaunchKernelEx(&l.cfg, paged_attn_kernel<T, D, 1, W>, a, 1);
 }
 
-template <typename T, int D, int WM, int C>
+template <typename T, int D, int WM, int W>
 cudaError_t prepare() {
-  cudaError_t e = cudaFuncSetAttribute(paged_attn_kernel<T, D, WM, C>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       pa_smem<D, WM, C>() + (C == 0 ? NS_MAX_ATTEND_SEQS * 8 : 0));
-  if (C > 8 && e == cudaSuccess)
-    e = cudaFuncSetAttribute(paged_attn_kernel<T, D, WM, C>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-  if (C > 0 && e == cudaSuccess) {
-    ClusterLaunch l(C * 64, C, pa_smem<D, 1, C>(), nullptr);
-    e = cudaOccupancyMaxActiveClusters(&resident<T, D, C>, paged_attn_kernel<T, D, WM, C>, &l.cfg);
-  }
-  return e;
+  cudaError_t e = cudaFuncSetAttribute(paged_attn_kernel<T, D, WM, W>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       pa_smem<D, WM, W>() + (W == kLine ? NS_MAX_ATTEND_SEQS * 8 : 0));
+  if (W == kLine) return e;
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(paged_attn_kernel<T, D, WM, W>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e != cudaSuccess) return e;
+  ClusterLaunch l(64, kThreads<W>, pa_smem<D, 1, W>(), nullptr);
+  return cudaOccupancyMaxActiveClusters(&resident<T, D, W>, paged_attn_kernel<T, D, WM, W>, &l.cfg);
 }
 
 // Up to 16 rows the keys are what costs: each is fetched once and the warps
-// split them.  A call whose items fit on the GPU as clusters of 16, else of 8,
-// all at once, with up to 8 tiles to a CTA, takes clusters.  Measured, line
-// against cluster, one new token, bf16 (us in a graph):
-//   32 heads on 8, 128 columns, 1 sequence:  100 tokens 8.4, 5.6;  4097: 12.9 (two CTAs to an SM), 11.1;
-//     8000: 15.2, 15.2;  16000 (16 tiles): 18.7, 25.4;  2 sequences (a second wave of clusters) 100: 8.6, 9.9
-//   28 on 4, 128 columns, 1 sequence, clusters of 16 (8):  4097: 13.7, 9.0 (11.3);  16000: 17.2, 15.2 (25.8);
-//     32000: 20.7, 25.8 (48.4)
-//   12 on 4, 64 columns, 4 sequences, clusters of 8:  1000: 9.6, 4.9;  8000: 16.0, 13.3;  16000: 20.3, 22.5
+// split them.  A call whose items fit on the GPU as clusters, all at once, with
+// up to 8 tiles to a CTA, takes clusters: of large CTAs where small ones would
+// have more than one tile each and the large ones still fit (7 clusters of 128
+// columns, 15 of small ones).  Measured, line, small, large, one new token,
+// bf16 (us in a graph; the line with two CTAs an SM and three tiles, which is
+// up to 3 us quicker for calls of this size):
+//   32 heads on 8, 128 columns, 1 sequence:  100 tokens 8.4, 4.9;  4097: 12.9, 9.0;  8000: 15.2, 13.3
+//   28 on 4, 128 columns, 1 sequence:  100: 8.4, 5.2, 6.0;  2000: 10.2, 6.2, 6.0;  8000: 15.0, 11.9, 10.0;
+//     16000: 17.2, -, 15.2;  32000 (16 tiles): 20.7, -, 25.8
+//   12 on 4, 64 columns, 1 sequence:  1000: 9.2, 4.3, 4.7;  8000: 14.8, 9.6, 7.6
+// Clusters of 8 large CTAs took 11.3 us for the 4097 tokens, two waves of
+// clusters (2 sequences, 32 heads on 8) 9.9 where the line takes 8.4.
 // Above 16 rows the products cost: they belong on the tensor cores of
 // ns_paged_umma.cu, which want queries that TMA can fetch (16-byte aligned,
 // strides multiples of 8); other queries take 64 rows a CTA here.  Measured
@@ -505,8 +509,9 @@ cudaError_t prepare() {
 template <typename T, int D>
 cudaError_t by_rows(const PagedAttnArgs &a, int sms, cudaStream_t st) {
   if (a.n * a.group <= 16) {
-    cudaError_t e;
-    if (launch_clusters<T, D, 16>(a, st, e) || launch_clusters<T, D, 8>(a, st, e)) return e;
+    if (a.max_len > kCluster * kKeys<kSmall> && clusters_fit<T, D, kLarge>(a))
+      return launch_clusters<T, D, kLarge>(a, st);
+    if (clusters_fit<T, D, kSmall>(a)) return launch_clusters<T, D, kSmall>(a, st);
     return launch<T, D, 1>(a, sms, st);
   }
   if (paged_umma_ok(a)) return launch_paged_umma(a, Type<T>::kBf16 ? NS_DTYPE_BF16 : NS_DTYPE_F16, D, sms, st);
@@ -518,10 +523,10 @@ cudaError_t by_dim(const PagedAttnArgs &a, int dim, int sms, cudaStream_t st) {
 }
 template <typename T, int D>
 cudaError_t prepare_all() {
-  cudaError_t e = prepare<T, D, 1, 0>();
-  if (e == cudaSuccess) e = prepare<T, D, 4, 0>();
-  if (e == cudaSuccess) e = prepare<T, D, 1, 8>();
-  if (e == cudaSuccess) e = prepare<T, D, 1, 16>();
+  cudaError_t e = prepare<T, D, 1, kLine>();
+  if (e == cudaSuccess) e = prepare<T, D, 4, kLine>();
+  if (e == cudaSuccess) e = prepare<T, D, 1, kSmall>();
+  if (e == cudaSuccess) e = prepare<T, D, 1, kLarge>();
   return e;
 }
 
