@@ -39,7 +39,7 @@ using namespace paged;
 
 // How a call is shared out (by_rows has the rule): the line, or a cluster to
 // an item, of CTAs as small as the line's, two or more to an SM, or of large
-// ones, alone on an SM with twice the warps and keys.
+// ones, one to an SM (128 columns), with twice the warps and keys.
 enum Way { kLine, kSmall, kLarge };
 constexpr int kCluster = 16;  // CTAs of an item: one for each row that it may have
 template <int W>
@@ -49,7 +49,7 @@ constexpr int kKeys = W == kLarge ? 128 : 64;  // of a tile
 template <int D>
 constexpr int kPerSm = D == 128 ? 3 : 4;  // CTAs of the line on an SM
 template <int D, int W>
-constexpr int kStages = D == 128 && W == kLine ? 2 : 3;  // tiles in flight
+constexpr int kStages = D == 128 && W != kLarge ? 2 : 3;  // tiles in flight
 constexpr int kMerge = 32 * 4 * 4;    // a lane's m, l (and padding), after its o
 
 template <int D, int W>
@@ -463,10 +463,13 @@ struct ClusterLaunch {
 template <typename T, int D, int W>
 int resident = 0;  // clusters that the GPU holds at once
 
-// Whether each item can have its own cluster with up to 8 tiles to a CTA.
+// Whether each item can have its own cluster with up to 8 tiles to a CTA (in
+// two waves of small CTAs: with one or two tiles).
 template <typename T, int D, int W>
 bool clusters_fit(const PagedAttnArgs &a) {
-  return (long long)a.n_seqs * a.kv_heads <= resident<T, D, W> && a.max_len <= 8 * kCluster * kKeys<W>;
+  const bool two_waves = W == kSmall && a.max_len > kCluster * kKeys<W> / 2 && a.max_len <= 2 * kCluster * kKeys<W>;
+  return (long long)a.n_seqs * a.kv_heads <= (two_waves ? 2 : 1) * resident<T, D, W> &&
+         a.max_len <= 8 * kCluster * kKeys<W>;
 }
 template <typename T, int D, int W>
 cudaError_t launch_clusters(const PagedAttnArgs &a, cudaStream_t st) {
@@ -490,15 +493,17 @@ cudaError_t prepare() {
 // split them.  A call whose items fit on the GPU as clusters, all at once, with
 // up to 8 tiles to a CTA, takes clusters: of large CTAs where small ones would
 // have more than one tile each and the large ones still fit (7 clusters of 128
-// columns, 15 of small ones).  Measured, line, small, large, one new token,
+// columns, three times as many of small ones).  Measured, line, small, large, one new token,
 // bf16 (us in a graph; the line with two CTAs an SM and three tiles, which is
 // up to 3 us quicker for calls of this size):
-//   32 heads on 8, 128 columns, 1 sequence:  100 tokens 8.4, 4.9;  4097: 12.9, 9.0;  8000: 15.2, 13.3
+//   32 heads on 8, 128 columns, 1 sequence:  100 tokens 8.4, 4.9;  4097: 12.9, 8.8;  8000: 15.2, 13.5
+//     2 sequences:  100: 8.4, 5.7;  4097: 14.4, 10.1;  8000: 17.8, 15.8
 //   28 on 4, 128 columns, 1 sequence:  100: 8.4, 5.2, 6.0;  2000: 10.2, 6.2, 6.0;  8000: 15.0, 11.9, 10.0;
 //     16000: 17.2, -, 15.2;  32000 (16 tiles): 20.7, -, 25.8
 //   12 on 4, 64 columns, 1 sequence:  1000: 9.2, 4.3, 4.7;  8000: 14.8, 9.6, 7.6
-// Clusters of 8 large CTAs took 11.3 us for the 4097 tokens, two waves of
-// clusters (2 sequences, 32 heads on 8) 9.9 where the line takes 8.4.
+//   32 heads on 8, 128 columns, 4 sequences (two waves):  100: 8.6, 10.1;  600: 10.5, 10.3;  2000: 15.3, 12.9;
+//     4097: 18.8, 19.2
+// Clusters of 8 large CTAs took 11.3 us for the 4097 tokens of one sequence.
 // Above 16 rows the products cost: they belong on the tensor cores of
 // ns_paged_umma.cu, which want queries that TMA can fetch (16-byte aligned,
 // strides multiples of 8); other queries take 64 rows a CTA here.  Measured
