@@ -493,9 +493,9 @@ cudaError_t prepare() {
 // split them.  A call whose items fit on the GPU as clusters, all at once, with
 // up to 8 tiles to a CTA, takes clusters: of large CTAs where small ones would
 // have more than one tile each and the large ones still fit (7 clusters of 128
-// columns, three times as many of small ones).  Measured, line, small, large, one new token,
-// bf16 (us in a graph; the line with two CTAs an SM and three tiles, which is
-// up to 3 us quicker for calls of this size):
+// columns, three times as many of small ones).  Measured, line, small, large,
+// one new token, bf16 (us in a graph; the line with two CTAs an SM and three
+// tiles, which is up to 3 us quicker for calls of this size):
 //   32 heads on 8, 128 columns, 1 sequence:  100 tokens 8.4, 4.9;  4097: 12.9, 8.8;  8000: 15.2, 13.5
 //     2 sequences:  100: 8.4, 5.7;  4097: 14.4, 10.1;  8000: 17.8, 15.8
 //   28 on 4, 128 columns, 1 sequence:  100: 8.4, 5.2, 6.0;  2000: 10.2, 6.2, 6.0;  8000: 15.0, 11.9, 10.0;
