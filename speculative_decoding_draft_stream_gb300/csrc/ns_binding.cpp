@@ -124,8 +124,11 @@ at::Tensor workspace(PyObject *o, int64_t need, c10::Device d, int64_t &bytes) {
   return t;
 }
 
+// The entries that allocate run on the current stream, whose memory torch's allocator gives them.
+ns_stream current_stream(c10::Device d) { return c10::cuda::getCurrentCUDAStream(d.index()).stream(); }
+
 ns_stream stream_of(PyObject *o, c10::Device d) {
-  if (o == Py_None) return c10::cuda::getCurrentCUDAStream(d.index()).stream();
+  if (o == Py_None) return current_stream(d);
   void *p = PyLong_AsVoidPtr(o);
   if (PyErr_Occurred()) throw Failed{};
   return p;
@@ -193,7 +196,7 @@ PyObject *none() {
   return Py_None;
 }
 
-// q, k, v, cu, max_len, scale, out, lse, stream
+// q, k, v, cu, max_len, scale, out, lse
 PyObject *attend_prompt(PyObject *const *a) {
   const at::Tensor &q = tensor(a[0], "q"), &k = tensor(a[1], "k"), &v = tensor(a[2], "v"), &cu = tensor(a[3], "cu");
   const c10::Device d = device_of(q, "q");
@@ -210,12 +213,12 @@ PyObject *attend_prompt(PyObject *const *a) {
                          (int32_t)dim, q.stride(0), q.stride(1), k.stride(0), k.stride(1), v.stride(0), v.stride(1),
                          static_cast<int32_t *>(bounds), (int32_t)cu.size(0) - 1, (int32_t)integer(a[4], "max_len"),
                          real(a[5], 1.0 / std::sqrt((double)dim)), out.data_ptr(), lse.data_ptr<float>(),
-                         stream_of(a[8], d)),
+                         current_stream(d)),
         "ns_attend_prompt");
   return pair(std::move(out), std::move(lse));
 }
 
-// q, k_pages, v_pages, table, lengths, seqs, mask, scale, max_len, out, lse, workspace, stream
+// q, k_pages, v_pages, table, lengths, seqs, mask, scale, max_len, out, lse, workspace
 PyObject *attend_paged(PyObject *const *a) {
   const at::Tensor &q = tensor(a[0], "q"), &k = tensor(a[1], "k_pages"), &v = tensor(a[2], "v_pages");
   const c10::Device d = device_of(q, "q");
@@ -242,7 +245,7 @@ PyObject *attend_paged(PyObject *const *a) {
                         (int32_t)k.size(2), k.stride(0), k.stride(1), k.stride(2), v.stride(0), v.stride(1), v.stride(2),
                         table, (int32_t)ld, (int32_t)rows, lengths, seqs, mask,
                         real(a[7], 1.0 / std::sqrt((double)dim)), (int32_t)integer(a[8], "max_len"), out.data_ptr(),
-                        lse.data_ptr<float>(), ws.data_ptr(), bytes, stream_of(a[12], d)),
+                        lse.data_ptr<float>(), ws.data_ptr(), bytes, current_stream(d)),
         "ns_attend_paged");
   return pair(std::move(out), std::move(lse));
 }
@@ -313,14 +316,14 @@ PyObject *fork_(PyObject *const *a) {
   return none();
 }
 
-// cache, seqs, n_new, workspace, stream
+// cache, seqs, n_new, workspace
 PyObject *extend(PyObject *const *a) {
   Cache &c = cache_of(a[0]);
   const int64_t n = count(a[1], "seqs");
   const int32_t *seqs = ints(a[1], "seqs", c.device, {n}), *add = ints(a[2], "n_new", c.device, {n});
   int64_t bytes;
   const at::Tensor ws = workspace(a[3], ns_pages_workspace(&c.c, (int32_t)n), c.device, bytes);
-  check(ns_pages_extend(&c.c, seqs, add, (int32_t)n, ws.data_ptr(), bytes, stream_of(a[4], c.device)),
+  check(ns_pages_extend(&c.c, seqs, add, (int32_t)n, ws.data_ptr(), bytes, current_stream(c.device)),
         "ns_pages_extend");
   return none();
 }
@@ -367,7 +370,7 @@ PyObject *copy_(PyObject *const *a) {
   return none();
 }
 
-// logits, ids, k, temperature, stream
+// logits, ids, k, temperature
 PyObject *token_logprobs(PyObject *const *a) {
   const at::Tensor &x = tensor(a[0], "logits");
   const c10::Device d = device_of(x, "logits");
@@ -389,7 +392,7 @@ PyObject *token_logprobs(PyObject *const *a) {
   const int64_t ld = rows > 1 ? x.stride(0) : std::max(x.stride(0), V);
   check(ns_token_logprobs(x.data_ptr(), code(type), (int32_t)rows, (int32_t)V, ld, real(a[3], 1.0), ids, (int32_t)m,
                           (int32_t)k, out[0].data_ptr<float>(), out[1].data_ptr<float>(), out[2].data_ptr<float>(),
-                          out[3].data_ptr<int32_t>(), out[4].data_ptr<float>(), stream_of(a[4], d)),
+                          out[3].data_ptr<int32_t>(), out[4].data_ptr<float>(), current_stream(d)),
         "ns_token_logprobs");
   PyObject *r = PyTuple_New(5);
   for (int i = 0; r && i < 5; ++i) {
@@ -412,16 +415,16 @@ PyObject *set_error(PyObject *const *a) {
 #define NS_ENTRY(name, n, f) \
   { name, reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(&entry<n, f>)), METH_FASTCALL, nullptr }
 PyMethodDef g_methods[] = {NS_ENTRY("set_error", 1, set_error),
-                           NS_ENTRY("attend_prompt", 9, attend_prompt),
-                           NS_ENTRY("attend_paged", 13, attend_paged),
+                           NS_ENTRY("attend_prompt", 8, attend_prompt),
+                           NS_ENTRY("attend_paged", 12, attend_paged),
                            NS_ENTRY("cache", 5, cache),
                            NS_ENTRY("truncate", 4, truncate),
                            NS_ENTRY("fork", 4, fork_),
-                           NS_ENTRY("extend", 5, extend),
+                           NS_ENTRY("extend", 4, extend),
                            NS_ENTRY("write", 7, write),
                            NS_ENTRY("compact", 6, compact),
                            NS_ENTRY("copy", 4, copy_),
-                           NS_ENTRY("token_logprobs", 5, token_logprobs),
+                           NS_ENTRY("token_logprobs", 4, token_logprobs),
                            {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_serving", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -12,8 +12,10 @@ and calls are native (csrc/ns_binding.cpp), because the small calls take less
 time than Python would need for them.  Everything is computed in the library's
 kernels, asynchronously on ``stream`` (the current stream when it is None).
 Outputs and workspaces come from torch's caching allocator unless they are
-passed in.  Inputs used on a stream other than the one they were made on must
-be ordered by the caller, as with any torch op.
+passed in; with ``stream`` they are made on that stream, so they are never
+memory that work still queued on another one uses.  Tensors used on a stream
+other than the one they were made on (inputs, and outputs that are read
+elsewhere) must be ordered by the caller, as with any torch op.
 """
 
 from __future__ import annotations
@@ -55,10 +57,17 @@ def _other(stream):
     return None if stream.cuda_stream == torch.cuda.current_stream().cuda_stream else stream
 
 
-def _record(stream, *made) -> None:
-    """Tensors made on the current stream and used on another are not reused before that one is done with them."""
-    for t in made:
+def _on(stream, call):
+    """call() with `stream` as the current one, so that what it allocates belongs to that stream: a block that the
+    caller's stream has freed may be in use by kernels still queued there, which nothing orders before `stream`.
+    The tensors it returns are not reused before both streams are done with them."""
+    caller = torch.cuda.current_stream()
+    with torch.cuda.stream(stream):
+        r = call()
+    for t in r or ():
         t.record_stream(stream)
+        t.record_stream(caller)
+    return r
 
 
 def attend_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu: torch.Tensor, max_len: int, *,
@@ -68,10 +77,9 @@ def attend_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu: torch.T
     and head strides are free positive multiples of 8 elements), cu int32 [B + 1] the sequences' bounds, max_len the
     longest.  Returns (out [T, Hq, D], lse fp32 [T, Hq]).  scale: 1 / sqrt(D) by default."""
     s = None if stream is None else _other(stream)
-    r = _native().attend_prompt(q, k, v, cu, max_len, scale, out, lse, None if s is None else s.cuda_stream)
     if s is not None:
-        _record(s, *r)
-    return r
+        return _on(s, lambda: attend_prompt(q, k, v, cu, max_len, scale=scale, out=out, lse=lse))
+    return _native().attend_prompt(q, k, v, cu, max_len, scale, out, lse)
 
 
 def attend_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, table: torch.Tensor,
@@ -84,20 +92,12 @@ def attend_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, 
     [max_seqs] (the new tokens included), seqs int32 [B] the cache sequences; mask int64 [B, n]: bit j of word i
     set where new token i sees new token j (None: j <= i).  max_len, a bound on the lengths, only sizes the
     launch.  Returns (out [B, n, Hq, D], lse fp32 [B, n, Hq])."""
-    b = _native()
     s = None if stream is None else _other(stream)
-    if s is None:
-        return b.attend_paged(q, k_pages, v_pages, table, lengths, seqs, mask, scale, max_len, out, lse, workspace,
-                              None)
-    made = []
-    if workspace is None and q.dim() == 4 and k_pages.dim() == 4:
-        need = load_library().ns_attend_paged_workspace(q.shape[0], q.shape[1], q.shape[2], k_pages.shape[1], q.shape[3])
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
-        made.append(workspace)
-    r = b.attend_paged(q, k_pages, v_pages, table, lengths, seqs, mask, scale, max_len, out, lse, workspace,
-                       s.cuda_stream)
-    _record(s, *r, *made)
-    return r
+    if s is not None:
+        return _on(s, lambda: attend_paged(q, k_pages, v_pages, table, lengths, seqs, mask=mask, scale=scale,
+                                           max_len=max_len, out=out, lse=lse, workspace=workspace))
+    return _native().attend_paged(q, k_pages, v_pages, table, lengths, seqs, mask, scale, max_len, out, lse,
+                                  workspace)
 
 
 class KvPages:
@@ -138,17 +138,10 @@ class KvPages:
                stream=None) -> None:
         """Lengthens sequences by n_new [n] positions; a partly filled last page that others hold too is copied."""
         s = None if stream is None else _other(stream)
-        if s is None:
-            self._b.extend(self._c, seqs, n_new, workspace, None)
-            return
-        made = []
-        if workspace is None:
-            # the bookkeeping words of each sequence and the list of free pages (csrc/ns_pages.cu)
-            workspace = torch.empty(4 * (4 + 6 * len(seqs) + self.refs.shape[0]), dtype=torch.uint8,
-                                    device=self.refs.device)
-            made.append(workspace)
-        self._b.extend(self._c, seqs, n_new, workspace, s.cuda_stream)
-        _record(s, *made)
+        if s is not None:
+            _on(s, lambda: self.extend(seqs, n_new, workspace))
+        else:
+            self._b.extend(self._c, seqs, n_new, workspace)
 
     def write(self, layer: int, seqs: torch.Tensor, cu: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor,
               stream=None) -> None:
@@ -185,10 +178,9 @@ def token_logprobs(logits: torch.Tensor, ids: Optional[torch.Tensor] = None, k: 
     logits [rows, V] fp32, bf16 or fp16 with a free row stride; the distribution's entropy and log-sum-exp, and
     the k most probable tokens (ties to the smaller id)."""
     s = None if stream is None else _other(stream)
-    r = _native().token_logprobs(logits, ids, k, temperature, None if s is None else s.cuda_stream)
     if s is not None:
-        _record(s, *r)
-    return TokenLogprobs._make(r)
+        return _on(s, lambda: token_logprobs(logits, ids, k, temperature=temperature))
+    return TokenLogprobs._make(_native().token_logprobs(logits, ids, k, temperature))
 
 
 def ops_error(clear: bool = False) -> int:
