@@ -257,10 +257,13 @@ struct Cache {
 };
 constexpr const char *kCache = "ns_kv_pages";
 
+// A cache is used while its device is the current one, where the launches go.
 Cache &cache_of(PyObject *o) {
   void *p = PyCapsule_GetPointer(o, kCache);
   if (!p) throw Failed{};
-  return *static_cast<Cache *>(p);
+  Cache &c = *static_cast<Cache *>(p);
+  if (c.device.index() != c10::cuda::current_device()) refuse("the cache must be on the current CUDA device");
+  return c;
 }
 
 // k, v, table, lengths, refs (the caller keeps the tensors alive)

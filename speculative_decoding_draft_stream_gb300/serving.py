@@ -104,7 +104,7 @@ class KvPages:
     """A paged key-value cache over the caller's tensors: k and v [layers, pages, heads, page_size, dim] (any element
     type; rows of dim consecutive elements, a multiple of 16 bytes; other strides free), table int32 [max_seqs,
     pages per sequence] (-1 past a sequence's last page), lengths int32 [max_seqs], refs int32 [pages] (how many
-    sequences hold a page).  ``KvPages.new`` makes an empty one."""
+    sequences hold a page).  Its device must be the current one in every call.  ``KvPages.new`` makes an empty one."""
 
     def __init__(self, k: torch.Tensor, v: torch.Tensor, table: torch.Tensor, lengths: torch.Tensor,
                  refs: torch.Tensor):

@@ -328,3 +328,28 @@ def test_many_pages_for_one_sequence(ns):
         b = Both(ns, 1, 9100, 1, 1, 8, 2, 9050)
         b.extend([1, 0], [37, want - 37])
         b.same()
+
+
+def test_a_cache_of_another_device_is_refused(ns):
+    """Each call looks at the current device, not only the one that made the cache.  A second device is stood in for by
+    a cache whose record says so; every argument is refused before it is used."""
+    import ctypes
+
+    from test_serving_abi import Pages as Record
+
+    class Cache(ctypes.Structure):
+        _fields_ = [("c", Record), ("type", ctypes.c_int8), ("device_type", ctypes.c_int8), ("device", ctypes.c_int8)]
+
+    make = ctypes.pythonapi.PyCapsule_New
+    make.restype, make.argtypes = ctypes.py_object, [ctypes.c_void_p] * 3
+    name = ctypes.create_string_buffer(b"ns_kv_pages")
+    record = Cache(Record(layers=1, pages=4, heads=1, page_size=8, row_bytes=16, max_seqs=2, table_ld=2), 2, 1, 1)
+    c = ns.KvPages.new(1, 4, 1, 8, 8, 2, 2)
+    c._c = make(ctypes.addressof(record), ctypes.addressof(name), None)
+    one, row = i32([0]), torch.zeros(1, 1, 8, dtype=torch.int16, device="cuda")
+    for f in (lambda: c.truncate(one), lambda: c.fork(one, one), lambda: c.extend(one, one),
+              lambda: c.write(0, one, i32([0, 1]), row, row), lambda: c.compact(one, one, i32([[0]]), one),
+              lambda: c.copy(one, one)):
+        with pytest.raises(ValueError, match="current CUDA device"):
+            f()
+    assert ns.ops_error() == 0
