@@ -332,34 +332,72 @@ __global__ void __launch_bounds__(kMoveThreads) copy_pages_kernel(ns_kv_pages c,
 }
 
 // New rows of one layer: a warp per token, its 16-byte pieces of every head
-// of k and v over the lanes.
+// of k and v over the lanes.  Only the first of a repeated sequence is
+// written: up to kWarpLooks sequences each warp looks through the entries
+// before its own; of more, the CTA looks once for all of its warps.  Measured,
+// by warps and by the CTA: 8 sequences of 4001 tokens 35.6, 36.9 us; 64 of one
+// token 3.6, 3.8; 256 of one 4.1, 3.9; 8192 of one 23.7, 15.5.
+constexpr int kWarpLooks = 128;
 __global__ void __launch_bounds__(kMoveThreads) write_kernel(ns_kv_pages c, int layer, const int32_t *seqs,
                                                              const int32_t *cu, int n, const void *k_rows,
                                                              const void *v_rows, int64_t k_token, int64_t k_head,
                                                              int64_t v_token, int64_t v_head, int tokens,
                                                              uint32_t *err) {
+  __shared__ int s_seq[kMoveWarps], s_at[kMoveWarps];  // each warp's sequence, and its place in the call
+  __shared__ uint32_t s_again;                         // warps whose sequence stands before that place too
   wait_for_previous();
-  const int lane = threadIdx.x & 31;
-  const int t = blockIdx.x * kMoveWarps + (threadIdx.x >> 5);
-  if (t >= tokens) return;
-  int lo = 0;  // the last i with cu[i] <= t, a 32nd of what is left at a time
-  for (int size = n; size > 1;) {
-    const int step = (size + 31) / 32, at = lo + lane * step;
-    const uint32_t before = __ballot_sync(0xffffffffu, lane * step < size && cu[at] <= t);
-    const int last = before ? 31 - __clz(before) : 0;
-    lo += last * step;
-    size = min(step, size - last * step);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int t = blockIdx.x * kMoveWarps + warp;
+  int lo = 0, t0 = 0, t1 = 0, s = -1, len = 0;
+  if (t < tokens) {  // the last i with cu[i] <= t, a 32nd of what is left at a time
+    for (int size = n; size > 1;) {
+      const int step = (size + 31) / 32, at = lo + lane * step;
+      const uint32_t before = __ballot_sync(0xffffffffu, lane * step < size && cu[at] <= t);
+      const int last = before ? 31 - __clz(before) : 0;
+      lo += last * step;
+      size = min(step, size - last * step);
+    }
+    t0 = cu[lo], t1 = cu[lo + 1], s = seqs[lo];
+    if (seq_ok(c, s)) len = c.lengths[s];
   }
-  const int t0 = cu[lo], t1 = cu[lo + 1];
+  uint32_t again = 0;  // (found while the length is on its way)
+  if (n <= kWarpLooks) {
+#pragma unroll
+    for (int j = lane; j < kWarpLooks; j += kWarp)
+      if (j < lo && seqs[j] == s) again = 1;
+    again = __reduce_or_sync(0xffffffffu, again);
+  } else {
+    if (lane == 0) s_seq[warp] = s, s_at[warp] = t < tokens ? lo : -1;
+    if (threadIdx.x == 0) s_again = 0;
+    __syncthreads();
+    int most = 0, all = NS_MAX_PAGE_SEQS, who[kMoveWarps];
+#pragma unroll
+    for (int w = 0; w < kMoveWarps; ++w) {
+      who[w] = s_seq[w];
+      most = max(most, s_at[w]), all = min(all, s_at[w] >= 0 ? s_at[w] : all);
+    }
+    int j = threadIdx.x;
+#pragma unroll 4
+    for (; j < all; j += kMoveThreads) {  // before every warp's place
+      const int x = seqs[j];
+#pragma unroll
+      for (int w = 0; w < kMoveWarps; ++w)
+        if (x == who[w]) again |= 1u << w;
+    }
+    for (; j < most; j += kMoveThreads) {
+      const int x = seqs[j];
+#pragma unroll
+      for (int w = 0; w < kMoveWarps; ++w)
+        if (x == who[w] && j < s_at[w]) again |= 1u << w;
+    }
+    again = __reduce_or_sync(0xffffffffu, again);
+    if (lane == 0 && again) atomicOr(&s_again, again);
+    __syncthreads();
+    again = s_again >> warp & 1;
+  }
   if (t < t0 || t >= t1) return;  // a token of no sequence
-  const int s = seqs[lo];
-  if (!seq_ok(c, s)) {
-    if (lane == 0) set_flag(err, NS_FLAG_BAD_SEQ);
-    return;
-  }
-  const int len = c.lengths[s];
   const long long pos = (long long)len - (t1 - t);
-  if (!len_ok(c, len) || pos < 0) {
+  if (!seq_ok(c, s) || again || !len_ok(c, len) || pos < 0) {
     if (lane == 0) set_flag(err, NS_FLAG_BAD_SEQ);
     return;
   }

@@ -353,3 +353,32 @@ def test_a_cache_of_another_device_is_refused(ns):
         with pytest.raises(ValueError, match="current CUDA device"):
             f()
     assert ns.ops_error() == 0
+
+
+def test_write_skips_repeated_sequences(ns):
+    """The rows of the first entry of a sequence are written, those of later ones are not."""
+    b = Both(ns, 1, 40, 2, 8, 8, 6, 5)
+    b.extend([0, 1, 2], [20, 9, 3])
+    k, v = (torch.randint(-100, 100, (37, 2, 8), generator=b.g).to(torch.int16) for _ in range(2))
+    # 20 tokens of sequence 0, 9 of 1, then 3 of 0 again, 2 of 1 again, 3 of 2
+    b.c.write(0, i32([0, 1, 0, 1, 2]), i32([0, 20, 29, 32, 34, 37]), k.cuda(), v.cuda())
+    b.r.write(0, [0, 1], [0, 20, 29], k.numpy(), v.numpy())
+    b.r.write(0, [2], [0, 3], k.numpy()[34:], v.numpy()[34:])
+    b.same(ns.FLAG_BAD_SEQ)
+
+
+def test_write_of_many_sequences_with_repeated_ones(ns):
+    n = 2100
+    b = Both(ns, 1, n + 10, 1, 4, 8, n, 2)
+    ids = list(range(n))
+    random.Random(4).shuffle(ids)
+    b.extend(ids, [1 + i % 3 for i in range(n)])
+    b.same()
+    b.write(0, ids, [1 + i % 3 for i in range(n)])
+    b.same()
+    seqs = ids[:1500] + ids[7:9] + ids[1500:] + ids[-1:]
+    k, v = (torch.randint(-100, 100, (len(seqs), 1, 8), generator=b.g).to(torch.int16) for _ in range(2))
+    b.c.write(0, i32(seqs), i32(list(range(len(seqs) + 1))), k.cuda(), v.cuda())
+    first = [i for i, s in enumerate(seqs) if s not in seqs[:i]]
+    b.r.write(0, [seqs[i] for i in first], list(range(len(first) + 1)), k.numpy()[first], v.numpy()[first])
+    b.same(ns.FLAG_BAD_SEQ)
