@@ -9,6 +9,7 @@
  * handle and allocate nothing: what they keep between their kernels goes into
  * a workspace that the caller gives, and may be used again by the next call
  * on the same stream.  Strides are in elements unless a name says bytes.
+ * Pointers are aligned to what they point to (NS_ERR_ARG), or as a call says.
  *
  * Problems that only the device can see (a sequence, page or token id out of
  * range, no free page) set a sticky flag in a word of the library, one for

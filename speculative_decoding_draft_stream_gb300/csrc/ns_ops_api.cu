@@ -42,6 +42,11 @@ ns_status current(const Device **out) {
 ns_status done(cudaError_t e) { return e == cudaSuccess ? NS_OK : NS_ERR_CUDA; }
 
 bool aligned(const void *p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+// Whether each pointer may be read as 32-bit words (NULL may).
+template <typename... P>
+bool words(const P *...p) {
+  return (... && aligned(p, 4));
+}
 
 bool attn_type(int dtype, int dim) {
   return (dtype == NS_DTYPE_BF16 || dtype == NS_DTYPE_F16) && (dim == 64 || dim == 128);
@@ -158,7 +163,7 @@ ns_status ns_attend_paged(const void *d_q, int32_t dtype, int32_t n_seqs, int32_
 
 ns_status ns_pages_truncate(const ns_kv_pages *c, const int32_t *d_seqs, const int32_t *d_new_len, int32_t n,
                             ns_stream stream) {
-  if (!cache_ok(c) || !page_seqs(n) || (n > 0 && !d_seqs)) return NS_ERR_ARG;
+  if (!cache_ok(c) || !page_seqs(n) || (n > 0 && !d_seqs) || !words(d_seqs, d_new_len)) return NS_ERR_ARG;
   if (n == 0) return NS_OK;
   const Device *d = nullptr;
   if (ns_status s = current(&d)) return s;
@@ -167,7 +172,7 @@ ns_status ns_pages_truncate(const ns_kv_pages *c, const int32_t *d_seqs, const i
 
 ns_status ns_pages_fork(const ns_kv_pages *c, const int32_t *d_src, const int32_t *d_dst, int32_t n,
                         ns_stream stream) {
-  if (!cache_ok(c) || !page_seqs(n) || (n > 0 && (!d_src || !d_dst))) return NS_ERR_ARG;
+  if (!cache_ok(c) || !page_seqs(n) || (n > 0 && (!d_src || !d_dst)) || !words(d_src, d_dst)) return NS_ERR_ARG;
   if (n == 0) return NS_OK;
   const Device *d = nullptr;
   if (ns_status s = current(&d)) return s;
@@ -180,7 +185,8 @@ int64_t ns_pages_workspace(const ns_kv_pages *c, int32_t n) {
 
 ns_status ns_pages_extend(const ns_kv_pages *c, const int32_t *d_seqs, const int32_t *d_n_new, int32_t n, void *d_ws,
                           int64_t ws_bytes, ns_stream stream) {
-  if (!cache_ok(c) || !page_seqs(n) || (n > 0 && (!d_seqs || !d_n_new || !d_ws || !aligned(d_ws, 16))))
+  if (!cache_ok(c) || !page_seqs(n) || (n > 0 && (!d_seqs || !d_n_new || !d_ws || !aligned(d_ws, 16))) ||
+      !words(d_seqs, d_n_new))
     return NS_ERR_ARG;
   if (n == 0) return NS_OK;
   if (ws_bytes < ns::pages_extend_ws(*c, n)) return NS_ERR_ARG;
@@ -195,7 +201,7 @@ ns_status ns_pages_write(const ns_kv_pages *c, int32_t layer, const int32_t *d_s
   if (!cache_ok(c) || layer < 0 || layer >= c->layers || !page_seqs(n) || tokens < 0) return NS_ERR_ARG;
   if (n == 0 || tokens == 0) return NS_OK;
   if (!d_seqs || !d_cu || !d_k_new || !d_v_new || !aligned(d_k_new, 16) || !aligned(d_v_new, 16) || k_token % 16 ||
-      k_head % 16 || v_token % 16 || v_head % 16)
+      k_head % 16 || v_token % 16 || v_head % 16 || !words(d_seqs, d_cu))
     return NS_ERR_ARG;
   const Device *d = nullptr;
   if (ns_status s = current(&d)) return s;
@@ -206,7 +212,7 @@ ns_status ns_pages_write(const ns_kv_pages *c, int32_t layer, const int32_t *d_s
 ns_status ns_pages_compact(const ns_kv_pages *c, const int32_t *d_seqs, const int32_t *d_base, const int32_t *d_keep,
                            int32_t keep_ld, const int32_t *d_n_keep, int32_t n, ns_stream stream) {
   if (!cache_ok(c) || !page_seqs(n) || keep_ld < 0 || (n > 0 && (!d_seqs || !d_base || !d_n_keep)) ||
-      (n > 0 && keep_ld > 0 && !d_keep))
+      (n > 0 && keep_ld > 0 && !d_keep) || !words(d_seqs, d_base, d_keep, d_n_keep))
     return NS_ERR_ARG;
   if (n == 0) return NS_OK;
   const Device *d = nullptr;
@@ -217,7 +223,7 @@ ns_status ns_pages_compact(const ns_kv_pages *c, const int32_t *d_seqs, const in
 
 ns_status ns_pages_copy(const ns_kv_pages *c, const int32_t *d_src, const int32_t *d_dst, int32_t n,
                         ns_stream stream) {
-  if (!cache_ok(c) || n < 0 || (n > 0 && (!d_src || !d_dst))) return NS_ERR_ARG;
+  if (!cache_ok(c) || n < 0 || (n > 0 && (!d_src || !d_dst)) || !words(d_src, d_dst)) return NS_ERR_ARG;
   if (n == 0) return NS_OK;
   const Device *d = nullptr;
   if (ns_status s = current(&d)) return s;
@@ -234,7 +240,8 @@ ns_status ns_token_logprobs(const void *d_logits, int32_t dtype, int32_t rows, i
     return NS_ERR_ARG;
   if (rows == 0) return NS_OK;
   if (rows > (1 << 27) || !d_logits || !aligned(d_logits, dtype == NS_DTYPE_F32 ? 4 : 2) ||
-      (n_ids > 0 && (!d_ids || !d_logprobs)) || (k > 0 && (!d_top_ids || !d_top_logprobs)))
+      (n_ids > 0 && (!d_ids || !d_logprobs)) || (k > 0 && (!d_top_ids || !d_top_logprobs)) ||
+      !words(d_ids, d_logprobs, d_entropy, d_lse, d_top_ids, d_top_logprobs))
     return NS_ERR_ARG;
   const Device *d = nullptr;
   if (ns_status s = current(&d)) return s;

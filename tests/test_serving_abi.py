@@ -156,3 +156,29 @@ def test_header_and_python_have_the_same_limits():
         assert f"#define NS_{name} {getattr(serving, name)}" in text
     for name in ("NO_PAGES", "BAD_SEQ", "SHARED_PAGE"):
         assert f"#define NS_FLAG_{name} {getattr(serving, 'FLAG_' + name):#x}u" in text
+
+
+@pytest.mark.parametrize("off", [1, 2, 3])
+def test_pages_refuse_integers_off_their_boundary(lib, off):
+    c, a, x = cache(), P(16), P(16 + off)
+    assert lib.ns_pages_truncate(c, x, a, 1, None) == ARG
+    assert lib.ns_pages_truncate(c, a, x, 1, None) == ARG
+    assert lib.ns_pages_fork(c, x, a, 1, None) == ARG
+    assert lib.ns_pages_fork(c, a, x, 1, None) == ARG
+    assert lib.ns_pages_extend(c, x, a, 1, a, 1 << 40, None) == ARG
+    assert lib.ns_pages_extend(c, a, x, 1, a, 1 << 40, None) == ARG
+    assert lib.ns_pages_write(c, 0, x, a, 1, a, a, 256, 128, 256, 128, 4, None) == ARG
+    assert lib.ns_pages_write(c, 0, a, x, 1, a, a, 256, 128, 256, 128, 4, None) == ARG
+    for place in range(4):
+        args = [a, a, a, a]
+        args[place] = x
+        assert lib.ns_pages_compact(c, args[0], args[1], args[2], 4, args[3], 1, None) == ARG
+    assert lib.ns_pages_copy(c, x, a, 1, None) == ARG
+    assert lib.ns_pages_copy(c, a, x, 1, None) == ARG
+
+
+@pytest.mark.parametrize("place", range(6))
+@pytest.mark.parametrize("off", [1, 2, 3])
+def test_logprobs_refuse_words_off_their_boundary(lib, place, off):
+    w = [P(16 + off if i == place else 16) for i in range(6)]  # ids, log probabilities, entropy, lse, top ids, theirs
+    assert lib.ns_token_logprobs(P(16), 2, 2, 10, 10, ctypes.c_float(1.0), w[0], 1, 2, *w[1:], None) == ARG
