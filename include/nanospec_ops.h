@@ -75,8 +75,9 @@ NS_API ns_status ns_attend_prompt(const void *d_q, const void *d_k, const void *
  * d_table[s * table_ld + p / page_size], row p % page_size.  New token i (at
  * position len - n + i) sees every position before len - n, and new token j
  * where bit j of d_mask[b * n + i] is set; d_mask NULL means j <= i (a chain).
- * A row that sees nothing (len 0, or an empty mask and no context) gives
- * zeros and an lse of -inf.
+ * No row sees the positions of a page whose id is out of range
+ * (NS_FLAG_BAD_ID).  A row that sees nothing (len 0, or an empty mask and no
+ * context) gives zeros and an lse of -inf.
  *   d_q    [n_seqs x n x q_heads x dim], strides in elements (even; with positive multiples of 8 and 16-byte
  *          alignment more than 16 rows, n * q_heads / kv_heads, are faster)
  *   d_k, d_v  [n_pages x kv_heads x page_size x dim] of one layer, strides in

@@ -63,6 +63,10 @@ __host__ __device__ constexpr int pa_smem() {
   return kStages<D, W> * pa_stage<D, W>() + (W != kLine ? 16 * (D + 2) * 4 : WM == 1 ? 32 * D / 2 * 4 + kMerge : 0);
 }
 
+// CTAs that an SM is to hold: as many as their shared memory allows (64 rows: their registers).
+template <int D, int WM, int W>
+constexpr int kResident = W == kLarge ? (D == 128 ? 1 : 2) : WM == 1 ? kPerSm<D> : (D == 128 ? 2 : 3);
+
 template <int W>
 __host__ __device__ inline long long pa_tiles(int len) {
   return len > 0 ? (len - 1) / kKeys<W> + 1 : 1;
@@ -103,7 +107,8 @@ __device__ __forceinline__ void push(uint32_t a, float x) {
 
 // (Clusters: at most 16 rows.)
 template <typename T, int D, int WM, int W>
-__global__ void __launch_bounds__(kThreads<W>) paged_attn_kernel(const PagedAttnArgs a, int blocks) {
+__global__ void __launch_bounds__(kThreads<W>, kResident<D, WM, W>)
+    paged_attn_kernel(const PagedAttnArgs a, int blocks) {
   constexpr int kPaThreads = kThreads<W>, kPaKeys = kKeys<W>, kWarps = kPaThreads / kWarp;
   constexpr int WK = kWarps / WM, NK = kPaKeys / WK, kRows = 16 * WM;
   constexpr int kLanesRow = D / 8;                    // threads that fetch a row
@@ -177,7 +182,8 @@ __global__ void __launch_bounds__(kThreads<W>) paged_attn_kernel(const PagedAttn
   }
   Cursor<W> cu = ld;
 
-  // page ids of the load cursor's tile, one for each eight rows, in as many lanes
+  // page ids of the load cursor's tile, one for each eight rows, in as many lanes (-1: past the sequence's end, -2: out
+  // of range)
   auto fetch_ids = [&]() {
     int id = -1;
     if (lane < kPaKeys / 8) {
@@ -186,7 +192,7 @@ __global__ void __launch_bounds__(kThreads<W>) paged_attn_kernel(const PagedAttn
         id = ld.table[p >> a.page_shift];
         if (id < 0 || id >= a.n_pages) {
           set_flag(a.err, NS_FLAG_BAD_ID);
-          id = -1;
+          id = -2;
         }
       }
     }
@@ -219,9 +225,15 @@ __global__ void __launch_bounds__(kThreads<W>) paged_attn_kernel(const PagedAttn
   long long left_ld = t1 - t0;
   int ids = fetch_ids();
   int st_ld = 0;
+  constexpr int kAhead = kStages<D, W> - 1;
+  uint32_t missing[kAhead] = {};  // of each tile in flight: its eights of rows without a page
   auto issue = [&]() {
+#pragma unroll
+    for (int i = 0; i + 1 < kAhead; ++i) missing[i] = missing[i + 1];
+    missing[kAhead - 1] = 0;
     if (left_ld > 0) {
       fetch(ids, st_ld);
+      missing[kAhead - 1] = __ballot_sync(0xffffffffu, ids == -2);
       st_ld = st_ld + 1 == kStages<D, W> ? 0 : st_ld + 1;
       --left_ld;
       if (left_ld > 0) {
@@ -232,7 +244,7 @@ __global__ void __launch_bounds__(kThreads<W>) paged_attn_kernel(const PagedAttn
     cp_commit();
   };
 #pragma unroll
-  for (int i = 0; i < kStages<D, W> - 1; ++i) issue();
+  for (int i = 0; i < kAhead; ++i) issue();
 
   Rows<T, D> rows;
   if (W != kLine) rows.clear();  // (a CTA of a short sequence may have no tile)
@@ -262,13 +274,14 @@ __global__ void __launch_bounds__(kThreads<W>) paged_attn_kernel(const PagedAttn
         }
       }
     }
-    cp_wait<kStages<D, W> - 2>();
+    cp_wait<kAhead - 1>();
     __syncthreads();  // the tile is there for everyone, and everyone is done with the stage to be filled next
+    const uint32_t gone = missing[0];
     issue();
     const uint32_t sk = s0 + st * pa_stage<D, W>(), sv = sk + kPaKeys * D * 2;
     st = st + 1 == kStages<D, W> ? 0 : st + 1;
     const int ctx = cu.len - a.n, p0 = cu.tile * kPaKeys, k0 = wk * NK;
-    if (p0 + kPaKeys <= ctx) {
+    if (p0 + kPaKeys <= ctx && !gone) {
       rows.template tile<NK, false>(q, sk, sv, k0, c, [](int, int) { return false; }, false);
     } else {
       const int n = a.n, j0 = p0 + k0 - ctx;  // the first key's node
@@ -279,7 +292,7 @@ __global__ void __launch_bounds__(kThreads<W>) paged_attn_kernel(const PagedAttn
           q, sk, sv, k0, c,
           [&](int h, int key) {
             const int j = j0 + key;
-            return j >= 0 && (j >= n || !((word[h] >> j) & 1));
+            return (j >= 0 && (j >= n || !((word[h] >> j) & 1))) || (gone >> ((k0 + key) >> 3) & 1);
           },
           wild);
     }

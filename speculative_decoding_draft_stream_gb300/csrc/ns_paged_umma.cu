@@ -7,7 +7,7 @@
 // all items' tiles (ns_paged_attn.cuh).  Keys and values come page by page:
 // each page's part of a tile is one TMA box for each 64 columns, its id
 // fetched a tile ahead.  A page id out of range is a box outside the tensor,
-// which reads as zeros.  Every row sees the context whole; in the tiles from
+// which reads as zeros; no row sees its places.  Every row sees the context whole; in the tiles from
 // there on a row sees the new tokens of its mask, and what lies behind the
 // sequence's end is put to zero before it is used.
 //
@@ -167,12 +167,16 @@ struct Mode {
     }
     template <int D>
     __device__ __forceinline__ void keys(const TreeArgs &a, const Work &w, int j, int kv, uint32_t dst,
-                                         const CUtensorMap *m, uint32_t bar, int lane) {
+                                         const CUtensorMap *m, uint32_t bar, int lane, uint32_t *missing) {
+      const int n = pages(a, w, j), page = 1 << a.page_shift, rows = min(page, kKeys);
       if (kv == 0) {
         ids = next;
         next = fetch(a, w, j + 1, lane);
+        // pages out of range, then the tile's eights of keys that lie in them
+        uint32_t out = __ballot_sync(0xffffffffu, lane < n && ids == a.n_pages);
+        if (out) out = __ballot_sync(0xffffffffu, lane < kKeys / 8 && (out >> (lane * 8 / rows) & 1));
+        if (lane == 0) *missing = out;
       }
-      const int n = pages(a, w, j), page = 1 << a.page_shift, rows = min(page, kKeys);
       if (lane == 0) mbar_expect_tx(bar, n * rows * D * 2);
       __syncwarp();
       if (lane < n) {

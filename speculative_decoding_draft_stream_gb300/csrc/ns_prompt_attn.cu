@@ -135,7 +135,7 @@ struct Mode {
     }
     template <int D>
     __device__ __forceinline__ void keys(const FaArgs &a, const Work &w, int j, int, uint32_t dst,
-                                         const CUtensorMap *m, uint32_t bar, int lane) {
+                                         const CUtensorMap *m, uint32_t bar, int lane, uint32_t *) {
       if (lane == 0) {
         mbar_expect_tx(bar, kKeys * D * 2);
         for (int h = 0; h < D / 64; ++h)

@@ -79,6 +79,7 @@ constexpr int kKeys = 128;           // keys of a tile
 constexpr int kHalf = 128 * 128;     // bytes of 128 rows of 64 elements
 constexpr float kLimit = 32768.f;    // a sum of 64 probabilities above this says that m is too low
 constexpr int kChecks = 4;           // value tiles looked through ahead of the product
+constexpr int kMissingTiles = 4;     // key tiles whose missing keys are kept (see there)
 constexpr int kWorkReaders = 11;     // loads, products, hidden values, and the eight softmax warps
 constexpr int kWorkBytes = 48;
 
@@ -96,7 +97,8 @@ struct Smem {
                        kQEmpty = kQFull + 8, kSFull = kQEmpty + 8, kPFull = kSFull + 16, kPvHalf = kPFull + 32,
                        kOFull = kPvHalf + 16, kOEmpty = kOFull + 16, kCheck = kOEmpty + 16,
                        kMerge = kCheck + 8 * kChecks, kWFull = kMerge + 16, kWEmpty = kWFull + 16, kSlot = kWEmpty + 16, kWork = kSlot + 16,
-                       kWildAny = kWork + 2 * kWorkBytes, kWild = kWildAny + 16,
+                       kWildAny = kWork + 2 * kWorkBytes, kMissing = kWildAny + 16,
+                       kWild = kMissing + 4 * kMissingTiles,
                        kEnd = kWild + 2 * (int)sizeof(typename M::Wild);
   static constexpr int kBytes = kEnd + 1024;  // the base is rounded up to 1024 bytes
   static_assert(kBytes <= 232448, "shared memory of a CTA");
@@ -116,6 +118,12 @@ __device__ __forceinline__ bool get_work(uint32_t base, int full, const uint8_t 
   if (!umma::inline_wait(base + full + 8 * (i & 1), (i >> 1) & 1, err)) return false;
   w = *reinterpret_cast<const Work *>(g + work_off + kWorkBytes * (i & 1));
   return w.n0 > 0;
+}
+
+// The keys that eight bits say are there no page for, eight keys a bit.
+__device__ __forceinline__ uint64_t eights(uint32_t bits) {
+  const uint64_t x = (bits & 0xffu) * 0x0101010101010101ull & 0x8040201008040201ull;  // byte e: whether bit e is set
+  return (uint64_t)__vcmpne4((uint32_t)(x >> 32), 0u) << 32 | __vcmpne4((uint32_t)x, 0u);
 }
 
 // Where the value of column d, key r of a value tile lies in it.
@@ -182,6 +190,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     Work w;
     typename M::Loader loader;
     int it = 0;  // ring position: K0 V0 K1 V1 ... over all items
+    // Key tile x (over all items) leaves its missing keys in word x % kMissingTiles.  They are read before the
+    // softmax hands over tile x's probabilities, scores of tile x + 1 are issued after that, and key tile x + 3 is
+    // loaded after those are over: a word is not written again before it was read.
+    static_assert(!M::kParts || kMissingTiles > kRing / 2, "the words outlive their tiles");
+    uint32_t *missing = reinterpret_cast<uint32_t *>(g + L::kMissing);
     bool ok = true;
     auto wait = [&](uint32_t bar, int phase) {
       return __all_sync(0xffffffffu, umma::inline_wait(base + bar, phase & 1, err));
@@ -206,7 +219,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int s = it % kRing;
           if (it >= kRing && !(ok = wait(L::kKvEmpty + 8 * s, it / kRing - 1))) break;
           loader.template keys<D>(a, w, j, kv, base + L::kKV + s * L::kTile, kv ? &tmV : &tmK,
-                                  base + L::kKvFull + 8 * s, lane);
+                                  base + L::kKvFull + 8 * s, lane, missing + it / 2 % kMissingTiles);
         }
       }
     }
@@ -448,6 +461,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     Work w;
     int ns = 0, items = 0;  // scores awaited, items of this row tile begun
     int merged = 0;         // items whose two accumulators were added up (M::kSplit)
+    int passed = 0;         // key tiles of the items before (M::kParts)
     bool ok = true;
     for (int i = 0; ok; ++i) {
       const bool more = get_work(base, L::kWFull, g, L::kWork, i, w, err);
@@ -464,8 +478,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int key_tile = M::kSplit ? 2 * j + t : j;
         uint32_t s[128], p[32];
         float sum;
+        // (only a cache's pages may be missing)
+        const uint32_t missing =
+            M::kParts ? *(reinterpret_cast<volatile uint32_t *>(g + L::kMissing) + (passed + j) % kMissingTiles) : 0u;
+        const bool masked = key_tile >= w.hidden || (M::kParts && missing != 0);
         auto mask = [&](int from) {  // keys that the row does not see, among 64
-          const uint64_t sees = row.sees(w, key_tile, from);
+          uint64_t sees = row.sees(w, key_tile, from);
+          if (M::kParts && missing) sees &= ~eights(missing >> (from / 8));
           NS_FA_MASK(s, from, sees)
         };
         auto most = [&](int from) {
@@ -517,11 +536,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         umma::wait_ld();
         umma::ld32(tS + 64, s + 64);
         umma::ld32(tS + 96, s + 96);
-        if (key_tile >= w.hidden) mask(0);
+        if (masked) mask(0);
         bool whole = false;  // the second half has come
         if (j == 0) {
           umma::wait_ld();
-          if (key_tile >= w.hidden) mask(64);
+          if (masked) mask(64);
           whole = true;
           m = fmaxf(most(0), most(64));
         }
@@ -530,7 +549,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const bool low = live && (sum > kLimit || m == kNegInf);
           if (__any_sync(0xffffffffu, low)) {
             umma::wait_ld();
-            if (key_tile >= w.hidden) mask(64);
+            if (masked) mask(64);
             whole = true;
             // the accumulator is still: S of this tile came after the last product into it
             raise(low, fmaxf(most(0), most(64)));
@@ -544,7 +563,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         l += sum;
         if (!whole) {
           umma::wait_ld();
-          if (key_tile >= w.hidden) mask(64);
+          if (masked) mask(64);
         }
         probabilities(64);
         if (j > 0) {
@@ -565,6 +584,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
       }
       if (!ok) break;
+      passed += key_tiles<M>(w);
       if (nt > 0) {
         ok = __all_sync(0xffffffffu, umma::inline_wait(base + L::kOFull + 8 * t, items & 1, err));
         if (!ok) break;

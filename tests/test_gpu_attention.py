@@ -670,3 +670,66 @@ def test_prompt_scores_that_rise_by_key_tile(ns, hq):
 def test_prompt_few_long_items(ns, lens, hq, hkv, d):
     """Keys split over the two halves of a CTA: even and odd numbers of tiles, several items to a CTA."""
     run_prompt(ns, lens, hq, hkv, d, BF16, 72)
+
+
+def run_missing_pages(ns, lens, n, hq, hkv, d, P, dtype, seed, share=0.3, masks=None, unaligned=False, all_of=()):
+    """Some page ids out of range: no row sees their positions, and everything else is as it is."""
+    g, rng = gen(seed), random.Random(seed)
+    dk, dv, table, keys, vals = make_cache(g, rng, lens, hkv, P, d, dtype)
+    B = len(lens)
+    there = []
+    for b, N in enumerate(lens):
+        gone = [rng.random() < share or b in all_of for _ in range(-(-N // P))]
+        for slot, x in enumerate(gone):
+            if x:
+                table[b, slot] = rng.choice([-1, -(1 << 31), dk.shape[0], (1 << 31) - 1])
+        there.append(torch.tensor([not gone[p // P] for p in range(N)], dtype=torch.bool))
+    q = normal(g, (B, n, hq, d), dtype)
+    if masks == "tree":
+        masks = tree_masks(rng, B, n)
+    dq = q.cuda()
+    if unaligned:
+        dq = torch.zeros((B, n, hq, d + 2), dtype=dtype, device="cuda")[..., 2:]
+        dq.copy_(q)
+    i32 = {"dtype": torch.int32, "device": "cuda"}
+    out, lse = ns.attend_paged(dq, dk, dv, table.cuda(), torch.tensor(lens, **i32), torch.arange(B, **i32),
+                               mask=None if masks is None else signed(masks).cuda())
+    out, lse = out.cpu(), lse.cpu()
+    assert ns.ops_error(clear=True) == (0x1 if not all(t.all() for t in there) else 0)
+    for b, N in enumerate(lens):
+        sees = torch.zeros(n, N, dtype=torch.bool)
+        for i in range(n):
+            word = (1 << (i + 1)) - 1 if masks is None else masks[b][i]
+            for p in range(N):
+                sees[i, p] = p < N - n or bool(word >> (p - N + n) & 1)
+        sees &= there[b]
+        for h in range(hq):
+            kh = h // (hq // hkv)
+            o, z, to, tz = attend_rows(q[b, :, h], keys[b][:, kh], vals[b][:, kh], sees, d ** -0.5)
+            check(out[b, :, h], o, to, f"out of sequence {b} head {h}")
+            check(lse[b, :, h], z, tz, f"lse of sequence {b} head {h}")
+
+
+@pytest.mark.parametrize("P", [8, 16, 64, 128, 256])
+@pytest.mark.parametrize("d,dtype", [(64, F16), (128, BF16)])
+def test_paged_missing_pages_are_seen_by_no_row(ns, P, d, dtype):
+    few = [700, 1, 130]                                  # clusters
+    many = [(300, 40, 777, 64, 129, 8)[i % 6] + i for i in range(40)]  # one line of tiles
+    run_missing_pages(ns, few, 1, 4, 2, d, P, dtype, 80 + P)
+    run_missing_pages(ns, [5000], 1, 8, 1, d, P, dtype, 81 + P)
+    run_missing_pages(ns, many, 1, 4, 4, d, P, dtype, 82 + P)
+    run_missing_pages(ns, [x + 5 for x in few], 5, 3, 1, d, P, dtype, 83 + P, masks="tree")
+    run_missing_pages(ns, [x + 40 for x in few], 40, 4, 2, d, P, dtype, 84 + P, masks="tree")
+    run_missing_pages(ns, [x + 33 for x in few], 33, 4, 2, d, P, dtype, 85 + P, unaligned=True)
+
+
+def test_paged_sequences_of_missing_pages_only(ns):
+    for n, hq, seed in ((1, 4, 90), (20, 8, 91)):
+        run_missing_pages(ns, [300, 41, 500], n, hq, 2, 64, 16, BF16, seed, share=0.0, all_of=(0, 2))
+        run_missing_pages(ns, [300, 41, 500], n, hq, 2, 128, 16, F16, seed, share=1.0)
+
+
+def test_paged_missing_pages_of_several_long_items_to_a_cta(ns):
+    lens = [150 + 47 * i for i in range(20)]
+    run_missing_pages(ns, lens, 24, 16, 16, 64, 16, BF16, 92, share=0.1, masks="tree")
+    run_missing_pages(ns, lens, 60, 16, 4, 128, 64, F16, 93, share=0.4, masks="tree")
