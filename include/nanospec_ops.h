@@ -199,6 +199,8 @@ NS_API ns_status ns_pages_copy(const ns_kv_pages *c, const int32_t *d_src, const
  *             NS_MAX_ALTERNATIVES): ordered by logit, ties to the smaller id, as
  *             every top-k of this library; NaN never ranks, places left over
  *             hold -1 and -inf
+ *   temperature  positive, and log2(e) / temperature finite in fp32 (from
+ *             about 4.3e-39 on)
  * A logit of -inf has probability 0.  A row of nothing but -inf has lse and
  * log probabilities of -inf and entropy 0; a row that holds a NaN or +inf has
  * NaN for each of these values, as the formula does.  Sums are fp32.

@@ -236,7 +236,7 @@ ns_status ns_token_logprobs(const void *d_logits, int32_t dtype, int32_t rows, i
                             ns_stream stream) {
   if (dtype < NS_DTYPE_BF16 || dtype > NS_DTYPE_F32 || rows < 0 || V < 1 || V > (1 << 30) || ld < V || n_ids < 0 ||
       k < 0 || k > NS_MAX_ALTERNATIVES || !std::isfinite(temperature) || !(temperature > 0.f) ||
-      !std::isfinite(1.f / temperature))
+      !std::isfinite(1.f / temperature * 1.4426950408889634f))  // the kernels' log2(e) / T
     return NS_ERR_ARG;
   if (rows == 0) return NS_OK;
   if (rows > (1 << 27) || !d_logits || !aligned(d_logits, dtype == NS_DTYPE_F32 ? 4 : 2) ||

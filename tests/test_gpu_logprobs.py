@@ -221,3 +221,17 @@ def test_refusals(ns):
         with pytest.raises(ns.NanoSpecError):
             f()
     assert ns.token_logprobs(x[:0], ids[:0], 3).top_ids.shape == (0, 3)
+
+
+@pytest.mark.parametrize("t", [4.3e-39, 1e-38, 1e-30, 1e30, 1e37])
+def test_extreme_temperatures(ns, t):
+    """One token has all the probability, or each the same; nothing is NaN."""
+    x = torch.tensor([[1.0, 3.0, -2.0, 0.5], [0.0, -1.0, -1.0, -3.0]])
+    ids = torch.tensor([[1, 0], [0, 3]], dtype=torch.int32)
+    r = ns.token_logprobs(x.cuda(), ids.cuda(), 1, temperature=t)
+    assert not any(torch.isnan(v.float()).any() for v in r) and r.top_ids[:, 0].tolist() == [1, 0]
+    if t < 1:
+        assert r.logprobs[:, 0].tolist() == [0.0, 0.0] and r.entropy.tolist() == [0.0, 0.0]
+        assert (r.logprobs[:, 1] < -1e29).all()
+    else:
+        assert (r.logprobs.cpu() + math.log(4)).abs().max() < 1e-6 and (r.entropy.cpu() - math.log(4)).abs().max() < 1e-6

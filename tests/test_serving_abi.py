@@ -182,3 +182,10 @@ def test_pages_refuse_integers_off_their_boundary(lib, off):
 def test_logprobs_refuse_words_off_their_boundary(lib, place, off):
     w = [P(16 + off if i == place else 16) for i in range(6)]  # ids, log probabilities, entropy, lse, top ids, theirs
     assert lib.ns_token_logprobs(P(16), 2, 2, 10, 10, ctypes.c_float(1.0), w[0], 1, 2, *w[1:], None) == ARG
+
+
+@pytest.mark.parametrize("t", [1e-45, 2.9e-39, 3e-39, 4.2e-39, float("inf")])
+def test_logprobs_refuse_temperatures_whose_inverse_overflows(lib, t):
+    """The kernels work in powers of two: log2(e) / T has to be finite, not 1 / T alone."""
+    w = [P(16)] * 6
+    assert lib.ns_token_logprobs(P(16), 2, 2, 10, 10, ctypes.c_float(t), w[0], 1, 2, *w[1:], None) == ARG
