@@ -55,7 +55,7 @@ NS_API ns_status ns_ops_get_error(uint32_t *flags, int32_t clear);
  *   d_cu  int32 [n_seqs + 1]: sequence s holds tokens d_cu[s] .. d_cu[s+1] - 1
  *         (0 first, not decreasing, `tokens` last; empty sequences are fine)
  *   max_len  HOST: no sequence is longer (tokens past it are not computed and
- *         flag NS_FLAG_BAD_SEQ)
+ *         flag NS_FLAG_BAD_SEQ; with 0, or no sequences, the call does nothing)
  *   d_out [tokens x q_heads x dim] of `dtype`, contiguous; d_lse fp32 [tokens x q_heads] or NULL
  * dim is 64 or 128.  Scores, softmax sums and the output's sums are fp32; the
  * probabilities are rounded to `dtype` before the product with v.  A value of

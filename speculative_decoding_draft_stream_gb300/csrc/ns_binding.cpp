@@ -208,10 +208,12 @@ PyObject *attend_prompt(PyObject *const *a) {
   void *bounds = given(cu, "cu", at::kInt, d);
   if (cu.dim() != 1 || cu.size(0) < 1) refuse("cu must have one more entry than there are sequences");
   fits(T, "tokens"), fits(hq, "q_heads"), fits(cu.size(0), "cu");
+  const int64_t max_len = integer(a[4], "max_len");
+  if (T > 0 && (max_len == 0 || cu.size(0) == 1)) refuse("tokens without a sequence: cu and max_len leave them out");
   at::Tensor out = output(a[6], "out", {T, hq, dim}, type, d), lse = output(a[7], "lse", {T, hq}, at::kFloat, d);
   check(ns_attend_prompt(q.data_ptr(), k.data_ptr(), v.data_ptr(), code(type), (int32_t)T, (int32_t)hq, (int32_t)hkv,
                          (int32_t)dim, q.stride(0), q.stride(1), k.stride(0), k.stride(1), v.stride(0), v.stride(1),
-                         static_cast<int32_t *>(bounds), (int32_t)cu.size(0) - 1, (int32_t)integer(a[4], "max_len"),
+                         static_cast<int32_t *>(bounds), (int32_t)cu.size(0) - 1, (int32_t)max_len,
                          real(a[5], 1.0 / std::sqrt((double)dim)), out.data_ptr(), lse.data_ptr<float>(),
                          current_stream(d)),
         "ns_attend_prompt");

@@ -733,3 +733,16 @@ def test_paged_missing_pages_of_several_long_items_to_a_cta(ns):
     lens = [150 + 47 * i for i in range(20)]
     run_missing_pages(ns, lens, 24, 16, 16, 64, 16, BF16, 92, share=0.1, masks="tree")
     run_missing_pages(ns, lens, 60, 16, 4, 128, 64, F16, 93, share=0.4, masks="tree")
+
+
+def test_prompt_tokens_without_sequences_are_refused(ns):
+    """A call that could compute nothing of its outputs."""
+    q = torch.zeros(10, 4, 64, dtype=BF16, device="cuda")
+    k = torch.zeros(10, 2, 64, dtype=BF16, device="cuda")
+    cu = torch.tensor([0, 10], dtype=torch.int32, device="cuda")
+    for args in ((cu, 0), (cu[1:], 10)):
+        with pytest.raises(ValueError):
+            ns.attend_prompt(q, k, k, *args)
+    assert ns.attend_prompt(q[:0], k[:0], k[:0], cu[:1], 0)[0].shape == (0, 4, 64)
+    assert ns.attend_prompt(q[:0], k[:0], k[:0], torch.zeros_like(cu), 0)[1].shape == (0, 4)
+    assert ns.ops_error() == 0
