@@ -11,6 +11,7 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
+#include <c10/core/GradMode.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -92,6 +93,12 @@ int32_t *ints_2d(PyObject *o, const char *what, c10::Device d, int64_t &rows, in
   return static_cast<int32_t *>(p);
 }
 
+// No operator has a gradient: a call that would have to record one is refused.
+void no_gradient(const at::Tensor &t, const char *what) {
+  if (t.requires_grad() && c10::GradMode::is_enabled())
+    refuse("%s requires a gradient, which this call does not have: detach it or use torch.no_grad()", what);
+}
+
 // Rows of consecutive elements in the last dimension.
 void rows_of(const at::Tensor &t, const char *what, c10::Device d, at::ScalarType type, int64_t dims) {
   if (t.dim() != dims) refuse("%s must have %d dimensions", what, (int)dims);
@@ -99,6 +106,7 @@ void rows_of(const at::Tensor &t, const char *what, c10::Device d, at::ScalarTyp
     refuse("%s must be %s on %s", what, c10::toString(type), d.str().c_str());
   if (t.size(dims - 1) > 1 && t.stride(dims - 1) != 1)
     refuse("%s must have consecutive elements in its last dimension", what);
+  no_gradient(t, what);
 }
 
 at::Tensor made(at::IntArrayRef shape, at::ScalarType type, c10::Device d) {
@@ -110,6 +118,7 @@ at::Tensor output(PyObject *o, const char *what, at::IntArrayRef shape, at::Scal
   const at::Tensor &t = tensor(o, what);
   given(t, what, type, d);
   if (t.sizes() != shape) refuse("%s has another shape than this call's", what);
+  no_gradient(t, what);
   return t;
 }
 

@@ -15,7 +15,9 @@ Outputs and workspaces come from torch's caching allocator unless they are
 passed in; with ``stream`` they are made on that stream, so they are never
 memory that work still queued on another one uses.  Tensors used on a stream
 other than the one they were made on (inputs, and outputs that are read
-elsewhere) must be ordered by the caller, as with any torch op.
+elsewhere) must be ordered by the caller, as with any torch op.  None of the
+operators has a gradient: outside ``torch.no_grad()`` tensors that require one
+are refused.
 """
 
 from __future__ import annotations
