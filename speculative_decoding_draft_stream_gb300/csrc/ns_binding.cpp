@@ -109,6 +109,9 @@ void rows_of(const at::Tensor &t, const char *what, c10::Device d, at::ScalarTyp
   no_gradient(t, what);
 }
 
+// The stride of axis i of rows; an axis of one may have any, and counts as dense.
+int64_t step(const at::Tensor &t, int64_t i) { return t.size(i) == 1 ? t.size(t.dim() - 1) : t.stride(i); }
+
 at::Tensor made(at::IntArrayRef shape, at::ScalarType type, c10::Device d) {
   return at::empty(shape, at::TensorOptions().dtype(type).device(d));
 }
@@ -221,7 +224,7 @@ PyObject *attend_prompt(PyObject *const *a) {
   if (T > 0 && (max_len == 0 || cu.size(0) == 1)) refuse("tokens without a sequence: cu and max_len leave them out");
   at::Tensor out = output(a[6], "out", {T, hq, dim}, type, d), lse = output(a[7], "lse", {T, hq}, at::kFloat, d);
   check(ns_attend_prompt(q.data_ptr(), k.data_ptr(), v.data_ptr(), code(type), (int32_t)T, (int32_t)hq, (int32_t)hkv,
-                         (int32_t)dim, q.stride(0), q.stride(1), k.stride(0), k.stride(1), v.stride(0), v.stride(1),
+                         (int32_t)dim, step(q, 0), step(q, 1), step(k, 0), step(k, 1), step(v, 0), step(v, 1),
                          static_cast<int32_t *>(bounds), (int32_t)cu.size(0) - 1, (int32_t)max_len,
                          real(a[5], 1.0 / std::sqrt((double)dim)), out.data_ptr(), lse.data_ptr<float>(),
                          current_stream(d)),
@@ -252,8 +255,8 @@ PyObject *attend_paged(PyObject *const *a) {
   const at::Tensor ws =
       workspace(a[11], ns_attend_paged_workspace((int32_t)B, (int32_t)n, (int32_t)hq, (int32_t)hkv, (int32_t)dim), d, bytes);
   check(ns_attend_paged(q.data_ptr(), code(type), (int32_t)B, (int32_t)n, (int32_t)hq, (int32_t)hkv, (int32_t)dim,
-                        q.stride(0), q.stride(1), q.stride(2), k.data_ptr(), v.data_ptr(), (int32_t)k.size(0),
-                        (int32_t)k.size(2), k.stride(0), k.stride(1), k.stride(2), v.stride(0), v.stride(1), v.stride(2),
+                        step(q, 0), step(q, 1), step(q, 2), k.data_ptr(), v.data_ptr(), (int32_t)k.size(0),
+                        (int32_t)k.size(2), step(k, 0), step(k, 1), step(k, 2), step(v, 0), step(v, 1), step(v, 2),
                         table, (int32_t)ld, (int32_t)rows, lengths, seqs, mask,
                         real(a[7], 1.0 / std::sqrt((double)dim)), (int32_t)integer(a[8], "max_len"), out.data_ptr(),
                         lse.data_ptr<float>(), ws.data_ptr(), bytes, current_stream(d)),
@@ -292,8 +295,8 @@ PyObject *cache(PyObject *const *a) {
   for (int i = 0; i < 4; ++i) fits(k.size(i), "a dimension of the cache");
   fits(k.size(4) * e, "a row"), fits(rows, "table"), fits(ld, "table");
   c.c.k = k.data_ptr(), c.c.v = v.data_ptr();
-  c.c.k_layer = k.stride(0) * e, c.c.k_page = k.stride(1) * e, c.c.k_head = k.stride(2) * e, c.c.k_token = k.stride(3) * e;
-  c.c.v_layer = v.stride(0) * e, c.c.v_page = v.stride(1) * e, c.c.v_head = v.stride(2) * e, c.c.v_token = v.stride(3) * e;
+  c.c.k_layer = step(k, 0) * e, c.c.k_page = step(k, 1) * e, c.c.k_head = step(k, 2) * e, c.c.k_token = step(k, 3) * e;
+  c.c.v_layer = step(v, 0) * e, c.c.v_page = step(v, 1) * e, c.c.v_head = step(v, 2) * e, c.c.v_token = step(v, 3) * e;
   c.c.layers = (int32_t)k.size(0), c.c.pages = (int32_t)k.size(1), c.c.heads = (int32_t)k.size(2);
   c.c.page_size = (int32_t)k.size(3), c.c.row_bytes = (int32_t)(k.size(4) * e);
   c.c.max_seqs = (int32_t)rows, c.c.table_ld = (int32_t)ld;
@@ -354,7 +357,7 @@ PyObject *write(PyObject *const *a) {
   fits(k.size(0), "tokens");
   const int32_t *seqs = ints(a[2], "seqs", c.device, {n}), *cu = ints(a[3], "cu", c.device, {n + 1});
   check(ns_pages_write(&c.c, (int32_t)integer(a[1], "layer"), seqs, cu, (int32_t)n, k.data_ptr(), v.data_ptr(),
-                       k.stride(0) * e, k.stride(1) * e, v.stride(0) * e, v.stride(1) * e, (int32_t)k.size(0),
+                       step(k, 0) * e, step(k, 1) * e, step(v, 0) * e, step(v, 1) * e, (int32_t)k.size(0),
                        stream_of(a[6], c.device)),
         "ns_pages_write");
   return none();

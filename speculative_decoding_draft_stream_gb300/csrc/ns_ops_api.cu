@@ -53,10 +53,11 @@ bool attn_type(int dtype, int dim) {
 }
 bool heads_ok(int q, int kv) { return q >= 1 && kv >= 1 && q <= 65535 && q % kv == 0; }
 bool by8(int64_t s) { return s % 8 == 0; }
-// A stride (elements) that a TMA map takes.  An axis of one place is never
-// stepped along: whatever its stride is, it becomes `row`.
+// An axis of one place is never stepped along: whatever its stride is, it becomes `row`.
+int64_t step(int64_t s, int places, int row) { return places == 1 ? row : s; }
+// A stride (elements) that a TMA map takes.
 bool map_stride(int64_t &s, int places, int row) {
-  if (places == 1) s = row;
+  s = step(s, places, row);
   return s > 0 && by8(s) && s < (int64_t)1 << 39;
 }
 
@@ -149,9 +150,9 @@ ns_status ns_attend_paged(const void *d_q, int32_t dtype, int32_t n_seqs, int32_
   ns::PagedAttnArgs a{};
   a.q = d_q, a.k = d_k, a.v = d_v;
   a.n_seqs = n_seqs, a.n = n, a.q_heads = q_heads, a.kv_heads = kv_heads, a.group = q_heads / kv_heads;
-  a.q_seq = q_seq, a.q_token = q_token, a.q_head = q_head;
-  a.k_page = k_page, a.k_head = k_head, a.k_token = k_token;
-  a.v_page = v_page, a.v_head = v_head, a.v_token = v_token;
+  a.q_seq = step(q_seq, n_seqs, dim), a.q_token = step(q_token, n, dim), a.q_head = step(q_head, q_heads, dim);
+  a.k_page = step(k_page, n_pages, dim), a.k_head = step(k_head, kv_heads, dim), a.k_token = k_token;
+  a.v_page = step(v_page, n_pages, dim), a.v_head = step(v_head, kv_heads, dim), a.v_token = v_token;
   a.n_pages = n_pages, a.table_ld = table_ld, a.max_seqs = max_seqs;
   while ((1 << a.page_shift) < page_size) ++a.page_shift;
   const int64_t most = (int64_t)table_ld * page_size;

@@ -746,3 +746,25 @@ def test_prompt_tokens_without_sequences_are_refused(ns):
     assert ns.attend_prompt(q[:0], k[:0], k[:0], cu[:1], 0)[0].shape == (0, 4, 64)
     assert ns.attend_prompt(q[:0], k[:0], k[:0], torch.zeros_like(cu), 0)[1].shape == (0, 4)
     assert ns.ops_error() == 0
+
+
+@pytest.mark.parametrize("n", [1, 40])
+def test_paged_strides_of_axes_of_one(ns, n):
+    """An axis of one may have any stride: the call is the same, bit for bit, as with dense ones."""
+    g, rng = gen(95), random.Random(95)
+    P, d = 64, 64
+    dk, dv, table, _, _ = make_cache(g, rng, [60], 1, P, d, BF16, spare=0)
+    i32 = {"dtype": torch.int32, "device": "cuda"}
+    rest = (table.cuda(), torch.tensor([60], **i32), torch.tensor([0], **i32))
+    q = normal(g, (1, n, 8, d), BF16).cuda()
+    want, wl = ns.attend_paged(q, dk, dv, *rest)
+    for s in (0, 3, 12, 8 * d * n + 1):
+        qs = torch.as_strided(q, q.shape, (s, 8 * d, d, 1))
+        ks, vs = (torch.as_strided(t, t.shape, (s, s, d, 1)) for t in (dk, dv))
+        for args in ((qs, dk, dv), (q, ks, vs), (qs, ks, vs)):
+            out, lse = ns.attend_paged(*args, *rest)
+            assert torch.equal(out, want) and torch.equal(lse, wl)
+    one, wl = ns.attend_paged(q[:, :, :1].contiguous(), dk, dv, *rest)
+    head = torch.as_strided(q, (1, n, 1, d), (1, 8 * d, 1, 1))
+    out, lse = ns.attend_paged(head, dk, dv, *rest)
+    assert torch.equal(out, one) and torch.equal(lse, wl) and ns.ops_error() == 0
