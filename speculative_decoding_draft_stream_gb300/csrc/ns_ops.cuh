@@ -56,9 +56,14 @@ struct PagedAttnArgs {
   void *ws;
   uint32_t *err;
 };
+// What a device holds of the kernels for few rows (found when it is first used).
+struct PagedFit {
+  int clusters[2][2][2];  // resident at once: dtype, dim 64 or 128, small or large CTAs
+};
 int64_t paged_attn_ws(int n_seqs, int n, int q_heads, int kv_heads, int dim, int sms);
-cudaError_t prepare_paged_attn();
-cudaError_t launch_paged_attn(const PagedAttnArgs &a, int dtype, int dim, int sms, cudaStream_t st);
+cudaError_t prepare_paged_attn(PagedFit *fit);
+cudaError_t launch_paged_attn(const PagedAttnArgs &a, int dtype, int dim, int sms, const PagedFit &fit,
+                              cudaStream_t st);
 
 // The same for more than 16 rows, on tcgen05 (ns_paged_umma.cu).
 bool paged_umma_ok(const PagedAttnArgs &a);

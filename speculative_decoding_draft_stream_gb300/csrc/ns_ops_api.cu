@@ -14,6 +14,7 @@ constexpr int kMaxDevices = 64;
 struct Device {
   bool ready = false;
   int sms = 0;
+  ns::PagedFit fit{};
   uint32_t *flags = nullptr;
 };
 std::mutex g_mutex;
@@ -31,7 +32,7 @@ ns_status current(const Device **out) {
     void *p = nullptr;
     if (cudaGetSymbolAddress(&p, g_ops_flags) != cudaSuccess) return NS_ERR_CUDA;
     if (cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return NS_ERR_CUDA;
-    if (ns::prepare_paged_attn() != cudaSuccess || ns::prepare_prompt_attn() != cudaSuccess) return NS_ERR_CUDA;
+    if (ns::prepare_paged_attn(&d.fit) != cudaSuccess || ns::prepare_prompt_attn() != cudaSuccess) return NS_ERR_CUDA;
     d.flags = static_cast<uint32_t *>(p);
     d.ready = true;
   }
@@ -159,7 +160,7 @@ ns_status ns_attend_paged(const void *d_q, int32_t dtype, int32_t n_seqs, int32_
   a.max_len = max_len == 0 || max_len > most ? (int32_t)most : max_len;
   a.table = d_table, a.lengths = d_lengths, a.seqs = d_seqs, a.mask = d_mask;
   a.scale = scale, a.out = d_out, a.lse = d_lse, a.ws = d_ws, a.err = d->flags;
-  return done(ns::launch_paged_attn(a, dtype, dim, d->sms, static_cast<cudaStream_t>(stream)));
+  return done(ns::launch_paged_attn(a, dtype, dim, d->sms, d->fit, static_cast<cudaStream_t>(stream)));
 }
 
 ns_status ns_pages_truncate(const ns_kv_pages *c, const int32_t *d_seqs, const int32_t *d_new_len, int32_t n,

@@ -473,15 +473,18 @@ struct ClusterLaunch {
     cfg.numAttrs = 1;
   }
 };
-template <typename T, int D, int W>
-int resident = 0;  // clusters that the GPU holds at once
+// Clusters that the device holds at once.
+template <typename T, int D, int W, typename Fit>
+auto &resident(Fit &fit) {
+  return fit.clusters[Type<T>::kBf16 ? NS_DTYPE_BF16 : NS_DTYPE_F16][D == 128][W == kLarge];
+}
 
 // Whether each item can have its own cluster with up to 8 tiles to a CTA (in
 // two waves of small CTAs: with one or two tiles).
 template <typename T, int D, int W>
-bool clusters_fit(const PagedAttnArgs &a) {
+bool clusters_fit(const PagedAttnArgs &a, const PagedFit &fit) {
   const bool two_waves = W == kSmall && a.max_len > kCluster * kKeys<W> / 2 && a.max_len <= 2 * kCluster * kKeys<W>;
-  return (long long)a.n_seqs * a.kv_heads <= (two_waves ? 2 : 1) * resident<T, D, W> &&
+  return (long long)a.n_seqs * a.kv_heads <= (two_waves ? 2 : 1) * resident<T, D, W>(fit) &&
          a.max_len <= 8 * kCluster * kKeys<W>;
 }
 template <typename T, int D, int W>
@@ -491,7 +494,7 @@ cudaError_t launch_clusters(const PagedAttnArgs &a, cudaStream_t st) {
 }
 
 template <typename T, int D, int WM, int W>
-cudaError_t prepare() {
+cudaError_t prepare(PagedFit *fit) {
   cudaError_t e = cudaFuncSetAttribute(paged_attn_kernel<T, D, WM, W>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        pa_smem<D, WM, W>() + (W == kLine ? NS_MAX_ATTEND_SEQS * 8 : 0));
   if (W == kLine) return e;
@@ -499,7 +502,7 @@ cudaError_t prepare() {
     e = cudaFuncSetAttribute(paged_attn_kernel<T, D, WM, W>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e != cudaSuccess) return e;
   ClusterLaunch l(64, kThreads<W>, pa_smem<D, 1, W>(), nullptr);
-  return cudaOccupancyMaxActiveClusters(&resident<T, D, W>, paged_attn_kernel<T, D, WM, W>, &l.cfg);
+  return cudaOccupancyMaxActiveClusters(&resident<T, D, W>(*fit), paged_attn_kernel<T, D, WM, W>, &l.cfg);
 }
 
 // Up to 16 rows the keys are what costs: each is fetched once and the warps
@@ -525,26 +528,26 @@ cudaError_t prepare() {
 // (twice 16) 49.5, 40.6; 64 rows 88.2, 40.9.  64 rows a CTA here: 16 draft
 // trees of 60 nodes (240 rows) 200, there 56.
 template <typename T, int D>
-cudaError_t by_rows(const PagedAttnArgs &a, int sms, cudaStream_t st) {
+cudaError_t by_rows(const PagedAttnArgs &a, int sms, const PagedFit &fit, cudaStream_t st) {
   if (a.n * a.group <= 16) {
-    if (a.max_len > kCluster * kKeys<kSmall> && clusters_fit<T, D, kLarge>(a))
+    if (a.max_len > kCluster * kKeys<kSmall> && clusters_fit<T, D, kLarge>(a, fit))
       return launch_clusters<T, D, kLarge>(a, st);
-    if (clusters_fit<T, D, kSmall>(a)) return launch_clusters<T, D, kSmall>(a, st);
+    if (clusters_fit<T, D, kSmall>(a, fit)) return launch_clusters<T, D, kSmall>(a, st);
     return launch<T, D, 1>(a, sms, st);
   }
   if (paged_umma_ok(a)) return launch_paged_umma(a, Type<T>::kBf16 ? NS_DTYPE_BF16 : NS_DTYPE_F16, D, sms, st);
   return launch<T, D, 4>(a, sms, st);
 }
 template <typename T>
-cudaError_t by_dim(const PagedAttnArgs &a, int dim, int sms, cudaStream_t st) {
-  return dim == 128 ? by_rows<T, 128>(a, sms, st) : by_rows<T, 64>(a, sms, st);
+cudaError_t by_dim(const PagedAttnArgs &a, int dim, int sms, const PagedFit &fit, cudaStream_t st) {
+  return dim == 128 ? by_rows<T, 128>(a, sms, fit, st) : by_rows<T, 64>(a, sms, fit, st);
 }
 template <typename T, int D>
-cudaError_t prepare_all() {
-  cudaError_t e = prepare<T, D, 1, kLine>();
-  if (e == cudaSuccess) e = prepare<T, D, 4, kLine>();
-  if (e == cudaSuccess) e = prepare<T, D, 1, kSmall>();
-  if (e == cudaSuccess) e = prepare<T, D, 1, kLarge>();
+cudaError_t prepare_all(PagedFit *fit) {
+  cudaError_t e = prepare<T, D, 1, kLine>(fit);
+  if (e == cudaSuccess) e = prepare<T, D, 4, kLine>(fit);
+  if (e == cudaSuccess) e = prepare<T, D, 1, kSmall>(fit);
+  if (e == cudaSuccess) e = prepare<T, D, 1, kLarge>(fit);
   return e;
 }
 
@@ -556,16 +559,17 @@ int64_t paged_attn_ws(int n_seqs, int n, int q_heads, int kv_heads, int dim, int
   return (((int64_t)(n_seqs + 1) * 8 + 255) & ~(int64_t)255) + rows * (dim + 2) * 4;
 }
 
-cudaError_t prepare_paged_attn() {
-  cudaError_t e = prepare_all<__nv_bfloat16, 128>();
-  if (e == cudaSuccess) e = prepare_all<__nv_bfloat16, 64>();
-  if (e == cudaSuccess) e = prepare_all<__half, 128>();
-  if (e == cudaSuccess) e = prepare_all<__half, 64>();
+cudaError_t prepare_paged_attn(PagedFit *fit) {
+  cudaError_t e = prepare_all<__nv_bfloat16, 128>(fit);
+  if (e == cudaSuccess) e = prepare_all<__nv_bfloat16, 64>(fit);
+  if (e == cudaSuccess) e = prepare_all<__half, 128>(fit);
+  if (e == cudaSuccess) e = prepare_all<__half, 64>(fit);
   return e == cudaSuccess ? prepare_paged_umma() : e;
 }
 
-cudaError_t launch_paged_attn(const PagedAttnArgs &a, int dtype, int dim, int sms, cudaStream_t st) {
-  return dtype == NS_DTYPE_BF16 ? by_dim<__nv_bfloat16>(a, dim, sms, st) : by_dim<__half>(a, dim, sms, st);
+cudaError_t launch_paged_attn(const PagedAttnArgs &a, int dtype, int dim, int sms, const PagedFit &fit,
+                              cudaStream_t st) {
+  return dtype == NS_DTYPE_BF16 ? by_dim<__nv_bfloat16>(a, dim, sms, fit, st) : by_dim<__half>(a, dim, sms, fit, st);
 }
 
 }  // namespace ns
