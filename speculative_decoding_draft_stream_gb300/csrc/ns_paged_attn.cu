@@ -63,9 +63,15 @@ __host__ __device__ constexpr int pa_smem() {
   return kStages<D, W> * pa_stage<D, W>() + (W != kLine ? 16 * (D + 2) * 4 : WM == 1 ? 32 * D / 2 * 4 + kMerge : 0);
 }
 
-// CTAs that an SM is to hold: as many as their shared memory allows (64 rows: their registers).
+// CTAs that an SM is to hold: as many as their shared memory allows (64 rows: their registers).  The line has that
+// many on each SM; its equal shares would end in a second, half empty wave if it had more.
 template <int D, int WM, int W>
 constexpr int kResident = W == kLarge ? (D == 128 ? 1 : 2) : WM == 1 ? kPerSm<D> : (D == 128 ? 2 : 3);
+template <int D, int WM, int W>
+constexpr bool kHeld = kResident<D, WM, W> * (pa_smem<D, WM, W>() + 1280) <= 228 * 1024;  // (1 KB is the system's)
+static_assert(kHeld<128, 1, kLine> && kHeld<64, 1, kLine> && kHeld<128, 4, kLine> && kHeld<64, 4, kLine> &&
+                  kHeld<128, 1, kSmall> && kHeld<64, 1, kSmall> && kHeld<128, 1, kLarge> && kHeld<64, 1, kLarge>,
+              "shared memory of an SM");
 
 template <int W>
 __host__ __device__ inline long long pa_tiles(int len) {
@@ -133,7 +139,9 @@ __global__ void __launch_bounds__(kThreads<W>, kResident<D, WM, W>)
     t0 = (long long)ld.nt * rank / C, t1 = (long long)ld.nt * (rank + 1) / C;
     ld.tile = (int)t0;
   } else {
-    long long *s_cum = reinterpret_cast<long long *>(smem + pa_smem<D, WM, W>());
+    // where the tiles will lie, so that a CTA's shared memory does not grow with the sequences
+    long long *s_cum = reinterpret_cast<long long *>(smem);
+    static_assert(NS_MAX_ATTEND_SEQS * 8 <= kStages<D, W> * pa_stage<D, W>(), "room for the sequences");
     __shared__ long long s_sum[kPaThreads / kWarp];
     // tiles of the sequences before each one
     long long total = 0;
@@ -179,6 +187,7 @@ __global__ void __launch_bounds__(kThreads<W>, kResident<D, WM, W>)
       ld.item = (int)quotient(local, ld.nt);
       ld.tile = (int)(local - (long long)ld.item * ld.nt);
     }
+    __syncthreads();  // everyone is done with s_cum before the first tile comes
   }
   Cursor<W> cu = ld;
 
@@ -448,10 +457,10 @@ template <typename T, int D, int WM>
 cudaError_t launch(const PagedAttnArgs &a, int sms, cudaStream_t st) {
   constexpr int kRows = 16 * WM;
   const int blocks = (a.n * a.group + kRows - 1) / kRows;
-  const int smem = pa_smem<D, WM, kLine>() + a.n_seqs * 8;
+  constexpr int kCtas = kResident<D, WM, kLine>;
   const long long most = pa_tiles<kLine>(a.max_len) * a.n_seqs * a.kv_heads * blocks;
-  const int ctas = (int)(most < (long long)kPerSm<D> * sms ? most : kPerSm<D> * sms);
-  paged_attn_kernel<T, D, WM, kLine><<<ctas, kThreads<kLine>, smem, st>>>(a, blocks);
+  const int ctas = (int)(most < (long long)kCtas * sms ? most : kCtas * sms);
+  paged_attn_kernel<T, D, WM, kLine><<<ctas, kThreads<kLine>, pa_smem<D, WM, kLine>(), st>>>(a, blocks);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   const int rows = a.n * a.group < kRows ? a.n * a.group : kRows;
@@ -496,7 +505,7 @@ cudaError_t launch_clusters(const PagedAttnArgs &a, cudaStream_t st) {
 template <typename T, int D, int WM, int W>
 cudaError_t prepare(PagedFit *fit) {
   cudaError_t e = cudaFuncSetAttribute(paged_attn_kernel<T, D, WM, W>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       pa_smem<D, WM, W>() + (W == kLine ? NS_MAX_ATTEND_SEQS * 8 : 0));
+                                       pa_smem<D, WM, W>());
   if (W == kLine) return e;
   if (e == cudaSuccess)
     e = cudaFuncSetAttribute(paged_attn_kernel<T, D, WM, W>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
@@ -526,7 +535,7 @@ cudaError_t prepare(PagedFit *fit) {
 // with 16 sequences of 2300 tokens, 32 heads on 8, 128 columns, pages of 64, by
 // 16 rows here and there (us): 4 rows 34.6, 40.8; 16 rows 38.1, 40.7; 20 rows
 // (twice 16) 49.5, 40.6; 64 rows 88.2, 40.9.  64 rows a CTA here: 16 draft
-// trees of 60 nodes (240 rows) 200, there 56.
+// trees of 60 nodes behind 512 to 4096 tokens (240 rows) 169, there 60.
 template <typename T, int D>
 cudaError_t by_rows(const PagedAttnArgs &a, int sms, const PagedFit &fit, cudaStream_t st) {
   if (a.n * a.group <= 16) {
@@ -554,7 +563,7 @@ cudaError_t prepare_all(PagedFit *fit) {
 }  // namespace
 
 int64_t paged_attn_ws(int n_seqs, int n, int q_heads, int kv_heads, int dim, int sms) {
-  // two parts for each CTA: up to 4 sms CTAs of 16 rows, or sms CTAs of 256 (4 sms of 64 are no more)
+  // two parts for each CTA: up to 4 sms CTAs of 16 rows, or sms CTAs of 256 (3 sms of 64 are no more)
   const int64_t rows = n * (q_heads / kv_heads) <= 16 ? (int64_t)kPerSm<64> * sms * 2 * 16 : (int64_t)sms * 2 * 256;
   return (((int64_t)(n_seqs + 1) * 8 + 255) & ~(int64_t)255) + rows * (dim + 2) * 4;
 }

@@ -768,3 +768,33 @@ def test_paged_strides_of_axes_of_one(ns, n):
     head = torch.as_strided(q, (1, n, 1, d), (1, 8 * d, 1, 1))
     out, lse = ns.attend_paged(head, dk, dv, *rest)
     assert torch.equal(out, one) and torch.equal(lse, wl) and ns.ops_error() == 0
+
+
+@pytest.mark.parametrize("seqs", [300, 448, 1500, 4096])
+@pytest.mark.parametrize("d,dtype", [(64, F16), (128, BF16)])
+def test_paged_many_sequences(ns, seqs, d, dtype):
+    """Up to the most sequences of a call, by few and by many rows: every CTA finds its share among all of them."""
+    g, rng = gen(seqs), random.Random(seqs)
+    P, hkv, pages = 8, 1, 64
+    lens = [rng.choice([0, 1, 7, 8, 9, 30, 64]) + (200 if i % 97 == 5 else 0) for i in range(seqs)]
+    k, v = normal(g, (pages, hkv, P, d), dtype), normal(g, (pages, hkv, P, d), dtype)
+    table = torch.tensor([[rng.randrange(pages) for _ in range(33)] for _ in range(seqs)], dtype=torch.int32)
+    i32 = {"dtype": torch.int32, "device": "cuda"}
+    rest = (k.cuda(), v.cuda(), table.cuda(), torch.tensor(lens, **i32), torch.arange(seqs, **i32))
+    some = [0, 1, 5, 102, seqs // 2, seqs - 2, seqs - 1] + rng.sample(range(seqs), 20)
+    for n, hq, off in ((1, 2, 0), (5, 4, 0), (5, 4, 2)):  # (queries off a 16-byte boundary: another kernel)
+        q = normal(g, (seqs, n, hq, d), dtype)
+        dq = torch.zeros((seqs, n, hq, d + off), dtype=dtype, device="cuda")[..., off:]
+        dq.copy_(q)
+        out, lse = ns.attend_paged(dq, *rest)
+        out, lse = out.cpu(), lse.cpu()
+        for b in some:
+            N = lens[b]
+            rows = [(int(table[b, p // P]), p % P) for p in range(N)]
+            kk, vv = (torch.stack([t[x, 0, y] for x, y in rows]) if rows else t[0, 0, :0] for t in (k, v))
+            sees = torch.tensor([[p <= N - n + i for p in range(N)] for i in range(n)], dtype=torch.bool).view(n, N)
+            for h in range(hq):
+                o, z, to, tz = attend_rows(q[b, :, h], kk, vv, sees, d ** -0.5)
+                check(out[b, :, h], o, to, f"out of sequence {b} head {h}")
+                check(lse[b, :, h], z, tz, f"lse of sequence {b} head {h}")
+    assert ns.ops_error() == 0
