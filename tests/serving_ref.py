@@ -125,3 +125,12 @@ class Pages:
     def copy(self, src, dst):
         for a, b in zip(src, dst):
             self.k[:, b], self.v[:, b] = self.k[:, a], self.v[:, a]
+
+
+def with_wild_values(o, v, sees):
+    """o [m, d] of finite values, as it is where some of v [n, d] are not: a row that sees a NaN, or infinities of both
+    signs, in a column has NaN there; infinities of one sign, that infinity (every probability is above 0)."""
+    s = sees.double()
+    nan, pos, neg = ((s @ w.double()) > 0 for w in (torch.isnan(v), v == math.inf, v == -math.inf))
+    o = torch.where(pos, torch.full_like(o, math.inf), torch.where(neg, torch.full_like(o, -math.inf), o))
+    return torch.where(nan | (pos & neg), torch.full_like(o, math.nan), o)
