@@ -21,7 +21,7 @@ prompts with several continuations each:
 from __future__ import annotations
 
 import argparse
-from typing import List, NamedTuple
+from typing import List, NamedTuple, Optional, Tuple
 
 import torch
 
@@ -67,8 +67,9 @@ class Answer(NamedTuple):
 
 
 def generate(model: Verifier, prompts: List[List[int]], samples: int = 2, tokens: int = 32, width: int = 4,
-             width2: int = 2, page_size: int = 16, window: int = 1024):
-    """`samples` continuations of each prompt, at least `tokens` long, and the prompts' mean log probabilities.
+             width2: int = 2, page_size: int = 16, window: int = 1024) -> Tuple[List[Answer], List[Optional[float]]]:
+    """`samples` continuations of each prompt, at least `tokens` long, and the prompts' mean log probabilities (None
+    for a prompt of one token, which has none to be scored).
 
     A step's tree: the chosen token, `width` proposals for the next one, `width2` for the one after each."""
     dev = model.head.device
@@ -98,7 +99,8 @@ def generate(model: Verifier, prompts: List[List[int]], samples: int = 2, tokens
     following = torch.cat([ids[1:], ids[:1]])
     following[cu[1:].long() - 1] = -1  # the last token of a prompt has none
     scored = token_logprobs(logits, following[:, None], k=samples)
-    prompt_scores = [float(scored.logprobs[a:b - 1, 0].mean()) for a, b in zip(cu.tolist(), cu.tolist()[1:])]
+    prompt_scores = [float(scored.logprobs[a:b - 1, 0].mean()) if b - a > 1 else None
+                     for a, b in zip(cu.tolist(), cu.tolist()[1:])]
 
     # Continuations: sequence n_prompts + i shares the pages of prompt i / samples.
     seqs = torch.arange(n_prompts, n_prompts + B, **i32)
@@ -195,7 +197,9 @@ def main() -> None:
     prompts = [torch.randint(model.V, (n,), generator=g).tolist() for n in (5, 64, 131)]
     answers, scores = generate(model, prompts, args.samples, args.tokens)
     for i, a in enumerate(answers):
-        print(f"prompt {i // args.samples} (mean log probability {scores[i // args.samples]:.2f}), answer {i % args.samples}: "
+        score = scores[i // args.samples]
+        said = "one token" if score is None else f"mean log probability {score:.2f}"
+        print(f"prompt {i // args.samples} ({said}), answer {i % args.samples}: "
               f"{len(a.tokens)} tokens in {len(a.accepted)} steps, mean log probability "
               f"{sum(a.logprobs) / len(a.logprobs):.2f}: {a.tokens[:12]} ...")
 

@@ -64,3 +64,33 @@ def test_answers_are_the_verifiers_choices(samples, page):
     if samples > 1:  # continuations of one prompt begin differently
         for j in range(0, len(answers), samples):
             assert len({answers[j + s].tokens[0] for s in range(samples)}) == samples
+
+
+@pytest.mark.parametrize("samples", [1, 2])
+def test_a_prompt_of_one_token(samples):
+    """It is continued like any other; there is nothing in it to score."""
+    from speculative_decoding_draft_stream_gb300.speculate import Verifier, generate
+
+    model = Verifier()
+    prompts = [[17], [3, 400, 5], [501]]
+    answers, scores = generate(model, prompts, samples, tokens=12)
+    assert scores[0] is None and scores[2] is None and scores[1] < 0
+    tol = 0.15  # (as above)
+    for i, a in enumerate(answers):
+        prompt = prompts[i // samples]
+        z = plain(model, prompt + a.tokens)
+        at = torch.arange(len(prompt) - 1, len(prompt) - 1 + len(a.tokens), device=z.device)
+        mine = z[at].gather(1, torch.tensor(a.tokens, device=z.device)[:, None])[:, 0]
+        assert len(a.tokens) >= 12 and bool((z[at].max(1).values[1:] - mine[1:] <= 2 * tol).all())
+        order = z[at[0]].topk(samples).values
+        assert abs(float(mine[0] - order[i % samples])) <= 2 * tol
+        want = z.log_softmax(-1)[at].gather(1, torch.tensor(a.tokens, device=z.device)[:, None])[:, 0]
+        assert bool(((torch.tensor(a.logprobs, device=z.device, dtype=torch.float64) - want).abs() <= 2 * tol).all())
+
+
+def test_the_command_answers(capsys, monkeypatch):
+    from speculative_decoding_draft_stream_gb300 import speculate
+
+    monkeypatch.setattr("sys.argv", ["speculate", "--samples", "1", "--tokens", "6"])
+    speculate.main()
+    assert capsys.readouterr().out.count("mean log probability") == 6
