@@ -45,7 +45,11 @@ def _native():
     global _binding
     if _binding is None:
         load_library()
-        from . import _serving
+        try:
+            from . import _serving
+        except ImportError as e:
+            raise ImportError("the serving operators' binding is missing or does not fit this torch: build.build() "
+                              "compiles it with g++ against torch's and Python's headers") from e
 
         _serving.set_error(NanoSpecError)
         _binding = _serving
