@@ -55,7 +55,9 @@ NS_API ns_status ns_ops_get_error(uint32_t *flags, int32_t clear);
  *   d_cu  int32 [n_seqs + 1]: sequence s holds tokens d_cu[s] .. d_cu[s+1] - 1
  *         (0 first, not decreasing, `tokens` last; empty sequences are fine)
  *   max_len  HOST: no sequence is longer (tokens past it are not computed and
- *         flag NS_FLAG_BAD_SEQ; with 0, or no sequences, the call does nothing)
+ *         flag NS_FLAG_BAD_SEQ; with 0, or no sequences, the call does
+ *         nothing).  It takes part in how the keys are split, so results of
+ *         another bound may differ by their rounding
  *   d_out [tokens x q_heads x dim] of `dtype`, contiguous; d_lse fp32 [tokens x q_heads] or NULL
  * dim is 64 or 128.  Scores, softmax sums and the output's sums are fp32; the
  * probabilities are rounded to `dtype` before the product with v.  A value of
@@ -83,12 +85,15 @@ NS_API ns_status ns_attend_prompt(const void *d_q, const void *d_k, const void *
  *   d_k, d_v  [n_pages x kv_heads x page_size x dim] of one layer, strides in
  *          elements (multiples of 8): page, head, token
  *   d_mask int64 [n_seqs x n] or NULL
- *   max_len  HOST: a bound on the lengths, used only to size the launch (0:
- *          table_ld * page_size); results do not depend on it
+ *   max_len  HOST: a bound on the lengths (0: table_ld * page_size) by which
+ *          the keys are split; results depend on it by their rounding alone,
+ *          and a length above it is attended all the same
  *   d_out  [n_seqs x n x q_heads x dim] contiguous, 16-byte aligned, d_lse fp32 [n_seqs x n x q_heads] or NULL
  *   d_ws   device workspace of ns_attend_paged_workspace(...) bytes, 16-byte
  *          aligned, contents immaterial
  * 1 <= n <= NS_MAX_NEW, dim 64 or 128, page_size a power of two from 8 to 1024.
+ * Scores, softmax sums and the output's sums are fp32; the probabilities are
+ * rounded to `dtype` before the product with v, as in ns_attend_prompt.
  */
 NS_API int64_t ns_attend_paged_workspace(int32_t n_seqs, int32_t n, int32_t q_heads, int32_t kv_heads, int32_t dim);
 NS_API ns_status ns_attend_paged(const void *d_q, int32_t dtype, int32_t n_seqs, int32_t n, int32_t q_heads,

@@ -96,8 +96,9 @@ def attend_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, 
     """Attention of n new tokens per sequence over one layer of a paged cache: q [B, n, Hq, D]; k_pages and
     v_pages [pages, Hkv, page_size, D] (strides free); table int32 [max_seqs, pages per sequence], lengths int32
     [max_seqs] (the new tokens included), seqs int32 [B] the cache sequences; mask int64 [B, n]: bit j of word i
-    set where new token i sees new token j (None: j <= i).  max_len, a bound on the lengths, only sizes the
-    launch.  Returns (out [B, n, Hq, D], lse fp32 [B, n, Hq])."""
+    set where new token i sees new token j (None: j <= i).  max_len, a bound on the lengths, takes part in how
+    the keys are split: results of another bound may differ by their rounding.  Returns (out [B, n, Hq, D], lse fp32
+    [B, n, Hq])."""
     s = None if stream is None else _other(stream)
     if s is not None:
         return _on(s, lambda: attend_paged(q, k_pages, v_pages, table, lengths, seqs, mask=mask, scale=scale,
