@@ -488,13 +488,15 @@ auto &resident(Fit &fit) {
   return fit.clusters[Type<T>::kBf16 ? NS_DTYPE_BF16 : NS_DTYPE_F16][D == 128][W == kLarge];
 }
 
-// Whether each item can have its own cluster with up to 8 tiles to a CTA (in
-// two waves of small CTAs: with one or two tiles).
+// Whether each item can have its own cluster with up to kMostTiles tiles to a
+// CTA (in two waves of small CTAs: with one or two tiles).
+template <int D>
+constexpr int kMostTiles = D == 128 ? 12 : 16;
 template <typename T, int D, int W>
 bool clusters_fit(const PagedAttnArgs &a, const PagedFit &fit) {
   const bool two_waves = W == kSmall && a.max_len > kCluster * kKeys<W> / 2 && a.max_len <= 2 * kCluster * kKeys<W>;
   return (long long)a.n_seqs * a.kv_heads <= (two_waves ? 2 : 1) * resident<T, D, W>(fit) &&
-         a.max_len <= 8 * kCluster * kKeys<W>;
+         a.max_len <= kMostTiles<D> * kCluster * kKeys<W>;
 }
 template <typename T, int D, int W>
 cudaError_t launch_clusters(const PagedAttnArgs &a, cudaStream_t st) {
@@ -516,18 +518,20 @@ cudaError_t prepare(PagedFit *fit) {
 
 // Up to 16 rows the keys are what costs: each is fetched once and the warps
 // split them.  A call whose items fit on the GPU as clusters, all at once, with
-// up to 8 tiles to a CTA, takes clusters: of large CTAs where small ones would
-// have more than one tile each and the large ones still fit (7 clusters of 128
-// columns, three times as many of small ones).  Measured, line, small, large,
-// one new token, bf16 (us in a graph; the line with two CTAs an SM and three
-// tiles, which is up to 3 us quicker for calls of this size):
-//   32 heads on 8, 128 columns, 1 sequence:  100 tokens 8.4, 4.9;  4097: 12.9, 8.8;  8000: 15.2, 13.5
-//     2 sequences:  100: 8.4, 5.7;  4097: 14.4, 10.1;  8000: 17.8, 15.8
-//   28 on 4, 128 columns, 1 sequence:  100: 8.4, 5.2, 6.0;  2000: 10.2, 6.2, 6.0;  8000: 15.0, 11.9, 10.0;
-//     16000: 17.2, -, 15.2;  32000 (16 tiles): 20.7, -, 25.8
-//   12 on 4, 64 columns, 1 sequence:  1000: 9.2, 4.3, 4.7;  8000: 14.8, 9.6, 7.6
-//   32 heads on 8, 128 columns, 4 sequences (two waves):  100: 8.6, 10.1;  600: 10.5, 10.3;  2000: 15.3, 12.9;
-//     4097: 18.8, 19.2
+// up to 12 (64 columns: 16) tiles to a CTA, takes clusters: of large CTAs where
+// small ones would have more than one tile each and the large ones still fit (7
+// clusters of 128 columns and 14 of 64, 21 and 33 of small ones).  Measured,
+// line, small, large, one new token, bf16 (us in a graph):
+//   32 heads on 8, 128 columns, 1 sequence:  100 tokens 8.5, 5.0, 10.1;  4097: 15.3, 8.6, 15.1;
+//     8000: 17.0, 13.1;  12000: 18.4, 17.7;  16000: 20.0, 22.3
+//     2 sequences:  100: 8.7, 5.5;  4097: 16.4, 9.9;  12000: 23.7, 22.9;  16000: 31.9, 30.8;  24000: 41.9, 44.1
+//   28 on 4, 128 columns, 1 sequence:  100: 8.6, 5.2, 5.9;  2000: 10.0, 5.8, 5.8;  8000: 18.3, 11.6, 9.9;
+//     16000: 20.0, 19.0, 14.9;  24000 (12 tiles): 21.6, 26.7, 20.3;  32000: 22.9, 35.5, 26.3
+//     5 sequences:  4097: 16.6, 10.7;  12000: 30.9, 26.3;  16000: 36.4, 33.8
+//   12 on 4, 64 columns, 1 sequence:  1000: 9.0, 4.4, 4.6;  8000: 17.7, 9.4, 7.5;  32000 (16 tiles): 23.8, 26.6, 19.2
+//     4 sequences:  12000: 18.4, 15.0;  16000: 20.2, 18.8;  24000: 25.4, 30.3
+//   32 heads on 8, 128 columns, 4 sequences (two waves):  100: 8.8, 10.0;  600: 10.5, 9.9;  2000: 15.1, 12.8;
+//     4097: 18.4, 19.2
 // Clusters of 8 large CTAs took 11.3 us for the 4097 tokens of one sequence.
 // Above 16 rows the products cost: they belong on the tensor cores of
 // ns_paged_umma.cu, which want queries that TMA can fetch (16-byte aligned,

@@ -798,3 +798,11 @@ def test_paged_many_sequences(ns, seqs, d, dtype):
                 check(out[b, :, h], o, to, f"out of sequence {b} head {h}")
                 check(lse[b, :, h], z, tz, f"lse of sequence {b} head {h}")
     assert ns.ops_error() == 0
+
+
+@pytest.mark.parametrize("d,most", [(64, 16), (128, 12)])
+def test_paged_around_the_longest_that_clusters_take(ns, d, most):
+    """One sequence of few heads (large CTAs) and of many (small ones), at the most tiles that a CTA of theirs takes."""
+    for heads, keys in ((2, 128), (16, 64)):
+        for n in (most * 16 * keys - 1, most * 16 * keys, most * 16 * keys + 1):
+            run_paged(ns, [n], 1, heads, heads, d, 64, BF16, n)
