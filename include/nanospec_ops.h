@@ -37,6 +37,7 @@ extern "C" {
 
 #define NS_MAX_NEW 64          /* new tokens of a sequence in ns_attend_paged (NS_MAX_ROWS)  */
 #define NS_MAX_ATTEND_SEQS 4096 /* sequences of one ns_attend_paged call                      */
+#define NS_MAX_POSITIONS 0x7ffffe00 /* table_ld * page_size of ns_attend_paged: ends of tiles fit 31 bits */
 #define NS_MAX_ALTERNATIVES 32 /* k of ns_token_logprobs                                      */
 
 /* The sticky flags of the current device (synchronises it); clears them when `clear` is non-zero. */
@@ -91,7 +92,8 @@ NS_API ns_status ns_attend_prompt(const void *d_q, const void *d_k, const void *
  *   d_out  [n_seqs x n x q_heads x dim] contiguous, 16-byte aligned, d_lse fp32 [n_seqs x n x q_heads] or NULL
  *   d_ws   device workspace of ns_attend_paged_workspace(...) bytes, 16-byte
  *          aligned, contents immaterial
- * 1 <= n <= NS_MAX_NEW, dim 64 or 128, page_size a power of two from 8 to 1024.
+ * 1 <= n <= NS_MAX_NEW, dim 64 or 128, page_size a power of two from 8 to 1024,
+ * table_ld * page_size at most NS_MAX_POSITIONS.
  * Scores, softmax sums and the output's sums are fp32; the probabilities are
  * rounded to `dtype` before the product with v, as in ns_attend_prompt.
  */

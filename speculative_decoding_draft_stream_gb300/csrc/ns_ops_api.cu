@@ -135,7 +135,7 @@ ns_status ns_attend_paged(const void *d_q, int32_t dtype, int32_t n_seqs, int32_
                           float *d_lse, void *d_ws, int64_t ws_bytes, ns_stream stream) {
   if (!attn_type(dtype, dim) || !heads_ok(q_heads, kv_heads) || n_seqs < 0 || n_seqs > NS_MAX_ATTEND_SEQS || n < 1 ||
       n > NS_MAX_NEW || n_pages < 1 || page_size < 8 || page_size > 1024 || (page_size & (page_size - 1)) ||
-      table_ld < 1 || max_seqs < 1 || (int64_t)table_ld * page_size > 0x7fffffffLL - 64 || max_len < 0 ||
+      table_ld < 1 || max_seqs < 1 || (int64_t)table_ld * page_size > NS_MAX_POSITIONS || max_len < 0 ||
       !std::isfinite(scale) || scale <= 0.f)
     return NS_ERR_ARG;
   if (n_seqs == 0) return NS_OK;

@@ -189,3 +189,8 @@ def test_logprobs_refuse_temperatures_whose_inverse_overflows(lib, t):
     """The kernels work in powers of two: log2(e) / T has to be finite, not 1 / T alone."""
     w = [P(16)] * 6
     assert lib.ns_token_logprobs(P(16), 2, 2, 10, 10, ctypes.c_float(t), w[0], 1, 2, *w[1:], None) == ARG
+
+
+@pytest.mark.parametrize("kw", [dict(ld=(1 << 27) - 8), dict(ld=(1 << 28) - 31, page=8)])
+def test_paged_refuses_tables_whose_last_tile_ends_past_31_bits(lib, kw):
+    assert paged(lib, **kw) == ARG
