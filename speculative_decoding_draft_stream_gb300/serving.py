@@ -111,13 +111,21 @@ class KvPages:
     """A paged key-value cache over the caller's tensors: k and v [layers, pages, heads, page_size, dim] (any element
     type; rows of dim consecutive elements, a multiple of 16 bytes; other strides free), table int32 [max_seqs,
     pages per sequence] (-1 past a sequence's last page), lengths int32 [max_seqs], refs int32 [pages] (how many
-    sequences hold a page).  Its device must be the current one in every call.  ``KvPages.new`` makes an empty one."""
+    sequences hold a page).  Their contents may be changed, but not which tensors they are: the cache works on the
+    memory that it was made over.  Its device must be the current one in every call.  ``KvPages.new`` makes an empty
+    one."""
 
     def __init__(self, k: torch.Tensor, v: torch.Tensor, table: torch.Tensor, lengths: torch.Tensor,
                  refs: torch.Tensor):
         self._b = _native()
         self._c = self._b.cache(k, v, table, lengths, refs)
-        self.k, self.v, self.table, self.lengths, self.refs = k, v, table, lengths, refs
+        self._over = k, v, table, lengths, refs  # kept alive: the native record has their addresses
+
+    k = property(lambda self: self._over[0])
+    v = property(lambda self: self._over[1])
+    table = property(lambda self: self._over[2])
+    lengths = property(lambda self: self._over[3])
+    refs = property(lambda self: self._over[4])
 
     @classmethod
     def new(cls, layers: int, pages: int, kv_heads: int, page_size: int, dim: int, max_seqs: int, max_pages: int,

@@ -382,3 +382,15 @@ def test_write_of_many_sequences_with_repeated_ones(ns):
     first = [i for i, s in enumerate(seqs) if s not in seqs[:i]]
     b.r.write(0, [seqs[i] for i in first], list(range(len(first) + 1)), k.numpy()[first], v.numpy()[first])
     b.same(ns.FLAG_BAD_SEQ)
+
+
+def test_a_caches_tensors_stay(ns):
+    """Another tensor in place of one of them would leave the cache working on memory that is given away."""
+    c = ns.KvPages.new(1, 4, 1, 8, 8, 2, 2)
+    for name in ("k", "v", "table", "lengths", "refs"):
+        before = getattr(c, name)
+        with pytest.raises(AttributeError):
+            setattr(c, name, torch.zeros_like(before))
+        assert getattr(c, name) is before
+    c.extend(i32([1]), i32([9]))
+    assert c.lengths.tolist() == [0, 9] and c.refs.tolist() == [1, 1, 0, 0] and ns.ops_error() == 0
