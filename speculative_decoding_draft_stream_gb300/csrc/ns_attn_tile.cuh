@@ -4,8 +4,9 @@
 // A row's state is (m, l, o): m the largest scaled score so far (in powers of
 // two), l = sum 2^(x - m), o = sum 2^(x - m) v.  A tile with a larger maximum
 // m' first multiplies l and o by 2^(m - m').  Scores, m, l and o are fp32.
-// Probabilities are rounded to the values' type for the product, l sums them
-// unrounded.  For fp16 they are all kept 2^8 times larger, so that
+// Probabilities are rounded to the values' type for the product, whose operands
+// have 16 bits (at most u sum p |v| with u its unit roundoff, beside the output's
+// own u |o|); l sums them unrounded.  For fp16 they are all kept 2^8 times larger, so that
 // probabilities down to 2^-32 of the largest are not lost to fp16's range.
 //
 // Keys and values lie in shared memory as rows of D elements whose 16-byte

@@ -22,9 +22,13 @@
 // workspace, and a fixed order of every sum.
 //
 // What bounds it: HBM for many rows (each logit crosses it once): 2048 rows of
-// 152064 in bf16 take 124 us, 5.0 TB/s; the exponentials and sums that hide
-// behind the loads are the rest.  For a few rows, latency (one wave of loads,
-// the joins): one row of 128256 in fp32 takes 10 us, 60 rows 12.5 us.
+// 152064 in bf16 with 5 alternatives take 122 us, 5.1 TB/s (100 us without
+// alternatives); the exponentials and sums that hide behind the loads are the
+// rest.  For a few rows, latency: a thread's batches of kLpVecs loads follow one
+// another, and what is left over comes a load at a time (one row of 128256 in
+// fp32 on 8 CTAs: three batches and up to four single loads), then the second
+// look and the joins.  With one given token and 10 alternatives one such row
+// takes 10.2 us (6.2 without alternatives), 60 rows of 151936 13.0 us (7.5).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -39,8 +43,9 @@ constexpr int kLpVecs = 4;        // 16-byte loads a thread keeps in flight
 constexpr int kLpMaxCluster = 8;  // portable cluster size
 constexpr int kLpMinSlice = 4096; // least logits of a CTA of a split row
 // Above 16 alternatives (kMany), 64 groups instead of 32: 32 groups' least
-// maximum lets a third of the threads through. 126 fp32 rows of 128256, k 32: 76 ->
-// 24 us; 298 bf16 rows, k 31: 41 -> 28; k 17: 27.5 -> 25.0; but k 14: 17.0 -> 17.9.
+// maximum lets a third of the threads through.  Rows of 128256, by 32 and by 64 groups
+// (us): 126 in fp32, k 14 17.0, 18.2; 17 18.9, 18.7; 24 23.1, 20.8; 32 75.5, 23.6;
+// 298 in bf16, k 14 21.0, 21.4; 17 22.9, 21.6; 31 40.9, 27.7.
 constexpr int kManyFrom = 17;
 constexpr int kLpBuffer = kLpMaxCluster * NS_MAX_ALTERNATIVES;  // candidates of a CTA, or the lists of a cluster
 constexpr float kLn2 = 0.69314718055994531f;
@@ -452,10 +457,11 @@ __global__ void __launch_bounds__(kLpThreads, 1024 / kLpThreads + 1024 / kLpThre
 }
 
 // A row is split while the call has fewer than two CTAs for each SM and every
-// CTA keeps kLpMinSlice logits: one row of 128256 fp32 logits takes 8.6 us on 8
-// CTAs, 11.9 on 2; 60 rows of 151936 10.5 us on 4 each, 11.7 on 8, 13.1 on 2.
-// Threads of a CTA: 512 or 1024 took 27 to 55 us for those 60 rows with 10
-// alternatives (12.5 with 256): the joins wait for more warps.
+// CTA keeps kLpMinSlice logits.  In fp32 with 10 alternatives, one row of 128256
+// takes 10.2 us on 8 CTAs, 10.6 on 4, 14.0 on 2, 15.2 on one; 60 rows of 151936
+// take 13.0 us on 4 each, 15.2 on 8, 16.2 on 2, 20.8 on one.
+// Threads of a CTA: 512 or 1024 took 27 to 55 us for those 60 rows: the joins
+// wait for more warps.
 constexpr int kLpThreads = 256;
 
 template <typename T, bool kMany>

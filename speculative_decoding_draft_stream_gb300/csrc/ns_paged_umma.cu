@@ -14,8 +14,8 @@
 // Bound by the products, the start of a CTA's items and the parts' way through
 // L2: trees of 60 nodes behind 512 to 4096 tokens, 16 sequences, 32 heads on
 // 8, bf16, pages of 16, take 56 us (0.57 PFLOP/s, 2.7 TB/s); with mma.sync
-// and 64 rows to a CTA they took 200 us.  Pages of 8 take 65 us: a box costs
-// the TMA engine some 85 cycles, whatever its size.
+// and 64 rows to a CTA they take nearly three times as long.  Pages of 8 take
+// 65 us: a box costs the TMA engine some 85 cycles, whatever its size.
 #include "ns_paged_attn.cuh"
 #include "ns_umma_attn.cuh"
 

@@ -10,7 +10,10 @@
 // first tile no maximum is taken (the sum is needed anyway) and the
 // accumulator in tensor memory is hardly ever rewritten.  Scores, sums and o
 // are fp32; a probability is rounded once, to the values' type, as an operand
-// of the second product (l sums it unrounded).  fp16 probabilities are kept
+// of the second product (l sums it unrounded).  With u that type's unit
+// roundoff it costs at most u sum p |v|, beside the output's own u |o|; in two
+// operands, a rounded one and the rest, the second product would cost twice as
+// much.  fp16 probabilities are kept
 // 2^6 times larger: within fp16's range under the bound on the sum, and 2^-30
 // of the largest is not lost.
 //
@@ -52,7 +55,7 @@
 // What bounds it: a tile of keys costs 2048 tensor-core cycles for the two row
 // tiles, and the softmax of 128 scores a thread nearly as many issue slots, so
 // both have to run all the time.  16381 tokens of 32 heads on 8, 128 columns,
-// bf16 take 1.40 ms, 1.57 PFLOP/s (0.81 of the measured cuBLAS burst); with the
+// bf16 take 1.40 ms, 1.57 PFLOP/s (0.83 of the measured cuBLAS burst); with the
 // exponentials left out the same kernel took 1.20 ms.  What other forms took
 // there: two threads to a row (640 threads) 1.76 ms, output warps of their own
 // 1.43 ms, a softmax of half tiles in 128 registers 1.50 ms, two threads that
