@@ -81,8 +81,9 @@ NS_API ns_status ns_attend_prompt(const void *d_q, const void *d_k, const void *
  * No row sees the positions of a page whose id is out of range
  * (NS_FLAG_BAD_ID).  A row that sees nothing (len 0, or an empty mask and no
  * context) gives zeros and an lse of -inf.
- *   d_q    [n_seqs x n x q_heads x dim], strides in elements (even; with positive multiples of 8 and 16-byte
- *          alignment more than 16 rows, n * q_heads / kv_heads, are faster; an axis of one counts as such)
+ *   d_q    [n_seqs x n x q_heads x dim], strides in elements (even; more than 16 rows, n * q_heads / kv_heads,
+ *          take about a third of the time with positive multiples of 8, as which an axis of one counts, and 16-byte
+ *          alignment)
  *   d_k, d_v  [n_pages x kv_heads x page_size x dim] of one layer, strides in
  *          elements (multiples of 8): page, head, token
  *   d_mask int64 [n_seqs x n] or NULL

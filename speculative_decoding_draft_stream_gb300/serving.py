@@ -97,8 +97,9 @@ def attend_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, 
     v_pages [pages, Hkv, page_size, D] (strides free); table int32 [max_seqs, pages per sequence], lengths int32
     [max_seqs] (the new tokens included), seqs int32 [B] the cache sequences; mask int64 [B, n]: bit j of word i
     set where new token i sees new token j (None: j <= i).  max_len, a bound on the lengths, takes part in how
-    the keys are split: results of another bound may differ by their rounding.  Returns (out [B, n, Hq, D], lse fp32
-    [B, n, Hq])."""
+    the keys are split: results of another bound may differ by their rounding.  With more than 16 rows (n * Hq / Hkv)
+    a q off a 16-byte boundary, or with strides other than positive multiples of 8 elements, takes about three times
+    as long.  Returns (out [B, n, Hq, D], lse fp32 [B, n, Hq])."""
     s = None if stream is None else _other(stream)
     if s is not None:
         return _on(s, lambda: attend_paged(q, k_pages, v_pages, table, lengths, seqs, mask=mask, scale=scale,
