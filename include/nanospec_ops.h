@@ -1,6 +1,6 @@
 /*
  * nanospec_ops.h — C ABI of the serving operators around the draft head
- * (GB300, sm_103a): attention over whole prompts, attention of new tokens
+ * (GB300, sm_103a): norms and rotation of heads, attention over whole prompts, attention of new tokens
  * over a paged key-value cache, the cache's bookkeeping and data movement,
  * and log probabilities of given tokens.
  *
@@ -42,6 +42,33 @@ extern "C" {
 
 /* The sticky flags of the current device (synchronises it); clears them when `clear` is non-zero. */
 NS_API ns_status ns_ops_get_error(uint32_t *flags, int32_t clear);
+
+/*
+ * Norms of queries and keys for each head and their rotation by position, in
+ * one pass.  A row x (one token, one head) of `dim` columns becomes
+ *   y = x * w / sqrt(mean(x^2) + eps)   (eps negative: no norm, y = x),
+ * and then the pairs i of its first `rotary` columns, (i, i + rotary / 2) or,
+ * with `neighbours`, (2i, 2i + 1), turn by t = position * inv_freq[i]:
+ *   (a, b) -> (a cos t - b sin t, b cos t + a sin t).
+ *   d_q   [tokens x q_heads x dim], d_k [tokens x kv_heads x dim] (NULL with
+ *         kv_heads 0) of `dtype` (bf16 or f16), rows of dim consecutive
+ *         elements, strides in elements, multiples of 8; 16-byte aligned
+ *   d_positions int32 [tokens]; d_inv_freq fp64 [rotary / 2], finite; rotary a
+ *         multiple of 16, 0 to dim
+ *   d_q_weight, d_k_weight [dim] of `dtype`, 16-byte aligned, or NULL (ones);
+ *         NULL without a norm
+ *   d_q_out, d_k_out as d_q and d_k, with strides of their own; an output may
+ *         be its input (the same address and strides), and may not overlap the
+ *         inputs otherwise
+ * dim is 64 or 128.  All arithmetic is fp32 and rounded once; angles are taken
+ * modulo a turn in 64-bit fixed point, so far positions lose nothing.
+ */
+NS_API ns_status ns_norm_rotate(const void *d_q, const void *d_k, int32_t dtype, int32_t tokens, int32_t q_heads,
+                                int32_t kv_heads, int32_t dim, int64_t q_token, int64_t q_head, int64_t k_token,
+                                int64_t k_head, const int32_t *d_positions, const double *d_inv_freq, int32_t rotary,
+                                int32_t neighbours, const void *d_q_weight, const void *d_k_weight, float eps,
+                                void *d_q_out, void *d_k_out, int64_t qo_token, int64_t qo_head, int64_t ko_token,
+                                int64_t ko_head, ns_stream stream);
 
 /*
  * Attention over whole prompts: causal, grouped heads, sequences packed one

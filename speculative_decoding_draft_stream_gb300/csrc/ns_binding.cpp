@@ -208,6 +208,73 @@ PyObject *none() {
   return Py_None;
 }
 
+// An output of rows like `in`: given (any strides), or made dense.
+at::Tensor rows_out(PyObject *o, const char *what, const at::Tensor &in, c10::Device d) {
+  if (o == Py_None) return made(in.sizes(), in.scalar_type(), d);
+  const at::Tensor &t = tensor(o, what);
+  rows_of(t, what, d, in.scalar_type(), in.dim());
+  if (t.sizes() != in.sizes()) refuse("%s has another shape than this call's", what);
+  return t;
+}
+
+// Whether rows of [tokens, heads, dim] lie apart, so that they may be written.
+bool rows_apart(const at::Tensor &t) {
+  const int64_t n = t.size(0), h = t.size(1), d = t.size(2), a = t.stride(0), b = t.stride(1);
+  if (t.numel() == 0) return true;
+  if (n > 1 && h > 1) return (b >= d && a >= (h - 1) * b + d) || (a >= d && b >= (n - 1) * a + d);
+  return (n == 1 || a >= d) && (h == 1 || b >= d);
+}
+
+// q, k, positions, inv_freq, q_weight, k_weight, eps, neighbours, q_out, k_out
+PyObject *norm_rotate(PyObject *const *a) {
+  const at::Tensor &q = tensor(a[0], "q");
+  const c10::Device d = device_of(q, "q");
+  const at::ScalarType type = attention_type(q);
+  rows_of(q, "q", d, type, 3);
+  const bool two = a[1] != Py_None;
+  const at::Tensor &k = two ? tensor(a[1], "k") : q;
+  if (two) rows_of(k, "k", d, type, 3);
+  const int64_t T = q.size(0), hq = q.size(1), dim = q.size(2), hkv = two ? k.size(1) : 0;
+  if (two && !shape_is(k, {T, hkv, dim})) refuse("q and k must be [tokens, heads, dim]");
+  if (dim != 64 && dim != 128) refuse("dim must be 64 or 128");
+  fits(T, "tokens"), fits(hq, "q_heads"), fits(hkv, "kv_heads");
+  const int32_t *pos = ints(a[2], "positions", d, {T});
+  const at::Tensor &f = tensor(a[3], "inv_freq");
+  void *freq = given(f, "inv_freq", at::kDouble, d);
+  if (f.dim() != 1 || f.size(0) % 8 || f.size(0) > dim / 2) refuse("inv_freq must have a multiple of 8, up to dim / 2");
+  const bool norm = a[6] != Py_None;
+  void *w[2] = {nullptr, nullptr};
+  for (int i = 0; i < 2; ++i) {
+    const char *what = i ? "k_weight" : "q_weight";
+    if (a[4 + i] == Py_None) continue;
+    if (!norm) refuse("%s without a norm: eps asks for one", what);
+    const at::Tensor &t = tensor(a[4 + i], what);
+    w[i] = given(t, what, type, d, {dim});
+    no_gradient(t, what);
+  }
+  const float eps = norm ? real(a[6], 0.0) : -1.f;
+  if (norm && !(eps >= 0.f)) refuse("eps must not be negative");
+  const int turned = PyObject_IsTrue(a[7]);
+  if (turned < 0) throw Failed{};
+  at::Tensor qo = rows_out(a[8], "q_out", q, d), ko = two ? rows_out(a[9], "k_out", k, d) : at::Tensor();
+  if (!rows_apart(qo) || (two && !rows_apart(ko))) refuse("q_out and k_out must have rows that lie apart");
+  check(ns_norm_rotate(q.data_ptr(), hkv ? k.data_ptr() : nullptr, code(type), (int32_t)T, (int32_t)hq, (int32_t)hkv,
+                       (int32_t)dim, step(q, 0), step(q, 1), step(k, 0), step(k, 1), pos,
+                       static_cast<const double *>(freq), (int32_t)f.size(0) * 2, turned, w[0], w[1], eps,
+                       qo.data_ptr(), hkv ? ko.data_ptr() : nullptr, step(qo, 0), step(qo, 1),
+                       two ? step(ko, 0) : 0, two ? step(ko, 1) : 0, current_stream(d)),
+        "ns_norm_rotate");
+  if (two) return pair(std::move(qo), std::move(ko));
+  PyObject *x = THPVariable_Wrap(std::move(qo)), *r = x ? PyTuple_New(2) : nullptr;
+  if (!r) {
+    Py_XDECREF(x);
+    return nullptr;
+  }
+  PyTuple_SET_ITEM(r, 0, x);
+  PyTuple_SET_ITEM(r, 1, none());
+  return r;
+}
+
 // q, k, v, cu, max_len, scale, out, lse
 PyObject *attend_prompt(PyObject *const *a) {
   const at::Tensor &q = tensor(a[0], "q"), &k = tensor(a[1], "k"), &v = tensor(a[2], "v"), &cu = tensor(a[3], "cu");
@@ -432,6 +499,7 @@ PyObject *set_error(PyObject *const *a) {
 #define NS_ENTRY(name, n, f) \
   { name, reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(&entry<n, f>)), METH_FASTCALL, nullptr }
 PyMethodDef g_methods[] = {NS_ENTRY("set_error", 1, set_error),
+                           NS_ENTRY("norm_rotate", 10, norm_rotate),
                            NS_ENTRY("attend_prompt", 8, attend_prompt),
                            NS_ENTRY("attend_paged", 12, attend_paged),
                            NS_ENTRY("cache", 5, cache),

@@ -26,6 +26,20 @@ cudaError_t launch_pages_compact(const ns_kv_pages &c, const int32_t *seqs, cons
 cudaError_t launch_pages_copy(const ns_kv_pages &c, const int32_t *src, const int32_t *dst, int n, uint32_t *err,
                               cudaStream_t st);
 
+// Norms and rotation of heads (ns_rotate.cu).
+struct RotateArgs {
+  const void *q, *k;
+  int32_t tokens, q_heads, kv_heads, rotary;
+  int64_t q_token, q_head, k_token, k_head;
+  const int32_t *positions;
+  const double *inv_freq;
+  const void *q_weight, *k_weight;
+  float eps;  // negative: no norm
+  void *q_out, *k_out;
+  int64_t qo_token, qo_head, ko_token, ko_head;
+};
+cudaError_t launch_rotate(const RotateArgs &a, int dtype, int dim, bool neighbours, int sms, cudaStream_t st);
+
 // Log probabilities (ns_logprobs.cu).
 struct LogprobArgs {
   const void *logits;

@@ -91,6 +91,34 @@ ns_status ns_ops_get_error(uint32_t *flags, int32_t clear) {
   return NS_OK;
 }
 
+ns_status ns_norm_rotate(const void *d_q, const void *d_k, int32_t dtype, int32_t tokens, int32_t q_heads,
+                         int32_t kv_heads, int32_t dim, int64_t q_token, int64_t q_head, int64_t k_token,
+                         int64_t k_head, const int32_t *d_positions, const double *d_inv_freq, int32_t rotary,
+                         int32_t neighbours, const void *d_q_weight, const void *d_k_weight, float eps, void *d_q_out,
+                         void *d_k_out, int64_t qo_token, int64_t qo_head, int64_t ko_token, int64_t ko_head,
+                         ns_stream stream) {
+  if (!attn_type(dtype, dim) || tokens < 0 || q_heads < 1 || q_heads > 65535 || kv_heads < 0 || kv_heads > 65535 ||
+      rotary < 0 || rotary > dim || rotary % 16 || std::isnan(eps) || std::isinf(eps) ||
+      (eps < 0.f && (d_q_weight || d_k_weight)))
+    return NS_ERR_ARG;
+  if (tokens == 0) return NS_OK;
+  if (!d_q || !d_q_out || (kv_heads > 0 && (!d_k || !d_k_out)) || !d_positions || (rotary > 0 && !d_inv_freq) ||
+      !aligned(d_q, 16) || !aligned(d_k, 16) || !aligned(d_q_out, 16) || !aligned(d_k_out, 16) ||
+      !aligned(d_positions, 4) || !aligned(d_inv_freq, 8) || !aligned(d_q_weight, 16) || !aligned(d_k_weight, 16) ||
+      !by8(q_token) || !by8(q_head) || !by8(k_token) || !by8(k_head) || !by8(qo_token) || !by8(qo_head) ||
+      !by8(ko_token) || !by8(ko_head))
+    return NS_ERR_ARG;
+  const Device *d = nullptr;
+  if (ns_status s = current(&d)) return s;
+  ns::RotateArgs a{};
+  a.q = d_q, a.k = d_k, a.tokens = tokens, a.q_heads = q_heads, a.kv_heads = kv_heads, a.rotary = rotary;
+  a.q_token = q_token, a.q_head = q_head, a.k_token = k_token, a.k_head = k_head;
+  a.positions = d_positions, a.inv_freq = d_inv_freq, a.q_weight = d_q_weight, a.k_weight = d_k_weight, a.eps = eps;
+  a.q_out = d_q_out, a.k_out = d_k_out;
+  a.qo_token = qo_token, a.qo_head = qo_head, a.ko_token = ko_token, a.ko_head = ko_head;
+  return done(ns::launch_rotate(a, dtype, dim, neighbours != 0, d->sms, static_cast<cudaStream_t>(stream)));
+}
+
 ns_status ns_attend_prompt(const void *d_q, const void *d_k, const void *d_v, int32_t dtype, int32_t tokens,
                            int32_t q_heads, int32_t kv_heads, int32_t dim, int64_t q_token, int64_t q_head,
                            int64_t k_token, int64_t k_head, int64_t v_token, int64_t v_head, const int32_t *d_cu,

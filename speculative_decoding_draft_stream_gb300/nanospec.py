@@ -40,7 +40,7 @@ EXPORTED = (
     # include/nanospec_ops.h (bound in serving.py)
     "ns_ops_get_error", "ns_attend_prompt", "ns_attend_paged_workspace", "ns_attend_paged", "ns_pages_truncate",
     "ns_pages_fork", "ns_pages_workspace", "ns_pages_extend", "ns_pages_write", "ns_pages_compact", "ns_pages_copy",
-    "ns_token_logprobs",
+    "ns_token_logprobs", "ns_norm_rotate",
 )
 NOALLOC_MAX_LOGITS = 1 << 20
 
@@ -106,6 +106,8 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
                                       P, P]),
         "ns_get_union": (I32, [P] + [ctypes.POINTER(P)] * 4 + [ctypes.POINTER(I64)]),
         "ns_ops_get_error": (I32, [ctypes.POINTER(ctypes.c_uint32), I32]),
+        "ns_norm_rotate": (I32, [P, P] + [I32] * 5 + [I64] * 4 + [P, P, I32, I32, P, P, ctypes.c_float, P, P] +
+                           [I64] * 4 + [P]),
         "ns_attend_prompt": (I32, [P] * 3 + [I32] * 5 + [I64] * 6 + [P, I32, I32, ctypes.c_float, P, P, P]),
         "ns_attend_paged_workspace": (I64, [I32] * 5),
         "ns_attend_paged": (I32, [P] + [I32] * 6 + [I64] * 3 + [P, P, I32, I32] + [I64] * 6 +

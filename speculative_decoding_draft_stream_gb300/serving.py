@@ -1,5 +1,7 @@
 """The serving operators around the draft head (include/nanospec_ops.h).
 
+* ``norm_rotate``     norms of queries and keys for each head, and their
+                      rotation by position;
 * ``attend_prompt``   causal attention over whole packed prompts;
 * ``attend_paged``    attention of a sequence's new tokens (one, or the nodes
                       of a draft tree) over a paged key-value cache;
@@ -71,9 +73,28 @@ def _on(stream, call):
     with torch.cuda.stream(stream):
         r = call()
     for t in r or ():
-        t.record_stream(stream)
-        t.record_stream(caller)
+        if t is not None:
+            t.record_stream(stream)
+            t.record_stream(caller)
     return r
+
+
+def norm_rotate(q: torch.Tensor, k: Optional[torch.Tensor], positions: torch.Tensor, inv_freq: torch.Tensor, *,
+                q_weight: Optional[torch.Tensor] = None, k_weight: Optional[torch.Tensor] = None,
+                eps: Optional[float] = None, neighbours: bool = False, q_out: Optional[torch.Tensor] = None,
+                k_out: Optional[torch.Tensor] = None, stream=None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """Norms of queries and keys for each head and their rotation by position, in one pass: q [T, Hq, D] and k
+    [T, Hkv, D] or None (bf16 or fp16, D 64 or 128; token and head strides are free multiples of 8 elements).  With
+    eps each row x becomes x * weight / sqrt(mean(x^2) + eps), weights [D] of q's type (None: ones); without, it stays.
+    Then the pairs i of the first 2 len(inv_freq) columns turn by positions * inv_freq[i]: pairs are halves (i, i +
+    len(inv_freq)) or, with neighbours, (2i, 2i + 1); positions int32 [T], inv_freq fp64 (a multiple of 8 of them, up
+    to D / 2).  Returns (q, k) rotated, in q_out and k_out where they are given: rows that lie apart, which may be q
+    and k themselves but may not overlap them otherwise."""
+    s = None if stream is None else _other(stream)
+    if s is not None:
+        return _on(s, lambda: norm_rotate(q, k, positions, inv_freq, q_weight=q_weight, k_weight=k_weight, eps=eps,
+                                          neighbours=neighbours, q_out=q_out, k_out=k_out))
+    return _native().norm_rotate(q, k, positions, inv_freq, q_weight, k_weight, eps, neighbours, q_out, k_out)
 
 
 def attend_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu: torch.Tensor, max_len: int, *,
