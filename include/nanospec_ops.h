@@ -157,6 +157,25 @@ typedef struct ns_kv_pages {
   int32_t *table, *lengths, *refs;
 } ns_kv_pages;
 
+/*
+ * The exponents of a cache of 8 bits, whose rows are row_bytes (64 or 128)
+ * codes in e4m3: a row with exponent byte b stands for code * 2^(b - 127), and
+ * for NaN in each element where b is 255.  Bytes [layers x pages x heads x
+ * page_size], a page's positions one after the other; strides in bytes.
+ * page_size, strides and addresses are multiples of 8.
+ *
+ * ns_pages_write_scaled rounds a row to the smallest power of two by which it
+ * fits: e = ceil(log2(max |x| / 448)), within +-40; codes are x 2^-e to nearest
+ * even (what is above 448 2^40 saturates), the byte is e + 127.  A row that
+ * holds an infinity or NaN gets 255.  Bytes below 87 and from 168 to 254, which
+ * no call writes, may lose precision in ns_attend_paged_scaled.
+ */
+typedef struct ns_kv_scales {
+  uint8_t *k, *v;
+  int64_t k_layer, k_page, k_head;
+  int64_t v_layer, v_page, v_head;
+} ns_kv_scales;
+
 /* Most sequences of one ns_pages_* call. */
 #define NS_MAX_PAGE_SEQS 8192
 
@@ -221,6 +240,56 @@ NS_API ns_status ns_pages_compact(const ns_kv_pages *c, const int32_t *d_seqs, c
  */
 NS_API ns_status ns_pages_copy(const ns_kv_pages *c, const int32_t *d_src, const int32_t *d_dst, int32_t n,
                                ns_stream stream);
+
+/*
+ * The calls above that move rows, over a cache of 8 bits: the exponents move
+ * along.  (ns_pages_truncate and ns_pages_fork move none and take any cache.)
+ */
+NS_API ns_status ns_pages_extend_scaled(const ns_kv_pages *c, const ns_kv_scales *s, const int32_t *d_seqs,
+                                        const int32_t *d_n_new, int32_t n, void *d_ws, int64_t ws_bytes,
+                                        ns_stream stream);
+NS_API ns_status ns_pages_compact_scaled(const ns_kv_pages *c, const ns_kv_scales *s, const int32_t *d_seqs,
+                                         const int32_t *d_base, const int32_t *d_keep, int32_t keep_ld,
+                                         const int32_t *d_n_keep, int32_t n, ns_stream stream);
+NS_API ns_status ns_pages_copy_scaled(const ns_kv_pages *c, const ns_kv_scales *s, const int32_t *d_src,
+                                      const int32_t *d_dst, int32_t n, ns_stream stream);
+
+/* ns_pages_write into a cache of 8 bits: rows of row_bytes elements of `dtype` (bf16 or f16), rounded as said above. */
+NS_API ns_status ns_pages_write_scaled(const ns_kv_pages *c, const ns_kv_scales *s, int32_t layer,
+                                       const int32_t *d_seqs, const int32_t *d_cu, int32_t n, const void *d_k_new,
+                                       const void *d_v_new, int32_t dtype, int64_t k_token, int64_t k_head,
+                                       int64_t v_token, int64_t v_head, int32_t tokens, ns_stream stream);
+
+/*
+ * The other way round: tokens d_cu[i] .. d_cu[i+1] - 1 of d_k and d_v become
+ * the last positions of sequence d_seqs[i] in one layer, bytes as they are or,
+ * with s, what the codes stand for, in `dtype` (bf16 or f16; ignored without
+ * s; f16 rounds what is above its range to infinity).  A sequence may stand
+ * there more than once.  Tokens of an invalid sequence or page are not written.
+ */
+NS_API ns_status ns_pages_read(const ns_kv_pages *c, const ns_kv_scales *s, int32_t layer, const int32_t *d_seqs,
+                               const int32_t *d_cu, int32_t n, void *d_k, void *d_v, int32_t dtype, int64_t k_token,
+                               int64_t k_head, int64_t v_token, int64_t v_head, int32_t tokens, ns_stream stream);
+
+/*
+ * ns_attend_paged over one layer of a cache of 8 bits: d_k and d_v are codes
+ * [n_pages x kv_heads x page_size x dim] with strides in bytes, multiples of
+ * 16, d_k_exp and d_v_exp their exponents [n_pages x kv_heads x page_size],
+ * strides of page and head multiples of 8, as the addresses are.  `dtype` is
+ * that of d_q and d_out.  The products see the codes' values exactly;
+ * probabilities are rounded to fp16 with the value's scale in them (up to 16
+ * rows, or queries as said at d_q that TMA cannot fetch), or to `dtype`.
+ */
+NS_API ns_status ns_attend_paged_scaled(const void *d_q, int32_t dtype, int32_t n_seqs, int32_t n, int32_t q_heads,
+                                        int32_t kv_heads, int32_t dim, int64_t q_seq, int64_t q_token, int64_t q_head,
+                                        const void *d_k, const void *d_v, int32_t n_pages, int32_t page_size,
+                                        int64_t k_page, int64_t k_head, int64_t k_token, int64_t v_page,
+                                        int64_t v_head, int64_t v_token, const uint8_t *d_k_exp,
+                                        const uint8_t *d_v_exp, int64_t ke_page, int64_t ke_head, int64_t ve_page,
+                                        int64_t ve_head, const int32_t *d_table, int32_t table_ld, int32_t max_seqs,
+                                        const int32_t *d_lengths, const int32_t *d_seqs, const int64_t *d_mask,
+                                        float scale, int32_t max_len, void *d_out, float *d_lse, void *d_ws,
+                                        int64_t ws_bytes, ns_stream stream);
 
 /*
  * Log probabilities of given tokens under softmax(logits / temperature), with

@@ -70,6 +70,21 @@ struct Type<__half> {
   }
 };
 
+// e4m3, two at a time (the first in the lower half), and the scale that a row's exponent byte stands for.
+__device__ __forceinline__ uint16_t to_e4m3(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint32_t from_e4m3(uint32_t pair) {  // (upper half ignored)
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)pair));
+  return r;
+}
+__device__ __forceinline__ float scale_of(uint32_t byte) {
+  return __uint_as_float(byte << 23 | (byte == 255u ? 0x400000u : 0u));  // 2^(byte - 127); 255: NaN
+}
+
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -91,6 +106,9 @@ __device__ __forceinline__ void ldsm4t(uint32_t a, uint32_t *r) {
 __device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool ok) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
 }
+__device__ __forceinline__ void cp8(uint32_t dst, const void *src, bool ok) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(ok ? 8 : 0) : "memory");
+}
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_wait() {
@@ -101,6 +119,34 @@ __device__ __forceinline__ void cp_wait() {
 template <int D>
 __device__ __forceinline__ uint32_t piece(int r, int c) {
   return (uint32_t)(r * (D * 2) + ((c ^ (r & 7)) << 4));
+}
+
+// The same of rows of D bytes.  Rows of 64 share a line of 128 by twos, and the
+// lines' pieces are permuted by twice the line, so that four rows two apart
+// have their first 16 bytes, and their 8-byte pieces, in different banks.
+template <int D>
+__device__ __forceinline__ uint32_t piece8(int r, int c) {
+  if (D == 128) return (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4));
+  return (uint32_t)((r >> 1) * 128 + ((((r & 1) * 4 + c) ^ (r & 6)) << 4));
+}
+__device__ __forceinline__ void lds16(uint32_t a, uint32_t *r) {
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(a)
+               : "memory");
+}
+__device__ __forceinline__ void lds8(uint32_t a, uint32_t *r) {
+  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(a) : "memory");
+}
+__device__ __forceinline__ uint32_t lds2(uint32_t a) {
+  uint16_t r;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(r) : "r"(a) : "memory");
+  return r;
+}
+__device__ __forceinline__ uint32_t lds1(uint32_t a) {
+  uint32_t r;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(r) : "r"(a) : "memory");
+  return r;
 }
 
 // State of 16 rows of a warp.  Lane (g = lane / 4, t = lane % 4) holds rows g
@@ -229,6 +275,146 @@ struct Rows {
     }
   }
 
+  // The same with keys and values of 8 bits (T is fp16): rows of D codes at sK
+  // and sV, their exponents' bytes at sKe and sVe.  cq: each row's factor c.
+  // Lane (g, t) reads columns D / 4 t .. of key g of each eight, so product kk's
+  // columns are D / 4 t + 4 kk .. + 3 (as q's must be), and columns D / 8 g .. of
+  // values 2 t, 2 t + 1, 2 t + 8 and 2 t + 9 of each 16: its share of o has
+  // columns D / 8 (2 t) + i and D / 8 (2 t + 1) + i in group i.
+  template <int NK, bool kMasked, typename Hidden>
+  __device__ __forceinline__ void tile8(const uint32_t (*q)[4], uint32_t sK, uint32_t sV, uint32_t sKe, uint32_t sVe,
+                                        int k0, const float *cq, const Hidden &hidden, bool wild) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    float s[NK / 8][4];
+#pragma unroll
+    for (int i = 0; i < NK / 8; ++i) {
+      uint32_t w[D / 16];
+      if (D == 128) {
+        lds16(sK + piece8<D>(k0 + i * 8 + g, 2 * t), w);
+        lds16(sK + piece8<D>(k0 + i * 8 + g, 2 * t + 1), w + D / 32);
+      } else {
+        lds16(sK + piece8<D>(k0 + i * 8 + g, t), w);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) Type<T>::mma(s[i], q[kk], from_e4m3(w[kk]), from_e4m3(w[kk] >> 16));
+    }
+    float unit[NK / 8][2];  // 2^-ve
+    float top[2] = {kNegInf, kNegInf};
+#pragma unroll
+    for (int i = 0; i < NK / 8; ++i) {
+      const uint32_t ke = lds2(sKe + k0 + i * 8 + 2 * t), ve = lds2(sVe + k0 + i * 8 + 2 * t);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const uint32_t bk = e ? ke >> 8 : ke & 255, bv = e ? ve >> 8 : ve & 255;
+        const float f = scale_of(bk);
+        // the byte as a number, less 127; NaN for 255
+        const float add = bv == 255u ? __uint_as_float(0x7fffffffu) : __uint_as_float(0x4b000000u | bv) - 8388735.f;
+        unit[i][e] = __uint_as_float((254u - min(bv, 254u)) << 23);  // (finite: a hidden key's p is 0)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float &x = s[i][2 * h + e];
+          x = fmaf(x * f, cq[h], add);
+          if (kMasked && hidden(h, i * 8 + 2 * t + e)) x = kNegInf;
+          top[h] = fmaxf(top[h], x);
+        }
+      }
+    }
+    float shift[2], p2[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], 1));
+      top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], 2));
+      const float now = fmaxf(m[h], top[h]), safe = now == kNegInf ? 0.f : now;
+      p2[h] = ex2(m[h] - safe);
+      m[h] = now;
+      shift[h] = Type<T>::kOffset - safe;
+    }
+    float add[2] = {0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < NK / 8; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        s[i][j] = ex2(s[i][j] + shift[j >> 1]);
+        add[j >> 1] = fmaf(s[i][j], unit[i][j & 1], add[j >> 1]);
+      }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) l[h] = l[h] * p2[h] + add[h];
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i) {
+      o[i][0] *= p2[0];
+      o[i][1] *= p2[0];
+      o[i][2] *= p2[1];
+      o[i][3] *= p2[1];
+    }
+    if (kMasked && wild) {  // one key at a time, and only into rows that see it
+#pragma unroll 1
+      for (int key = 0; key < NK; ++key) {
+        float pa = 0.f, pb = 0.f;
+#pragma unroll
+        for (int i = 0; i < NK / 8; ++i)
+          if (i == key >> 3) {
+            pa = (key & 1) ? s[i][1] : s[i][0];
+            pb = (key & 1) ? s[i][3] : s[i][2];
+          }
+        const int from = (lane & ~3) | ((key & 7) >> 1);
+        pa = __shfl_sync(0xffffffffu, pa, from);
+        pb = __shfl_sync(0xffffffffu, pb, from);
+        const bool ha = hidden(0, key), hb = hidden(1, key);
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int d = D / 8 * (2 * t + e) + i;
+            const float v = Type<T>::unpack(from_e4m3(lds1(sV + piece8<D>(k0 + key, d >> 4) + (d & 15)))).x;
+            if (!ha) o[i][e] = fmaf(pa, v, o[i][e]);
+            if (!hb) o[i][2 + e] = fmaf(pb, v, o[i][2 + e]);
+          }
+      }
+      return;
+    }
+#pragma unroll
+    for (int kb = 0; kb < NK / 16; ++kb) {
+      const uint32_t a[4] = {Type<T>::pack(s[2 * kb][0], s[2 * kb][1]), Type<T>::pack(s[2 * kb][2], s[2 * kb][3]),
+                             Type<T>::pack(s[2 * kb + 1][0], s[2 * kb + 1][1]),
+                             Type<T>::pack(s[2 * kb + 1][2], s[2 * kb + 1][3])};
+      uint32_t v[4][D / 32];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int row = k0 + kb * 16 + 2 * t + (r & 1) + (r >> 1) * 8;
+        if (D == 128)
+          lds16(sV + piece8<D>(row, g), v[r]);
+        else
+          lds8(sV + piece8<D>(row, g >> 1) + (g & 1) * 8, v[r]);
+      }
+#pragma unroll
+      for (int x = 0; x < D / 32; ++x)
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {  // columns 4 x + 2 y and the next, of keys 2 t, 2 t + 1; 2 t + 8, 2 t + 9
+          const uint32_t sel = y ? 0x7362u : 0x5140u;
+          const uint32_t lo = __byte_perm(v[0][x], v[1][x], sel), hi = __byte_perm(v[2][x], v[3][x], sel);
+          Type<T>::mma(o[4 * x + 2 * y], a, from_e4m3(lo), from_e4m3(hi));
+          Type<T>::mma(o[4 * x + 2 * y + 1], a, from_e4m3(lo >> 16), from_e4m3(hi >> 16));
+        }
+    }
+  }
+
+  // This lane's columns of row h (of its two), two neighbours at a time: to(column, o, o).
+  template <bool F8, typename To>
+  __device__ __forceinline__ void columns(int h, const To &to) const {
+    const int t = threadIdx.x & 3;
+    if constexpr (F8) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int i = 0; i < D / 8; i += 2) to(D / 8 * (2 * t + e) + i, o[i][2 * h + e], o[i + 1][2 * h + e]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) to(8 * i + 2 * t, o[i][2 * h], o[i][2 * h + 1]);
+    }
+  }
+
   // The lanes of a row add up their shares of l (once, after the last tile).
   __device__ __forceinline__ void sum_l() {
 #pragma unroll
@@ -263,6 +449,19 @@ __device__ __forceinline__ bool wild_pieces(uint32_t a, int n, int tid, int thre
   }
   const uint32_t m = __vmaxu2(most[0], most[1]);
   return (m & 0xffffu) >= Type<T>::kInf || (m >> 16) >= Type<T>::kInf;
+}
+
+// The same of n 16-byte pieces of e4m3 codes: NaN is all ones but the sign.
+__device__ __forceinline__ bool wild_codes(uint32_t a, int n, int tid, int threads) {
+  uint32_t any = 0;
+#pragma unroll 8
+  for (int i = tid; i < n; i += threads) {
+    uint32_t x[4];
+    lds16(a + 16u * (uint32_t)i, x);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) any |= __vcmpeq4(x[j] & 0x7f7f7f7fu, 0x7f7f7f7fu);
+  }
+  return any != 0;
 }
 
 }  // namespace attn

@@ -299,14 +299,26 @@ PyObject *attend_prompt(PyObject *const *a) {
   return pair(std::move(out), std::move(lse));
 }
 
-// q, k_pages, v_pages, table, lengths, seqs, mask, scale, max_len, out, lse, workspace
+constexpr at::ScalarType kCodes = at::kFloat8_e4m3fn;  // of a cache of 8 bits
+
+// The exponents of rows `of` (all but the last dimension).
+void exponents_of(const at::Tensor &t, const char *what, c10::Device d, const at::Tensor &of) {
+  rows_of(t, what, d, at::kByte, of.dim() - 1);
+  if (t.sizes() != of.sizes().slice(0, of.dim() - 1)) refuse("%s must have a byte for each row", what);
+}
+
+// q, k_pages, v_pages, table, lengths, seqs, mask, scale, max_len, out, lse, workspace, k_exp, v_exp
 PyObject *attend_paged(PyObject *const *a) {
   const at::Tensor &q = tensor(a[0], "q"), &k = tensor(a[1], "k_pages"), &v = tensor(a[2], "v_pages");
   const c10::Device d = device_of(q, "q");
   const at::ScalarType type = attention_type(q);
-  rows_of(q, "q", d, type, 4), rows_of(k, "k_pages", d, type, 4), rows_of(v, "v_pages", d, type, 4);
+  const bool scaled = a[12] != Py_None || a[13] != Py_None;
+  const at::ScalarType held = scaled ? kCodes : type;
+  rows_of(q, "q", d, type, 4), rows_of(k, "k_pages", d, held, 4), rows_of(v, "v_pages", d, held, 4);
   const int64_t B = q.size(0), n = q.size(1), hq = q.size(2), dim = q.size(3), hkv = k.size(1);
   if (k.size(3) != dim || v.sizes() != k.sizes()) refuse("k_pages and v_pages must have q's dim");
+  const at::Tensor &ke = scaled ? tensor(a[12], "k_exp") : k, &ve = scaled ? tensor(a[13], "v_exp") : v;
+  if (scaled) exponents_of(ke, "k_exp", d, k), exponents_of(ve, "v_exp", d, v);
   if (hkv == 0 || hq % hkv) refuse("q_heads must be a multiple of kv_heads");
   if (n < 1 || n > NS_MAX_NEW || B > NS_MAX_ATTEND_SEQS)
     refuse("at most %d new tokens and %d sequences", NS_MAX_NEW, NS_MAX_ATTEND_SEQS);
@@ -321,6 +333,18 @@ PyObject *attend_paged(PyObject *const *a) {
   int64_t bytes;
   const at::Tensor ws =
       workspace(a[11], ns_attend_paged_workspace((int32_t)B, (int32_t)n, (int32_t)hq, (int32_t)hkv, (int32_t)dim), d, bytes);
+  if (scaled) {
+    check(ns_attend_paged_scaled(q.data_ptr(), code(type), (int32_t)B, (int32_t)n, (int32_t)hq, (int32_t)hkv,
+                                 (int32_t)dim, step(q, 0), step(q, 1), step(q, 2), k.data_ptr(), v.data_ptr(),
+                                 (int32_t)k.size(0), (int32_t)k.size(2), step(k, 0), step(k, 1), step(k, 2),
+                                 step(v, 0), step(v, 1), step(v, 2), static_cast<const uint8_t *>(ke.data_ptr()),
+                                 static_cast<const uint8_t *>(ve.data_ptr()), step(ke, 0), step(ke, 1), step(ve, 0),
+                                 step(ve, 1), table, (int32_t)ld, (int32_t)rows, lengths, seqs, mask,
+                                 real(a[7], 1.0 / std::sqrt((double)dim)), (int32_t)integer(a[8], "max_len"),
+                                 out.data_ptr(), lse.data_ptr<float>(), ws.data_ptr(), bytes, current_stream(d)),
+          "ns_attend_paged_scaled");
+    return pair(std::move(out), std::move(lse));
+  }
   check(ns_attend_paged(q.data_ptr(), code(type), (int32_t)B, (int32_t)n, (int32_t)hq, (int32_t)hkv, (int32_t)dim,
                         step(q, 0), step(q, 1), step(q, 2), k.data_ptr(), v.data_ptr(), (int32_t)k.size(0),
                         (int32_t)k.size(2), step(k, 0), step(k, 1), step(k, 2), step(v, 0), step(v, 1), step(v, 2),
@@ -335,6 +359,8 @@ struct Cache {
   ns_kv_pages c;
   at::ScalarType type;
   c10::Device device;
+  bool scaled;  // of 8 bits, with exponents
+  ns_kv_scales s;
 };
 constexpr const char *kCache = "ns_kv_pages";
 
@@ -347,7 +373,7 @@ Cache &cache_of(PyObject *o) {
   return c;
 }
 
-// k, v, table, lengths, refs (the caller keeps the tensors alive)
+// k, v, table, lengths, refs, k_exp, v_exp (the caller keeps the tensors alive)
 PyObject *cache(PyObject *const *a) {
   const at::Tensor &k = tensor(a[0], "k"), &v = tensor(a[1], "v");
   const c10::Device d = device_of(k, "k");
@@ -355,7 +381,7 @@ PyObject *cache(PyObject *const *a) {
   if (k.sizes() != v.sizes()) refuse("k and v must be [layers, pages, heads, page_size, dim]");
   const int64_t e = (int64_t)k.element_size();
   int64_t rows, ld;
-  Cache c{{}, k.scalar_type(), d};
+  Cache c{{}, k.scalar_type(), d, a[5] != Py_None || a[6] != Py_None, {}};
   c.c.table = ints_2d(a[2], "table", d, rows, ld);
   c.c.lengths = ints(a[3], "lengths", d, {rows});
   c.c.refs = ints(a[4], "refs", d, {k.size(1)});
@@ -367,6 +393,16 @@ PyObject *cache(PyObject *const *a) {
   c.c.layers = (int32_t)k.size(0), c.c.pages = (int32_t)k.size(1), c.c.heads = (int32_t)k.size(2);
   c.c.page_size = (int32_t)k.size(3), c.c.row_bytes = (int32_t)(k.size(4) * e);
   c.c.max_seqs = (int32_t)rows, c.c.table_ld = (int32_t)ld;
+  if (c.scaled) {
+    const at::Tensor &ke = tensor(a[5], "k_exp"), &ve = tensor(a[6], "v_exp");
+    if (c.type != kCodes) refuse("a cache with exponents must hold %s", c10::toString(kCodes));
+    exponents_of(ke, "k_exp", d, k), exponents_of(ve, "v_exp", d, v);
+    if ((k.size(4) != 64 && k.size(4) != 128) || k.size(3) % 8)
+      refuse("a cache with exponents must have 64 or 128 columns and pages of a multiple of 8");
+    c.s.k = static_cast<uint8_t *>(ke.data_ptr()), c.s.v = static_cast<uint8_t *>(ve.data_ptr());
+    c.s.k_layer = step(ke, 0), c.s.k_page = step(ke, 1), c.s.k_head = step(ke, 2);
+    c.s.v_layer = step(ve, 0), c.s.v_page = step(ve, 1), c.s.v_head = step(ve, 2);
+  }
   Cache *mine = new Cache(c);
   PyObject *cap =
       PyCapsule_New(mine, kCache, [](PyObject *o) { delete static_cast<Cache *>(PyCapsule_GetPointer(o, kCache)); });
@@ -407,8 +443,11 @@ PyObject *extend(PyObject *const *a) {
   const int32_t *seqs = ints(a[1], "seqs", c.device, {n}), *add = ints(a[2], "n_new", c.device, {n});
   int64_t bytes;
   const at::Tensor ws = workspace(a[3], ns_pages_workspace(&c.c, (int32_t)n), c.device, bytes);
-  check(ns_pages_extend(&c.c, seqs, add, (int32_t)n, ws.data_ptr(), bytes, current_stream(c.device)),
-        "ns_pages_extend");
+  const ns_stream st = current_stream(c.device);
+  if (c.scaled)
+    check(ns_pages_extend_scaled(&c.c, &c.s, seqs, add, (int32_t)n, ws.data_ptr(), bytes, st), "ns_pages_extend_scaled");
+  else
+    check(ns_pages_extend(&c.c, seqs, add, (int32_t)n, ws.data_ptr(), bytes, st), "ns_pages_extend");
   return none();
 }
 
@@ -417,17 +456,57 @@ PyObject *write(PyObject *const *a) {
   Cache &c = cache_of(a[0]);
   const int64_t n = count(a[2], "seqs");
   const at::Tensor &k = tensor(a[4], "k_new"), &v = tensor(a[5], "v_new");
-  rows_of(k, "k_new", c.device, c.type, 3), rows_of(v, "v_new", c.device, c.type, 3);
-  const int64_t e = (int64_t)k.element_size();
-  if (k.size(1) != c.c.heads || k.size(2) * e != c.c.row_bytes || v.sizes() != k.sizes())
-    refuse("k_new and v_new must be [tokens, %d, %d]", (int)c.c.heads, (int)(c.c.row_bytes / e));
+  const at::ScalarType type = c.scaled ? k.scalar_type() : c.type;
+  if (type != c.type && type != at::kBFloat16 && type != at::kHalf) refuse("k_new must be bf16 or fp16");
+  if (c.scaled && type == c.type) refuse("k_new must be bf16 or fp16: write makes the codes");
+  rows_of(k, "k_new", c.device, type, 3), rows_of(v, "v_new", c.device, type, 3);
+  const int64_t e = (int64_t)k.element_size(), dim = c.scaled ? c.c.row_bytes : c.c.row_bytes / e;
+  if (k.size(1) != c.c.heads || k.size(2) != dim || v.sizes() != k.sizes())
+    refuse("k_new and v_new must be [tokens, %d, %d]", (int)c.c.heads, (int)dim);
   fits(k.size(0), "tokens");
   const int32_t *seqs = ints(a[2], "seqs", c.device, {n}), *cu = ints(a[3], "cu", c.device, {n + 1});
+  if (c.scaled) {
+    check(ns_pages_write_scaled(&c.c, &c.s, (int32_t)integer(a[1], "layer"), seqs, cu, (int32_t)n, k.data_ptr(),
+                                v.data_ptr(), code(type), step(k, 0) * e, step(k, 1) * e, step(v, 0) * e,
+                                step(v, 1) * e, (int32_t)k.size(0), stream_of(a[6], c.device)),
+          "ns_pages_write_scaled");
+    return none();
+  }
   check(ns_pages_write(&c.c, (int32_t)integer(a[1], "layer"), seqs, cu, (int32_t)n, k.data_ptr(), v.data_ptr(),
                        step(k, 0) * e, step(k, 1) * e, step(v, 0) * e, step(v, 1) * e, (int32_t)k.size(0),
                        stream_of(a[6], c.device)),
         "ns_pages_write");
   return none();
+}
+
+// cache, layer, seqs, cu, tokens, half (of a cache of 8 bits: fp16 rows, not bf16), k_out, v_out
+PyObject *read(PyObject *const *a) {
+  Cache &c = cache_of(a[0]);
+  const int64_t n = count(a[2], "seqs"), tokens = integer(a[4], "tokens");
+  if (tokens < 0) refuse("tokens must not be negative");
+  const int half = PyObject_IsTrue(a[5]);
+  if (half < 0) throw Failed{};
+  const at::ScalarType type = !c.scaled ? c.type : half ? at::kHalf : at::kBFloat16;
+  const int64_t e = (int64_t)c10::elementSize(type), dim = c.scaled ? c.c.row_bytes : c.c.row_bytes / e;
+  at::Tensor out[2];
+  for (int i = 0; i < 2; ++i) {
+    const char *what = i ? "v_out" : "k_out";
+    if (a[6 + i] == Py_None) {
+      out[i] = made({tokens, c.c.heads, dim}, type, c.device);
+      continue;
+    }
+    out[i] = tensor(a[6 + i], what);
+    rows_of(out[i], what, c.device, type, 3);
+    if (!shape_is(out[i], {tokens, c.c.heads, dim})) refuse("%s has another shape than this call's", what);
+    if (!rows_apart(out[i])) refuse("%s must have rows that lie apart", what);
+  }
+  const int32_t *seqs = ints(a[2], "seqs", c.device, {n}), *cu = ints(a[3], "cu", c.device, {n + 1});
+  check(ns_pages_read(&c.c, c.scaled ? &c.s : nullptr, (int32_t)integer(a[1], "layer"), seqs, cu, (int32_t)n,
+                      out[0].data_ptr(), out[1].data_ptr(), half ? NS_DTYPE_F16 : NS_DTYPE_BF16, step(out[0], 0) * e,
+                      step(out[0], 1) * e, step(out[1], 0) * e, step(out[1], 1) * e, (int32_t)tokens,
+                      current_stream(c.device)),
+        "ns_pages_read");
+  return pair(std::move(out[0]), std::move(out[1]));
 }
 
 // cache, seqs, base, keep, n_keep, stream
@@ -440,8 +519,12 @@ PyObject *compact(PyObject *const *a) {
   fits(ld, "keep");
   const int32_t *seqs = ints(a[1], "seqs", c.device, {n}), *base = ints(a[2], "base", c.device, {n});
   const int32_t *n_keep = ints(a[4], "n_keep", c.device, {n});
-  check(ns_pages_compact(&c.c, seqs, base, keep, (int32_t)ld, n_keep, (int32_t)n, stream_of(a[5], c.device)),
-        "ns_pages_compact");
+  const ns_stream st = stream_of(a[5], c.device);
+  if (c.scaled)
+    check(ns_pages_compact_scaled(&c.c, &c.s, seqs, base, keep, (int32_t)ld, n_keep, (int32_t)n, st),
+          "ns_pages_compact_scaled");
+  else
+    check(ns_pages_compact(&c.c, seqs, base, keep, (int32_t)ld, n_keep, (int32_t)n, st), "ns_pages_compact");
   return none();
 }
 
@@ -450,7 +533,11 @@ PyObject *copy_(PyObject *const *a) {
   Cache &c = cache_of(a[0]);
   const int64_t n = count(a[1], "src");
   const int32_t *src = ints(a[1], "src", c.device, {n}), *dst = ints(a[2], "dst", c.device, {n});
-  check(ns_pages_copy(&c.c, src, dst, (int32_t)n, stream_of(a[3], c.device)), "ns_pages_copy");
+  const ns_stream st = stream_of(a[3], c.device);
+  if (c.scaled)
+    check(ns_pages_copy_scaled(&c.c, &c.s, src, dst, (int32_t)n, st), "ns_pages_copy_scaled");
+  else
+    check(ns_pages_copy(&c.c, src, dst, (int32_t)n, st), "ns_pages_copy");
   return none();
 }
 
@@ -501,12 +588,13 @@ PyObject *set_error(PyObject *const *a) {
 PyMethodDef g_methods[] = {NS_ENTRY("set_error", 1, set_error),
                            NS_ENTRY("norm_rotate", 10, norm_rotate),
                            NS_ENTRY("attend_prompt", 8, attend_prompt),
-                           NS_ENTRY("attend_paged", 12, attend_paged),
-                           NS_ENTRY("cache", 5, cache),
+                           NS_ENTRY("attend_paged", 14, attend_paged),
+                           NS_ENTRY("cache", 7, cache),
                            NS_ENTRY("truncate", 4, truncate),
                            NS_ENTRY("fork", 4, fork_),
                            NS_ENTRY("extend", 4, extend),
                            NS_ENTRY("write", 7, write),
+                           NS_ENTRY("read", 8, read),
                            NS_ENTRY("compact", 6, compact),
                            NS_ENTRY("copy", 4, copy_),
                            NS_ENTRY("token_logprobs", 4, token_logprobs),

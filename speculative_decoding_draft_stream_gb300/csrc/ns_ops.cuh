@@ -16,15 +16,24 @@ cudaError_t launch_pages_truncate(const ns_kv_pages &c, const int32_t *seqs, con
 cudaError_t launch_pages_fork(const ns_kv_pages &c, const int32_t *src, const int32_t *dst, int n, uint32_t *err,
                               cudaStream_t st);
 int64_t pages_extend_ws(const ns_kv_pages &c, int n);
-cudaError_t launch_pages_extend(const ns_kv_pages &c, const int32_t *seqs, const int32_t *n_new, int n, void *ws,
-                                uint32_t *err, cudaStream_t st);
+// (sc: the exponents of a cache of 8 bits, or NULL)
+cudaError_t launch_pages_extend(const ns_kv_pages &c, const ns_kv_scales *sc, const int32_t *seqs,
+                                const int32_t *n_new, int n, void *ws, uint32_t *err, cudaStream_t st);
 cudaError_t launch_pages_write(const ns_kv_pages &c, int layer, const int32_t *seqs, const int32_t *cu, int n,
                                const void *k_new, const void *v_new, int64_t k_token, int64_t k_head,
                                int64_t v_token, int64_t v_head, int tokens, uint32_t *err, cudaStream_t st);
-cudaError_t launch_pages_compact(const ns_kv_pages &c, const int32_t *seqs, const int32_t *base, const int32_t *keep,
-                                 int keep_ld, const int32_t *n_keep, int n, uint32_t *err, cudaStream_t st);
-cudaError_t launch_pages_copy(const ns_kv_pages &c, const int32_t *src, const int32_t *dst, int n, uint32_t *err,
-                              cudaStream_t st);
+cudaError_t launch_pages_write_scaled(const ns_kv_pages &c, const ns_kv_scales &sc, int layer, const int32_t *seqs,
+                                      const int32_t *cu, int n, const void *k_new, const void *v_new, int dtype,
+                                      int64_t k_token, int64_t k_head, int64_t v_token, int64_t v_head, int tokens,
+                                      uint32_t *err, cudaStream_t st);
+cudaError_t launch_pages_read(const ns_kv_pages &c, const ns_kv_scales *sc, int layer, const int32_t *seqs,
+                              const int32_t *cu, int n, void *k, void *v, int dtype, int64_t k_token, int64_t k_head,
+                              int64_t v_token, int64_t v_head, int tokens, uint32_t *err, cudaStream_t st);
+cudaError_t launch_pages_compact(const ns_kv_pages &c, const ns_kv_scales *sc, const int32_t *seqs,
+                                 const int32_t *base, const int32_t *keep, int keep_ld, const int32_t *n_keep, int n,
+                                 uint32_t *err, cudaStream_t st);
+cudaError_t launch_pages_copy(const ns_kv_pages &c, const ns_kv_scales *sc, const int32_t *src, const int32_t *dst,
+                              int n, uint32_t *err, cudaStream_t st);
 
 // Norms and rotation of heads (ns_rotate.cu).
 struct RotateArgs {
@@ -69,15 +78,22 @@ struct PagedAttnArgs {
   float *lse;
   void *ws;
   uint32_t *err;
+  const uint8_t *k_exp, *v_exp;  // a cache of 8 bits: each row's exponent
+  int64_t ke_page, ke_head, ve_page, ve_head;
 };
 // What a device holds of the kernels for few rows (found when it is first used).
 struct PagedFit {
-  int clusters[2][2][2];  // resident at once: dtype, dim 64 or 128, small or large CTAs
+  int clusters[2][2][2][2];  // resident at once: cache of 8 bits, dtype, dim 64 or 128, small or large CTAs
 };
 int64_t paged_attn_ws(int n_seqs, int n, int q_heads, int kv_heads, int dim, int sms);
 cudaError_t prepare_paged_attn(PagedFit *fit);
 cudaError_t launch_paged_attn(const PagedAttnArgs &a, int dtype, int dim, int sms, const PagedFit &fit,
                               cudaStream_t st);
+
+// The same over a cache of 8 bits (ns_paged_attn8.cu).
+cudaError_t prepare_paged_attn8(PagedFit *fit);
+cudaError_t launch_paged_attn8(const PagedAttnArgs &a, int dtype, int dim, int sms, const PagedFit &fit,
+                               cudaStream_t st);
 
 // The same for more than 16 rows, on tcgen05 (ns_paged_umma.cu).
 bool paged_umma_ok(const PagedAttnArgs &a);

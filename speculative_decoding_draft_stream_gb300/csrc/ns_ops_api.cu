@@ -75,6 +75,15 @@ bool cache_ok(const ns_kv_pages *c) {
          c->table_ld <= (1 << 20) && (int64_t)c->table_ld * c->page_size <= 0x7fffffffLL &&
          (int64_t)c->page_size * c->row_bytes <= 0x7fffffffLL / 16 && (int64_t)c->heads * c->row_bytes <= 0x7fffffffLL;
 }
+// (sc: NULL for a cache of 16 bits)
+bool scales_ok(const ns_kv_pages *c, const ns_kv_scales *sc) {
+  if (!sc) return true;
+  if (!sc->k || !sc->v || !aligned(sc->k, 8) || !aligned(sc->v, 8)) return false;
+  const int64_t strides[6] = {sc->k_layer, sc->k_page, sc->k_head, sc->v_layer, sc->v_page, sc->v_head};
+  for (int64_t s : strides)
+    if (!by8(s)) return false;
+  return (c->row_bytes == 64 || c->row_bytes == 128) && c->page_size % 8 == 0;
+}
 bool page_seqs(int n) { return n >= 0 && n <= NS_MAX_PAGE_SEQS; }
 
 }  // namespace
@@ -154,13 +163,20 @@ int64_t ns_attend_paged_workspace(int32_t n_seqs, int32_t n, int32_t q_heads, in
   return ns::paged_attn_ws(n_seqs, n, q_heads, kv_heads, dim, d->sms);
 }
 
-ns_status ns_attend_paged(const void *d_q, int32_t dtype, int32_t n_seqs, int32_t n, int32_t q_heads,
-                          int32_t kv_heads, int32_t dim, int64_t q_seq, int64_t q_token, int64_t q_head,
-                          const void *d_k, const void *d_v, int32_t n_pages, int32_t page_size, int64_t k_page,
-                          int64_t k_head, int64_t k_token, int64_t v_page, int64_t v_head, int64_t v_token,
-                          const int32_t *d_table, int32_t table_ld, int32_t max_seqs, const int32_t *d_lengths,
-                          const int32_t *d_seqs, const int64_t *d_mask, float scale, int32_t max_len, void *d_out,
-                          float *d_lse, void *d_ws, int64_t ws_bytes, ns_stream stream) {
+// The exponents of a cache of 8 bits (k NULL: a cache of 16).
+struct Exponents {
+  const uint8_t *k, *v;
+  int64_t k_page, k_head, v_page, v_head;
+};
+
+static ns_status attend_paged(const void *d_q, int32_t dtype, int32_t n_seqs, int32_t n, int32_t q_heads,
+                              int32_t kv_heads, int32_t dim, int64_t q_seq, int64_t q_token, int64_t q_head,
+                              const void *d_k, const void *d_v, int32_t n_pages, int32_t page_size, int64_t k_page,
+                              int64_t k_head, int64_t k_token, int64_t v_page, int64_t v_head, int64_t v_token,
+                              const Exponents &x, const int32_t *d_table, int32_t table_ld, int32_t max_seqs,
+                              const int32_t *d_lengths, const int32_t *d_seqs, const int64_t *d_mask, float scale,
+                              int32_t max_len, void *d_out, float *d_lse, void *d_ws, int64_t ws_bytes,
+                              ns_stream stream) {
   if (!attn_type(dtype, dim) || !heads_ok(q_heads, kv_heads) || n_seqs < 0 || n_seqs > NS_MAX_ATTEND_SEQS || n < 1 ||
       n > NS_MAX_NEW || n_pages < 1 || page_size < 8 || page_size > 1024 || (page_size & (page_size - 1)) ||
       table_ld < 1 || max_seqs < 1 || (int64_t)table_ld * page_size > NS_MAX_POSITIONS || max_len < 0 ||
@@ -172,6 +188,10 @@ ns_status ns_attend_paged(const void *d_q, int32_t dtype, int32_t n_seqs, int32_
       !aligned(d_lengths, 4) || !aligned(d_seqs, 4) || !aligned(d_mask, 8) || !aligned(d_ws, 16) || q_seq % 2 ||
       q_token % 2 || q_head % 2 || !by8(k_page) || !by8(k_head) || !by8(k_token) || !by8(v_page) || !by8(v_head) ||
       !by8(v_token))
+    return NS_ERR_ARG;
+  if (x.k && (!aligned(x.k, 8) || !aligned(x.v, 8) || !by8(x.k_page) || !by8(x.k_head) || !by8(x.v_page) ||
+              !by8(x.v_head) || k_page % 16 || k_head % 16 || k_token % 16 || v_page % 16 || v_head % 16 ||
+              v_token % 16))
     return NS_ERR_ARG;
   const Device *d = nullptr;
   if (ns_status s = current(&d)) return s;
@@ -188,7 +208,38 @@ ns_status ns_attend_paged(const void *d_q, int32_t dtype, int32_t n_seqs, int32_
   a.max_len = max_len == 0 || max_len > most ? (int32_t)most : max_len;
   a.table = d_table, a.lengths = d_lengths, a.seqs = d_seqs, a.mask = d_mask;
   a.scale = scale, a.out = d_out, a.lse = d_lse, a.ws = d_ws, a.err = d->flags;
-  return done(ns::launch_paged_attn(a, dtype, dim, d->sms, d->fit, static_cast<cudaStream_t>(stream)));
+  a.k_exp = x.k, a.v_exp = x.v, a.ke_page = x.k_page, a.ke_head = x.k_head, a.ve_page = x.v_page, a.ve_head = x.v_head;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return done(x.k ? ns::launch_paged_attn8(a, dtype, dim, d->sms, d->fit, st)
+                  : ns::launch_paged_attn(a, dtype, dim, d->sms, d->fit, st));
+}
+
+ns_status ns_attend_paged(const void *d_q, int32_t dtype, int32_t n_seqs, int32_t n, int32_t q_heads,
+                          int32_t kv_heads, int32_t dim, int64_t q_seq, int64_t q_token, int64_t q_head,
+                          const void *d_k, const void *d_v, int32_t n_pages, int32_t page_size, int64_t k_page,
+                          int64_t k_head, int64_t k_token, int64_t v_page, int64_t v_head, int64_t v_token,
+                          const int32_t *d_table, int32_t table_ld, int32_t max_seqs, const int32_t *d_lengths,
+                          const int32_t *d_seqs, const int64_t *d_mask, float scale, int32_t max_len, void *d_out,
+                          float *d_lse, void *d_ws, int64_t ws_bytes, ns_stream stream) {
+  return attend_paged(d_q, dtype, n_seqs, n, q_heads, kv_heads, dim, q_seq, q_token, q_head, d_k, d_v, n_pages,
+                      page_size, k_page, k_head, k_token, v_page, v_head, v_token, Exponents{}, d_table, table_ld,
+                      max_seqs, d_lengths, d_seqs, d_mask, scale, max_len, d_out, d_lse, d_ws, ws_bytes, stream);
+}
+
+ns_status ns_attend_paged_scaled(const void *d_q, int32_t dtype, int32_t n_seqs, int32_t n, int32_t q_heads,
+                                 int32_t kv_heads, int32_t dim, int64_t q_seq, int64_t q_token, int64_t q_head,
+                                 const void *d_k, const void *d_v, int32_t n_pages, int32_t page_size, int64_t k_page,
+                                 int64_t k_head, int64_t k_token, int64_t v_page, int64_t v_head, int64_t v_token,
+                                 const uint8_t *d_k_exp, const uint8_t *d_v_exp, int64_t ke_page, int64_t ke_head,
+                                 int64_t ve_page, int64_t ve_head, const int32_t *d_table, int32_t table_ld,
+                                 int32_t max_seqs, const int32_t *d_lengths, const int32_t *d_seqs,
+                                 const int64_t *d_mask, float scale, int32_t max_len, void *d_out, float *d_lse,
+                                 void *d_ws, int64_t ws_bytes, ns_stream stream) {
+  if (n_seqs > 0 && (!d_k_exp || !d_v_exp)) return NS_ERR_ARG;
+  return attend_paged(d_q, dtype, n_seqs, n, q_heads, kv_heads, dim, q_seq, q_token, q_head, d_k, d_v, n_pages,
+                      page_size, k_page, k_head, k_token, v_page, v_head, v_token,
+                      Exponents{d_k_exp, d_v_exp, ke_page, ke_head, ve_page, ve_head}, d_table, table_ld, max_seqs,
+                      d_lengths, d_seqs, d_mask, scale, max_len, d_out, d_lse, d_ws, ws_bytes, stream);
 }
 
 ns_status ns_pages_truncate(const ns_kv_pages *c, const int32_t *d_seqs, const int32_t *d_new_len, int32_t n,
@@ -213,16 +264,26 @@ int64_t ns_pages_workspace(const ns_kv_pages *c, int32_t n) {
   return cache_ok(c) && page_seqs(n) ? ns::pages_extend_ws(*c, n) : 0;
 }
 
-ns_status ns_pages_extend(const ns_kv_pages *c, const int32_t *d_seqs, const int32_t *d_n_new, int32_t n, void *d_ws,
-                          int64_t ws_bytes, ns_stream stream) {
-  if (!cache_ok(c) || !page_seqs(n) || (n > 0 && (!d_seqs || !d_n_new || !d_ws || !aligned(d_ws, 16))) ||
+static ns_status pages_extend(const ns_kv_pages *c, const ns_kv_scales *sc, const int32_t *d_seqs,
+                              const int32_t *d_n_new, int32_t n, void *d_ws, int64_t ws_bytes, ns_stream stream) {
+  if (!cache_ok(c) || !scales_ok(c, sc) || !page_seqs(n) || (n > 0 && (!d_seqs || !d_n_new || !d_ws || !aligned(d_ws, 16))) ||
       !words(d_seqs, d_n_new))
     return NS_ERR_ARG;
   if (n == 0) return NS_OK;
   if (ws_bytes < ns::pages_extend_ws(*c, n)) return NS_ERR_ARG;
   const Device *d = nullptr;
   if (ns_status s = current(&d)) return s;
-  return done(ns::launch_pages_extend(*c, d_seqs, d_n_new, n, d_ws, d->flags, static_cast<cudaStream_t>(stream)));
+  return done(ns::launch_pages_extend(*c, sc, d_seqs, d_n_new, n, d_ws, d->flags, static_cast<cudaStream_t>(stream)));
+}
+
+ns_status ns_pages_extend(const ns_kv_pages *c, const int32_t *d_seqs, const int32_t *d_n_new, int32_t n, void *d_ws,
+                          int64_t ws_bytes, ns_stream stream) {
+  return pages_extend(c, nullptr, d_seqs, d_n_new, n, d_ws, ws_bytes, stream);
+}
+
+ns_status ns_pages_extend_scaled(const ns_kv_pages *c, const ns_kv_scales *s, const int32_t *d_seqs,
+                                 const int32_t *d_n_new, int32_t n, void *d_ws, int64_t ws_bytes, ns_stream stream) {
+  return s ? pages_extend(c, s, d_seqs, d_n_new, n, d_ws, ws_bytes, stream) : NS_ERR_ARG;
 }
 
 ns_status ns_pages_write(const ns_kv_pages *c, int32_t layer, const int32_t *d_seqs, const int32_t *d_cu, int32_t n,
@@ -239,25 +300,80 @@ ns_status ns_pages_write(const ns_kv_pages *c, int32_t layer, const int32_t *d_s
                                      tokens, d->flags, static_cast<cudaStream_t>(stream)));
 }
 
-ns_status ns_pages_compact(const ns_kv_pages *c, const int32_t *d_seqs, const int32_t *d_base, const int32_t *d_keep,
-                           int32_t keep_ld, const int32_t *d_n_keep, int32_t n, ns_stream stream) {
-  if (!cache_ok(c) || !page_seqs(n) || keep_ld < 0 || (n > 0 && (!d_seqs || !d_base || !d_n_keep)) ||
+static ns_status pages_compact(const ns_kv_pages *c, const ns_kv_scales *sc, const int32_t *d_seqs,
+                               const int32_t *d_base, const int32_t *d_keep, int32_t keep_ld, const int32_t *d_n_keep,
+                               int32_t n, ns_stream stream) {
+  if (!cache_ok(c) || !scales_ok(c, sc) || !page_seqs(n) || keep_ld < 0 || (n > 0 && (!d_seqs || !d_base || !d_n_keep)) ||
       (n > 0 && keep_ld > 0 && !d_keep) || !words(d_seqs, d_base, d_keep, d_n_keep))
     return NS_ERR_ARG;
   if (n == 0) return NS_OK;
   const Device *d = nullptr;
   if (ns_status s = current(&d)) return s;
-  return done(ns::launch_pages_compact(*c, d_seqs, d_base, d_keep, keep_ld, d_n_keep, n, d->flags,
+  return done(ns::launch_pages_compact(*c, sc, d_seqs, d_base, d_keep, keep_ld, d_n_keep, n, d->flags,
                                        static_cast<cudaStream_t>(stream)));
+}
+
+ns_status ns_pages_compact(const ns_kv_pages *c, const int32_t *d_seqs, const int32_t *d_base, const int32_t *d_keep,
+                           int32_t keep_ld, const int32_t *d_n_keep, int32_t n, ns_stream stream) {
+  return pages_compact(c, nullptr, d_seqs, d_base, d_keep, keep_ld, d_n_keep, n, stream);
+}
+
+ns_status ns_pages_compact_scaled(const ns_kv_pages *c, const ns_kv_scales *s, const int32_t *d_seqs,
+                                  const int32_t *d_base, const int32_t *d_keep, int32_t keep_ld,
+                                  const int32_t *d_n_keep, int32_t n, ns_stream stream) {
+  return s ? pages_compact(c, s, d_seqs, d_base, d_keep, keep_ld, d_n_keep, n, stream) : NS_ERR_ARG;
+}
+
+static ns_status pages_copy(const ns_kv_pages *c, const ns_kv_scales *sc, const int32_t *d_src, const int32_t *d_dst,
+                            int32_t n, ns_stream stream) {
+  if (!cache_ok(c) || !scales_ok(c, sc) || n < 0 || (n > 0 && (!d_src || !d_dst)) || !words(d_src, d_dst)) return NS_ERR_ARG;
+  if (n == 0) return NS_OK;
+  const Device *d = nullptr;
+  if (ns_status s = current(&d)) return s;
+  return done(ns::launch_pages_copy(*c, sc, d_src, d_dst, n, d->flags, static_cast<cudaStream_t>(stream)));
 }
 
 ns_status ns_pages_copy(const ns_kv_pages *c, const int32_t *d_src, const int32_t *d_dst, int32_t n,
                         ns_stream stream) {
-  if (!cache_ok(c) || n < 0 || (n > 0 && (!d_src || !d_dst)) || !words(d_src, d_dst)) return NS_ERR_ARG;
-  if (n == 0) return NS_OK;
+  return pages_copy(c, nullptr, d_src, d_dst, n, stream);
+}
+
+ns_status ns_pages_copy_scaled(const ns_kv_pages *c, const ns_kv_scales *s, const int32_t *d_src,
+                               const int32_t *d_dst, int32_t n, ns_stream stream) {
+  return s ? pages_copy(c, s, d_src, d_dst, n, stream) : NS_ERR_ARG;
+}
+
+ns_status ns_pages_write_scaled(const ns_kv_pages *c, const ns_kv_scales *s, int32_t layer, const int32_t *d_seqs,
+                                const int32_t *d_cu, int32_t n, const void *d_k_new, const void *d_v_new,
+                                int32_t dtype, int64_t k_token, int64_t k_head, int64_t v_token, int64_t v_head,
+                                int32_t tokens, ns_stream stream) {
+  if (!cache_ok(c) || !s || !scales_ok(c, s) || layer < 0 || layer >= c->layers || !page_seqs(n) || tokens < 0 ||
+      (dtype != NS_DTYPE_BF16 && dtype != NS_DTYPE_F16))
+    return NS_ERR_ARG;
+  if (n == 0 || tokens == 0) return NS_OK;
+  if (!d_seqs || !d_cu || !d_k_new || !d_v_new || !aligned(d_k_new, 16) || !aligned(d_v_new, 16) || k_token % 16 ||
+      k_head % 16 || v_token % 16 || v_head % 16 || !words(d_seqs, d_cu))
+    return NS_ERR_ARG;
   const Device *d = nullptr;
-  if (ns_status s = current(&d)) return s;
-  return done(ns::launch_pages_copy(*c, d_src, d_dst, n, d->flags, static_cast<cudaStream_t>(stream)));
+  if (ns_status e = current(&d)) return e;
+  return done(ns::launch_pages_write_scaled(*c, *s, layer, d_seqs, d_cu, n, d_k_new, d_v_new, dtype, k_token, k_head,
+                                            v_token, v_head, tokens, d->flags, static_cast<cudaStream_t>(stream)));
+}
+
+ns_status ns_pages_read(const ns_kv_pages *c, const ns_kv_scales *s, int32_t layer, const int32_t *d_seqs,
+                        const int32_t *d_cu, int32_t n, void *d_k, void *d_v, int32_t dtype, int64_t k_token,
+                        int64_t k_head, int64_t v_token, int64_t v_head, int32_t tokens, ns_stream stream) {
+  if (!cache_ok(c) || !scales_ok(c, s) || layer < 0 || layer >= c->layers || !page_seqs(n) || tokens < 0 ||
+      (s && dtype != NS_DTYPE_BF16 && dtype != NS_DTYPE_F16))
+    return NS_ERR_ARG;
+  if (n == 0 || tokens == 0) return NS_OK;
+  if (!d_seqs || !d_cu || !d_k || !d_v || !aligned(d_k, 16) || !aligned(d_v, 16) || k_token % 16 || k_head % 16 ||
+      v_token % 16 || v_head % 16 || !words(d_seqs, d_cu))
+    return NS_ERR_ARG;
+  const Device *d = nullptr;
+  if (ns_status e = current(&d)) return e;
+  return done(ns::launch_pages_read(*c, s, layer, d_seqs, d_cu, n, d_k, d_v, dtype, k_token, k_head, v_token, v_head,
+                                    tokens, d->flags, static_cast<cudaStream_t>(stream)));
 }
 
 ns_status ns_token_logprobs(const void *d_logits, int32_t dtype, int32_t rows, int32_t V, int64_t ld,

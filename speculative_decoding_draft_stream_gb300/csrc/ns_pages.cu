@@ -15,6 +15,12 @@
 // for four calls; 64 children with their 64 MB of copied last pages 34 us;
 // 8 sequences of 4001 new rows of which every second stays in 12 layers 166 us
 // (393 MB read and 332 MB written by the compaction: 126 us of it).
+//
+// A cache of 8 bits (ns_kv_scales) has a power of two for each row: the movers
+// take its byte along, and write and read convert.  Both are bound by their
+// loads' latency and HBM, as the plain ones are; a row's largest element costs
+// four shuffles of packed halves, its codes four conversions a lane.
+#include "ns_attn_tile.cuh"
 #include "ns_internal.cuh"
 #include "ns_ops.cuh"
 
@@ -136,6 +142,11 @@ __global__ void __launch_bounds__(kSeqThreads) fork_kernel(ns_kv_pages c, const 
   }
   __syncthreads();  // every thread has seen the destination empty
   if (threadIdx.x == 0) c.lengths[b] = len;
+}
+
+// The exponents of a layer's head (page 0).
+__device__ __forceinline__ uint8_t *scales_of(const ns_kv_scales &s, int kv, int layer, int head) {
+  return kv ? s.v + layer * s.v_layer + head * s.v_head : s.k + layer * s.k_layer + head * s.k_head;
 }
 
 // Workspace of an extension, int32 words: [0] copies, [1] unused, then per
@@ -294,9 +305,10 @@ __global__ void __launch_bounds__(kExtendThreads) extend_kernel(ns_kv_pages c, c
 // Copies whole pages.  A warp takes one (page pair, layer, head) of k or v:
 // page_size rows of row_bytes, 16 bytes a lane.  The pairs' number is on the
 // device when n_ptr is given (at most n).
-__global__ void __launch_bounds__(kMoveThreads) copy_pages_kernel(ns_kv_pages c, const int32_t *src,
-                                                                  const int32_t *dst, const int32_t *n_ptr, int n,
-                                                                  uint32_t *err) {
+template <bool kScaled>
+__global__ void __launch_bounds__(kMoveThreads)
+    copy_pages_kernel(ns_kv_pages c, const ns_kv_scales sc, const int32_t *src, const int32_t *dst,
+                      const int32_t *n_ptr, int n, uint32_t *err) {
   wait_for_previous();
   const int lane = threadIdx.x & 31;
   const int pairs = n_ptr ? min(*n_ptr, n) : n;
@@ -330,26 +342,30 @@ __global__ void __launch_bounds__(kMoveThreads) copy_pages_kernel(ns_kv_pages c,
         if (x < units) *reinterpret_cast<uint4 *>(to + x / cols * st + x % cols * 16) = val[q];
       }
     }
+    if (kScaled) {
+      uint8_t *exps = scales_of(sc, kv, layer, head);
+      const int64_t page = kv ? sc.v_page : sc.k_page;
+      const uint2 *ef = reinterpret_cast<const uint2 *>(exps + a * page);
+      for (int x = lane; x < c.page_size / 8; x += kWarp) reinterpret_cast<uint2 *>(exps + b * page)[x] = ef[x];
+    }
   }
 }
 
-// New rows of one layer: a warp per token, its 16-byte pieces of every head
-// of k and v over the lanes.  Only the first of a repeated sequence is
+// Where token t of a call's new rows lies: a whole CTA asks, a warp for each
+// token.  False where the warp has none, or (with a flag) an invalid one; rows
+// to be written (kWrite) may not be another sequence's too.  Only the first of a repeated sequence is
 // written: up to kWarpLooks sequences each warp looks through the entries
 // before its own; of more, the CTA looks once for all of its warps.  Measured,
 // by warps and by the CTA: 8 sequences of 4001 tokens 35.6, 36.9 us; 64 of one
 // token 3.6, 3.8; 256 of one 4.1, 3.9; 8192 of one 23.7, 15.5.
 constexpr int kWarpLooks = 128;
-__global__ void __launch_bounds__(kMoveThreads) write_kernel(ns_kv_pages c, int layer, const int32_t *seqs,
-                                                             const int32_t *cu, int n, const void *k_rows,
-                                                             const void *v_rows, int64_t k_token, int64_t k_head,
-                                                             int64_t v_token, int64_t v_head, int tokens,
-                                                             uint32_t *err) {
+template <bool kWrite>
+__device__ __forceinline__ bool find_row(const ns_kv_pages &c, const int32_t *seqs, const int32_t *cu, int n,
+                                         int tokens, uint32_t *err, int &t, int &page, int &r) {
   __shared__ int s_seq[kMoveWarps], s_at[kMoveWarps];  // each warp's sequence, and its place in the call
   __shared__ uint32_t s_again;                         // warps whose sequence stands before that place too
-  wait_for_previous();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int t = blockIdx.x * kMoveWarps + warp;
+  t = blockIdx.x * kMoveWarps + warp;
   int lo = 0, t0 = 0, t1 = 0, s = -1, len = 0;
   if (t < tokens) {  // the last i with cu[i] <= t, a 32nd of what is left at a time
     for (int size = n; size > 1;) {
@@ -363,7 +379,8 @@ __global__ void __launch_bounds__(kMoveThreads) write_kernel(ns_kv_pages c, int 
     if (seq_ok(c, s)) len = c.lengths[s];
   }
   uint32_t again = 0;  // (found while the length is on its way)
-  if (n <= kWarpLooks) {
+  if (!kWrite) {
+  } else if (n <= kWarpLooks) {
 #pragma unroll
     for (int j = lane; j < kWarpLooks; j += kWarp)
       if (j < lo && seqs[j] == s) again = 1;
@@ -397,21 +414,35 @@ __global__ void __launch_bounds__(kMoveThreads) write_kernel(ns_kv_pages c, int 
     __syncthreads();
     again = s_again >> warp & 1;
   }
-  if (t < t0 || t >= t1) return;  // a token of no sequence
+  if (t < t0 || t >= t1) return false;  // a token of no sequence
   const long long pos = (long long)len - (t1 - t);
   if (!seq_ok(c, s) || again || !len_ok(c, len) || pos < 0) {
     if (lane == 0) set_flag(err, NS_FLAG_BAD_SEQ);
-    return;
+    return false;
   }
-  const int page = c.table[(size_t)s * c.table_ld + (int)(pos / c.page_size)], r = (int)(pos % c.page_size);
+  page = c.table[(size_t)s * c.table_ld + (int)(pos / c.page_size)], r = (int)(pos % c.page_size);
   if (page < 0 || page >= c.pages) {
     if (lane == 0) set_flag(err, NS_FLAG_BAD_ID);
-    return;
+    return false;
   }
-  if (c.refs[page] > 1) {
+  if (kWrite && c.refs[page] > 1) {
     if (lane == 0) set_flag(err, NS_FLAG_SHARED_PAGE);
-    return;
+    return false;
   }
+  return true;
+}
+
+// New rows of one layer: a warp per token, its 16-byte pieces of every head of
+// k and v over the lanes.
+__global__ void __launch_bounds__(kMoveThreads) write_kernel(ns_kv_pages c, int layer, const int32_t *seqs,
+                                                             const int32_t *cu, int n, const void *k_rows,
+                                                             const void *v_rows, int64_t k_token, int64_t k_head,
+                                                             int64_t v_token, int64_t v_head, int tokens,
+                                                             uint32_t *err) {
+  wait_for_previous();
+  int t, page, r;
+  if (!find_row<true>(c, seqs, cu, n, tokens, err, t, page, r)) return;
+  const int lane = threadIdx.x & 31;
   const int cols = c.row_bytes / 16, units = c.heads * cols;
   char *kd = static_cast<char *>(c.k) + layer * c.k_layer + page * c.k_page + r * c.k_token;
   char *vd = static_cast<char *>(c.v) + layer * c.v_layer + page * c.v_page + r * c.v_token;
@@ -438,6 +469,142 @@ __global__ void __launch_bounds__(kMoveThreads) write_kernel(ns_kv_pages c, int 
   }
 }
 
+// The last rows of sequences, out of the cache: the same, the other way round.
+__global__ void __launch_bounds__(kMoveThreads) read_kernel(ns_kv_pages c, int layer, const int32_t *seqs,
+                                                            const int32_t *cu, int n, void *k_rows, void *v_rows,
+                                                            int64_t k_token, int64_t k_head, int64_t v_token,
+                                                            int64_t v_head, int tokens, uint32_t *err) {
+  wait_for_previous();
+  int t, page, r;
+  if (!find_row<false>(c, seqs, cu, n, tokens, err, t, page, r)) return;
+  const int lane = threadIdx.x & 31, cols = c.row_bytes / 16, units = c.heads * cols;
+  const char *ks = static_cast<const char *>(c.k) + layer * c.k_layer + page * c.k_page + r * c.k_token;
+  const char *vs = static_cast<const char *>(c.v) + layer * c.v_layer + page * c.v_page + r * c.v_token;
+  char *kd = static_cast<char *>(k_rows) + t * k_token, *vd = static_cast<char *>(v_rows) + t * v_token;
+  for (int x0 = lane; x0 < units; x0 += kWarp * 4) {
+    uint4 a[4], b[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int x = x0 + q * kWarp;
+      if (x < units) {
+        a[q] = *reinterpret_cast<const uint4 *>(ks + x / cols * c.k_head + x % cols * 16);
+        b[q] = *reinterpret_cast<const uint4 *>(vs + x / cols * c.v_head + x % cols * 16);
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int x = x0 + q * kWarp;
+      if (x < units) {
+        *reinterpret_cast<uint4 *>(kd + x / cols * k_head + x % cols * 16) = a[q];
+        *reinterpret_cast<uint4 *>(vd + x / cols * v_head + x % cols * 16) = b[q];
+      }
+    }
+  }
+}
+
+// A lane's eight elements of a row of D, which D / 8 lanes have, as codes: the
+// row's byte is the smallest exponent e (biased, within +-40) with max |x| <=
+// 448 2^e, and 255 where an element is not finite; codes are x 2^-e in e4m3, to
+// nearest even.  (x 2^-e is exact: fp32 holds it.)
+template <typename T, int D>
+__device__ __forceinline__ uint2 to_codes(const uint4 &x, uint32_t &byte) {
+  const uint32_t *w = reinterpret_cast<const uint32_t *>(&x);
+  uint32_t most = __vmaxu2(__vmaxu2(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu),
+                           __vmaxu2(w[2] & 0x7fff7fffu, w[3] & 0x7fff7fffu));
+#pragma unroll
+  for (int off = D / 16; off > 0; off >>= 1) most = __vmaxu2(most, __shfl_xor_sync(0xffffffffu, most, off));
+  most = max(most & 0xffffu, most >> 16);
+  const bool fine = most < attn::Type<T>::kInf;
+  const uint32_t top = __float_as_uint(attn::Type<T>::unpack(most).x);
+  const int e = min(max((int)(top >> 23) - 127 - 8 + ((top & 0x7fffffu) > 0x600000u ? 1 : 0), -40), 40);
+  byte = fine ? (uint32_t)(e + 127) : 255u;
+  const float f = __uint_as_float((uint32_t)(127 - e) << 23);
+  uint32_t c[2] = {0, 0};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 v = attn::Type<T>::unpack(w[i]);
+    c[i >> 1] |= (uint32_t)attn::to_e4m3(v.x * f, v.y * f) << 16 * (i & 1);
+  }
+  return fine ? make_uint2(c[0], c[1]) : make_uint2(0, 0);
+}
+template <typename T>
+__device__ __forceinline__ uint4 from_codes(const uint2 &c, uint32_t byte) {
+  const float f = attn::scale_of(byte);
+  uint4 x;
+  uint32_t *w = reinterpret_cast<uint32_t *>(&x);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 v = attn::Type<__half>::unpack(attn::from_e4m3((i & 2 ? c.y : c.x) >> 16 * (i & 1)));
+    w[i] = attn::Type<T>::pack(v.x * f, v.y * f);
+  }
+  return x;
+}
+
+// write and read of a cache of 8 bits: a warp per token, D / 8 lanes a row.
+constexpr int kScaledUnroll = 4;
+template <typename T, int D, bool kWrite>
+__global__ void __launch_bounds__(kMoveThreads)
+    scaled_kernel(ns_kv_pages c, const ns_kv_scales sc, int layer, const int32_t *seqs, const int32_t *cu, int n,
+                  void *k_rows, void *v_rows, int64_t k_token, int64_t k_head, int64_t v_token, int64_t v_head,
+                  int tokens, uint32_t *err) {
+  constexpr int kPer = kWarp * 8 / D, U = kScaledUnroll;  // heads at once
+  wait_for_previous();
+  int t, page, r;
+  if (!find_row<kWrite>(c, seqs, cu, n, tokens, err, t, page, r)) return;
+  const int lane = threadIdx.x & 31, sub = lane / (D / 8), col = lane % (D / 8);
+  char *kc = static_cast<char *>(c.k) + layer * c.k_layer + page * c.k_page + r * c.k_token + col * 8;
+  char *vc = static_cast<char *>(c.v) + layer * c.v_layer + page * c.v_page + r * c.v_token + col * 8;
+  char *kr = static_cast<char *>(k_rows) + t * k_token + col * 16, *vr = static_cast<char *>(v_rows) + t * v_token + col * 16;
+  uint8_t *ke = sc.k + layer * sc.k_layer + page * sc.k_page + r, *ve = sc.v + layer * sc.v_layer + page * sc.v_page + r;
+  for (int h0 = 0; h0 < c.heads; h0 += kPer * U) {
+    if constexpr (kWrite) {
+      uint4 x[U][2];
+#pragma unroll
+      for (int q = 0; q < U; ++q) {
+        const int h = h0 + q * kPer + sub;
+        x[q][0] = x[q][1] = make_uint4(0, 0, 0, 0);
+        if (h < c.heads) {
+          x[q][0] = __ldcs(reinterpret_cast<const uint4 *>(kr + h * k_head));
+          x[q][1] = __ldcs(reinterpret_cast<const uint4 *>(vr + h * v_head));
+        }
+      }
+#pragma unroll
+      for (int q = 0; q < U; ++q) {
+        const int h = h0 + q * kPer + sub;
+        if (h0 + q * kPer >= c.heads) break;
+        uint32_t bk, bv;
+        const uint2 a = to_codes<T, D>(x[q][0], bk), b = to_codes<T, D>(x[q][1], bv);
+        if (h < c.heads) {
+          *reinterpret_cast<uint2 *>(kc + h * c.k_head) = a;
+          *reinterpret_cast<uint2 *>(vc + h * c.v_head) = b;
+          if (col == 0) ke[h * sc.k_head] = (uint8_t)bk;
+          if (col == 1) ve[h * sc.v_head] = (uint8_t)bv;
+        }
+      }
+    } else {
+      uint2 x[U][2];
+      uint32_t e[U][2];
+#pragma unroll
+      for (int q = 0; q < U; ++q) {
+        const int h = h0 + q * kPer + sub;
+        if (h < c.heads) {
+          x[q][0] = *reinterpret_cast<const uint2 *>(kc + h * c.k_head);
+          x[q][1] = *reinterpret_cast<const uint2 *>(vc + h * c.v_head);
+          e[q][0] = ke[h * sc.k_head], e[q][1] = ve[h * sc.v_head];
+        }
+      }
+#pragma unroll
+      for (int q = 0; q < U; ++q) {
+        const int h = h0 + q * kPer + sub;
+        if (h < c.heads) {
+          *reinterpret_cast<uint4 *>(kr + h * k_head) = from_codes<T>(x[q][0], e[q][0]);
+          *reinterpret_cast<uint4 *>(vr + h * v_head) = from_codes<T>(x[q][1], e[q][1]);
+        }
+      }
+    }
+  }
+}
+
 // Kept rows move down.  A CTA takes one sequence, k or v, and kMoverWarps of
 // its (layer, head, part of the row), a warp each.  It walks the
 // kept rows in order, kMoveRows at a time: the threads find each row's two
@@ -452,10 +619,12 @@ __global__ void __launch_bounds__(kMoveThreads) write_kernel(ns_kv_pages c, int 
 constexpr int kMoverWarps = 4;
 constexpr int kMoveRows = 128;
 constexpr int kMoveBatch = 16;
+template <bool kScaled>
 __global__ void __launch_bounds__(kMoverWarps * 32, 4)
-    compact_kernel(ns_kv_pages c, const int32_t *seqs, const int32_t *base, const int32_t *keep, int keep_ld,
+    compact_kernel(ns_kv_pages c, const ns_kv_scales sc, const int32_t *seqs, const int32_t *base, const int32_t *keep, int keep_ld,
                    const int32_t *n_keep, int seg_bytes, uint32_t *err) {
   __shared__ long long s_from[2][kMoveRows], s_to[2][kMoveRows];  // -1: stays
+  __shared__ long long s_exp[kScaled ? 2 : 1][2][kScaled ? kMoveRows : 1];  // the same rows' bytes: from, to
   wait_for_previous();
   const int tid = threadIdx.x, lane = tid & 31, i = blockIdx.z, kv = blockIdx.y;
   const int s = seqs[i], m = n_keep[i], b0 = base[i];
@@ -470,7 +639,7 @@ __global__ void __launch_bounds__(kMoverWarps * 32, 4)
   const int64_t sp = kv ? c.v_page : c.k_page, st = kv ? c.v_token : c.k_token;
   auto find = [&](int t0) {  // the places of rows t0 .. t0 + kMoveRows - 1
     const int t = t0 + tid, slot = (t0 / kMoveRows) & 1;
-    long long src = -1, dst = -1;
+    long long src = -1, dst = -1, e_src = 0, e_dst = 0;
     if (t < m) {
       const int from = kp[t];
       if (from < t || (t > 0 && from <= kp[t - 1]) || (long long)b0 + from >= len) {
@@ -485,11 +654,16 @@ __global__ void __launch_bounds__(kMoverWarps * 32, 4)
         } else {
           src = pa * sp + p % c.page_size * st;
           dst = pb * sp + d % c.page_size * st;
+          if (kScaled) {
+            const int64_t page = kv ? sc.v_page : sc.k_page;
+            e_src = pa * page + p % c.page_size, e_dst = pb * page + d % c.page_size;
+          }
         }
       }
     }
     s_from[slot][tid] = src;
     s_to[slot][tid] = dst;
+    if (kScaled) s_exp[slot][0][tid] = e_src, s_exp[slot][1][tid] = e_dst;
   };
   static_assert(kMoveRows == kMoverWarps * 32, "a thread finds one row's places");
   const int segs = (c.row_bytes + seg_bytes - 1) / seg_bytes;
@@ -507,6 +681,21 @@ __global__ void __launch_bounds__(kMoverWarps * 32, 4)
     if (t0 + kMoveRows < m) find(t0 + kMoveRows);
     if (!mine) continue;
     const int slot = (t0 / kMoveRows) & 1, rows = min(kMoveRows, m - t0);
+    if (kScaled && seg == 0) {  // (the loads of all these rows before their stores, as below)
+      uint8_t *exps = scales_of(sc, kv, layer, head), val[kMoveRows / kWarp];
+#pragma unroll
+      for (int q = 0; q < kMoveRows / kWarp; ++q) {
+        const int t = q * kWarp + lane;
+        if (t < rows && s_from[slot][t] >= 0) val[q] = exps[s_exp[slot][0][t]];
+      }
+      __syncwarp();
+#pragma unroll
+      for (int q = 0; q < kMoveRows / kWarp; ++q) {
+        const int t = q * kWarp + lane;
+        if (t < rows && s_from[slot][t] >= 0) exps[s_exp[slot][1][t]] = val[q];
+      }
+      __syncwarp();
+    }
     for (int q0 = 0; q0 < rows; q0 += per * kMoveBatch) {
       uint4 val[kMoveBatch];
 #pragma unroll
@@ -545,13 +734,14 @@ cudaError_t launch_pages_fork(const ns_kv_pages &c, const int32_t *src, const in
 
 int64_t pages_extend_ws(const ns_kv_pages &c, int n) { return 4 * (4 + 6 * (int64_t)n + c.pages); }
 
-cudaError_t launch_pages_extend(const ns_kv_pages &c, const int32_t *seqs, const int32_t *n_new, int n, void *ws,
-                                uint32_t *err, cudaStream_t st) {
+cudaError_t launch_pages_extend(const ns_kv_pages &c, const ns_kv_scales *sc, const int32_t *seqs,
+                                const int32_t *n_new, int n, void *ws, uint32_t *err, cudaStream_t st) {
   cudaError_t e = launch(extend_kernel, dim3(1), kExtendThreads, extend_smem(n), st, c, seqs, n_new, n, ws, err);
   if (e != cudaSuccess) return e;
   const ExtendWs w(ws, n);
   const unsigned grid = grid_for((long long)n * c.layers * c.heads * 2, 2432);
-  return launch(copy_pages_kernel, dim3(grid), kMoveThreads, 0, st, c, w.src, w.dst, w.n_copies, n, err);
+  return launch(sc ? copy_pages_kernel<true> : copy_pages_kernel<false>, dim3(grid), kMoveThreads, 0, st, c,
+                sc ? *sc : ns_kv_scales{}, w.src, w.dst, w.n_copies, n, err);
 }
 
 cudaError_t launch_pages_write(const ns_kv_pages &c, int layer, const int32_t *seqs, const int32_t *cu, int n,
@@ -561,8 +751,40 @@ cudaError_t launch_pages_write(const ns_kv_pages &c, int layer, const int32_t *s
                 k_new, v_new, k_token, k_head, v_token, v_head, tokens, err);
 }
 
-cudaError_t launch_pages_compact(const ns_kv_pages &c, const int32_t *seqs, const int32_t *base, const int32_t *keep,
-                                 int keep_ld, const int32_t *n_keep, int n, uint32_t *err, cudaStream_t st) {
+template <typename T, bool kWrite>
+cudaError_t launch_scaled(const ns_kv_pages &c, const ns_kv_scales &sc, int layer, const int32_t *seqs,
+                          const int32_t *cu, int n, void *k, void *v, int64_t k_token, int64_t k_head,
+                          int64_t v_token, int64_t v_head, int tokens, uint32_t *err, cudaStream_t st) {
+  return launch(c.row_bytes == 128 ? scaled_kernel<T, 128, kWrite> : scaled_kernel<T, 64, kWrite>,
+                dim3((tokens + kMoveWarps - 1) / kMoveWarps), kMoveThreads, 0, st, c, sc, layer, seqs, cu, n, k, v,
+                k_token, k_head, v_token, v_head, tokens, err);
+}
+
+cudaError_t launch_pages_write_scaled(const ns_kv_pages &c, const ns_kv_scales &sc, int layer, const int32_t *seqs,
+                                      const int32_t *cu, int n, const void *k_new, const void *v_new, int dtype,
+                                      int64_t k_token, int64_t k_head, int64_t v_token, int64_t v_head, int tokens,
+                                      uint32_t *err, cudaStream_t st) {
+  void *k = const_cast<void *>(k_new), *v = const_cast<void *>(v_new);
+  return dtype == NS_DTYPE_BF16 ? launch_scaled<__nv_bfloat16, true>(c, sc, layer, seqs, cu, n, k, v, k_token, k_head,
+                                                                     v_token, v_head, tokens, err, st)
+                                : launch_scaled<__half, true>(c, sc, layer, seqs, cu, n, k, v, k_token, k_head,
+                                                              v_token, v_head, tokens, err, st);
+}
+
+cudaError_t launch_pages_read(const ns_kv_pages &c, const ns_kv_scales *sc, int layer, const int32_t *seqs,
+                              const int32_t *cu, int n, void *k, void *v, int dtype, int64_t k_token, int64_t k_head,
+                              int64_t v_token, int64_t v_head, int tokens, uint32_t *err, cudaStream_t st) {
+  if (!sc)
+    return launch(read_kernel, dim3((tokens + kMoveWarps - 1) / kMoveWarps), kMoveThreads, 0, st, c, layer, seqs, cu,
+                  n, k, v, k_token, k_head, v_token, v_head, tokens, err);
+  return dtype == NS_DTYPE_BF16 ? launch_scaled<__nv_bfloat16, false>(c, *sc, layer, seqs, cu, n, k, v, k_token,
+                                                                      k_head, v_token, v_head, tokens, err, st)
+                                : launch_scaled<__half, false>(c, *sc, layer, seqs, cu, n, k, v, k_token, k_head,
+                                                               v_token, v_head, tokens, err, st);
+}
+
+cudaError_t launch_pages_compact(const ns_kv_pages &c, const ns_kv_scales *sc, const int32_t *seqs,
+                                 const int32_t *base, const int32_t *keep, int keep_ld, const int32_t *n_keep, int n, uint32_t *err, cudaStream_t st) {
   // A warp takes up to 512 bytes of a row, less where the CTAs are too few to keep HBM busy: 16001 rows of 12 x 4
   // x 256 bytes of k and v move in 163 us by whole rows (192 CTAs), in about 118 us by halves.
   constexpr int kEnough = 304;
@@ -575,17 +797,19 @@ cudaError_t launch_pages_compact(const ns_kv_pages &c, const int32_t *seqs, cons
   if (units > 0x7fffffffLL - kMoverWarps) return cudaErrorInvalidValue;
   if (keep_ld > 0) {
     const dim3 grid((unsigned)((units + kMoverWarps - 1) / kMoverWarps), 2, (unsigned)n);
-    cudaError_t e = launch(compact_kernel, grid, kMoverWarps * 32, 0, st, c, seqs, base, keep, keep_ld, n_keep,
+    cudaError_t e = launch(sc ? compact_kernel<true> : compact_kernel<false>, grid, kMoverWarps * 32, 0, st, c,
+                           sc ? *sc : ns_kv_scales{}, seqs, base, keep, keep_ld, n_keep,
                            seg_bytes, err);
     if (e != cudaSuccess) return e;
   }
   return launch(truncate_kernel, dim3(n), kSeqThreads, 0, st, c, seqs, n_keep, base, keep_ld, err);
 }
 
-cudaError_t launch_pages_copy(const ns_kv_pages &c, const int32_t *src, const int32_t *dst, int n, uint32_t *err,
-                              cudaStream_t st) {
+cudaError_t launch_pages_copy(const ns_kv_pages &c, const ns_kv_scales *sc, const int32_t *src, const int32_t *dst,
+                              int n, uint32_t *err, cudaStream_t st) {
   const dim3 grid(grid_for((long long)n * c.layers * c.heads * 2, 2432));
-  return launch(copy_pages_kernel, grid, kMoveThreads, 0, st, c, src, dst, nullptr, n, err);
+  return launch(sc ? copy_pages_kernel<true> : copy_pages_kernel<false>, grid, kMoveThreads, 0, st, c,
+                sc ? *sc : ns_kv_scales{}, src, dst, nullptr, n, err);
 }
 
 }  // namespace ns

@@ -5,7 +5,8 @@
 * ``attend_prompt``   causal attention over whole packed prompts;
 * ``attend_paged``    attention of a sequence's new tokens (one, or the nodes
                       of a draft tree) over a paged key-value cache;
-* ``KvPages``         the paged cache: truncate, fork, extend, write, compact, copy;
+* ``KvPages``         the paged cache, of 16 or 8 bits: truncate, fork, extend,
+                      write, read, compact, copy;
 * ``token_logprobs``  log probabilities of given tokens, entropy, alternatives;
 * ``ops_error``       the sticky device flags of these calls.
 
@@ -113,6 +114,7 @@ def attend_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, 
                  lengths: torch.Tensor, seqs: torch.Tensor, *, mask: Optional[torch.Tensor] = None,
                  scale: Optional[float] = None, max_len: int = 0, out: Optional[torch.Tensor] = None,
                  lse: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                 k_exp: Optional[torch.Tensor] = None, v_exp: Optional[torch.Tensor] = None,
                  stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
     """Attention of n new tokens per sequence over one layer of a paged cache: q [B, n, Hq, D]; k_pages and
     v_pages [pages, Hkv, page_size, D] (strides free); table int32 [max_seqs, pages per sequence], lengths int32
@@ -120,13 +122,15 @@ def attend_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, 
     set where new token i sees new token j (None: j <= i).  max_len, a bound on the lengths, takes part in how
     the keys are split: results of another bound may differ by their rounding.  With more than 16 rows (n * Hq / Hkv)
     a q off a 16-byte boundary, or with strides other than positive multiples of 8 elements, takes about three times
-    as long.  Returns (out [B, n, Hq, D], lse fp32 [B, n, Hq])."""
+    as long.  With k_exp and v_exp, uint8 [pages, Hkv, page_size], the pages are a cache of 8 bits (KvPages): codes in
+    e4m3 and the exponent of each row.  Returns (out [B, n, Hq, D], lse fp32 [B, n, Hq])."""
     s = None if stream is None else _other(stream)
     if s is not None:
         return _on(s, lambda: attend_paged(q, k_pages, v_pages, table, lengths, seqs, mask=mask, scale=scale,
-                                           max_len=max_len, out=out, lse=lse, workspace=workspace))
+                                           max_len=max_len, out=out, lse=lse, workspace=workspace, k_exp=k_exp,
+                                           v_exp=v_exp))
     return _native().attend_paged(q, k_pages, v_pages, table, lengths, seqs, mask, scale, max_len, out, lse,
-                                  workspace)
+                                  workspace, k_exp, v_exp)
 
 
 class KvPages:
@@ -135,29 +139,43 @@ class KvPages:
     pages per sequence] (-1 past a sequence's last page), lengths int32 [max_seqs], refs int32 [pages] (how many
     sequences hold a page).  Their contents may be changed, but not which tensors they are: the cache works on the
     memory that it was made over.  Its device must be the current one in every call.  ``KvPages.new`` makes an empty
-    one."""
+    one.
+
+    A cache of 8 bits: k and v of torch.float8_e4m3fn (64 or 128 columns, pages of a multiple of 8) with k_exp and
+    v_exp, uint8 [layers, pages, heads, page_size].  A row stands for its codes times 2^(exponent - 127), and for NaN
+    where the byte is 255.  ``write`` rounds bf16 or fp16 rows to it, by the smallest power of two by which the row
+    fits (within 2^-40 and 2^40; a row that holds an infinity or NaN gets 255), ``read`` gives rows back, ``attend``
+    works on them as they are, and every call that moves rows moves their exponents too."""
 
     def __init__(self, k: torch.Tensor, v: torch.Tensor, table: torch.Tensor, lengths: torch.Tensor,
-                 refs: torch.Tensor):
+                 refs: torch.Tensor, k_exp: Optional[torch.Tensor] = None, v_exp: Optional[torch.Tensor] = None):
         self._b = _native()
-        self._c = self._b.cache(k, v, table, lengths, refs)
-        self._over = k, v, table, lengths, refs  # kept alive: the native record has their addresses
+        self._c = self._b.cache(k, v, table, lengths, refs, k_exp, v_exp)
+        # kept alive: the native record has their addresses
+        self._over = k, v, table, lengths, refs, k_exp, v_exp
 
     k = property(lambda self: self._over[0])
     v = property(lambda self: self._over[1])
     table = property(lambda self: self._over[2])
     lengths = property(lambda self: self._over[3])
     refs = property(lambda self: self._over[4])
+    k_exp = property(lambda self: self._over[5])
+    v_exp = property(lambda self: self._over[6])
 
     @classmethod
     def new(cls, layers: int, pages: int, kv_heads: int, page_size: int, dim: int, max_seqs: int, max_pages: int,
-            dtype=torch.bfloat16, device=None) -> "KvPages":
-        """An empty cache of `pages` pages for up to max_seqs sequences of up to max_pages pages each."""
+            dtype=torch.bfloat16, device=None, scaled: bool = False) -> "KvPages":
+        """An empty cache of `pages` pages for up to max_seqs sequences of up to max_pages pages each;
+        scaled: one of 8 bits, with exponents, whatever dtype says."""
         device = torch.device("cuda", torch.cuda.current_device()) if device is None else device
-        k = torch.empty((layers, pages, kv_heads, page_size, dim), dtype=dtype, device=device)
+        k = torch.empty((layers, pages, kv_heads, page_size, dim), dtype=torch.float8_e4m3fn if scaled else dtype,
+                        device=device)
         i32 = {"dtype": torch.int32, "device": device}
+        exps = [None, None]
+        if scaled:
+            exps = [torch.zeros(k.shape[:4], dtype=torch.uint8, device=device) for _ in range(2)]
         return cls(k, torch.empty_like(k), torch.full((max_seqs, max_pages), -1, **i32), torch.zeros(max_seqs, **i32),
-                   torch.zeros(pages, **i32))
+                   torch.zeros(pages, **i32), *exps)
 
     @staticmethod
     def _handle(stream):
@@ -183,8 +201,23 @@ class KvPages:
     def write(self, layer: int, seqs: torch.Tensor, cu: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor,
               stream=None) -> None:
         """Writes k_new and v_new [tokens, heads, dim] as the last positions of the sequences in one layer; tokens
-        cu[i] .. cu[i + 1] - 1 are sequence seqs[i]'s (cu int32 [n + 1])."""
+        cu[i] .. cu[i + 1] - 1 are sequence seqs[i]'s (cu int32 [n + 1]).  Into a cache of 8 bits: bf16 or fp16."""
         self._b.write(self._c, layer, seqs, cu, k_new, v_new, self._handle(stream))
+
+    def read(self, layer: int, seqs: torch.Tensor, cu: torch.Tensor, tokens: int, *, dtype=None,
+             k_out: Optional[torch.Tensor] = None, v_out: Optional[torch.Tensor] = None,
+             stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+        """The other way round: the last cu[i + 1] - cu[i] positions of each sequence seqs[i] in one layer, as rows
+        cu[i] .. cu[i + 1] - 1 of (k, v) [tokens, heads, dim]; of a cache of 8 bits what the codes stand for, in dtype
+        (bf16, which holds every value, or fp16), otherwise the elements as they are.  Rows of no sequence, or of an
+        invalid one, are not written."""
+        s = None if stream is None else _other(stream)
+        if s is not None:
+            return _on(s, lambda: self.read(layer, seqs, cu, tokens, dtype=dtype, k_out=k_out, v_out=v_out))
+        scaled = self.k_exp is not None
+        if dtype not in ((None, torch.bfloat16, torch.float16) if scaled else (None, self.k.dtype)):
+            raise ValueError(f"a cache of {self.k.dtype} does not give rows of {dtype}")
+        return self._b.read(self._c, layer, seqs, cu, tokens, scaled and dtype == torch.float16, k_out, v_out)
 
     def compact(self, seqs: torch.Tensor, base: torch.Tensor, keep: torch.Tensor, n_keep: torch.Tensor,
                 stream=None) -> None:
@@ -198,6 +231,8 @@ class KvPages:
 
     def attend(self, layer: int, q: torch.Tensor, seqs: torch.Tensor, **kw) -> Tuple[torch.Tensor, torch.Tensor]:
         """attend_paged over one layer of this cache."""
+        if self.k_exp is not None:
+            kw = dict(kw, k_exp=self.k_exp[layer], v_exp=self.v_exp[layer])
         return attend_paged(q, self.k[layer], self.v[layer], self.table, self.lengths, seqs, **kw)
 
 
