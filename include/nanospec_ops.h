@@ -37,6 +37,7 @@ extern "C" {
 
 #define NS_MAX_NEW 64          /* new tokens of a sequence in ns_attend_paged (NS_MAX_ROWS)  */
 #define NS_MAX_ATTEND_SEQS 4096 /* sequences of one ns_attend_paged call                      */
+#define NS_MAX_GROUPS 512      /* groups of one ns_attend_shared call                         */
 #define NS_MAX_POSITIONS 0x7ffffe00 /* table_ld * page_size of ns_attend_paged: ends of tiles fit 31 bits */
 #define NS_MAX_ALTERNATIVES 32 /* k of ns_token_logprobs                                      */
 
@@ -133,6 +134,34 @@ NS_API ns_status ns_attend_paged(const void *d_q, int32_t dtype, int32_t n_seqs,
                                  const int32_t *d_table, int32_t table_ld, int32_t max_seqs, const int32_t *d_lengths,
                                  const int32_t *d_seqs, const int64_t *d_mask, float scale, int32_t max_len,
                                  void *d_out, float *d_lse, void *d_ws, int64_t ws_bytes, ns_stream stream);
+
+/*
+ * ns_attend_paged for groups of sequences that begin with the same pages, as
+ * samples of one prompt do after ns_pages_fork: call sequences d_groups[g] ..
+ * d_groups[g+1] - 1 (int32 [n_groups + 1], 0 first, not decreasing, n_seqs
+ * last) are group g.  How much its members share is found in the table: the
+ * positions in pages that stand at the beginning of every member's row and are
+ * context for all of them, in whole tiles of 128.  They are read once for each
+ * 256 rows of the group (new tokens and the query heads of a key-value head)
+ * and the rest of each sequence as in ns_attend_paged; results differ from its
+ * by their rounding alone.  Groups that are not as said are flagged
+ * (NS_FLAG_BAD_SEQ) and nothing is shared; a sequence that is invalid ends its
+ * group's sharing.
+ * The sequences' queries follow one another as the tokens do: q_seq is
+ * n * q_token, unless n or n_seqs is 1.  d_q is 16-byte aligned, its strides
+ * positive multiples of 8, as d_k's and d_v's are.  d_ws: device workspace of
+ * ns_attend_shared_workspace(...) bytes, 16-byte aligned, contents immaterial.
+ */
+NS_API int64_t ns_attend_shared_workspace(int32_t n_seqs, int32_t n_groups, int32_t n, int32_t q_heads,
+                                          int32_t kv_heads, int32_t dim);
+NS_API ns_status ns_attend_shared(const void *d_q, int32_t dtype, int32_t n_seqs, int32_t n, int32_t q_heads,
+                                  int32_t kv_heads, int32_t dim, int64_t q_seq, int64_t q_token, int64_t q_head,
+                                  const void *d_k, const void *d_v, int32_t n_pages, int32_t page_size, int64_t k_page,
+                                  int64_t k_head, int64_t k_token, int64_t v_page, int64_t v_head, int64_t v_token,
+                                  const int32_t *d_table, int32_t table_ld, int32_t max_seqs, const int32_t *d_lengths,
+                                  const int32_t *d_seqs, const int32_t *d_groups, int32_t n_groups,
+                                  const int64_t *d_mask, float scale, int32_t max_len, void *d_out, float *d_lse,
+                                  void *d_ws, int64_t ws_bytes, ns_stream stream);
 
 /*
  * A paged key-value cache of several layers, as the ns_pages_* calls see it.

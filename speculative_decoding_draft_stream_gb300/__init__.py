@@ -22,6 +22,7 @@ from .serving import (  # noqa: F401
     TokenLogprobs,
     attend_paged,
     attend_prompt,
+    attend_shared,
     norm_rotate,
     ops_error,
     token_logprobs,

@@ -307,12 +307,12 @@ void exponents_of(const at::Tensor &t, const char *what, c10::Device d, const at
   if (t.sizes() != of.sizes().slice(0, of.dim() - 1)) refuse("%s must have a byte for each row", what);
 }
 
-// q, k_pages, v_pages, table, lengths, seqs, mask, scale, max_len, out, lse, workspace, k_exp, v_exp
+// q, k_pages, v_pages, table, lengths, seqs, mask, scale, max_len, out, lse, workspace, k_exp, v_exp, groups
 PyObject *attend_paged(PyObject *const *a) {
   const at::Tensor &q = tensor(a[0], "q"), &k = tensor(a[1], "k_pages"), &v = tensor(a[2], "v_pages");
   const c10::Device d = device_of(q, "q");
   const at::ScalarType type = attention_type(q);
-  const bool scaled = a[12] != Py_None || a[13] != Py_None;
+  const bool scaled = a[12] != Py_None || a[13] != Py_None, shared = a[14] != Py_None;
   const at::ScalarType held = scaled ? kCodes : type;
   rows_of(q, "q", d, type, 4), rows_of(k, "k_pages", d, held, 4), rows_of(v, "v_pages", d, held, 4);
   const int64_t B = q.size(0), n = q.size(1), hq = q.size(2), dim = q.size(3), hkv = k.size(1);
@@ -330,9 +330,33 @@ PyObject *attend_paged(PyObject *const *a) {
     mask = static_cast<const int64_t *>(given(tensor(a[6], "mask"), "mask", at::kLong, d, {B, n}));
   fits(hq, "q_heads"), fits(k.size(0), "pages"), fits(k.size(2), "page_size"), fits(rows, "table"), fits(ld, "table");
   at::Tensor out = output(a[9], "out", q.sizes(), type, d), lse = output(a[10], "lse", {B, n, hq}, at::kFloat, d);
-  int64_t bytes;
-  const at::Tensor ws =
-      workspace(a[11], ns_attend_paged_workspace((int32_t)B, (int32_t)n, (int32_t)hq, (int32_t)hkv, (int32_t)dim), d, bytes);
+  int64_t bytes, G = 0;
+  const int32_t *groups = nullptr;
+  if (shared) {
+    const at::Tensor &t = tensor(a[14], "groups");
+    if (t.dim() != 1 || t.size(0) < 1 || t.size(0) > NS_MAX_GROUPS + 1 || (t.size(0) == 1 && B > 0))
+      refuse("groups must have one more entry than there are groups, %d at most", NS_MAX_GROUPS);
+    G = t.size(0) - 1;
+    groups = ints(a[14], "groups", d, {G + 1});
+    if (B > 1 && n > 1 && q.stride(0) != n * q.stride(1))
+      refuse("q's sequences must follow one another as their tokens do");
+  }
+  const at::Tensor ws = workspace(a[11],
+                                  shared ? ns_attend_shared_workspace((int32_t)B, (int32_t)G, (int32_t)n, (int32_t)hq,
+                                                                      (int32_t)hkv, (int32_t)dim)
+                                         : ns_attend_paged_workspace((int32_t)B, (int32_t)n, (int32_t)hq,
+                                                                     (int32_t)hkv, (int32_t)dim),
+                                  d, bytes);
+  if (shared) {
+    check(ns_attend_shared(q.data_ptr(), code(type), (int32_t)B, (int32_t)n, (int32_t)hq, (int32_t)hkv, (int32_t)dim,
+                           step(q, 0), step(q, 1), step(q, 2), k.data_ptr(), v.data_ptr(), (int32_t)k.size(0),
+                           (int32_t)k.size(2), step(k, 0), step(k, 1), step(k, 2), step(v, 0), step(v, 1), step(v, 2),
+                           table, (int32_t)ld, (int32_t)rows, lengths, seqs, groups, (int32_t)G, mask,
+                           real(a[7], 1.0 / std::sqrt((double)dim)), (int32_t)integer(a[8], "max_len"), out.data_ptr(),
+                           lse.data_ptr<float>(), ws.data_ptr(), bytes, current_stream(d)),
+          "ns_attend_shared");
+    return pair(std::move(out), std::move(lse));
+  }
   if (scaled) {
     check(ns_attend_paged_scaled(q.data_ptr(), code(type), (int32_t)B, (int32_t)n, (int32_t)hq, (int32_t)hkv,
                                  (int32_t)dim, step(q, 0), step(q, 1), step(q, 2), k.data_ptr(), v.data_ptr(),
@@ -588,7 +612,7 @@ PyObject *set_error(PyObject *const *a) {
 PyMethodDef g_methods[] = {NS_ENTRY("set_error", 1, set_error),
                            NS_ENTRY("norm_rotate", 10, norm_rotate),
                            NS_ENTRY("attend_prompt", 8, attend_prompt),
-                           NS_ENTRY("attend_paged", 14, attend_paged),
+                           NS_ENTRY("attend_paged", 15, attend_paged),
                            NS_ENTRY("cache", 7, cache),
                            NS_ENTRY("truncate", 4, truncate),
                            NS_ENTRY("fork", 4, fork_),

@@ -100,6 +100,12 @@ bool paged_umma_ok(const PagedAttnArgs &a);
 cudaError_t prepare_paged_umma();
 cudaError_t launch_paged_umma(const PagedAttnArgs &a, int dtype, int dim, int sms, cudaStream_t st);
 
+// The same for groups of sequences that begin with the same pages (ns_shared_attn.cu).
+int64_t shared_attn_ws(int n_seqs, int n_groups, int n, int q_heads, int kv_heads, int dim, int sms);
+cudaError_t prepare_shared_attn();
+cudaError_t launch_shared_attn(const PagedAttnArgs &a, const int32_t *groups, int n_groups, int dtype, int dim,
+                               int sms, cudaStream_t st);
+
 // Attention over whole prompts (ns_prompt_attn.cu).
 struct PromptAttnArgs {
   const void *q, *k, *v;

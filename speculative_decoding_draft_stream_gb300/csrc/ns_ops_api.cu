@@ -32,7 +32,9 @@ ns_status current(const Device **out) {
     void *p = nullptr;
     if (cudaGetSymbolAddress(&p, g_ops_flags) != cudaSuccess) return NS_ERR_CUDA;
     if (cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return NS_ERR_CUDA;
-    if (ns::prepare_paged_attn(&d.fit) != cudaSuccess || ns::prepare_prompt_attn() != cudaSuccess) return NS_ERR_CUDA;
+    if (ns::prepare_paged_attn(&d.fit) != cudaSuccess || ns::prepare_prompt_attn() != cudaSuccess ||
+        ns::prepare_shared_attn() != cudaSuccess)
+      return NS_ERR_CUDA;
     d.flags = static_cast<uint32_t *>(p);
     d.ready = true;
   }
@@ -168,12 +170,17 @@ struct Exponents {
   const uint8_t *k, *v;
   int64_t k_page, k_head, v_page, v_head;
 };
+// Groups of sequences (n 0: none).
+struct Groups {
+  const int32_t *cu;
+  int32_t n;
+};
 
 static ns_status attend_paged(const void *d_q, int32_t dtype, int32_t n_seqs, int32_t n, int32_t q_heads,
                               int32_t kv_heads, int32_t dim, int64_t q_seq, int64_t q_token, int64_t q_head,
                               const void *d_k, const void *d_v, int32_t n_pages, int32_t page_size, int64_t k_page,
                               int64_t k_head, int64_t k_token, int64_t v_page, int64_t v_head, int64_t v_token,
-                              const Exponents &x, const int32_t *d_table, int32_t table_ld, int32_t max_seqs,
+                              const Exponents &x, const Groups &groups, const int32_t *d_table, int32_t table_ld, int32_t max_seqs,
                               const int32_t *d_lengths, const int32_t *d_seqs, const int64_t *d_mask, float scale,
                               int32_t max_len, void *d_out, float *d_lse, void *d_ws, int64_t ws_bytes,
                               ns_stream stream) {
@@ -193,9 +200,13 @@ static ns_status attend_paged(const void *d_q, int32_t dtype, int32_t n_seqs, in
               !by8(x.v_head) || k_page % 16 || k_head % 16 || k_token % 16 || v_page % 16 || v_head % 16 ||
               v_token % 16))
     return NS_ERR_ARG;
+  if (groups.n && (!groups.cu || !aligned(groups.cu, 4) || (n > 1 && n_seqs > 1 && q_seq != n * q_token)))
+    return NS_ERR_ARG;
   const Device *d = nullptr;
   if (ns_status s = current(&d)) return s;
-  if (ws_bytes < ns::paged_attn_ws(n_seqs, n, q_heads, kv_heads, dim, d->sms)) return NS_ERR_ARG;
+  if (ws_bytes < (groups.n ? ns::shared_attn_ws(n_seqs, groups.n, n, q_heads, kv_heads, dim, d->sms)
+                           : ns::paged_attn_ws(n_seqs, n, q_heads, kv_heads, dim, d->sms)))
+    return NS_ERR_ARG;
   ns::PagedAttnArgs a{};
   a.q = d_q, a.k = d_k, a.v = d_v;
   a.n_seqs = n_seqs, a.n = n, a.q_heads = q_heads, a.kv_heads = kv_heads, a.group = q_heads / kv_heads;
@@ -210,6 +221,10 @@ static ns_status attend_paged(const void *d_q, int32_t dtype, int32_t n_seqs, in
   a.scale = scale, a.out = d_out, a.lse = d_lse, a.ws = d_ws, a.err = d->flags;
   a.k_exp = x.k, a.v_exp = x.v, a.ke_page = x.k_page, a.ke_head = x.k_head, a.ve_page = x.v_page, a.ve_head = x.v_head;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (groups.n) {
+    if (!ns::paged_umma_ok(a)) return NS_ERR_ARG;
+    return done(ns::launch_shared_attn(a, groups.cu, groups.n, dtype, dim, d->sms, st));
+  }
   return done(x.k ? ns::launch_paged_attn8(a, dtype, dim, d->sms, d->fit, st)
                   : ns::launch_paged_attn(a, dtype, dim, d->sms, d->fit, st));
 }
@@ -222,8 +237,8 @@ ns_status ns_attend_paged(const void *d_q, int32_t dtype, int32_t n_seqs, int32_
                           const int32_t *d_seqs, const int64_t *d_mask, float scale, int32_t max_len, void *d_out,
                           float *d_lse, void *d_ws, int64_t ws_bytes, ns_stream stream) {
   return attend_paged(d_q, dtype, n_seqs, n, q_heads, kv_heads, dim, q_seq, q_token, q_head, d_k, d_v, n_pages,
-                      page_size, k_page, k_head, k_token, v_page, v_head, v_token, Exponents{}, d_table, table_ld,
-                      max_seqs, d_lengths, d_seqs, d_mask, scale, max_len, d_out, d_lse, d_ws, ws_bytes, stream);
+                      page_size, k_page, k_head, k_token, v_page, v_head, v_token, Exponents{}, Groups{}, d_table,
+                      table_ld, max_seqs, d_lengths, d_seqs, d_mask, scale, max_len, d_out, d_lse, d_ws, ws_bytes, stream);
 }
 
 ns_status ns_attend_paged_scaled(const void *d_q, int32_t dtype, int32_t n_seqs, int32_t n, int32_t q_heads,
@@ -238,8 +253,37 @@ ns_status ns_attend_paged_scaled(const void *d_q, int32_t dtype, int32_t n_seqs,
   if (n_seqs > 0 && (!d_k_exp || !d_v_exp)) return NS_ERR_ARG;
   return attend_paged(d_q, dtype, n_seqs, n, q_heads, kv_heads, dim, q_seq, q_token, q_head, d_k, d_v, n_pages,
                       page_size, k_page, k_head, k_token, v_page, v_head, v_token,
-                      Exponents{d_k_exp, d_v_exp, ke_page, ke_head, ve_page, ve_head}, d_table, table_ld, max_seqs,
-                      d_lengths, d_seqs, d_mask, scale, max_len, d_out, d_lse, d_ws, ws_bytes, stream);
+                      Exponents{d_k_exp, d_v_exp, ke_page, ke_head, ve_page, ve_head}, Groups{}, d_table, table_ld,
+                      max_seqs, d_lengths, d_seqs, d_mask, scale, max_len, d_out, d_lse, d_ws, ws_bytes, stream);
+}
+
+static bool groups_ok(int n_seqs, int n_groups) {
+  return n_groups >= 0 && n_groups <= NS_MAX_GROUPS && (n_groups > 0 || n_seqs == 0);
+}
+
+int64_t ns_attend_shared_workspace(int32_t n_seqs, int32_t n_groups, int32_t n, int32_t q_heads, int32_t kv_heads,
+                                   int32_t dim) {
+  if (n_seqs < 0 || n_seqs > NS_MAX_ATTEND_SEQS || !groups_ok(n_seqs, n_groups) || n < 1 || n > NS_MAX_NEW ||
+      !heads_ok(q_heads, kv_heads) || (dim != 64 && dim != 128) || n_groups == 0)
+    return 0;
+  const Device *d = nullptr;
+  if (current(&d)) return 0;
+  return ns::shared_attn_ws(n_seqs, n_groups, n, q_heads, kv_heads, dim, d->sms);
+}
+
+ns_status ns_attend_shared(const void *d_q, int32_t dtype, int32_t n_seqs, int32_t n, int32_t q_heads,
+                           int32_t kv_heads, int32_t dim, int64_t q_seq, int64_t q_token, int64_t q_head,
+                           const void *d_k, const void *d_v, int32_t n_pages, int32_t page_size, int64_t k_page,
+                           int64_t k_head, int64_t k_token, int64_t v_page, int64_t v_head, int64_t v_token,
+                           const int32_t *d_table, int32_t table_ld, int32_t max_seqs, const int32_t *d_lengths,
+                           const int32_t *d_seqs, const int32_t *d_groups, int32_t n_groups, const int64_t *d_mask,
+                           float scale, int32_t max_len, void *d_out, float *d_lse, void *d_ws, int64_t ws_bytes,
+                           ns_stream stream) {
+  if (!groups_ok(n_seqs, n_groups)) return NS_ERR_ARG;
+  return attend_paged(d_q, dtype, n_seqs, n, q_heads, kv_heads, dim, q_seq, q_token, q_head, d_k, d_v, n_pages,
+                      page_size, k_page, k_head, k_token, v_page, v_head, v_token, Exponents{},
+                      Groups{d_groups, n_groups}, d_table, table_ld, max_seqs, d_lengths, d_seqs, d_mask, scale,
+                      max_len, d_out, d_lse, d_ws, ws_bytes, stream);
 }
 
 ns_status ns_pages_truncate(const ns_kv_pages *c, const int32_t *d_seqs, const int32_t *d_new_len, int32_t n,

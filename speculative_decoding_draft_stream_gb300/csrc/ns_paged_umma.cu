@@ -16,8 +16,7 @@
 // 8, bf16, pages of 16, take 56 us (0.57 PFLOP/s, 2.7 TB/s); with mma.sync
 // and 64 rows to a CTA they take nearly three times as long.  Pages of 8 take
 // 65 us: a box costs the TMA engine some 85 cycles, whatever its size.
-#include "ns_paged_attn.cuh"
-#include "ns_umma_attn.cuh"
+#include "ns_paged_mode.cuh"
 
 namespace ns {
 namespace {
@@ -142,51 +141,16 @@ struct Mode {
   using Args = TreeArgs;
   using Work = TreeWork;
   using Dealer = TreeDealer;
-  static constexpr bool kParts = true, kSplit = false;
+  static constexpr bool kParts = true, kSplit = false, kLiveParts = false, kWhole = true;
   static constexpr int kStageRow = 64;
 
-  struct Loader {
-    int ids, next;  // lane l: the id of the l-th page of this tile, and of the next
-    // pages of tile j that hold keys of the sequence
-    __device__ __forceinline__ int pages(const TreeArgs &a, const Work &w, int j) const {
-      const int rows = min(kKeys, w.len - (w.j0 + j) * kKeys), page = 1 << a.page_shift;
-      return rows <= 0 ? 0 : page >= kKeys ? 1 : (rows + page - 1) >> a.page_shift;
-    }
-    __device__ __forceinline__ int fetch(const TreeArgs &a, const Work &w, int j, int lane) const {
-      if (j >= w.n0 || lane >= pages(a, w, j)) return 0;
-      const int p = ((w.j0 + j) * kKeys >> a.page_shift) + lane;
-      const int id = a.table[(size_t)w.seq * a.table_ld + p];
-      if (id >= 0 && id < a.n_pages) return id;
-      set_flag(a.err, NS_FLAG_BAD_ID);
-      return a.n_pages;  // outside the tensor: zeros
-    }
-    __device__ __forceinline__ void begin(const TreeArgs &a, const Work &w, int lane) { next = fetch(a, w, 0, lane); }
+  struct Loader : paged::PageLoader<TreeArgs, TreeWork> {
     __device__ __forceinline__ void queries(const TreeArgs &a, const Work &w, int t, int h, uint32_t dst,
                                             const CUtensorMap *m, uint32_t bar) {
       umma::tma4(dst, m, h * 64, w.unit * a.pack, w.node0 + t * a.per_tile, w.b, bar);
     }
-    template <int D>
-    __device__ __forceinline__ void keys(const TreeArgs &a, const Work &w, int j, int kv, uint32_t dst,
-                                         const CUtensorMap *m, uint32_t bar, int lane, uint32_t *missing) {
-      const int n = pages(a, w, j), page = 1 << a.page_shift, rows = min(page, kKeys);
-      if (kv == 0) {
-        ids = next;
-        next = fetch(a, w, j + 1, lane);
-        // pages out of range, then the tile's eights of keys that lie in them
-        uint32_t out = __ballot_sync(0xffffffffu, lane < n && ids == a.n_pages);
-        if (out) out = __ballot_sync(0xffffffffu, lane < kKeys / 8 && (out >> (lane * 8 / rows) & 1));
-        if (lane == 0) *missing = out;
-      }
-      if (lane == 0) mbar_expect_tx(bar, n * rows * D * 2);
-      __syncwarp();
-      if (lane < n) {
-        const int row = page > kKeys ? (w.j0 + j) * kKeys & (page - 1) : 0;
-        for (int h = 0; h < D / 64; ++h)
-          umma::tma4(dst + h * fa::kHalf + lane * rows * 128, m, h * 64, row, w.unit * a.pack / a.group, ids, bar);
-      }
-      __syncwarp();
-    }
   };
+  using Wild = paged::NodeWild<TreeWork>;
 
   struct Row {
     bool live;
@@ -209,31 +173,18 @@ struct Mode {
     }
   };
 
-  struct Wild {  // new tokens whose value is not finite, per column
-    unsigned long long nan[128], pos[128], neg[128];
-    __device__ __forceinline__ void none(int d) { nan[d] = pos[d] = neg[d] = 0; }
-    // (a value of the context stays: every row sees it)
-    __device__ __forceinline__ bool note(const Work &w, int j, int r, int d, float x) {
-      const int node = (w.j0 + j) * kKeys + r - w.ctx;
-      if (node < 0) return false;
-      (x != x ? nan[d] : x > 0.f ? pos[d] : neg[d]) |= 1ull << node;
-      return true;
-    }
-    __device__ __forceinline__ int seen(const Row &row, int d) const {
-      const bool n = nan[d] & row.word, p = pos[d] & row.word, b = neg[d] & row.word;
-      return n || (p && b) ? 1 : p ? 2 : b ? 3 : 0;
-    }
-  };
-
-  // Rows of a value tile behind the sequence's end: what the ring held before, or what their page holds.
   template <typename T, int D>
   static __device__ __forceinline__ bool clear(const TreeArgs &, const Work &w, int j, uint8_t *tile, int lane) {
-    const int r0 = max(0, w.len - (w.j0 + j) * kKeys);
-    for (int h = 0; h < D / 64; ++h)
-      for (int x = r0 * 8 + lane; x < kKeys * 8; x += kWarp)
-        reinterpret_cast<uint4 *>(tile + h * fa::kHalf)[x] = make_uint4(0, 0, 0, 0);
-    __syncwarp();
-    return r0 < kKeys;
+    return paged::clear_behind<D>(w, j, tile, lane);
+  }
+
+  // Where a part's row lies: 256 rows to a part, column by column.
+  template <int D>
+  static __device__ __forceinline__ void part(const TreeArgs &a, const Work &w, int t, int r, float *&o, int &pitch,
+                                              float2 *&ml) {
+    o = a.part_o + (int64_t)w.slot * D * 256 + t * 128 + r;
+    pitch = 256;
+    ml = a.part_ml + w.slot * 256 + t * 128 + r;
   }
 };
 

@@ -46,7 +46,9 @@
 // what each row sees, and where its result goes:
 //   Args (with pack, per_tile, c, err), Work (with n0, n1: key tiles of the
 //   two row tiles, and hidden: the first that some row does not see whole),
-//   Dealer, Loader, Row, Wild.
+//   Dealer, Loader, Row, Wild; kParts: items may be split, and a part's rows lie
+//   where part() says (kLiveParts: only rows that there are), for a join; kWhole:
+//   items that are not split are written out.
 // kSplit: an item is one row tile, and row tile 1 the same rows again with
 // every other tile of keys; row tile 0's threads add the two up.
 //
@@ -639,7 +641,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (M::kSplit && w.n1 > 0) mbar_arrive(base + L::kOEmpty + 8);
         };
         if (M::kSplit && t == 1) {
-        } else if (!M::kParts || w.slot < 0) {
+        } else if (!M::kParts || (M::kWhole && w.slot < 0)) {
           const float inv = l == 0.f ? 0.f : 1.f / l;
           const long long to = live ? reinterpret_cast<long long>(static_cast<T *>(a.out) + row.at * D) : 0;
 #pragma unroll 1
@@ -674,8 +676,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             flush(to, q * kRow);
           }
           if (live && a.lse) a.lse[row.at] = l == 0.f ? kNegInf : (m - kOffset<T> + log2f(l)) * attn::kLn2;
-        } else {  // a part: fp32 sums for the join, column by column (32 rows of a column are one line)
-          float *to = a.part_o + (int64_t)w.slot * D * 256 + t * 128 + r;
+        } else if constexpr (M::kParts) {  // a part: fp32 sums for the join, column by column (32 rows of a column: a line)
+          float *to;
+          float2 *ml;
+          int pitch;
+          M::template part<D>(a, w, t, r, to, pitch, ml);
 #pragma unroll 1
           for (int q = 0; q < D / 32; ++q) {
             uint32_t o[32];
@@ -687,9 +692,10 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int e = 0; e < 32; ++e) o[e] = fixed(o[e], q * 32 + e);
             }
 #pragma unroll
-            for (int e = 0; e < 32; ++e) to[(q * 32 + e) * 256] = __uint_as_float(o[e]);
+            for (int e = 0; e < 32; ++e)
+              if (!M::kLiveParts || live) to[(q * 32 + e) * pitch] = __uint_as_float(o[e]);
           }
-          a.part_ml[w.slot * 256 + t * 128 + r] = make_float2(m, l);
+          if (!M::kLiveParts || live) *ml = make_float2(m, l);
         }
       }
       __syncwarp();

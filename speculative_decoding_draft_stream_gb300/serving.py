@@ -5,6 +5,8 @@
 * ``attend_prompt``   causal attention over whole packed prompts;
 * ``attend_paged``    attention of a sequence's new tokens (one, or the nodes
                       of a draft tree) over a paged key-value cache;
+* ``attend_shared``   the same for sequences that share a long prefix, which
+                      is read once for all of them;
 * ``KvPages``         the paged cache, of 16 or 8 bits: truncate, fork, extend,
                       write, read, compact, copy;
 * ``token_logprobs``  log probabilities of given tokens, entropy, alternatives;
@@ -130,7 +132,27 @@ def attend_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, 
                                            max_len=max_len, out=out, lse=lse, workspace=workspace, k_exp=k_exp,
                                            v_exp=v_exp))
     return _native().attend_paged(q, k_pages, v_pages, table, lengths, seqs, mask, scale, max_len, out, lse,
-                                  workspace, k_exp, v_exp)
+                                  workspace, k_exp, v_exp, None)
+
+
+def attend_shared(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, table: torch.Tensor,
+                  lengths: torch.Tensor, seqs: torch.Tensor, groups: torch.Tensor, *,
+                  mask: Optional[torch.Tensor] = None, scale: Optional[float] = None, max_len: int = 0,
+                  out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                  workspace: Optional[torch.Tensor] = None, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """attend_paged for groups of sequences that begin with the same pages, as samples of one prompt do after
+    KvPages.fork: seqs[groups[g]] .. seqs[groups[g + 1] - 1] are a group (groups int32 [G + 1], at most 512 groups, 0
+    first and B last).  What the members of a group share is found in the table, in whole tiles of 128 positions, and
+    read once for all of them; the rest of each sequence as in attend_paged, from whose results these differ by their
+    rounding alone.  q [B, n, Hq, D]: sequences follow one another as their tokens do (stride(0) is n * stride(1)), on
+    a 16-byte boundary, with strides that are positive multiples of 8.  It pays where a group's members are many and
+    what they share is long.  Returns (out [B, n, Hq, D], lse fp32 [B, n, Hq])."""
+    s = None if stream is None else _other(stream)
+    if s is not None:
+        return _on(s, lambda: attend_shared(q, k_pages, v_pages, table, lengths, seqs, groups, mask=mask, scale=scale,
+                                            max_len=max_len, out=out, lse=lse, workspace=workspace))
+    return _native().attend_paged(q, k_pages, v_pages, table, lengths, seqs, mask, scale, max_len, out, lse,
+                                  workspace, None, None, groups)
 
 
 class KvPages:
@@ -229,8 +251,13 @@ class KvPages:
         """Copies pages src [n] onto pages dst [n] in every layer."""
         self._b.copy(self._c, src, dst, self._handle(stream))
 
-    def attend(self, layer: int, q: torch.Tensor, seqs: torch.Tensor, **kw) -> Tuple[torch.Tensor, torch.Tensor]:
-        """attend_paged over one layer of this cache."""
+    def attend(self, layer: int, q: torch.Tensor, seqs: torch.Tensor, groups: Optional[torch.Tensor] = None,
+               **kw) -> Tuple[torch.Tensor, torch.Tensor]:
+        """attend_paged over one layer of this cache; with groups, attend_shared (not of 8 bits)."""
+        if groups is not None:
+            if self.k_exp is not None:
+                raise ValueError("a cache of 8 bits does not share prefixes")
+            return attend_shared(q, self.k[layer], self.v[layer], self.table, self.lengths, seqs, groups, **kw)
         if self.k_exp is not None:
             kw = dict(kw, k_exp=self.k_exp[layer], v_exp=self.v_exp[layer])
         return attend_paged(q, self.k[layer], self.v[layer], self.table, self.lengths, seqs, **kw)
