@@ -68,6 +68,14 @@ struct Type<__half> {
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
   }
+  // (the compiler may move it)
+  static __device__ __forceinline__ void mma_free(float *d, const uint32_t *a, uint32_t b0, uint32_t b1) {
+    asm(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, "
+        "%2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  }
 };
 
 // e4m3, two at a time (the first in the lower half), and the scale that a row's exponent byte stands for.
@@ -285,48 +293,65 @@ struct Rows {
   __device__ __forceinline__ void tile8(const uint32_t (*q)[4], uint32_t sK, uint32_t sV, uint32_t sKe, uint32_t sVe,
                                         int k0, const float *cq, const Hidden &hidden, bool wild) {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    static_assert(NK % 32 == 0 || NK == 16, "a lane an exponent, or two lanes");
     float s[NK / 8][4];
+    constexpr int kAtOnce = NK < 32 ? NK / 8 : 4;  // eights of keys whose products take turns
 #pragma unroll
-    for (int i = 0; i < NK / 8; ++i) {
-      uint32_t w[D / 16];
-      if (D == 128) {
-        lds16(sK + piece8<D>(k0 + i * 8 + g, 2 * t), w);
-        lds16(sK + piece8<D>(k0 + i * 8 + g, 2 * t + 1), w + D / 32);
-      } else {
-        lds16(sK + piece8<D>(k0 + i * 8 + g, t), w);
-      }
+    for (int i0 = 0; i0 < NK / 8; i0 += kAtOnce) {
+      uint32_t w[kAtOnce][D / 16];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
-#pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk) Type<T>::mma(s[i], q[kk], from_e4m3(w[kk]), from_e4m3(w[kk] >> 16));
-    }
-    float unit[NK / 8][2];  // 2^-ve
-    float top[2] = {kNegInf, kNegInf};
-#pragma unroll
-    for (int i = 0; i < NK / 8; ++i) {
-      const uint32_t ke = lds2(sKe + k0 + i * 8 + 2 * t), ve = lds2(sVe + k0 + i * 8 + 2 * t);
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const uint32_t bk = e ? ke >> 8 : ke & 255, bv = e ? ve >> 8 : ve & 255;
-        const float f = scale_of(bk);
-        // the byte as a number, less 127; NaN for 255
-        const float add = bv == 255u ? __uint_as_float(0x7fffffffu) : __uint_as_float(0x4b000000u | bv) - 8388735.f;
-        unit[i][e] = __uint_as_float((254u - min(bv, 254u)) << 23);  // (finite: a hidden key's p is 0)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          float &x = s[i][2 * h + e];
-          x = fmaf(x * f, cq[h], add);
-          if (kMasked && hidden(h, i * 8 + 2 * t + e)) x = kNegInf;
-          top[h] = fmaxf(top[h], x);
+      for (int i = 0; i < kAtOnce; ++i) {
+        const int row = k0 + (i0 + i) * 8 + g;
+        if (D == 128) {
+          lds16(sK + piece8<D>(row, 2 * t), w[i]);
+          lds16(sK + piece8<D>(row, 2 * t + 1), w[i] + D / 32);
+        } else {
+          lds16(sK + piece8<D>(row, t), w[i]);
         }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s[i0 + i][j] = 0.f;
       }
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk)
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i)
+          Type<T>::mma_free(s[i0 + i], q[kk], from_e4m3(w[i][kk]), from_e4m3(w[i][kk] >> 16));
+    }
+    // A lane turns one key's two exponents into factors (NK > 32: one of each 32), and the others ask it.
+    float top[2] = {kNegInf, kNegInf};
+    float unit[NK / 8][2];  // 2^-ve
+#pragma unroll
+    for (int b0 = 0; b0 < NK; b0 += 32) {
+      const int at = k0 + b0 + (NK < 32 ? lane & (NK - 1) : lane);
+      const uint32_t bk = lds1(sKe + at), bv = lds1(sVe + at);
+      const float f = __uint_as_float(bk << 23);  // (255: infinity, and NaN with what is added)
+      // the byte as a number, less 127; NaN where either is 255
+      const float add = max(bk, bv) == 255u ? __uint_as_float(0x7fffffffu) : __uint_as_float(0x4b000000u | bv) - 8388735.f;
+      const float u = __uint_as_float((254u - min(bv, 254u)) << 23);  // (finite: a hidden key's p is 0)
+#pragma unroll
+      for (int i = b0 / 8; i < (b0 + 32 < NK ? b0 + 32 : NK) / 8; ++i)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int from = i * 8 - b0 + 2 * t + e;
+          const float ff = __shfl_sync(0xffffffffu, f, from), aa = __shfl_sync(0xffffffffu, add, from);
+          unit[i][e] = __shfl_sync(0xffffffffu, u, from);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            float &x = s[i][2 * h + e];
+            x = fmaf(x * ff, cq[h], aa);
+            if (kMasked && hidden(h, i * 8 + 2 * t + e)) x = kNegInf;
+            top[h] = fmaxf(top[h], x);
+          }
+        }
     }
     float shift[2], p2[2];
+    bool grows = false;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], 1));
       top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], 2));
       const float now = fmaxf(m[h], top[h]), safe = now == kNegInf ? 0.f : now;
+      grows |= now > m[h];
       p2[h] = ex2(m[h] - safe);
       m[h] = now;
       shift[h] = Type<T>::kOffset - safe;
@@ -341,12 +366,14 @@ struct Rows {
       }
 #pragma unroll
     for (int h = 0; h < 2; ++h) l[h] = l[h] * p2[h] + add[h];
+    if (__any_sync(0xffffffffu, grows)) {
 #pragma unroll
-    for (int i = 0; i < D / 8; ++i) {
-      o[i][0] *= p2[0];
-      o[i][1] *= p2[0];
-      o[i][2] *= p2[1];
-      o[i][3] *= p2[1];
+      for (int i = 0; i < D / 8; ++i) {
+        o[i][0] *= p2[0];
+        o[i][1] *= p2[0];
+        o[i][2] *= p2[1];
+        o[i][3] *= p2[1];
+      }
     }
     if (kMasked && wild) {  // one key at a time, and only into rows that see it
 #pragma unroll 1
@@ -376,9 +403,6 @@ struct Rows {
     }
 #pragma unroll
     for (int kb = 0; kb < NK / 16; ++kb) {
-      const uint32_t a[4] = {Type<T>::pack(s[2 * kb][0], s[2 * kb][1]), Type<T>::pack(s[2 * kb][2], s[2 * kb][3]),
-                             Type<T>::pack(s[2 * kb + 1][0], s[2 * kb + 1][1]),
-                             Type<T>::pack(s[2 * kb + 1][2], s[2 * kb + 1][3])};
       uint32_t v[4][D / 32];
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
@@ -388,14 +412,17 @@ struct Rows {
         else
           lds8(sV + piece8<D>(row, g >> 1) + (g & 1) * 8, v[r]);
       }
+      const uint32_t a[4] = {Type<T>::pack(s[2 * kb][0], s[2 * kb][1]), Type<T>::pack(s[2 * kb][2], s[2 * kb][3]),
+                             Type<T>::pack(s[2 * kb + 1][0], s[2 * kb + 1][1]),
+                             Type<T>::pack(s[2 * kb + 1][2], s[2 * kb + 1][3])};
 #pragma unroll
       for (int x = 0; x < D / 32; ++x)
 #pragma unroll
         for (int y = 0; y < 2; ++y) {  // columns 4 x + 2 y and the next, of keys 2 t, 2 t + 1; 2 t + 8, 2 t + 9
           const uint32_t sel = y ? 0x7362u : 0x5140u;
           const uint32_t lo = __byte_perm(v[0][x], v[1][x], sel), hi = __byte_perm(v[2][x], v[3][x], sel);
-          Type<T>::mma(o[4 * x + 2 * y], a, from_e4m3(lo), from_e4m3(hi));
-          Type<T>::mma(o[4 * x + 2 * y + 1], a, from_e4m3(lo >> 16), from_e4m3(hi >> 16));
+          Type<T>::mma_free(o[4 * x + 2 * y], a, from_e4m3(lo), from_e4m3(hi));
+          Type<T>::mma_free(o[4 * x + 2 * y + 1], a, from_e4m3(lo >> 16), from_e4m3(hi >> 16));
         }
     }
   }

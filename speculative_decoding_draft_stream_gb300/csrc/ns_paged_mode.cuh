@@ -9,8 +9,8 @@
 namespace ns {
 namespace paged {
 
-// A whole warp fetches key and value tiles, a lane a page.  Work has the cache's sequence (seq, len), the tiles (j0, n0)
-// and the heads (unit); Args the table and the pages.
+// A whole warp fetches key and value tiles, a lane a page.  Work has the cache's sequence (seq, len), the tiles (j0,
+// tiles()) and the heads (unit); Args the table and the pages.
 template <typename Args, typename Work>
 struct PageLoader {
   int ids, next;  // lane l: the id of the l-th page of this tile, and of the next
@@ -20,7 +20,7 @@ struct PageLoader {
     return rows <= 0 ? 0 : page >= fa::kKeys ? 1 : (rows + page - 1) >> a.page_shift;
   }
   __device__ __forceinline__ int fetch(const Args &a, const Work &w, int j, int lane) const {
-    if (j >= w.n0 || lane >= pages(a, w, j)) return 0;
+    if (j >= w.tiles() || lane >= pages(a, w, j)) return 0;
     const int p = ((w.j0 + j) * fa::kKeys >> a.page_shift) + lane;
     const int id = a.table[(size_t)w.seq * a.table_ld + p];
     if (id >= 0 && id < a.n_pages) return id;

@@ -44,6 +44,7 @@ struct Work {
   int unit, node0;   // query heads unit * pack .., first new token of row tile 0
   int j0, slot;      // first key tile; the part's place (-1: the item is whole)
   int ctx;           // positions that every row sees: len - n
+  __device__ __forceinline__ int tiles() const { return n0; }
 };
 
 using paged::quotient;

@@ -115,6 +115,7 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
 // ---------------------------------------------------------------------------
 // Attend
 // ---------------------------------------------------------------------------
+template <bool S>
 struct Work {
   int n0, n1, hidden;
   int seq, len;       // the cache's sequence (a prefix: its group's first), the end of the keys
@@ -122,24 +123,31 @@ struct Work {
   int unit;           // query heads unit * pack ..
   int j0, slot;       // first key tile; the part's place
   int ctx;            // positions that every row sees (a prefix: all)
+  __device__ __forceinline__ int tiles() const { return S ? n0 + n1 : n0; }
 };
 constexpr int kAllSeen = 0x7fffffff;
+// What an item's beginning and end take, in tiles: the line has that many more for each item, so that shares are equal
+// in time.  Without: 64 sequences of 4 prompts (28 heads on 4, one new token each) 68.0 us, the CTAs with the tails
+// 25 us longer at work than the others; with 1, 2, 3, 4: see the table of launch.
+constexpr int kItemCost = 2;
 
 // A CTA's share of the line, item by item (a whole warp): entries 0 .. n_groups - 1 are prefixes, the others tails.
-// Lane l holds entry 32 chunk + l.
+// Lane l holds entry 32 chunk + l.  S: items of one row tile (attn_kernel's kSplit), otherwise of two.
+template <bool S>
 struct Dealer {
+  static constexpr int kRowTiles = S ? 1 : 2;
   long long at, end;        // next tile, the share's end
   long long base;           // tiles before the chunk's entries
   int item_base;            // prefix items before them
   int cta, lane, l, chunk;  // l: the lane whose entry is dealt
-  int nt, items;            // this lane's entry: tiles of an item, items
+  int nt, items;            // this lane's entry: an item's place in the line (its tiles and cost), items
   int x, y;                 // first sequence and members, or cache sequence and its length
   int from;                 // a tail's first tile
   long long excl, sum;      // tiles before this lane's entry in the chunk, and of the chunk
   int item_excl, item_sum;  // prefix items
 
   __device__ __forceinline__ int blocks(const SharedArgs &a, int members) const {
-    return (members * a.n + 2 * a.per_tile - 1) / (2 * a.per_tile);
+    return (members * a.n + kRowTiles * a.per_tile - 1) / (kRowTiles * a.per_tile);
   }
   __device__ __forceinline__ void load(const SharedArgs &a, int k) {
     chunk = k;
@@ -157,6 +165,7 @@ struct Dealer {
       nt = max(1, (y + kKeys - 1) / kKeys - from);  // an empty sequence: one tile, all masked
       items = a.units * a.tail_blocks;
     }
+    if (nt > 0) nt += kItemCost;
     const int prefix = e < a.n_groups ? items : 0;
     excl = (long long)nt * items, item_excl = prefix;
 #pragma unroll
@@ -191,58 +200,67 @@ struct Dealer {
       base += sum, item_base += item_sum;
     }
   }
-  __device__ __forceinline__ Work next(const SharedArgs &a) {
-    Work w{};
-    if (at >= end) return w;
-    while (at >= base + sum) {
-      base += sum, item_base += item_sum;
-      load(a, chunk + 1);
+  __device__ __forceinline__ Work<S> next(const SharedArgs &a) {
+    Work<S> w{};
+    for (;;) {
+      if (at >= end) return w;
+      while (at >= base + sum) {
+        base += sum, item_base += item_sum;
+        load(a, chunk + 1);
+      }
+      if (piece(a, w)) return w;
     }
+  }
+  // The CTA's next piece of an item; false where it has nothing of the item but its cost.
+  __device__ __forceinline__ bool piece(const SharedArgs &a, Work<S> &w) {
     // the entry that the next tile is in
     l = __ffs(__ballot_sync(0xffffffffu, base + excl + (long long)nt * items > at)) - 1;
     const int e = chunk * 32 + l, n = __shfl_sync(0xffffffffu, nt, l), all = __shfl_sync(0xffffffffu, items, l);
     const int p = __shfl_sync(0xffffffffu, x, l), q = __shfl_sync(0xffffffffu, y, l);
     const int first = __shfl_sync(0xffffffffu, from, l), prior = item_base + __shfl_sync(0xffffffffu, item_excl, l);
     const long long local = at - base - __shfl_sync(0xffffffffu, excl, l);
-    const int item = (int)quotient(local, n), tile = (int)(local - (long long)item * n);
-    const int count = (int)min((long long)(n - tile), end - at);
+    const int item = (int)quotient(local, n), place = (int)(local - (long long)item * n);
+    const int left = (int)min((long long)(n - place), end - at);  // of the line, in this item
+    const int tile = max(0, place - kItemCost), count = left - max(0, kItemCost - place);
+    at += left;
+    if (count <= 0) return false;
     w.n0 = count;
     if (e < a.n_groups) {
       const int b = all / a.units;
-      w.unit = item / b, w.tok0 = p * a.n + item % b * 2 * a.per_tile, w.tok_end = (p + q) * a.n;
-      w.seq = a.seqs[p], w.len = n * kKeys, w.j0 = tile, w.ctx = kAllSeen, w.hidden = count;
+      w.unit = item / b, w.tok0 = p * a.n + item % b * kRowTiles * a.per_tile, w.tok_end = (p + q) * a.n;
+      w.seq = a.seqs[p], w.len = (n - kItemCost) * kKeys, w.j0 = tile, w.ctx = kAllSeen, w.hidden = count;
       w.slot = prior + item + cta;
     } else {
       const int b = e - a.n_groups;
-      w.unit = item / a.tail_blocks, w.tok0 = b * a.n + item % a.tail_blocks * 2 * a.per_tile;
+      w.unit = item / a.tail_blocks, w.tok0 = b * a.n + item % a.tail_blocks * kRowTiles * a.per_tile;
       w.tok_end = (b + 1) * a.n;
       w.seq = p, w.len = q, w.j0 = first + tile, w.ctx = q - a.n;
       w.hidden = max(0, (w.ctx > 0 ? w.ctx / kKeys : 0) - w.j0);
       w.slot = b * all + item + cta;
     }
-    w.n1 = w.tok0 + a.per_tile < w.tok_end ? count : 0;
-    at += count;
-    return w;
+    if (S)
+      w.n1 = count / 2, w.n0 -= w.n1;
+    else
+      w.n1 = w.tok0 + a.per_tile < w.tok_end ? count : 0;
+    return true;
   }
 };
 
-using SharedWork = Work;
-using SharedDealer = Dealer;
-
+template <bool S>
 struct Mode {
   using Args = SharedArgs;
-  using Work = SharedWork;
-  using Dealer = SharedDealer;
-  static constexpr bool kParts = true, kSplit = false, kLiveParts = true, kWhole = false;
-  static constexpr int kStageRow = 64;
+  using Work = ns::Work<S>;
+  using Dealer = ns::Dealer<S>;
+  static constexpr bool kParts = true, kSplit = S, kLiveParts = true, kWhole = false;
+  static constexpr int kStageRow = 64, kRows = S ? 128 : 256;  // (of a part)
 
-  struct Loader : paged::PageLoader<SharedArgs, SharedWork> {
+  struct Loader : paged::PageLoader<SharedArgs, Work> {
     __device__ __forceinline__ void queries(const SharedArgs &a, const Work &w, int t, int h, uint32_t dst,
                                             const CUtensorMap *m, uint32_t bar) {
       umma::tma3(dst, m, h * 64, w.unit * a.pack, w.tok0 + t * a.per_tile, bar);
     }
   };
-  using Wild = paged::NodeWild<SharedWork>;
+  using Wild = paged::NodeWild<Work>;
 
   struct Row {
     bool live;
@@ -275,7 +293,7 @@ struct Mode {
   static __device__ __forceinline__ void part(const SharedArgs &a, const Work &w, int t, int r, float *&o, int &pitch,
                                               float2 *&ml) {
     const bool tail = w.ctx != kAllSeen;
-    pitch = tail ? a.tail_rows : 256;
+    pitch = tail ? a.tail_rows : kRows;
     const int row = tail ? t * a.per_tile * a.pack + r : t * 128 + r;
     o = (tail ? a.tail_o : a.part_o) + (int64_t)w.slot * D * pitch + row;
     ml = (tail ? a.tail_ml : a.part_ml) + (int64_t)w.slot * pitch + row;
@@ -285,29 +303,32 @@ struct Mode {
 // ---------------------------------------------------------------------------
 // Merge
 // ---------------------------------------------------------------------------
-// A CTA has 32 rows (lanes) and 32 columns; its warps take a row's parts in
-// turns and add up in warp order.
+// A CTA has 32 rows, a lane each.  G = 8: its warps take the parts of 32
+// columns in turns and add up in warp order; G = 1: each has all parts of D / 8
+// columns.
 constexpr int kMergeWarps = 8;
-template <typename T, int D>
+template <typename T, int D, bool S, int G>
 __global__ void __launch_bounds__(kMergeWarps * 32) merge_kernel(const SharedArgs a, int ctas) {
-  __shared__ float s_o[kMergeWarps][32][33], s_m[kMergeWarps][32], s_l[kMergeWarps][32];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, unit = blockIdx.y, col0 = blockIdx.z * 32;
+  constexpr int N = G == 1 ? D / 8 : 32, kRowTiles = S ? 1 : 2;  // columns of a warp
+  __shared__ float s_o[G][G > 1 ? N : 1][33], s_m[G][32], s_l[G][32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, unit = blockIdx.y;
+  const int col0 = G == 1 ? warp * N : blockIdx.z * N;
   const int row = blockIdx.x * 32 + lane, tok = row / a.pack, h = row % a.pack;
   const bool live = tok < a.n_seqs * a.n;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int b = live ? tok / a.n : 0, node = live ? tok % a.n : 0;
   const long long total = a.cum[a.n_groups + a.n_seqs];
   auto first_of = [&](int c) { return quotient(total * c, ctas); };
-  // the row's pieces: CTAs c0 .. of an item, where place + (c * D + column) * pitch is its element of CTA c's part
-  int pieces[2] = {0, 0}, c0[2] = {0, 0}, pitch[2] = {256, a.tail_rows};
+  // the row's pieces: CTAs c0 .. of an item, where (slot + c) * pitch is CTA c's part
+  int pieces[2] = {0, 0}, c0[2] = {0, 0}, pitch[2] = {kRowTiles * 128, a.tail_rows};
   int64_t slot[2] = {0, 0};
   int in_part[2] = {0, 0};
   if (live) {
-    const int X = 2 * a.per_tile, g = a.group_of[b], nt = a.shared[g];
+    const int X = kRowTiles * a.per_tile, g = a.group_of[b], nt = a.shared[g];
     if (nt > 0) {
       const int2 bounds = a.bounds[g];
       const int v = tok - bounds.x * a.n, blocks = (bounds.y * a.n + X - 1) / X, item = unit * blocks + v / X;
-      const long long from = a.cum[g] + (long long)item * nt;
+      const long long from = a.cum[g] + (long long)item * (nt + kItemCost) + kItemCost;
       c0[0] = (int)quotient((from + 1) * ctas - 1, total);
       pieces[0] = (int)quotient((from + nt) * ctas - 1, total) - c0[0] + 1;
       slot[0] = a.items_before[g] + item;
@@ -315,61 +336,75 @@ __global__ void __launch_bounds__(kMergeWarps * 32) merge_kernel(const SharedArg
     }
     const long long cb = a.cum[a.n_groups + b];
     const int items = a.units * a.tail_blocks, item = unit * a.tail_blocks + node / X;
-    const long long n = quotient(a.cum[a.n_groups + b + 1] - cb, items), from = cb + item * n;
+    const long long n = quotient(a.cum[a.n_groups + b + 1] - cb, items), from = cb + item * n + kItemCost;
     c0[1] = (int)quotient((from + 1) * ctas - 1, total);
-    pieces[1] = (int)quotient((from + n) * ctas - 1, total) - c0[1] + 1;
+    pieces[1] = (int)quotient((from + n - kItemCost) * ctas - 1, total) - c0[1] + 1;
     slot[1] = b * items + item;
     in_part[1] = node % X * a.pack + h;
   }
-  float m = kNegInf, l = 0.f, o[32];
+  float m = kNegInf, l = 0.f, o[N];
 #pragma unroll
-  for (int i = 0; i < 32; ++i) o[i] = 0.f;
+  for (int i = 0; i < N; ++i) o[i] = 0.f;
   const int all = pieces[0] + pieces[1];
-  for (int p = warp; __any_sync(0xffffffffu, p < all); p += kMergeWarps) {
+  for (int p = G == 1 ? 0 : warp; __any_sync(0xffffffffu, p < all); p += G) {
     if (p >= all) continue;
     const int k = p >= pieces[0], c = c0[k] + p - (k ? pieces[0] : 0);
-    if (first_of(c) == first_of(c + 1)) continue;  // a CTA without tiles
+    if (total < ctas && first_of(c) == first_of(c + 1)) continue;  // a CTA without tiles
     const int64_t at = (slot[k] + c) * pitch[k];
     const float2 ml = (k ? a.tail_ml : a.part_ml)[at + in_part[k]];
     const float *src = (k ? a.tail_o : a.part_o) + at * D + (int64_t)col0 * pitch[k] + in_part[k];
-    float x[32];
+    float x[N];
 #pragma unroll
-    for (int i = 0; i < 32; ++i) x[i] = src[(int64_t)i * pitch[k]];
+    for (int i = 0; i < N; ++i) x[i] = src[(int64_t)i * pitch[k]];
     const float now = fmaxf(m, ml.x), safe = now == kNegInf ? 0.f : now;
     const float f0 = attn::ex2(m - safe), f1 = attn::ex2(ml.x - safe);
     m = now, l = l * f0 + ml.y * f1;
 #pragma unroll
-    for (int i = 0; i < 32; ++i) o[i] = fmaf(x[i], f1, o[i] * f0);
+    for (int i = 0; i < N; ++i) o[i] = fmaf(x[i], f1, o[i] * f0);
   }
-#pragma unroll
-  for (int i = 0; i < 32; ++i) s_o[warp][i][lane] = o[i];
-  s_m[warp][lane] = m, s_l[warp][lane] = l;
-  __syncthreads();
-  // a thread has four columns of a row
-  m = kNegInf, l = 0.f;
-#pragma unroll
-  for (int w = 0; w < kMergeWarps; ++w) m = fmaxf(m, s_m[w][lane]);
-  const float safe = m == kNegInf ? 0.f : m;
-  float y[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-  for (int w = 0; w < kMergeWarps; ++w) {
-    const float f = attn::ex2(s_m[w][lane] - safe);
-    l = fmaf(s_l[w][lane], f, l);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) y[i] = fmaf(s_o[w][warp * 4 + i][lane], f, y[i]);
-  }
-  if (!live) return;
-  const float inv = l == 0.f ? 0.f : 1.f / l;
   const int64_t at = (int64_t)tok * a.q_heads + unit * a.pack + h;
-  *reinterpret_cast<uint2 *>(static_cast<T *>(a.out) + at * D + col0 + warp * 4) =
-      make_uint2(attn::Type<T>::pack(y[0] * inv, y[1] * inv), attn::Type<T>::pack(y[2] * inv, y[3] * inv));
-  if (a.lse && col0 == 0 && warp == 0) a.lse[at] = l == 0.f ? kNegInf : (m - fa::kOffset<T> + log2f(l)) * attn::kLn2;
+  T *out = static_cast<T *>(a.out) + at * D + col0;
+  if constexpr (G == 1) {
+    if (!live) return;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+    for (int i = 0; i < N; i += 8)
+      *reinterpret_cast<uint4 *>(out + i) = make_uint4(
+          attn::Type<T>::pack(o[i] * inv, o[i + 1] * inv), attn::Type<T>::pack(o[i + 2] * inv, o[i + 3] * inv),
+          attn::Type<T>::pack(o[i + 4] * inv, o[i + 5] * inv), attn::Type<T>::pack(o[i + 6] * inv, o[i + 7] * inv));
+    if (a.lse && warp == 0) a.lse[at] = l == 0.f ? kNegInf : (m - fa::kOffset<T> + log2f(l)) * attn::kLn2;
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) s_o[warp][i][lane] = o[i];
+    s_m[warp][lane] = m, s_l[warp][lane] = l;
+    __syncthreads();
+    // a thread has four columns of a row
+    m = kNegInf, l = 0.f;
+#pragma unroll
+    for (int w = 0; w < G; ++w) m = fmaxf(m, s_m[w][lane]);
+    const float safe = m == kNegInf ? 0.f : m;
+    float y[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int w = 0; w < G; ++w) {
+      const float f = attn::ex2(s_m[w][lane] - safe);
+      l = fmaf(s_l[w][lane], f, l);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) y[i] = fmaf(s_o[w][warp * 4 + i][lane], f, y[i]);
+    }
+    if (!live) return;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    *reinterpret_cast<uint2 *>(out + warp * 4) =
+        make_uint2(attn::Type<T>::pack(y[0] * inv, y[1] * inv), attn::Type<T>::pack(y[2] * inv, y[3] * inv));
+    if (a.lse && col0 == 0 && warp == 0)
+      a.lse[at] = l == 0.f ? kNegInf : (m - fa::kOffset<T> + log2f(l)) * attn::kLn2;
+  }
 }
 
 // ---------------------------------------------------------------------------
 // Shapes, workspace and launches
 // ---------------------------------------------------------------------------
 struct Shape {
+  bool split;  // items of one row tile
   int pack, per_tile, units, tail_blocks, tail_rows;
   int64_t parts, tails;  // places of prefix and tail parts
 };
@@ -378,7 +413,9 @@ Shape shape_of(int n_seqs, int n_groups, int n, int q_heads, int kv_heads, int s
   const int group = q_heads / kv_heads;
   s.pack = group <= 128 ? group : 1;
   s.per_tile = 128 / s.pack, s.units = q_heads / s.pack;
-  const int X = 2 * s.per_tile;
+  // One row tile where the groups have no more tokens than that on average: its keys keep both softmax groups busy.
+  s.split = n_groups > 0 && (int64_t)n_seqs * n <= (int64_t)n_groups * s.per_tile;
+  const int X = (s.split ? 1 : 2) * s.per_tile;
   s.tail_blocks = (n + X - 1) / X;
   s.tail_rows = ((n < X ? n : X) * s.pack + 7) & ~7;
   // Groups have sum ceil(tokens / X) blocks, with two members and so two tokens each at least.
@@ -400,15 +437,15 @@ struct Layout {
     };
     bounds = take(8LL * n_groups), shared = take(4LL * n_groups), group_of = take(4LL * n_seqs);
     cum = take(8LL * (n_groups + n_seqs + 1)), items = take(4LL * n_groups);
-    part_ml = take(s.parts * 256 * 8), tail_ml = take(s.tails * s.tail_rows * 8);
-    part_o = take(s.parts * 256 * dim * 4), tail_o = take(s.tails * s.tail_rows * dim * 4);
+    part_ml = take(s.parts * (s.split ? 128 : 256) * 8), tail_ml = take(s.tails * s.tail_rows * 8);
+    part_o = take(s.parts * (s.split ? 128 : 256) * dim * 4), tail_o = take(s.tails * s.tail_rows * dim * 4);
     bytes = at;
   }
 };
 
-template <typename T, int D>
-cudaError_t launch(const PagedAttnArgs &p, const int32_t *groups, int n_groups, int sms, cudaStream_t st) {
-  const Shape s = shape_of(p.n_seqs, n_groups, p.n, p.q_heads, p.kv_heads, sms);
+template <typename T, int D, bool S>
+cudaError_t launch(const PagedAttnArgs &p, const Shape &s, const int32_t *groups, int n_groups, int sms,
+                   cudaStream_t st) {
   const Layout at(s, p.n_seqs, n_groups, D);
   char *ws = static_cast<char *>(p.ws);
   SharedArgs a{};
@@ -446,13 +483,34 @@ cudaError_t launch(const PagedAttnArgs &p, const int32_t *groups, int n_groups, 
   cfg.stream = st;
   cfg.gridDim = dim3((unsigned)sms);
   cfg.blockDim = dim3(fa::kThreads);
-  cfg.dynamicSmemBytes = fa::Smem<D, Mode>::kBytes;
-  e = cudaLaunchKernelEx(&cfg, fa::attn_kernel<T, D, Mode>, tmQ, tmK, tmV, a);
+  cfg.dynamicSmemBytes = fa::Smem<D, Mode<S>>::kBytes;
+  e = cudaLaunchKernelEx(&cfg, fa::attn_kernel<T, D, Mode<S>>, tmQ, tmK, tmV, a);
   if (e != cudaSuccess) return e;
-  cfg.gridDim = dim3((unsigned)(((int64_t)p.n_seqs * p.n * a.pack + 31) / 32), (unsigned)a.units, D / 32);
+  // an item's parts: some more than its share of the CTAs, if the prefixes are of like lengths
+  const int64_t tokens = (int64_t)p.n_seqs * p.n;
+  const bool many = (int64_t)sms * (S ? 1 : 2) * a.per_tile >= 4 * a.units * tokens;
+  cfg.gridDim = dim3((unsigned)((tokens * a.pack + 31) / 32), (unsigned)a.units, many ? D / 32 : 1);
   cfg.blockDim = dim3(kMergeWarps * 32);
   cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, merge_kernel<T, D>, a, sms);
+  return many ? cudaLaunchKernelEx(&cfg, merge_kernel<T, D, S, 8>, a, sms)
+              : cudaLaunchKernelEx(&cfg, merge_kernel<T, D, S, 1>, a, sms);
+}
+
+template <typename T, int D>
+cudaError_t by_shape(const PagedAttnArgs &p, const int32_t *groups, int n_groups, int sms, cudaStream_t st) {
+  const Shape s = shape_of(p.n_seqs, n_groups, p.n, p.q_heads, p.kv_heads, sms);
+  return s.split ? launch<T, D, true>(p, s, groups, n_groups, sms, st)
+                 : launch<T, D, false>(p, s, groups, n_groups, sms, st);
+}
+
+template <typename T, int D>
+cudaError_t prepare() {
+  cudaError_t e = cudaFuncSetAttribute(fa::attn_kernel<T, D, Mode<false>>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       fa::Smem<D, Mode<false>>::kBytes);
+  return e != cudaSuccess ? e
+                          : cudaFuncSetAttribute(fa::attn_kernel<T, D, Mode<true>>,
+                                                 cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                 fa::Smem<D, Mode<true>>::kBytes);
 }
 
 }  // namespace
@@ -462,24 +520,19 @@ int64_t shared_attn_ws(int n_seqs, int n_groups, int n, int q_heads, int kv_head
 }
 
 cudaError_t prepare_shared_attn() {
-  cudaError_t e = cudaSuccess;
-  auto set = [&](const void *f, int bytes) {
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  };
-  set((const void *)fa::attn_kernel<__nv_bfloat16, 128, Mode>, fa::Smem<128, Mode>::kBytes);
-  set((const void *)fa::attn_kernel<__nv_bfloat16, 64, Mode>, fa::Smem<64, Mode>::kBytes);
-  set((const void *)fa::attn_kernel<__half, 128, Mode>, fa::Smem<128, Mode>::kBytes);
-  set((const void *)fa::attn_kernel<__half, 64, Mode>, fa::Smem<64, Mode>::kBytes);
-  return e;
+  cudaError_t e = prepare<__nv_bfloat16, 128>();
+  if (e == cudaSuccess) e = prepare<__nv_bfloat16, 64>();
+  if (e == cudaSuccess) e = prepare<__half, 128>();
+  return e == cudaSuccess ? prepare<__half, 64>() : e;
 }
 
 cudaError_t launch_shared_attn(const PagedAttnArgs &a, const int32_t *groups, int n_groups, int dtype, int dim,
                                int sms, cudaStream_t st) {
   if (dtype == NS_DTYPE_BF16)
-    return dim == 128 ? launch<__nv_bfloat16, 128>(a, groups, n_groups, sms, st)
-                      : launch<__nv_bfloat16, 64>(a, groups, n_groups, sms, st);
-  return dim == 128 ? launch<__half, 128>(a, groups, n_groups, sms, st)
-                    : launch<__half, 64>(a, groups, n_groups, sms, st);
+    return dim == 128 ? by_shape<__nv_bfloat16, 128>(a, groups, n_groups, sms, st)
+                      : by_shape<__nv_bfloat16, 64>(a, groups, n_groups, sms, st);
+  return dim == 128 ? by_shape<__half, 128>(a, groups, n_groups, sms, st)
+                    : by_shape<__half, 64>(a, groups, n_groups, sms, st);
 }
 
 }  // namespace ns

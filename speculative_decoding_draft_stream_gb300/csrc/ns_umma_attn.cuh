@@ -196,8 +196,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     typename M::Loader loader;
     int it = 0;  // ring position: K0 V0 K1 V1 ... over all items
     // Key tile x (over all items) leaves its missing keys in word x % kMissingTiles.  They are read before the
-    // softmax hands over tile x's probabilities, scores of tile x + 1 are issued after that, and key tile x + 3 is
-    // loaded after those are over: a word is not written again before it was read.
+    // softmax hands over tile x's probabilities, scores of tile x + 1 (M::kSplit: x + 2) are issued after that, and key
+    // tile x + 3 (x + 4) is loaded after those are over: a word is not written again before it was read.
     static_assert(!M::kParts || kMissingTiles > kRing / 2, "the words outlive their tiles");
     uint32_t *missing = reinterpret_cast<uint32_t *>(g + L::kMissing);
     bool ok = true;
@@ -485,7 +485,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         float sum;
         // (only a cache's pages may be missing)
         const uint32_t missing =
-            M::kParts ? *(reinterpret_cast<volatile uint32_t *>(g + L::kMissing) + (passed + j) % kMissingTiles) : 0u;
+            M::kParts ? *(reinterpret_cast<volatile uint32_t *>(g + L::kMissing) + (passed + key_tile) % kMissingTiles)
+                      : 0u;
         const bool masked = key_tile >= w.hidden || (M::kParts && missing != 0);
         auto mask = [&](int from) {  // keys that the row does not see, among 64
           uint64_t sees = row.sees(w, key_tile, from);
@@ -685,6 +686,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int q = 0; q < D / 32; ++q) {
             uint32_t o[32];
             umma::ld32(tO + q * 32, o);
+            if constexpr (M::kSplit) {
+              if (w.n1 > 0) {
+                uint32_t o1[32];
+                umma::ld32(tO + 128 + q * 32, o1);
+                umma::wait_ld();
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                  o[e] = __float_as_uint(__uint_as_float(o[e]) * f0 + __uint_as_float(o1[e]) * f1);
+              }
+            }
             umma::wait_ld();
             if (q + 1 == D / 32) drained();
             if (wild) {
