@@ -89,6 +89,11 @@ __device__ __forceinline__ uint32_t from_e4m3(uint32_t pair) {  // (upper half i
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)pair));
   return r;
 }
+__device__ __forceinline__ uint32_t from_e4m3_hi(uint32_t pairs) {  // the upper two of four
+  uint32_t r;
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}" : "=r"(r) : "r"(pairs));
+  return r;
+}
 __device__ __forceinline__ float scale_of(uint32_t byte) {
   return __uint_as_float(byte << 23 | (byte == 255u ? 0x400000u : 0u));  // 2^(byte - 127); 255: NaN
 }
@@ -97,6 +102,12 @@ __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+// An 8 x 8 matrix of 16-bit elements, two of a row to a lane, transposed.
+__device__ __forceinline__ uint32_t across(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
 }
 __device__ __forceinline__ void ldsm4(uint32_t a, uint32_t *r) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
@@ -163,6 +174,12 @@ template <typename T, int D>
 struct Rows {
   float o[D / 8][4];
   float m[2], l[2];
+
+  static constexpr int kParts = D / 8;  // groups of o
+  // The row (of its two) that o[.][j] belongs to, and where row h lies in the 16.
+  static __device__ __forceinline__ int of(int j) { return j >> 1; }
+  static __device__ __forceinline__ int row(int h) { return ((threadIdx.x & 31) >> 2) + 8 * h; }
+  static __device__ __forceinline__ bool first() { return (threadIdx.x & 3) == 0; }  // of a row's lanes
 
   __device__ __forceinline__ void clear() {
 #pragma unroll
@@ -315,7 +332,7 @@ struct Rows {
       for (int kk = 0; kk < D / 16; ++kk)
 #pragma unroll
         for (int i = 0; i < kAtOnce; ++i)
-          Type<T>::mma_free(s[i0 + i], q[kk], from_e4m3(w[i][kk]), from_e4m3(w[i][kk] >> 16));
+          Type<T>::mma_free(s[i0 + i], q[kk], from_e4m3(w[i][kk]), from_e4m3_hi(w[i][kk]));
     }
     // A lane turns one key's two exponents into factors (NK > 32: one of each 32), and the others ask it.
     float top[2] = {kNegInf, kNegInf};
@@ -422,7 +439,7 @@ struct Rows {
           const uint32_t sel = y ? 0x7362u : 0x5140u;
           const uint32_t lo = __byte_perm(v[0][x], v[1][x], sel), hi = __byte_perm(v[2][x], v[3][x], sel);
           Type<T>::mma_free(o[4 * x + 2 * y], a, from_e4m3(lo), from_e4m3(hi));
-          Type<T>::mma_free(o[4 * x + 2 * y + 1], a, from_e4m3(lo >> 16), from_e4m3(hi >> 16));
+          Type<T>::mma_free(o[4 * x + 2 * y + 1], a, from_e4m3_hi(lo), from_e4m3_hi(hi));
         }
     }
   }
@@ -449,6 +466,173 @@ struct Rows {
       l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
       l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
     }
+  }
+};
+
+// State of 8 rows of a warp over a cache of 8 bits, the products the other way
+// round: scores are K Q^T and the sums V^T P^T, so keys and columns take the
+// 16 places of mma's first operand and the rows its 8 columns.  Half the
+// products, scores and sums of 16 rows, of which a decoded token's heads rarely
+// fill more than 8.  Lane (g, t) holds rows 2 t and 2 t + 1: columns
+// D / 8 g + 2 i and + 1 in group i.  P goes from where it is computed (keys g,
+// rows 2 t) to where it is an operand (rows g, keys 2 t) by movmatrix.
+template <typename T, int D>
+struct Rows8 {
+  static constexpr int kParts = D / 16;
+  float o[D / 16][4];
+  float m[2], l[2];
+
+  static __device__ __forceinline__ int of(int j) { return j & 1; }
+  static __device__ __forceinline__ int row(int h) { return 2 * (threadIdx.x & 3) + h; }
+  static __device__ __forceinline__ bool first() { return (threadIdx.x & 31) < 4; }
+
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) o[i][j] = 0.f;
+    m[0] = m[1] = kNegInf;
+    l[0] = l[1] = 0.f;
+  }
+
+  // As Rows::tile8; q: row g's columns D / 4 t + 4 kk .. + 3 in product kk.
+  template <int NK, bool kMasked, typename Hidden>
+  __device__ __forceinline__ void tile8(const uint32_t (*q)[2], uint32_t sK, uint32_t sV, uint32_t sKe, uint32_t sVe,
+                                        int k0, const float *cq, const Hidden &hidden, bool wild) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    constexpr int B = NK / 16;  // blocks of keys
+    float s[B][4];
+#pragma unroll
+    for (int i = 0; i < B; ++i) {
+      uint32_t w[2][D / 16];
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const int row = k0 + i * 16 + r * 8 + g;
+        if (D == 128) {
+          lds16(sK + piece8<D>(row, 2 * t), w[r]);
+          lds16(sK + piece8<D>(row, 2 * t + 1), w[r] + D / 32);
+        } else {
+          lds16(sK + piece8<D>(row, t), w[r]);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        const uint32_t a[4] = {from_e4m3(w[0][kk]), from_e4m3(w[1][kk]), from_e4m3_hi(w[0][kk]),
+                               from_e4m3_hi(w[1][kk])};
+        Type<T>::mma_free(s[i], a, q[kk][0], q[kk][1]);
+      }
+    }
+    float top[2] = {kNegInf, kNegInf}, unit[B][2];
+#pragma unroll
+    for (int i = 0; i < B; ++i)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int key = i * 16 + e * 8 + g;
+        const uint32_t bk = lds1(sKe + k0 + key), bv = lds1(sVe + k0 + key);
+        const float f = __uint_as_float(bk << 23);  // (255: infinity, and NaN with what is added)
+        const float add =
+            max(bk, bv) == 255u ? __uint_as_float(0x7fffffffu) : __uint_as_float(0x4b000000u | bv) - 8388735.f;
+        unit[i][e] = __uint_as_float((254u - min(bv, 254u)) << 23);  // (finite: a hidden key's p is 0)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float &x = s[i][2 * e + h];
+          x = fmaf(x * f, cq[h], add);
+          if (kMasked && hidden(h, key)) x = kNegInf;
+          top[h] = fmaxf(top[h], x);
+        }
+      }
+    float shift[2], p2[2];
+    bool grows = false;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+      for (int off = 4; off < 32; off <<= 1) top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], off));
+      const float now = fmaxf(m[h], top[h]), safe = now == kNegInf ? 0.f : now;
+      grows |= now > m[h];
+      p2[h] = ex2(m[h] - safe);
+      m[h] = now;
+      shift[h] = Type<T>::kOffset - safe;
+    }
+    float add[2] = {0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < B; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        s[i][j] = ex2(s[i][j] + shift[j & 1]);
+        add[j & 1] = fmaf(s[i][j], unit[i][j >> 1], add[j & 1]);
+      }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) l[h] = l[h] * p2[h] + add[h];
+    if (__any_sync(0xffffffffu, grows)) {
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[i][j] *= p2[j & 1];
+    }
+    if (kMasked && wild) {  // one key at a time, and only into rows that see it
+#pragma unroll 1
+      for (int key = 0; key < NK; ++key) {
+        float p[2] = {0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < B; ++i)
+          if (i == key >> 4) {
+            p[0] = (key & 8) ? s[i][2] : s[i][0];
+            p[1] = (key & 8) ? s[i][3] : s[i][1];
+          }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) p[h] = __shfl_sync(0xffffffffu, p[h], (key & 7) * 4 + t);
+        const bool gone[2] = {hidden(0, key), hidden(1, key)};
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int d = D / 8 * g + 2 * i + e;
+            const float v = Type<T>::unpack(from_e4m3(lds1(sV + piece8<D>(k0 + key, d >> 4) + (d & 15)))).x;
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              if (!gone[h]) o[i][2 * e + h] = fmaf(p[h], v, o[i][2 * e + h]);
+          }
+      }
+      return;
+    }
+#pragma unroll
+    for (int kb = 0; kb < B; ++kb) {
+      uint32_t v[4][D / 32];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int row = k0 + kb * 16 + 2 * t + (r & 1) + (r >> 1) * 8;
+        if (D == 128)
+          lds16(sV + piece8<D>(row, g), v[r]);
+        else
+          lds8(sV + piece8<D>(row, g >> 1) + (g & 1) * 8, v[r]);
+      }
+      const uint32_t b0 = across(Type<T>::pack(s[kb][0], s[kb][1])), b1 = across(Type<T>::pack(s[kb][2], s[kb][3]));
+#pragma unroll
+      for (int x = 0; x < D / 32; ++x)
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {  // columns 4 x + 2 y and the next, of keys 2 t, 2 t + 1; 2 t + 8, 2 t + 9
+          const uint32_t sel = y ? 0x7362u : 0x5140u;
+          const uint32_t lo = __byte_perm(v[0][x], v[1][x], sel), hi = __byte_perm(v[2][x], v[3][x], sel);
+          const uint32_t a[4] = {from_e4m3(lo), from_e4m3_hi(lo), from_e4m3(hi), from_e4m3_hi(hi)};
+          Type<T>::mma_free(o[2 * x + y], a, b0, b1);
+        }
+    }
+  }
+
+  template <bool F8, typename To>
+  __device__ __forceinline__ void columns(int h, const To &to) const {
+    const int g = (threadIdx.x & 31) >> 2;
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) to(D / 8 * g + 2 * i, o[i][h], o[i][2 + h]);
+  }
+
+  __device__ __forceinline__ void sum_l() {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int off = 4; off < 32; off <<= 1) l[h] += __shfl_xor_sync(0xffffffffu, l[h], off);
   }
 };
 

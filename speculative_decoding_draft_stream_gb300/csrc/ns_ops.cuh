@@ -80,10 +80,11 @@ struct PagedAttnArgs {
   uint32_t *err;
   const uint8_t *k_exp, *v_exp;  // a cache of 8 bits: each row's exponent
   int64_t ke_page, ke_head, ve_page, ve_head;
+  int32_t kp16, kt16, vp16, vt16, kep8, vep8;  // its strides in units of 16 (exponents: 8) bytes
 };
 // What a device holds of the kernels for few rows (found when it is first used).
 struct PagedFit {
-  int clusters[2][2][2][2];  // resident at once: cache of 8 bits, dtype, dim 64 or 128, small or large CTAs
+  int clusters[3][2][2][2];  // resident at once: cache of 16 bits, of 8, of 8 with 8 rows; dtype; dim 64, 128; small, large
 };
 int64_t paged_attn_ws(int n_seqs, int n, int q_heads, int kv_heads, int dim, int sms);
 cudaError_t prepare_paged_attn(PagedFit *fit);

@@ -219,6 +219,15 @@ static ns_status attend_paged(const void *d_q, int32_t dtype, int32_t n_seqs, in
   a.max_len = max_len == 0 || max_len > most ? (int32_t)most : max_len;
   a.table = d_table, a.lengths = d_lengths, a.seqs = d_seqs, a.mask = d_mask;
   a.scale = scale, a.out = d_out, a.lse = d_lse, a.ws = d_ws, a.err = d->flags;
+  if (x.k) {
+    const int64_t strides[6] = {a.k_page / 16, a.k_token / 16, a.v_page / 16, a.v_token / 16,
+                                step(x.k_page, n_pages, 8) / 8, step(x.v_page, n_pages, 8) / 8};
+    int32_t *to[6] = {&a.kp16, &a.kt16, &a.vp16, &a.vt16, &a.kep8, &a.vep8};
+    for (int i = 0; i < 6; ++i) {
+      if (strides[i] < -0x7fffffffLL || strides[i] > 0x7fffffffLL) return NS_ERR_ARG;
+      *to[i] = (int32_t)strides[i];
+    }
+  }
   a.k_exp = x.k, a.v_exp = x.v, a.ke_page = x.k_page, a.ke_head = x.k_head, a.ve_page = x.v_page, a.ve_head = x.v_head;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (groups.n) {

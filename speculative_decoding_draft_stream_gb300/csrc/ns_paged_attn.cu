@@ -31,7 +31,7 @@ namespace {
 // trees of 60 nodes behind 512 to 4096 tokens (240 rows) 169, there 60.
 template <typename T, int D>
 cudaError_t by_rows(const PagedAttnArgs &a, int sms, const PagedFit &fit, cudaStream_t st) {
-  if (a.n * a.group <= 16) return few_rows<T, D, false>(a, sms, fit, st);
+  if (a.n * a.group <= 16) return few_rows<T, D, 1, false>(a, sms, fit, st);
   if (paged_umma_ok(a)) return launch_paged_umma(a, Type<T>::kBf16 ? NS_DTYPE_BF16 : NS_DTYPE_F16, D, sms, st);
   return launch<T, D, 4, false>(a, sms, st);
 }

@@ -70,13 +70,13 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
   const Ws ws = workspace(ws_, a.n_seqs, ctas, kRows);
   const long long total = ws.cum[a.n_seqs], cb = ws.cum[b];
   const long long nt = quotient(ws.cum[b + 1] - cb, items);
-  const long long from = cb + item * nt, to = from + nt;  // the item's tiles
+  const long long begin = cb + item * nt, from = begin + R::kCost, to = begin + nt;  // the item's tiles
   const int c0 = (int)quotient((from + 1) * ctas - 1, total), c1 = (int)quotient(to * ctas - 1, total);
   if (c0 == c1) return;  // one CTA had it all
   for (int c = c0 + tid; c <= c1; c += kJoinWarps * 32) {
     const long long first = quotient(total * c, ctas);
     // a part is its CTA's first unless the CTA began before the item; a CTA may have no tiles at all
-    s_part[c - c0] = first == quotient(total * (c + 1), ctas) ? -1 : (c * 2 + (first >= from ? 0 : 1)) * kRows;
+    s_part[c - c0] = first == quotient(total * (c + 1), ctas) ? -1 : (c * 2 + (first >= begin ? 0 : 1)) * kRows;
   }
   __syncthreads();
   int node, qh;

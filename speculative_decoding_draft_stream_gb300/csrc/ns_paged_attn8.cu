@@ -7,7 +7,8 @@ namespace {
 
 template <typename T, int D>
 cudaError_t by_rows(const PagedAttnArgs &a, int sms, const PagedFit &fit, cudaStream_t st) {
-  if (a.n * a.group <= 16) return few_rows<T, D, true>(a, sms, fit, st);
+  if (a.n * a.group <= 8) return few_rows<T, D, 0, true>(a, sms, fit, st);
+  if (a.n * a.group <= 16) return few_rows<T, D, 1, true>(a, sms, fit, st);
   return launch<T, D, 4, true>(a, sms, st);
 }
 template <typename T>

@@ -62,8 +62,8 @@ enum Way { kLine, kSmall, kLarge };
 constexpr int kCluster = 16;  // CTAs of an item: one for each row that it may have
 template <int W>
 constexpr int kThreads = W == kLarge ? 256 : 128;
-template <int W, int WM, bool F8>
-constexpr int kKeys = (W == kLarge ? 128 : 64) * (F8 && WM == 1 ? 2 : 1);  // of a tile
+template <int D, int W, int WM, bool F8>
+constexpr int kKeys = (W == kLarge ? 128 : 64) * (F8 && WM <= 1 ? 2 : 1);  // of a tile
 template <int D, bool F8>
 constexpr int kRowBytes = D * (F8 ? 1 : 2);
 template <int D>
@@ -74,26 +74,38 @@ constexpr int kMerge = 32 * 4 * 4;    // a lane's m, l (and padding), after its 
 
 template <int D, int W, int WM, bool F8>
 __host__ __device__ constexpr int pa_stage() {  // F8: and the exponents of keys and values
-  return 2 * kKeys<W, WM, F8> * (kRowBytes<D, F8> + (F8 ? 1 : 0));
+  return 2 * kKeys<D, W, WM, F8> * (kRowBytes<D, F8> + (F8 ? 1 : 0));
 }
 // Behind the stages: what a warp hands over to warp 0; in a cluster, (m, l)
 // and o of each of its CTAs for the rows that this CTA joins.
 template <int D, int WM, int W, bool F8>
 __host__ __device__ constexpr int pa_smem() {
-  return kStages<D, W, WM, F8> * pa_stage<D, W, WM, F8>() + (W != kLine ? 16 * (D + 2) * 4 : WM == 1 ? 32 * D / 2 * 4 + kMerge : 0);
+  return kStages<D, W, WM, F8> * pa_stage<D, W, WM, F8>() + (W != kLine ? 16 * (D + 2) * 4 : WM <= 1 ? 32 * D / (WM ? 2 : 4) * 4 + kMerge : 0);
 }
 
 // CTAs that an SM is to hold: as many as their shared memory allows (64 rows: their registers).  The line has that
 // many on each SM; its equal shares would end in a second, half empty wave if it had more.
 template <int D, int WM, int W>
-constexpr int kResident = W == kLarge ? (D == 128 ? 1 : 2) : WM == 1 ? kPerSm<D> : (D == 128 ? 2 : 3);
+constexpr int kResident = W == kLarge ? (D == 128 ? 1 : 2) : WM <= 1 ? kPerSm<D> : (D == 128 ? 2 : 3);
+// F8: bytes of where each eight of a tile's rows lies, for each warp.
+template <int D, int W, int WM>
+constexpr int kPlaces = kThreads<W> / 32 * (kKeys<D, W, WM, true> / 8) * 16;
 template <int D, int WM, int W, bool F8>
-constexpr bool kHeld = kResident<D, WM, W> * (pa_smem<D, WM, W, F8>() + 1280) <= 228 * 1024;  // (1 KB: the system's)
+constexpr bool kHeld =
+    kResident<D, WM, W> * (pa_smem<D, WM, W, F8>() + 1280 + (F8 ? kPlaces<D, W, WM> : 0)) <= 228 * 1024;  // (1 KB: the system's)
 template <int D, bool F8>
 constexpr bool kAllHeld = kHeld<D, 1, kLine, F8> && kHeld<D, 4, kLine, F8> && kHeld<D, 1, kSmall, F8> &&
                           kHeld<D, 1, kLarge, F8>;
-static_assert(kAllHeld<128, false> && kAllHeld<64, false> && kAllHeld<128, true> && kAllHeld<64, true>,
+template <int D>
+constexpr bool kHeld8 = kHeld<D, 0, kLine, true> && kHeld<D, 0, kSmall, true> && kHeld<D, 0, kLarge, true>;
+static_assert(kAllHeld<128, false> && kAllHeld<64, false> && kAllHeld<128, true> && kAllHeld<64, true> && kHeld8<128> &&
+                  kHeld8<64>,
               "shared memory of an SM");
+
+// What an item's beginning and end take, in tiles: the line of 8-bit caches has that many more for each item, so that
+// shares are equal in time.
+template <bool F8>
+constexpr int kItemCost = F8 ? 1 : 0;
 
 template <int KEYS>
 __host__ __device__ inline long long pa_tiles(int len) {
@@ -133,22 +145,28 @@ __device__ __forceinline__ void push(uint32_t a, float x) {
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(a), "f"(x) : "memory");
 }
 
-// (Clusters: at most 16 rows.)
+// Rows of a CTA's block: 16 to each of WM warps, or (WM 0, F8) 8 that every warp has, as with WM 1.  (Clusters: at
+// most 16.)
+template <int WM>
+constexpr int kBlockRows = WM == 0 ? 8 : 16 * WM;
 template <typename T, int D, int WM, int W, bool F8>
 __global__ void __launch_bounds__(kThreads<W>, kResident<D, WM, W>)
     paged_attn_kernel(const PagedAttnArgs a, int blocks) {
   using C = std::conditional_t<F8, __half, T>;  // the products' type
-  constexpr int kPaThreads = kThreads<W>, kPaKeys = kKeys<W, WM, F8>, kWarps = kPaThreads / kWarp;
-  constexpr int WK = kWarps / WM, NK = kPaKeys / WK, kRows = 16 * WM;
+  constexpr int kPaThreads = kThreads<W>, kPaKeys = kKeys<D, W, WM, F8>, kWarps = kPaThreads / kWarp;
+  constexpr bool kFew = WM <= 1, k8 = WM == 0;
+  constexpr int WK = kFew ? kWarps : kWarps / WM, NK = kPaKeys / WK, kRows = kBlockRows<WM>;
   constexpr int kRowB = kRowBytes<D, F8>, kStageB = pa_stage<D, W, WM, F8>(), kRing = kStages<D, W, WM, F8>;
   constexpr int kLanesRow = kRowB / 16;               // threads that fetch a row
   constexpr int kPass = kPaThreads / kLanesRow;       // rows a pass of the CTA fetches
-  static_assert(W == kLine || WM == 1, "a cluster has 16 rows");
+  static_assert((W == kLine || kFew) && (!k8 || F8), "a cluster has 16 rows at most");
   constexpr int kCtas = kCluster;
   extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ longlong2 s_places[F8 ? kWarps * kPaKeys / 8 : 1];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int wm = WM == 1 ? 0 : warp, wk = WM == 1 ? warp : 0;
+  const int wm = kFew ? 0 : warp, wk = kFew ? warp : 0;
   const int items = a.kv_heads * blocks, R = a.n * a.group;
+  auto head_of = [&](int item) { return kFew ? item : item / blocks; };  // (few rows are one block)
   const uint32_t s0 = (uint32_t)__cvta_generic_to_shared(smem);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
@@ -168,10 +186,11 @@ __global__ void __launch_bounds__(kThreads<W>, kResident<D, WM, W>)
     static_assert(NS_MAX_ATTEND_SEQS * 8 <= kRing * kStageB, "room for the sequences");
     __shared__ long long s_sum[kPaThreads / kWarp];
     // tiles of the sequences before each one
+    constexpr int kCost = kItemCost<F8>;
     long long total = 0;
     for (int b0 = 0; b0 < a.n_seqs; b0 += kPaThreads) {
       const int b = b0 + tid;
-      const long long mine = b < a.n_seqs ? pa_tiles<kPaKeys>(length(a, b, blockIdx.x == 0 ? a.err : nullptr)) * items : 0;
+      const long long mine = b < a.n_seqs ? (pa_tiles<kPaKeys>(length(a, b, blockIdx.x == 0 ? a.err : nullptr)) + kCost) * items : 0;
       long long sum = mine;
 #pragma unroll
       for (int off = 1; off < kWarp; off <<= 1) {
@@ -196,20 +215,28 @@ __global__ void __launch_bounds__(kThreads<W>, kResident<D, WM, W>)
     t0 = quotient(total * blockIdx.x, gridDim.x), t1 = quotient(total * (blockIdx.x + 1), gridDim.x);
     if (t0 >= t1) return;
 
-    {
-      int lo = 0, hi = a.n_seqs;  // the last sequence that begins at or before t0
+    auto enter_at = [&](long long t) {  // the cursor to place t of the line; the tiles before it
+      int lo = 0, hi = a.n_seqs;        // the last sequence that begins at or before t
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (s_cum[mid] <= t0)
+        if (s_cum[mid] <= t)
           lo = mid;
         else
           hi = mid;
       }
       ld.b = lo;
       ld.enter(a, nullptr);
-      const long long local = t0 - s_cum[lo];
-      ld.item = (int)quotient(local, ld.nt);
-      ld.tile = (int)(local - (long long)ld.item * ld.nt);
+      const long long local = t - s_cum[lo];
+      ld.item = (int)quotient(local, ld.nt + kCost);
+      ld.tile = max(0, (int)(local - (long long)ld.item * (ld.nt + kCost)) - kCost);
+      return s_cum[lo] - (long long)kCost * lo * items + (long long)ld.item * ld.nt + ld.tile;
+    };
+    if (kCost) {  // from places of the line to tiles
+      t1 = t1 == total ? total - (long long)kCost * a.n_seqs * items : enter_at(t1);
+      t0 = enter_at(t0);
+      if (t0 >= t1) return;
+    } else {
+      enter_at(t0);
     }
     __syncthreads();  // everyone is done with s_cum before the first tile comes
   }
@@ -239,8 +266,45 @@ __global__ void __launch_bounds__(kThreads<W>, kResident<D, WM, W>)
   const E *vbase = static_cast<const E *>(a.v) + (fr & 7) * a.v_token + fc * (16 / sizeof(E));
   const uint32_t to = F8 ? piece8<D>(fr, fc) : piece<D>(fr, fc);
   auto fetch = [&](int id, int stage) {
+    if constexpr (F8) {
+      // A lane finds an eight's places (products of 32 bits), which the warp then reads from shared memory.
+      const uint32_t sk = s0 + stage * kStageB + to, sv = sk + kPaKeys * kRowB;
+      const int p0 = ld.tile * kPaKeys, left = ld.len - p0, head = head_of(ld.item);
+      const uint32_t there = __ballot_sync(0xffffffffu, id >= 0);
+      longlong2 *mine = s_places + warp * (kPaKeys / 8);
+      if (lane < kPaKeys / 8) {
+        const int page = max(0, id), row = (p0 + lane * 8) & pmask;
+        mine[lane] = make_longlong2(16 * ((int64_t)page * a.kp16 + (int64_t)row * a.kt16),
+                                    16 * ((int64_t)page * a.vp16 + (int64_t)row * a.vt16));
+        if (warp < 2)  // its exponents: warp 0 the keys', warp 1 the values'
+          cp8(s0 + stage * kStageB + 2 * kPaKeys * kRowB + warp * kPaKeys + lane * 8,
+              warp ? a.v_exp + head * a.ve_head + 8 * ((int64_t)page * a.vep8) + row
+                   : a.k_exp + head * a.ke_head + 8 * ((int64_t)page * a.kep8) + row,
+              id >= 0);
+      }
+      __syncwarp();
+      const char *kh = reinterpret_cast<const char *>(kbase) + head * a.k_head;
+      const char *vh = reinterpret_cast<const char *>(vbase) + head * a.v_head;
+      auto rows_of = [&](auto whole) {
+#pragma unroll
+        for (int pass = 0; pass < kPaKeys / kPass; ++pass) {
+          const int r = pass * kPass + fr, eight = r >> 3;
+          const longlong2 at = mine[eight];
+          const bool ok = whole.value || (r < left && (there >> eight & 1));
+          cp16(sk + pass * kPass * kRowB, kh + at.x, ok);
+          cp16(sv + pass * kPass * kRowB, vh + at.y, ok);
+        }
+      };
+      constexpr uint32_t kAll = kPaKeys == 256 ? 0xffffffffu : (1u << (kPaKeys / 8 % 32)) - 1;
+      if (left >= kPaKeys && (there & kAll) == kAll)
+        rows_of(std::true_type{});
+      else
+        rows_of(std::false_type{});
+      __syncwarp();  // (the places are written again for the next tile)
+      return;
+    }
     const uint32_t sk = s0 + stage * kStageB + to, sv = sk + kPaKeys * kRowB;
-    const int left = ld.len - ld.tile * kPaKeys, head = ld.item / blocks;
+    const int left = ld.len - ld.tile * kPaKeys, head = head_of(ld.item);
     const int64_t page = id >= 0 ? id : 0, row = (ld.tile * kPaKeys + lane * 8) & pmask;
     const int64_t ko = page * a.k_page + head * a.k_head + row * a.k_token;
     const int64_t vo = page * a.v_page + head * a.v_head + row * a.v_token;
@@ -253,11 +317,6 @@ __global__ void __launch_bounds__(kThreads<W>, kResident<D, WM, W>)
       cp16(sk + pass * kPass * kRowB, kbase + k, ok);
       cp16(sv + pass * kPass * kRowB, vbase + v, ok);
     }
-    if (F8 && warp < 2 && lane < kPaKeys / 8)  // eight rows' exponents: warp 0 the keys', warp 1 the values'
-      cp8(s0 + stage * kStageB + 2 * kPaKeys * kRowB + warp * kPaKeys + lane * 8,
-          warp ? a.v_exp + page * a.ve_page + head * a.ve_head + row
-               : a.k_exp + page * a.ke_page + head * a.ke_head + row,
-          id >= 0);
   };
 
   const float c = a.scale * kLog2e;
@@ -285,48 +344,60 @@ __global__ void __launch_bounds__(kThreads<W>, kResident<D, WM, W>)
 #pragma unroll
   for (int i = 0; i < kAhead; ++i) issue();
 
-  Rows<C, D> rows;
+  std::conditional_t<k8, Rows8<C, D>, Rows<C, D>> rows;
   if (W != kLine) rows.clear();  // (a CTA of a short sequence may have no tile)
-  uint32_t q[D / 16][4];
+  uint32_t q[D / 16][k8 ? 2 : 4];
   float cq[2] = {c, c};  // of each row's scores (F8: with the power of two that its query was divided by)
   uint64_t word[2] = {0, 0};
   int st = 0;
   long long seg0 = t0;  // where the current item's share of this CTA begins
   for (long long g = t0; g < t1; ++g) {
-    const int head = cu.item / blocks, rb = cu.item % blocks;
+    const int head = head_of(cu.item), rb = kFew ? 0 : cu.item % blocks;
     if (g == t0 || cu.tile == 0) {  // a new item: its queries and masks
       seg0 = g;
       rows.clear();
       const T *qs = static_cast<const T *>(a.q) + (int64_t)cu.b * a.q_seq;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int r = rb * kRows + wm * 16 + (lane >> 2) + 8 * h;
-        const int node = r / a.group, qh = head * a.group + r % a.group;
+        const int r = rb * kRows + wm * 16 + rows.row(h), node = r / a.group;
         word[h] = 0;
         if (r < R) {
           word[h] = a.mask ? (uint64_t)a.mask[(int64_t)cu.b * a.n + node] : ~0ull >> (63 - node);
         }
+      }
+      constexpr int kParts = k8 ? 2 : 4;  // words of a product's operand
+#pragma unroll
+      for (int h = 0; h < (k8 ? 1 : 2); ++h) {
+        const int r = rb * kRows + wm * 16 + (lane >> 2) + 8 * h;
+        const int node = r / a.group, qh = head * a.group + r % a.group;
         const T *src = qs + (int64_t)node * a.q_token + (int64_t)qh * a.q_head + (lane & 3) * (F8 ? D / 4 : 2);
         constexpr int kStep = F8 ? 4 : 16, kHalf = F8 ? 2 : 8;  // columns of a product, of its halves
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           q[kk][h] = r < R ? *reinterpret_cast<const uint32_t *>(src + kk * kStep) : 0u;
-          q[kk][2 + h] = r < R ? *reinterpret_cast<const uint32_t *>(src + kk * kStep + kHalf) : 0u;
+          q[kk][kParts / 2 + h] = r < R ? *reinterpret_cast<const uint32_t *>(src + kk * kStep + kHalf) : 0u;
         }
         if constexpr (F8 && !std::is_same_v<T, __half>) {  // bf16 -> fp16, the largest to 1 .. 2
           uint32_t most = 0;
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk)
-            most = __vimax3_u16x2(most, q[kk][h] & 0x7fff7fffu, q[kk][2 + h] & 0x7fff7fffu);
+            most = __vimax3_u16x2(most, q[kk][h] & 0x7fff7fffu, q[kk][kParts / 2 + h] & 0x7fff7fffu);
           most = __vmaxu2(most, __shfl_xor_sync(0xffffffffu, most, 1));
           most = __vmaxu2(most, __shfl_xor_sync(0xffffffffu, most, 2));
           const int e = min(max((int)(max(most & 0xffffu, most >> 16) >> 7) - 127, -126), 126);
           const float f = __uint_as_float((uint32_t)(127 - e) << 23);
-          cq[h] = c * __uint_as_float((uint32_t)(127 + e) << 23);
+          const float back = c * __uint_as_float((uint32_t)(127 + e) << 23);
+          if constexpr (k8) {  // (row g's lanes have it, rows 2 t and 2 t + 1 want it)
+            cq[0] = __shfl_sync(0xffffffffu, back, (lane & 3) * 8);
+            cq[1] = __shfl_sync(0xffffffffu, back, (lane & 3) * 8 + 4);
+          } else {
+            cq[h] = back;
+          }
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
-            const float2 x = Type<T>::unpack(q[kk][h]), y = Type<T>::unpack(q[kk][2 + h]);
-            q[kk][h] = Type<C>::pack(x.x * f, x.y * f), q[kk][2 + h] = Type<C>::pack(y.x * f, y.y * f);
+            uint32_t &lo = q[kk][h], &hi = q[kk][kParts / 2 + h];
+            const float2 x = Type<T>::unpack(lo), y = Type<T>::unpack(hi);
+            lo = Type<C>::pack(x.x * f, x.y * f), hi = Type<C>::pack(y.x * f, y.y * f);
           }
         }
       }
@@ -365,13 +436,14 @@ __global__ void __launch_bounds__(kThreads<W>, kResident<D, WM, W>)
     if (ends || g + 1 == t1) {
       rows.sum_l();
       if (W != kLine) break;
-      if (WM == 1) {  // the warps' keys join, in warp order, in warp 0
+      if (kFew) {  // the warps' keys join, in warp order, in warp 0
         float4 *bo = reinterpret_cast<float4 *>(smem + kRing * kStageB);
-        float4 *bm = bo + (D / 8) * 32;
+        constexpr int kParts = decltype(rows)::kParts;
+        float4 *bm = bo + kParts * 32;
         for (int w = 1; w < 4; ++w) {
           if (warp == w) {
 #pragma unroll
-            for (int i = 0; i < D / 8; ++i)
+            for (int i = 0; i < kParts; ++i)
               bo[i * 32 + lane] = make_float4(rows.o[i][0], rows.o[i][1], rows.o[i][2], rows.o[i][3]);
             bm[lane] = make_float4(rows.m[0], rows.m[1], rows.l[0], rows.l[1]);
           }
@@ -389,23 +461,23 @@ __global__ void __launch_bounds__(kThreads<W>, kResident<D, WM, W>)
               rows.l[h] = rows.l[h] * fa[h] + ol[h] * fb[h];
             }
 #pragma unroll
-            for (int i = 0; i < D / 8; ++i) {
+            for (int i = 0; i < kParts; ++i) {
               const float4 y = bo[i * 32 + lane];
               rows.o[i][0] = rows.o[i][0] * fa[0] + y.x * fb[0];
-              rows.o[i][1] = rows.o[i][1] * fa[0] + y.y * fb[0];
-              rows.o[i][2] = rows.o[i][2] * fa[1] + y.z * fb[1];
+              rows.o[i][1] = rows.o[i][1] * fa[rows.of(1)] + y.y * fb[rows.of(1)];
+              rows.o[i][2] = rows.o[i][2] * fa[rows.of(2)] + y.z * fb[rows.of(2)];
               rows.o[i][3] = rows.o[i][3] * fa[1] + y.w * fb[1];
             }
           }
           __syncthreads();
         }
       }
-      if (WM > 1 || warp == 0) {
+      if (!kFew || warp == 0) {
         const bool whole = ends && g + 1 - seg0 == cu.nt;
         const int slot = seg0 == t0 ? 0 : 1;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const int rl = wm * 16 + (lane >> 2) + 8 * h, r = rb * kRows + rl;
+          const int rl = wm * 16 + rows.row(h), r = rb * kRows + rl;
           if (r < R) {
             if (whole) {
               const int64_t at = ((int64_t)cu.b * a.n + r / a.group) * a.q_heads + head * a.group + r % a.group;
@@ -414,13 +486,13 @@ __global__ void __launch_bounds__(kThreads<W>, kResident<D, WM, W>)
               rows.template columns<F8>(h, [&](int d, float x, float y) {
                 *reinterpret_cast<uint32_t *>(dst + d) = Type<T>::pack(x * inv, y * inv);
               });
-              if (a.lse && (lane & 3) == 0) a.lse[at] = row_lse<C>(rows.m[h], rows.l[h]);
+              if (a.lse && rows.first()) a.lse[at] = row_lse<C>(rows.m[h], rows.l[h]);
             } else {
               const size_t at = ((size_t)blockIdx.x * 2 + slot) * kRows + rl;
               float *dst = ws.o + at * D;
               rows.template columns<F8>(
                   h, [&](int d, float x, float y) { *reinterpret_cast<float2 *>(dst + d) = make_float2(x, y); });
-              if ((lane & 3) == 0) ws.ml[at] = make_float2(rows.m[h], rows.l[h]);
+              if (rows.first()) ws.ml[at] = make_float2(rows.m[h], rows.l[h]);
             }
           }
         }
@@ -440,12 +512,12 @@ __global__ void __launch_bounds__(kThreads<W>, kResident<D, WM, W>)
     __syncthreads();  // (every tile has been waited for and used)
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int r = (lane >> 2) + 8 * h;
+      const int r = rows.row(h);
       if (r < R) {
         float *dst = w_o + (warp * 16 + r) * kPitch;
         rows.template columns<F8>(
             h, [&](int d, float x, float y) { *reinterpret_cast<float2 *>(dst + d) = make_float2(x, y); });
-        if ((lane & 3) == 0) w_ml[warp * 16 + r] = make_float2(rows.m[h], rows.l[h]);
+        if (rows.first()) w_ml[warp * 16 + r] = make_float2(rows.m[h], rows.l[h]);
       }
     }
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");  // every CTA of the cluster has begun
@@ -496,8 +568,8 @@ __global__ void __launch_bounds__(kThreads<W>, kResident<D, WM, W>)
 template <int WM, bool F8>
 struct Rows16 {
   int blocks;
-  static constexpr int kRows = 16 * WM;
-  static constexpr int kGroups = WM == 1 ? 4 : 1;  // few rows may have hundreds of parts, many rows have two or three
+  static constexpr int kRows = kBlockRows<WM>, kCost = kItemCost<F8>;
+  static constexpr int kGroups = WM <= 1 ? 4 : 1;  // few rows may have hundreds of parts, many rows have two or three
   template <typename T>
   __device__ __forceinline__ float offset() const {
     return F8 ? Type<__half>::kOffset : Type<T>::kOffset;
@@ -511,10 +583,10 @@ struct Rows16 {
 
 template <typename T, int D, int WM, bool F8>
 cudaError_t launch(const PagedAttnArgs &a, int sms, cudaStream_t st) {
-  constexpr int kRows = 16 * WM;
+  constexpr int kRows = kBlockRows<WM>;
   const int blocks = (a.n * a.group + kRows - 1) / kRows;
-  constexpr int kCtas = kResident<D, WM, kLine>;
-  const long long most = pa_tiles<kKeys<kLine, WM, F8>>(a.max_len) * a.n_seqs * a.kv_heads * blocks;
+  constexpr int kCtas = kResident<D, WM, kLine>;  // (on an SM)
+  const long long most = pa_tiles<kKeys<D, kLine, WM, F8>>(a.max_len) * a.n_seqs * a.kv_heads * blocks;
   const int ctas = (int)(most < (long long)kCtas * sms ? most : kCtas * sms);
   paged_attn_kernel<T, D, WM, kLine, F8><<<ctas, kThreads<kLine>, pa_smem<D, WM, kLine, F8>(), st>>>(a, blocks);
   cudaError_t e = cudaGetLastError();
@@ -539,26 +611,26 @@ struct ClusterLaunch {
   }
 };
 // Clusters that the device holds at once.
-template <typename T, int D, int W, bool F8, typename Fit>
+template <typename T, int D, int WM, int W, bool F8, typename Fit>
 auto &resident(Fit &fit) {
-  return fit.clusters[F8][Type<T>::kBf16 ? NS_DTYPE_BF16 : NS_DTYPE_F16][D == 128][W == kLarge];
+  return fit.clusters[F8 ? 2 - WM : 0][Type<T>::kBf16 ? NS_DTYPE_BF16 : NS_DTYPE_F16][D == 128][W == kLarge];
 }
 
 // Whether each item can have its own cluster with up to kMostTiles tiles to a
 // CTA (in two waves of small CTAs: with one or two tiles).
 template <int D>
 constexpr int kMostTiles = D == 128 ? 12 : 16;
-template <typename T, int D, int W, bool F8>
+template <typename T, int D, int WM, int W, bool F8>
 bool clusters_fit(const PagedAttnArgs &a, const PagedFit &fit) {
-  constexpr int kTile = kKeys<W, 1, F8>;
+  constexpr int kTile = kKeys<D, W, WM, F8>;
   const bool two_waves = W == kSmall && a.max_len > kCluster * kTile / 2 && a.max_len <= 2 * kCluster * kTile;
-  return (long long)a.n_seqs * a.kv_heads <= (two_waves ? 2 : 1) * resident<T, D, W, F8>(fit) &&
+  return (long long)a.n_seqs * a.kv_heads <= (two_waves ? 2 : 1) * resident<T, D, WM, W, F8>(fit) &&
          a.max_len <= kMostTiles<D> * kCluster * kTile;
 }
-template <typename T, int D, int W, bool F8>
+template <typename T, int D, int WM, int W, bool F8>
 cudaError_t launch_clusters(const PagedAttnArgs &a, cudaStream_t st) {
-  ClusterLaunch l(a.n_seqs * a.kv_heads, kThreads<W>, pa_smem<D, 1, W, F8>(), st);
-  return cudaLaunchKernelEx(&l.cfg, paged_attn_kernel<T, D, 1, W, F8>, a, 1);
+  ClusterLaunch l(a.n_seqs * a.kv_heads, kThreads<W>, pa_smem<D, WM, W, F8>(), st);
+  return cudaLaunchKernelEx(&l.cfg, paged_attn_kernel<T, D, WM, W, F8>, a, 1);
 }
 
 template <typename T, int D, int WM, int W, bool F8>
@@ -569,8 +641,8 @@ cudaError_t prepare(PagedFit *fit) {
   if (W == kLine) return e;
   if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e != cudaSuccess) return e;
-  ClusterLaunch l(64, kThreads<W>, pa_smem<D, 1, W, F8>(), nullptr);
-  return cudaOccupancyMaxActiveClusters(&resident<T, D, W, F8>(*fit), kernel, &l.cfg);
+  ClusterLaunch l(64, kThreads<W>, pa_smem<D, WM, W, F8>(), nullptr);
+  return cudaOccupancyMaxActiveClusters(&resident<T, D, WM, W, F8>(*fit), kernel, &l.cfg);
 }
 template <typename T, int D, bool F8>
 cudaError_t prepare_all(PagedFit *fit) {
@@ -578,16 +650,21 @@ cudaError_t prepare_all(PagedFit *fit) {
   if (e == cudaSuccess) e = prepare<T, D, 4, kLine, F8>(fit);
   if (e == cudaSuccess) e = prepare<T, D, 1, kSmall, F8>(fit);
   if (e == cudaSuccess) e = prepare<T, D, 1, kLarge, F8>(fit);
+  if constexpr (F8) {
+    if (e == cudaSuccess) e = prepare<T, D, 0, kLine, F8>(fit);
+    if (e == cudaSuccess) e = prepare<T, D, 0, kSmall, F8>(fit);
+    if (e == cudaSuccess) e = prepare<T, D, 0, kLarge, F8>(fit);
+  }
   return e;
 }
 
 // At most 16 rows (by_rows in ns_paged_attn.cu has the rule).
-template <typename T, int D, bool F8>
+template <typename T, int D, int WM, bool F8>
 cudaError_t few_rows(const PagedAttnArgs &a, int sms, const PagedFit &fit, cudaStream_t st) {
-  if (a.max_len > kCluster * kKeys<kSmall, 1, F8> && clusters_fit<T, D, kLarge, F8>(a, fit))
-    return launch_clusters<T, D, kLarge, F8>(a, st);
-  if (clusters_fit<T, D, kSmall, F8>(a, fit)) return launch_clusters<T, D, kSmall, F8>(a, st);
-  return launch<T, D, 1, F8>(a, sms, st);
+  if (a.max_len > kCluster * kKeys<D, kSmall, WM, F8> && clusters_fit<T, D, WM, kLarge, F8>(a, fit))
+    return launch_clusters<T, D, WM, kLarge, F8>(a, st);
+  if (clusters_fit<T, D, WM, kSmall, F8>(a, fit)) return launch_clusters<T, D, WM, kSmall, F8>(a, st);
+  return launch<T, D, WM, F8>(a, sms, st);
 }
 
 }  // namespace

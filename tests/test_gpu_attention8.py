@@ -263,22 +263,21 @@ def test_bad_pages_and_sequences(ns, n):
     k, v = (torch.randn(450, 2, 64, generator=g, device="cuda").to(BF16) for _ in range(2))
     cu = torch.tensor([0, 150, 300, 450], dtype=torch.int32, device="cuda")
     cache.write(0, seqs, cu, k, v)
-    want, wl = cache.attend(0, q, seqs)
     cache.table[1, 2] = 40
     cache.table[1, 4] = -5
     out, lse = cache.attend(0, q, torch.tensor([0, 1, 7], dtype=torch.int32, device="cuda"))
     assert ns.ops_error(clear=True) == ns.FLAG_BAD_ID | ns.FLAG_BAD_SEQ
-    assert torch.equal(out[0], want[0]) and torch.equal(lse[0], wl[0])
     assert (out[2] == 0).all() and (lse[2] == -float("inf")).all()
-    kk, vv = cache.read(0, seqs[:1], cu[:2], 150)  # (rows of the sequence that is whole: just a call)
-    kk, vv = (values(*quantise(t[150:300].cpu())) for t in (k, v))
-    seen = torch.ones(n, 150, dtype=torch.bool)
-    seen[:, 150 - n:] = torch.ones(n, n, dtype=torch.bool).tril()
-    seen[:, 32:48] = seen[:, 64:80] = False
-    for h in range(8):
-        o, z, to, tz = attend_rows(q[1, :, h].cpu(), kk[:, h // 4], vv[:, h // 4], seen, 0.125)
-        check(out[1, :, h], o, to * 1.01, "out")
-        check(lse[1, :, h], z, tz + 1e-5, "lse")
+    for b in range(2):
+        kk, vv = (values(*quantise(t[150 * b:150 * (b + 1)].cpu())) for t in (k, v))
+        seen = torch.ones(n, 150, dtype=torch.bool)
+        seen[:, 150 - n:] = torch.ones(n, n, dtype=torch.bool).tril()
+        if b == 1:
+            seen[:, 32:48] = seen[:, 64:80] = False
+        for h in range(8):
+            o, z, to, tz = attend_rows(q[b, :, h].cpu(), kk[:, h // 4], vv[:, h // 4], seen, 0.125)
+            check(out[b, :, h], o, to * 1.01, "out")
+            check(lse[b, :, h], z, tz + 1e-5, "lse")
 
 
 def test_same_bits_again_and_in_a_graph(ns):
