@@ -27,8 +27,9 @@ LIB_NAME = "libnanospec.so"
 LIB_PATH = os.path.join(PKG_DIR, LIB_NAME)
 BINDING_PATH = os.path.join(PKG_DIR, "_serving.so")
 SOURCES = ["ns_api.cu", "ns_state.cu", "ns_topk.cu", "ns_noalloc.cu", "ns_umma.cu", "ns_slots.cu", "ns_step.cu",
-           "ns_dense.cu", "ns_pages.cu", "ns_rotate.cu", "ns_logprobs.cu", "ns_paged_attn.cu", "ns_paged_attn8.cu", "ns_paged_umma.cu", "ns_shared_attn.cu", "ns_prompt_attn.cu",
-           "ns_ops_api.cu"]
+           "ns_dense.cu", "ns_pages.cu", "ns_rotate.cu", "ns_logprobs.cu", "ns_paged_attn.cu", "ns_paged_attn8.cu",
+           "ns_paged_umma.cu", "ns_paged_umma8.cu", "ns_shared_attn.cu", "ns_shared_attn8.cu",
+           "ns_prompt_attn.cu", "ns_ops_api.cu"]
 BINDING = "ns_binding.cpp"
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH_FLAGS + [

@@ -337,14 +337,16 @@ struct Rows {
     // A lane turns one key's two exponents into factors (NK > 32: one of each 32), and the others ask it.
     float top[2] = {kNegInf, kNegInf};
     float unit[NK / 8][2];  // 2^-ve
+    uint32_t bad[(NK + 31) / 32];  // keys whose value is NaN
 #pragma unroll
     for (int b0 = 0; b0 < NK; b0 += 32) {
       const int at = k0 + b0 + (NK < 32 ? lane & (NK - 1) : lane);
-      const uint32_t bk = lds1(sKe + at), bv = lds1(sVe + at);
+      const uint32_t bk = lds1(sKe + at), byte = lds1(sVe + at), bv = byte == 255u ? 127u : byte;
+      bad[b0 / 32] = __ballot_sync(0xffffffffu, byte == 255u);
       const float f = __uint_as_float(bk << 23);  // (255: infinity, and NaN with what is added)
-      // the byte as a number, less 127; NaN where either is 255
-      const float add = max(bk, bv) == 255u ? __uint_as_float(0x7fffffffu) : __uint_as_float(0x4b000000u | bv) - 8388735.f;
-      const float u = __uint_as_float((254u - min(bv, 254u)) << 23);  // (finite: a hidden key's p is 0)
+      // the value's byte as a number, less 127; NaN where the key's is 255
+      const float add = bk == 255u ? __uint_as_float(0x7fffffffu) : __uint_as_float(0x4b000000u | bv) - 8388735.f;
+      const float u = __uint_as_float((254u - bv) << 23);
 #pragma unroll
       for (int i = b0 / 8; i < (b0 + 32 < NK ? b0 + 32 : NK) / 8; ++i)
 #pragma unroll
@@ -381,6 +383,18 @@ struct Rows {
         s[i][j] = ex2(s[i][j] + shift[j >> 1]);
         add[j >> 1] = fmaf(s[i][j], unit[i][j & 1], add[j >> 1]);
       }
+    uint32_t any_bad = 0;
+#pragma unroll
+    for (int b = 0; b < (NK + 31) / 32; ++b) any_bad |= bad[b];
+    if (any_bad) {  // (after l: a value is no part of it)
+#pragma unroll
+      for (int i = 0; i < NK / 8; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int key = i * 8 + 2 * t + (j & 1);
+          if ((bad[key / 32] >> (key % 32) & 1) && !(kMasked && hidden(j >> 1, key))) s[i][j] = __uint_as_float(0x7fffffffu);
+        }
+    }
 #pragma unroll
     for (int h = 0; h < 2; ++h) l[h] = l[h] * p2[h] + add[h];
     if (__any_sync(0xffffffffu, grows)) {
@@ -525,16 +539,17 @@ struct Rows8 {
       }
     }
     float top[2] = {kNegInf, kNegInf}, unit[B][2];
+    uint32_t bad = 0;  // keys of this lane whose value is NaN
 #pragma unroll
     for (int i = 0; i < B; ++i)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int key = i * 16 + e * 8 + g;
-        const uint32_t bk = lds1(sKe + k0 + key), bv = lds1(sVe + k0 + key);
+        const uint32_t bk = lds1(sKe + k0 + key), byte = lds1(sVe + k0 + key), bv = byte == 255u ? 127u : byte;
+        bad |= (byte == 255u ? 1u : 0u) << (2 * i + e);
         const float f = __uint_as_float(bk << 23);  // (255: infinity, and NaN with what is added)
-        const float add =
-            max(bk, bv) == 255u ? __uint_as_float(0x7fffffffu) : __uint_as_float(0x4b000000u | bv) - 8388735.f;
-        unit[i][e] = __uint_as_float((254u - min(bv, 254u)) << 23);  // (finite: a hidden key's p is 0)
+        const float add = bk == 255u ? __uint_as_float(0x7fffffffu) : __uint_as_float(0x4b000000u | bv) - 8388735.f;
+        unit[i][e] = __uint_as_float((254u - bv) << 23);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           float &x = s[i][2 * e + h];
@@ -563,6 +578,14 @@ struct Rows8 {
         s[i][j] = ex2(s[i][j] + shift[j & 1]);
         add[j & 1] = fmaf(s[i][j], unit[i][j >> 1], add[j & 1]);
       }
+    if (bad) {  // (after l: a value is no part of it)
+#pragma unroll
+      for (int i = 0; i < B; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if ((bad >> (2 * i + (j >> 1)) & 1) && !(kMasked && hidden(j & 1, i * 16 + (j >> 1) * 8 + g)))
+            s[i][j] = __uint_as_float(0x7fffffffu);
+    }
 #pragma unroll
     for (int h = 0; h < 2; ++h) l[h] = l[h] * p2[h] + add[h];
     if (__any_sync(0xffffffffu, grows)) {

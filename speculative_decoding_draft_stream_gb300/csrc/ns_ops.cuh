@@ -100,12 +100,20 @@ cudaError_t launch_paged_attn8(const PagedAttnArgs &a, int dtype, int dim, int s
 bool paged_umma_ok(const PagedAttnArgs &a);
 cudaError_t prepare_paged_umma();
 cudaError_t launch_paged_umma(const PagedAttnArgs &a, int dtype, int dim, int sms, cudaStream_t st);
+// and over a cache of 8 bits (ns_paged_umma8.cu).
+bool paged_umma8_ok(const PagedAttnArgs &a);
+cudaError_t prepare_paged_umma8();
+cudaError_t launch_paged_umma8(const PagedAttnArgs &a, int dtype, int dim, int sms, cudaStream_t st);
 
-// The same for groups of sequences that begin with the same pages (ns_shared_attn.cu).
+// The same for groups of sequences that begin with the same pages (ns_shared_attn.cuh).
 int64_t shared_attn_ws(int n_seqs, int n_groups, int n, int q_heads, int kv_heads, int dim, int sms);
 cudaError_t prepare_shared_attn();
 cudaError_t launch_shared_attn(const PagedAttnArgs &a, const int32_t *groups, int n_groups, int dtype, int dim,
                                int sms, cudaStream_t st);
+// and over a cache of 8 bits (ns_shared_attn8.cu).
+cudaError_t prepare_shared_attn8();
+cudaError_t launch_shared_attn8(const PagedAttnArgs &a, const int32_t *groups, int n_groups, int dtype, int dim,
+                                int sms, cudaStream_t st);
 
 // Attention over whole prompts (ns_prompt_attn.cu).
 struct PromptAttnArgs {

@@ -9,6 +9,7 @@ template <typename T, int D>
 cudaError_t by_rows(const PagedAttnArgs &a, int sms, const PagedFit &fit, cudaStream_t st) {
   if (a.n * a.group <= 8) return few_rows<T, D, 0, true>(a, sms, fit, st);
   if (a.n * a.group <= 16) return few_rows<T, D, 1, true>(a, sms, fit, st);
+  if (paged_umma8_ok(a)) return launch_paged_umma8(a, Type<T>::kBf16 ? NS_DTYPE_BF16 : NS_DTYPE_F16, D, sms, st);
   return launch<T, D, 4, true>(a, sms, st);
 }
 template <typename T>
@@ -23,7 +24,7 @@ cudaError_t prepare_paged_attn8(PagedFit *fit) {
   if (e == cudaSuccess) e = prepare_all<__nv_bfloat16, 64, true>(fit);
   if (e == cudaSuccess) e = prepare_all<__half, 128, true>(fit);
   if (e == cudaSuccess) e = prepare_all<__half, 64, true>(fit);
-  return e;
+  return e == cudaSuccess ? prepare_paged_umma8() : e;
 }
 
 cudaError_t launch_paged_attn8(const PagedAttnArgs &a, int dtype, int dim, int sms, const PagedFit &fit,

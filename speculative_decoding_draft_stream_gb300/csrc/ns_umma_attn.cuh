@@ -48,7 +48,8 @@
 //   two row tiles, and hidden: the first that some row does not see whole),
 //   Dealer, Loader, Row, Wild; kParts: items may be split, and a part's rows lie
 //   where part() says (kLiveParts: only rows that there are), for a join; kWhole:
-//   items that are not split are written out.
+//   items that are not split are written out; kCodes: keys and values are of 8
+//   bits, and four more warps (Converter) make 16 of them.
 // kSplit: an item is one row tile, and row tile 1 the same rows again with
 // every other tile of keys; row tile 0's threads add the two up.
 //
@@ -77,15 +78,21 @@ using attn::Type;
 using attn::ex2;
 using attn::kNegInf;
 
-constexpr int kThreads = 384;
+constexpr int kThreads = 384;          // (M::kCodes: and four warps that convert)
+template <typename M>
+constexpr int kThreadsOf = M::kCodes ? kThreads + 128 : kThreads;
 constexpr int kRing = 4;             // key or value tiles in flight: keys in the even places
 static_assert(kRing % 2 == 0, "keys and values take turns");
 constexpr int kKeys = 128;           // keys of a tile
 constexpr int kHalf = 128 * 128;     // bytes of 128 rows of 64 elements
 constexpr float kLimit = 32768.f;    // a sum of 64 probabilities above this says that m is too low
+// bf16 probabilities have fp32's range, so m may stay lower (M::kHigh; sums of values up to 2^97 still fit fp32): where
+// keys are of very different sizes the limit above is passed in every few tiles, at 2 to 4 us each.
+template <typename T, typename M>
+constexpr float kLimitOf = M::kHigh && Type<T>::kBf16 ? 1073741824.f : kLimit;
 constexpr int kChecks = 4;           // value tiles looked through ahead of the product
 constexpr int kMissingTiles = 4;     // key tiles whose missing keys are kept (see there)
-constexpr int kWorkReaders = 11;     // loads, products, hidden values, and the eight softmax warps
+constexpr int kWorkReaders = 11;     // loads, products, hidden values, and the eight softmax warps (M::kCodes: and four)
 constexpr int kWorkBytes = 48;
 
 template <typename T>
@@ -104,7 +111,13 @@ struct Smem {
                        kMerge = kCheck + 8 * kChecks, kWFull = kMerge + 16, kWEmpty = kWFull + 16, kSlot = kWEmpty + 16, kWork = kSlot + 16,
                        kWildAny = kWork + 2 * kWorkBytes, kMissing = kWildAny + 16,
                        kWild = kMissing + 4 * kMissingTiles,
-                       kEnd = kWild + 2 * (int)sizeof(typename M::Wild);
+                       kRawFull = kWild + 2 * (int)sizeof(typename M::Wild),  // (M::kCodes)
+                       kRaw = (kRawFull + 8 * kRing + 127) / 128 * 128,
+                       kEnd = M::kCodes ? kRaw + (D == 64 ? kRing * 64 * kKeys : 0) : kRawFull;
+  // M::kCodes: where the codes of ring slot s come to
+  static __device__ __forceinline__ uint32_t raw(uint32_t base, int s) {
+    return D == 64 ? base + kRaw + s * 64 * kKeys : base + kKV + s * kTile + kHalf;
+  }
   static constexpr int kBytes = kEnd + 1024;  // the base is rounded up to 1024 bytes
   static_assert(kBytes <= 232448, "shared memory of a CTA");
 };
@@ -143,7 +156,7 @@ __device__ __forceinline__ int value_at(int r, int d) {
   }
 
 template <typename T, int D, typename M>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreadsOf<M>, 1)
     attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                        const __grid_constant__ CUtensorMap tmV, const __grid_constant__ typename M::Args a) {
   using L = Smem<D, M>;
@@ -159,7 +172,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (tid == 0) {
     for (int s = 0; s < kRing; ++s) {
-      mbar_init(base + L::kKvFull + 8 * s, 1);
+      mbar_init(base + L::kKvFull + 8 * s, M::kCodes ? 4 : 1);
+      if (M::kCodes) mbar_init(base + L::kRawFull + 8 * s, 1);
       mbar_init(base + L::kKvEmpty + 8 * s, 1 + (s & 1));  // the products; values: and the check
     }
     mbar_init(base + L::kQFull, 1);
@@ -172,7 +186,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(base + L::kOFull + 8 * i, 1);
       mbar_init(base + L::kOEmpty + 8 * i, 128);
       mbar_init(base + L::kWFull + 8 * i, 1);
-      mbar_init(base + L::kWEmpty + 8 * i, kWorkReaders);
+      mbar_init(base + L::kWEmpty + 8 * i, kWorkReaders + (M::kCodes ? 4 : 0));
     }
     mbar_init(base + L::kMerge, 128);
     for (int i = 0; i < kChecks; ++i) mbar_init(base + L::kCheck + 8 * i, 1);
@@ -188,9 +202,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *reinterpret_cast<uint32_t *>(g + L::kSlot);
   if (M::kParts) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join waits for this grid
 
-  // registers: 128 threads x 88 + 256 x 208 = 384 x 168, the launch's own
-  if (warp < 4)
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+  // registers: 128 threads x 88 + 256 x 208 = 384 x 168, or 256 x 72 + 256 x 184 = 512 x 128, the launch's own
+  if (warp < 4) {
+    if constexpr (M::kCodes)
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    else
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+  }
   if (warp == 0) {  // loads
     Work w;
     typename M::Loader loader;
@@ -200,6 +218,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // tile x + 3 (x + 4) is loaded after those are over: a word is not written again before it was read.
     static_assert(!M::kParts || kMissingTiles > kRing / 2, "the words outlive their tiles");
     uint32_t *missing = reinterpret_cast<uint32_t *>(g + L::kMissing);
+    constexpr int kFull = M::kCodes ? L::kRawFull : L::kKvFull;  // what a tile's bytes complete
     bool ok = true;
     auto wait = [&](uint32_t bar, int phase) {
       return __all_sync(0xffffffffu, umma::inline_wait(base + bar, phase & 1, err));
@@ -223,14 +242,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int kv = 0; kv < 2; ++kv, ++it) {
           const int s = it % kRing;
           if (it >= kRing && !(ok = wait(L::kKvEmpty + 8 * s, it / kRing - 1))) break;
-          loader.template keys<D>(a, w, j, kv, base + L::kKV + s * L::kTile, kv ? &tmV : &tmK,
-                                  base + L::kKvFull + 8 * s, lane, missing + it / 2 % kMissingTiles);
+          const uint32_t to = M::kCodes ? L::raw(base, s) : base + L::kKV + s * L::kTile;
+          loader.template keys<D>(a, w, j, kv, to, kv ? &tmV : &tmK, base + kFull + 8 * s, lane,
+                                  missing + it / 2 % kMissingTiles);
         }
       }
     }
     // nothing may still be landing in shared memory when the CTA leaves
     if (i > 0) wait(L::kQFull, i - 1);
-    for (int q = it > kRing ? it - kRing : 0; q < it; ++q) wait(L::kKvFull + 8 * (q % kRing), q / kRing);
+    for (int q = it > kRing ? it - kRing : 0; q < it; ++q) wait(kFull + 8 * (q % kRing), q / kRing);
   } else if (warp == 1) {
     if (umma::elect()) {  // products
       // A product that waits for its operands leaves the tensor cores idle: only one or two are queued behind
@@ -456,8 +476,39 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (w.n0 == 0) break;
     }
+  } else if (M::kCodes && warp >= kThreads / 32) {  // keys and values of 8 bits
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if constexpr (M::kCodes) {
+      Work w;
+      typename M::template Converter<T, D> converter;
+      const int cw = warp - kThreads / 32;
+      int it = 0;  // ring position
+      bool ok = true;
+      for (int i = 0; ok; ++i) {
+        const bool more = get_work(base, L::kWFull, g, L::kWork, i, w, err);
+        if (!__all_sync(0xffffffffu, more)) break;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(base + L::kWEmpty + 8 * (i & 1));
+        const int n = key_tiles<M>(w);
+        converter.begin(a, w, cw, lane, n);
+        for (int x = 0; x < 2 * n; ++x, ++it) {
+          const int s = it % kRing;
+          ok = __all_sync(0xffffffffu, umma::inline_wait(base + L::kRawFull + 8 * s, (it / kRing) & 1, err));
+          if (!ok) break;
+          const uint32_t now = converter.exps[x & 1];
+          if (x & 1) converter.exponents(a, w, (x + 1) / 2, n, cw, lane);  // (of the next tile, while this is converted)
+          converter.tile(base + L::kKV + s * L::kTile, L::raw(base, s), now, cw, lane);
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) mbar_arrive(base + L::kKvFull + 8 * s);
+        }
+      }
+    }
   } else {  // softmax of row tile t
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    if constexpr (M::kCodes)
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
+    else
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     const int t = (warp - 4) >> 2, wq = warp & 3;
     const int r = wq * 32 + lane;
     const uint32_t lanes = (uint32_t)(wq * 32) << 16;
@@ -552,7 +603,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         probabilities(0);
         if (j > 0) {
-          const bool low = live && (sum > kLimit || m == kNegInf);
+          const bool low = live && (sum > kLimitOf<T, M> || m == kNegInf);
           if (__any_sync(0xffffffffu, low)) {
             umma::wait_ld();
             if (masked) mask(64);
@@ -573,7 +624,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         probabilities(64);
         if (j > 0) {
-          const bool low = live && sum > kLimit;
+          const bool low = live && sum > kLimitOf<T, M>;
           if (__any_sync(0xffffffffu, low)) {
             // the product with the first half must be over before the accumulator is touched
             ok = __all_sync(0xffffffffu, umma::inline_wait(base + L::kPvHalf + 8 * t, ns & 1, err));

@@ -184,5 +184,8 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
 // first, strides in bytes of all but the innermost), 128-byte swizzle.
 bool encode_16bit(CUtensorMap *m, const void *ptr, int rank, const uint64_t *dims, const uint64_t *strides,
                   const uint32_t *box);
+// The same of bytes, with the 128-byte swizzle or none.
+bool encode_8bit(CUtensorMap *m, const void *ptr, int rank, const uint64_t *dims, const uint64_t *strides,
+                 const uint32_t *box, bool swizzled);
 
 }  // namespace ns

@@ -5,6 +5,11 @@ fp16's): probabilities that carry the values' scales are kept in fp16 with the l
 by at most 2^-25 there, 2^-33 of that largest, times its code (at most 448): 2^-33 * 448 * n * max p_j 2^ve_j in all.
 A query in fp16, its largest element at 1 or above, is off by 2^-25 of that element: the score by
 2^-25 max |q| sum |k| scale.
+
+Beyond 16 rows in fp16 the values' scales are in the values: keys and values are codes times their power of two in
+fp16, off by at most 2^-25 (half a step below 2^-14, where it cannot hold them), and probabilities are kept 2^6 times
+larger, so that one (relative to the largest, at most 1) is off by at most 2^-25 2^-6.  So a score is off by
+2^-25 sum |q| scale, and an output by 2^-31 sum |v| over the keys that it sees, and 2^-25 sum p = 2^-25.
 """
 
 import random
@@ -130,11 +135,12 @@ def run(ns, lens, n, hq, hkv, d, dtype, page, seed, mask=None, layout="plain", s
                     p = torch.where(sees, torch.exp((qq.double() @ fine.T) * scale - z.nan_to_num(neginf=0.0)[:, None]), 0.0)
                     big = (p * torch.nan_to_num(vs)).amax(-1)
                     pv = p @ torch.nan_to_num(v).abs()
+                    if dtype == F16 and n * grp > 16:
+                        more = more + 2.0 ** -25 * scale * qq.double().abs().sum(-1)
+                        to = to + 2.0 ** -31 * (sees.double() @ torch.nan_to_num(v).abs()) + 2.0 ** -25
                     tz = tz + more
                     to = to + 2 * more[:, None] * pv + (2.0 ** -33 * 448 * L) * big[:, None]
                 o[wild], z[wild] = float("nan"), float("nan")
-                nan_row = (sees.double() @ (ve[ip, h, ir] == 255).double()) > 0 if L else wild
-                o[nan_row], z[nan_row] = float("nan"), float("nan")
                 check(out[b, :, hh], o, to, f"out of sequence {b} head {hh}")
                 check(lse[b, :, hh], z, tz, f"lse of sequence {b} head {hh}")
     assert ns.ops_error() == 0
@@ -223,7 +229,8 @@ def test_queries_of_any_size(ns, n, d):
 @pytest.mark.parametrize("n,hq", [(3, 4), (20, 4), (40, 2)])
 @pytest.mark.parametrize("d", [64, 128])
 def test_rows_that_are_not_finite(ns, n, hq, d):
-    """Keys and values with exponent 255 and codes that are NaN reach the rows that see them and no others."""
+    """Keys and values with exponent 255 and codes that are NaN reach the rows that see them and no others; a value
+    does not reach the log-sum-exp."""
     L = 200
     words = [[(1 << i) if i % 3 else 0 for i in range(n)], [(1 << (i + 1)) - 1 for i in range(n)]]
 
