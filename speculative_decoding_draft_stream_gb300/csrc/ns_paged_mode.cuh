@@ -13,8 +13,9 @@ namespace paged {
 
 // A whole warp fetches key and value tiles, a lane a page.  Work has the cache's sequence (seq, len), the tiles (j0,
 // tiles()) and the heads (unit); Args the table and the pages.
-// F8: codes, a box of all columns to a page.
-template <typename Args, typename Work, bool F8>
+// F8: codes, a box of all columns to a page.  P: of 16 bits and 128 columns, a box of all columns to a page (fa::Tile),
+// where heads or columns come in strides that leave a dimension for it (page_pairs).
+template <typename Args, typename Work, bool F8, bool P>
 struct PageLoader {
   int ids, next;  // lane l: the id of the l-th page of this tile, and of the next
   // pages of tile j that hold keys of the sequence
@@ -49,7 +50,10 @@ struct PageLoader {
       const int row = page > fa::kKeys ? (w.j0 + j) * fa::kKeys & (page - 1) : 0;
       if (F8)
         umma::tma4(dst + lane * rows * D, m, 0, row, w.unit * a.pack / a.group, ids, bar);
-      for (int h = 0; h < (F8 ? 0 : D / 64); ++h)
+      else if (P)
+        umma::tma5(dst + lane * rows * 256, m, 0, 0, (kv ? a.pairs.vz : a.pairs.kz) * (w.unit * a.pack / a.group),
+                   (kv ? a.pairs.vw : a.pairs.kw) * (w.unit * a.pack / a.group) + row / 8, ids, bar);
+      for (int h = 0; h < (F8 || P ? 0 : D / 64); ++h)
         umma::tma4(dst + h * fa::kHalf + lane * rows * 128, m, h * 64, row, w.unit * a.pack / a.group, ids, bar);
     }
     __syncwarp();
@@ -65,9 +69,36 @@ struct Exponents {
 inline Exponents exponents_of(const PagedAttnArgs &p) {
   return Exponents{p.k_exp, p.v_exp, p.ke_head, p.ve_head, p.kep8, p.vep8};
 }
+// A page of 128 columns of 16 bits in one box: dimensions are 64 columns, 8 rows, the two 64s, eights of rows, pages, and
+// a head is a step of the third (heads next to each other) or of the fourth (heads a page's rows apart).
+constexpr int kPairShift = 5;  // pages of up to 32
+struct Pairs {
+  int32_t kz, kw, vz, vw;  // a head's step in either
+};
+inline bool pair_steps(int64_t head, int64_t token, int page, int heads, int32_t &z, int32_t &w) {
+  z = head == 128 ? 2 : 0, w = head == 128 ? 0 : page / 8;
+  return head == 128 || head == token * page || heads == 1;
+}
+inline bool page_pairs(const PagedAttnArgs &p, Pairs *s) {
+  const int page = 1 << p.page_shift;
+  return pair_steps(p.k_head, p.k_token, page, p.kv_heads, s->kz, s->kw) &&
+         pair_steps(p.v_head, p.v_token, page, p.kv_heads, s->vz, s->vw);
+}
+
 // Maps of a layer's keys and values, 16 bits or codes.
-template <int D, bool F8>
-bool page_maps(const PagedAttnArgs &p, CUtensorMap *k, CUtensorMap *v) {
+template <int D, bool F8, bool P>
+bool page_maps(const PagedAttnArgs &p, const Pairs &s, CUtensorMap *k, CUtensorMap *v) {
+  if (P) {
+    const uint64_t page = 1ull << p.page_shift;
+    const uint32_t box[5] = {64, 8, 2, (uint32_t)(page < fa::kKeys ? page : fa::kKeys) / 8, 1};
+    auto map = [&](CUtensorMap *m, const void *at, int64_t token, int64_t in_page, int z) {
+      const uint64_t heads = p.kv_heads, eights = page / 8;
+      const uint64_t dims[5] = {64, 8, z ? 2 * heads : 2, z ? eights : eights * heads, (uint64_t)p.n_pages};
+      const uint64_t strides[4] = {(uint64_t)token * 2, 128, (uint64_t)token * 16, (uint64_t)in_page * 2};
+      return encode_16bit(m, at, 5, dims, strides, box);
+    };
+    return map(k, p.k, p.k_token, p.k_page, s.kz) && map(v, p.v, p.v_token, p.v_page, s.vz);
+  }
   const uint64_t page = 1ull << p.page_shift, e = F8 ? 1 : 2;
   const uint64_t dims[4] = {D, page, (uint64_t)p.kv_heads, (uint64_t)p.n_pages};
   const uint64_t sk[3] = {p.k_token * e, p.k_head * e, p.k_page * e}, sv[3] = {p.v_token * e, p.v_head * e, p.v_page * e};
@@ -207,12 +238,12 @@ struct NodeWild {  // new tokens whose value is not finite, per column
 };
 
 // Rows of a value tile behind the sequence's end: what the ring held before, or what their page holds.
-template <int D, typename Work>
+template <int D, typename M, typename Work>
 __device__ __forceinline__ bool clear_behind(const Work &w, int j, uint8_t *tile, int lane) {
   const int r0 = max(0, w.len - (w.j0 + j) * fa::kKeys);
   for (int h = 0; h < D / 64; ++h)
     for (int x = r0 * 8 + lane; x < fa::kKeys * 8; x += kWarp)
-      reinterpret_cast<uint4 *>(tile + h * fa::kHalf)[x] = make_uint4(0, 0, 0, 0);
+      *reinterpret_cast<uint4 *>(tile + fa::Tile<D, M>::piece(x >> 3, h, x & 7)) = make_uint4(0, 0, 0, 0);
   __syncwarp();
   return r0 < fa::kKeys;
 }

@@ -39,6 +39,7 @@ struct TreeArgs {
   long long *cum;  // [n_seqs + 1] tiles before each sequence, for the join
   uint32_t *err;
   paged::Exponents rows;  // (of 8 bits)
+  paged::Pairs pairs;     // (Mode's P)
 };
 
 struct Work {
@@ -142,15 +143,15 @@ using TreeWork = Work;
 using TreeDealer = Dealer;
 
 // F8: of a cache of 8 bits, whose keys and values are converted.
-template <bool F8>
+template <bool F8, bool P>
 struct Mode {
   using Args = TreeArgs;
   using Work = TreeWork;
   using Dealer = TreeDealer;
-  static constexpr bool kParts = true, kSplit = false, kLiveParts = false, kWhole = true, kCodes = F8, kHigh = F8;
+  static constexpr bool kParts = true, kSplit = false, kLiveParts = false, kWhole = true, kCodes = F8, kHigh = F8, kPaired = P;
   static constexpr int kStageRow = 64;
 
-  struct Loader : paged::PageLoader<TreeArgs, TreeWork, F8> {
+  struct Loader : paged::PageLoader<TreeArgs, TreeWork, F8, P> {
     __device__ __forceinline__ void queries(const TreeArgs &a, const Work &w, int t, int h, uint32_t dst,
                                             const CUtensorMap *m, uint32_t bar) {
       umma::tma4(dst, m, h * 64, w.unit * a.pack, w.node0 + t * a.per_tile, w.b, bar);
@@ -183,7 +184,7 @@ struct Mode {
 
   template <typename T, int D>
   static __device__ __forceinline__ bool clear(const TreeArgs &, const Work &w, int j, uint8_t *tile, int lane) {
-    return paged::clear_behind<D>(w, j, tile, lane);
+    return paged::clear_behind<D, Mode>(w, j, tile, lane);
   }
 
   // Where a part's row lies: 256 rows to a part, column by column.
@@ -299,8 +300,8 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const TreeArgs 
   }
 }
 
-template <typename T, int D, bool F8>
-cudaError_t launch(const PagedAttnArgs &p, int sms, cudaStream_t st) {
+template <typename T, int D, bool F8, bool P>
+cudaError_t launch(const PagedAttnArgs &p, const paged::Pairs &pairs, int sms, cudaStream_t st) {
   TreeArgs a{};
   a.table = p.table, a.lengths = p.lengths, a.seqs = p.seqs, a.mask = p.mask;
   a.n_seqs = p.n_seqs, a.n = p.n, a.q_heads = p.q_heads, a.group = p.group;
@@ -318,13 +319,14 @@ cudaError_t launch(const PagedAttnArgs &p, int sms, cudaStream_t st) {
   const paged::Ws ws = paged::workspace(p.ws, p.n_seqs, ctas, 256);
   a.cum = ws.cum, a.part_ml = ws.ml, a.part_o = ws.o;
   a.rows = paged::exponents_of(p);
+  a.pairs = pairs;
   CUtensorMap tmQ, tmK, tmV;
   const uint64_t dq[4] = {D, (uint64_t)p.q_heads, (uint64_t)p.n, (uint64_t)p.n_seqs};
   const uint64_t sq[3] = {(uint64_t)p.q_head * 2, (uint64_t)p.q_token * 2, (uint64_t)p.q_seq * 2};
   const uint32_t bq[4] = {64, (uint32_t)a.pack, (uint32_t)a.per_tile, 1};
-  if (!encode_16bit(&tmQ, p.q, 4, dq, sq, bq) || !paged::page_maps<D, F8>(p, &tmK, &tmV))
+  if (!encode_16bit(&tmQ, p.q, 4, dq, sq, bq) || !paged::page_maps<D, F8, P>(p, pairs, &tmK, &tmV))
     return cudaErrorInvalidValue;
-  using M = Mode<F8>;
+  using M = Mode<F8, P>;
   fa::attn_kernel<T, D, M><<<ctas, fa::kThreadsOf<M>, fa::Smem<D, M>::kBytes, st>>>(tmQ, tmK, tmV, a);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
@@ -344,23 +346,39 @@ cudaError_t launch(const PagedAttnArgs &p, int sms, cudaStream_t st) {
               : cudaLaunchKernelEx(&cfg, tree_join_kernel<T, D, 1>, a, ctas);
 }
 
+// A page's columns in one box where pages are small: with pages of 16 the boxes, not the products, are what a tile takes.
 template <typename T, int D, bool F8>
+cudaError_t by_pages(const PagedAttnArgs &p, int sms, cudaStream_t st) {
+  paged::Pairs pairs{};
+  if constexpr (D == 128 && !F8) {
+    if (p.page_shift <= paged::kPairShift && paged::page_pairs(p, &pairs)) return launch<T, D, F8, true>(p, pairs, sms, st);
+  }
+  return launch<T, D, F8, false>(p, pairs, sms, st);
+}
+
+template <typename T, int D, bool F8, bool P>
 cudaError_t prepare() {
-  return cudaFuncSetAttribute(fa::attn_kernel<T, D, Mode<F8>>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              fa::Smem<D, Mode<F8>>::kBytes);
+  using M = Mode<F8, P>;
+  return cudaFuncSetAttribute(fa::attn_kernel<T, D, M>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              fa::Smem<D, M>::kBytes);
 }
 template <bool F8>
 cudaError_t prepare_all() {
-  cudaError_t e = prepare<__nv_bfloat16, 128, F8>();
-  if (e == cudaSuccess) e = prepare<__nv_bfloat16, 64, F8>();
-  if (e == cudaSuccess) e = prepare<__half, 128, F8>();
-  return e == cudaSuccess ? prepare<__half, 64, F8>() : e;
+  cudaError_t e = prepare<__nv_bfloat16, 128, F8, false>();
+  if (e == cudaSuccess) e = prepare<__nv_bfloat16, 64, F8, false>();
+  if (e == cudaSuccess) e = prepare<__half, 128, F8, false>();
+  if (e == cudaSuccess) e = prepare<__half, 64, F8, false>();
+  if constexpr (!F8) {
+    if (e == cudaSuccess) e = prepare<__nv_bfloat16, 128, F8, true>();
+    if (e == cudaSuccess) e = prepare<__half, 128, F8, true>();
+  }
+  return e;
 }
 template <bool F8>
 cudaError_t launch_any(const PagedAttnArgs &a, int dtype, int dim, int sms, cudaStream_t st) {
   if (dtype == NS_DTYPE_BF16)
-    return dim == 128 ? launch<__nv_bfloat16, 128, F8>(a, sms, st) : launch<__nv_bfloat16, 64, F8>(a, sms, st);
-  return dim == 128 ? launch<__half, 128, F8>(a, sms, st) : launch<__half, 64, F8>(a, sms, st);
+    return dim == 128 ? by_pages<__nv_bfloat16, 128, F8>(a, sms, st) : by_pages<__nv_bfloat16, 64, F8>(a, sms, st);
+  return dim == 128 ? by_pages<__half, 128, F8>(a, sms, st) : by_pages<__half, 64, F8>(a, sms, st);
 }
 
 }  // namespace

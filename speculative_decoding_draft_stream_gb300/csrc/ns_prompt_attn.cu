@@ -124,7 +124,7 @@ struct Mode {
   using Args = FaArgs;
   using Work = ns::Work;
   using Dealer = ns::Dealer<S>;
-  static constexpr bool kParts = false, kSplit = S, kWhole = true, kCodes = false, kHigh = false;
+  static constexpr bool kParts = false, kSplit = S, kWhole = true, kCodes = false, kHigh = false, kPaired = false;
   static constexpr int kStageRow = 128;
 
   struct Loader {

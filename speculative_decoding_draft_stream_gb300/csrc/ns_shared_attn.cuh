@@ -40,9 +40,9 @@ struct SharedArgs {
   void *out;
   float *lse;
   uint32_t *err;
-  // the plan: of each group its first sequence and members, its shared tiles; of each sequence its group
-  int2 *bounds;
-  int32_t *shared, *group_of;
+  // the plan: of each group its first sequence, members, shared tiles and the first's sequence in the cache; then of each
+  // sequence the cache's, its length, the tiles that it shares and its group
+  int4 *plan;
   // the line: tiles before each group's items and then each sequence's, and all; prefix items before each group's
   long long *cum;
   int32_t *items_before;
@@ -50,6 +50,7 @@ struct SharedArgs {
   float2 *part_ml, *tail_ml;
   float *part_o, *tail_o;
   paged::Exponents rows;  // (of 8 bits)
+  paged::Pairs pairs;     // (Mode's P)
 };
 
 // ---------------------------------------------------------------------------
@@ -61,30 +62,36 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
   __shared__ int s_min;
   const int g = blockIdx.x / kPlanCtas, rank = blockIdx.x % kPlanCtas, tid = threadIdx.x;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  auto cluster_sync = []() {
+    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+  };
+  auto valid = [&](int s, int &len) {
+    len = s >= 0 && s < a.max_seqs ? a.lengths[s] : -1;
+    return len >= 0 && (long long)len <= ((long long)a.table_ld << a.page_shift);
+  };
   // Groups that do not cover the sequences one after the other: nothing is shared, the first has them all.
+  const int from = a.groups[g], to = a.groups[g + 1];
   int bad = a.groups[0] != 0 || a.groups[a.n_groups] != a.n_seqs;
   for (int i = tid; i < a.n_groups; i += kPlanThreads) bad |= a.groups[i] < 0 || a.groups[i + 1] < a.groups[i];
+  if (tid == 0) s_min = 0x7fffffff;
   bad = __syncthreads_or(bad);
-  const int first = bad ? 0 : a.groups[g], members = bad ? (g == 0 ? a.n_seqs : 0) : a.groups[g + 1] - first;
+  const int first = bad ? 0 : from, members = bad ? (g == 0 ? a.n_seqs : 0) : to - from;
   // positions that every member has as context, and in whole pages
   int most = bad || members < 2 ? 0 : 0x7fffffff;
   for (int i = tid; i < members; i += kPlanThreads) {
-    const int s = a.seqs[first + i];
-    const int len = s >= 0 && s < a.max_seqs ? a.lengths[s] : -1;
-    if (len < 0 || (long long)len > ((long long)a.table_ld << a.page_shift)) {
-      if (rank == 0) set_flag(a.err, NS_FLAG_BAD_SEQ);
-      most = 0;
-    } else {
+    int len;
+    if (valid(a.seqs[first + i], len))
       most = min(most, max(0, len - a.n) >> a.page_shift);
-    }
-    if (rank == 0) a.group_of[first + i] = g;
+    else
+      most = 0;
   }
-  if (tid == 0) s_min = 0x7fffffff;
-  __syncthreads();
-  atomicMin(&s_min, most);
+  most = __reduce_min_sync(0xffffffffu, most);
+  if ((tid & 31) == 0) atomicMin(&s_min, most);
   __syncthreads();
   most = s_min;  // pages
-  if (most > 0) {  // (most < 2^31 here: there are two members at least)
+  __syncthreads();
+  if (most > 0) {  // (and less than 2^31: there are two members at least)
     const int32_t *lead = a.table + (size_t)a.seqs[first] * a.table_ld;
     int same = most;
     for (int i = 1 + rank; i < members; i += kPlanCtas) {
@@ -93,26 +100,37 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
       for (int p = tid; p < same; p += kPlanThreads)
         if (row[p] != lead[p]) same = min(same, p);
     }
-    atomicMin(&s_min, same);
-    __syncthreads();
-    most = s_min;
+    same = __reduce_min_sync(0xffffffffu, same);
+    if ((tid & 31) == 0) atomicMin(&s_min, same);
   }
-  const uint32_t there = smem_u32(s_most + rank);
-  if (tid == 0) {
-    uint32_t to;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(to) : "r"(there));
-    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");  // all have begun
-    asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(to), "r"(most) : "memory");
-  } else {
-    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+  cluster_sync();  // all have begun, and found their part
+  uint32_t there;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(there) : "r"(smem_u32(s_most)));
+  if (tid == 0) asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(there + 4 * rank), "r"(s_min) : "memory");
+  cluster_sync();
+  most = 0x7fffffff;
+#pragma unroll
+  for (int i = 0; i < kPlanCtas; ++i) {
+    int x;
+    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(x) : "r"(there + 4 * i) : "memory");
+    most = min(most, x);
   }
-  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+  if (members == 0) most = 0;
+  const int shared = (int)(((long long)most << a.page_shift) / kKeys);
   if (rank == 0 && tid == 0) {
-    for (int i = 0; i < kPlanCtas; ++i) most = min(most, s_most[i]);
-    a.bounds[g] = make_int2(first, members);
-    a.shared[g] = (int)(((long long)most << a.page_shift) / kKeys);
+    a.plan[g] = make_int4(first, members, shared, members > 0 ? a.seqs[first] : 0);
     if (bad && g == 0) set_flag(a.err, NS_FLAG_BAD_SEQ);
   }
+  for (int i = rank * kPlanThreads + tid; i < members; i += kPlanCtas * kPlanThreads) {
+    const int s = a.seqs[first + i];
+    int len;
+    if (!valid(s, len)) {
+      set_flag(a.err, NS_FLAG_BAD_SEQ);
+      len = 0;
+    }
+    a.plan[a.n_groups + first + i] = make_int4(s, len, shared, g);
+  }
+  cluster_sync();  // nobody leaves before its memory has been read
 }
 
 // ---------------------------------------------------------------------------
@@ -132,7 +150,8 @@ constexpr int kAllSeen = 0x7fffffff;
 // What an item's beginning and end take, in tiles: the line has that many more for each item, so that shares are equal
 // in time.  Without: 64 sequences of 4 prompts (28 heads on 4, one new token each) 68.0 us, the CTAs with the tails
 // 25 us longer at work than the others; with 1, 2, 3, 4: see the table of launch.
-constexpr int kItemCost = 2;
+template <bool S>
+constexpr int kItemCost = S ? 3 : 2;
 
 // A CTA's share of the line, item by item (a whole warp): entries 0 .. n_groups - 1 are prefixes, the others tails.
 // Lane l holds entry 32 chunk + l.  S: items of one row tile (attn_kernel's kSplit), otherwise of two.
@@ -145,7 +164,7 @@ struct Dealer {
   int cta, lane, l, chunk;  // l: the lane whose entry is dealt
   int nt, items;            // this lane's entry: an item's place in the line (its tiles and cost), items
   int x, y;                 // first sequence and members, or cache sequence and its length
-  int from;                 // a tail's first tile
+  int from;                 // a tail's first tile, or the cache sequence of a prefix's first
   long long excl, sum;      // tiles before this lane's entry in the chunk, and of the chunk
   int item_excl, item_sum;  // prefix items
 
@@ -156,19 +175,19 @@ struct Dealer {
     chunk = k;
     const int e = k * 32 + lane;
     nt = items = x = y = from = 0;
-    if (e < a.n_groups) {
-      const int2 b = a.bounds[e];
-      x = b.x, y = b.y, nt = a.shared[e];
-      items = nt > 0 ? a.units * blocks(a, y) : 0;
-    } else if (e < a.n_groups + a.n_seqs) {
-      x = a.seqs[e - a.n_groups];
-      y = x >= 0 && x < a.max_seqs ? a.lengths[x] : 0;
-      if (y < 0 || (long long)y > ((long long)a.table_ld << a.page_shift)) y = 0;  // (the plan has flagged it)
-      from = a.shared[a.group_of[e - a.n_groups]];
-      nt = max(1, (y + kKeys - 1) / kKeys - from);  // an empty sequence: one tile, all masked
-      items = a.units * a.tail_blocks;
+    if (e < a.n_groups + a.n_seqs) {
+      const int4 r = a.plan[e];
+      x = r.x, y = r.y;
+      if (e < a.n_groups) {
+        nt = r.z, from = r.w;
+        items = nt > 0 ? a.units * blocks(a, y) : 0;
+      } else {
+        from = r.z;
+        nt = max(1, (y + kKeys - 1) / kKeys - from);  // an empty sequence: one tile, all masked
+        items = a.units * a.tail_blocks;
+      }
     }
-    if (nt > 0) nt += kItemCost;
+    if (nt > 0) nt += kItemCost<S>;
     const int prefix = e < a.n_groups ? items : 0;
     excl = (long long)nt * items, item_excl = prefix;
 #pragma unroll
@@ -224,14 +243,14 @@ struct Dealer {
     const long long local = at - base - __shfl_sync(0xffffffffu, excl, l);
     const int item = (int)quotient(local, n), place = (int)(local - (long long)item * n);
     const int left = (int)min((long long)(n - place), end - at);  // of the line, in this item
-    const int tile = max(0, place - kItemCost), count = left - max(0, kItemCost - place);
+    const int tile = max(0, place - kItemCost<S>), count = left - max(0, kItemCost<S> - place);
     at += left;
     if (count <= 0) return false;
     w.n0 = count;
     if (e < a.n_groups) {
       const int b = all / a.units;
       w.unit = item / b, w.tok0 = p * a.n + item % b * kRowTiles * a.per_tile, w.tok_end = (p + q) * a.n;
-      w.seq = a.seqs[p], w.len = (n - kItemCost) * kKeys, w.j0 = tile, w.ctx = kAllSeen, w.hidden = count;
+      w.seq = first, w.len = (n - kItemCost<S>) * kKeys, w.j0 = tile, w.ctx = kAllSeen, w.hidden = count;
       w.slot = prior + item + cta;
     } else {
       const int b = e - a.n_groups;
@@ -250,15 +269,15 @@ struct Dealer {
 };
 
 // F8: of a cache of 8 bits, whose keys and values are converted.
-template <bool S, bool F8>
+template <bool S, bool F8, bool P>
 struct Mode {
   using Args = SharedArgs;
   using Work = ns::Work<S>;
   using Dealer = ns::Dealer<S>;
-  static constexpr bool kParts = true, kSplit = S, kLiveParts = true, kWhole = false, kCodes = F8, kHigh = true;
+  static constexpr bool kParts = true, kSplit = S, kLiveParts = true, kWhole = false, kCodes = F8, kHigh = true, kPaired = P;
   static constexpr int kStageRow = 64, kRows = S ? 128 : 256;  // (of a part)
 
-  struct Loader : paged::PageLoader<SharedArgs, Work, F8> {
+  struct Loader : paged::PageLoader<SharedArgs, Work, F8, P> {
     __device__ __forceinline__ void queries(const SharedArgs &a, const Work &w, int t, int h, uint32_t dst,
                                             const CUtensorMap *m, uint32_t bar) {
       umma::tma3(dst, m, h * 64, w.unit * a.pack, w.tok0 + t * a.per_tile, bar);
@@ -292,7 +311,7 @@ struct Mode {
 
   template <typename T, int D>
   static __device__ __forceinline__ bool clear(const SharedArgs &, const Work &w, int j, uint8_t *tile, int lane) {
-    return paged::clear_behind<D>(w, j, tile, lane);
+    return paged::clear_behind<D, Mode>(w, j, tile, lane);
   }
 
   template <int D>
@@ -321,6 +340,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) merge_kernel(const SharedArg
   const int col0 = G == 1 ? warp * N : blockIdx.z * N;
   const int row = blockIdx.x * 32 + lane, tok = row / a.pack, h = row % a.pack;
   const bool live = tok < a.n_seqs * a.n;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int b = live ? tok / a.n : 0, node = live ? tok % a.n : 0;
   const long long total = a.cum[a.n_groups + a.n_seqs];
@@ -330,11 +350,12 @@ __global__ void __launch_bounds__(kMergeWarps * 32) merge_kernel(const SharedArg
   int64_t slot[2] = {0, 0};
   int in_part[2] = {0, 0};
   if (live) {
-    const int X = kRowTiles * a.per_tile, g = a.group_of[b], nt = a.shared[g];
+    const int4 mine = a.plan[a.n_groups + b];
+    const int X = kRowTiles * a.per_tile, g = mine.w, nt = mine.z;
     if (nt > 0) {
-      const int2 bounds = a.bounds[g];
+      const int4 bounds = a.plan[g];
       const int v = tok - bounds.x * a.n, blocks = (bounds.y * a.n + X - 1) / X, item = unit * blocks + v / X;
-      const long long from = a.cum[g] + (long long)item * (nt + kItemCost) + kItemCost;
+      const long long from = a.cum[g] + (long long)item * (nt + kItemCost<S>) + kItemCost<S>;
       c0[0] = (int)quotient((from + 1) * ctas - 1, total);
       pieces[0] = (int)quotient((from + nt) * ctas - 1, total) - c0[0] + 1;
       slot[0] = a.items_before[g] + item;
@@ -342,9 +363,9 @@ __global__ void __launch_bounds__(kMergeWarps * 32) merge_kernel(const SharedArg
     }
     const long long cb = a.cum[a.n_groups + b];
     const int items = a.units * a.tail_blocks, item = unit * a.tail_blocks + node / X;
-    const long long n = quotient(a.cum[a.n_groups + b + 1] - cb, items), from = cb + item * n + kItemCost;
+    const long long n = quotient(a.cum[a.n_groups + b + 1] - cb, items), from = cb + item * n + kItemCost<S>;
     c0[1] = (int)quotient((from + 1) * ctas - 1, total);
-    pieces[1] = (int)quotient((from + n - kItemCost) * ctas - 1, total) - c0[1] + 1;
+    pieces[1] = (int)quotient((from + n - kItemCost<S>) * ctas - 1, total) - c0[1] + 1;
     slot[1] = b * items + item;
     in_part[1] = node % X * a.pack + h;
   }
@@ -433,7 +454,7 @@ Shape shape_of(int n_seqs, int n_groups, int n, int q_heads, int kv_heads, int s
 }
 
 struct Layout {
-  int64_t bounds, shared, group_of, cum, items, part_ml, tail_ml, part_o, tail_o, bytes;
+  int64_t plan, cum, items, part_ml, tail_ml, part_o, tail_o, bytes;
   Layout(const Shape &s, int n_seqs, int n_groups, int dim) {
     int64_t at = 0;
     auto take = [&](int64_t n) {
@@ -441,7 +462,7 @@ struct Layout {
       at = (at + n + 255) & ~(int64_t)255;
       return was;
     };
-    bounds = take(8LL * n_groups), shared = take(4LL * n_groups), group_of = take(4LL * n_seqs);
+    plan = take(16LL * (n_groups + n_seqs));
     cum = take(8LL * (n_groups + n_seqs + 1)), items = take(4LL * n_groups);
     part_ml = take(s.parts * (s.split ? 128 : 256) * 8), tail_ml = take(s.tails * s.tail_rows * 8);
     part_o = take(s.parts * (s.split ? 128 : 256) * dim * 4), tail_o = take(s.tails * s.tail_rows * dim * 4);
@@ -449,9 +470,9 @@ struct Layout {
   }
 };
 
-template <typename T, int D, bool S, bool F8>
-cudaError_t launch(const PagedAttnArgs &p, const Shape &s, const int32_t *groups, int n_groups, int sms,
-                   cudaStream_t st) {
+template <typename T, int D, bool S, bool F8, bool P>
+cudaError_t launch(const PagedAttnArgs &p, const Shape &s, const paged::Pairs &pairs, const int32_t *groups,
+                   int n_groups, int sms, cudaStream_t st) {
   const Layout at(s, p.n_seqs, n_groups, D);
   char *ws = static_cast<char *>(p.ws);
   SharedArgs a{};
@@ -460,22 +481,19 @@ cudaError_t launch(const PagedAttnArgs &p, const Shape &s, const int32_t *groups
   a.pack = s.pack, a.per_tile = s.per_tile, a.units = s.units, a.tail_blocks = s.tail_blocks, a.tail_rows = s.tail_rows;
   a.page_shift = p.page_shift, a.table_ld = p.table_ld, a.max_seqs = p.max_seqs, a.n_pages = p.n_pages;
   a.c = p.scale * attn::kLog2e, a.out = p.out, a.lse = p.lse, a.err = p.err;
-  a.bounds = reinterpret_cast<int2 *>(ws + at.bounds), a.shared = reinterpret_cast<int32_t *>(ws + at.shared);
-  a.group_of = reinterpret_cast<int32_t *>(ws + at.group_of), a.cum = reinterpret_cast<long long *>(ws + at.cum);
+  a.plan = reinterpret_cast<int4 *>(ws + at.plan), a.cum = reinterpret_cast<long long *>(ws + at.cum);
   a.items_before = reinterpret_cast<int32_t *>(ws + at.items);
   a.part_ml = reinterpret_cast<float2 *>(ws + at.part_ml), a.tail_ml = reinterpret_cast<float2 *>(ws + at.tail_ml);
   a.part_o = reinterpret_cast<float *>(ws + at.part_o), a.tail_o = reinterpret_cast<float *>(ws + at.tail_o);
   a.rows = paged::exponents_of(p);
+  a.pairs = pairs;
   CUtensorMap tmQ, tmK, tmV;
   const uint64_t dq[3] = {D, (uint64_t)p.q_heads, (uint64_t)p.n_seqs * p.n};
   const uint64_t sq[2] = {(uint64_t)p.q_head * 2, (uint64_t)(p.n > 1 ? p.q_token : p.q_seq) * 2};
   const uint32_t bq[3] = {64, (uint32_t)a.pack, (uint32_t)a.per_tile};
-  if (!encode_16bit(&tmQ, p.q, 3, dq, sq, bq) || !paged::page_maps<D, F8>(p, &tmK, &tmV))
+  if (!encode_16bit(&tmQ, p.q, 3, dq, sq, bq) || !paged::page_maps<D, F8, P>(p, pairs, &tmK, &tmV))
     return cudaErrorInvalidValue;
-  using M = Mode<S, F8>;
-  plan_kernel<<<n_groups * kPlanCtas, kPlanThreads, 0, st>>>(a);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
+  using M = Mode<S, F8, P>;
   cudaLaunchConfig_t cfg{};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -483,6 +501,10 @@ cudaError_t launch(const PagedAttnArgs &p, const Shape &s, const int32_t *groups
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   cfg.stream = st;
+  cfg.gridDim = dim3((unsigned)n_groups * kPlanCtas);
+  cfg.blockDim = dim3(kPlanThreads);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, plan_kernel, a);
+  if (e != cudaSuccess) return e;
   cfg.gridDim = dim3((unsigned)sms);
   cfg.blockDim = dim3(fa::kThreadsOf<M>);
   cfg.dynamicSmemBytes = fa::Smem<D, M>::kBytes;
@@ -498,39 +520,54 @@ cudaError_t launch(const PagedAttnArgs &p, const Shape &s, const int32_t *groups
               : cudaLaunchKernelEx(&cfg, merge_kernel<T, D, S, 1>, a, sms);
 }
 
-template <typename T, int D, bool F8>
-cudaError_t by_shape(const PagedAttnArgs &p, const int32_t *groups, int n_groups, int sms, cudaStream_t st) {
+template <typename T, int D, bool F8, bool P>
+cudaError_t by_shape(const PagedAttnArgs &p, const paged::Pairs &pairs, const int32_t *groups, int n_groups, int sms,
+                     cudaStream_t st) {
   const Shape s = shape_of(p.n_seqs, n_groups, p.n, p.q_heads, p.kv_heads, sms);
-  return s.split ? launch<T, D, true, F8>(p, s, groups, n_groups, sms, st)
-                 : launch<T, D, false, F8>(p, s, groups, n_groups, sms, st);
+  return s.split ? launch<T, D, true, F8, P>(p, s, pairs, groups, n_groups, sms, st)
+                 : launch<T, D, false, F8, P>(p, s, pairs, groups, n_groups, sms, st);
+}
+// (as by_pages of ns_paged_tree.cuh)
+template <typename T, int D, bool F8>
+cudaError_t by_pages(const PagedAttnArgs &p, const int32_t *groups, int n_groups, int sms, cudaStream_t st) {
+  paged::Pairs pairs{};
+  if constexpr (D == 128 && !F8) {
+    if (p.page_shift <= paged::kPairShift && paged::page_pairs(p, &pairs))
+      return by_shape<T, D, F8, true>(p, pairs, groups, n_groups, sms, st);
+  }
+  return by_shape<T, D, F8, false>(p, pairs, groups, n_groups, sms, st);
 }
 
-template <typename T, int D, bool S, bool F8>
+template <typename T, int D, bool F8, bool P>
 cudaError_t prepare() {
-  return cudaFuncSetAttribute(fa::attn_kernel<T, D, Mode<S, F8>>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              fa::Smem<D, Mode<S, F8>>::kBytes);
+  auto set = [](auto *kernel, int bytes) {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  };
+  using Whole = Mode<false, F8, P>;
+  using Split = Mode<true, F8, P>;
+  const cudaError_t e = set(fa::attn_kernel<T, D, Whole>, fa::Smem<D, Whole>::kBytes);
+  return e == cudaSuccess ? set(fa::attn_kernel<T, D, Split>, fa::Smem<D, Split>::kBytes) : e;
 }
 template <bool F8>
 cudaError_t prepare_all() {
-  cudaError_t e = cudaSuccess;
-  auto both = [&](auto with, auto without) {
-    if (e == cudaSuccess) e = with();
-    if (e == cudaSuccess) e = without();
-  };
-  both(prepare<__nv_bfloat16, 128, true, F8>, prepare<__nv_bfloat16, 128, false, F8>);
-  both(prepare<__nv_bfloat16, 64, true, F8>, prepare<__nv_bfloat16, 64, false, F8>);
-  both(prepare<__half, 128, true, F8>, prepare<__half, 128, false, F8>);
-  both(prepare<__half, 64, true, F8>, prepare<__half, 64, false, F8>);
+  cudaError_t e = prepare<__nv_bfloat16, 128, F8, false>();
+  if (e == cudaSuccess) e = prepare<__nv_bfloat16, 64, F8, false>();
+  if (e == cudaSuccess) e = prepare<__half, 128, F8, false>();
+  if (e == cudaSuccess) e = prepare<__half, 64, F8, false>();
+  if constexpr (!F8) {
+    if (e == cudaSuccess) e = prepare<__nv_bfloat16, 128, F8, true>();
+    if (e == cudaSuccess) e = prepare<__half, 128, F8, true>();
+  }
   return e;
 }
 template <bool F8>
 cudaError_t launch_any(const PagedAttnArgs &a, const int32_t *groups, int n_groups, int dtype, int dim, int sms,
                        cudaStream_t st) {
   if (dtype == NS_DTYPE_BF16)
-    return dim == 128 ? by_shape<__nv_bfloat16, 128, F8>(a, groups, n_groups, sms, st)
-                      : by_shape<__nv_bfloat16, 64, F8>(a, groups, n_groups, sms, st);
-  return dim == 128 ? by_shape<__half, 128, F8>(a, groups, n_groups, sms, st)
-                    : by_shape<__half, 64, F8>(a, groups, n_groups, sms, st);
+    return dim == 128 ? by_pages<__nv_bfloat16, 128, F8>(a, groups, n_groups, sms, st)
+                      : by_pages<__nv_bfloat16, 64, F8>(a, groups, n_groups, sms, st);
+  return dim == 128 ? by_pages<__half, 128, F8>(a, groups, n_groups, sms, st)
+                    : by_pages<__half, 64, F8>(a, groups, n_groups, sms, st);
 }
 
 }  // namespace

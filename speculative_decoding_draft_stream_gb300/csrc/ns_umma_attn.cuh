@@ -144,10 +144,21 @@ __device__ __forceinline__ uint64_t eights(uint32_t bits) {
   return (uint64_t)__vcmpne4((uint32_t)(x >> 32), 0u) << 32 | __vcmpne4((uint32_t)x, 0u);
 }
 
-// Where the value of column d, key r of a value tile lies in it.
-__device__ __forceinline__ int value_at(int r, int d) {
-  return (d >> 6) * kHalf + r * 128 + ((((d & 63) >> 3) ^ (r & 7)) << 4) + (d & 7) * 2;
-}
+// How key and value tiles lie: 64 columns of all rows and then the others, or (M::kPaired, of 128 columns) both of eight
+// rows and then of the next eight, as one TMA box brings them.
+template <int D, typename M>
+struct Tile {
+  static constexpr bool kPair = M::kPaired && D == 128;
+  static constexpr int kEight = kPair ? 2048 : 1024, kNext = kPair ? 1024 : kHalf;  // bytes from eight rows, from 64 columns to the next
+  // 16-byte piece c of row r, 64 columns h (before the swizzle)
+  static __device__ __forceinline__ int piece(int r, int h, int c) {
+    return h * kNext + (r >> 3) * kEight + (r & 7) * 128 + c * 16;
+  }
+  // the value of column d, key r
+  static __device__ __forceinline__ int at(int r, int d) {
+    return piece(r, d >> 6, (d & 63) >> 3 ^ (r & 7)) + (d & 7) * 2;
+  }
+};
 
 // -inf where bit e of `sees` is not set, scores from, from + 1, ... of a register array
 #define NS_FA_MASK(s, from, sees)                                             \
@@ -162,6 +173,7 @@ __global__ void __launch_bounds__(kThreadsOf<M>, 1)
   using L = Smem<D, M>;
   using Work = typename M::Work;
   using Wild = typename M::Wild;
+  using KV = Tile<D, M>;
   constexpr bool kBf16 = sizeof(T) == 2 && kOffset<T> == 0.f;
   constexpr uint32_t kIdS = umma::idesc(kBf16, kKeys, false), kIdO = umma::idesc(kBf16, D, true);
   extern __shared__ uint8_t smem_raw[];
@@ -270,25 +282,27 @@ __global__ void __launch_bounds__(kThreadsOf<M>, 1)
       };
       // S_t = Q_t K^T; the look at the next barrier comes before the last two products
       auto scores = [&](int t, int slot, uint32_t bar, int phase) {
-        const uint64_t A = umma::desc_k(base + L::kQ + t * L::kTile), B = umma::desc_k(base + L::kKV + slot * L::kTile);
+        const uint64_t A = umma::desc_k(base + L::kQ + t * L::kTile);
+        const uint64_t B = umma::desc_k(base + L::kKV + slot * L::kTile, KV::kEight);
         bool seen = false;
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           if (kk == D / 16 - 2) seen = peek(bar, phase);
-          const uint32_t off = ((kk >> 2) * kHalf + (kk & 3) * 32) >> 4;  // in the descriptors' 16-byte units
-          umma::mma_ss(tmem + t * 128, A + off, B + off, kIdS, kk != 0);
+          // in the descriptors' 16-byte units
+          const uint32_t offA = ((kk >> 2) * kHalf + (kk & 3) * 32) >> 4, offB = ((kk >> 2) * KV::kNext + (kk & 3) * 32) >> 4;
+          umma::mma_ss(tmem + t * 128, A + offA, B + offB, kIdS, kk != 0);
         }
         umma::commit(base + L::kSFull + 8 * t);
         return seen;
       };
       // O_t += P_t V, 64 keys
       auto values = [&](int t, int slot, int h, bool more, uint32_t bar, int phase) {
-        const uint64_t V = umma::desc_mn(base + L::kKV + slot * L::kTile, kHalf);
+        const uint64_t V = umma::desc_mn(base + L::kKV + slot * L::kTile, KV::kNext, KV::kEight);
         bool seen = false;
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk) {
           if (kk == 2) seen = peek(bar, phase);
-          umma::mma_ts(tmem + 256 + t * 128, tmem + t * 128 + (h * 4 + kk) * 8, V + (h * 4 + kk) * (2048 >> 4), kIdO,
+          umma::mma_ts(tmem + 256 + t * 128, tmem + t * 128 + (h * 4 + kk) * 8, V + (h * 4 + kk) * (2 * KV::kEight >> 4), kIdO,
                        more || h > 0 || kk > 0);
         }
         return seen;
@@ -439,7 +453,7 @@ __global__ void __launch_bounds__(kThreadsOf<M>, 1)
           }
           for (int d = lane; d < D; d += kWarp) {
             for (int r = 0; r < kKeys; ++r) {
-              T *v = reinterpret_cast<T *>(tile + value_at(r, d));
+              T *v = reinterpret_cast<T *>(tile + KV::at(r, d));
               const float x = static_cast<float>(*v);
               if (!(fabsf(x) < __int_as_float(0x7f800000)) && wild->note(w, j, r, d, x)) *v = static_cast<T>(0.f);
             }

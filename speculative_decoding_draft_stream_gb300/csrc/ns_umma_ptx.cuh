@@ -36,15 +36,15 @@ __device__ __forceinline__ bool elect() {
 }
 
 // Shared-memory operand descriptors, 128-byte swizzle (descriptor version 1).
-// K-major (rows of 64 16-bit elements along K, 8-row groups 1024 bytes apart):
-__device__ __forceinline__ uint64_t desc_k(uint32_t saddr) {
-  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | (uint64_t)1 << 16 | (uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 |
+// K-major (rows of 64 16-bit elements along K, 8-row groups 1024 bytes apart, or `apart`):
+__device__ __forceinline__ uint64_t desc_k(uint32_t saddr, uint32_t apart = 1024) {
+  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | (uint64_t)1 << 16 | (uint64_t)(apart >> 4) << 32 | (uint64_t)1 << 46 |
          (uint64_t)2 << 61;
 }
 // MN-major (rows of 64 elements along M or N, one row per k; 8-row groups
-// 1024 bytes apart along K, the next 64 elements of M or N `lead` bytes on):
-__device__ __forceinline__ uint64_t desc_mn(uint32_t saddr, uint32_t lead) {
-  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | (uint64_t)(lead >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 |
+// 1024 bytes, or `apart`, apart along K, the next 64 elements of M or N `lead` bytes on):
+__device__ __forceinline__ uint64_t desc_mn(uint32_t saddr, uint32_t lead, uint32_t apart = 1024) {
+  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | (uint64_t)(lead >> 4) << 16 | (uint64_t)(apart >> 4) << 32 |
          (uint64_t)1 << 46 | (uint64_t)2 << 61;
 }
 // Instruction descriptor: fp32 accumulator, 16-bit operands (bf16 or fp16),
@@ -128,6 +128,14 @@ __device__ __forceinline__ void tma4(uint32_t dst, const CUtensorMap *m, int x, 
       : "memory");
 }
 
+__device__ __forceinline__ void tma5(uint32_t dst, const CUtensorMap *m, int x, int y, int z, int w, int v, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, "
+      "%6}], [%7];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(v), "r"(bar)
+      : "memory");
+}
+
 // Whether a phase is over; never waits.
 __device__ __forceinline__ bool test_wait(uint32_t bar, uint32_t parity) {
   uint32_t ok;
@@ -180,7 +188,7 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
 
 }  // namespace umma
 
-// Tensor map of 16-bit elements in 3 or 4 dimensions (sizes and box innermost
+// Tensor map of 16-bit elements in 3 to 5 dimensions (sizes and box innermost
 // first, strides in bytes of all but the innermost), 128-byte swizzle.
 bool encode_16bit(CUtensorMap *m, const void *ptr, int rank, const uint64_t *dims, const uint64_t *strides,
                   const uint32_t *box);
