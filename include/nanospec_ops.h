@@ -144,7 +144,9 @@ NS_API ns_status ns_attend_paged(const void *d_q, int32_t dtype, int32_t n_seqs,
  * context for all of them, in whole tiles of 128.  They are read once for each
  * 256 rows of the group (new tokens and the query heads of a key-value head)
  * and the rest of each sequence as in ns_attend_paged; results differ from its
- * by their rounding alone.  Groups that are not as said are flagged
+ * by their rounding alone.  Where sharing would not pay (more than 128 rows to
+ * a sequence; up to 16 rows and 128 MB of keys and values by max_len) the call
+ * is that call.  Groups that are not as said are flagged
  * (NS_FLAG_BAD_SEQ) and nothing is shared; a sequence that is invalid ends its
  * group's sharing.
  * The sequences' queries follow one another as the tokens do: q_seq is
@@ -319,6 +321,18 @@ NS_API ns_status ns_attend_paged_scaled(const void *d_q, int32_t dtype, int32_t 
                                         const int32_t *d_lengths, const int32_t *d_seqs, const int64_t *d_mask,
                                         float scale, int32_t max_len, void *d_out, float *d_lse, void *d_ws,
                                         int64_t ws_bytes, ns_stream stream);
+
+/* ns_attend_shared over one layer of a cache of 8 bits, as ns_attend_paged_scaled has it (positive strides). */
+NS_API ns_status ns_attend_shared_scaled(const void *d_q, int32_t dtype, int32_t n_seqs, int32_t n, int32_t q_heads,
+                                         int32_t kv_heads, int32_t dim, int64_t q_seq, int64_t q_token,
+                                         int64_t q_head, const void *d_k, const void *d_v, int32_t n_pages,
+                                         int32_t page_size, int64_t k_page, int64_t k_head, int64_t k_token,
+                                         int64_t v_page, int64_t v_head, int64_t v_token, const uint8_t *d_k_exp,
+                                         const uint8_t *d_v_exp, int64_t ke_page, int64_t ke_head, int64_t ve_page,
+                                         int64_t ve_head, const int32_t *d_table, int32_t table_ld, int32_t max_seqs,
+                                         const int32_t *d_lengths, const int32_t *d_seqs, const int32_t *d_groups,
+                                         int32_t n_groups, const int64_t *d_mask, float scale, int32_t max_len,
+                                         void *d_out, float *d_lse, void *d_ws, int64_t ws_bytes, ns_stream stream);
 
 /*
  * Log probabilities of given tokens under softmax(logits / temperature), with

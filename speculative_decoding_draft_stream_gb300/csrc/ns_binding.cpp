@@ -347,6 +347,18 @@ PyObject *attend_paged(PyObject *const *a) {
                                          : ns_attend_paged_workspace((int32_t)B, (int32_t)n, (int32_t)hq,
                                                                      (int32_t)hkv, (int32_t)dim),
                                   d, bytes);
+  if (shared && scaled) {
+    check(ns_attend_shared_scaled(q.data_ptr(), code(type), (int32_t)B, (int32_t)n, (int32_t)hq, (int32_t)hkv,
+                                  (int32_t)dim, step(q, 0), step(q, 1), step(q, 2), k.data_ptr(), v.data_ptr(),
+                                  (int32_t)k.size(0), (int32_t)k.size(2), step(k, 0), step(k, 1), step(k, 2),
+                                  step(v, 0), step(v, 1), step(v, 2), static_cast<const uint8_t *>(ke.data_ptr()),
+                                  static_cast<const uint8_t *>(ve.data_ptr()), step(ke, 0), step(ke, 1), step(ve, 0),
+                                  step(ve, 1), table, (int32_t)ld, (int32_t)rows, lengths, seqs, groups, (int32_t)G,
+                                  mask, real(a[7], 1.0 / std::sqrt((double)dim)), (int32_t)integer(a[8], "max_len"),
+                                  out.data_ptr(), lse.data_ptr<float>(), ws.data_ptr(), bytes, current_stream(d)),
+          "ns_attend_shared_scaled");
+    return pair(std::move(out), std::move(lse));
+  }
   if (shared) {
     check(ns_attend_shared(q.data_ptr(), code(type), (int32_t)B, (int32_t)n, (int32_t)hq, (int32_t)hkv, (int32_t)dim,
                            step(q, 0), step(q, 1), step(q, 2), k.data_ptr(), v.data_ptr(), (int32_t)k.size(0),

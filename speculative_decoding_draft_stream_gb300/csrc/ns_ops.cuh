@@ -109,7 +109,7 @@ cudaError_t launch_paged_umma8(const PagedAttnArgs &a, int dtype, int dim, int s
 int64_t shared_attn_ws(int n_seqs, int n_groups, int n, int q_heads, int kv_heads, int dim, int sms);
 cudaError_t prepare_shared_attn();
 cudaError_t launch_shared_attn(const PagedAttnArgs &a, const int32_t *groups, int n_groups, int dtype, int dim,
-                               int sms, cudaStream_t st);
+                               int sms, const PagedFit &fit, cudaStream_t st);
 // and over a cache of 8 bits (ns_shared_attn8.cu).
 cudaError_t prepare_shared_attn8();
 cudaError_t launch_shared_attn8(const PagedAttnArgs &a, const int32_t *groups, int n_groups, int dtype, int dim,

@@ -231,8 +231,8 @@ static ns_status attend_paged(const void *d_q, int32_t dtype, int32_t n_seqs, in
   a.k_exp = x.k, a.v_exp = x.v, a.ke_page = x.k_page, a.ke_head = x.k_head, a.ve_page = x.v_page, a.ve_head = x.v_head;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (groups.n) {
-    if (!ns::paged_umma_ok(a)) return NS_ERR_ARG;
-    return done(ns::launch_shared_attn(a, groups.cu, groups.n, dtype, dim, d->sms, st));
+    if (!(x.k ? ns::paged_umma8_ok(a) : ns::paged_umma_ok(a))) return NS_ERR_ARG;
+    return done(ns::launch_shared_attn(a, groups.cu, groups.n, dtype, dim, d->sms, d->fit, st));
   }
   return done(x.k ? ns::launch_paged_attn8(a, dtype, dim, d->sms, d->fit, st)
                   : ns::launch_paged_attn(a, dtype, dim, d->sms, d->fit, st));
@@ -293,6 +293,24 @@ ns_status ns_attend_shared(const void *d_q, int32_t dtype, int32_t n_seqs, int32
                       page_size, k_page, k_head, k_token, v_page, v_head, v_token, Exponents{},
                       Groups{d_groups, n_groups}, d_table, table_ld, max_seqs, d_lengths, d_seqs, d_mask, scale,
                       max_len, d_out, d_lse, d_ws, ws_bytes, stream);
+}
+
+ns_status ns_attend_shared_scaled(const void *d_q, int32_t dtype, int32_t n_seqs, int32_t n, int32_t q_heads,
+                                  int32_t kv_heads, int32_t dim, int64_t q_seq, int64_t q_token, int64_t q_head,
+                                  const void *d_k, const void *d_v, int32_t n_pages, int32_t page_size, int64_t k_page,
+                                  int64_t k_head, int64_t k_token, int64_t v_page, int64_t v_head, int64_t v_token,
+                                  const uint8_t *d_k_exp, const uint8_t *d_v_exp, int64_t ke_page, int64_t ke_head,
+                                  int64_t ve_page, int64_t ve_head, const int32_t *d_table, int32_t table_ld,
+                                  int32_t max_seqs, const int32_t *d_lengths, const int32_t *d_seqs,
+                                  const int32_t *d_groups, int32_t n_groups, const int64_t *d_mask, float scale,
+                                  int32_t max_len, void *d_out, float *d_lse, void *d_ws, int64_t ws_bytes,
+                                  ns_stream stream) {
+  if (!groups_ok(n_seqs, n_groups) || (n_seqs > 0 && (!d_k_exp || !d_v_exp))) return NS_ERR_ARG;
+  return attend_paged(d_q, dtype, n_seqs, n, q_heads, kv_heads, dim, q_seq, q_token, q_head, d_k, d_v, n_pages,
+                      page_size, k_page, k_head, k_token, v_page, v_head, v_token,
+                      Exponents{d_k_exp, d_v_exp, ke_page, ke_head, ve_page, ve_head}, Groups{d_groups, n_groups},
+                      d_table, table_ld, max_seqs, d_lengths, d_seqs, d_mask, scale, max_len, d_out, d_lse, d_ws,
+                      ws_bytes, stream);
 }
 
 ns_status ns_pages_truncate(const ns_kv_pages *c, const int32_t *d_seqs, const int32_t *d_new_len, int32_t n,

@@ -1,10 +1,27 @@
-// attend_shared over a cache of 16 bits (ns_shared_attn.cuh).
+// attend_shared: whether a call shares, and the kernels over a cache of 16 bits (ns_shared_attn.cuh).
+#include <algorithm>
+
 #include "ns_shared_attn.cuh"
 
 namespace ns {
 
+// Whether a call shares.  Beyond 128 rows to a sequence its own tokens fill the row tiles, and all that sharing saves is
+// reading; and few keys are read again from L2 sooner than a plan, the parts and their merge take.  Measured, not shared
+// and shared, 32 heads on 8, 128 columns, bf16, pages of 16 (us in a graph; MB by max_len):
+//   one token:  8 sequences behind 500 (19 MB) 13.3, 20.6;  behind 2101 (69) 18.3, 21.8;  behind 4000 (129) 24.0, 25.1;
+//     behind 8000 (254) 35.6, 28.3;  16 behind 2101 (140) 25.5, 24.9;  24 (211) 32.2, 28.0;  32 behind 500 (81) 19.5,
+//     29.1;  behind 2000 (268) 38.0, 30.5;  2 behind 16000 (126) 25.9, 31.9
+//   16 sequences behind 6007:  4 new tokens 52.7, 32.3;  8: 70.7, 39.6;  16: 70.8, 54.7;  32 (128 rows): 73.7, 72.9;
+//     60 (240 rows): 88, 113
+static bool pays(const PagedAttnArgs &a, int dim) {
+  constexpr int64_t kFew = 128LL << 20;
+  const int64_t bytes = (int64_t)a.n_seqs * a.max_len * a.kv_heads * dim * (a.k_exp ? 2 : 4);
+  return a.n * a.group <= 128 && (bytes > kFew || a.n * a.group > 16);
+}
+
 int64_t shared_attn_ws(int n_seqs, int n_groups, int n, int q_heads, int kv_heads, int dim, int sms) {
-  return Layout(shape_of(n_seqs, n_groups, n, q_heads, kv_heads, sms), n_seqs, n_groups, dim).bytes;
+  const int64_t shared = Layout(shape_of(n_seqs, n_groups, n, q_heads, kv_heads, sms), n_seqs, n_groups, dim).bytes;
+  return std::max(n * (q_heads / kv_heads) <= 128 ? shared : 0, paged_attn_ws(n_seqs, n, q_heads, kv_heads, dim, sms));
 }
 
 cudaError_t prepare_shared_attn() {
@@ -12,8 +29,32 @@ cudaError_t prepare_shared_attn() {
   return e == cudaSuccess ? prepare_shared_attn8() : e;
 }
 
+// Flags groups that are not as they should be, where nothing else looks at them.
+__global__ void __launch_bounds__(256) groups_kernel(const int32_t *groups, int n_groups, int n_seqs, uint32_t *err) {
+  bool bad = groups[0] != 0 || groups[n_groups] != n_seqs;
+  for (int i = threadIdx.x; i < n_groups; i += 256) bad |= groups[i] < 0 || groups[i + 1] < groups[i];
+  if (bad) set_flag(err, NS_FLAG_BAD_SEQ);
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // (done means that what was launched before is done too)
+}
+
 cudaError_t launch_shared_attn(const PagedAttnArgs &a, const int32_t *groups, int n_groups, int dtype, int dim,
-                               int sms, cudaStream_t st) {
+                               int sms, const PagedFit &fit, cudaStream_t st) {
+  if (!pays(a, dim)) {
+    const cudaError_t e = a.k_exp ? launch_paged_attn8(a, dtype, dim, sms, fit, st)
+                                  : launch_paged_attn(a, dtype, dim, sms, fit, st);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cfg.stream = st;
+    cfg.gridDim = dim3(1);
+    cfg.blockDim = dim3(256);
+    return cudaLaunchKernelEx(&cfg, groups_kernel, groups, n_groups, a.n_seqs, a.err);
+  }
   if (a.k_exp) return launch_shared_attn8(a, groups, n_groups, dtype, dim, sms, st);
   return launch_any<false>(a, groups, n_groups, dtype, dim, sms, st);
 }

@@ -42,7 +42,7 @@ EXPORTED = (
     "ns_pages_fork", "ns_pages_workspace", "ns_pages_extend", "ns_pages_write", "ns_pages_compact", "ns_pages_copy",
     "ns_token_logprobs", "ns_norm_rotate", "ns_pages_extend_scaled", "ns_pages_compact_scaled", "ns_pages_copy_scaled",
     "ns_pages_write_scaled", "ns_pages_read", "ns_attend_paged_scaled", "ns_attend_shared_workspace",
-    "ns_attend_shared",
+    "ns_attend_shared", "ns_attend_shared_scaled",
 )
 NOALLOC_MAX_LOGITS = 1 << 20
 
@@ -131,6 +131,8 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "ns_attend_shared_workspace": (I64, [I32] * 6),
         "ns_attend_shared": (I32, [P] + [I32] * 6 + [I64] * 3 + [P, P, I32, I32] + [I64] * 6 +
                              [P, I32, I32, P, P, P, I32, P, ctypes.c_float, I32, P, P, P, I64, P]),
+        "ns_attend_shared_scaled": (I32, [P] + [I32] * 6 + [I64] * 3 + [P, P, I32, I32] + [I64] * 6 + [P, P] +
+                                    [I64] * 4 + [P, I32, I32, P, P, P, I32, P, ctypes.c_float, I32, P, P, P, I64, P]),
         "ns_token_logprobs": (I32, [P, I32, I32, I32, I64, ctypes.c_float, P, I32, I32] + [P] * 6),
     }
     for name, (res, args) in sig.items():

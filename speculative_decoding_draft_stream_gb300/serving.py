@@ -139,20 +139,23 @@ def attend_shared(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
                   lengths: torch.Tensor, seqs: torch.Tensor, groups: torch.Tensor, *,
                   mask: Optional[torch.Tensor] = None, scale: Optional[float] = None, max_len: int = 0,
                   out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
-                  workspace: Optional[torch.Tensor] = None, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+                  workspace: Optional[torch.Tensor] = None, k_exp: Optional[torch.Tensor] = None,
+                  v_exp: Optional[torch.Tensor] = None, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
     """attend_paged for groups of sequences that begin with the same pages, as samples of one prompt do after
     KvPages.fork: seqs[groups[g]] .. seqs[groups[g + 1] - 1] are a group (groups int32 [G + 1], at most 512 groups, 0
     first and B last).  What the members of a group share is found in the table, in whole tiles of 128 positions, and
     read once for all of them; the rest of each sequence as in attend_paged, from whose results these differ by their
     rounding alone.  q [B, n, Hq, D]: sequences follow one another as their tokens do (stride(0) is n * stride(1)), on
-    a 16-byte boundary, with strides that are positive multiples of 8.  It pays where a group's members are many and
-    what they share is long.  Returns (out [B, n, Hq, D], lse fp32 [B, n, Hq])."""
+    a 16-byte boundary, with strides that are positive multiples of 8.  It pays where a group's members are many, what
+    they share is long and their new tokens are few; where it would not (more than 128 rows, n * Hq / Hkv, or up to 16
+    and 128 MB of keys and values by max_len), the call is attend_paged's.  k_exp and v_exp: as there.  Returns (out [B, n, Hq, D], lse fp32 [B, n, Hq])."""
     s = None if stream is None else _other(stream)
     if s is not None:
         return _on(s, lambda: attend_shared(q, k_pages, v_pages, table, lengths, seqs, groups, mask=mask, scale=scale,
-                                            max_len=max_len, out=out, lse=lse, workspace=workspace))
+                                            max_len=max_len, out=out, lse=lse, workspace=workspace, k_exp=k_exp,
+                                            v_exp=v_exp))
     return _native().attend_paged(q, k_pages, v_pages, table, lengths, seqs, mask, scale, max_len, out, lse,
-                                  workspace, None, None, groups)
+                                  workspace, k_exp, v_exp, groups)
 
 
 class KvPages:
@@ -253,13 +256,11 @@ class KvPages:
 
     def attend(self, layer: int, q: torch.Tensor, seqs: torch.Tensor, groups: Optional[torch.Tensor] = None,
                **kw) -> Tuple[torch.Tensor, torch.Tensor]:
-        """attend_paged over one layer of this cache; with groups, attend_shared (not of 8 bits)."""
-        if groups is not None:
-            if self.k_exp is not None:
-                raise ValueError("a cache of 8 bits does not share prefixes")
-            return attend_shared(q, self.k[layer], self.v[layer], self.table, self.lengths, seqs, groups, **kw)
+        """attend_paged over one layer of this cache; with groups, attend_shared."""
         if self.k_exp is not None:
             kw = dict(kw, k_exp=self.k_exp[layer], v_exp=self.v_exp[layer])
+        if groups is not None:
+            return attend_shared(q, self.k[layer], self.v[layer], self.table, self.lengths, seqs, groups, **kw)
         return attend_paged(q, self.k[layer], self.v[layer], self.table, self.lengths, seqs, **kw)
 
 

@@ -6,6 +6,7 @@ import random
 import pytest
 import torch
 
+from serving8_ref import quantise, values
 from serving_ref import attend_rows, check, with_wild_values
 
 pytestmark = pytest.mark.gpu
@@ -42,10 +43,11 @@ def signed(w):
 
 
 def run(ns, prompts, tails, n, hq, hkv, d, dtype, page, seed, mask=None, layout="plain", spoil=None, gone=(),
-        groups=None, flags=0, max_len=0):
+        groups=None, flags=0, max_len=0, wide=True):
     """prompts[g]: positions that group g's members begin with; tails[g]: what each of them holds behind, new tokens
     included.  mask: None, "tree" or words of each sequence.  spoil(k, v, row): changes pool rows, row(b, p) being
-    where position p of sequence b lies.  gone: (sequence, slot) whose page is out of range."""
+    where position p of sequence b lies.  gone: (sequence, slot) whose page is out of range.  wide: a table for 2^20
+    positions, by which a call of few rows shares, however short its sequences are."""
     g = torch.Generator().manual_seed(seed)
     rng = random.Random(seed)
     seq_of = [(i, p, t) for i, (p, ts) in enumerate(zip(prompts, tails)) for t in ts]
@@ -63,7 +65,7 @@ def run(ns, prompts, tails, n, hq, hkv, d, dtype, page, seed, mask=None, layout=
         own = held[b] - p // page
         rows.append(taken[i] + order[at:at + own])
         at += own
-    table = torch.full((B + 2, max(held + [1]) + 1), -1, dtype=torch.int32)
+    table = torch.full((B + 2, (1 << 20) // page if wide else max(held + [1]) + 1), -1, dtype=torch.int32)
     seqs = rng.sample(range(B + 2), B)
     lengths = torch.zeros(B + 2, dtype=torch.int32)
     missing = [[False] * x for x in lens]
@@ -144,6 +146,14 @@ def test_new_tokens(ns, n, mask):
     run(ns, [700, 260], [[n, n + 3, 200 + n], [n + 1] * 4], n, 12, 4, 64, F16, 16, n, mask, layout="strided")
 
 
+@pytest.mark.parametrize("n", [1, 60])
+def test_calls_that_do_not_share(ns, n):
+    """Few keys in all, or many rows: attend_paged's kernels, with the groups looked at all the same."""
+    run(ns, [700, 260], [[n, n + 3, 200 + n], [n + 1] * 4], n, 8, 2, 128, BF16, 16, 20, wide=False)
+    run(ns, [300, 300, 140], [[n, n + 1], [n + 2], [n, n]], n, 4, 1, 64, BF16, 16, 10, groups=[0, 3, 2, 5],
+        flags=ns.FLAG_BAD_SEQ, wide=False)
+
+
 def test_many_members_and_groups(ns):
     """Rows of a group over several items; groups of one; prompts that share nothing whole."""
     run(ns, [520], [[1 + i % 7 for i in range(100)]], 1, 4, 1, 128, BF16, 16, 3)
@@ -202,7 +212,7 @@ def test_pages_out_of_range(ns):
 
 def test_sequences_out_of_range_end_their_groups_sharing(ns):
     g = torch.Generator(device="cuda").manual_seed(1)
-    cache = ns.KvPages.new(1, 100, 2, 16, 64, 4, 30)
+    cache = ns.KvPages.new(1, 100, 2, 16, 64, 4, 1 << 16)
     cache.extend(i32([0]), i32([300]))
     cache.k.normal_(generator=g), cache.v.normal_(generator=g)
     cache.fork(i32([0, 0]), i32([1, 2]))
@@ -217,7 +227,7 @@ def test_sequences_out_of_range_end_their_groups_sharing(ns):
 
 def test_after_a_fork_twice_the_same_bits_and_from_a_graph(ns):
     g = torch.Generator(device="cuda").manual_seed(2)
-    cache = ns.KvPages.new(2, 400, 4, 16, 128, 10, 60)
+    cache = ns.KvPages.new(2, 400, 4, 16, 128, 10, 1 << 16)
     cache.k.normal_(generator=g), cache.v.normal_(generator=g)
     own, kids = i32([0, 1]), list(range(2, 10))
     cache.extend(own, i32([700, 333]))
@@ -258,6 +268,58 @@ def test_after_a_fork_twice_the_same_bits_and_from_a_graph(ns):
     assert all(torch.equal(x, a) for x in outs) and ns.ops_error() == 0
 
 
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("d,page", [(64, 8), (128, 16), (128, 64)])
+@pytest.mark.parametrize("n", [1, 5, 20])
+def test_eight_bits(ns, dtype, d, page, n):
+    """A cache of 8 bits, its members after a fork, against what its codes stand for (test_gpu_attention8's bounds beyond
+    16 rows)."""
+    g = torch.Generator().manual_seed(n + d)
+    prompts, tails = [700, 150], [[n, n + 40, n + 7], [n, n + 3]]
+    kids = [(i, t) for i, ts in enumerate(tails) for t in ts]
+    cache = ns.KvPages.new(2, 400, 2, page, d, 7, (1 << 20) // page, scaled=True)
+    for t in (cache.k, cache.v):
+        t.view(torch.uint8).fill_(0x7f)  # what no row stands on may be anything
+    cache.k_exp.fill_(255), cache.v_exp.fill_(255)
+    rows = {}
+
+    def write(seq, count, upto):
+        cu = torch.tensor([0, count], dtype=torch.int32, device="cuda")
+        k, v = ((torch.randn(count, 2, d, generator=g) * torch.exp(torch.randn(count, 2, 1, generator=g))).to(dtype)
+                for _ in range(2))
+        cache.write(1, i32([seq]), cu, k.cuda(), v.cuda())
+        rows[seq] = [torch.cat((a, values(*quantise(b)))) for a, b in zip(rows.get(seq, [torch.empty(0, 2, d).double()] * 2),
+                                                                          (k, v))]
+
+    cache.extend(i32([0, 1]), i32(prompts))
+    for i, p in enumerate(prompts):
+        write(i, p, p)
+    cache.fork(i32([i for i, _ in kids]), i32(list(range(2, 7))))
+    cache.extend(i32(list(range(2, 7))), i32([t for _, t in kids]))
+    for b, (i, t) in enumerate(kids):
+        rows[2 + b] = list(rows[i])
+        write(2 + b, t, t)
+    hq = 8
+    q = torch.randn(5, n, hq, d, generator=g).to(dtype)
+    out, lse = cache.attend(1, q.cuda(), i32(list(range(2, 7))), groups=i32([0, 3, 5]))
+    assert ns.ops_error() == 0
+    out, lse = out.cpu(), lse.cpu()
+    for b in range(5):
+        k, v = rows[2 + b]
+        L = len(k)
+        sees = torch.ones(n, L, dtype=torch.bool)
+        sees[:, L - n:] = torch.ones(n, n, dtype=torch.bool).tril()
+        for h in range(hq):
+            kk, vv = k[:, h // 4], v[:, h // 4]
+            o, z, to, tz = attend_rows(q[b, :, h], kk, vv, sees, d ** -0.5)
+            if dtype == F16:
+                more = 2.0 ** -25 * d ** -0.5 * q[b, :, h].double().abs().sum(-1)
+                to = to + 2 * more[:, None] * vv.abs().amax() + 2.0 ** -31 * (sees.double() @ vv.abs()) + 2.0 ** -25
+                tz = tz + more
+            check(out[b, :, h], o, to, f"out of {b} head {h}")
+            check(lse[b, :, h], z, tz, f"lse of {b} head {h}")
+
+
 def test_refusals(ns):
     cache = ns.KvPages.new(1, 8, 2, 16, 64, 4, 2)
     q, seqs = torch.zeros(4, 2, 4, 64, dtype=BF16, device="cuda"), i32([0, 1, 2, 3])
@@ -273,7 +335,6 @@ def test_refusals(ns):
         lambda: call(groups=i32([0] * 514)),
         lambda: call(q=torch.zeros(4, 3, 4, 64, dtype=BF16, device="cuda")[:, :2]),
         lambda: call(q=q.float()),
-        lambda: ns.KvPages.new(1, 8, 2, 16, 64, 4, 2, scaled=True).attend(0, q, seqs, groups=groups),
     ]
     for i, f in enumerate(bad):
         with pytest.raises((ValueError, TypeError)):
