@@ -15,6 +15,11 @@ prompts with several continuations each:
 4. accept: the path of nodes that the verifier agrees with is kept
    (``compact``), the rest is dropped, and the stream of candidates grows.
 
+With ``rotary`` the model has norms of queries and keys and rotates them by
+position (``norm_rotate``) instead of learned positions; with ``scaled`` the
+cache holds 8 bits; with ``shared`` a prompt's continuations attend to it
+together (``attend_shared``).
+
     python -m speculative_decoding_draft_stream_gb300.speculate
 """
 
@@ -26,13 +31,15 @@ from typing import List, NamedTuple, Optional, Tuple
 import torch
 
 from .nanospec import Handle
-from .serving import KvPages, attend_prompt, ops_error, token_logprobs
+from .serving import KvPages, attend_prompt, norm_rotate, ops_error, token_logprobs
 
 
 class Verifier:
-    """Attention layers with a residual stream, learned positions and an output head, in bf16."""
+    """Attention layers with a residual stream, learned positions and an output head, in bf16; with rotary, norms of
+    queries and keys and their rotation in the place of the positions."""
 
-    def __init__(self, V=512, H=256, layers=2, q_heads=4, kv_heads=2, dim=64, positions=1024, seed=0, device="cuda"):
+    def __init__(self, V=512, H=256, layers=2, q_heads=4, kv_heads=2, dim=64, positions=1024, seed=0, device="cuda",
+                 rotary=False):
         g = torch.Generator().manual_seed(seed)
 
         def weight(rows, cols, size):
@@ -44,6 +51,11 @@ class Verifier:
         width = (q_heads + 2 * kv_heads) * dim
         self.qkv = [weight(width, H, 1.5 * H ** -0.5) for _ in range(layers)]
         self.out = [weight(H, q_heads * dim, 0.5 * (q_heads * dim) ** -0.5) for _ in range(layers)]
+        self.inv_freq = None
+        if rotary:
+            self.pos = torch.zeros_like(self.pos)
+            self.inv_freq = (10000.0 ** (-torch.arange(0, dim, 2, dtype=torch.float64) / dim)).to(device)
+            self.norms = [[(1.5 + weight(1, dim, 0.2)[0]).contiguous() for _ in range(2)] for _ in range(layers)]
 
     @staticmethod
     def norm(x):
@@ -55,6 +67,9 @@ class Verifier:
         for layer in range(self.layers):
             y = (self.norm(x) @ self.qkv[layer].T).view(len(ids), -1, self.dim)
             q, k, v = y.split([self.q_heads, self.kv_heads, self.kv_heads], 1)
+            if self.inv_freq is not None:
+                q, k = norm_rotate(q, k, positions, self.inv_freq, q_weight=self.norms[layer][0],
+                                   k_weight=self.norms[layer][1], eps=1e-5)
             x = x + attend(layer, q, k, v).reshape(len(ids), -1) @ self.out[layer].T
         h = self.norm(x)
         return h, (h @ self.head.T).float()
@@ -67,11 +82,13 @@ class Answer(NamedTuple):
 
 
 def generate(model: Verifier, prompts: List[List[int]], samples: int = 2, tokens: int = 32, width: int = 4,
-             width2: int = 2, page_size: int = 16, window: int = 1024) -> Tuple[List[Answer], List[Optional[float]]]:
+             width2: int = 2, page_size: int = 16, window: int = 1024, scaled: bool = False,
+             shared: bool = False) -> Tuple[List[Answer], List[Optional[float]]]:
     """`samples` continuations of each prompt, at least `tokens` long, and the prompts' mean log probabilities (None
     for a prompt of one token, which has none to be scored).
 
-    A step's tree: the chosen token, `width` proposals for the next one, `width2` for the one after each."""
+    A step's tree: the chosen token, `width` proposals for the next one, `width2` for the one after each.  scaled: a
+    cache of 8 bits; shared: what a prompt's continuations share is read once for all of them."""
     dev = model.head.device
     i32 = {"dtype": torch.int32, "device": dev}
     n_prompts, B = len(prompts), len(prompts) * samples
@@ -81,7 +98,7 @@ def generate(model: Verifier, prompts: List[List[int]], samples: int = 2, tokens
         raise ValueError(f"{longest} positions wanted, the model has {len(model.pos)}")
     per_seq = -(-longest // page_size)
     pages = KvPages.new(model.layers, per_seq * (B + n_prompts), model.kv_heads, page_size, model.dim, B + n_prompts,
-                        per_seq, device=dev)
+                        per_seq, device=dev, scaled=scaled)
 
     # Prefill: sequences 0 .. n_prompts - 1 of the cache hold the prompts.
     ids = torch.tensor(sum(prompts, []), **i32)
@@ -123,6 +140,7 @@ def generate(model: Verifier, prompts: List[List[int]], samples: int = 2, tokens
     depths = torch.tensor(depth, **i32)
     tree_cu = torch.arange(0, (B + 1) * n, n, **i32)
     grow = torch.full((B,), n, **i32)
+    groups = torch.arange(0, B + 1, samples, **i32) if shared else None
 
     with Handle(model.V, model.H, window, max_tree=n, max_k=max(width, width2), batch=B,
                 max_prompt=max(map(len, prompts))) as heads:
@@ -151,7 +169,7 @@ def generate(model: Verifier, prompts: List[List[int]], samples: int = 2, tokens
 
             def verify(layer, q, k, v):
                 pages.write(layer, seqs, tree_cu, k, v)
-                o, _ = pages.attend(layer, q.unflatten(0, (B, n)), seqs, mask=mask, max_len=max(length) + n)
+                o, _ = pages.attend(layer, q.unflatten(0, (B, n)), seqs, groups, mask=mask, max_len=max(length) + n)
                 return o.flatten(0, 1)
 
             hidden, logits = model.forward(nodes.reshape(-1), (base[:, None] + depths).reshape(-1), verify)
@@ -191,11 +209,14 @@ def main() -> None:
     ap = argparse.ArgumentParser(description=__doc__.split("\n")[0])
     ap.add_argument("--samples", type=int, default=2)
     ap.add_argument("--tokens", type=int, default=32)
+    ap.add_argument("--rotary", action="store_true", help="rotated queries and keys with norms")
+    ap.add_argument("--scaled", action="store_true", help="a cache of 8 bits")
+    ap.add_argument("--shared", action="store_true", help="continuations of a prompt attend to it together")
     args = ap.parse_args()
     g = torch.Generator().manual_seed(1)
-    model = Verifier()
+    model = Verifier(rotary=args.rotary)
     prompts = [torch.randint(model.V, (n,), generator=g).tolist() for n in (5, 64, 131)]
-    answers, scores = generate(model, prompts, args.samples, args.tokens)
+    answers, scores = generate(model, prompts, args.samples, args.tokens, scaled=args.scaled, shared=args.shared)
     for i, a in enumerate(answers):
         score = scores[i // args.samples]
         said = "one token" if score is None else f"mean log probability {score:.2f}"
