@@ -420,7 +420,8 @@ __device__ __forceinline__ bool find_row(const ns_kv_pages &c, const int32_t *se
     if (lane == 0) set_flag(err, NS_FLAG_BAD_SEQ);
     return false;
   }
-  page = c.table[(size_t)s * c.table_ld + (int)(pos / c.page_size)], r = (int)(pos % c.page_size);
+  const int at = (int)pos;  // (below 2^31: a division of 64 bits takes a hundred instructions)
+  page = c.table[(size_t)s * c.table_ld + at / c.page_size], r = at % c.page_size;
   if (page < 0 || page >= c.pages) {
     if (lane == 0) set_flag(err, NS_FLAG_BAD_ID);
     return false;
@@ -469,34 +470,122 @@ __global__ void __launch_bounds__(kMoveThreads) write_kernel(ns_kv_pages c, int 
   }
 }
 
-// The last rows of sequences, out of the cache: the same, the other way round.
+// Where the tokens of a CTA lie, `per` of them to a warp: the page (-1: not to
+// be touched) and row of each.  Looking for a place is four or five loads one
+// after the other: with several tokens to a warp, a lane each of the first warp
+// does it for all of the CTA's.  Measured, one and four tokens to a warp, writing
+// and reading 8 bits: 960 tokens of 8 heads 4.7 and 6.2 us, 3.7 and 4.3; 32008 of
+// 4 heads 26.4 and 25.1, 20.7 and 17.1.
+struct Places {
+  int page[kMoveWarps * 4], row[kMoveWarps * 4];
+  int seq[kMoveWarps * 4], at[kMoveWarps * 4];  // the different sequences of the CTA's tokens, and their places in the call
+  int different;
+  uint32_t again;  // of them, those that stand before that place too
+};
+template <bool kWrite>
+__device__ __forceinline__ void find_rows(const ns_kv_pages &c, const int32_t *seqs, const int32_t *cu, int n,
+                                          int tokens, int per, uint32_t *err, Places &p) {
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int all = kMoveWarps * per, t = blockIdx.x * all + lane;
+  const bool mine = tid < kWarp && lane < all && t < tokens;
+  int lo = 0, t0 = 0, t1 = 0, s = -1, mark = 0, page = -1, row = 0;
+  long long pos = -1;
+  if (tid < kWarp) {
+    if (mine) {  // the last i with cu[i] <= t
+      for (int hi = n; hi - lo > 1;) {
+        const int mid = (lo + hi) >> 1;
+        if (cu[mid] <= t)
+          lo = mid;
+        else
+          hi = mid;
+      }
+      t0 = cu[lo], t1 = cu[lo + 1], s = seqs[lo];
+    }
+    const int before = __shfl_up_sync(0xffffffffu, lo, 1);
+    const uint32_t heads = __ballot_sync(0xffffffffu, mine && (lane == 0 || lo != before));
+    mark = __popc(heads & (0xffffffffu >> (31 - lane))) - 1;
+    if (kWrite) {
+      if (heads >> lane & 1) p.seq[mark] = s, p.at[mark] = lo;
+      if (lane == 0) p.different = __popc(heads), p.again = 0;
+    }
+  }
+  if (kWrite) __syncthreads();
+  if (mine && t >= t0 && t < t1) {  // (a token of no sequence is left alone)
+    const int len = seq_ok(c, s) ? c.lengths[s] : -1;
+    pos = (long long)len - (t1 - t);
+    if (len < 0 || !len_ok(c, len) || pos < 0) {
+      set_flag(err, NS_FLAG_BAD_SEQ);
+    } else {
+      page = c.table[(size_t)s * c.table_ld + (int)pos / c.page_size], row = (int)pos % c.page_size;
+      if (page < 0 || page >= c.pages) {
+        set_flag(err, NS_FLAG_BAD_ID);
+        page = -1;
+      }
+    }
+  }
+  if (kWrite) {  // only the first of a repeated sequence
+    uint32_t again = 0;
+    const int k = p.different, most = k ? p.at[k - 1] : 0;
+    for (int j = tid; j < most; j += kMoveThreads) {
+      const int x = seqs[j];
+      for (int d = 0; d < k; ++d)
+        if (x == p.seq[d] && j < p.at[d]) again |= 1u << d;
+    }
+    again = __reduce_or_sync(0xffffffffu, again);
+    if (lane == 0 && again) atomicOr(&p.again, again);
+    __syncthreads();
+    if (page >= 0 && (p.again >> mark & 1)) {
+      set_flag(err, NS_FLAG_BAD_SEQ);
+      page = -1;
+    } else if (page >= 0 && c.refs[page] > 1) {
+      set_flag(err, NS_FLAG_SHARED_PAGE);
+      page = -1;
+    }
+  }
+  if (tid < kWarp) p.page[lane] = page, p.row[lane] = row;
+  __syncthreads();
+}
+
+// The last rows of sequences, out of the cache: the other way round.
+template <bool kMany>
 __global__ void __launch_bounds__(kMoveThreads) read_kernel(ns_kv_pages c, int layer, const int32_t *seqs,
                                                             const int32_t *cu, int n, void *k_rows, void *v_rows,
                                                             int64_t k_token, int64_t k_head, int64_t v_token,
-                                                            int64_t v_head, int tokens, uint32_t *err) {
+                                                            int64_t v_head, int tokens, int per, uint32_t *err) {
+  __shared__ Places places;
   wait_for_previous();
   int t, page, r;
-  if (!find_row<false>(c, seqs, cu, n, tokens, err, t, page, r)) return;
+  if (kMany)
+    find_rows<false>(c, seqs, cu, n, tokens, per, err, places);
+  else if (!find_row<false>(c, seqs, cu, n, tokens, err, t, page, r))
+    return;
   const int lane = threadIdx.x & 31, cols = c.row_bytes / 16, units = c.heads * cols;
-  const char *ks = static_cast<const char *>(c.k) + layer * c.k_layer + page * c.k_page + r * c.k_token;
-  const char *vs = static_cast<const char *>(c.v) + layer * c.v_layer + page * c.v_page + r * c.v_token;
-  char *kd = static_cast<char *>(k_rows) + t * k_token, *vd = static_cast<char *>(v_rows) + t * v_token;
-  for (int x0 = lane; x0 < units; x0 += kWarp * 4) {
-    uint4 a[4], b[4];
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int x = x0 + q * kWarp;
-      if (x < units) {
-        a[q] = *reinterpret_cast<const uint4 *>(ks + x / cols * c.k_head + x % cols * 16);
-        b[q] = *reinterpret_cast<const uint4 *>(vs + x / cols * c.v_head + x % cols * 16);
-      }
+  for (int i = 0; i < (kMany ? per : 1); ++i) {
+    if (kMany) {
+      const int at = (threadIdx.x >> 5) * per + i;
+      t = blockIdx.x * kMoveWarps * per + at, page = places.page[at], r = places.row[at];
+      if (page < 0) continue;
     }
+    const char *ks = static_cast<const char *>(c.k) + layer * c.k_layer + page * c.k_page + r * c.k_token;
+    const char *vs = static_cast<const char *>(c.v) + layer * c.v_layer + page * c.v_page + r * c.v_token;
+    char *kd = static_cast<char *>(k_rows) + t * k_token, *vd = static_cast<char *>(v_rows) + t * v_token;
+    for (int x0 = lane; x0 < units; x0 += kWarp * 4) {
+      uint4 a[4], b[4];
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int x = x0 + q * kWarp;
-      if (x < units) {
-        *reinterpret_cast<uint4 *>(kd + x / cols * k_head + x % cols * 16) = a[q];
-        *reinterpret_cast<uint4 *>(vd + x / cols * v_head + x % cols * 16) = b[q];
+      for (int q = 0; q < 4; ++q) {
+        const int x = x0 + q * kWarp;
+        if (x < units) {
+          a[q] = *reinterpret_cast<const uint4 *>(ks + x / cols * c.k_head + x % cols * 16);
+          b[q] = *reinterpret_cast<const uint4 *>(vs + x / cols * c.v_head + x % cols * 16);
+        }
+      }
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int x = x0 + q * kWarp;
+        if (x < units) {
+          *reinterpret_cast<uint4 *>(kd + x / cols * k_head + x % cols * 16) = a[q];
+          *reinterpret_cast<uint4 *>(vd + x / cols * v_head + x % cols * 16) = b[q];
+        }
       }
     }
   }
@@ -540,66 +629,68 @@ __device__ __forceinline__ uint4 from_codes(const uint2 &c, uint32_t byte) {
   return x;
 }
 
-// write and read of a cache of 8 bits: a warp per token, D / 8 lanes a row.
+// write and read of a cache of 8 bits: D / 8 lanes have a row, a warp its
+// tokens' rows, some heads at a time, kScaledUnroll of each of k and v in flight.
 constexpr int kScaledUnroll = 4;
-template <typename T, int D, bool kWrite>
-__global__ void __launch_bounds__(kMoveThreads)
+template <typename T, int D, bool kWrite, bool kMany>
+__global__ void __launch_bounds__(kMoveThreads, 4)
     scaled_kernel(ns_kv_pages c, const ns_kv_scales sc, int layer, const int32_t *seqs, const int32_t *cu, int n,
                   void *k_rows, void *v_rows, int64_t k_token, int64_t k_head, int64_t v_token, int64_t v_head,
-                  int tokens, uint32_t *err) {
+                  int tokens, int per, uint32_t *err) {
   constexpr int kPer = kWarp * 8 / D, U = kScaledUnroll;  // heads at once
+  __shared__ Places places;
   wait_for_previous();
-  int t, page, r;
-  if (!find_row<kWrite>(c, seqs, cu, n, tokens, err, t, page, r)) return;
-  const int lane = threadIdx.x & 31, sub = lane / (D / 8), col = lane % (D / 8);
-  char *kc = static_cast<char *>(c.k) + layer * c.k_layer + page * c.k_page + r * c.k_token + col * 8;
-  char *vc = static_cast<char *>(c.v) + layer * c.v_layer + page * c.v_page + r * c.v_token + col * 8;
-  char *kr = static_cast<char *>(k_rows) + t * k_token + col * 16, *vr = static_cast<char *>(v_rows) + t * v_token + col * 16;
-  uint8_t *ke = sc.k + layer * sc.k_layer + page * sc.k_page + r, *ve = sc.v + layer * sc.v_layer + page * sc.v_page + r;
-  for (int h0 = 0; h0 < c.heads; h0 += kPer * U) {
-    if constexpr (kWrite) {
-      uint4 x[U][2];
+  int t, one_page, one_row;
+  if (kMany)
+    find_rows<kWrite>(c, seqs, cu, n, tokens, per, err, places);
+  else if (!find_row<kWrite>(c, seqs, cu, n, tokens, err, t, one_page, one_row))
+    return;
+  const int lane = threadIdx.x & 31, sub = lane / (D / 8), col = lane % (D / 8), first = (threadIdx.x >> 5) * per;
+  if (kMany) t = blockIdx.x * kMoveWarps * per + first;
+  char *kc = static_cast<char *>(c.k) + layer * c.k_layer + col * 8, *vc = static_cast<char *>(c.v) + layer * c.v_layer + col * 8;
+  uint8_t *ke = sc.k + layer * sc.k_layer, *ve = sc.v + layer * sc.v_layer;
+  char *kr = static_cast<char *>(k_rows) + (int64_t)t * k_token + col * 16;
+  char *vr = static_cast<char *>(v_rows) + (int64_t)t * v_token + col * 16;
+  const int groups = (c.heads + kPer - 1) / kPer, units = (kMany ? per : 1) * groups;  // heads at once, of all tokens
+  for (int u0 = 0, next = 0, h0 = 0; u0 < units; u0 += U) {  // (next: the next unit's token, h0: its first head)
+    uint4 x[U][2];  // (read: the codes in the first two words, the exponents in the others)
+    int page[U], row[U], head[U], tok[U];
 #pragma unroll
-      for (int q = 0; q < U; ++q) {
-        const int h = h0 + q * kPer + sub;
-        x[q][0] = x[q][1] = make_uint4(0, 0, 0, 0);
-        if (h < c.heads) {
-          x[q][0] = __ldcs(reinterpret_cast<const uint4 *>(kr + h * k_head));
-          x[q][1] = __ldcs(reinterpret_cast<const uint4 *>(vr + h * v_head));
-        }
+    for (int q = 0; q < U; ++q) {
+      const int u = u0 + q;
+      tok[q] = next, head[q] = h0 + sub;
+      h0 += kPer;
+      if (kMany && h0 >= c.heads) h0 = 0, ++next;
+      page[q] = u < units && head[q] < c.heads ? (kMany ? places.page[first + tok[q]] : one_page) : -1;
+      row[q] = !kMany ? one_row : u < units ? places.row[first + tok[q]] : 0;
+      x[q][0] = x[q][1] = make_uint4(0, 0, 0, 0);
+      if (page[q] < 0) continue;
+      if constexpr (kWrite) {
+        x[q][0] = __ldcs(reinterpret_cast<const uint4 *>(kr + tok[q] * k_token + head[q] * k_head));
+        x[q][1] = __ldcs(reinterpret_cast<const uint4 *>(vr + tok[q] * v_token + head[q] * v_head));
+      } else {
+        const uint2 a = *reinterpret_cast<const uint2 *>(kc + page[q] * c.k_page + row[q] * c.k_token + head[q] * c.k_head);
+        const uint2 b = *reinterpret_cast<const uint2 *>(vc + page[q] * c.v_page + row[q] * c.v_token + head[q] * c.v_head);
+        x[q][0] = make_uint4(a.x, a.y, ke[page[q] * sc.k_page + head[q] * sc.k_head + row[q]], 0);
+        x[q][1] = make_uint4(b.x, b.y, ve[page[q] * sc.v_page + head[q] * sc.v_head + row[q]], 0);
       }
+    }
 #pragma unroll
-      for (int q = 0; q < U; ++q) {
-        const int h = h0 + q * kPer + sub;
-        if (h0 + q * kPer >= c.heads) break;
+    for (int q = 0; q < U; ++q) {
+      if constexpr (kWrite) {
         uint32_t bk, bv;
         const uint2 a = to_codes<T, D>(x[q][0], bk), b = to_codes<T, D>(x[q][1], bv);
-        if (h < c.heads) {
-          *reinterpret_cast<uint2 *>(kc + h * c.k_head) = a;
-          *reinterpret_cast<uint2 *>(vc + h * c.v_head) = b;
-          if (col == 0) ke[h * sc.k_head] = (uint8_t)bk;
-          if (col == 1) ve[h * sc.v_head] = (uint8_t)bv;
-        }
-      }
-    } else {
-      uint2 x[U][2];
-      uint32_t e[U][2];
-#pragma unroll
-      for (int q = 0; q < U; ++q) {
-        const int h = h0 + q * kPer + sub;
-        if (h < c.heads) {
-          x[q][0] = *reinterpret_cast<const uint2 *>(kc + h * c.k_head);
-          x[q][1] = *reinterpret_cast<const uint2 *>(vc + h * c.v_head);
-          e[q][0] = ke[h * sc.k_head], e[q][1] = ve[h * sc.v_head];
-        }
-      }
-#pragma unroll
-      for (int q = 0; q < U; ++q) {
-        const int h = h0 + q * kPer + sub;
-        if (h < c.heads) {
-          *reinterpret_cast<uint4 *>(kr + h * k_head) = from_codes<T>(x[q][0], e[q][0]);
-          *reinterpret_cast<uint4 *>(vr + h * v_head) = from_codes<T>(x[q][1], e[q][1]);
-        }
+        if (page[q] < 0) continue;
+        *reinterpret_cast<uint2 *>(kc + page[q] * c.k_page + row[q] * c.k_token + head[q] * c.k_head) = a;
+        *reinterpret_cast<uint2 *>(vc + page[q] * c.v_page + row[q] * c.v_token + head[q] * c.v_head) = b;
+        if (col == 0) ke[page[q] * sc.k_page + head[q] * sc.k_head + row[q]] = (uint8_t)bk;
+        if (col == 1) ve[page[q] * sc.v_page + head[q] * sc.v_head + row[q]] = (uint8_t)bv;
+      } else {
+        if (page[q] < 0) continue;
+        *reinterpret_cast<uint4 *>(kr + tok[q] * k_token + head[q] * k_head) =
+            from_codes<T>(make_uint2(x[q][0].x, x[q][0].y), x[q][0].z);
+        *reinterpret_cast<uint4 *>(vr + tok[q] * v_token + head[q] * v_head) =
+            from_codes<T>(make_uint2(x[q][1].x, x[q][1].y), x[q][1].z);
       }
     }
   }
@@ -751,13 +842,19 @@ cudaError_t launch_pages_write(const ns_kv_pages &c, int layer, const int32_t *s
                 k_new, v_new, k_token, k_head, v_token, v_head, tokens, err);
 }
 
+// Four tokens to a warp where there are enough for every SM to have some warps all the same.
+int tokens_of_warp(int tokens) { return tokens >= 8192 ? 4 : 1; }
+
 template <typename T, bool kWrite>
 cudaError_t launch_scaled(const ns_kv_pages &c, const ns_kv_scales &sc, int layer, const int32_t *seqs,
                           const int32_t *cu, int n, void *k, void *v, int64_t k_token, int64_t k_head,
                           int64_t v_token, int64_t v_head, int tokens, uint32_t *err, cudaStream_t st) {
-  return launch(c.row_bytes == 128 ? scaled_kernel<T, 128, kWrite> : scaled_kernel<T, 64, kWrite>,
-                dim3((tokens + kMoveWarps - 1) / kMoveWarps), kMoveThreads, 0, st, c, sc, layer, seqs, cu, n, k, v,
-                k_token, k_head, v_token, v_head, tokens, err);
+  const int per = tokens_of_warp(tokens);
+  auto *kernel = c.row_bytes == 128 ? per > 1 ? scaled_kernel<T, 128, kWrite, true> : scaled_kernel<T, 128, kWrite, false>
+                 : per > 1          ? scaled_kernel<T, 64, kWrite, true>
+                                    : scaled_kernel<T, 64, kWrite, false>;
+  return launch(kernel, dim3((tokens + kMoveWarps * per - 1) / (kMoveWarps * per)), kMoveThreads, 0, st, c, sc, layer, seqs, cu,
+                n, k, v, k_token, k_head, v_token, v_head, tokens, per, err);
 }
 
 cudaError_t launch_pages_write_scaled(const ns_kv_pages &c, const ns_kv_scales &sc, int layer, const int32_t *seqs,
@@ -774,9 +871,11 @@ cudaError_t launch_pages_write_scaled(const ns_kv_pages &c, const ns_kv_scales &
 cudaError_t launch_pages_read(const ns_kv_pages &c, const ns_kv_scales *sc, int layer, const int32_t *seqs,
                               const int32_t *cu, int n, void *k, void *v, int dtype, int64_t k_token, int64_t k_head,
                               int64_t v_token, int64_t v_head, int tokens, uint32_t *err, cudaStream_t st) {
-  if (!sc)
-    return launch(read_kernel, dim3((tokens + kMoveWarps - 1) / kMoveWarps), kMoveThreads, 0, st, c, layer, seqs, cu,
-                  n, k, v, k_token, k_head, v_token, v_head, tokens, err);
+  if (!sc) {
+    const int per = tokens_of_warp(tokens);
+    return launch(per > 1 ? read_kernel<true> : read_kernel<false>, dim3((tokens + kMoveWarps * per - 1) / (kMoveWarps * per)), kMoveThreads, 0, st, c,
+                  layer, seqs, cu, n, k, v, k_token, k_head, v_token, v_head, tokens, per, err);
+  }
   return dtype == NS_DTYPE_BF16 ? launch_scaled<__nv_bfloat16, false>(c, *sc, layer, seqs, cu, n, k, v, k_token,
                                                                       k_head, v_token, v_head, tokens, err, st)
                                 : launch_scaled<__half, false>(c, *sc, layer, seqs, cu, n, k, v, k_token, k_head,

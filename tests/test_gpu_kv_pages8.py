@@ -241,6 +241,44 @@ def test_read_of_ragged_sequences(ns, scaled):
     assert (mark[:2] == 5).all() and ns.ops_error(clear=True) == ns.FLAG_BAD_SEQ
 
 
+@pytest.mark.parametrize("scaled", [False, True])
+@pytest.mark.parametrize("short", [3, 200])
+def test_many_tokens(ns, scaled, short):
+    """Calls of which a warp takes several tokens: long sequences and many of a few, one a second time, one that does not
+    exist, one whose page another holds, and tokens behind the last."""
+    g = torch.Generator().manual_seed(short)
+    lens = [5001] + [1 + i % 7 for i in range(short)] + [3100, 1, 17]
+    B = len(lens)
+    c = ns.KvPages.new(1, 700 + B, 2, 16, 64, B + 3, 400, scaled=scaled)
+    c.extend(i32(list(range(B))), i32(lens))
+    c.fork(i32([B - 1]), i32([B]))
+    for t in (c.k, c.v):
+        t.view(torch.uint8 if scaled else BF16).zero_()
+    order = list(range(B)) + [0, B + 7]  # a sequence again, one that is not there
+    took = lens + [40, 9]
+    cu = [0]
+    for n in took:
+        cu.append(cu[-1] + n)
+    T = cu[-1] + 30
+    assert T >= 8192
+    k, v = (torch.randn(T, 2, 64, generator=g).to(BF16) for _ in range(2))
+    c.write(0, i32(order), i32(cu), k.cuda(), v.cuda())
+    assert ns.ops_error(clear=True) == ns.FLAG_BAD_SEQ | ns.FLAG_SHARED_PAGE
+    mark = torch.full((2, T, 2, 64), 7.0, dtype=BF16, device="cuda")
+    got = c.read(0, i32(order), i32(cu), T, k_out=mark[0], v_out=mark[1])
+    assert ns.ops_error(clear=True) == ns.FLAG_BAD_SEQ
+    for x, out in zip((k, v), got):
+        want = values(*quantise(x)).to(BF16) if scaled else x
+        want = want.clone()
+        want[cu[B - 1]:cu[B]] = 0  # (another holds its page: as it was)
+        want[cu[B]:cu[B + 1]] = want[4961:5001]  # the first one's rows, not the second's
+        want[cu[B + 1]:] = 7  # nothing there
+        if scaled:
+            fresh = cu[B - 1], cu[B]
+            want[fresh[0]:fresh[1]] = out[fresh[0]:fresh[1]].cpu()  # (no exponents yet)
+        assert torch.equal(out.cpu(), want)
+
+
 def test_invalid_writes_are_skipped(ns):
     c = ns.KvPages.new(1, 8, 2, 8, 64, 4, 4, scaled=True)
     c.k.view(torch.uint8).zero_(), c.v.view(torch.uint8).zero_()
