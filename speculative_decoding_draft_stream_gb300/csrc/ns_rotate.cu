@@ -21,7 +21,11 @@
 // heads.  Long calls take chunks of several heads (a row's arithmetic is about
 // 110 instructions a lane, a chunk's angles 350), short ones a head to each.
 //
-// Bound by HBM where there are many tokens, by the launch where there are few.
+// Bound by HBM where there are many tokens, by the launch where there are few:
+// 62.0 us for 335 MB (80 % of a copy's rate), 5.7 us for 15.7 MB, 2.7 us for
+// one token.  Two rows' loads in flight a lane and 3 CTAs an SM: with four rows
+// and 2 CTAs 64.7, 6.4 and 2.9 us, with two rows and 4 CTAs (spills) 67.9, 5.9
+// and 3.3.  Chunks of at most 4 heads took 67.0 us, of 16 71.5.
 #include "ns_attn_tile.cuh"
 #include "ns_internal.cuh"
 #include "ns_ops.cuh"
@@ -32,7 +36,7 @@ namespace {
 using attn::Type;
 
 constexpr int kRotThreads = 256;
-constexpr int kInFlight = 4;  // rows whose loads a lane has under way
+constexpr int kInFlight = 2;  // rows whose loads a lane has under way
 
 // f / (2 pi) modulo 1 in units of 2^-64 turns.
 __device__ __forceinline__ int64_t turns(double f) {
@@ -47,7 +51,8 @@ __device__ __forceinline__ int64_t turns(double f) {
 }
 
 template <typename T, int D, bool kNeighbours>
-__global__ void __launch_bounds__(kRotThreads) rotate_kernel(const RotateArgs a, int chunk, int q_chunks, int chunks) {
+__global__ void __launch_bounds__(kRotThreads, 3)
+    rotate_kernel(const RotateArgs a, int chunk, int q_chunks, int chunks) {
   constexpr int L = D / 16, kRows = kRotThreads / L;
   __shared__ int64_t s_turns[D / 2];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -143,7 +148,8 @@ __global__ void __launch_bounds__(kRotThreads) rotate_kernel(const RotateArgs a,
 
 template <typename T, int D, bool kNeighbours>
 cudaError_t launch(const RotateArgs &a, int sms, cudaStream_t st) {
-  // The largest chunk, up to 8 heads, that leaves each SM 64 rows at work.
+  // The largest chunk, up to 8 heads, that leaves each SM 64 rows at work: one of 256 rows
+  // took 7.4 us for 15.7 MB where this takes 5.7, and made no difference at 335 MB.
   const long long rows = (long long)a.tokens * (a.q_heads + a.kv_heads);
   int chunk = 1;
   while (chunk < 8 && rows / (2 * chunk) >= 64LL * sms) chunk *= 2;
