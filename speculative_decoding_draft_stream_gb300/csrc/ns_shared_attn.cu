@@ -5,9 +5,9 @@
 
 namespace ns {
 
-// Whether a call shares.  Beyond 128 rows to a sequence its own tokens fill the row tiles, and all that sharing saves is
-// reading; and few keys are read again from L2 sooner than a plan, the parts and their merge take.  Measured, not shared
-// and shared, 32 heads on 8, 128 columns, bf16, pages of 16 (us in a graph; MB by max_len):
+// Whether a call shares.  Beyond 128 rows to a sequence its own tokens fill the row tiles, and all that sharing saves
+// is reading; and few keys are read again from L2 sooner than a plan, the parts and their merge take.  Measured, not
+// shared and shared, 32 heads on 8, 128 columns, bf16, pages of 16 (us in a graph; MB by max_len):
 //   one token:  8 sequences behind 500 (19 MB) 13.3, 20.6;  behind 2101 (69) 18.3, 21.8;  behind 4000 (129) 24.0, 25.1;
 //     behind 8000 (254) 35.6, 28.3;  16 behind 2101 (140) 25.5, 24.9;  24 (211) 32.2, 28.0;  32 behind 500 (81) 19.5,
 //     29.1;  behind 2000 (268) 38.0, 30.5;  2 behind 16000 (126) 25.9, 31.9
@@ -31,11 +31,11 @@ cudaError_t prepare_shared_attn() {
 
 // Flags groups that are not as they should be, where nothing else looks at them.
 __global__ void __launch_bounds__(256) groups_kernel(const int32_t *groups, int n_groups, int n_seqs, uint32_t *err) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // (what writes the groups may still run until then)
   bool bad = groups[0] != 0 || groups[n_groups] != n_seqs;
   for (int i = threadIdx.x; i < n_groups; i += 256) bad |= groups[i] < 0 || groups[i + 1] < groups[i];
   if (bad) set_flag(err, NS_FLAG_BAD_SEQ);
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // (done means that what was launched before is done too)
 }
 
 cudaError_t launch_shared_attn(const PagedAttnArgs &a, const int32_t *groups, int n_groups, int dtype, int dim,
