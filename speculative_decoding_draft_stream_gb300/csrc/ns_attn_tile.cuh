@@ -157,11 +157,6 @@ __device__ __forceinline__ void lds16(uint32_t a, uint32_t *r) {
 __device__ __forceinline__ void lds8(uint32_t a, uint32_t *r) {
   asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(a) : "memory");
 }
-__device__ __forceinline__ uint32_t lds2(uint32_t a) {
-  uint16_t r;
-  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(r) : "r"(a) : "memory");
-  return r;
-}
 __device__ __forceinline__ uint32_t lds1(uint32_t a) {
   uint32_t r;
   asm volatile("ld.shared.u8 %0, [%1];" : "=r"(r) : "r"(a) : "memory");
@@ -310,9 +305,9 @@ struct Rows {
   __device__ __forceinline__ void tile8(const uint32_t (*q)[4], uint32_t sK, uint32_t sV, uint32_t sKe, uint32_t sVe,
                                         int k0, const float *cq, const Hidden &hidden, bool wild) {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    static_assert(NK % 32 == 0 || NK == 16, "a lane an exponent, or two lanes");
+    static_assert(NK % 32 == 0, "a lane an exponent");
     float s[NK / 8][4];
-    constexpr int kAtOnce = NK < 32 ? NK / 8 : 4;  // eights of keys whose products take turns
+    constexpr int kAtOnce = 4;  // eights of keys whose products take turns
 #pragma unroll
     for (int i0 = 0; i0 < NK / 8; i0 += kAtOnce) {
       uint32_t w[kAtOnce][D / 16];
@@ -334,13 +329,13 @@ struct Rows {
         for (int i = 0; i < kAtOnce; ++i)
           Type<T>::mma_free(s[i0 + i], q[kk], from_e4m3(w[i][kk]), from_e4m3_hi(w[i][kk]));
     }
-    // A lane turns one key's two exponents into factors (NK > 32: one of each 32), and the others ask it.
+    // A lane turns one key's two exponents of each 32 into factors, and the others ask it.
     float top[2] = {kNegInf, kNegInf};
     float unit[NK / 8][2];  // 2^-ve
-    uint32_t bad[(NK + 31) / 32];  // keys whose value is NaN
+    uint32_t bad[NK / 32];  // keys whose value is NaN
 #pragma unroll
     for (int b0 = 0; b0 < NK; b0 += 32) {
-      const int at = k0 + b0 + (NK < 32 ? lane & (NK - 1) : lane);
+      const int at = k0 + b0 + lane;
       const uint32_t bk = lds1(sKe + at), byte = lds1(sVe + at), bv = byte == 255u ? 127u : byte;
       bad[b0 / 32] = __ballot_sync(0xffffffffu, byte == 255u);
       const float f = __uint_as_float(bk << 23);  // (255: infinity, and NaN with what is added)
@@ -348,7 +343,7 @@ struct Rows {
       const float add = bk == 255u ? __uint_as_float(0x7fffffffu) : __uint_as_float(0x4b000000u | bv) - 8388735.f;
       const float u = __uint_as_float((254u - bv) << 23);
 #pragma unroll
-      for (int i = b0 / 8; i < (b0 + 32 < NK ? b0 + 32 : NK) / 8; ++i)
+      for (int i = b0 / 8; i < b0 / 8 + 4; ++i)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const int from = i * 8 - b0 + 2 * t + e;
@@ -385,14 +380,15 @@ struct Rows {
       }
     uint32_t any_bad = 0;
 #pragma unroll
-    for (int b = 0; b < (NK + 31) / 32; ++b) any_bad |= bad[b];
+    for (int b = 0; b < NK / 32; ++b) any_bad |= bad[b];
     if (any_bad) {  // (after l: a value is no part of it)
 #pragma unroll
       for (int i = 0; i < NK / 8; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const int key = i * 8 + 2 * t + (j & 1);
-          if ((bad[key / 32] >> (key % 32) & 1) && !(kMasked && hidden(j >> 1, key))) s[i][j] = __uint_as_float(0x7fffffffu);
+          if ((bad[key / 32] >> (key % 32) & 1) && !(kMasked && hidden(j >> 1, key)))
+            s[i][j] = __uint_as_float(0x7fffffffu);
         }
     }
 #pragma unroll

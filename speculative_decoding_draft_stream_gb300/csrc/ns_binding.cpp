@@ -481,7 +481,8 @@ PyObject *extend(PyObject *const *a) {
   const at::Tensor ws = workspace(a[3], ns_pages_workspace(&c.c, (int32_t)n), c.device, bytes);
   const ns_stream st = current_stream(c.device);
   if (c.scaled)
-    check(ns_pages_extend_scaled(&c.c, &c.s, seqs, add, (int32_t)n, ws.data_ptr(), bytes, st), "ns_pages_extend_scaled");
+    check(ns_pages_extend_scaled(&c.c, &c.s, seqs, add, (int32_t)n, ws.data_ptr(), bytes, st),
+          "ns_pages_extend_scaled");
   else
     check(ns_pages_extend(&c.c, seqs, add, (int32_t)n, ws.data_ptr(), bytes, st), "ns_pages_extend");
   return none();

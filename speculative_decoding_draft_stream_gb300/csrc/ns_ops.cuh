@@ -84,7 +84,8 @@ struct PagedAttnArgs {
 };
 // What a device holds of the kernels for few rows (found when it is first used).
 struct PagedFit {
-  int clusters[3][2][2][2];  // resident at once: cache of 16 bits, of 8, of 8 with 8 rows; dtype; dim 64, 128; small, large
+  // resident at once: cache of 16 bits, of 8, of 8 with 8 rows; dtype; dim 64, 128; small, large
+  int clusters[3][2][2][2];
 };
 int64_t paged_attn_ws(int n_seqs, int n, int q_heads, int kv_heads, int dim, int sms);
 cudaError_t prepare_paged_attn(PagedFit *fit);

@@ -180,10 +180,10 @@ static ns_status attend_paged(const void *d_q, int32_t dtype, int32_t n_seqs, in
                               int32_t kv_heads, int32_t dim, int64_t q_seq, int64_t q_token, int64_t q_head,
                               const void *d_k, const void *d_v, int32_t n_pages, int32_t page_size, int64_t k_page,
                               int64_t k_head, int64_t k_token, int64_t v_page, int64_t v_head, int64_t v_token,
-                              const Exponents &x, const Groups &groups, const int32_t *d_table, int32_t table_ld, int32_t max_seqs,
-                              const int32_t *d_lengths, const int32_t *d_seqs, const int64_t *d_mask, float scale,
-                              int32_t max_len, void *d_out, float *d_lse, void *d_ws, int64_t ws_bytes,
-                              ns_stream stream) {
+                              const Exponents &x, const Groups &groups, const int32_t *d_table, int32_t table_ld,
+                              int32_t max_seqs, const int32_t *d_lengths, const int32_t *d_seqs,
+                              const int64_t *d_mask, float scale, int32_t max_len, void *d_out, float *d_lse,
+                              void *d_ws, int64_t ws_bytes, ns_stream stream) {
   if (!attn_type(dtype, dim) || !heads_ok(q_heads, kv_heads) || n_seqs < 0 || n_seqs > NS_MAX_ATTEND_SEQS || n < 1 ||
       n > NS_MAX_NEW || n_pages < 1 || page_size < 8 || page_size > 1024 || (page_size & (page_size - 1)) ||
       table_ld < 1 || max_seqs < 1 || (int64_t)table_ld * page_size > NS_MAX_POSITIONS || max_len < 0 ||
@@ -247,7 +247,8 @@ ns_status ns_attend_paged(const void *d_q, int32_t dtype, int32_t n_seqs, int32_
                           float *d_lse, void *d_ws, int64_t ws_bytes, ns_stream stream) {
   return attend_paged(d_q, dtype, n_seqs, n, q_heads, kv_heads, dim, q_seq, q_token, q_head, d_k, d_v, n_pages,
                       page_size, k_page, k_head, k_token, v_page, v_head, v_token, Exponents{}, Groups{}, d_table,
-                      table_ld, max_seqs, d_lengths, d_seqs, d_mask, scale, max_len, d_out, d_lse, d_ws, ws_bytes, stream);
+                      table_ld, max_seqs, d_lengths, d_seqs, d_mask, scale, max_len, d_out, d_lse, d_ws, ws_bytes,
+                      stream);
 }
 
 ns_status ns_attend_paged_scaled(const void *d_q, int32_t dtype, int32_t n_seqs, int32_t n, int32_t q_heads,
@@ -337,8 +338,8 @@ int64_t ns_pages_workspace(const ns_kv_pages *c, int32_t n) {
 
 static ns_status pages_extend(const ns_kv_pages *c, const ns_kv_scales *sc, const int32_t *d_seqs,
                               const int32_t *d_n_new, int32_t n, void *d_ws, int64_t ws_bytes, ns_stream stream) {
-  if (!cache_ok(c) || !scales_ok(c, sc) || !page_seqs(n) || (n > 0 && (!d_seqs || !d_n_new || !d_ws || !aligned(d_ws, 16))) ||
-      !words(d_seqs, d_n_new))
+  if (!cache_ok(c) || !scales_ok(c, sc) || !page_seqs(n) ||
+      (n > 0 && (!d_seqs || !d_n_new || !d_ws || !aligned(d_ws, 16))) || !words(d_seqs, d_n_new))
     return NS_ERR_ARG;
   if (n == 0) return NS_OK;
   if (ws_bytes < ns::pages_extend_ws(*c, n)) return NS_ERR_ARG;
@@ -374,8 +375,9 @@ ns_status ns_pages_write(const ns_kv_pages *c, int32_t layer, const int32_t *d_s
 static ns_status pages_compact(const ns_kv_pages *c, const ns_kv_scales *sc, const int32_t *d_seqs,
                                const int32_t *d_base, const int32_t *d_keep, int32_t keep_ld, const int32_t *d_n_keep,
                                int32_t n, ns_stream stream) {
-  if (!cache_ok(c) || !scales_ok(c, sc) || !page_seqs(n) || keep_ld < 0 || (n > 0 && (!d_seqs || !d_base || !d_n_keep)) ||
-      (n > 0 && keep_ld > 0 && !d_keep) || !words(d_seqs, d_base, d_keep, d_n_keep))
+  if (!cache_ok(c) || !scales_ok(c, sc) || !page_seqs(n) || keep_ld < 0 ||
+      (n > 0 && (!d_seqs || !d_base || !d_n_keep)) || (n > 0 && keep_ld > 0 && !d_keep) ||
+      !words(d_seqs, d_base, d_keep, d_n_keep))
     return NS_ERR_ARG;
   if (n == 0) return NS_OK;
   const Device *d = nullptr;
@@ -397,7 +399,8 @@ ns_status ns_pages_compact_scaled(const ns_kv_pages *c, const ns_kv_scales *s, c
 
 static ns_status pages_copy(const ns_kv_pages *c, const ns_kv_scales *sc, const int32_t *d_src, const int32_t *d_dst,
                             int32_t n, ns_stream stream) {
-  if (!cache_ok(c) || !scales_ok(c, sc) || n < 0 || (n > 0 && (!d_src || !d_dst)) || !words(d_src, d_dst)) return NS_ERR_ARG;
+  if (!cache_ok(c) || !scales_ok(c, sc) || n < 0 || (n > 0 && (!d_src || !d_dst)) || !words(d_src, d_dst))
+    return NS_ERR_ARG;
   if (n == 0) return NS_OK;
   const Device *d = nullptr;
   if (ns_status s = current(&d)) return s;

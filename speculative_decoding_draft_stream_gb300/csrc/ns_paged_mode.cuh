@@ -69,8 +69,8 @@ struct Exponents {
 inline Exponents exponents_of(const PagedAttnArgs &p) {
   return Exponents{p.k_exp, p.v_exp, p.ke_head, p.ve_head, p.kep8, p.vep8};
 }
-// A page of 128 columns of 16 bits in one box: dimensions are 64 columns, 8 rows, the two 64s, eights of rows, pages, and
-// a head is a step of the third (heads next to each other) or of the fourth (heads a page's rows apart).
+// A page of 128 columns of 16 bits in one box: dimensions are 64 columns, 8 rows, the two 64s, eights of rows, pages,
+// and a head is a step of the third (heads next to each other) or of the fourth (heads a page's rows apart).
 constexpr int kPairShift = 5;  // pages of up to 32
 struct Pairs {
   int32_t kz, kw, vz, vw;  // a head's step in either
@@ -101,7 +101,8 @@ bool page_maps(const PagedAttnArgs &p, const Pairs &s, CUtensorMap *k, CUtensorM
   }
   const uint64_t page = 1ull << p.page_shift, e = F8 ? 1 : 2;
   const uint64_t dims[4] = {D, page, (uint64_t)p.kv_heads, (uint64_t)p.n_pages};
-  const uint64_t sk[3] = {p.k_token * e, p.k_head * e, p.k_page * e}, sv[3] = {p.v_token * e, p.v_head * e, p.v_page * e};
+  const uint64_t sk[3] = {p.k_token * e, p.k_head * e, p.k_page * e};
+  const uint64_t sv[3] = {p.v_token * e, p.v_head * e, p.v_page * e};
   const uint32_t box[4] = {F8 ? D : 64, (uint32_t)(page < fa::kKeys ? page : fa::kKeys), 1, 1};
   if (F8) return encode_8bit(k, p.k, 4, dims, sk, box, D == 128) && encode_8bit(v, p.v, 4, dims, sv, box, D == 128);
   return encode_16bit(k, p.k, 4, dims, sk, box) && encode_16bit(v, p.v, 4, dims, sv, box);

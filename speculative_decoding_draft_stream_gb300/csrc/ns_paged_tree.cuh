@@ -5,8 +5,8 @@
 // An item is 2 * (128 / group) new tokens of one sequence, all query heads of
 // one key-value head, and the sequence's keys; the CTAs have equal shares of
 // all items' tiles (ns_paged_attn.cuh).  Keys and values come page by page:
-// each page's part of a tile is one TMA box for each 64 columns, its id
-// fetched a tile ahead.  A page id out of range is a box outside the tensor,
+// each page's part of a tile is one TMA box (of 64 columns, or of a small page's
+// 128), its id fetched a tile ahead.  A page id out of range is a box outside the tensor,
 // which reads as zeros; no row sees its places.  Every row sees the context whole; in the tiles from
 // there on a row sees the new tokens of its mask, and what lies behind the
 // sequence's end is put to zero before it is used.
@@ -14,8 +14,12 @@
 // Bound by the products, the start of a CTA's items and the parts' way through
 // L2: trees of 60 nodes behind 512 to 4096 tokens, 16 sequences, 32 heads on
 // 8, bf16, pages of 16, take 56 us (0.57 PFLOP/s, 2.7 TB/s); with mma.sync
-// and 64 rows to a CTA they take nearly three times as long.  Pages of 8 take
-// 65 us: a box costs the TMA engine some 85 cycles, whatever its size.
+// and 64 rows to a CTA they take nearly three times as long.
+//
+// Over a cache of 8 bits four more warps make 16 bits of the codes that TMA has
+// brought, in place of the products' wait for them: the same trees take 70.5 us
+// (201 with mma.sync and 64 rows to a CTA), bound by that conversion, a tile's
+// keys and values one after the other.  Without kHigh's limit 77 us.
 #pragma once
 
 #include "ns_paged_mode.cuh"
@@ -148,7 +152,8 @@ struct Mode {
   using Args = TreeArgs;
   using Work = TreeWork;
   using Dealer = TreeDealer;
-  static constexpr bool kParts = true, kSplit = false, kLiveParts = false, kWhole = true, kCodes = F8, kHigh = F8, kPaired = P;
+  static constexpr bool kParts = true, kSplit = false, kLiveParts = false, kWhole = true;
+  static constexpr bool kCodes = F8, kHigh = F8, kPaired = P;
   static constexpr int kStageRow = 64;
 
   struct Loader : paged::PageLoader<TreeArgs, TreeWork, F8, P> {
@@ -346,12 +351,14 @@ cudaError_t launch(const PagedAttnArgs &p, const paged::Pairs &pairs, int sms, c
               : cudaLaunchKernelEx(&cfg, tree_join_kernel<T, D, 1>, a, ctas);
 }
 
-// A page's columns in one box where pages are small: with pages of 16 the boxes, not the products, are what a tile takes.
+// A page's columns in one box where pages are small: with pages of 16 the boxes, not the products, are what a tile
+// takes.  16 trees of 60 nodes behind 6007 tokens, pages of 16: 102 us with a box for each 64 columns, 88 so.
 template <typename T, int D, bool F8>
 cudaError_t by_pages(const PagedAttnArgs &p, int sms, cudaStream_t st) {
   paged::Pairs pairs{};
   if constexpr (D == 128 && !F8) {
-    if (p.page_shift <= paged::kPairShift && paged::page_pairs(p, &pairs)) return launch<T, D, F8, true>(p, pairs, sms, st);
+    if (p.page_shift <= paged::kPairShift && paged::page_pairs(p, &pairs))
+      return launch<T, D, F8, true>(p, pairs, sms, st);
   }
   return launch<T, D, F8, false>(p, pairs, sms, st);
 }

@@ -353,8 +353,8 @@ __global__ void __launch_bounds__(kMoveThreads)
 
 // Where token t of a call's new rows lies: a whole CTA asks, a warp for each
 // token.  False where the warp has none, or (with a flag) an invalid one; rows
-// to be written (kWrite) may not be another sequence's too.  Only the first of a repeated sequence is
-// written: up to kWarpLooks sequences each warp looks through the entries
+// to be written (kWrite) may not be another sequence's too.  Only the first of a
+// repeated sequence is written: up to kWarpLooks sequences each warp looks through the entries
 // before its own; of more, the CTA looks once for all of its warps.  Measured,
 // by warps and by the CTA: 8 sequences of 4001 tokens 35.6, 36.9 us; 64 of one
 // token 3.6, 3.8; 256 of one 4.1, 3.9; 8192 of one 23.7, 15.5.
@@ -478,7 +478,7 @@ __global__ void __launch_bounds__(kMoveThreads) write_kernel(ns_kv_pages c, int 
 // 4 heads 26.4 and 25.1, 20.7 and 17.1.
 struct Places {
   int page[kMoveWarps * 4], row[kMoveWarps * 4];
-  int seq[kMoveWarps * 4], at[kMoveWarps * 4];  // the different sequences of the CTA's tokens, and their places in the call
+  int seq[kMoveWarps * 4], at[kMoveWarps * 4];  // the CTA's different sequences, and their places in the call
   int different;
   uint32_t again;  // of them, those that stand before that place too
 };
@@ -647,7 +647,8 @@ __global__ void __launch_bounds__(kMoveThreads, 4)
     return;
   const int lane = threadIdx.x & 31, sub = lane / (D / 8), col = lane % (D / 8), first = (threadIdx.x >> 5) * per;
   if (kMany) t = blockIdx.x * kMoveWarps * per + first;
-  char *kc = static_cast<char *>(c.k) + layer * c.k_layer + col * 8, *vc = static_cast<char *>(c.v) + layer * c.v_layer + col * 8;
+  char *kc = static_cast<char *>(c.k) + layer * c.k_layer + col * 8;
+  char *vc = static_cast<char *>(c.v) + layer * c.v_layer + col * 8;
   uint8_t *ke = sc.k + layer * sc.k_layer, *ve = sc.v + layer * sc.v_layer;
   char *kr = static_cast<char *>(k_rows) + (int64_t)t * k_token + col * 16;
   char *vr = static_cast<char *>(v_rows) + (int64_t)t * v_token + col * 16;
@@ -669,8 +670,9 @@ __global__ void __launch_bounds__(kMoveThreads, 4)
         x[q][0] = __ldcs(reinterpret_cast<const uint4 *>(kr + tok[q] * k_token + head[q] * k_head));
         x[q][1] = __ldcs(reinterpret_cast<const uint4 *>(vr + tok[q] * v_token + head[q] * v_head));
       } else {
-        const uint2 a = *reinterpret_cast<const uint2 *>(kc + page[q] * c.k_page + row[q] * c.k_token + head[q] * c.k_head);
-        const uint2 b = *reinterpret_cast<const uint2 *>(vc + page[q] * c.v_page + row[q] * c.v_token + head[q] * c.v_head);
+        const char *ks = kc + page[q] * c.k_page + row[q] * c.k_token + head[q] * c.k_head;
+        const char *vs = vc + page[q] * c.v_page + row[q] * c.v_token + head[q] * c.v_head;
+        const uint2 a = *reinterpret_cast<const uint2 *>(ks), b = *reinterpret_cast<const uint2 *>(vs);
         x[q][0] = make_uint4(a.x, a.y, ke[page[q] * sc.k_page + head[q] * sc.k_head + row[q]], 0);
         x[q][1] = make_uint4(b.x, b.y, ve[page[q] * sc.v_page + head[q] * sc.v_head + row[q]], 0);
       }
@@ -712,8 +714,8 @@ constexpr int kMoveRows = 128;
 constexpr int kMoveBatch = 16;
 template <bool kScaled>
 __global__ void __launch_bounds__(kMoverWarps * 32, 4)
-    compact_kernel(ns_kv_pages c, const ns_kv_scales sc, const int32_t *seqs, const int32_t *base, const int32_t *keep, int keep_ld,
-                   const int32_t *n_keep, int seg_bytes, uint32_t *err) {
+    compact_kernel(ns_kv_pages c, const ns_kv_scales sc, const int32_t *seqs, const int32_t *base,
+                   const int32_t *keep, int keep_ld, const int32_t *n_keep, int seg_bytes, uint32_t *err) {
   __shared__ long long s_from[2][kMoveRows], s_to[2][kMoveRows];  // -1: stays
   __shared__ long long s_exp[kScaled ? 2 : 1][2][kScaled ? kMoveRows : 1];  // the same rows' bytes: from, to
   wait_for_previous();
@@ -850,11 +852,10 @@ cudaError_t launch_scaled(const ns_kv_pages &c, const ns_kv_scales &sc, int laye
                           const int32_t *cu, int n, void *k, void *v, int64_t k_token, int64_t k_head,
                           int64_t v_token, int64_t v_head, int tokens, uint32_t *err, cudaStream_t st) {
   const int per = tokens_of_warp(tokens);
-  auto *kernel = c.row_bytes == 128 ? per > 1 ? scaled_kernel<T, 128, kWrite, true> : scaled_kernel<T, 128, kWrite, false>
-                 : per > 1          ? scaled_kernel<T, 64, kWrite, true>
-                                    : scaled_kernel<T, 64, kWrite, false>;
-  return launch(kernel, dim3((tokens + kMoveWarps * per - 1) / (kMoveWarps * per)), kMoveThreads, 0, st, c, sc, layer, seqs, cu,
-                n, k, v, k_token, k_head, v_token, v_head, tokens, per, err);
+  auto *one = c.row_bytes == 128 ? scaled_kernel<T, 128, kWrite, false> : scaled_kernel<T, 64, kWrite, false>;
+  auto *many = c.row_bytes == 128 ? scaled_kernel<T, 128, kWrite, true> : scaled_kernel<T, 64, kWrite, true>;
+  return launch(per > 1 ? many : one, dim3((tokens + kMoveWarps * per - 1) / (kMoveWarps * per)), kMoveThreads, 0, st,
+                c, sc, layer, seqs, cu, n, k, v, k_token, k_head, v_token, v_head, tokens, per, err);
 }
 
 cudaError_t launch_pages_write_scaled(const ns_kv_pages &c, const ns_kv_scales &sc, int layer, const int32_t *seqs,
@@ -873,8 +874,9 @@ cudaError_t launch_pages_read(const ns_kv_pages &c, const ns_kv_scales *sc, int 
                               int64_t v_token, int64_t v_head, int tokens, uint32_t *err, cudaStream_t st) {
   if (!sc) {
     const int per = tokens_of_warp(tokens);
-    return launch(per > 1 ? read_kernel<true> : read_kernel<false>, dim3((tokens + kMoveWarps * per - 1) / (kMoveWarps * per)), kMoveThreads, 0, st, c,
-                  layer, seqs, cu, n, k, v, k_token, k_head, v_token, v_head, tokens, per, err);
+    const dim3 grid((tokens + kMoveWarps * per - 1) / (kMoveWarps * per));
+    return launch(per > 1 ? read_kernel<true> : read_kernel<false>, grid, kMoveThreads, 0, st, c, layer, seqs, cu, n,
+                  k, v, k_token, k_head, v_token, v_head, tokens, per, err);
   }
   return dtype == NS_DTYPE_BF16 ? launch_scaled<__nv_bfloat16, false>(c, *sc, layer, seqs, cu, n, k, v, k_token,
                                                                       k_head, v_token, v_head, tokens, err, st)
@@ -883,7 +885,8 @@ cudaError_t launch_pages_read(const ns_kv_pages &c, const ns_kv_scales *sc, int 
 }
 
 cudaError_t launch_pages_compact(const ns_kv_pages &c, const ns_kv_scales *sc, const int32_t *seqs,
-                                 const int32_t *base, const int32_t *keep, int keep_ld, const int32_t *n_keep, int n, uint32_t *err, cudaStream_t st) {
+                                 const int32_t *base, const int32_t *keep, int keep_ld, const int32_t *n_keep, int n,
+                                 uint32_t *err, cudaStream_t st) {
   // A warp takes up to 512 bytes of a row, less where the CTAs are too few to keep HBM busy: 16001 rows of 12 x 4
   // x 256 bytes of k and v move in 163 us by whole rows (192 CTAs), in about 118 us by halves.
   constexpr int kEnough = 304;

@@ -20,6 +20,13 @@
 // Item i of the line and CTA c meet in at most one piece, and i + c grows from
 // piece to piece, so it is the piece's place.  No atomics whose order matters:
 // the same inputs give the same bits.
+//
+// What bounds it: for few rows the chain of three kernels, each waiting for the
+// one before (8 sequences of one prompt of 2101 tokens, 32 heads on 8: 22 us,
+// and 18 where each reads it from L2, which the rule in ns_shared_attn.cu then
+// prefers); for many sequences the items' starts and the parts' way through
+// L2 (64 of four prompts of 3001 to 16000 tokens, 28 heads on 4, fp16: 55 us;
+// without sharing 162); for trees the products of all rows, shared or not.
 #pragma once
 
 #include "ns_paged_mode.cuh"
@@ -40,8 +47,8 @@ struct SharedArgs {
   void *out;
   float *lse;
   uint32_t *err;
-  // the plan: of each group its first sequence, members, shared tiles and the first's sequence in the cache; then of each
-  // sequence the cache's, its length, the tiles that it shares and its group
+  // the plan: of each group its first sequence, members, shared tiles and the first's sequence in the cache; then of
+  // each sequence the cache's, its length, the tiles that it shares and its group
   int4 *plan;
   // the line: tiles before each group's items and then each sequence's, and all; prefix items before each group's
   long long *cum;
@@ -149,7 +156,8 @@ struct Work {
 constexpr int kAllSeen = 0x7fffffff;
 // What an item's beginning and end take, in tiles: the line has that many more for each item, so that shares are equal
 // in time.  Without: 64 sequences of 4 prompts (28 heads on 4, one new token each) 68.0 us, the CTAs with the tails
-// 25 us longer at work than the others; with 1, 2, 3, 4: see the table of launch.
+// 25 us longer at work than the others.  With 2, 3 and 4: 54.5, 54.3, 56.0 us, and 8 sequences of one prompt of 2101
+// 23.8, 22.9, 24.4 (items of one row tile); 16 trees of 60 nodes behind 6007 tokens 115, 119, 120 (of two).
 template <bool S>
 constexpr int kItemCost = S ? 3 : 2;
 
@@ -274,7 +282,8 @@ struct Mode {
   using Args = SharedArgs;
   using Work = ns::Work<S>;
   using Dealer = ns::Dealer<S>;
-  static constexpr bool kParts = true, kSplit = S, kLiveParts = true, kWhole = false, kCodes = F8, kHigh = true, kPaired = P;
+  static constexpr bool kParts = true, kSplit = S, kLiveParts = true, kWhole = false;
+  static constexpr bool kCodes = F8, kHigh = true, kPaired = P;
   static constexpr int kStageRow = 64, kRows = S ? 128 : 256;  // (of a part)
 
   struct Loader : paged::PageLoader<SharedArgs, Work, F8, P> {

@@ -92,7 +92,7 @@ template <typename T, typename M>
 constexpr float kLimitOf = M::kHigh && Type<T>::kBf16 ? 1073741824.f : kLimit;
 constexpr int kChecks = 4;           // value tiles looked through ahead of the product
 constexpr int kMissingTiles = 4;     // key tiles whose missing keys are kept (see there)
-constexpr int kWorkReaders = 11;     // loads, products, hidden values, and the eight softmax warps (M::kCodes: and four)
+constexpr int kWorkReaders = 11;     // loads, products, hidden values, eight softmax warps (M::kCodes: and four)
 constexpr int kWorkBytes = 48;
 
 template <typename T>
@@ -108,8 +108,8 @@ struct Smem {
   static constexpr int kKvFull = kMisc, kKvEmpty = kKvFull + 8 * kRing, kQFull = kKvEmpty + 8 * kRing,
                        kQEmpty = kQFull + 8, kSFull = kQEmpty + 8, kPFull = kSFull + 16, kPvHalf = kPFull + 32,
                        kOFull = kPvHalf + 16, kOEmpty = kOFull + 16, kCheck = kOEmpty + 16,
-                       kMerge = kCheck + 8 * kChecks, kWFull = kMerge + 16, kWEmpty = kWFull + 16, kSlot = kWEmpty + 16, kWork = kSlot + 16,
-                       kWildAny = kWork + 2 * kWorkBytes, kMissing = kWildAny + 16,
+                       kMerge = kCheck + 8 * kChecks, kWFull = kMerge + 16, kWEmpty = kWFull + 16,
+                       kSlot = kWEmpty + 16, kWork = kSlot + 16, kWildAny = kWork + 2 * kWorkBytes, kMissing = kWildAny + 16,
                        kWild = kMissing + 4 * kMissingTiles,
                        kRawFull = kWild + 2 * (int)sizeof(typename M::Wild),  // (M::kCodes)
                        kRaw = (kRawFull + 8 * kRing + 127) / 128 * 128,
@@ -144,12 +144,13 @@ __device__ __forceinline__ uint64_t eights(uint32_t bits) {
   return (uint64_t)__vcmpne4((uint32_t)(x >> 32), 0u) << 32 | __vcmpne4((uint32_t)x, 0u);
 }
 
-// How key and value tiles lie: 64 columns of all rows and then the others, or (M::kPaired, of 128 columns) both of eight
-// rows and then of the next eight, as one TMA box brings them.
+// How key and value tiles lie: 64 columns of all rows and then the others, or (M::kPaired, of 128 columns) both of
+// eight rows and then of the next eight, as one TMA box brings them.
 template <int D, typename M>
 struct Tile {
   static constexpr bool kPair = M::kPaired && D == 128;
-  static constexpr int kEight = kPair ? 2048 : 1024, kNext = kPair ? 1024 : kHalf;  // bytes from eight rows, from 64 columns to the next
+  // bytes from eight rows, and from 64 columns, to the next
+  static constexpr int kEight = kPair ? 2048 : 1024, kNext = kPair ? 1024 : kHalf;
   // 16-byte piece c of row r, 64 columns h (before the swizzle)
   static __device__ __forceinline__ int piece(int r, int h, int c) {
     return h * kNext + (r >> 3) * kEight + (r & 7) * 128 + c * 16;
@@ -289,7 +290,8 @@ __global__ void __launch_bounds__(kThreadsOf<M>, 1)
         for (int kk = 0; kk < D / 16; ++kk) {
           if (kk == D / 16 - 2) seen = peek(bar, phase);
           // in the descriptors' 16-byte units
-          const uint32_t offA = ((kk >> 2) * kHalf + (kk & 3) * 32) >> 4, offB = ((kk >> 2) * KV::kNext + (kk & 3) * 32) >> 4;
+          const uint32_t offA = ((kk >> 2) * kHalf + (kk & 3) * 32) >> 4;
+          const uint32_t offB = ((kk >> 2) * KV::kNext + (kk & 3) * 32) >> 4;
           umma::mma_ss(tmem + t * 128, A + offA, B + offB, kIdS, kk != 0);
         }
         umma::commit(base + L::kSFull + 8 * t);

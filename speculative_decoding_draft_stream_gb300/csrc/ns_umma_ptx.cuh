@@ -128,7 +128,8 @@ __device__ __forceinline__ void tma4(uint32_t dst, const CUtensorMap *m, int x, 
       : "memory");
 }
 
-__device__ __forceinline__ void tma5(uint32_t dst, const CUtensorMap *m, int x, int y, int z, int w, int v, uint32_t bar) {
+__device__ __forceinline__ void tma5(uint32_t dst, const CUtensorMap *m, int x, int y, int z, int w, int v,
+                                     uint32_t bar) {
   asm volatile(
       "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, "
       "%6}], [%7];" ::"r"(dst),
