@@ -125,7 +125,8 @@ def attend_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, 
     the keys are split: results of another bound may differ by their rounding.  With more than 16 rows (n * Hq / Hkv)
     a q off a 16-byte boundary, or with strides other than positive multiples of 8 elements, takes about three times
     as long.  With k_exp and v_exp, uint8 [pages, Hkv, page_size], the pages are a cache of 8 bits (KvPages): codes in
-    e4m3 and the exponent of each row.  Returns (out [B, n, Hq, D], lse fp32 [B, n, Hq])."""
+    e4m3 and the exponent of each row (more than 16 rows in fp16 see at most 65504 of what bf16 rows have written).
+    Returns (out [B, n, Hq, D], lse fp32 [B, n, Hq])."""
     s = None if stream is None else _other(stream)
     if s is not None:
         return _on(s, lambda: attend_paged(q, k_pages, v_pages, table, lengths, seqs, mask=mask, scale=scale,

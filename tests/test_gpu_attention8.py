@@ -345,3 +345,25 @@ def test_refusals(ns):
     with pytest.raises(ns.NanoSpecError):
         ns.attend_paged(q, k, v, *rest, k_exp=off, v_exp=ve)
     assert ns.ops_error() == 0
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_values_beyond_fp16(ns, d):
+    """A value row of 448 * 2^10 among ones, all with the same weight: as it is for up to 16 rows, and where it is made an
+    fp16 (20 rows in fp16) 65504.  Sums of at most 64 terms are exact enough: u for a weight, u for the output."""
+    L, page = 64, 16
+    x = torch.ones(4, 1, page, d, dtype=torch.float64)
+    x[0, 0, 3] = 448.0 * 2 ** 10
+    cv, ev = quantise(x)
+    ck, ek = quantise(torch.zeros_like(x))
+    pool = [c.float().to(E4M3).cuda() for c in (ck, cv)]
+    table = torch.arange(4, dtype=torch.int32, device="cuda")[None]
+    one = torch.tensor([L], dtype=torch.int32, device="cuda")
+    for dtype, n, top in ((BF16, 1, 448.0 * 2 ** 10), (BF16, 20, 448.0 * 2 ** 10), (F16, 1, 448.0 * 2 ** 10), (F16, 20, 65504.0)):
+        q = torch.zeros(1, n, 1, d, dtype=dtype, device="cuda")
+        out, _ = ns.attend_paged(q, *pool, table, one, one - L, k_exp=ek.cuda(), v_exp=ev.cuda())
+        seen = torch.arange(L - n + 1, L + 1, dtype=torch.float64)
+        want = ((seen - 1 + top) / seen)[:, None].expand(n, d)
+        u = torch.finfo(dtype).eps
+        assert torch.allclose(out[0, :, 0].cpu().double(), want, rtol=1.1 * u, atol=0), (dtype, n)
+    assert ns.ops_error() == 0
