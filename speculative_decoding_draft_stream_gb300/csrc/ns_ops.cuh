@@ -81,12 +81,15 @@ struct PagedAttnArgs {
   const uint8_t *k_exp, *v_exp;  // a cache of 8 bits: each row's exponent
   int64_t ke_page, ke_head, ve_page, ve_head;
   int32_t kp16, kt16, vp16, vt16, kep8, vep8;  // its strides in units of 16 (exponents: 8) bytes
+  const int32_t *groups;  // to be looked at, of a call of ns_attend_shared that does not share
+  int32_t n_groups;
 };
 // What a device holds of the kernels for few rows (found when it is first used).
 struct PagedFit {
   // resident at once: cache of 16 bits, of 8, of 8 with 8 rows; dtype; dim 64, 128; small, large
   int clusters[3][2][2][2];
 };
+cudaError_t launch_groups(const PagedAttnArgs &a, cudaStream_t st);  // looks at them, after what was launched before
 int64_t paged_attn_ws(int n_seqs, int n, int q_heads, int kv_heads, int dim, int sms);
 cudaError_t prepare_paged_attn(PagedFit *fit);
 cudaError_t launch_paged_attn(const PagedAttnArgs &a, int dtype, int dim, int sms, const PagedFit &fit,

@@ -39,7 +39,26 @@ template <typename T>
 cudaError_t by_dim(const PagedAttnArgs &a, int dim, int sms, const PagedFit &fit, cudaStream_t st) {
   return dim == 128 ? by_rows<T, 128>(a, sms, fit, st) : by_rows<T, 64>(a, sms, fit, st);
 }
+
+__global__ void __launch_bounds__(256) groups_kernel(const PagedAttnArgs a) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // (what writes the groups may still run until then)
+  look_at_groups(a.groups, a.n_groups, a.n_seqs, a.err);
+}
 }  // namespace
+
+cudaError_t launch_groups(const PagedAttnArgs &a, cudaStream_t st) {
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cfg.stream = st;
+  cfg.gridDim = dim3(1);
+  cfg.blockDim = dim3(256);
+  return cudaLaunchKernelEx(&cfg, groups_kernel, a);
+}
 
 int64_t paged_attn_ws(int n_seqs, int n, int q_heads, int kv_heads, int dim, int sms) {
   // two parts for each CTA: up to 4 sms CTAs of 16 rows, or sms CTAs of 256 (3 sms of 64 are no more)

@@ -638,7 +638,8 @@ bool clusters_fit(const PagedAttnArgs &a, const PagedFit &fit) {
 template <typename T, int D, int WM, int W, bool F8>
 cudaError_t launch_clusters(const PagedAttnArgs &a, cudaStream_t st) {
   ClusterLaunch l(a.n_seqs * a.kv_heads, kThreads<W>, pa_smem<D, WM, W, F8>(), st);
-  return cudaLaunchKernelEx(&l.cfg, paged_attn_kernel<T, D, WM, W, F8>, a, 1);
+  const cudaError_t e = cudaLaunchKernelEx(&l.cfg, paged_attn_kernel<T, D, WM, W, F8>, a, 1);
+  return e != cudaSuccess || !a.groups ? e : launch_groups(a, st);
 }
 
 template <typename T, int D, int WM, int W, bool F8>

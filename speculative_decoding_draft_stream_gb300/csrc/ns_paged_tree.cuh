@@ -44,6 +44,8 @@ struct TreeArgs {
   uint32_t *err;
   paged::Exponents rows;  // (of 8 bits)
   paged::Pairs pairs;     // (Mode's P)
+  const int32_t *groups;  // (as PagedAttnArgs has them)
+  int32_t n_groups;
 };
 
 struct Work {
@@ -227,6 +229,10 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const TreeArgs 
   const bool live = in_tile < a.per_tile && node < a.n;
   const int64_t at = ((int64_t)b * a.n + node) * a.q_heads + item / a.blocks * a.pack + (rl & 127) % a.pack;
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (b == a.n_seqs) {
+    if (blockIdx.y == 0 && blockIdx.z == 0) paged::look_at_groups(a.groups, a.n_groups, a.n_seqs, a.err);
+    return;
+  }
   if (!__any_sync(0xffffffffu, live)) return;  // (every warp has the same rows)
   const long long total = a.cum[a.n_seqs], cb = a.cum[b];
   const long long nt = quotient(a.cum[b + 1] - cb, items);
@@ -325,6 +331,7 @@ cudaError_t launch(const PagedAttnArgs &p, const paged::Pairs &pairs, int sms, c
   a.cum = ws.cum, a.part_ml = ws.ml, a.part_o = ws.o;
   a.rows = paged::exponents_of(p);
   a.pairs = pairs;
+  a.groups = p.groups, a.n_groups = p.n_groups;
   CUtensorMap tmQ, tmK, tmV;
   const uint64_t dq[4] = {D, (uint64_t)p.q_heads, (uint64_t)p.n, (uint64_t)p.n_seqs};
   const uint64_t sq[3] = {(uint64_t)p.q_head * 2, (uint64_t)p.q_token * 2, (uint64_t)p.q_seq * 2};
@@ -338,7 +345,7 @@ cudaError_t launch(const PagedAttnArgs &p, const paged::Pairs &pairs, int sms, c
   cudaLaunchConfig_t cfg{};
   // an item's parts: some more than its share of the CTAs, if the sequences are of like lengths
   const bool many = ctas >= 6LL * p.n_seqs * items;
-  cfg.gridDim = dim3((unsigned)((long long)p.n_seqs * items), 8, many ? D / 32 : 1);
+  cfg.gridDim = dim3((unsigned)((long long)p.n_seqs * items + (p.groups ? 1 : 0)), 8, many ? D / 32 : 1);
   cfg.blockDim = dim3(kJoinThreads);
   cfg.dynamicSmemBytes = ctas * 4;
   cfg.stream = st;

@@ -29,31 +29,13 @@ cudaError_t prepare_shared_attn() {
   return e == cudaSuccess ? prepare_shared_attn8() : e;
 }
 
-// Flags groups that are not as they should be, where nothing else looks at them.
-__global__ void __launch_bounds__(256) groups_kernel(const int32_t *groups, int n_groups, int n_seqs, uint32_t *err) {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // (what writes the groups may still run until then)
-  bool bad = groups[0] != 0 || groups[n_groups] != n_seqs;
-  for (int i = threadIdx.x; i < n_groups; i += 256) bad |= groups[i] < 0 || groups[i + 1] < groups[i];
-  if (bad) set_flag(err, NS_FLAG_BAD_SEQ);
-}
-
 cudaError_t launch_shared_attn(const PagedAttnArgs &a, const int32_t *groups, int n_groups, int dtype, int dim,
                                int sms, const PagedFit &fit, cudaStream_t st) {
   if (!pays(a, dim)) {
-    const cudaError_t e = a.k_exp ? launch_paged_attn8(a, dtype, dim, sms, fit, st)
-                                  : launch_paged_attn(a, dtype, dim, sms, fit, st);
-    if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg{};
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    cfg.stream = st;
-    cfg.gridDim = dim3(1);
-    cfg.blockDim = dim3(256);
-    return cudaLaunchKernelEx(&cfg, groups_kernel, groups, n_groups, a.n_seqs, a.err);
+    PagedAttnArgs own = a;
+    own.groups = groups, own.n_groups = n_groups;
+    return a.k_exp ? launch_paged_attn8(own, dtype, dim, sms, fit, st)
+                   : launch_paged_attn(own, dtype, dim, sms, fit, st);
   }
   if (a.k_exp) return launch_shared_attn8(a, groups, n_groups, dtype, dim, sms, st);
   return launch_any<false>(a, groups, n_groups, dtype, dim, sms, st);

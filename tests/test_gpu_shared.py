@@ -347,3 +347,28 @@ def test_refusals(ns):
     none = ns.attend_shared(q[:0], *args[:4], seqs[:0], i32([0]))
     assert none[0].shape == (0, 2, 4, 64)
     assert ns.ops_error() == 0
+
+
+@pytest.mark.parametrize("n,hq", [(1, 4), (3, 4), (60, 4)])
+def test_many_sequences_that_do_not_share(ns, n, hq):
+    """Calls of few keys whose items are too many for clusters (and of many rows): the groups are looked at there too."""
+    tails = [[n, n + 1]] * 20
+    run(ns, [140] * 20, tails, n, hq, 2, 64, BF16, 16, 21, wide=False)
+    for groups in ([0, 20, 10, 40], [1, 40], [0, 39]):
+        run(ns, [140] * 20, tails, n, hq, 2, 64, BF16, 16, 21, groups=groups, flags=ns.FLAG_BAD_SEQ, wide=False)
+
+
+def test_groups_of_eight_bits_that_are_not_as_they_should_be(ns):
+    for B in (3, 60):  # (clusters, the line)
+        cache = ns.KvPages.new(1, 4 * B, 2, 16, 64, B, 4, scaled=True)
+        seqs, count = i32(list(range(B))), i32([50] * B)
+        cache.extend(seqs, count)
+        x = torch.randn(50 * B, 2, 64, device="cuda").to(BF16)
+        cache.write(0, seqs, i32(list(range(0, 50 * B + 1, 50))), x, x)
+        for n in (1, 4, 40):
+            q = torch.randn(B, n, 8, 64, device="cuda").to(BF16)
+            want, _ = cache.attend(0, q, seqs)
+            out, _ = cache.attend(0, q, seqs, groups=i32([0, 1, B]))
+            assert ns.ops_error() == 0 and (torch.equal(out, want) or 16 < 4 * n <= 128)
+            out, _ = cache.attend(0, q, seqs, groups=i32([0, 2, 1, B]))
+            assert ns.ops_error(clear=True) == ns.FLAG_BAD_SEQ and (torch.equal(out, want) or 16 < 4 * n <= 128)
