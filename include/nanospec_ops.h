@@ -90,7 +90,8 @@ NS_API ns_status ns_norm_rotate(const void *d_q, const void *d_k, int32_t dtype,
  *   d_out [tokens x q_heads x dim] of `dtype`, contiguous; d_lse fp32 [tokens x q_heads] or NULL
  * dim is 64 or 128.  Scores, softmax sums and the output's sums are fp32; the
  * probabilities are rounded to `dtype` before the product with v.  A value of
- * v that is not finite reaches only rows that see it.
+ * v that is not finite reaches only rows that see it; bf16 values with |v| times
+ * a sequence's length / 64 of 2^113 and more may overflow in the sums.
  */
 NS_API ns_status ns_attend_prompt(const void *d_q, const void *d_k, const void *d_v, int32_t dtype, int32_t tokens,
                                   int32_t q_heads, int32_t kv_heads, int32_t dim, int64_t q_token, int64_t q_head,
@@ -124,7 +125,10 @@ NS_API ns_status ns_attend_prompt(const void *d_q, const void *d_k, const void *
  * 1 <= n <= NS_MAX_NEW, dim 64 or 128, page_size a power of two from 8 to 1024,
  * table_ld * page_size at most NS_MAX_POSITIONS.
  * Scores, softmax sums and the output's sums are fp32; the probabilities are
- * rounded to `dtype` before the product with v, as in ns_attend_prompt.
+ * rounded to `dtype` before the product with v, as in ns_attend_prompt.  With
+ * more than 16 rows, as there, a sum of the output may pass its final size on
+ * its way by 2^15 for each 64 keys: bf16 values v with |v| len / 64 of 2^113
+ * and more may overflow (16 rows: |v| len of 2^128).
  */
 NS_API int64_t ns_attend_paged_workspace(int32_t n_seqs, int32_t n, int32_t q_heads, int32_t kv_heads, int32_t dim);
 NS_API ns_status ns_attend_paged(const void *d_q, int32_t dtype, int32_t n_seqs, int32_t n, int32_t q_heads,
@@ -144,7 +148,8 @@ NS_API ns_status ns_attend_paged(const void *d_q, int32_t dtype, int32_t n_seqs,
  * context for all of them, in whole tiles of 128.  They are read once for each
  * 256 rows of the group (new tokens and the query heads of a key-value head)
  * and the rest of each sequence as in ns_attend_paged; results differ from its
- * by their rounding alone.  Where sharing would not pay (more than 128 rows to
+ * by their rounding alone (and values are as large as it takes them with more
+ * than 16 rows).  Where sharing would not pay (more than 128 rows to
  * a sequence; up to 16 rows and 128 MB of keys and values by max_len) the call
  * is that call.  Groups that are not as said are flagged
  * (NS_FLAG_BAD_SEQ) and nothing is shared; a sequence that is invalid ends its

@@ -283,7 +283,7 @@ struct Mode {
   using Work = ns::Work<S>;
   using Dealer = ns::Dealer<S>;
   static constexpr bool kParts = true, kSplit = S, kLiveParts = true, kWhole = false;
-  static constexpr bool kCodes = F8, kHigh = true, kPaired = P;
+  static constexpr bool kCodes = F8, kHigh = F8, kPaired = P;
   static constexpr int kStageRow = 64, kRows = S ? 128 : 256;  // (of a part)
 
   struct Loader : paged::PageLoader<SharedArgs, Work, F8, P> {

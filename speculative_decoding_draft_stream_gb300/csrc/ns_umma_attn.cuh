@@ -5,11 +5,13 @@
 //   x_j = scale log2(e) q . k_j,  m = running bound of max x,
 //   l = sum 2^(x_j - m),  o = sum 2^(x_j - m) v_j;   out = o / l.
 // m is the first tile's maximum, and is raised (l and o multiplied by
-// 2^(old - new)) only when the sum of 64 probabilities passes 2^15: any m
+// 2^(old - new)) only when the sum of 64 probabilities passes 2^15 (2^30 in
+// bf16 over a cache of 8 bits, M::kHigh): any m
 // that is not far below the maximum gives the same quotient, so after the
 // first tile no maximum is taken (the sum is needed anyway) and the
-// accumulator in tensor memory is hardly ever rewritten.  Scores, sums and o
-// are fp32; a probability is rounded once, to the values' type, as an operand
+// accumulator in tensor memory is hardly ever rewritten.  o may be as much
+// larger meanwhile: with N keys up to N / 64 2^15 max |v| has to fit fp32.
+// Scores, sums and o are fp32; a probability is rounded once, to the values' type, as an operand
 // of the second product (l sums it unrounded).  With u that type's unit
 // roundoff it costs at most u sum p |v|, beside the output's own u |o|; in two
 // operands, a rounded one and the rest, the second product would cost twice as
@@ -86,8 +88,9 @@ static_assert(kRing % 2 == 0, "keys and values take turns");
 constexpr int kKeys = 128;           // keys of a tile
 constexpr int kHalf = 128 * 128;     // bytes of 128 rows of 64 elements
 constexpr float kLimit = 32768.f;    // a sum of 64 probabilities above this says that m is too low
-// bf16 probabilities have fp32's range, so m may stay lower (M::kHigh; sums of values up to 2^97 still fit fp32): where
-// keys are of very different sizes the limit above is passed in every few tiles, at 2 to 4 us each.
+// bf16 probabilities have fp32's range, so m may stay lower where the values are known to be small (M::kHigh: codes of 8
+// bits are at most 448 2^40, and 2^25 64s of them times 2^30 2^49 fit fp32): where keys are of very different sizes the
+// limit above is passed in every few tiles, at 2 to 4 us each.  Values of 16 bits may have fp32's range themselves.
 template <typename T, typename M>
 constexpr float kLimitOf = M::kHigh && Type<T>::kBf16 ? 1073741824.f : kLimit;
 constexpr int kChecks = 4;           // value tiles looked through ahead of the product

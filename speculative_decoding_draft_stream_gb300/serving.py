@@ -105,7 +105,8 @@ def attend_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu: torch.T
                   lse: Optional[torch.Tensor] = None, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
     """Causal attention over packed prompts: q [T, Hq, D], k and v [T, Hkv, D] (bf16 or fp16, D 64 or 128; token
     and head strides are free positive multiples of 8 elements), cu int32 [B + 1] the sequences' bounds, max_len the
-    longest.  Returns (out [T, Hq, D], lse fp32 [T, Hq]).  scale: 1 / sqrt(D) by default."""
+    longest.  Returns (out [T, Hq, D], lse fp32 [T, Hq]).  scale: 1 / sqrt(D) by default.  bf16 values of 2^113 / (a
+    sequence's length / 64) and more may overflow in the sums."""
     s = None if stream is None else _other(stream)
     if s is not None:
         return _on(s, lambda: attend_prompt(q, k, v, cu, max_len, scale=scale, out=out, lse=lse))
@@ -124,9 +125,10 @@ def attend_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, 
     set where new token i sees new token j (None: j <= i).  max_len, a bound on the lengths, takes part in how
     the keys are split: results of another bound may differ by their rounding.  With more than 16 rows (n * Hq / Hkv)
     a q off a 16-byte boundary, or with strides other than positive multiples of 8 elements, takes about three times
-    as long.  With k_exp and v_exp, uint8 [pages, Hkv, page_size], the pages are a cache of 8 bits (KvPages): codes in
-    e4m3 and the exponent of each row (more than 16 rows in fp16 see at most 65504 of what bf16 rows have written).
-    Returns (out [B, n, Hq, D], lse fp32 [B, n, Hq])."""
+    as long, and bf16 values may overflow as in attend_prompt (up to 16 rows: of 2^128 / length).  With k_exp and
+    v_exp, uint8 [pages, Hkv, page_size], the pages are a cache of 8 bits (KvPages): codes in e4m3 and the exponent of
+    each row (more than 16 rows in fp16 see at most 65504 of what bf16 rows have written).  Returns (out [B, n, Hq, D],
+    lse fp32 [B, n, Hq])."""
     s = None if stream is None else _other(stream)
     if s is not None:
         return _on(s, lambda: attend_paged(q, k_pages, v_pages, table, lengths, seqs, mask=mask, scale=scale,
@@ -146,9 +148,9 @@ def attend_shared(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
     KvPages.fork: seqs[groups[g]] .. seqs[groups[g + 1] - 1] are a group (groups int32 [G + 1], at most 512 groups, 0
     first and B last).  What the members of a group share is found in the table, in whole tiles of 128 positions, and
     read once for all of them; the rest of each sequence as in attend_paged, from whose results these differ by their
-    rounding alone.  q [B, n, Hq, D]: sequences follow one another as their tokens do (stride(0) is n * stride(1)), on
-    a 16-byte boundary, with strides that are positive multiples of 8.  It pays where a group's members are many, what
-    they share is long and their new tokens are few; where it would not (more than 128 rows, n * Hq / Hkv, or up to 16
+    rounding alone (and bf16 values may overflow as there with more than 16 rows).  q [B, n, Hq, D]: sequences follow
+    one another as their tokens do (stride(0) is n * stride(1)), on a 16-byte boundary, with strides that are positive
+    multiples of 8.  It pays where a group's members are many, what they share is long and their new tokens are few; where it would not (more than 128 rows, n * Hq / Hkv, or up to 16
     and 128 MB of keys and values by max_len), the call is attend_paged's.  k_exp and v_exp: as there.  Returns (out
     [B, n, Hq, D], lse fp32 [B, n, Hq])."""
     s = None if stream is None else _other(stream)
