@@ -241,6 +241,7 @@ PyObject *norm_rotate(PyObject *const *a) {
   const int32_t *pos = ints(a[2], "positions", d, {T});
   const at::Tensor &f = tensor(a[3], "inv_freq");
   void *freq = given(f, "inv_freq", at::kDouble, d);
+  no_gradient(f, "inv_freq");
   if (f.dim() != 1 || f.size(0) % 8 || f.size(0) > dim / 2) refuse("inv_freq must have a multiple of 8, up to dim / 2");
   const bool norm = a[6] != Py_None;
   void *w[2] = {nullptr, nullptr};
