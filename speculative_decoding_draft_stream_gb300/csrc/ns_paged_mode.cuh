@@ -154,9 +154,9 @@ struct PageConverter {
     const int page = __shfl_sync(0xffffffffu, next, row >> 3);
     const int pos = ((w.j0 + j) * fa::kKeys + row) & ((1 << a.page_shift) - 1);
     exps[0] = exps[1] = 127;
-    if (page >= 0 && page < a.n_pages) {
-      exps[0] = __ldg(a.rows.ke + head * a.rows.ke_head + 8 * ((int64_t)page * a.rows.kep8) + pos);
-      exps[1] = __ldg(a.rows.ve + head * a.rows.ve_head + 8 * ((int64_t)page * a.rows.vep8) + pos);
+    if (page >= 0 && page < a.n_pages) {  // (coherent loads: this kernel may have begun before the bytes were written)
+      exps[0] = a.rows.ke[head * a.rows.ke_head + 8 * ((int64_t)page * a.rows.kep8) + pos];
+      exps[1] = a.rows.ve[head * a.rows.ve_head + 8 * ((int64_t)page * a.rows.vep8) + pos];
     }
     next = fetch(a, w, j + 1, n, lane);
   }
