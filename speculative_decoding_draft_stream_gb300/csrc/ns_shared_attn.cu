@@ -13,7 +13,14 @@ namespace ns {
 //     29.1;  behind 2000 (268) 38.0, 30.5;  2 behind 16000 (126) 25.9, 31.9
 //   16 sequences behind 6007:  4 new tokens 52.7, 32.3;  8: 70.7, 39.6;  16: 70.8, 54.7;  32 (128 rows): 73.7, 72.9;
 //     60 (240 rows): 88, 113
-static bool pays(const PagedAttnArgs &a, int dim) {
+// Groups of one member on average, and contexts of less than a tile by max_len, have nothing to share.  What the plan,
+// the row tiles and the parts cost then (one new token, 8, 32; not shared, shared):
+//   32 heads on 8, 128 columns:  1 sequence behind 16000 19.9, 28.9; 29.0, 29.0; 29.5, 29.7;  64 behind 3000 128, 159;
+//     149, 164; 160, 183;  the same of 8 bits 81.5, 202.5; 193, 204; 202, 220
+//   12 on 4, 64 columns:  16 behind 2101 14.6, 29.9; 22.3, 29.4; 22.7, 30.9;  1 behind 16000 10.8, 25.4; 29.6, 25.7;
+//     29.9, 26.7 (row tiles of one sequence with their keys split, which attend_paged does not have)
+static bool pays(const PagedAttnArgs &a, int n_groups, int dim) {
+  if (n_groups >= a.n_seqs || a.max_len - a.n < kKeys) return false;
   constexpr int64_t kFew = 128LL << 20;
   const int64_t bytes = (int64_t)a.n_seqs * a.max_len * a.kv_heads * dim * (a.k_exp ? 2 : 4);
   return a.n * a.group <= 128 && (bytes > kFew || a.n * a.group > 16);
@@ -31,7 +38,7 @@ cudaError_t prepare_shared_attn() {
 
 cudaError_t launch_shared_attn(const PagedAttnArgs &a, const int32_t *groups, int n_groups, int dtype, int dim,
                                int sms, const PagedFit &fit, cudaStream_t st) {
-  if (!pays(a, dim)) {
+  if (!pays(a, n_groups, dim)) {
     PagedAttnArgs own = a;
     own.groups = groups, own.n_groups = n_groups;
     return a.k_exp ? launch_paged_attn8(own, dtype, dim, sms, fit, st)
