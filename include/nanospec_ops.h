@@ -150,9 +150,9 @@ NS_API ns_status ns_attend_paged(const void *d_q, int32_t dtype, int32_t n_seqs,
  * and the rest of each sequence as in ns_attend_paged; results differ from its
  * by their rounding alone (and values are as large as it takes them with more
  * than 16 rows).  Where sharing would not pay (more than 128 rows to
- * a sequence; up to 16 rows and 128 MB of keys and values by max_len; no fewer
- * groups than sequences, or by max_len less than 128 positions of context) the
- * call is that call.  Groups that are not as said are flagged
+ * a sequence; up to 192 MB of keys and values by max_len, with more than 16
+ * rows counted as of 16 bits; no fewer groups than sequences, or by max_len
+ * less than 128 positions of context) the call is that call.  Groups that are not as said are flagged
  * (NS_FLAG_BAD_SEQ) and nothing is shared; a sequence that is invalid ends its
  * group's sharing.
  * The sequences' queries follow one another as the tokens do: q_seq is

@@ -151,9 +151,9 @@ def attend_shared(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
     rounding alone (and bf16 values may overflow as there with more than 16 rows).  q [B, n, Hq, D]: sequences follow
     one another as their tokens do (stride(0) is n * stride(1)), on a 16-byte boundary, with strides that are positive
     multiples of 8.  It pays where a group's members are many, what they share is long and their new tokens are few;
-    where it would not (more than 128 rows, n * Hq / Hkv; up to 16 and 128 MB of keys and values by max_len; no fewer
-    groups than sequences, or by max_len less than 128 positions of context), the call is attend_paged's.  k_exp and
-    v_exp: as there.  Returns (out [B, n, Hq, D], lse fp32 [B, n, Hq])."""
+    where it would not (more than 128 rows, n * Hq / Hkv; up to 192 MB of keys and values by max_len, with more than 16
+    rows counted as of 16 bits; no fewer groups than sequences, or by max_len less than 128 positions of context), the
+    call is attend_paged's.  k_exp and v_exp: as there.  Returns (out [B, n, Hq, D], lse fp32 [B, n, Hq])."""
     s = None if stream is None else _other(stream)
     if s is not None:
         return _on(s, lambda: attend_shared(q, k_pages, v_pages, table, lengths, seqs, groups, mask=mask, scale=scale,

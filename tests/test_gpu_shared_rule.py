@@ -58,3 +58,16 @@ def test_groups_that_are_not_as_they_should_be_are_flagged(ns, flaw):  # noqa: F
         out, _ = c.attend(0, q, seqs, groups=i32(flaw))
         assert ns.ops_error(clear=True) == ns.FLAG_BAD_SEQ
         assert (out.float() - want.float()).norm() <= 0.01 * want.float().norm()
+
+
+@pytest.mark.parametrize("scaled", [False, True])
+@pytest.mark.parametrize("n,hq,B,length,max_len", [(1, 8, 8, 900, 19200), (8, 8, 24, 900, 908), (32, 8, 40, 700, 700),
+                                                   (5, 16, 24, 901, 1000)])
+def test_few_keys(ns, scaled, n, hq, B, length, max_len):  # noqa: F811
+    """Sequences that share nearly all, up to 192 MB of keys and values by max_len."""
+    if scaled and n == 1:
+        max_len *= 2
+    c, seqs, g = cache_of(ns, [length] * B, 128, scaled, True, BF16, n)
+    c.table.copy_(c.table[:1].expand_as(c.table))
+    assert B * max_len * 2 * 128 * (2 if scaled and n == 1 else 4) <= 192 << 20
+    assert both(ns, c, seqs, g, n, hq, 128, BF16, [0, B], max_len=max_len)
