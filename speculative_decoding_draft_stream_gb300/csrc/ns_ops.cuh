@@ -79,7 +79,7 @@ struct PagedAttnArgs {
   void *ws;
   uint32_t *err;
   const uint8_t *k_exp, *v_exp;  // a cache of 8 bits: each row's exponent
-  int64_t ke_page, ke_head, ve_page, ve_head;
+  int64_t ke_head, ve_head;
   int32_t kp16, kt16, vp16, vt16, kep8, vep8;  // its strides in units of 16 (exponents: 8) bytes
   const int32_t *groups;  // to be looked at, of a call of ns_attend_shared that does not share
   int32_t n_groups;

@@ -228,7 +228,7 @@ static ns_status attend_paged(const void *d_q, int32_t dtype, int32_t n_seqs, in
       *to[i] = (int32_t)strides[i];
     }
   }
-  a.k_exp = x.k, a.v_exp = x.v, a.ke_page = x.k_page, a.ke_head = x.k_head, a.ve_page = x.v_page, a.ve_head = x.v_head;
+  a.k_exp = x.k, a.v_exp = x.v, a.ke_head = x.k_head, a.ve_head = x.v_head;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (groups.n) {
     if (!(x.k ? ns::paged_umma8_ok(a) : ns::paged_umma_ok(a))) return NS_ERR_ARG;
