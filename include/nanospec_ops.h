@@ -62,7 +62,8 @@ NS_API ns_status ns_ops_get_error(uint32_t *flags, int32_t clear);
  *         be its input (the same address and strides), and may not overlap the
  *         inputs otherwise
  * dim is 64 or 128.  All arithmetic is fp32 and rounded once; angles are taken
- * modulo a turn in 64-bit fixed point, so far positions lose nothing.
+ * modulo a turn in 64-bit fixed point and are good to about 2^-26 of a turn,
+ * at far positions as at near ones.
  */
 NS_API ns_status ns_norm_rotate(const void *d_q, const void *d_k, int32_t dtype, int32_t tokens, int32_t q_heads,
                                 int32_t kv_heads, int32_t dim, int64_t q_token, int64_t q_head, int64_t k_token,
@@ -313,11 +314,14 @@ NS_API ns_status ns_pages_read(const ns_kv_pages *c, const ns_kv_scales *s, int3
  * [n_pages x kv_heads x page_size x dim] with strides in bytes, multiples of
  * 16, d_k_exp and d_v_exp their exponents [n_pages x kv_heads x page_size],
  * strides of page and head multiples of 8, as the addresses are.  `dtype` is
- * that of d_q and d_out.  The products see the codes' values exactly, and
- * probabilities are rounded to fp16 with the value's scale in them (up to 16
- * rows, or queries as said at d_q that TMA cannot fetch), or to `dtype`.  More
- * rows in fp16 see what an fp16 holds: a code times its power of two is rounded
- * below 2^-14, and beyond 65504, which rows written from fp16 are not, is 65504.
+ * that of d_q and d_out.  The products see the codes' values exactly; bf16
+ * queries become fp16 with a row's largest element at 1 to 2, so that one below
+ * 2^-14 of that is off by up to 2^-25 of it, and probabilities are rounded to
+ * fp16 with the value's scale in them (up to 16 rows, or queries as said at d_q
+ * that TMA cannot fetch); or queries stay as they are and probabilities are
+ * rounded to `dtype`.  Those rows in fp16 see what an fp16 holds: a code times
+ * its power of two is rounded below 2^-14, and beyond 65504, which rows written
+ * from fp16 are not, is 65504.
  */
 NS_API ns_status ns_attend_paged_scaled(const void *d_q, int32_t dtype, int32_t n_seqs, int32_t n, int32_t q_heads,
                                         int32_t kv_heads, int32_t dim, int64_t q_seq, int64_t q_token, int64_t q_head,

@@ -11,9 +11,11 @@
 // fractions (2^-24 of 10^6).  Only t modulo a turn counts, so f_i / 2 pi is
 // kept as a 64-bit fixed-point fraction of a turn, from the 53 bits of f_i and
 // 64 bits of 1 / 2 pi; its product with the position wraps by itself, and the
-// upper 32 bits are the angle: off by at most 2^-33 turns and position * 2^-53
-// of f_i's own rounding.  It takes a few integer instructions; the same product
-// in fp64 would wait for two fp64 units an SM.
+// upper 32 bits are the angle.  Cut there, it is off by up to 2^-32 turns, and
+// as an fp32 number by up to 2^-26 turns more (24 bits of half a turn), wherever
+// the position is; beside that, position * 2^-53 of f_i's own rounding.  It
+// takes a few integer instructions; the same product in fp64 would wait for two
+// fp64 units an SM.
 //
 // Layout: D / 16 lanes have a row, 16 columns each, so that every lane has
 // both columns of its eight pairs and nothing is exchanged but the sum of

@@ -22,7 +22,7 @@
 // the same inputs give the same bits.
 //
 // What bounds it: for few rows the chain of three kernels, each waiting for the
-// one before (8 sequences of one prompt of 2101 tokens, 32 heads on 8: 22 us,
+// one before (8 sequences of one prompt of 2101 tokens, 32 heads on 8: 23 us,
 // and 18 where each reads it from L2, which the rule in ns_shared_attn.cu then
 // prefers); for many sequences the items' starts and the parts' way through
 // L2 (64 of four prompts of 3001 to 16000 tokens, 28 heads on 4, fp16: 55 us;

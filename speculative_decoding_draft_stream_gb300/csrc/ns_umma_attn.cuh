@@ -6,25 +6,24 @@
 //   l = sum 2^(x_j - m),  o = sum 2^(x_j - m) v_j;   out = o / l.
 // m is the first tile's maximum, and is raised (l and o multiplied by
 // 2^(old - new)) only when the sum of 64 probabilities passes 2^15 (2^30 in
-// bf16 over a cache of 8 bits, M::kHigh): any m
-// that is not far below the maximum gives the same quotient, so after the
-// first tile no maximum is taken (the sum is needed anyway) and the
-// accumulator in tensor memory is hardly ever rewritten.  o may be as much
-// larger meanwhile: with N keys up to N / 64 2^15 max |v| has to fit fp32.
-// Scores, sums and o are fp32; a probability is rounded once, to the values' type, as an operand
-// of the second product (l sums it unrounded).  With u that type's unit
-// roundoff it costs at most u sum p |v|, beside the output's own u |o|; in two
-// operands, a rounded one and the rest, the second product would cost twice as
-// much.  fp16 probabilities are kept
-// 2^6 times larger: within fp16's range under the bound on the sum, and 2^-30
-// of the largest is not lost.
+// bf16 over a cache of 8 bits, M::kHigh): any m that is not far below the
+// maximum gives the same quotient, so after the first tile no maximum is taken
+// (the sum is needed anyway) and the accumulator in tensor memory is hardly ever
+// rewritten.  o may be as much larger meanwhile: of N keys, N / 64 2^15 max |v|
+// has to fit fp32.  Scores, sums and o are fp32; a probability is rounded once,
+// to the values' type, as an operand of the second product (l sums it
+// unrounded).  With u that type's unit roundoff it costs at most u sum p |v|,
+// beside the output's own u |o|; in two operands, a rounded one and the rest,
+// the second product would cost twice as much.  fp16 probabilities are kept 2^6
+// times larger: within fp16's range under the bound on the sum, and 2^-30 of the
+// largest is not lost.
 //
 // Rows: the query heads that share a key-value head are packed with their
 // tokens into tiles of 128 rows (128 / group tokens each), so a tile of keys
 // is fetched once for all of them; a work item is two such row tiles and some
 // key tiles.
 //
-// A CTA (one per SM, it keeps taking items) has five roles:
+// A CTA (one per SM, it keeps taking items) has five roles, or six:
 //   warp 0     TMA loads: the item's queries, then key and value tiles into a
 //              ring of four;
 //   warp 1     tcgen05.mma: S_i = Q_i K^T into tensor memory, O_i += P_i V
@@ -35,7 +34,9 @@
 //   warp 3     deals the items;
 //   warps 4-7 and 8-11  softmax of row tile 0 and 1: a thread has a row, reads
 //              its 128 scores, writes its probabilities over them (16 bits
-//              each), and at the item's end scales O and stores it.
+//              each), and at the item's end scales O and stores it;
+//   warps 12-15  (M::kCodes alone) make 16 bits of the codes that warp 0's
+//              loads bring, before products and warp 2 see a tile.
 // Tensor memory: S_0, S_1, O_0, O_1, 128 fp32 columns each: all of it.
 //
 // Hidden values: a probability of 0 times a value that is infinite or NaN
@@ -88,9 +89,10 @@ static_assert(kRing % 2 == 0, "keys and values take turns");
 constexpr int kKeys = 128;           // keys of a tile
 constexpr int kHalf = 128 * 128;     // bytes of 128 rows of 64 elements
 constexpr float kLimit = 32768.f;    // a sum of 64 probabilities above this says that m is too low
-// bf16 probabilities have fp32's range, so m may stay lower where the values are known to be small (M::kHigh: codes of 8
-// bits are at most 448 2^40, and 2^25 64s of them times 2^30 2^49 fit fp32): where keys are of very different sizes the
-// limit above is passed in every few tiles, at 2 to 4 us each.  Values of 16 bits may have fp32's range themselves.
+// bf16 probabilities have fp32's range, so m may stay lower where the values are known to be small (M::kHigh: codes of
+// 8 bits stand for less than 2^49, and sums over 2^25 64s of keys of 2^30 2^49 fit fp32): where keys are of very
+// different sizes the limit above is passed in every few tiles, at 2 to 4 us each.  Values of 16 bits may have fp32's
+// range themselves.
 template <typename T, typename M>
 constexpr float kLimitOf = M::kHigh && Type<T>::kBf16 ? 1073741824.f : kLimit;
 constexpr int kChecks = 4;           // value tiles looked through ahead of the product
